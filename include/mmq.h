@@ -23,7 +23,8 @@
  *    synchronously before anything is enqueued.
  *  - Return value: 0 on success, a negative MMQ_ERR_* code otherwise
  *    (mmq_strerror gives the text).  Nothing is written on an error return.
- *  - Inputs must be finite; NaN/Inf activations are outside the contract.
+ *  - Inputs must be finite; NaN/Inf activations are outside the contract
+ *    (the operators between the projections say otherwise for themselves).
  *  - All device pointers must be 16-byte aligned (tensor-memory-access
  *    copies require it).
  */
@@ -444,6 +445,60 @@ const char* mmq_strerror(int code);
  * While enabled, a GEMM's weights must not be written by the kernel
  * launched just before it on the same stream. */
 void mmq_set_programmatic_launch(int enable);
+
+/* ---- the operators between the projections of a decoder layer ----
+ *
+ * These have no counterpart on the pages (which stop at the projections);
+ * the formulas below are the contract.  Their finiteness rule is their own:
+ * NaN and Inf inputs are allowed and go where the formulas carry them. */
+
+/* Element types of 16-bit buffers (MMQ_TYPE_F32 where a call says so). */
+#define MMQ_TYPE_F16 0
+#define MMQ_TYPE_BF16 1
+#define MMQ_TYPE_F32 2
+
+/* Query / key head norms, rotary positions and the cache write. */
+typedef struct {
+    const float* qkv;        /* [tokens][ld]: per row heads query heads, then
+                              * kv_heads key heads, then kv_heads value heads,
+                              * head_dim values each (a fused q/k/v GEMM's C)  */
+    void* q;                 /* [tokens][heads][head_dim], type                */
+    void* k_cache;           /* [n_slots][kv_heads][head_dim], type            */
+    void* v_cache;           /* the same                                       */
+    const float* q_weight;   /* [head_dim], or NULL: query heads not normed    */
+    const float* k_weight;   /* [head_dim], or NULL: key heads not normed      */
+    const float* cos_table;  /* [table_rows][rot / 2] (NULL if rot == 0)       */
+    const float* sin_table;  /* the same                                       */
+    const int32_t* positions;/* [axes][tokens], axes = used sections           */
+    const int32_t* slots;    /* [tokens]; negative: the token is not cached    */
+    int64_t ld, tokens, table_rows, n_slots;
+    int32_t heads, kv_heads, head_dim;
+    int32_t rot;             /* first rot values of a head are rotated         */
+    int32_t sections[4];     /* rotated pairs per position axis, sum rot / 2;
+                              * pair j belongs to the axis whose section holds
+                              * it; {rot / 2, 0, 0, 0} for plain positions     */
+    int32_t interleaved;     /* 0: pairs (j, j + rot/2); 1: pairs (2j, 2j + 1) */
+    int32_t type;            /* MMQ_TYPE_F16 or MMQ_TYPE_BF16                  */
+    float eps;
+} mmq_qk_norm_rope_t;
+
+/* One pass over the rows of qkv.  Per query or key head x (f32):
+ *     y = x * rsqrt(mean(x^2) + eps) * weight         (if the weight is given)
+ *     (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c)    per rotated pair j,
+ * c, s = row positions[axis(j)][t] of the tables, column j.  Value heads are
+ * copied.  All arithmetic is f32; each output is rounded once to `type`.
+ * Query heads go to q, key and value heads to row slots[t] of the caches (a
+ * paged cache is the same array: slot = page * page_size + place).  Two tokens
+ * with the same slot race.  A position outside [0, table_rows) makes the
+ * token's query rows NaN and writes nothing to the caches; a slot >= n_slots
+ * writes nothing to the caches; either sets the device status word to
+ * MMQ_ERR_ARG (mmq_status).  tokens == 0 does nothing.
+ * head_dim a multiple of 8 in 16..256, rot a multiple of 8 in 0..head_dim, ld
+ * a multiple of 4, all pointers 16-byte aligned (positions, slots: 4-byte);
+ * MMQ_ERR_ARG / MMQ_ERR_ALIGN / MMQ_ERR_DEVICE / MMQ_ERR_CUDA.  Takes part in
+ * programmatic launch; the tables and weights must then not be written by the
+ * kernel launched just before. */
+int mmq_qk_norm_rope(const mmq_qk_norm_rope_t* p, void* stream);
 
 /* Test hook: force the K split of the dot-product kernels (q4_K, M <= 4;
  * q6_K, M <= 16) for later calls on this host thread: ks = 1, 2 or 4 warps

@@ -30,6 +30,7 @@ MMQ_PATH_TC = 2
 MMQ_PATH_SMALL_M = 3
 MMQ_HOST_NOALLOC_SCRATCH_BYTES = 64 << 20
 SMALL_M_MAX = 64
+MMQ_TYPE_F16, MMQ_TYPE_BF16, MMQ_TYPE_F32 = 0, 1, 2
 MMQ_GGUF_F32, MMQ_GGUF_F16, MMQ_GGUF_Q4_K, MMQ_GGUF_Q6_K = 0, 1, 12, 14
 
 # Every symbol include/mmq.h declares.
@@ -42,6 +43,7 @@ EXPORTS = (
     "mmq_q6K_block_dots",
     "mmq_gguf_open", "mmq_gguf_close", "mmq_gguf_tensor_count", "mmq_gguf_find", "mmq_gguf_tensor_info",
     "mmq_gguf_read", "mmq_gguf_write",
+    "mmq_qk_norm_rope",
     "mmq_status", "mmq_strerror", "mmq_debug_inject_timeout", "mmq_debug_force_gemv_split",
     "mmq_set_programmatic_launch",
 )
@@ -55,6 +57,18 @@ class MMQError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {strerror(code)} ({code})")
         self.code = code
+
+
+_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class mmq_qk_norm_rope_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("qkv", _P), ("q", _P), ("k_cache", _P), ("v_cache", _P), ("q_weight", _P), ("k_weight", _P),
+                ("cos_table", _P), ("sin_table", _P), ("positions", _P), ("slots", _P),
+                ("ld", _I64), ("tokens", _I64), ("table_rows", _I64), ("n_slots", _I64),
+                ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("rot", _I32), ("sections", _I32 * 4),
+                ("interleaved", _I32), ("type", _I32), ("eps", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -114,6 +128,7 @@ def load_library(path: str = LIB_PATH):
                 "mmq_gguf_write": ([ctypes.c_char_p, I, ctypes.POINTER(ctypes.c_char_p),
                                     ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_int64),
                                     ctypes.POINTER(P)], ctypes.c_int),
+                "mmq_qk_norm_rope": ([ctypes.POINTER(mmq_qk_norm_rope_t), P], ctypes.c_int),
                 "mmq_status": ([P], ctypes.c_int),
                 "mmq_strerror": ([ctypes.c_int], ctypes.c_char_p),
                 "mmq_debug_inject_timeout": ([ctypes.c_int], None),
@@ -590,4 +605,77 @@ def pack_q4K(v, sc, m, d_bits, dmin_bits):
     ptr = lambda a: a.ctypes.data_as(ctypes.c_void_p)
     _check(mmq_pack_q4K(ptr(v), ptr(sc), ptr(m), ptr(d_bits), ptr(dmin_bits), N, K, ptr(out)),
            "mmq_pack_q4K")
+    return out
+
+
+# ---- the operators between the projections of a decoder layer ---------------
+def mmq_qk_norm_rope(p, stream):
+    return load_library().mmq_qk_norm_rope(ctypes.byref(p), stream)
+
+
+def _type16(t) -> int:
+    import torch
+    if t.dtype == torch.float16:
+        return MMQ_TYPE_F16
+    if t.dtype == torch.bfloat16:
+        return MMQ_TYPE_BF16
+    raise MMQError(MMQ_ERR_ARG, f"float16 or bfloat16 expected, got {t.dtype}")
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise MMQError(MMQ_ERR_ARG, what)
+
+
+def _raw_stream(device, stream):
+    import torch
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, sections=None, out=None, stream=None):
+    """Head norms, rotary positions and the cache write after a fused q/k/v projection.
+
+    qkv float32 [T][(heads + 2 kv_heads) D] (rows may be strided); k_cache,
+    v_cache float16 or bfloat16 [..., kv_heads, D], contiguous, the leading
+    dimensions being the slots (pages x page size, say), written at slots
+    int32 [T] (negative: not cached); cos, sin float32 [rows][R/2]; positions
+    int32 [T], or [axes][T] with `sections`, the rotated pairs per axis;
+    q_weight, k_weight float32 [D] or None for no norm.  Returns the query
+    heads [T][heads][D] in the cache's type.  A position or slot out of range
+    shows in status()."""
+    import torch
+    kind = _type16(k_cache)
+    kv_heads, D = k_cache.shape[-2:]
+    T, width = qkv.shape
+    f32, i32 = torch.float32, torch.int32
+    _need(qkv.is_cuda and qkv.dtype is f32 and qkv.stride(1) == 1 and width == (heads + 2 * kv_heads) * D,
+          "qk_norm_rope: qkv must be float32 [T][(heads + 2 kv_heads) D] on the GPU")
+    _need(v_cache.dtype is k_cache.dtype and v_cache.shape == k_cache.shape and k_cache.is_contiguous()
+          and v_cache.is_contiguous(), "qk_norm_rope: k_cache and v_cache must be alike and contiguous")
+    _need(cos.dtype is f32 and sin.dtype is f32 and cos.dim() == 2 and cos.shape == sin.shape
+          and cos.is_contiguous() and sin.is_contiguous(), "qk_norm_rope: cos and sin must be float32 [rows][R/2]")
+    half = cos.shape[1]
+    parts = [half] if sections is None else list(sections)
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _need(positions.dtype is i32 and positions.is_contiguous() and positions.numel() == axes * T
+          and 1 <= len(parts) <= 4 and len(parts) == axes and sum(parts) == half,
+          "qk_norm_rope: positions must be int32 [T] or [axes][T], one section per axis, sections adding up to R/2")
+    _need(slots.dtype is i32 and slots.is_contiguous() and slots.numel() == T, "qk_norm_rope: slots must be int32 [T]")
+    for w in (q_weight, k_weight):
+        _need(w is None or (w.dtype is f32 and w.is_contiguous() and w.numel() == D),
+              "qk_norm_rope: a norm weight must be float32 [D]")
+    for t in (k_cache, v_cache, cos, sin, positions, slots, q_weight, k_weight, out):
+        _need(t is None or t.device == qkv.device, "qk_norm_rope: every tensor must be on qkv's device")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=k_cache.dtype, device=qkv.device)
+    _need(out.dtype is k_cache.dtype and out.is_contiguous() and out.shape == (T, heads, D),
+          "qk_norm_rope: out must be contiguous [T][heads][D] of the cache's type")
+    p = mmq_qk_norm_rope_t(
+        qkv.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+        cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+        qkv.stride(0) if T > 1 else width, T, cos.shape[0], k_cache.numel() // max(1, kv_heads * D),
+        heads, kv_heads, D, 2 * half, (_I32 * 4)(*parts), 1 if interleaved else 0, kind, eps)
+    _check(mmq_qk_norm_rope(p, _raw_stream(qkv.device, stream)), "mmq_qk_norm_rope")
     return out

@@ -441,6 +441,41 @@ int mmq_q6K_block_dots(mmq_q8_1_t aq, const uint8_t* bq6k_dev, int32_t* S, int64
     return from_cuda(mmq::launch_gemm_q6k(aq, bq6k_dev, nullptr, S, M, N, K, static_cast<cudaStream_t>(stream)));
 }
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+int mmq_qk_norm_rope(const mmq_qk_norm_rope_t* p, void* stream) {
+    if (!p) return MMQ_ERR_ARG;
+    const int64_t kMax = (int64_t(1) << 31) - 1;
+    if (p->tokens < 0 || p->tokens > kMax || p->n_slots < 0 || p->n_slots > kMax) return MMQ_ERR_ARG;
+    if (p->heads < 1 || p->kv_heads < 1 || p->heads > 65535 || p->kv_heads > 65535) return MMQ_ERR_ARG;
+    if (p->head_dim < 16 || p->head_dim > 256 || p->head_dim % 8) return MMQ_ERR_ARG;
+    if (p->rot < 0 || p->rot > p->head_dim || p->rot % 8) return MMQ_ERR_ARG;
+    if (p->type != MMQ_TYPE_F16 && p->type != MMQ_TYPE_BF16) return MMQ_ERR_ARG;
+    const int64_t width = (int64_t(p->heads) + 2 * int64_t(p->kv_heads)) * p->head_dim;
+    if (p->ld < width || p->ld % 4) return MMQ_ERR_ARG;
+    int64_t pairs = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (p->sections[i] < 0) return MMQ_ERR_ARG;
+        pairs += p->sections[i];
+    }
+    if (pairs != p->rot / 2 || p->table_rows < 0 || p->table_rows > kMax) return MMQ_ERR_ARG;
+    if (p->tokens == 0) return check_device();
+    if (!p->qkv || !p->q || !p->slots) return MMQ_ERR_ARG;
+    if (p->n_slots > 0 && (!p->k_cache || !p->v_cache)) return MMQ_ERR_ARG;
+    if (p->rot > 0 && (!p->positions || (p->table_rows > 0 && (!p->cos_table || !p->sin_table)))) return MMQ_ERR_ARG;
+    for (const void* v : {static_cast<const void*>(p->qkv), static_cast<const void*>(p->q),
+                          static_cast<const void*>(p->k_cache), static_cast<const void*>(p->v_cache),
+                          static_cast<const void*>(p->q_weight), static_cast<const void*>(p->k_weight),
+                          static_cast<const void*>(p->cos_table), static_cast<const void*>(p->sin_table)})
+        if (!aligned16(v)) return MMQ_ERR_ALIGN;
+    if (!aligned4(p->positions) || !aligned4(p->slots)) return MMQ_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_qk_norm_rope(*p, status, static_cast<cudaStream_t>(stream)));
+}
+
 int mmq_status(void* stream) {
     int* p = mmq::status_word_ptr();
     if (!p) return MMQ_ERR_CUDA;
