@@ -500,6 +500,53 @@ typedef struct {
  * kernel launched just before. */
 int mmq_qk_norm_rope(const mmq_qk_norm_rope_t* p, void* stream);
 
+/* Attention of a batch whose sequences share one long prefix. */
+typedef struct {
+    const void* q;           /* [tokens][heads][head_dim], type; tokens =
+                              * batch * q_len, q_stride values between tokens  */
+    void* out;               /* [tokens][heads][head_dim], out_type            */
+    const void* k_prefix;    /* the prefix's keys, type: token i's head h at   */
+    const void* v_prefix;    /* i * prefix_token_stride + h *
+                              * prefix_head_stride values; and its values      */
+    const void* k_cache;     /* [n_pages][page_size][kv_heads][head_dim], type */
+    const void* v_cache;     /* the same                                       */
+    const int32_t* page_table;/* [batch][table_width] page numbers              */
+    const int32_t* lens;     /* [batch] tokens in each sequence's own suffix,
+                              * its q_len new ones among them                  */
+    int64_t q_stride, prefix, prefix_token_stride, prefix_head_stride;
+    int64_t n_pages, table_width;
+    int32_t batch, q_len, heads, kv_heads, head_dim;
+    int32_t page_size;       /* a power of two                                 */
+    int32_t type, out_type;  /* MMQ_TYPE_F16 / BF16; out_type also F32         */
+    float scale;
+} mmq_shared_prefix_attention_t;
+
+/* Device workspace of one call (its sizes only; 0 for sizes the call
+ * refuses).  256-byte aligned, caller-owned, not used by anything else until
+ * the stream passes the call. */
+size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t* p);
+
+/* Token j = 0 .. q_len - 1 of sequence b sees every prefix key and the first
+ * lens[b] - q_len + 1 + j keys of its own suffix (key i on page
+ * page_table[b][i / page_size], place i % page_size); head h uses kv head
+ * h / (heads / kv_heads).  With s = scale * q.k over those keys,
+ *     out = sum_i exp(s_i - max s) v_i / sum_i exp(s_i - max s)
+ * and zeros for a token that sees no key.  Scores, the running maximum and
+ * sum and the values' sum are f32; the weights are rounded to `type` for the
+ * product with the values (a relative 2^-11 or 2^-8 per weight, unbiased), so
+ * an f32 out is no more precise than that.  The prefix is read once per 128 or
+ * so rows of the batch rather than once per sequence.  What the caches hold
+ * past a token's last key is never read.  Results are bitwise the same run to
+ * run on one device and build.  A length over table_width * page_size is cut
+ * to it, and a page number outside [0, n_pages) stands for a page of zeros;
+ * either sets the device status word to MMQ_ERR_ARG.
+ * head_dim 64 or 128; heads a multiple of kv_heads; strides multiples of 8;
+ * pointers 16-byte aligned (page_table, lens: 4-byte); batch == 0 does
+ * nothing.  MMQ_ERR_ARG (a small workspace included) / MMQ_ERR_ALIGN /
+ * MMQ_ERR_DEVICE / MMQ_ERR_RESOURCE / MMQ_ERR_CUDA. */
+int mmq_shared_prefix_attention(const mmq_shared_prefix_attention_t* p, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* Test hook: force the K split of the dot-product kernels (q4_K, M <= 4;
  * q6_K, M <= 16) for later calls on this host thread: ks = 1, 2 or 4 warps
  * per row group (the SwiGLU epilogue takes 1 or 2; a forced 4 makes its

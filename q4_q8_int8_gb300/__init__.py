@@ -43,7 +43,7 @@ EXPORTS = (
     "mmq_q6K_block_dots",
     "mmq_gguf_open", "mmq_gguf_close", "mmq_gguf_tensor_count", "mmq_gguf_find", "mmq_gguf_tensor_info",
     "mmq_gguf_read", "mmq_gguf_write",
-    "mmq_qk_norm_rope",
+    "mmq_qk_norm_rope", "mmq_shared_prefix_attention", "mmq_shared_prefix_attention_workspace",
     "mmq_status", "mmq_strerror", "mmq_debug_inject_timeout", "mmq_debug_force_gemv_split",
     "mmq_set_programmatic_launch",
 )
@@ -69,6 +69,16 @@ class mmq_qk_norm_rope_t(ctypes.Structure):
                 ("ld", _I64), ("tokens", _I64), ("table_rows", _I64), ("n_slots", _I64),
                 ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("rot", _I32), ("sections", _I32 * 4),
                 ("interleaved", _I32), ("type", _I32), ("eps", ctypes.c_float)]
+
+
+class mmq_shared_prefix_attention_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("q", _P), ("out", _P), ("k_prefix", _P), ("v_prefix", _P), ("k_cache", _P), ("v_cache", _P),
+                ("page_table", _P), ("lens", _P),
+                ("q_stride", _I64), ("prefix", _I64), ("prefix_token_stride", _I64), ("prefix_head_stride", _I64),
+                ("n_pages", _I64), ("table_width", _I64),
+                ("batch", _I32), ("q_len", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32),
+                ("page_size", _I32), ("type", _I32), ("out_type", _I32), ("scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -129,6 +139,9 @@ def load_library(path: str = LIB_PATH):
                                     ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_int64),
                                     ctypes.POINTER(P)], ctypes.c_int),
                 "mmq_qk_norm_rope": ([ctypes.POINTER(mmq_qk_norm_rope_t), P], ctypes.c_int),
+                "mmq_shared_prefix_attention_workspace": ([ctypes.POINTER(mmq_shared_prefix_attention_t)], S),
+                "mmq_shared_prefix_attention": ([ctypes.POINTER(mmq_shared_prefix_attention_t), P, S, P],
+                                                ctypes.c_int),
                 "mmq_status": ([P], ctypes.c_int),
                 "mmq_strerror": ([ctypes.c_int], ctypes.c_char_p),
                 "mmq_debug_inject_timeout": ([ctypes.c_int], None),
@@ -678,4 +691,69 @@ def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, 
         qkv.stride(0) if T > 1 else width, T, cos.shape[0], k_cache.numel() // max(1, kv_heads * D),
         heads, kv_heads, D, 2 * half, (_I32 * 4)(*parts), 1 if interleaved else 0, kind, eps)
     _check(mmq_qk_norm_rope(p, _raw_stream(qkv.device, stream)), "mmq_qk_norm_rope")
+    return out
+
+
+def mmq_shared_prefix_attention_workspace(p):
+    return load_library().mmq_shared_prefix_attention_workspace(ctypes.byref(p))
+
+
+def mmq_shared_prefix_attention(p, workspace, workspace_bytes, stream):
+    return load_library().mmq_shared_prefix_attention(ctypes.byref(p), workspace, workspace_bytes, stream)
+
+
+def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table, lens, q_len: int = 1, scale=None,
+                            out=None, workspace=None, stream=None):
+    """Attention of a batch whose sequences share one prefix, each with its own paged suffix.
+
+    q float16 or bfloat16 [batch q_len][heads][D] (tokens may be strided),
+    D 64 or 128; k_prefix, v_prefix [P][kv_heads][D] (tokens and heads may be
+    strided, both alike; P may be 0); k_cache, v_cache [pages][page_size]
+    [kv_heads][D], contiguous; page_table int32 [batch][width]; lens int32
+    [batch]: the tokens of each sequence's suffix, its q_len new ones among
+    them (token j sees lens - q_len + 1 + j of them).  scale: 1/sqrt(D) by
+    default.  Returns [batch q_len][heads][D] in q's type, or into `out`
+    (which may also be float32).  `workspace`: a CUDA uint8 tensor of
+    mmq_shared_prefix_attention_workspace bytes, allocated per call if None."""
+    import torch
+    kind = _type16(q)
+    T, heads, D = q.shape
+    P, kv_heads = k_prefix.shape[:2]
+    n_pages, page_size = k_cache.shape[:2]
+    batch, width = page_table.shape
+    dt, dev = q.dtype, q.device
+    _need(q.is_cuda and q.stride(2) == 1 and q.stride(1) == D and T == batch * q_len,
+          "shared_prefix_attention: q must be [batch q_len][heads][D] on the GPU, heads contiguous")
+    _need(k_prefix.dtype is dt and v_prefix.dtype is dt and v_prefix.shape == k_prefix.shape and k_prefix.shape[2] == D
+          and (P == 0 or (k_prefix.stride() == v_prefix.stride() and k_prefix.stride(2) == 1)),
+          "shared_prefix_attention: k_prefix and v_prefix must be alike, [P][kv_heads][D] in q's type")
+    _need(k_cache.dtype is dt and v_cache.dtype is dt and v_cache.shape == k_cache.shape
+          and k_cache.shape[2:] == (kv_heads, D) and k_cache.is_contiguous() and v_cache.is_contiguous(),
+          "shared_prefix_attention: the caches must be contiguous [pages][page_size][kv_heads][D] in q's type")
+    _need(page_table.dtype is torch.int32 and page_table.is_contiguous() and lens.dtype is torch.int32
+          and lens.is_contiguous() and lens.numel() == batch,
+          "shared_prefix_attention: page_table must be int32 [batch][width], lens int32 [batch]")
+    for t in (k_prefix, v_prefix, k_cache, v_cache, page_table, lens, out, workspace):
+        _need(t is None or t.device == dev, "shared_prefix_attention: every tensor must be on q's device")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=dt, device=dev)
+    _need(out.shape == q.shape and out.is_contiguous() and (out.dtype is dt or out.dtype is torch.float32),
+          "shared_prefix_attention: out must be contiguous [batch q_len][heads][D] in q's type or float32")
+    p = mmq_shared_prefix_attention_t(
+        q.data_ptr(), out.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        page_table.data_ptr(), lens.data_ptr(),
+        q.stride(0) if T > 1 else heads * D, P, k_prefix.stride(0) if P > 1 else kv_heads * D,
+        k_prefix.stride(1) if kv_heads > 1 else D, n_pages, width,
+        batch, q_len, heads, kv_heads, D, page_size, kind, kind if out.dtype is dt else MMQ_TYPE_F32,
+        D ** -0.5 if scale is None else scale)
+    if batch == 0:
+        return out
+    if workspace is None:
+        need = mmq_shared_prefix_attention_workspace(p)
+        _need(need > 0, "shared_prefix_attention: sizes")
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _check(mmq_shared_prefix_attention(p, workspace.data_ptr(), workspace.numel(), _raw_stream(dev, stream)),
+           "mmq_shared_prefix_attention")
     return out

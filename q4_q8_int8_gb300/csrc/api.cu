@@ -476,6 +476,57 @@ int mmq_qk_norm_rope(const mmq_qk_norm_rope_t* p, void* stream) {
     return from_cuda(mmq::launch_qk_norm_rope(*p, status, static_cast<cudaStream_t>(stream)));
 }
 
+// The sizes of an attention call (no pointers): MMQ_OK or MMQ_ERR_ARG.
+static int check_attention_sizes(const mmq_shared_prefix_attention_t* p) {
+    if (!p) return MMQ_ERR_ARG;
+    const int64_t kMax = (int64_t(1) << 31) - 1;
+    if (p->batch < 0 || p->q_len < 1 || p->heads < 1 || p->kv_heads < 1 || p->kv_heads > 65535) return MMQ_ERR_ARG;
+    if (p->heads > 65535 || p->heads % p->kv_heads) return MMQ_ERR_ARG;
+    if (int64_t(p->batch) * p->q_len * p->heads > kMax) return MMQ_ERR_ARG;
+    if (p->head_dim != 64 && p->head_dim != 128) return MMQ_ERR_ARG;
+    if (p->page_size < 1 || p->page_size > (1 << 20) || (p->page_size & (p->page_size - 1))) return MMQ_ERR_ARG;
+    if (p->prefix < 0 || p->prefix > kMax || p->n_pages < 0 || p->n_pages > kMax) return MMQ_ERR_ARG;
+    if (p->table_width < 0 || p->table_width > kMax / p->page_size) return MMQ_ERR_ARG;
+    if (p->type != MMQ_TYPE_F16 && p->type != MMQ_TYPE_BF16) return MMQ_ERR_ARG;
+    if (p->out_type != p->type && p->out_type != MMQ_TYPE_F32) return MMQ_ERR_ARG;
+    if (!(p->scale > 0.f && p->scale < 1e30f)) return MMQ_ERR_ARG;
+    const int64_t kStride = int64_t(1) << 40;
+    if (p->q_stride < int64_t(p->heads) * p->head_dim || p->q_stride % 8 || p->q_stride > kStride) return MMQ_ERR_ARG;
+    if (p->prefix > 0) {
+        const int64_t ts = p->prefix_token_stride, hs = p->prefix_head_stride;
+        if (ts < p->head_dim || hs < p->head_dim || ts % 8 || hs % 8 || ts > kStride / 2 || hs > kStride / 2)
+            return MMQ_ERR_ARG;
+    }
+    return MMQ_OK;
+}
+
+size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t* p) {
+    if (check_attention_sizes(p) || p->batch == 0 || check_device()) return 0;
+    return mmq::shared_prefix_attention_workspace(*p);
+}
+
+int mmq_shared_prefix_attention(const mmq_shared_prefix_attention_t* p, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    int rc = check_attention_sizes(p);
+    if (rc) return rc;
+    if (p->batch == 0) return check_device();
+    if (!p->q || !p->out || !p->lens || !workspace) return MMQ_ERR_ARG;
+    if (p->prefix > 0 && (!p->k_prefix || !p->v_prefix)) return MMQ_ERR_ARG;
+    if (p->table_width > 0 && !p->page_table) return MMQ_ERR_ARG;
+    if (p->table_width > 0 && p->n_pages > 0 && (!p->k_cache || !p->v_cache)) return MMQ_ERR_ARG;
+    for (const void* v : {p->q, static_cast<const void*>(p->out), p->k_prefix, p->v_prefix, p->k_cache, p->v_cache})
+        if (!aligned16(v)) return MMQ_ERR_ALIGN;
+    if (!aligned4(p->page_table) || !aligned4(p->lens)) return MMQ_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return MMQ_ERR_ALIGN;
+    if ((rc = check_device())) return rc;
+    const size_t need = mmq::shared_prefix_attention_workspace(*p);
+    if (need == 0) return MMQ_ERR_CUDA;
+    if (workspace_bytes < need) return MMQ_ERR_ARG;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_shared_prefix_attention(*p, workspace, status, static_cast<cudaStream_t>(stream)));
+}
+
 int mmq_status(void* stream) {
     int* p = mmq::status_word_ptr();
     if (!p) return MMQ_ERR_CUDA;

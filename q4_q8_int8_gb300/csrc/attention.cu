@@ -1,0 +1,471 @@
+// Attention of a batch whose sequences share one prefix: softmax over the
+// prefix keys, then each token's own paged suffix, in f32, computed in parts
+// and joined by the running maximum and sum:
+//   part p of a row:  m_p = max s,  l_p = sum 2^(s - m_p),  o_p = sum 2^(s - m_p) v
+//   row:              out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p,  m = max m_p
+// with s = q.k * scale * log2(e).  A row with no key at all (an empty prefix
+// and an empty suffix) is zero.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attention.h"
+#include "mmq_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace {
+
+using namespace mmq::ptx;
+using mmq::AttnArgs;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half*) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         __nv_bfloat16*) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ------------------------------------------------------- few rows per key
+// One CTA: up to 16 rows that see the same keys (a token's heads of one kv
+// head over a part of its suffix; or any 16 rows over a part of the prefix).
+// Bound by the key / value bytes, so rows are padded to the 16 of one
+// mma.sync tile and the four warps take 16-key slabs in turn, each warp with
+// its own cp.async ring (4 warps x 3 stages x 16 keys x K and V, 96 KB at 128
+// dims, two CTAs per SM: 192 KB in flight), its own running maximum and sum,
+// joined through shared memory at the end.  Keys past the row's limit are
+// filled with zeros, not read, so what the cache holds there cannot matter.
+// Weights are rounded to the cache's type for the second product (their sum
+// is taken in f32 before that); both products accumulate in f32.
+constexpr int kWarps = 4, kSlab = 16, kStages = 3;
+
+template <int D>
+constexpr int row_smem() {
+    return kWarps * kStages * 2 * kSlab * D * 2;
+}
+
+template <typename T, int D, bool kPrefix>
+__global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const mmq_shared_prefix_attention_t& p = a.p;
+    T* const tag = nullptr;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, G = a.group;
+    const int tiles_per_token = (G + 15) / 16;
+
+    // Rows [r0, r1) and keys [k0, k1) of this CTA.
+    int64_t r0, r1, k0, k1;
+    int part = blockIdx.z;
+    const int32_t* pages = nullptr;
+    if (kPrefix) {
+        r0 = int64_t(blockIdx.x) * 16;
+        r1 = min(r0 + 16, a.tokens * G);
+        k0 = part * a.part_keys;
+        k1 = min(k0 + a.part_keys, p.prefix);
+    } else {
+        const int64_t t = blockIdx.x / tiles_per_token;
+        const int b = int(t / p.q_len);
+        r0 = t * G + int64_t(blockIdx.x % tiles_per_token) * 16;
+        r1 = min(r0 + 16, t * G + G);
+        pages = p.page_table + int64_t(b) * p.table_width;
+        const int64_t room = p.table_width << a.page_shift;
+        int64_t len = p.lens[b];
+        if (len > room) {
+            if (threadIdx.x == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+            len = room;
+        }
+        len = max(int64_t(0), len - p.q_len + 1 + t % p.q_len);
+        const int64_t step = ((len + a.suffix_parts - 1) / a.suffix_parts + 63) & ~int64_t(63);
+        k0 = min(part * step, len);
+        k1 = min(k0 + step, len);
+        part += a.prefix_parts;
+    }
+    const int64_t part_row = int64_t(part) * a.tokens;
+    const int grow = lane >> 2, gcol = lane & 3;
+    auto token_head = [&](int64_t r) { return (r / G) * p.heads + int64_t(h) * G + r % G; };
+
+    if (k0 >= k1) {
+        if (threadIdx.x < 16 && r0 + threadIdx.x < r1)
+            a.part_ml[part_row * p.heads + token_head(r0 + threadIdx.x)] = make_float2(-INFINITY, 0.f);
+        return;
+    }
+
+    // Query fragments: rows grow and grow + 8, zero past r1.
+    uint32_t qf[D / 16][4];
+    {
+        const int64_t ra = r0 + grow, rb = ra + 8;
+        const T* qa = static_cast<const T*>(p.q) + (ra / G) * p.q_stride + (int64_t(h) * G + ra % G) * D;
+        const T* qb = static_cast<const T*>(p.q) + (rb / G) * p.q_stride + (int64_t(h) * G + rb % G) * D;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int c = kk * 16 + 2 * gcol;
+            qf[kk][0] = ra < r1 ? *reinterpret_cast<const uint32_t*>(qa + c) : 0u;
+            qf[kk][1] = rb < r1 ? *reinterpret_cast<const uint32_t*>(qb + c) : 0u;
+            qf[kk][2] = ra < r1 ? *reinterpret_cast<const uint32_t*>(qa + c + 8) : 0u;
+            qf[kk][3] = rb < r1 ? *reinterpret_cast<const uint32_t*>(qb + c + 8) : 0u;
+        }
+    }
+
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages * 2 * kSlab * D * 2);
+    constexpr uint32_t kHalfStage = kSlab * D * 2;
+    constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
+    const int64_t slabs = (k1 - k0 + kSlab - 1) / kSlab;
+    bool bad_page = false;
+
+    // Slab i's rows: 32 / kChunks rows of 16-byte chunks per step, chunk c of
+    // row r at c ^ (r & 7) (conflict-free for ldmatrix).
+    auto fetch = [&](int64_t i, int stage) {
+        const uint32_t base = ring + uint32_t(stage) * 2 * kHalfStage;
+        constexpr int kRows = 32 / kChunks;
+        const int c = lane % kChunks;
+#pragma unroll
+        for (int j = 0; j < kSlab / kRows; ++j) {
+            const int r = j * kRows + lane / kChunks;
+            const int64_t key = k0 + i * kSlab + r;
+            bool valid = key < k1;
+            int64_t off = 0;
+            if (valid) {
+                if (kPrefix) {
+                    off = key * p.prefix_token_stride + h * p.prefix_head_stride;
+                } else {
+                    const int32_t id = pages[key >> a.page_shift];
+                    if (id < 0 || id >= p.n_pages) {
+                        bad_page = true;
+                        valid = false;
+                    } else {
+                        off = ((((int64_t(id) << a.page_shift) + (key & ((int64_t(1) << a.page_shift) - 1))) *
+                                p.kv_heads) + h) * D;
+                    }
+                }
+            }
+            const uint32_t dst = base + uint32_t(r * D * 2 + ((c ^ (r & 7)) << 4));
+            const T* kp = static_cast<const T*>(kPrefix ? p.k_prefix : p.k_cache) + off + c * 8;
+            const T* vp = static_cast<const T*>(kPrefix ? p.v_prefix : p.v_cache) + off + c * 8;
+            cp_async16(dst, valid ? kp : static_cast<const T*>(p.q), valid);
+            cp_async16(dst + kHalfStage, valid ? vp : static_cast<const T*>(p.q), valid);
+        }
+    };
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    // This warp's slabs: warp, warp + 4, ...
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (warp + int64_t(s) * kWarps < slabs) fetch(warp + int64_t(s) * kWarps, s);
+        cp_async_commit();
+    }
+    int stage = 0;
+    for (int64_t i = warp; i < slabs; i += kWarps) {
+        const int64_t ahead = i + int64_t(kStages - 1) * kWarps;
+        if (ahead < slabs) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+        cp_async_commit();
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t kb = ring + uint32_t(stage) * 2 * kHalfStage, vb = kb + kHalfStage;
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        const int m = lane >> 3, r7 = lane & 7;
+        const uint32_t krow = uint32_t(((m >> 1) * 8 + r7) * D * 2), vrow = uint32_t(((m & 1) * 8 + r7) * D * 2);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t b[4];
+            ldmatrix4(b, kb + krow + uint32_t(((kk * 2 + (m & 1)) ^ r7) << 4));
+            mma16816(s0, qf[kk], b[0], b[1], tag);
+            mma16816(s1, qf[kk], b[2], b[3], tag);
+        }
+        const int64_t left = k1 - (k0 + i * kSlab);   // keys of this slab: all from 16 on
+        float x[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int key = (k & 2 ? 8 : 0) + 2 * gcol + (k & 1);
+            x[k] = key < left ? x[k] * a.scale_log2 : -INFINITY;
+        }
+        float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+        const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+            // (-inf) - (-inf) only where the sums are still zero
+            const float f0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0), f1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                o[n][0] *= f0; o[n][1] *= f0;
+                o[n][2] *= f1; o[n][3] *= f1;
+            }
+            m0 = n0;
+            m1 = n1;
+        }
+        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = exp2f(x[k] - b0);
+            x[k + 4] = exp2f(x[k + 4] - b1);
+        }
+        l0 += (x[0] + x[1]) + (x[2] + x[3]);
+        l1 += (x[4] + x[5]) + (x[6] + x[7]);
+        const uint32_t pf[4] = {pack16(x[0], x[1], tag), pack16(x[4], x[5], tag), pack16(x[2], x[3], tag),
+                                pack16(x[6], x[7], tag)};
+#pragma unroll
+        for (int dc = 0; dc < D / 16; ++dc) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, vb + vrow + uint32_t(((dc * 2 + (m >> 1)) ^ r7) << 4));
+            mma16816(o[2 * dc], pf, b[0], b[1], tag);
+            mma16816(o[2 * dc + 1], pf, b[2], b[3], tag);
+        }
+        __syncwarp();
+        if (++stage == kStages) stage = 0;
+    }
+    cp_async_wait<0>();
+    if (bad_page) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+
+    // Join the four warps: their rows in shared memory, f32 [warp][16][D], and
+    // (m, l) [warp][16].
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(smem);
+    __shared__ float2 sml[kWarps][16];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+        *reinterpret_cast<float2*>(so + (warp * 16 + grow) * D + n * 8 + 2 * gcol) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(so + (warp * 16 + grow + 8) * D + n * 8 + 2 * gcol) = make_float2(o[n][2], o[n][3]);
+    }
+    if (gcol == 0) {
+        sml[warp][grow] = make_float2(m0, l0);
+        sml[warp][grow + 8] = make_float2(m1, l1);
+    }
+    __syncthreads();
+    constexpr int kLanes = D / 4, kRowsAtOnce = kWarps * 32 / kLanes;
+    const int c4 = (threadIdx.x % kLanes) * 4;
+    for (int r = threadIdx.x / kLanes; r < 16 && r0 + r < r1; r += kRowsAtOnce) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sml[w][r].x);
+        float ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 ml = sml[w][r];
+            // a warp without keys has l = 0 (and m = -inf)
+            const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - mm);
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + c4);
+            ll = fmaf(f, ml.y, ll);
+            acc.x = fmaf(f, v.x, acc.x); acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z); acc.w = fmaf(f, v.w, acc.w);
+        }
+        const int64_t at = part_row * p.heads + token_head(r0 + r);
+        *reinterpret_cast<float4*>(a.part_o + at * D + c4) = acc;
+        if (c4 == 0) a.part_ml[at] = make_float2(mm, ll);
+    }
+}
+
+// ------------------------------------------------------------------- join
+// One warp per (token, head): the parts' (m, l) give each part's factor, then
+// one pass over their sums; parts without keys are not read.
+__device__ __forceinline__ void store_out(void* out, int type, int64_t at, float x, float y) {
+    if (type == MMQ_TYPE_F32)
+        *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = make_float2(x, y);
+    else if (type == MMQ_TYPE_F16)
+        *reinterpret_cast<uint32_t*>(static_cast<__half*>(out) + at) = pack16(x, y, static_cast<__half*>(nullptr));
+    else
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(out) + at) =
+            pack16(x, y, static_cast<__nv_bfloat16*>(nullptr));
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = a.tokens * a.p.heads;
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int parts = a.prefix_parts + a.suffix_parts;
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[i * rows + row].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f;
+    float2 acc[D / 64];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) acc[c] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float2 ml = a.part_ml[i * rows + row];
+        if (ml.y == 0.f) continue;
+        const float f = exp2f(ml.x - m);
+        l = fmaf(f, ml.y, l);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float2 v = *reinterpret_cast<const float2*>(a.part_o + (i * rows + row) * D + c * 64 + 2 * lane);
+            acc[c].x = fmaf(f, v.x, acc[c].x);
+            acc[c].y = fmaf(f, v.y, acc[c].y);
+        }
+    }
+    const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+        store_out(a.p.out, a.p.out_type, row * D + c * 64 + 2 * lane, acc[c].x * r, acc[c].y * r);
+}
+
+// A kernel of this call that follows another: it may be scheduled before the
+// other ends, and waits for it (griddep_wait) before it touches memory.
+cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_t s, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cfg;
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// Parts for `units` independent pieces of up to `keys` keys each, on `slots`
+// resident CTAs: enough to give every slot a piece, none shorter than `least`.
+int split(int64_t units, int64_t keys, int64_t slots, int64_t least) {
+    if (keys <= 0) return 0;
+    int64_t n = (slots + units - 1) / units;
+    const int64_t most = (keys + least - 1) / least;
+    if (n > most) n = most;
+    if (n > 64) n = 64;
+    return int(n < 1 ? 1 : n);
+}
+
+void plan(AttnArgs& a, int nsm) {
+    const mmq_shared_prefix_attention_t& p = a.p;
+    a.tokens = int64_t(p.batch) * p.q_len;
+    a.group = p.heads / p.kv_heads;
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
+    const int64_t rows = a.tokens * a.group;
+    const int64_t slots = int64_t(nsm) * 2;
+    a.prefix_parts = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 256);
+    a.part_keys = 0;
+    if (a.prefix_parts) {
+        a.part_keys = ((p.prefix + a.prefix_parts - 1) / a.prefix_parts + 63) & ~int64_t(63);
+        a.prefix_parts = int((p.prefix + a.part_keys - 1) / a.part_keys);
+    }
+    a.suffix_parts = split(a.tokens * ((a.group + 15) / 16) * p.kv_heads, p.table_width << a.page_shift, slots, 256);
+}
+
+size_t ml_bytes(const AttnArgs& a) {
+    const size_t n = size_t(a.prefix_parts + a.suffix_parts) * size_t(a.tokens) * size_t(a.p.heads) * sizeof(float2);
+    return (n + 255) & ~size_t(255);
+}
+
+template <typename T, int D>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    cudaError_t e;
+    bool first = true;
+    auto config = [&](dim3 grid, dim3 block, size_t smem) {
+        const bool f = first;
+        first = false;
+        return f ? mmq::launch_config(grid, block, smem, s, attr) : follow_config(grid, block, smem, s, attr);
+    };
+    constexpr int smem = row_smem<D>();
+    if (a.suffix_parts) {
+        if ((e = cudaFuncSetAttribute(attn_rows_kernel<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+            return e;
+        const dim3 grid(unsigned(a.tokens * ((a.group + 15) / 16)), unsigned(a.p.kv_heads), unsigned(a.suffix_parts));
+        const cudaLaunchConfig_t cfg = config(grid, dim3(kWarps * 32), smem);
+        if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, false>, a))) return e;
+    }
+    if (a.prefix_parts) {
+        if ((e = cudaFuncSetAttribute(attn_rows_kernel<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+            return e;
+        const dim3 grid(unsigned((a.tokens * a.group + 15) / 16), unsigned(a.p.kv_heads), unsigned(a.prefix_parts));
+        const cudaLaunchConfig_t cfg = config(grid, dim3(kWarps * 32), smem);
+        if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, true>, a))) return e;
+    }
+    const cudaLaunchConfig_t cfg = config(dim3(unsigned((a.tokens * a.p.heads + 7) / 8)), dim3(256), 0);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, a);
+}
+
+}  // namespace
+
+namespace mmq {
+
+size_t shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t& p) {
+    const int nsm = sm_count();
+    if (!nsm) return 0;
+    AttnArgs a;
+    a.p = p;
+    plan(a, nsm);
+    return ml_bytes(a) + size_t(a.prefix_parts + a.suffix_parts) * size_t(a.tokens) * size_t(p.heads) *
+                             size_t(p.head_dim) * sizeof(float);
+}
+
+cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& p, void* workspace, int* status,
+                                           cudaStream_t s) {
+    const int nsm = sm_count();
+    if (!nsm) return cudaErrorInvalidDevice;
+    AttnArgs a;
+    a.p = p;
+    plan(a, nsm);
+    a.status = status;
+    a.part_ml = static_cast<float2*>(workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a));
+    if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, s) : launch<__half, 128>(a, s);
+    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, s) : launch<__nv_bfloat16, 128>(a, s);
+}
+
+}  // namespace mmq

@@ -151,6 +151,10 @@ cudaError_t launch_gemm_q6k_tc(mmq_q8_1_t aq, const uint8_t* w, float* C, int32_
                                int64_t K, int* status, int inject_timeout, cudaStream_t s);
 // Head norms + rotary positions + cache write (qk_rope.cu); tokens >= 1.
 cudaError_t launch_qk_norm_rope(const mmq_qk_norm_rope_t& p, int* status, cudaStream_t s);
+// Shared-prefix attention (attention.cu); batch >= 1.
+size_t shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t& p);   // 0 on a CUDA error
+cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& p, void* workspace, int* status,
+                                           cudaStream_t s);
 int small_m_launch_count(int64_t M, int64_t N, int64_t K);   // kernels per call, -1 on a CUDA error
 constexpr int64_t kSmallMMax = 64;
 

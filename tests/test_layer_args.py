@@ -39,3 +39,36 @@ def test_rope_refuses_alignment(name, by):
 
 def test_null_structs():
     assert mmq.load_library().mmq_qk_norm_rope(None, None) == mmq.MMQ_ERR_ARG
+    assert mmq.load_library().mmq_shared_prefix_attention(None, None, 0, None) == mmq.MMQ_ERR_ARG
+    assert mmq.load_library().mmq_shared_prefix_attention_workspace(None) == 0
+
+
+def attn(workspace=0x100, ws_bytes=1 << 40, **change):
+    f = dict(q=0x10000, out=0x20000, k_prefix=0x30000, v_prefix=0x40000, k_cache=0x50000, v_cache=0x60000,
+             page_table=0x70000, lens=0x80000, q_stride=512, prefix=100, prefix_token_stride=128,
+             prefix_head_stride=64, n_pages=8, table_width=2, batch=4, q_len=1, heads=8, kv_heads=2, head_dim=64,
+             page_size=16, type=mmq.MMQ_TYPE_F16, out_type=mmq.MMQ_TYPE_F16, scale=0.125)
+    f.update(change)
+    return mmq.mmq_shared_prefix_attention(mmq.mmq_shared_prefix_attention_t(**f), workspace, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=None), dict(out=None), dict(k_prefix=None), dict(v_prefix=None), dict(k_cache=None), dict(v_cache=None),
+    dict(page_table=None), dict(lens=None), dict(workspace=None), dict(batch=-1), dict(q_len=0), dict(heads=0),
+    dict(heads=7), dict(kv_heads=0), dict(kv_heads=3), dict(head_dim=32), dict(head_dim=96), dict(head_dim=256),
+    dict(page_size=0), dict(page_size=12), dict(page_size=1 << 21), dict(prefix=-1), dict(n_pages=-1),
+    dict(table_width=-1), dict(table_width=1 << 30), dict(type=2), dict(out_type=1), dict(out_type=3), dict(scale=0.0),
+    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_stride=504), dict(q_stride=516),
+    dict(prefix_token_stride=60), dict(prefix_token_stride=132), dict(prefix_head_stride=32),
+    dict(prefix_head_stride=68), dict(batch=1 << 30)])
+def test_attention_refuses_arguments(change):
+    assert attn(**change) == mmq.MMQ_ERR_ARG
+    p = {k: v for k, v in change.items() if isinstance(v, (int, float)) and k != "workspace"}
+    if p:   # a size it refuses has no workspace either
+        assert mmq.mmq_shared_prefix_attention_workspace(mmq.mmq_shared_prefix_attention_t(**p)) == 0
+
+
+@pytest.mark.parametrize("name,by", [("q", 8), ("out", 4), ("k_prefix", 2), ("v_prefix", 8), ("k_cache", 4),
+                                     ("v_cache", 2), ("page_table", 2), ("lens", 1), ("workspace", 128)])
+def test_attention_refuses_alignment(name, by):
+    assert attn(**{name: 0x90000 + by}) == mmq.MMQ_ERR_ALIGN
