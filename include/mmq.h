@@ -547,6 +547,47 @@ size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t
 int mmq_shared_prefix_attention(const mmq_shared_prefix_attention_t* p, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* A whole mixture-of-experts FFN on q4_K experts for a few tokens. */
+#define MMQ_MOE_MAX_TOKENS 64
+#define MMQ_MOE_MAX_EXPERTS 256
+#define MMQ_MOE_MAX_PAIRS 512   /* tokens * top_k */
+typedef struct {
+    const float* x;          /* [tokens][model]                                */
+    const float* w_router;   /* [experts][model]                               */
+    const uint8_t* w_gu;     /* q4_K [experts][2 ffn][model / 256][144]: rows
+                              * alternate gate and up (mmq_interleave_rows_q4K
+                              * per expert)                                    */
+    const uint8_t* w_down;   /* q4_K [experts][model][ffn / 256][144]          */
+    const float* residual;   /* [tokens][model] or NULL                        */
+    float* out;              /* [tokens][model]; may be residual or x          */
+    int32_t* ids;            /* [tokens][top_k] chosen experts, best first     */
+    float* weights;          /* [tokens][top_k] their weights                  */
+    int32_t tokens, model, ffn, experts, top_k;
+    int32_t renormalize;     /* 0: w = p; else w = p / the chosen p's sum      */
+} mmq_q4K_moe_t;
+
+/* Device workspace of one call (its sizes only; 0 for sizes the call
+ * refuses).  256-byte aligned, caller-owned, not used by anything else until
+ * the stream passes the call. */
+size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p);
+
+/* Per token: p = softmax(x . w_router^T); the top_k experts with the largest
+ * p (ties: the lower number; a NaN ranks last); w their p, or p over the
+ * chosen p's sum; and
+ *     out = residual + sum over the chosen e of w_e * h_e . Wd_e^T,
+ *     h_e = silu(x . Wg_e^T) * (x . Wu_e^T),  silu(g) = g / (1 + exp(-g)).
+ * The activations x and h are not quantized: each product takes them as the
+ * sum of two fp16 values (within 2^-22 of the value or 2^-32 of the largest of
+ * its 256 neighbours) against the weights' exact integers, with f32 sums, so
+ * the result is that of f32 arithmetic on the dequantized weights.  Only the
+ * chosen experts' weights are read, once per 4 to 16 tokens of an expert.
+ * Results are bitwise the same run to run on one device and build.
+ * tokens 1..64 (0 does nothing), experts 1..256, top_k 1..16 and at most
+ * experts, tokens * top_k at most 512, model and ffn multiples of 256;
+ * pointers 16-byte aligned (ids, weights: 4-byte).  MMQ_ERR_ARG (a small
+ * workspace included) / MMQ_ERR_ALIGN / MMQ_ERR_DEVICE / MMQ_ERR_CUDA. */
+int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test hook: force the K split of the dot-product kernels (q4_K, M <= 4;
  * q6_K, M <= 16) for later calls on this host thread: ks = 1, 2 or 4 warps
  * per row group (the SwiGLU epilogue takes 1 or 2; a forced 4 makes its

@@ -44,6 +44,7 @@ EXPORTS = (
     "mmq_gguf_open", "mmq_gguf_close", "mmq_gguf_tensor_count", "mmq_gguf_find", "mmq_gguf_tensor_info",
     "mmq_gguf_read", "mmq_gguf_write",
     "mmq_qk_norm_rope", "mmq_shared_prefix_attention", "mmq_shared_prefix_attention_workspace",
+    "mmq_q4K_moe", "mmq_q4K_moe_workspace",
     "mmq_status", "mmq_strerror", "mmq_debug_inject_timeout", "mmq_debug_force_gemv_split",
     "mmq_set_programmatic_launch",
 )
@@ -79,6 +80,13 @@ class mmq_shared_prefix_attention_t(ctypes.Structure):
                 ("n_pages", _I64), ("table_width", _I64),
                 ("batch", _I32), ("q_len", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32),
                 ("page_size", _I32), ("type", _I32), ("out_type", _I32), ("scale", ctypes.c_float)]
+
+
+class mmq_q4K_moe_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("x", _P), ("w_router", _P), ("w_gu", _P), ("w_down", _P), ("residual", _P), ("out", _P), ("ids", _P),
+                ("weights", _P), ("tokens", _I32), ("model", _I32), ("ffn", _I32), ("experts", _I32), ("top_k", _I32),
+                ("renormalize", _I32)]
 
 
 _lock = threading.Lock()
@@ -142,6 +150,8 @@ def load_library(path: str = LIB_PATH):
                 "mmq_shared_prefix_attention_workspace": ([ctypes.POINTER(mmq_shared_prefix_attention_t)], S),
                 "mmq_shared_prefix_attention": ([ctypes.POINTER(mmq_shared_prefix_attention_t), P, S, P],
                                                 ctypes.c_int),
+                "mmq_q4K_moe_workspace": ([ctypes.POINTER(mmq_q4K_moe_t)], S),
+                "mmq_q4K_moe": ([ctypes.POINTER(mmq_q4K_moe_t), P, S, P], ctypes.c_int),
                 "mmq_status": ([P], ctypes.c_int),
                 "mmq_strerror": ([ctypes.c_int], ctypes.c_char_p),
                 "mmq_debug_inject_timeout": ([ctypes.c_int], None),
@@ -757,3 +767,58 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     _check(mmq_shared_prefix_attention(p, workspace.data_ptr(), workspace.numel(), _raw_stream(dev, stream)),
            "mmq_shared_prefix_attention")
     return out
+
+
+def mmq_q4K_moe_workspace(p):
+    return load_library().mmq_q4K_moe_workspace(ctypes.byref(p))
+
+
+def mmq_q4K_moe(p, workspace, workspace_bytes, stream):
+    return load_library().mmq_q4K_moe(ctypes.byref(p), workspace, workspace_bytes, stream)
+
+
+def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, residual=None, out=None, workspace=None,
+            stream=None):
+    """A mixture-of-experts FFN on q4_K experts for a few tokens (up to 64).
+
+    x float32 [T][model]; w_router float32 [E][model]; w_gu uint8
+    [E][2 ffn][model/256][144], each expert's gate and up rows interleaved
+    (interleave_rows_q4K); w_down uint8 [E][model][ffn/256][144]; residual
+    float32 [T][model] or None.  Returns (out float32 [T][model], the chosen
+    experts int32 [T][top_k], best first, and their weights float32
+    [T][top_k]: softmax values, divided by their sum if `renormalize`).
+    `workspace`: a CUDA uint8 tensor of mmq_q4K_moe_workspace bytes, allocated
+    per call if None."""
+    import torch
+    T, model = x.shape
+    E = w_router.shape[0]
+    ffn = w_down.shape[2] * 256
+    f32, u8, dev = torch.float32, torch.uint8, x.device
+    _need(x.is_cuda and x.dtype is f32 and x.is_contiguous(), "q4K_moe: x must be contiguous float32 [T][model] on the GPU")
+    _need(w_router.dtype is f32 and w_router.is_contiguous() and w_router.shape == (E, model),
+          "q4K_moe: w_router must be contiguous float32 [E][model]")
+    _need(w_gu.dtype is u8 and w_gu.is_contiguous() and w_gu.shape == (E, 2 * ffn, model // 256, 144)
+          and w_down.dtype is u8 and w_down.is_contiguous() and w_down.shape == (E, model, ffn // 256, 144),
+          "q4K_moe: w_gu must be uint8 [E][2 ffn][model/256][144], w_down [E][model][ffn/256][144]")
+    for t in (w_router, w_gu, w_down, residual, out, workspace):
+        _need(t is None or t.device == dev, "q4K_moe: every tensor must be on x's device")
+    if out is None:
+        out = torch.empty((T, model), dtype=f32, device=dev)
+    for t in (residual, out):
+        _need(t is None or (t.dtype is f32 and t.is_contiguous() and t.shape == (T, model)),
+              "q4K_moe: residual and out must be contiguous float32 [T][model]")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=f32, device=dev)
+    p = mmq_q4K_moe_t(x.data_ptr(), w_router.data_ptr(), w_gu.data_ptr(), w_down.data_ptr(),
+                      None if residual is None else residual.data_ptr(), out.data_ptr(), ids.data_ptr(),
+                      weights.data_ptr(), T, model, ffn, E, top_k, 1 if renormalize else 0)
+    if T == 0:
+        return out, ids, weights
+    if workspace is None:
+        need = mmq_q4K_moe_workspace(p)
+        _need(need > 0, "q4K_moe: sizes")
+        workspace = torch.empty(need, dtype=u8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _check(mmq_q4K_moe(p, workspace.data_ptr(), workspace.numel(), _raw_stream(dev, stream)), "mmq_q4K_moe")
+    return out, ids, weights

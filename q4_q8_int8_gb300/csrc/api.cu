@@ -527,6 +527,43 @@ int mmq_shared_prefix_attention(const mmq_shared_prefix_attention_t* p, void* wo
     return from_cuda(mmq::launch_shared_prefix_attention(*p, workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
+// The sizes of a mixture-of-experts call (no pointers): MMQ_OK or MMQ_ERR_ARG.
+static int check_moe_sizes(const mmq_q4K_moe_t* p) {
+    if (!p) return MMQ_ERR_ARG;
+    if (p->tokens < 0 || p->tokens > MMQ_MOE_MAX_TOKENS || p->experts < 1 || p->experts > MMQ_MOE_MAX_EXPERTS)
+        return MMQ_ERR_ARG;
+    if (p->top_k < 1 || p->top_k > 16 || p->top_k > p->experts || p->tokens * p->top_k > MMQ_MOE_MAX_PAIRS)
+        return MMQ_ERR_ARG;
+    const int32_t kMax = 1 << 20;
+    if (p->model < 256 || p->model % 256 || p->model > kMax || p->ffn < 256 || p->ffn % 256 || p->ffn > kMax)
+        return MMQ_ERR_ARG;
+    return MMQ_OK;
+}
+
+size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p) {
+    if (check_moe_sizes(p) || p->tokens == 0 || check_device()) return 0;
+    return mmq::q4K_moe_workspace(*p);
+}
+
+int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_moe_sizes(p);
+    if (rc) return rc;
+    if (p->tokens == 0) return check_device();
+    if (!p->x || !p->w_router || !p->w_gu || !p->w_down || !p->out || !p->ids || !p->weights || !workspace)
+        return MMQ_ERR_ARG;
+    for (const void* v : {static_cast<const void*>(p->x), static_cast<const void*>(p->w_router),
+                          static_cast<const void*>(p->w_gu), static_cast<const void*>(p->w_down),
+                          static_cast<const void*>(p->residual), static_cast<const void*>(p->out)})
+        if (!aligned16(v)) return MMQ_ERR_ALIGN;
+    if (!aligned4(p->ids) || !aligned4(p->weights)) return MMQ_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return MMQ_ERR_ALIGN;
+    if ((rc = check_device())) return rc;
+    const size_t need = mmq::q4K_moe_workspace(*p);
+    if (need == 0) return MMQ_ERR_CUDA;
+    if (workspace_bytes < need) return MMQ_ERR_ARG;
+    return from_cuda(mmq::launch_q4K_moe(*p, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 int mmq_status(void* stream) {
     int* p = mmq::status_word_ptr();
     if (!p) return MMQ_ERR_CUDA;

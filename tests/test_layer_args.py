@@ -41,6 +41,8 @@ def test_null_structs():
     assert mmq.load_library().mmq_qk_norm_rope(None, None) == mmq.MMQ_ERR_ARG
     assert mmq.load_library().mmq_shared_prefix_attention(None, None, 0, None) == mmq.MMQ_ERR_ARG
     assert mmq.load_library().mmq_shared_prefix_attention_workspace(None) == 0
+    assert mmq.load_library().mmq_q4K_moe(None, None, 0, None) == mmq.MMQ_ERR_ARG
+    assert mmq.load_library().mmq_q4K_moe_workspace(None) == 0
 
 
 def attn(workspace=0x100, ws_bytes=1 << 40, **change):
@@ -72,3 +74,25 @@ def test_attention_refuses_arguments(change):
                                      ("v_cache", 2), ("page_table", 2), ("lens", 1), ("workspace", 128)])
 def test_attention_refuses_alignment(name, by):
     assert attn(**{name: 0x90000 + by}) == mmq.MMQ_ERR_ALIGN
+
+
+def moe(workspace=0x100, ws_bytes=1 << 40, **change):
+    f = dict(x=0x10000, w_router=0x20000, w_gu=0x30000, w_down=0x40000, residual=None, out=0x50000, ids=0x60000,
+             weights=0x70000, tokens=4, model=512, ffn=256, experts=8, top_k=2, renormalize=1)
+    f.update(change)
+    return mmq.mmq_q4K_moe(mmq.mmq_q4K_moe_t(**f), workspace, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(x=None), dict(w_router=None), dict(w_gu=None), dict(w_down=None), dict(out=None), dict(ids=None),
+    dict(weights=None), dict(workspace=None), dict(tokens=-1), dict(tokens=65), dict(model=0), dict(model=384),
+    dict(ffn=0), dict(ffn=300), dict(experts=0), dict(experts=257), dict(top_k=0), dict(top_k=9),
+    dict(top_k=17, experts=64), dict(tokens=64, top_k=9, experts=16), dict(model=1 << 21), dict(ffn=1 << 21)])
+def test_moe_refuses_arguments(change):
+    assert moe(**change) == mmq.MMQ_ERR_ARG
+
+
+@pytest.mark.parametrize("name,by", [("x", 8), ("w_router", 4), ("w_gu", 1), ("w_down", 8), ("residual", 4), ("out", 8),
+                                     ("ids", 2), ("weights", 1), ("workspace", 128)])
+def test_moe_refuses_alignment(name, by):
+    assert moe(**{name: 0x90000 + by}) == mmq.MMQ_ERR_ALIGN
