@@ -636,25 +636,22 @@ def mmq_qk_norm_rope(p, stream):
     return load_library().mmq_qk_norm_rope(ctypes.byref(p), stream)
 
 
-def _type16(t) -> int:
+def _refuse(what: str):
+    raise MMQError(MMQ_ERR_ARG, what)
+
+
+_t = None   # torch, imported by the first call of one of these
+
+
+def _torch():
+    global _t
     import torch
-    if t.dtype == torch.float16:
-        return MMQ_TYPE_F16
-    if t.dtype == torch.bfloat16:
-        return MMQ_TYPE_BF16
-    raise MMQError(MMQ_ERR_ARG, f"float16 or bfloat16 expected, got {t.dtype}")
+    _t = torch
+    return torch
 
 
-def _need(ok, what: str):
-    if not ok:
-        raise MMQError(MMQ_ERR_ARG, what)
-
-
-def _raw_stream(device, stream):
-    import torch
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
-
-
+# One new token costs these calls a few microseconds on the device, so each
+# checks its arguments in a few flat expressions and calls the library once.
 def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
                  eps: float = 1e-6, interleaved: bool = False, sections=None, out=None, stream=None):
     """Head norms, rotary positions and the cache write after a fused q/k/v projection.
@@ -667,40 +664,53 @@ def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, 
     q_weight, k_weight float32 [D] or None for no norm.  Returns the query
     heads [T][heads][D] in the cache's type.  A position or slot out of range
     shows in status()."""
-    import torch
-    kind = _type16(k_cache)
-    kv_heads, D = k_cache.shape[-2:]
+    torch = _t or _torch()
+    f32, i32, dt, dev = torch.float32, torch.int32, k_cache.dtype, qkv.get_device()
+    kc = k_cache.shape
+    kv_heads, D = kc[-2], kc[-1]
     T, width = qkv.shape
-    f32, i32 = torch.float32, torch.int32
-    _need(qkv.is_cuda and qkv.dtype is f32 and qkv.stride(1) == 1 and width == (heads + 2 * kv_heads) * D,
-          "qk_norm_rope: qkv must be float32 [T][(heads + 2 kv_heads) D] on the GPU")
-    _need(v_cache.dtype is k_cache.dtype and v_cache.shape == k_cache.shape and k_cache.is_contiguous()
-          and v_cache.is_contiguous(), "qk_norm_rope: k_cache and v_cache must be alike and contiguous")
-    _need(cos.dtype is f32 and sin.dtype is f32 and cos.dim() == 2 and cos.shape == sin.shape
-          and cos.is_contiguous() and sin.is_contiguous(), "qk_norm_rope: cos and sin must be float32 [rows][R/2]")
-    half = cos.shape[1]
-    parts = [half] if sections is None else list(sections)
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _need(positions.dtype is i32 and positions.is_contiguous() and positions.numel() == axes * T
-          and 1 <= len(parts) <= 4 and len(parts) == axes and sum(parts) == half,
-          "qk_norm_rope: positions must be int32 [T] or [axes][T], one section per axis, sections adding up to R/2")
-    _need(slots.dtype is i32 and slots.is_contiguous() and slots.numel() == T, "qk_norm_rope: slots must be int32 [T]")
+    ld, step = qkv.stride()
+    if dt is torch.float16:
+        kind = MMQ_TYPE_F16
+    elif dt is torch.bfloat16:
+        kind = MMQ_TYPE_BF16
+    else:
+        _refuse("qk_norm_rope: the caches must be float16 or bfloat16")
+    if dev < 0 or qkv.dtype is not f32 or step != 1 or width != (heads + 2 * kv_heads) * D:
+        _refuse("qk_norm_rope: qkv must be float32 [T][(heads + 2 kv_heads) D] on the GPU")
+    if (v_cache.dtype is not dt or v_cache.shape != kc or not k_cache.is_contiguous() or not v_cache.is_contiguous()
+            or k_cache.get_device() != dev or v_cache.get_device() != dev):
+        _refuse("qk_norm_rope: k_cache and v_cache must be alike and contiguous, on qkv's device")
+    table = cos.shape
+    if (len(table) != 2 or sin.shape != table or cos.dtype is not f32 or sin.dtype is not f32
+            or not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != dev or sin.get_device() != dev):
+        _refuse("qk_norm_rope: cos and sin must be contiguous float32 [rows][R/2] on qkv's device")
+    rows, half = table
+    axes = 1 if sections is None else len(sections)
+    if (positions.dtype is not i32 or not positions.is_contiguous() or positions.numel() != axes * T
+            or positions.get_device() != dev or slots.dtype is not i32 or not slots.is_contiguous()
+            or slots.numel() != T or slots.get_device() != dev or axes < 1 or axes > 4
+            or (sections is not None and sum(sections) != half) or (positions.dim() == 2 and positions.shape[0] != axes)):
+        _refuse("qk_norm_rope: positions must be int32 [T] or [axes][T] with one section per axis (adding up to R/2), "
+                "slots int32 [T], on qkv's device")
     for w in (q_weight, k_weight):
-        _need(w is None or (w.dtype is f32 and w.is_contiguous() and w.numel() == D),
-              "qk_norm_rope: a norm weight must be float32 [D]")
-    for t in (k_cache, v_cache, cos, sin, positions, slots, q_weight, k_weight, out):
-        _need(t is None or t.device == qkv.device, "qk_norm_rope: every tensor must be on qkv's device")
+        if w is not None and (w.dtype is not f32 or not w.is_contiguous() or w.numel() != D or w.get_device() != dev):
+            _refuse("qk_norm_rope: a norm weight must be float32 [D] on qkv's device")
     if out is None:
-        out = torch.empty((T, heads, D), dtype=k_cache.dtype, device=qkv.device)
-    _need(out.dtype is k_cache.dtype and out.is_contiguous() and out.shape == (T, heads, D),
-          "qk_norm_rope: out must be contiguous [T][heads][D] of the cache's type")
+        out = torch.empty((T, heads, D), dtype=dt, device=qkv.device)
+    elif (out.dtype is not dt or not out.is_contiguous() or out.shape != (T, heads, D) or out.get_device() != dev):
+        _refuse("qk_norm_rope: out must be contiguous [T][heads][D] of the cache's type, on qkv's device")
     p = mmq_qk_norm_rope_t(
         qkv.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
         cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-        qkv.stride(0) if T > 1 else width, T, cos.shape[0], k_cache.numel() // max(1, kv_heads * D),
-        heads, kv_heads, D, 2 * half, (_I32 * 4)(*parts), 1 if interleaved else 0, kind, eps)
-    _check(mmq_qk_norm_rope(p, _raw_stream(qkv.device, stream)), "mmq_qk_norm_rope")
+        ld if T > 1 else width, T, rows, k_cache.numel() // (kv_heads * D) if kv_heads * D else 0,
+        heads, kv_heads, D, 2 * half, (half,) if sections is None else tuple(sections),
+        1 if interleaved else 0, kind, eps)
+    rc = (_lib or load_library()).mmq_qk_norm_rope(
+        p, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_qk_norm_rope")
     return out
 
 
@@ -725,48 +735,71 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     default.  Returns [batch q_len][heads][D] in q's type, or into `out`
     (which may also be float32).  `workspace`: a CUDA uint8 tensor of
     mmq_shared_prefix_attention_workspace bytes, allocated per call if None."""
-    import torch
-    kind = _type16(q)
-    T, heads, D = q.shape
-    P, kv_heads = k_prefix.shape[:2]
-    n_pages, page_size = k_cache.shape[:2]
+    torch = _t or _torch()
+    dt, dev, i32 = q.dtype, q.get_device(), torch.int32
+    if dt is torch.float16:
+        kind = MMQ_TYPE_F16
+    elif dt is torch.bfloat16:
+        kind = MMQ_TYPE_BF16
+    else:
+        _refuse("shared_prefix_attention: q must be float16 or bfloat16")
+    qs = q.shape
+    T, heads, D = qs
+    P, kv_heads, pd = k_prefix.shape
+    n_pages, page_size, ch, cd = k_cache.shape
     batch, width = page_table.shape
-    dt, dev = q.dtype, q.device
-    _need(q.is_cuda and q.stride(2) == 1 and q.stride(1) == D and T == batch * q_len,
-          "shared_prefix_attention: q must be [batch q_len][heads][D] on the GPU, heads contiguous")
-    _need(k_prefix.dtype is dt and v_prefix.dtype is dt and v_prefix.shape == k_prefix.shape and k_prefix.shape[2] == D
-          and (P == 0 or (k_prefix.stride() == v_prefix.stride() and k_prefix.stride(2) == 1)),
-          "shared_prefix_attention: k_prefix and v_prefix must be alike, [P][kv_heads][D] in q's type")
-    _need(k_cache.dtype is dt and v_cache.dtype is dt and v_cache.shape == k_cache.shape
-          and k_cache.shape[2:] == (kv_heads, D) and k_cache.is_contiguous() and v_cache.is_contiguous(),
-          "shared_prefix_attention: the caches must be contiguous [pages][page_size][kv_heads][D] in q's type")
-    _need(page_table.dtype is torch.int32 and page_table.is_contiguous() and lens.dtype is torch.int32
-          and lens.is_contiguous() and lens.numel() == batch,
-          "shared_prefix_attention: page_table must be int32 [batch][width], lens int32 [batch]")
-    for t in (k_prefix, v_prefix, k_cache, v_cache, page_table, lens, out, workspace):
-        _need(t is None or t.device == dev, "shared_prefix_attention: every tensor must be on q's device")
+    q_step, q_head, q_one = q.stride()
+    k_step, k_head, k_one = k_prefix.stride()
+    if dev < 0 or q_one != 1 or q_head != D or T != batch * q_len:
+        _refuse("shared_prefix_attention: q must be [batch q_len][heads][D] on the GPU, its heads contiguous")
+    if (k_prefix.dtype is not dt or v_prefix.dtype is not dt or v_prefix.shape != k_prefix.shape or pd != D
+            or k_prefix.get_device() != dev or v_prefix.get_device() != dev
+            or (P and (k_one != 1 or v_prefix.stride() != (k_step, k_head, 1)))):
+        _refuse("shared_prefix_attention: k_prefix and v_prefix must be alike, [P][kv_heads][D] in q's type, on q's device")
+    if (k_cache.dtype is not dt or v_cache.dtype is not dt or v_cache.shape != k_cache.shape or ch != kv_heads or cd != D
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous() or k_cache.get_device() != dev
+            or v_cache.get_device() != dev):
+        _refuse("shared_prefix_attention: the caches must be contiguous [pages][page_size][kv_heads][D] in q's type, on "
+                "q's device")
+    if (page_table.dtype is not i32 or not page_table.is_contiguous() or page_table.get_device() != dev
+            or lens.dtype is not i32 or not lens.is_contiguous() or lens.numel() != batch or lens.get_device() != dev):
+        _refuse("shared_prefix_attention: page_table must be int32 [batch][width], lens int32 [batch], on q's device")
     if out is None:
-        out = torch.empty((T, heads, D), dtype=dt, device=dev)
-    _need(out.shape == q.shape and out.is_contiguous() and (out.dtype is dt or out.dtype is torch.float32),
-          "shared_prefix_attention: out must be contiguous [batch q_len][heads][D] in q's type or float32")
+        out = torch.empty(qs, dtype=dt, device=q.device)
+        out_kind = kind
+    else:
+        out_kind = MMQ_TYPE_F32 if out.dtype is torch.float32 else kind
+        if (out.shape != qs or not out.is_contiguous() or out.get_device() != dev
+                or (out.dtype is not dt and out_kind != MMQ_TYPE_F32)):
+            _refuse("shared_prefix_attention: out must be contiguous [batch q_len][heads][D] in q's type or float32")
+    if batch == 0:
+        return out
     p = mmq_shared_prefix_attention_t(
         q.data_ptr(), out.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         page_table.data_ptr(), lens.data_ptr(),
-        q.stride(0) if T > 1 else heads * D, P, k_prefix.stride(0) if P > 1 else kv_heads * D,
-        k_prefix.stride(1) if kv_heads > 1 else D, n_pages, width,
-        batch, q_len, heads, kv_heads, D, page_size, kind, kind if out.dtype is dt else MMQ_TYPE_F32,
+        q_step if T > 1 else heads * D, P, k_step if P > 1 else kv_heads * D, k_head if kv_heads > 1 else D,
+        n_pages, width, batch, q_len, heads, kv_heads, D, page_size, kind, out_kind,
         D ** -0.5 if scale is None else scale)
-    if batch == 0:
-        return out
+    lib = _lib or load_library()
     if workspace is None:
-        need = mmq_shared_prefix_attention_workspace(p)
-        _need(need > 0, "shared_prefix_attention: sizes")
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
-    _check(mmq_shared_prefix_attention(p, workspace.data_ptr(), workspace.numel(), _raw_stream(dev, stream)),
-           "mmq_shared_prefix_attention")
+        workspace = _workspace(lib.mmq_shared_prefix_attention_workspace(p), q.device, stream, "shared_prefix_attention")
+    elif workspace.get_device() != dev:
+        _refuse("shared_prefix_attention: workspace must be on q's device")
+    rc = lib.mmq_shared_prefix_attention(
+        p, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_shared_prefix_attention")
     return out
+
+
+def _workspace(need: int, device, stream, what: str):
+    if not need:
+        _refuse(f"{what}: sizes")
+    ws = _t.empty(need, dtype=_t.uint8, device=device)
+    if stream is not None:   # the allocator knows the current stream only
+        ws.record_stream(stream)
+    return ws
 
 
 def mmq_q4K_moe_workspace(p):
@@ -789,36 +822,42 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
     [T][top_k]: softmax values, divided by their sum if `renormalize`).
     `workspace`: a CUDA uint8 tensor of mmq_q4K_moe_workspace bytes, allocated
     per call if None."""
-    import torch
-    T, model = x.shape
-    E = w_router.shape[0]
-    ffn = w_down.shape[2] * 256
-    f32, u8, dev = torch.float32, torch.uint8, x.device
-    _need(x.is_cuda and x.dtype is f32 and x.is_contiguous(), "q4K_moe: x must be contiguous float32 [T][model] on the GPU")
-    _need(w_router.dtype is f32 and w_router.is_contiguous() and w_router.shape == (E, model),
-          "q4K_moe: w_router must be contiguous float32 [E][model]")
-    _need(w_gu.dtype is u8 and w_gu.is_contiguous() and w_gu.shape == (E, 2 * ffn, model // 256, 144)
-          and w_down.dtype is u8 and w_down.is_contiguous() and w_down.shape == (E, model, ffn // 256, 144),
-          "q4K_moe: w_gu must be uint8 [E][2 ffn][model/256][144], w_down [E][model][ffn/256][144]")
-    for t in (w_router, w_gu, w_down, residual, out, workspace):
-        _need(t is None or t.device == dev, "q4K_moe: every tensor must be on x's device")
+    torch = _t or _torch()
+    f32, u8, dev, device = torch.float32, torch.uint8, x.get_device(), x.device
+    xs = x.shape
+    T, model = xs
+    E, rm = w_router.shape
+    ge, gf, gs, gb = w_gu.shape
+    de, dm, ds, db = w_down.shape
+    if dev < 0 or x.dtype is not f32 or not x.is_contiguous():
+        _refuse("q4K_moe: x must be contiguous float32 [T][model] on the GPU")
+    if w_router.dtype is not f32 or not w_router.is_contiguous() or rm != model or w_router.get_device() != dev:
+        _refuse("q4K_moe: w_router must be contiguous float32 [E][model] on x's device")
+    if (w_gu.dtype is not u8 or not w_gu.is_contiguous() or ge != E or gf != 512 * ds or gs * 256 != model or gb != 144
+            or w_down.dtype is not u8 or not w_down.is_contiguous() or de != E or dm != model or db != 144
+            or w_gu.get_device() != dev or w_down.get_device() != dev):
+        _refuse("q4K_moe: w_gu must be uint8 [E][2 ffn][model/256][144], w_down [E][model][ffn/256][144], on x's device")
+    if residual is not None and (residual.dtype is not f32 or not residual.is_contiguous() or residual.shape != xs
+                                 or residual.get_device() != dev):
+        _refuse("q4K_moe: residual must be contiguous float32 [T][model] on x's device")
     if out is None:
-        out = torch.empty((T, model), dtype=f32, device=dev)
-    for t in (residual, out):
-        _need(t is None or (t.dtype is f32 and t.is_contiguous() and t.shape == (T, model)),
-              "q4K_moe: residual and out must be contiguous float32 [T][model]")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=f32, device=dev)
-    p = mmq_q4K_moe_t(x.data_ptr(), w_router.data_ptr(), w_gu.data_ptr(), w_down.data_ptr(),
-                      None if residual is None else residual.data_ptr(), out.data_ptr(), ids.data_ptr(),
-                      weights.data_ptr(), T, model, ffn, E, top_k, 1 if renormalize else 0)
+        out = torch.empty(xs, dtype=f32, device=device)
+    elif out.dtype is not f32 or not out.is_contiguous() or out.shape != xs or out.get_device() != dev:
+        _refuse("q4K_moe: out must be contiguous float32 [T][model] on x's device")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+    weights = torch.empty((T, top_k), dtype=f32, device=device)
     if T == 0:
         return out, ids, weights
+    p = mmq_q4K_moe_t(x.data_ptr(), w_router.data_ptr(), w_gu.data_ptr(), w_down.data_ptr(),
+                      None if residual is None else residual.data_ptr(), out.data_ptr(), ids.data_ptr(),
+                      weights.data_ptr(), T, model, 256 * ds, E, top_k, 1 if renormalize else 0)
+    lib = _lib or load_library()
     if workspace is None:
-        need = mmq_q4K_moe_workspace(p)
-        _need(need > 0, "q4K_moe: sizes")
-        workspace = torch.empty(need, dtype=u8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
-    _check(mmq_q4K_moe(p, workspace.data_ptr(), workspace.numel(), _raw_stream(dev, stream)), "mmq_q4K_moe")
+        workspace = _workspace(lib.mmq_q4K_moe_workspace(p), device, stream, "q4K_moe")
+    elif workspace.get_device() != dev:
+        _refuse("q4K_moe: workspace must be on x's device")
+    rc = lib.mmq_q4K_moe(p, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_q4K_moe")
     return out, ids, weights
