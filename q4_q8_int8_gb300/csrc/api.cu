@@ -561,7 +561,9 @@ int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes,
     const size_t need = mmq::q4K_moe_workspace(*p);
     if (need == 0) return MMQ_ERR_CUDA;
     if (workspace_bytes < need) return MMQ_ERR_ARG;
-    return from_cuda(mmq::launch_q4K_moe(*p, workspace, static_cast<cudaStream_t>(stream)));
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_q4K_moe(*p, workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
 int mmq_status(void* stream) {

@@ -30,14 +30,10 @@ using namespace mmq::tc;
 constexpr int kMaxTokens = MMQ_MOE_MAX_TOKENS;
 constexpr int kMaxExperts = MMQ_MOE_MAX_EXPERTS;
 constexpr int kMaxPairs = MMQ_MOE_MAX_PAIRS;
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kBlk = 144;     // bytes of a q4_K super-block
-constexpr int kStages = 4;    // super-blocks per row in flight per warp
-
-// One (super-block, group of four tokens) of activations in shared memory, in
-// the order the matrix instructions take them: 8 steps x 32 lanes x 16 bytes,
-// then the sub-block sums, 32 lanes x 4 bytes, then the four tokens' 2^e.
-constexpr int kAct = 8 * 512 + 128 + 16;
+constexpr int kStages = 4;    // weight tiles (16 rows x one super-block) in flight per warp
+constexpr int kTile = 16 * kBlk;
 
 // Which tokens go to which expert: pair i = token i / top_k, its i % top_k-th
 // expert; order lists the pairs by expert.
@@ -51,11 +47,11 @@ struct Plan {
 struct MoeArgs {
     mmq_q4K_moe_t p;
     float* logits;   // [tokens][experts]
-    Plan* plan;
-    float* h;        // [pairs][ffn], rows in the plan's order
-    float* y;        // [slices][pairs][model], rows by pair
-    int slices;      // parts of the down product's sum over ffn
-    int act_sb;      // super-blocks of activations held at once
+    float* h;        // first product, rows in the plan's order: h [pairs][ffn], or if its sum is in
+                     // parts [gu_slices][pairs][2 ffn] of gate and up, alternating
+    float* y;        // second product [down_slices][pairs][model], rows by pair
+    int gu_slices, down_slices;
+    int* status;
 };
 
 // ----------------------------------------------------------------- router
@@ -149,18 +145,19 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* i
     if (store && lane < p.top_k) p.weights[t * p.top_k + lane] = mine / (p.renormalize ? picked : sum);
 }
 
-// Fill `plan` (shared memory) from the logits; block 0 also stores it, the
-// chosen experts and their weights.  scratch: kMaxPairs + 2 * kWarps ints.
-__device__ void make_plan(const MoeArgs& a, Plan* plan, int* scratch) {
+// Fill `plan` (shared memory) from the logits; `store`: also the chosen
+// experts and their weights to the caller.  scratch: kMaxPairs + 2 * kWarps ints.
+__device__ void make_plan(const MoeArgs& a, Plan* plan, int* scratch, bool store) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* ids = scratch;
     int* totals = scratch + kMaxPairs;
-    for (int t = warp; t < a.p.tokens; t += kWarps) choose(a, t, lane, ids, blockIdx.x == 0);
+    for (int t = warp; t < a.p.tokens; t += kWarps) choose(a, t, lane, ids, store);
     __syncthreads();
-    static_assert(kMaxExperts == kThreads, "one thread per expert");
+    static_assert(kMaxExperts <= kThreads, "one thread per expert");
     const int e = threadIdx.x, pairs = a.p.tokens * a.p.top_k;
     int n = 0;
-    for (int i = 0; i < pairs; ++i) n += ids[i] == e;
+    if (e < a.p.experts)
+        for (int i = 0; i < pairs; ++i) n += ids[i] == e;
     // exclusive prefixes over the experts: of the pairs, and of the active ones
     int before = n;
 #pragma unroll
@@ -198,23 +195,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
     asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
@@ -223,6 +208,7 @@ __device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ float silu_times(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
 
 // One row's part in a lane: lane t of a row's four holds sub-blocks 2t and
 // 2t + 1, the low and high nibbles of the row's bytes 32 t .. 32 t + 31.
@@ -257,289 +243,296 @@ __device__ __forceinline__ void unpack_hi(uint32_t w, const RowScale& r, uint32_
     x13 = h2u(__hfma2(u2h(((w >> 8) & 0x00F000F0u) | 0x64006400u), r.s_hi, r.b_hi));
 }
 
-// One warp: 256 f32 activations of one token into column pair `tok` (0..3) of
-// one activation block at shared address `blk`.
-__device__ __forceinline__ void put_act(const float* x, uint32_t blk, int tok, int lane) {
-    const float4 v[2] = {reinterpret_cast<const float4*>(x)[lane], reinterpret_cast<const float4*>(x)[lane + 32]};
+// A group of four tokens' activations of one super-block, as the second
+// operand of the matrix instructions: column 2 i is token i's hi, 2 i + 1 its
+// lo, so lane (column g, t) holds one part of the values of sub-blocks 2t and
+// 2t + 1 of token g / 2: step w takes values 4w .. 4w + 3 of both, in the order
+// 0, 2, 1, 3 that unpacking the nibbles gives.
+struct Act {
+    uint32_t b[8][4];
+    uint32_t sums;   // the two sub-blocks' sums
+    float up;        // token t's 2^e (the lane's column of the result)
+};
+template <typename Load>   // load(i): values 4 i .. 4 i + 3 of the lane's 64, f32
+__device__ __forceinline__ void make_act(Act& act, int lane, Load load) {
     float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+#pragma unroll 8
+    for (int i = 0; i < 16; ++i) {
+        const float4 v = load(i);
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // 2^e with top 2^-e in [128, 256), e from -126 on
     int e = int(__float_as_uint(top) >> 23) - 127 - 7;
     e = e < -126 ? -126 : e;
-    const float up = __uint_as_float(uint32_t(127 + e) << 23), down = __uint_as_float(uint32_t(127 - e) << 23);
+    const float down = __uint_as_float(uint32_t(127 - e) << 23);
+    const bool is_lo = (lane >> 2) & 1;
+    auto part = [&](float f) {
+        const __half hi = __float2half_rn(f);
+        return is_lo ? __float2half_rn(f - __half2float(hi)) : hi;
+    };
+    __half sums[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int quad = lane + 32 * i, sub = quad >> 3, w = quad & 7;
-        const float f[4] = {v[i].x * down, v[i].y * down, v[i].z * down, v[i].w * down};
-        __half hi[4], lo[4];
+    for (int c = 0; c < 2; ++c) {
+        float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            hi[k] = __float2half_rn(f[k]);
-            lo[k] = __float2half_rn(f[k] - __half2float(hi[k]));
+        for (int w = 0; w < 8; ++w) {
+            const float4 u = load(8 * c + w);
+            const float f[4] = {u.x * down, u.y * down, u.z * down, u.w * down};
+            act.b[w][2 * c] = h2u(__halves2half2(part(f[0]), part(f[2])));
+            act.b[w][2 * c + 1] = h2u(__halves2half2(part(f[1]), part(f[3])));
+            s += (f[0] + f[1]) + (f[2] + f[3]);
         }
-        const uint32_t at = blk + uint32_t(((w * 8 + 2 * tok) * 4 + (sub >> 1)) * 16 + (sub & 1) * 8);
-        const uint32_t h0 = h2u(__halves2half2(hi[0], hi[2])), h1 = h2u(__halves2half2(hi[1], hi[3]));
-        const uint32_t l0 = h2u(__halves2half2(lo[0], lo[2])), l1 = h2u(__halves2half2(lo[1], lo[3]));
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + 64u), "r"(l0), "r"(l1) : "memory");
-        float s = (f[0] + f[1]) + (f[2] + f[3]);
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        if (w == 0) {
-            const __half sh = __float2half_rn(s), sl = __float2half_rn(s - __half2float(sh));
-            const uint32_t xa = blk + 4096u + uint32_t((2 * tok * 4 + (sub >> 1)) * 4 + (sub & 1) * 2);
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(xa), "h"(__half_as_ushort(sh)) : "memory");
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(xa + 16u), "h"(__half_as_ushort(sl)) : "memory");
-        }
+        sums[c] = part(s);
     }
-    if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(blk + 4224u + 4u * uint32_t(tok)), "f"(up) : "memory");
+    act.sums = h2u(__halves2half2(sums[0], sums[1]));
+    act.up = __shfl_sync(0xffffffffu, __uint_as_float(uint32_t(127 + e) << 23), 8 * (lane & 3));
 }
 
-__host__ __device__ constexpr int act_bytes(int sb, int ng) { return sb * ng * kAct; }
-__host__ __device__ constexpr int ring_bytes(int mt) { return kWarps * kStages * 16 * mt * kBlk; }
-__host__ __device__ constexpr int red_pitch(int mt) { return 16 * mt + 4; }
-__host__ __device__ constexpr int red_bytes(int ng, int mt) { return kWarps * 4 * ng * red_pitch(mt) * 4; }
+constexpr int kRedPitch = 24;   // floats per token: 16 rows, and no two lanes on one bank
+template <int NG>
+struct Smem {
+    static constexpr int kBatch = 2 / NG;                                     // tiles per team and barrier
+    static constexpr int kRed = kBatch * kWarps * 4 * NG * kRedPitch * 4;     // one buffer of partial sums
+    static constexpr int kRing = kWarps * kStages * kTile;
+    static constexpr int kBytes = kRing + 2 * kRed + 128;                     // + alignment
+};
+static_assert(Smem<1>::kBytes <= 200 * 1024 && Smem<2>::kBytes <= 200 * 1024, "shared memory budget");
 
-// Both products of the experts.  A CTA walks items, (active expert, slice of
-// the sum, block of rows), consecutive ones so that the activations it holds
-// in shared memory change rarely; a team of KS warps owns 16 MT rows of an
-// item, its warps taking every KS-th super-block, and 4 NG tokens at a time.
-// Each warp streams its rows' super-blocks through its own cp.async ring,
-// which runs on over the items.
-template <int NG, int MT, int KS, bool kDown>
-__global__ void __launch_bounds__(kThreads) moe_expert_kernel(const MoeArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+// Both products of the experts.  Activations are stationary: a warp keeps the
+// operand of one super-block for 4 NG tokens in registers and streams weight
+// tiles (16 rows x that super-block, 2304 bytes, one TMA box) through a ring of
+// its own; the KS warps of a team hold the KS super-blocks of a row (a slice of
+// it, where it has more than 16), so a team reads whole rows, and their partial
+// sums of a tile are joined through shared memory, in a fixed order.  One CTA
+// per SM; the row tiles of all active experts are dealt out in equal
+// consecutive runs, a run being one (expert, slice).
+template <int NG, bool kDown>
+__global__ void __launch_bounds__(kThreads, 1)
+moe_expert_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ Plan plan;
     __shared__ int scratch[kMaxPairs + 2 * kWarps];
+    __shared__ uint64_t bars[kWarps * kStages];
+    __shared__ uint32_t abort_word;
     const mmq_q4K_moe_t& p = a.p;
-    griddep_launch_dependents();
-    griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int ks = warp % KS, team = warp / KS;
-    constexpr int kRows = 16 * MT, kBlockRows = kRows * (kWarps / KS), kTok = 4 * NG;
-
+    const AbortFlag abort_flag{smem_u32(&abort_word)};
+    const uint32_t bar0 = smem_u32(&bars[warp * kStages]);
+    if (threadIdx.x == 0) abort_flag.set(0u);
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(bar0 + 8u * uint32_t(i), 1);
+        fence_barrier_init();
+        if (warp == 0) prefetch_tmap(&map);
+    }
+    // The logits are complete before the second product starts: the first one
+    // lets it be scheduled only after its own wait for the router.
     if (!kDown) {
-        make_plan(a, &plan, scratch);
-        if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < int(sizeof(Plan) / 4); i += kThreads)
-                reinterpret_cast<int*>(a.plan)[i] = reinterpret_cast<const int*>(&plan)[i];
+        griddep_wait();
+        griddep_launch_dependents();
     } else {
-        for (int i = threadIdx.x; i < int(sizeof(Plan) / 4); i += kThreads)
-            reinterpret_cast<int*>(&plan)[i] = reinterpret_cast<const int*>(a.plan)[i];
-        __syncthreads();
+        griddep_launch_dependents();
     }
+    make_plan(a, &plan, scratch, !kDown && blockIdx.x == 0);
 
-    const int rows = kDown ? p.model : 2 * p.ffn, inner = kDown ? p.ffn : p.model;
-    const int nsb = inner / 256;
-    const int64_t pitch = int64_t(nsb) * kBlk;
-    const uint8_t* const weights = kDown ? p.w_down : p.w_gu;
-    const int blocks = (rows + kBlockRows - 1) / kBlockRows;
-    const int slices = kDown ? a.slices : 1;
-    const int per = (nsb + slices - 1) / slices;
-    const int64_t items = int64_t(plan.active) * slices * blocks;
-    const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+    const int rows = kDown ? p.model : 2 * p.ffn, nsb = (kDown ? p.ffn : p.model) / 256;
+    const int slices = kDown ? a.down_slices : a.gu_slices;
+    const int per = (nsb + slices - 1) / slices, teams = kWarps / per;
+    const int team = warp / per, ks = warp - team * per;
+    const int tiles = rows / 16;
+    const int64_t total = int64_t(plan.active) * slices * tiles;
+    const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
+    constexpr int kTok = 4 * NG, kBatch = Smem<NG>::kBatch;
 
-    const uint32_t act = smem_u32(smem);
-    const uint32_t ring = act + uint32_t(act_bytes(a.act_sb, NG)) + uint32_t(warp * kStages * kRows * kBlk);
-    float* const red = reinterpret_cast<float*>(smem + act_bytes(a.act_sb, NG) + ring_bytes(MT));
-
-    // A position in this warp's stream: item, pass over its tokens, super-block.
-    struct At {
-        int64_t item;
-        int pass, passes, sb, sb0, sb1;
-        const uint8_t* row;   // the team's first row
-    };
-    auto enter = [&](At& s) {   // item s.item, pass 0
-        const int64_t q = s.item / blocks;
-        const int act_i = int(q / slices), slice = int(q % slices), block = int(s.item % blocks);
-        const int n = plan.start[act_i + 1] - plan.start[act_i];
-        s.pass = 0;
-        s.passes = (n + kTok - 1) / kTok;
-        s.sb0 = slice * per;
-        s.sb1 = min(nsb, s.sb0 + per);
-        s.sb = s.sb0 + ks;
-        s.row = weights + (int64_t(plan.expert[act_i]) * rows + int64_t(block) * kBlockRows + team * kRows) * pitch;
-    };
-    // Skips to the next position with a super-block for this warp.
-    auto settle = [&](At& s) {
-        while (s.item < i1 && s.sb >= s.sb1) {
-            s.sb = s.sb0 + ks;
-            if (++s.pass >= s.passes) {
-                if (++s.item < i1) enter(s);
-            } else if (s.sb >= s.sb1) {
-                s.pass = s.passes;   // this warp has none in this slice
-            }
+    // Where a warp's weight stream is: a run's tiles team, team + teams, ... ,
+    // once per pass over the run's tokens.
+    struct Stream {
+        int64_t at;          // first tile of the run
+        int count, tile;     // tiles of the run, the next one
+        int passes, x, y;    // passes left, box coordinates of the run's first tile
+    } in;
+    auto enter = [&]() {   // the run that starts at tile in.at; skips runs without a tile for this warp
+        while (in.at < i1) {
+            const int64_t q = in.at / tiles;
+            const int first = int(in.at - q * tiles), act = int(q / slices), slice = int(q - int64_t(act) * slices);
+            in.count = int(min(int64_t(tiles - first), i1 - in.at));
+            in.passes = (plan.start[act + 1] - plan.start[act] + kTok - 1) / kTok;
+            in.x = (slice * per + ks) * kBlk;
+            in.y = plan.expert[act] * rows + first * 16;
+            in.tile = team;
+            if (team < in.count && slice * per + ks < nsb) return;
+            in.at += in.count;
         }
     };
-    At in = {i0, 0, 0, 0, 0, 0, nullptr};
-    if (i0 < i1) {
-        enter(in);
-        settle(in);
-    }
-    int in_stage = 0, out_stage = 0;
-    auto issue = [&]() {
-        if (in.item < i1) {
-            const int left = rows - (int(in.item % blocks) * kBlockRows + team * kRows);
-            const uint8_t* src = in.row + int64_t(in.sb) * kBlk;
-            const uint32_t dst = ring + uint32_t(in_stage * kRows * kBlk);
-#pragma unroll
-            for (int j = 0; j < (kRows * 9 + 31) / 32; ++j) {
-                const int c = lane + 32 * j, r = c / 9, o = (c - r * 9) * 16;
-                if (c < kRows * 9 && r < left) cp_async16(dst + uint32_t(r * kBlk + o), src + r * pitch + o);
-            }
-            in.sb += KS;
-            settle(in);
-        }
-        cp_async_commit();
+    in.at = team < teams ? i0 : i1;
+    enter();
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages * kTile);
+    int in_stage = 0, out_stage = 0, pending = 0;
+    uint32_t out_phase = 0;
+    auto issue = [&]() {   // lane 0 only
+        if (in.at >= i1 || abort_flag.raised()) return;
+        mbar_arrive_expect_tx(bar0 + 8u * uint32_t(in_stage), kTile);
+        tma_load_2d(ring + uint32_t(in_stage * kTile), &map, bar0 + 8u * uint32_t(in_stage), in.x, in.y + in.tile * 16);
+        ++pending;
         if (++in_stage == kStages) in_stage = 0;
+        in.tile += teams;
+        if (in.tile >= in.count) {
+            in.tile = team;
+            if (--in.passes == 0) {
+                in.at += in.count;
+                enter();
+            }
+        }
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue();
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) issue();
+    if (kDown) griddep_wait();   // the first product
 
-    int64_t held = -1;   // which activations shared memory holds
-    for (int64_t item = i0; item < i1; ++item) {
-        const int64_t q = item / blocks;
-        const int act_i = int(q / slices), slice = int(q % slices), block = int(item % blocks);
+    float* const red0 = reinterpret_cast<float*>(smem + Smem<NG>::kRing);
+    int buffer = 0;
+    for (int64_t at = i0; at < i1;) {
+        const int64_t q = at / tiles;
+        const int first_tile = int(at - q * tiles), act_i = int(q / slices), slice = int(q - int64_t(act_i) * slices);
+        const int count = int(min(int64_t(tiles - first_tile), i1 - at));
         const int first = plan.start[act_i], n = plan.start[act_i + 1] - first;
-        const int sb0 = slice * per, sb1 = min(nsb, sb0 + per);
-        const int row0 = block * kBlockRows + team * kRows;
-        for (int pass = 0; pass * kTok < n; ++pass) {
-            const int ntok = min(kTok, n - pass * kTok), ng = (ntok + 3) / 4;
-            float tot[MT][NG][2];
+        const int sb = slice * per + ks, held = min(per, nsb - slice * per);   // super-blocks of this slice
+        const bool works = team < teams && sb < nsb;
+        for (int done = 0; done < n; done += kTok) {
+            const int ntok = min(kTok, n - done);
+            Act act[NG];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < NG; ++j) tot[m][j][0] = tot[m][j][1] = 0.f;
-            for (int part = sb0; part < sb1; part += a.act_sb) {
-                const int end = min(sb1, part + a.act_sb);
-                // one token's activations are the same for every expert of the first product
-                const int64_t want = (((!kDown && p.tokens == 1) ? 0 : int64_t(act_i)) * (kMaxPairs + 1) + pass) * (int64_t(nsb) + 1) + part;
-                if (want != held) {
-                    __syncthreads();
-                    const int count = (end - part) * ntok;
-                    for (int i = warp; i < count; i += kWarps) {
-                        const int sb = part + i / ntok, j = i % ntok;
-                        const int pos = first + pass * kTok + j;
-                        const float* x = kDown ? a.h + int64_t(pos) * p.ffn
-                                               : p.x + int64_t(plan.order[pos] / p.top_k) * p.model;
-                        put_act(x + sb * 256, act + uint32_t(((sb - part) * NG + j / 4) * kAct), j & 3, lane);
-                    }
-                    held = want;
-                    __syncthreads();
+            for (int j = 0; j < NG; ++j) {
+                const int tok = 4 * j + (g >> 1), pos = first + done + tok;
+                const bool have = works && tok < ntok;
+                const int64_t col = int64_t(sb) * 256 + 64 * t;
+                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!kDown) {
+                    const float* x = p.x + (have ? int64_t(plan.order[pos] / p.top_k) * p.model + col : 0);
+                    make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
+                } else if (a.gu_slices == 1) {
+                    const float* x = a.h + (have ? int64_t(pos) * p.ffn + col : 0);
+                    make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
+                } else {
+                    const int64_t pairs = int64_t(p.tokens) * p.top_k;
+                    make_act(act[j], lane, [&](int i) {
+                        float4 u = zero, v = zero;
+                        if (have) {
+                            for (int s = 0; s < a.gu_slices; ++s) {
+                                const float4* x = reinterpret_cast<const float4*>(
+                                    a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
+                                const float4 c = x[0], d = x[1];
+                                u.x += c.x; u.y += c.y; u.z += c.z; u.w += c.w;
+                                v.x += d.x; v.y += d.y; v.z += d.z; v.w += d.w;
+                            }
+                        }
+                        return make_float4(silu_times(u.x, u.y), silu_times(u.z, u.w), silu_times(v.x, v.y),
+                                           silu_times(v.z, v.w));
+                    });
                 }
-                for (int sb = part + (((ks - (part - sb0)) % KS) + KS) % KS; sb < end; sb += KS) {
-                    cp_async_wait<kStages - 2>();
-                    __syncwarp();
-                    issue();   // into the stage before this one, which every lane has read
-                    const uint32_t st = ring + uint32_t(out_stage * kRows * kBlk);
-                    const uint32_t ab = act + uint32_t((sb - part) * NG * kAct);
-                    if (++out_stage == kStages) out_stage = 0;
-                    float acc[MT][NG][4];
+            }
+            for (int j0 = 0; j0 < count; j0 += teams * kBatch) {
+                float* const red = red0 + buffer * (Smem<NG>::kRed / 4);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                for (int nb = 0; nb < kBatch; ++nb) {
+                    const int tile = j0 + nb * teams + team;
+                    if (!works || tile >= count) continue;
+                    if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag,
+                                                              a.status)))
+                        continue;
+                    const uint32_t st = ring + uint32_t(out_stage * kTile);
+                    const uint32_t ra = st + uint32_t(g * kBlk), rb = ra + 8 * kBlk;
+                    const RowScale r0 = row_scale(lds128(ra), t), r1 = row_scale(lds128(rb), t);
+                    uint32_t w0[8], w1[8];
 #pragma unroll
-                        for (int j = 0; j < NG; ++j)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.f;
-                    RowScale r0[MT], r1[MT];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        r0[m] = row_scale(lds128(st + uint32_t((16 * m + g) * kBlk)), t);
-                        r1[m] = row_scale(lds128(st + uint32_t((16 * m + g + 8) * kBlk)), t);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 u = lds128(ra + uint32_t(16 + 32 * t + 16 * i));
+                        const uint4 v = lds128(rb + uint32_t(16 + 32 * t + 16 * i));
+                        w0[4 * i] = u.x; w0[4 * i + 1] = u.y; w0[4 * i + 2] = u.z; w0[4 * i + 3] = u.w;
+                        w1[4 * i] = v.x; w1[4 * i + 1] = v.y; w1[4 * i + 2] = v.z; w1[4 * i + 3] = v.w;
                     }
+                    float lo[NG][4], hi[NG][4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t w0[MT][4], w1[MT][4];
+                    for (int j = 0; j < NG; ++j)
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const uint4 u = lds128(st + uint32_t((16 * m + g) * kBlk + 16 + 32 * t + 16 * half));
-                            const uint4 v = lds128(st + uint32_t((16 * m + g + 8) * kBlk + 16 + 32 * t + 16 * half));
-                            w0[m][0] = u.x; w0[m][1] = u.y; w0[m][2] = u.z; w0[m][3] = u.w;
-                            w1[m][0] = v.x; w1[m][1] = v.y; w1[m][2] = v.z; w1[m][3] = v.w;
-                        }
+                        for (int k = 0; k < 4; ++k) lo[j][k] = hi[j][k] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t lo[MT][4], hi[MT][4];
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+                        unpack_lo(w0[i], r0, x0, x2);
+                        unpack_lo(w1[i], r1, x1, x3);
+                        unpack_hi(w0[i], r0, y0, y2);
+                        unpack_hi(w1[i], r1, y1, y3);
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                unpack_lo(w0[m][i], r0[m], lo[m][0], lo[m][2]);
-                                unpack_lo(w1[m][i], r1[m], lo[m][1], lo[m][3]);
-                                unpack_hi(w0[m][i], r0[m], hi[m][0], hi[m][2]);
-                                unpack_hi(w1[m][i], r1[m], hi[m][1], hi[m][3]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < NG; ++j) {
-                                if (j < ng) {
-                                    const uint4 b = lds128(ab + uint32_t(j * kAct + (4 * half + i) * 512 + lane * 16));
-#pragma unroll
-                                    for (int m = 0; m < MT; ++m) {
-                                        mma16816(acc[m][j], lo[m], b.x, b.y);
-                                        mma16816(acc[m][j], hi[m], b.z, b.w);
-                                    }
-                                }
-                            }
+                        for (int j = 0; j < NG; ++j) {
+                            mma16816(lo[j], x0, x1, x2, x3, act[j].b[i][0], act[j].b[i][1]);
+                            mma16816(hi[j], y0, y1, y2, y3, act[j].b[i][2], act[j].b[i][3]);
                         }
                     }
+                    float* mine = red + (nb * kWarps + warp) * (kTok * kRedPitch) + t * kRedPitch + g;
 #pragma unroll
                     for (int j = 0; j < NG; ++j) {
-                        if (j < ng) {
-                            const uint32_t xs = lds32(ab + uint32_t(j * kAct + 4096 + lane * 4));
-                            const float up = __uint_as_float(lds32(ab + uint32_t(j * kAct + 4224 + t * 4)));
-#pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                float mn[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma1688(mn, r0[m].m, r1[m].m, xs);
-                                const float* s = acc[m][j];
-                                tot[m][j][0] = fmaf(up, r0[m].d * (s[0] + s[1]) - r0[m].dmin * (mn[0] + mn[1]), tot[m][j][0]);
-                                tot[m][j][1] = fmaf(up, r1[m].d * (s[2] + s[3]) - r1[m].dmin * (mn[2] + mn[3]), tot[m][j][1]);
-                            }
-                        }
+                        float mn[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma1688(mn, r0.m, r1.m, act[j].sums);
+                        const float s0 = (lo[j][0] + hi[j][0]) + (lo[j][1] + hi[j][1]);
+                        const float s1 = (lo[j][2] + hi[j][2]) + (lo[j][3] + hi[j][3]);
+                        mine[4 * j * kRedPitch] = act[j].up * (r0.d * s0 - r0.dmin * (mn[0] + mn[1]));
+                        mine[4 * j * kRedPitch + 8] = act[j].up * (r1.d * s1 - r1.dmin * (mn[2] + mn[3]));
+                    }
+                    // The stores above depend on every load from the stage, so
+                    // those are done in every lane: the next copy may land in it.
+                    __syncwarp();
+                    if (lane == 0) {
+                        --pending;
+                        issue();
+                    }
+                    if (++out_stage == kStages) {
+                        out_stage = 0;
+                        out_phase ^= 1u;
                     }
                 }
-            }
-            // Join the team's warps (in their order) and store.
-            float* mine = red + warp * kTok * red_pitch(MT);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    mine[(4 * j + t) * red_pitch(MT) + 16 * m + g] = tot[m][j][0];
-                    mine[(4 * j + t) * red_pitch(MT) + 16 * m + g + 8] = tot[m][j][1];
-                }
-            if (KS == 1) __syncwarp(); else __syncthreads();
-            const float* base = red + team * KS * kTok * red_pitch(MT);
-            auto sum = [&](int tok, int r) {
-                float s = base[tok * red_pitch(MT) + r];
-#pragma unroll
-                for (int w = 1; w < KS; ++w) s += base[(w * kTok + tok) * red_pitch(MT) + r];
-                return s;
-            };
-            const int me = ks * 32 + lane;
-            if (kDown) {
-                for (int i = me; i < kRows * ntok; i += KS * 32) {
-                    const int tok = i / kRows, r = i % kRows;
-                    const int pair = plan.order[first + pass * kTok + tok];
-                    if (row0 + r < rows)
-                        a.y[(int64_t(slice) * p.tokens * p.top_k + pair) * p.model + row0 + r] = sum(tok, r);
-                }
-            } else {
-                for (int i = me; i < kRows / 2 * ntok; i += KS * 32) {
-                    const int tok = i / (kRows / 2), f = i % (kRows / 2);
-                    if (row0 + 2 * f < rows) {
-                        const float gate = sum(tok, 2 * f), up = sum(tok, 2 * f + 1);
-                        a.h[int64_t(first + pass * kTok + tok) * p.ffn + row0 / 2 + f] = gate / (1.f + expf(-gate)) * up;
+                __syncthreads();
+                // Join: the tiles of this batch in order, 16 rows each; a
+                // buffer is written again only after the next barrier.
+                const int batch = min(teams * kBatch, count - j0);
+                auto sum = [&](int tile, int tok, int r) {
+                    const int nb = tile / teams, tm = tile - nb * teams;
+                    const float* from = red + (nb * kWarps + tm * per) * (kTok * kRedPitch) + tok * kRedPitch + r;
+                    float s = 0.f;
+#pragma unroll 4
+                    for (int w = 0; w < held; ++w) s += from[w * (kTok * kRedPitch)];
+                    return s;
+                };
+                const int row0 = (first_tile + j0) * 16, width = batch * 16;
+                if (kDown || slices > 1) {
+                    for (int i = threadIdx.x; i < width * ntok; i += kThreads) {
+                        const int tok = i / width, r = i - tok * width, pos = first + done + tok;
+                        float* y = kDown ? a.y + (int64_t(slice) * p.tokens * p.top_k + plan.order[pos]) * p.model
+                                         : a.h + (int64_t(slice) * p.tokens * p.top_k + pos) * rows;
+                        y[row0 + r] = sum(r >> 4, tok, r & 15);
+                    }
+                } else {
+                    for (int i = threadIdx.x; i < width / 2 * ntok; i += kThreads) {
+                        const int tok = i / (width / 2), f = i - tok * (width / 2);
+                        const float gate = sum(f >> 3, tok, 2 * f & 15), up = sum(f >> 3, tok, (2 * f & 15) + 1);
+                        a.h[int64_t(first + done + tok) * p.ffn + row0 / 2 + f] = silu_times(gate, up);
                     }
                 }
+                buffer ^= 1;
             }
-            if (KS == 1) __syncwarp(); else __syncthreads();
         }
+        at += count;
     }
-    cp_async_wait<0>();
+    // Only after a wait ran out is anything still in flight.
+    if (lane == 0)
+        for (; pending > 0; --pending) {
+            wait_drain(bar0 + 8u * uint32_t(out_stage), out_phase, a.status);
+            if (++out_stage == kStages) {
+                out_stage = 0;
+                out_phase ^= 1u;
+            }
+        }
 }
 
 // ---------------------------------------------------------------- combine
@@ -555,7 +548,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const MoeArgs a) {
     for (int k = 0; k < p.top_k; ++k) {
         const int64_t pair = int64_t(t) * p.top_k + k;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < a.slices; ++i) {
+        for (int i = 0; i < a.down_slices; ++i) {
             const float4 v = *reinterpret_cast<const float4*>(a.y + (i * pairs + pair) * p.model + c);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
@@ -582,36 +575,39 @@ cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_
     return cfg;
 }
 
+// A row's super-blocks in slices of at most 16, one per warp of a team.
+int slices_of(int inner) { return (inner / 256 + kWarps - 1) / kWarps; }
+
 struct Sizes {
-    size_t logits, plan, h, y, bytes;
-    int slices;
+    size_t logits, h, y, bytes;
 };
 Sizes sizes(const mmq_q4K_moe_t& p) {
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
     Sizes z;
     const size_t pairs = size_t(p.tokens) * size_t(p.top_k);
-    z.slices = 1;
+    const int gu = slices_of(p.model);
     z.logits = 0;
-    z.plan = z.logits + up(size_t(p.tokens) * size_t(p.experts) * 4);
-    z.h = z.plan + up(sizeof(Plan));
-    z.y = z.h + up(pairs * size_t(p.ffn) * 4);
-    z.bytes = z.y + size_t(z.slices) * pairs * size_t(p.model) * 4;
+    z.h = z.logits + up(size_t(p.tokens) * size_t(p.experts) * 4);
+    z.y = z.h + up(pairs * size_t(p.ffn) * 4 * (gu > 1 ? 2 * size_t(gu) : 1));
+    z.bytes = z.y + size_t(slices_of(p.ffn)) * pairs * size_t(p.model) * 4;
     return z;
 }
 
-template <int NG, int MT, int KS, bool kDown>
-cudaError_t launch_expert(MoeArgs a, int nsm, cudaStream_t s) {
-    const int nsb = (kDown ? a.p.ffn : a.p.model) / 256;
-    a.act_sb = nsb < 16 ? nsb : 16;
-    const int smem = act_bytes(a.act_sb, NG) + ring_bytes(MT) + red_bytes(NG, MT);
+template <int NG, bool kDown>
+cudaError_t launch_expert(const MoeArgs& a, int nsm, cudaStream_t s) {
+    const int rows = kDown ? a.p.model : 2 * a.p.ffn;
+    const uint64_t pitch = uint64_t((kDown ? a.p.ffn : a.p.model) / 256) * kBlk;
+    CUtensorMap map;
+    if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
+                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    constexpr int smem = Smem<NG>::kBytes;
     cudaError_t e;
-    int resident = 0;
-    if ((e = cudaFuncSetAttribute(moe_expert_kernel<NG, MT, KS, kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, moe_expert_kernel<NG, MT, KS, kDown>, kThreads, smem)))
+    if ((e = cudaFuncSetAttribute(moe_expert_kernel<NG, kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
         return e;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm * (resident > 0 ? resident : 1))), dim3(kThreads), smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_expert_kernel<NG, MT, KS, kDown>, a);
+    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(kThreads), smem, s, attr);
+    return cudaLaunchKernelEx(&cfg, moe_expert_kernel<NG, kDown>, map, a);
 }
 
 }  // namespace
@@ -620,7 +616,7 @@ namespace mmq {
 
 size_t q4K_moe_workspace(const mmq_q4K_moe_t& p) { return sizes(p).bytes; }
 
-cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, cudaStream_t s) {
+cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status, cudaStream_t s) {
     int dev = 0, nsm = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev))) return e;
@@ -629,17 +625,19 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, cudaStream_t
     MoeArgs a;
     a.p = p;
     a.logits = reinterpret_cast<float*>(ws + z.logits);
-    a.plan = reinterpret_cast<Plan*>(ws + z.plan);
     a.h = reinterpret_cast<float*>(ws + z.h);
     a.y = reinterpret_cast<float*>(ws + z.y);
-    a.slices = z.slices;
-    a.act_sb = 0;
+    a.gu_slices = slices_of(p.model);
+    a.down_slices = slices_of(p.ffn);
+    a.status = status;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t first = launch_config(dim3(unsigned((p.experts + 3) / 4), unsigned((p.tokens + 3) / 4)),
                                                    dim3(128), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
-    if ((e = launch_expert<1, 1, 8, false>(a, nsm, s))) return e;
-    if ((e = launch_expert<1, 1, 8, true>(a, nsm, s))) return e;
+    // Four tokens at a time where an expert gets few on average, else eight.
+    const bool few = p.tokens <= 4 || p.tokens * p.top_k <= 2 * p.experts;
+    if ((e = few ? launch_expert<1, false>(a, nsm, s) : launch_expert<2, false>(a, nsm, s))) return e;
+    if ((e = few ? launch_expert<1, true>(a, nsm, s) : launch_expert<2, true>(a, nsm, s))) return e;
     cudaLaunchAttribute last_attr[1];
     const cudaLaunchConfig_t last = follow_config(dim3(unsigned((p.model / 4 + 127) / 128), unsigned(p.tokens)), dim3(128), 0, s, last_attr);
     return cudaLaunchKernelEx(&last, moe_combine_kernel, a);
