@@ -537,6 +537,12 @@ static int check_moe_sizes(const mmq_q4K_moe_t* p) {
     const int32_t kMax = 1 << 20;
     if (p->model < 256 || p->model % 256 || p->model > kMax || p->ffn < 256 || p->ffn % 256 || p->ffn > kMax)
         return MMQ_ERR_ARG;
+    // Row tiles and tensor-map rows are counted in 32 bits.
+    const int64_t rows = p->model > 2 * p->ffn ? p->model : 2 * p->ffn;
+    const int64_t inner = p->model > p->ffn ? p->model : p->ffn;
+    if (rows * p->experts > (int64_t(1) << 31) - 1 ||
+        rows / 16 * ((inner / 256 + 15) / 16) * p->tokens * p->top_k > (int64_t(1) << 31) - 1)
+        return MMQ_ERR_ARG;
     return MMQ_OK;
 }
 

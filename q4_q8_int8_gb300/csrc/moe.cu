@@ -32,15 +32,21 @@ constexpr int kMaxExperts = MMQ_MOE_MAX_EXPERTS;
 constexpr int kMaxPairs = MMQ_MOE_MAX_PAIRS;
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kBlk = 144;     // bytes of a q4_K super-block
-constexpr int kStages = 4;    // weight tiles (16 rows x one super-block) in flight per warp
-constexpr int kTile = 16 * kBlk;
+// A weight tile is 32 rows x one super-block, one TMA box, two per warp in
+// flight: 32 boxes per SM.  Streaming 604 MB through such rings with no other
+// work takes 92 us (6.5 TB/s) with 32 boxes of 16 or of 32 rows in flight per
+// SM, but 127 us with 48 and 154 us with 64.
+constexpr int kRows = 32, kStages = 2;
+constexpr int kTile = kRows * kBlk;
 
 // Which tokens go to which expert: pair i = token i / top_k, its i % top_k-th
-// expert; order lists the pairs by expert.
+// expert.  An active expert (one with a token) has its pairs in a row of
+// `order`, and one pass over its weights per kTok of them.
 struct Plan {
-    int active;                      // experts with a token
+    int active;
     int expert[kMaxExperts];
-    int start[kMaxExperts + 1];      // an active expert's pairs: order[start[a]] .. order[start[a + 1] - 1]
+    int start[kMaxExperts + 1];   // an active expert's pairs: order[start[a]] .. order[start[a + 1] - 1]
+    int pass[kMaxExperts + 1];    // passes of the active experts before it
     int order[kMaxPairs];
 };
 
@@ -55,40 +61,51 @@ struct MoeArgs {
 };
 
 // ----------------------------------------------------------------- router
-// One warp: one expert's logits for four tokens.
-__global__ void __launch_bounds__(128) moe_router_kernel(const MoeArgs a) {
+// One CTA: one expert's logits for four tokens, the sum split over its warps
+// so that a thread's loads are all in flight at once.
+constexpr int kRouterThreads = 256;
+__global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const mmq_q4K_moe_t& p = a.p;
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int t0 = blockIdx.y * 4;
-    if (e >= p.experts) return;
+    __shared__ float part[kRouterThreads / 32][4];
+    const int e = blockIdx.x, t0 = blockIdx.y * 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float4* w = reinterpret_cast<const float4*>(p.w_router + int64_t(e) * p.model);
-    const float* x = p.x + int64_t(t0) * p.model;
+    const float4* x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)   // past the last token: the last one again
+        x[j] = reinterpret_cast<const float4*>(p.x + int64_t(min(t0 + j, p.tokens - 1)) * p.model);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const int n4 = p.model / 4;
 #pragma unroll 4
-    for (int i = lane; i < n4; i += 32) {
+    for (int i = threadIdx.x; i < n4; i += kRouterThreads) {
         const float4 wv = w[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (t0 + j < p.tokens) {
-                const float4 xv = reinterpret_cast<const float4*>(x + int64_t(j) * p.model)[i];
-                acc[j] = fmaf(wv.x, xv.x, fmaf(wv.y, xv.y, fmaf(wv.z, xv.z, fmaf(wv.w, xv.w, acc[j]))));
-            }
+            const float4 xv = x[j][i];
+            acc[j] = fmaf(wv.x, xv.x, fmaf(wv.y, xv.y, fmaf(wv.z, xv.z, fmaf(wv.w, xv.w, acc[j]))));
         }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], m);
-        if (lane == 0 && t0 + j < p.tokens) a.logits[int64_t(t0 + j) * p.experts + e] = acc[j];
+        if (lane == 0) part[warp][j] = acc[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4 && t0 + int(threadIdx.x) < p.tokens) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRouterThreads / 32; ++i) s += part[i][threadIdx.x];
+        a.logits[int64_t(t0 + threadIdx.x) * p.experts + e] = s;
     }
 }
 
-// One warp: token t's softmax and its top_k experts.  NaN ranks below every
-// number, so the chosen experts are always distinct and in range.
-__device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* ids, bool store) {
+// One warp: token t's softmax and its top_k experts, best first.  A choice is
+// two warp reductions over keys that order the values e^(logit - max), from 0
+// to 1 and so by their bits; NaN ranks below every number, so the chosen
+// experts are always distinct and in range.
+__device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* ids, uint64_t* tokens_of, bool store) {
     const mmq_q4K_moe_t& p = a.p;
     constexpr int kPer = kMaxExperts / 32;
     float v[kPer];
@@ -102,89 +119,108 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* i
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
     float sum = 0.f;
+    uint32_t key[kPer];   // 0: none or taken, 1: NaN, else the value's bits + 2
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const bool in = lane + 32 * j < p.experts;
-        v[j] = in ? expf(v[j] - top) : 0.f;
-        sum += v[j];
+        key[j] = 0;
+        if (lane + 32 * j < p.experts) {
+            v[j] = expf(v[j] - top);
+            sum += v[j];
+            key[j] = v[j] == v[j] ? __float_as_uint(v[j]) + 2u : 1u;
+        }
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    uint32_t taken = 0;
-    float picked = 0.f, mine = 0.f;   // lane i keeps the i-th choice's weight
+    float picked = 0.f, mine = 0.f;   // lane i keeps the i-th choice
+    int chosen = 0;
     for (int i = 0; i < p.top_k; ++i) {
-        float best = -2.f, value = 0.f;
+        uint32_t best = 0;
         int at = kMaxExperts;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const float key = v[j] == v[j] ? v[j] : -1.f;
-            if (lane + 32 * j < p.experts && !((taken >> j) & 1u) && key > best) {
-                best = key;
-                value = v[j];
+        for (int j = 0; j < kPer; ++j)
+            if (key[j] > best) {
+                best = key[j];
                 at = lane + 32 * j;
             }
-        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+        at = __reduce_min_sync(0xffffffffu, best == most ? at : kMaxExperts);
+        const float value = most > 1u ? __uint_as_float(most - 2u) : __int_as_float(0x7FC00000);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) {
-            const float ob = __shfl_xor_sync(0xffffffffu, best, m), ov = __shfl_xor_sync(0xffffffffu, value, m);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, m);
-            if (ob > best || (ob == best && oa < at)) {
-                best = ob;
-                value = ov;
-                at = oa;
-            }
-        }
-        if ((at & 31) == lane) taken |= 1u << (at >> 5);
+        for (int j = 0; j < kPer; ++j)
+            if (lane + 32 * j == at) key[j] = 0;
         picked += value;
-        if (lane == i) mine = value;
-        if (lane == 0) {
-            ids[t * p.top_k + i] = at;
-            if (store && p.ids) p.ids[t * p.top_k + i] = at;
+        if (lane == i) {
+            mine = value;
+            chosen = at;
         }
     }
-    if (store && lane < p.top_k) p.weights[t * p.top_k + lane] = mine / (p.renormalize ? picked : sum);
+    if (lane < p.top_k) {
+        ids[t * p.top_k + lane] = chosen;
+        atomicOr(reinterpret_cast<unsigned long long*>(tokens_of + chosen), 1ull << t);
+    }
+    if (store) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (lane < p.top_k) {
+            p.ids[t * p.top_k + lane] = chosen;
+            p.weights[t * p.top_k + lane] = mine / (p.renormalize ? picked : sum);
+        }
+    }
 }
 
-// Fill `plan` (shared memory) from the logits; `store`: also the chosen
-// experts and their weights to the caller.  scratch: kMaxPairs + 2 * kWarps ints.
-__device__ void make_plan(const MoeArgs& a, Plan* plan, int* scratch, bool store) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* ids = scratch;
-    int* totals = scratch + kMaxPairs;
-    for (int t = warp; t < a.p.tokens; t += kWarps) choose(a, t, lane, ids, store);
+struct PlanScratch {
+    uint64_t tokens_of[kMaxExperts];   // one bit per token of an expert
+    int ids[kMaxPairs];
+    int totals[3][kWarps];
+};
+
+// Fill `plan` (shared memory) from the logits, for passes of `pass_tokens`;
+// `store`: also the chosen experts and their weights to the caller.
+__device__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, int pass_tokens, bool store) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
+    static_assert(kMaxExperts <= kThreads && kMaxTokens <= 64, "one thread per expert, one bit per token");
+    if (e < kMaxExperts) z->tokens_of[e] = 0;
     __syncthreads();
-    static_assert(kMaxExperts <= kThreads, "one thread per expert");
-    const int e = threadIdx.x, pairs = a.p.tokens * a.p.top_k;
-    int n = 0;
-    if (e < a.p.experts)
-        for (int i = 0; i < pairs; ++i) n += ids[i] == e;
-    // exclusive prefixes over the experts: of the pairs, and of the active ones
-    int before = n;
+    for (int t = warp; t < a.p.tokens; t += kWarps) choose(a, t, lane, z->ids, z->tokens_of, store);
+    __syncthreads();
+    uint64_t mine = e < kMaxExperts ? z->tokens_of[e] : 0;
+    const int n = __popcll(mine), passes = (n + pass_tokens - 1) / pass_tokens;
+    // prefixes over the experts: of their pairs, their passes, and the active ones
+    int pairs = n, pass = passes;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, before, m);
-        if (lane >= m) before += o;
+        const int u = __shfl_up_sync(0xffffffffu, pairs, m), v = __shfl_up_sync(0xffffffffu, pass, m);
+        if (lane >= m) {
+            pairs += u;
+            pass += v;
+        }
     }
     const uint32_t live = __ballot_sync(0xffffffffu, n > 0);
     if (lane == 31) {
-        totals[warp] = before;
-        totals[kWarps + warp] = __popc(live);
+        z->totals[0][warp] = pairs;
+        z->totals[1][warp] = pass;
+        z->totals[2][warp] = __popc(live);
     }
     __syncthreads();
-    int at = before - n, rank = __popc(live & ((1u << lane) - 1u));
+    int at = pairs - n, first = pass - passes, rank = __popc(live & ((1u << lane) - 1u));
     for (int w = 0; w < warp; ++w) {
-        at += totals[w];
-        rank += totals[kWarps + w];
+        at += z->totals[0][w];
+        first += z->totals[1][w];
+        rank += z->totals[2][w];
     }
     if (n > 0) {
         plan->expert[rank] = e;
         plan->start[rank] = at;
-        for (int i = 0; i < pairs; ++i)
-            if (ids[i] == e) plan->order[at++] = i;
+        plan->pass[rank] = first;
+        for (; mine; mine &= mine - 1) {
+            const int t = __ffsll(static_cast<long long>(mine)) - 1;
+            int j = 0;
+            while (z->ids[t * a.p.top_k + j] != e) ++j;
+            plan->order[at++] = t * a.p.top_k + j;
+        }
     }
     if (e == kThreads - 1) {
-        plan->active = rank + (n > 0);
-        plan->start[rank + (n > 0)] = pairs;
+        plan->active = rank;
+        plan->start[rank] = at;
+        plan->pass[rank] = first;
     }
     __syncthreads();
 }
@@ -255,12 +291,13 @@ struct Act {
 };
 template <typename Load>   // load(i): values 4 i .. 4 i + 3 of the lane's 64, f32
 __device__ __forceinline__ void make_act(Act& act, int lane, Load load) {
+    float4 v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = load(i);
     float top = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < 16; ++i) {
-        const float4 v = load(i);
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     // 2^e with top 2^-e in [128, 256), e from -126 on
@@ -278,7 +315,7 @@ __device__ __forceinline__ void make_act(Act& act, int lane, Load load) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            const float4 u = load(8 * c + w);
+            const float4 u = v[8 * c + w];
             const float f[4] = {u.x * down, u.y * down, u.z * down, u.w * down};
             act.b[w][2 * c] = h2u(__halves2half2(part(f[0]), part(f[2])));
             act.b[w][2 * c + 1] = h2u(__halves2half2(part(f[1]), part(f[3])));
@@ -290,187 +327,208 @@ __device__ __forceinline__ void make_act(Act& act, int lane, Load load) {
     act.up = __shfl_sync(0xffffffffu, __uint_as_float(uint32_t(127 + e) << 23), 8 * (lane & 3));
 }
 
-constexpr int kRedPitch = 24;   // floats per token: 16 rows, and no two lanes on one bank
+constexpr int kRedPitch = kRows + 8;   // floats per token: the four lanes of a row on four banks
 template <int NG>
 struct Smem {
-    static constexpr int kBatch = 2 / NG;                                     // tiles per team and barrier
-    static constexpr int kRed = kBatch * kWarps * 4 * NG * kRedPitch * 4;     // one buffer of partial sums
+    static constexpr int kBuffers = 5 - NG;                         // batches of partial sums between the warps
+    static constexpr int kPart = 4 * NG * kRedPitch;                // floats of one warp's tile
+    static constexpr int kRed = kWarps * kPart * 4;                 // bytes of one buffer
     static constexpr int kRing = kWarps * kStages * kTile;
-    static constexpr int kBytes = kRing + 2 * kRed + 128;                     // + alignment
+    static constexpr int kBytes = kRing + kBuffers * kRed + 128;    // + alignment
 };
-static_assert(Smem<1>::kBytes <= 200 * 1024 && Smem<2>::kBytes <= 200 * 1024, "shared memory budget");
+static_assert(Smem<2>::kBytes <= 208 * 1024, "shared memory budget");
+
+// A run of row tiles of one (active expert, slice, pass).
+struct Run {
+    int a, slice, pass, first, count, left;   // left: tiles the CTA still has, this run's among them
+    __device__ __forceinline__ void next(const Plan& plan, int slices, int tiles) {
+        left -= count;
+        first = 0;
+        count = min(tiles, left);
+        if (++pass == plan.pass[a + 1] - plan.pass[a]) {
+            pass = 0;
+            if (++slice == slices) {
+                slice = 0;
+                ++a;
+            }
+        }
+    }
+};
 
 // Both products of the experts.  Activations are stationary: a warp keeps the
 // operand of one super-block for 4 NG tokens in registers and streams weight
-// tiles (16 rows x that super-block, 2304 bytes, one TMA box) through a ring of
-// its own; the KS warps of a team hold the KS super-blocks of a row (a slice of
-// it, where it has more than 16), so a team reads whole rows, and their partial
-// sums of a tile are joined through shared memory, in a fixed order.  One CTA
-// per SM; the row tiles of all active experts are dealt out in equal
-// consecutive runs, a run being one (expert, slice).
+// tiles of that super-block through a ring of its own; the warps of a team hold the super-blocks of a row (or of a slice of
+// at most 16 of it), so a team reads whole rows.  The partial sums of a batch
+// (one tile per team) meet in shared memory: the warps take turns to add a
+// batch up, in a fixed order, and store it, and none of the others waits for
+// that unless it is a few batches ahead.  One CTA per SM; the row tiles of
+// all passes of all active experts are dealt out in equal consecutive parts.
 template <int NG, bool kDown>
 __global__ void __launch_bounds__(kThreads, 1)
 moe_expert_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ Plan plan;
-    __shared__ int scratch[kMaxPairs + 2 * kWarps];
-    __shared__ uint64_t bars[kWarps * kStages];
+    __shared__ PlanScratch scratch;
+    constexpr int kBuffers = Smem<NG>::kBuffers;
+    __shared__ uint64_t bars[kWarps * kStages + 2 * kBuffers];
     __shared__ uint32_t abort_word;
+    __shared__ int start_at;
     const mmq_q4K_moe_t& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const AbortFlag abort_flag{smem_u32(&abort_word)};
-    const uint32_t bar0 = smem_u32(&bars[warp * kStages]);
-    if (threadIdx.x == 0) abort_flag.set(0u);
+    const uint32_t bar0 = smem_u32(&bars[warp * kStages]), red_full = smem_u32(&bars[kWarps * kStages]);
+    const uint32_t red_empty = red_full + 8 * kBuffers;
+    constexpr int kTok = 4 * NG;
+    if (threadIdx.x == 0) {
+        abort_flag.set(0u);
+        for (int i = 0; i < kBuffers; ++i) {
+            mbar_init(red_full + 8u * uint32_t(i), kWarps);
+            mbar_init(red_empty + 8u * uint32_t(i), 1);
+        }
+        prefetch_tmap(&map);
+    }
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(bar0 + 8u * uint32_t(i), 1);
         fence_barrier_init();
-        if (warp == 0) prefetch_tmap(&map);
     }
     // The logits are complete before the second product starts: the first one
     // lets it be scheduled only after its own wait for the router.
-    if (!kDown) {
-        griddep_wait();
-        griddep_launch_dependents();
-    } else {
-        griddep_launch_dependents();
-    }
-    make_plan(a, &plan, scratch, !kDown && blockIdx.x == 0);
+    if (!kDown) griddep_wait();
+    griddep_launch_dependents();
+    make_plan(a, &plan, &scratch, kTok, !kDown && blockIdx.x == 0);
 
     const int rows = kDown ? p.model : 2 * p.ffn, nsb = (kDown ? p.ffn : p.model) / 256;
     const int slices = kDown ? a.down_slices : a.gu_slices;
     const int per = (nsb + slices - 1) / slices, teams = kWarps / per;
     const int team = warp / per, ks = warp - team * per;
-    const int tiles = rows / 16;
-    const int64_t total = int64_t(plan.active) * slices * tiles;
-    const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
-    constexpr int kTok = 4 * NG, kBatch = Smem<NG>::kBatch;
+    const int tiles = rows / kRows, each = slices * tiles;   // tiles of a pass
+    const uint32_t total = uint32_t(plan.pass[plan.active] * each);
+    const int i0 = int(uint64_t(total) * blockIdx.x / gridDim.x), i1 = int(uint64_t(total) * (blockIdx.x + 1) / gridDim.x);
+    if (i0 >= i1) return;
+    if (int(threadIdx.x) < plan.active) {
+        const int p0 = i0 / each;
+        if (plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1]) start_at = threadIdx.x;
+    }
+    __syncthreads();
+    Run run;
+    {
+        run.a = start_at;
+        const int local = i0 - plan.pass[run.a] * each, passes = plan.pass[run.a + 1] - plan.pass[run.a];
+        const int sp = local / tiles;
+        run.first = local - sp * tiles;
+        run.slice = sp / passes;
+        run.pass = sp - run.slice * passes;
+        run.left = i1 - i0;
+        run.count = min(tiles - run.first, run.left);
+    }
 
-    // Where a warp's weight stream is: a run's tiles team, team + teams, ... ,
-    // once per pass over the run's tokens.
-    struct Stream {
-        int64_t at;          // first tile of the run
-        int count, tile;     // tiles of the run, the next one
-        int passes, x, y;    // passes left, box coordinates of the run's first tile
-    } in;
-    auto enter = [&]() {   // the run that starts at tile in.at; skips runs without a tile for this warp
-        while (in.at < i1) {
-            const int64_t q = in.at / tiles;
-            const int first = int(in.at - q * tiles), act = int(q / slices), slice = int(q - int64_t(act) * slices);
-            in.count = int(min(int64_t(tiles - first), i1 - in.at));
-            in.passes = (plan.start[act + 1] - plan.start[act] + kTok - 1) / kTok;
-            in.x = (slice * per + ks) * kBlk;
-            in.y = plan.expert[act] * rows + first * 16;
-            in.tile = team;
-            if (team < in.count && slice * per + ks < nsb) return;
-            in.at += in.count;
+    // The warp's weight stream: tiles team, team + teams, ... of each run.
+    Run in = run;
+    int in_tile = team, in_stage = 0, out_stage = 0, pending = 0;
+    uint32_t out_phase = 0;
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages * kTile);
+    auto settle = [&]() {   // to a run with a tile for this warp
+        while (in.left > 0 && (in_tile >= in.count || in.slice * per + ks >= nsb)) {
+            in.next(plan, slices, tiles);
+            in_tile = team;
         }
     };
-    in.at = team < teams ? i0 : i1;
-    enter();
-    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages * kTile);
-    int in_stage = 0, out_stage = 0, pending = 0;
-    uint32_t out_phase = 0;
-    auto issue = [&]() {   // lane 0 only
-        if (in.at >= i1 || abort_flag.raised()) return;
-        mbar_arrive_expect_tx(bar0 + 8u * uint32_t(in_stage), kTile);
-        tma_load_2d(ring + uint32_t(in_stage * kTile), &map, bar0 + 8u * uint32_t(in_stage), in.x, in.y + in.tile * 16);
+    auto issue = [&]() {
+        if (in.left <= 0 || abort_flag.raised()) return;
+        const uint32_t bar = bar0 + 8u * uint32_t(in_stage);
+        mbar_arrive_expect_tx(bar, kTile);
+        tma_load_2d(ring + uint32_t(in_stage * kTile), &map, bar, (in.slice * per + ks) * kBlk,
+                    plan.expert[in.a] * rows + (in.first + in_tile) * kRows);
         ++pending;
         if (++in_stage == kStages) in_stage = 0;
-        in.tile += teams;
-        if (in.tile >= in.count) {
-            in.tile = team;
-            if (--in.passes == 0) {
-                in.at += in.count;
-                enter();
-            }
-        }
+        in_tile += teams;
+        settle();
     };
+    if (team >= teams) in.left = 0;
+    settle();
     if (lane == 0)
         for (int i = 0; i < kStages; ++i) issue();
     if (kDown) griddep_wait();   // the first product
 
     float* const red0 = reinterpret_cast<float*>(smem + Smem<NG>::kRing);
-    int buffer = 0;
-    for (int64_t at = i0; at < i1;) {
-        const int64_t q = at / tiles;
-        const int first_tile = int(at - q * tiles), act_i = int(q / slices), slice = int(q - int64_t(act_i) * slices);
-        const int count = int(min(int64_t(tiles - first_tile), i1 - at));
-        const int first = plan.start[act_i], n = plan.start[act_i + 1] - first;
-        const int sb = slice * per + ks, held = min(per, nsb - slice * per);   // super-blocks of this slice
+    int buffer = 0, turn = 0;
+    uint32_t red_phase = 0;
+    for (; run.left > 0; run.next(plan, slices, tiles)) {
+        const int first = plan.start[run.a] + run.pass * kTok;
+        const int ntok = min(kTok, plan.start[run.a + 1] - first);
+        const int sb = run.slice * per + ks, held = min(per, nsb - run.slice * per);   // super-blocks of this slice
         const bool works = team < teams && sb < nsb;
-        for (int done = 0; done < n; done += kTok) {
-            const int ntok = min(kTok, n - done);
-            Act act[NG];
+        Act act[NG];
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const int tok = 4 * j + (g >> 1), pos = first + done + tok;
-                const bool have = works && tok < ntok;
-                const int64_t col = int64_t(sb) * 256 + 64 * t;
-                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!kDown) {
-                    const float* x = p.x + (have ? int64_t(plan.order[pos] / p.top_k) * p.model + col : 0);
-                    make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
-                } else if (a.gu_slices == 1) {
-                    const float* x = a.h + (have ? int64_t(pos) * p.ffn + col : 0);
-                    make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
-                } else {
-                    const int64_t pairs = int64_t(p.tokens) * p.top_k;
-                    make_act(act[j], lane, [&](int i) {
-                        float4 u = zero, v = zero;
-                        if (have) {
-                            for (int s = 0; s < a.gu_slices; ++s) {
-                                const float4* x = reinterpret_cast<const float4*>(
-                                    a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
-                                const float4 c = x[0], d = x[1];
-                                u.x += c.x; u.y += c.y; u.z += c.z; u.w += c.w;
-                                v.x += d.x; v.y += d.y; v.z += d.z; v.w += d.w;
-                            }
+        for (int j = 0; j < NG; ++j) {
+            const int tok = 4 * j + (g >> 1), pos = first + tok;
+            const bool have = works && tok < ntok;
+            const int64_t col = int64_t(sb) * 256 + 64 * t;
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!kDown) {
+                const float* x = p.x + (have ? int64_t(plan.order[pos] / p.top_k) * p.model + col : 0);
+                make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
+            } else if (a.gu_slices == 1) {
+                const float* x = a.h + (have ? int64_t(pos) * p.ffn + col : 0);
+                make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
+            } else {
+                const int64_t pairs = int64_t(p.tokens) * p.top_k;
+                make_act(act[j], lane, [&](int i) {
+                    float4 u = zero, v = zero;
+                    if (have) {
+                        for (int s = 0; s < a.gu_slices; ++s) {
+                            const float4* x =
+                                reinterpret_cast<const float4*>(a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
+                            const float4 c = x[0], d = x[1];
+                            u.x += c.x; u.y += c.y; u.z += c.z; u.w += c.w;
+                            v.x += d.x; v.y += d.y; v.z += d.z; v.w += d.w;
                         }
-                        return make_float4(silu_times(u.x, u.y), silu_times(u.z, u.w), silu_times(v.x, v.y),
-                                           silu_times(v.z, v.w));
-                    });
-                }
-            }
-            for (int j0 = 0; j0 < count; j0 += teams * kBatch) {
-                float* const red = red0 + buffer * (Smem<NG>::kRed / 4);
-#pragma unroll
-                for (int nb = 0; nb < kBatch; ++nb) {
-                    const int tile = j0 + nb * teams + team;
-                    if (!works || tile >= count) continue;
-                    if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag,
-                                                              a.status)))
-                        continue;
-                    const uint32_t st = ring + uint32_t(out_stage * kTile);
-                    const uint32_t ra = st + uint32_t(g * kBlk), rb = ra + 8 * kBlk;
-                    const RowScale r0 = row_scale(lds128(ra), t), r1 = row_scale(lds128(rb), t);
-                    uint32_t w0[8], w1[8];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 u = lds128(ra + uint32_t(16 + 32 * t + 16 * i));
-                        const uint4 v = lds128(rb + uint32_t(16 + 32 * t + 16 * i));
-                        w0[4 * i] = u.x; w0[4 * i + 1] = u.y; w0[4 * i + 2] = u.z; w0[4 * i + 3] = u.w;
-                        w1[4 * i] = v.x; w1[4 * i + 1] = v.y; w1[4 * i + 2] = v.z; w1[4 * i + 3] = v.w;
                     }
+                    return make_float4(silu_times(u.x, u.y), silu_times(u.z, u.w), silu_times(v.x, v.y),
+                                       silu_times(v.z, v.w));
+                });
+            }
+        }
+        for (int j0 = 0; j0 < run.count; j0 += teams) {
+            float* const red = red0 + buffer * (Smem<NG>::kRed / 4);
+            // The buffer's last batch has been added up (at first: passes at once).
+            if (!__all_sync(0xffffffffu, wait_bounded(red_empty + 8u * uint32_t(buffer), red_phase ^ 1u, abort_flag, a.status)))
+                break;
+            if (works && j0 + team < run.count) {
+                if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag, a.status)))
+                    break;
+                const uint32_t st = ring + uint32_t(out_stage * kTile);
+#pragma unroll 1
+                for (int m = 0; m < kRows; m += 16) {
+                    const uint32_t ra = st + uint32_t((m + g) * kBlk), rb = ra + 8 * kBlk;
+                    const RowScale r0 = row_scale(lds128(ra), t), r1 = row_scale(lds128(rb), t);
                     float lo[NG][4], hi[NG][4];
 #pragma unroll
                     for (int j = 0; j < NG; ++j)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) lo[j][k] = hi[j][k] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
-                        unpack_lo(w0[i], r0, x0, x2);
-                        unpack_lo(w1[i], r1, x1, x3);
-                        unpack_hi(w0[i], r0, y0, y2);
-                        unpack_hi(w1[i], r1, y1, y3);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint4 u = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
+                        const uint4 v = lds128(rb + uint32_t(16 + 32 * t + 16 * half));
+                        const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int j = 0; j < NG; ++j) {
-                            mma16816(lo[j], x0, x1, x2, x3, act[j].b[i][0], act[j].b[i][1]);
-                            mma16816(hi[j], y0, y1, y2, y3, act[j].b[i][2], act[j].b[i][3]);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+                            unpack_lo(w0[i], r0, x0, x2);
+                            unpack_lo(w1[i], r1, x1, x3);
+                            unpack_hi(w0[i], r0, y0, y2);
+                            unpack_hi(w1[i], r1, y1, y3);
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) {
+                                const uint32_t* b = act[j].b[4 * half + i];
+                                mma16816(lo[j], x0, x1, x2, x3, b[0], b[1]);
+                                mma16816(hi[j], y0, y1, y2, y3, b[2], b[3]);
+                            }
                         }
                     }
-                    float* mine = red + (nb * kWarps + warp) * (kTok * kRedPitch) + t * kRedPitch + g;
+                    float* mine = red + warp * Smem<NG>::kPart + t * kRedPitch + m + g;
 #pragma unroll
                     for (int j = 0; j < NG; ++j) {
                         float mn[4] = {0.f, 0.f, 0.f, 0.f};
@@ -480,49 +538,56 @@ moe_expert_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
                         mine[4 * j * kRedPitch] = act[j].up * (r0.d * s0 - r0.dmin * (mn[0] + mn[1]));
                         mine[4 * j * kRedPitch + 8] = act[j].up * (r1.d * s1 - r1.dmin * (mn[2] + mn[3]));
                     }
-                    // The stores above depend on every load from the stage, so
-                    // those are done in every lane: the next copy may land in it.
-                    __syncwarp();
-                    if (lane == 0) {
-                        --pending;
-                        issue();
-                    }
-                    if (++out_stage == kStages) {
-                        out_stage = 0;
-                        out_phase ^= 1u;
+                }
+                // The stores above depend on every load from the stage, so
+                // those are done in every lane: the next copy may land in it.
+                __syncwarp();
+                if (lane == 0) {
+                    --pending;
+                    issue();
+                }
+                if (++out_stage == kStages) {
+                    out_stage = 0;
+                    out_phase ^= 1u;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(red_full + 8u * uint32_t(buffer));
+            if (turn == warp) {   // this warp adds the batch up: two rows of one token per lane and step
+                if (!__all_sync(0xffffffffu, wait_bounded(red_full + 8u * uint32_t(buffer), red_phase, abort_flag, a.status)))
+                    break;
+                const int batch = min(teams, run.count - j0);
+                const int r = 2 * (lane & 15);
+                for (int tm = 0; tm < batch; ++tm) {
+                    const int row = (run.first + j0 + tm) * kRows + r;
+                    for (int tok = lane >> 4; tok < ntok; tok += 2) {
+                        const float* from = red + tm * per * Smem<NG>::kPart + tok * kRedPitch + r;
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll 8
+                        for (int w = 0; w < held; ++w) {
+                            const float2 f = *reinterpret_cast<const float2*>(from + w * Smem<NG>::kPart);
+                            s0 += f.x;
+                            s1 += f.y;
+                        }
+                        const int pos = first + tok;
+                        const int64_t base = int64_t(run.slice) * p.tokens * p.top_k;
+                        if (kDown)
+                            *reinterpret_cast<float2*>(a.y + (base + plan.order[pos]) * rows + row) = make_float2(s0, s1);
+                        else if (slices > 1)
+                            *reinterpret_cast<float2*>(a.h + (base + pos) * rows + row) = make_float2(s0, s1);
+                        else
+                            a.h[int64_t(pos) * p.ffn + (row >> 1)] = silu_times(s0, s1);
                     }
                 }
-                __syncthreads();
-                // Join: the tiles of this batch in order, 16 rows each; a
-                // buffer is written again only after the next barrier.
-                const int batch = min(teams * kBatch, count - j0);
-                auto sum = [&](int tile, int tok, int r) {
-                    const int nb = tile / teams, tm = tile - nb * teams;
-                    const float* from = red + (nb * kWarps + tm * per) * (kTok * kRedPitch) + tok * kRedPitch + r;
-                    float s = 0.f;
-#pragma unroll 4
-                    for (int w = 0; w < held; ++w) s += from[w * (kTok * kRedPitch)];
-                    return s;
-                };
-                const int row0 = (first_tile + j0) * 16, width = batch * 16;
-                if (kDown || slices > 1) {
-                    for (int i = threadIdx.x; i < width * ntok; i += kThreads) {
-                        const int tok = i / width, r = i - tok * width, pos = first + done + tok;
-                        float* y = kDown ? a.y + (int64_t(slice) * p.tokens * p.top_k + plan.order[pos]) * p.model
-                                         : a.h + (int64_t(slice) * p.tokens * p.top_k + pos) * rows;
-                        y[row0 + r] = sum(r >> 4, tok, r & 15);
-                    }
-                } else {
-                    for (int i = threadIdx.x; i < width / 2 * ntok; i += kThreads) {
-                        const int tok = i / (width / 2), f = i - tok * (width / 2);
-                        const float gate = sum(f >> 3, tok, 2 * f & 15), up = sum(f >> 3, tok, (2 * f & 15) + 1);
-                        a.h[int64_t(first + done + tok) * p.ffn + row0 / 2 + f] = silu_times(gate, up);
-                    }
-                }
-                buffer ^= 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(red_empty + 8u * uint32_t(buffer));
+            }
+            if (++turn == kWarps) turn = 0;
+            if (++buffer == kBuffers) {
+                buffer = 0;
+                red_phase ^= 1u;
             }
         }
-        at += count;
     }
     // Only after a wait ran out is anything still in flight.
     if (lane == 0)
@@ -545,6 +610,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const MoeArgs a) {
     const int64_t pairs = int64_t(p.tokens) * p.top_k;
     const int64_t at = int64_t(t) * p.model + c;
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int k = 0; k < p.top_k; ++k) {
         const int64_t pair = int64_t(t) * p.top_k + k;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -599,7 +665,7 @@ cudaError_t launch_expert(const MoeArgs& a, int nsm, cudaStream_t s) {
     const uint64_t pitch = uint64_t((kDown ? a.p.ffn : a.p.model) / 256) * kBlk;
     CUtensorMap map;
     if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
-                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     constexpr int smem = Smem<NG>::kBytes;
     cudaError_t e;
@@ -631,8 +697,8 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     a.down_slices = slices_of(p.ffn);
     a.status = status;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t first = launch_config(dim3(unsigned((p.experts + 3) / 4), unsigned((p.tokens + 3) / 4)),
-                                                   dim3(128), 0, s, attr);
+    const cudaLaunchConfig_t first = launch_config(dim3(unsigned(p.experts), unsigned((p.tokens + 3) / 4)),
+                                                   dim3(kRouterThreads), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
     // Four tokens at a time where an expert gets few on average, else eight.
     const bool few = p.tokens <= 4 || p.tokens * p.top_k <= 2 * p.experts;
