@@ -269,14 +269,22 @@ __device__ __forceinline__ RowScale row_scale(const uint4& head, int t) {
     r.dmin = __half2float(__ushort_as_half(uint16_t(head.x >> 16)));
     return r;
 }
-// Four nibbles' sc q as two fp16 pairs: elements {0, 2} and {1, 3} of the word.
-__device__ __forceinline__ void unpack_lo(uint32_t w, const RowScale& r, uint32_t& x02, uint32_t& x13) {
-    x02 = h2u(__hfma2(u2h((w & 0x000F000Fu) | 0x64006400u), r.s_lo, r.b_lo));
-    x13 = h2u(__hfma2(u2h(((w >> 8) & 0x000F000Fu) | 0x64006400u), r.s_lo, r.b_lo));
+// (a & b) | c in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
-__device__ __forceinline__ void unpack_hi(uint32_t w, const RowScale& r, uint32_t& x02, uint32_t& x13) {
-    x02 = h2u(__hfma2(u2h((w & 0x00F000F0u) | 0x64006400u), r.s_hi, r.b_hi));
-    x13 = h2u(__hfma2(u2h(((w >> 8) & 0x00F000F0u) | 0x64006400u), r.s_hi, r.b_hi));
+// Four nibbles' sc q as two fp16 pairs: elements {0, 2} and {1, 3} of the word.
+__device__ __forceinline__ void unpack_lo(uint32_t w, uint32_t w8, const RowScale& r, uint32_t magic, uint32_t& x02,
+                                          uint32_t& x13) {
+    x02 = h2u(__hfma2(u2h(and_or(w, 0x000F000Fu, magic)), r.s_lo, r.b_lo));
+    x13 = h2u(__hfma2(u2h(and_or(w8, 0x000F000Fu, magic)), r.s_lo, r.b_lo));
+}
+__device__ __forceinline__ void unpack_hi(uint32_t w, uint32_t w8, const RowScale& r, uint32_t magic, uint32_t& x02,
+                                          uint32_t& x13) {
+    x02 = h2u(__hfma2(u2h(and_or(w, 0x00F000F0u, magic)), r.s_hi, r.b_hi));
+    x13 = h2u(__hfma2(u2h(and_or(w8, 0x00F000F0u, magic)), r.s_hi, r.b_hi));
 }
 
 // A group of four tokens' activations of one super-block, as the second
@@ -453,7 +461,8 @@ moe_expert_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
 
     float* const red0 = reinterpret_cast<float*>(smem + Smem<NG>::kRing);
     int buffer = 0, turn = 0;
-    uint32_t red_phase = 0;
+    uint32_t red_phase = 0, magic;   // fp16 1024 twice, kept in a register: one constant per instruction
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
     for (; run.left > 0; run.next(plan, slices, tiles)) {
         const int first = plan.start[run.a] + run.pass * kTok;
         const int ntok = min(kTok, plan.start[run.a + 1] - first);
@@ -516,10 +525,11 @@ moe_expert_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
-                            unpack_lo(w0[i], r0, x0, x2);
-                            unpack_lo(w1[i], r1, x1, x3);
-                            unpack_hi(w0[i], r0, y0, y2);
-                            unpack_hi(w1[i], r1, y1, y3);
+                            const uint32_t p0 = w0[i] >> 8, p1 = w1[i] >> 8;
+                            unpack_lo(w0[i], p0, r0, magic, x0, x2);
+                            unpack_lo(w1[i], p1, r1, magic, x1, x3);
+                            unpack_hi(w0[i], p0, r0, magic, y0, y2);
+                            unpack_hi(w1[i], p1, r1, magic, y1, y3);
 #pragma unroll
                             for (int j = 0; j < NG; ++j) {
                                 const uint32_t* b = act[j].b[4 * half + i];
