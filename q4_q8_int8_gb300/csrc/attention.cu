@@ -388,6 +388,24 @@ int split(int64_t units, int64_t keys, int64_t slots, int64_t least) {
     return int(n < 1 ? 1 : n);
 }
 
+// Parts of the prefix for the tensor-core kernel: `units` row blocks over
+// `tiles` key tiles each, one CTA per SM.  A CTA's item costs its key tiles
+// and about three more for its queries, first scores and results; a part more
+// costs the join a little.
+int64_t tc_parts(int64_t units, int64_t tiles, int64_t nsm) {
+    int64_t best = 1;
+    double least = 1e300;
+    for (int64_t n = 1; n <= tiles && n <= 64; ++n) {
+        const int64_t rounds = (units * n + nsm - 1) / nsm, each = (tiles + n - 1) / n;
+        const double cost = double(rounds * (each + 3)) + 0.25 * double(n);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
 void plan(AttnArgs& a, int nsm) {
     const mmq_shared_prefix_attention_t& p = a.p;
     a.tokens = int64_t(p.batch) * p.q_len;
@@ -397,11 +415,20 @@ void plan(AttnArgs& a, int nsm) {
     while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
     const int64_t rows = a.tokens * a.group;
     const int64_t slots = int64_t(nsm) * 2;
-    a.prefix_parts = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 256);
+    a.prefix_tiles = rows <= 16 ? 0 : rows <= 128 ? 1 : 2;
+    a.prefix_parts = 0;
     a.part_keys = 0;
-    if (a.prefix_parts) {
-        a.part_keys = ((p.prefix + a.prefix_parts - 1) / a.prefix_parts + 63) & ~int64_t(63);
-        a.prefix_parts = int((p.prefix + a.part_keys - 1) / a.part_keys);
+    if (p.prefix > 0) {
+        const int64_t tile = a.prefix_tiles ? 128 : 64;
+        int64_t n;
+        if (a.prefix_tiles) {
+            const int64_t units = (rows + 128 * a.prefix_tiles - 1) / (128 * a.prefix_tiles) * p.kv_heads;
+            n = tc_parts(units, (p.prefix + tile - 1) / tile, nsm);
+        } else {
+            n = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 256);
+        }
+        a.part_keys = ((p.prefix + n - 1) / n + tile - 1) / tile * tile;
+        a.prefix_parts = int((p.prefix + a.part_keys - 1) / a.part_keys) * (a.prefix_tiles == 1 ? 2 : 1);
     }
     a.suffix_parts = split(a.tokens * ((a.group + 15) / 16) * p.kv_heads, p.table_width << a.page_shift, slots, 256);
 }
@@ -412,7 +439,7 @@ size_t ml_bytes(const AttnArgs& a) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, int nsm, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     cudaError_t e;
     bool first = true;
@@ -429,7 +456,10 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         const cudaLaunchConfig_t cfg = config(grid, dim3(kWarps * 32), smem);
         if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, false>, a))) return e;
     }
-    if (a.prefix_parts) {
+    if (a.prefix_parts && a.prefix_tiles) {
+        const cudaLaunchConfig_t cfg = config(dim3(1), dim3(1), 0);
+        if ((e = mmq::launch_attention_prefix(a, nsm, cfg))) return e;
+    } else if (a.prefix_parts) {
         if ((e = cudaFuncSetAttribute(attn_rows_kernel<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
             return e;
         const dim3 grid(unsigned((a.tokens * a.group + 15) / 16), unsigned(a.p.kv_heads), unsigned(a.prefix_parts));
@@ -464,8 +494,8 @@ cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& 
     a.status = status;
     a.part_ml = static_cast<float2*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a));
-    if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, s) : launch<__half, 128>(a, s);
-    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, s) : launch<__nv_bfloat16, 128>(a, s);
+    if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);
+    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, nsm, s) : launch<__nv_bfloat16, 128>(a, nsm, s);
 }
 
 }  // namespace mmq

@@ -20,11 +20,15 @@ struct AttnArgs {
     int* status;
     int64_t tokens;       // batch * q_len
     int group;            // heads per kv head
+    int prefix_tiles;     // 128-row tiles per CTA of the tensor-core prefix kernel; 0: the few-row kernel
     int prefix_parts;     // parts 0 .. prefix_parts - 1
     int64_t part_keys;    // prefix keys per part, a multiple of the kernel's key tile
     int suffix_parts;     // the parts after them
     int page_shift;
     float scale_log2;     // scale * log2(e)
 };
+
+// The prefix's parts on the tensor cores (attention_tc.cu); cfg: stream and attributes.
+cudaError_t launch_attention_prefix(const AttnArgs& a, int nsm, const cudaLaunchConfig_t& cfg);
 
 }  // namespace mmq

@@ -1,0 +1,439 @@
+// The shared prefix's part of shared-prefix attention on the tensor cores.
+//
+// All rows of one kv head (every token's heads of its group) see the same
+// keys, so a key tile is read once for 128 or 256 rows: two products of
+// 128 rows x 128 keys x D per tile, S = Q K^T and O += P V with
+// P = 2^(S scale log2(e) - m), P rounded to the cache's type, everything else
+// f32.  At 2 x 128 rows and D = 128 a 64 KB pair of tiles carries 16.8 MFLOP
+// twice over, so with many rows the tensor cores bound it and with few rows the
+// key / value bytes.
+//
+// One CTA per SM:
+//   warps 0-3, 4-7  softmax groups 0 and 1, thread = row (its tensor-memory
+//                   lane): read S, keep the row's maximum and sum, write P over
+//                   S, and now and then scale O
+//   warp 8          TMA producer: key and value tiles (128 keys, 128-byte
+//                   swizzled panels of 64 values) through a ring of four
+//   warp 9          MMA issuer: S_i = Q_i K^T, O_i += P_i V, P from tensor memory
+// More than 128 rows: the groups hold two row tiles and share each key tile.
+// Up to 128: both hold the same rows and take key tiles in turn, as two parts.
+// While one group does its softmax the tensor cores work for the other.
+//
+// O is only scaled when a row's maximum has grown by more than 2^8 since the
+// last time (P then stays below 2^8, far inside fp16's range, and nothing is
+// lost: the factor is common to P, the sum and O).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "attention.h"
+#include "mmq_internal.h"
+#include "sm103_ptx.cuh"
+#include "tc_common.cuh"
+
+namespace {
+
+using namespace mmq::ptx;
+using namespace mmq::tc;
+using mmq::AttnArgs;
+
+constexpr int kKeys = 128, kRows = 128;
+constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;   // S_i at 128 i (P_i over its first 64 columns), O_i at 256 + 128 i
+constexpr float kGrow = 8.f;
+
+template <int D>
+struct Layout {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kSlots = 512 / D;                   // 128 KB of tiles in flight: one CTA per SM
+    static constexpr int kPanel = kKeys * 128;               // 128 rows of 64 16-bit values
+    static constexpr int kTile = kPanels * kPanel;
+    static constexpr int kOffQ = 0;                          // two row tiles
+    static constexpr int kOffRing = 2 * kTile;
+    static constexpr int kOffBar = kOffRing + kSlots * kTile;
+    // barriers: full, empty per slot; q_full, s_full, p_full, o_full per group; drain
+    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 9) * 8;
+    static constexpr int kBytes = kOffMisc + 16 + 1024;
+};
+static_assert(Layout<128>::kBytes <= 232448, "shared memory budget");
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_16(int N, bool b_rows_are_k) {
+    const uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return idesc_f16_f32(kRows, N) | (fmt << 7) | (fmt << 10) | (b_rows_are_k ? 1u << 16 : 0u);
+}
+
+template <typename T, int D, bool kTwo>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
+    using L = Layout<D>;
+    constexpr int kSlots = L::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::kOffBar;
+    auto full = [&](int s) { return bar0 + 8u * uint32_t(s); };
+    auto empty = [&](int s) { return bar0 + 8u * uint32_t(kSlots + s); };
+    auto q_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + g); };
+    auto s_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 2 + g); };
+    auto p_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 4 + g); };
+    auto o_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 6 + g); };
+    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+    const AbortFlag abort_flag{sbase + L::kOffMisc + 4};
+    const mmq_shared_prefix_attention_t& p = a.p;
+    int* const status = a.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(q_full(g), 4);
+            mbar_init(s_full(g), 1);
+            mbar_init(p_full(g), 4);
+            mbar_init(o_full(g), 1);
+        }
+        mbar_init(drain, 1);
+        abort_flag.set(0u);
+        fence_barrier_init();
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
+    __syncwarp();
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // Items: (row block, kv head, part), parts of one head's keys next to each other.
+    const int64_t rows = a.tokens * a.group;
+    const int per_unit = kTwo ? 2 * kRows : kRows;
+    const int units = int((rows + per_unit - 1) / per_unit);
+    const int parts = a.prefix_parts / (kTwo ? 1 : 2);
+    const int items = units * p.kv_heads * parts;
+    struct Item {
+        int h, part, steps;   // steps: rounds of (S, P V), both groups' together
+        int64_t r0, k0, k1;
+    };
+    auto get = [&](int i) {
+        Item w;
+        w.part = i % parts;
+        const int u = i / parts;
+        w.h = u / units;
+        w.r0 = int64_t(u % units) * per_unit;
+        w.k0 = w.part * a.part_keys;
+        w.k1 = min(w.k0 + a.part_keys, p.prefix);
+        const int tiles = int((w.k1 - w.k0 + kKeys - 1) / kKeys);
+        w.steps = kTwo ? 2 * tiles : tiles;
+        return w;
+    };
+
+    if (warp == kWarpTma) {
+        // ---------------------------------------------------------- producer
+        if (lane == 0) {
+            Ring<kSlots> r;
+            int issued[kSlots] = {};
+            uint32_t par[kSlots] = {};
+            auto load = [&](const CUtensorMap* map, int h, int64_t key) {
+                if (!wait_bounded(empty(r.slot), r.phase ^ 1u, abort_flag, status)) return false;
+                const uint32_t dst = sbase + uint32_t(L::kOffRing + r.slot * L::kTile);
+                mbar_arrive_expect_tx(full(r.slot), uint32_t(L::kTile));
+#pragma unroll
+                for (int c = 0; c < L::kPanels; ++c)
+                    tma_load_3d(dst + uint32_t(c * L::kPanel), map, full(r.slot), 64 * c, h, int32_t(key));
+                issued[r.slot] = 1;
+                par[r.slot] = r.phase;
+                r.next();
+                return true;
+            };
+            for (int i = blockIdx.x; i < items; i += gridDim.x) {
+                const Item w = get(i);
+                // in the order the MMA warp takes them
+                auto key = [&](int v) { return w.k0 + int64_t(kTwo ? v >> 1 : v) * kKeys; };
+                auto want = [&](int v) { return v < w.steps && (!kTwo || !(v & 1)); };
+                if (want(0) && !load(&maps.k, w.h, key(0))) goto producer_done;
+                if (want(1) && !load(&maps.k, w.h, key(1))) goto producer_done;
+                for (int v = 0; v < w.steps; ++v) {
+                    if (want(v) && !load(&maps.v, w.h, key(v))) goto producer_done;
+                    if (want(v + 2) && !load(&maps.k, w.h, key(v + 2))) goto producer_done;
+                }
+            }
+        producer_done:
+            for (int s = 0; s < kSlots; ++s)
+                if (issued[s]) wait_drain(full(s), par[s], status);
+        }
+    } else if (warp == kWarpMma) {
+        // -------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            Ring<kSlots> r;
+            int k_slot = 0, v_slot = 0;
+            uint32_t q_phase = 0, p_phase[2] = {0, 0};
+            constexpr uint32_t kIdQK = idesc_16<T>(kKeys, false), kIdPV = idesc_16<T>(D, true);
+            auto take = [&](int& slot) {
+                if (!wait_bounded(full(r.slot), r.phase, abort_flag, status)) return false;
+                tc_fence_after();
+                slot = r.slot;
+                r.next();
+                return true;
+            };
+            auto qk = [&](int v) {
+                const int g = v & 1;
+                if (!kTwo || g == 0)
+                    if (!take(k_slot)) return false;
+                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
+                const uint64_t dk = smem_desc_sw128(sbase + uint32_t(L::kOffRing + k_slot * L::kTile));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = uint64_t(((kk >> 2) * L::kPanel + (kk & 3) * 32) >> 4);
+                    mma_f16(tmem + kColS + 128u * uint32_t(g), dq + off, dk + off, kIdQK, uint32_t(kk > 0));
+                }
+                mma_commit(s_full(g));
+                if (!kTwo || g == 1) mma_commit(empty(k_slot));
+                return true;
+            };
+            for (int i = blockIdx.x; i < items; i += gridDim.x) {
+                const Item w = get(i);
+                for (int g = 0; g < 2; ++g)
+                    if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
+                q_phase ^= 1u;
+                tc_fence_after();
+                if (!qk(0)) goto mma_done;
+                if (w.steps > 1 && !qk(1)) goto mma_done;
+                for (int v = 0; v < w.steps; ++v) {
+                    const int g = v & 1;
+                    if ((!kTwo || g == 0) && !take(v_slot)) goto mma_done;
+                    if (!wait_bounded(p_full(g), p_phase[g], abort_flag, status)) goto mma_done;
+                    p_phase[g] ^= 1u;
+                    tc_fence_after();
+                    const uint64_t dv =
+                        smem_desc_mn_sw128(sbase + uint32_t(L::kOffRing + v_slot * L::kTile), uint32_t(L::kPanel));
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)   // 16 keys = 16 rows of 128 bytes
+                        mma_f16_ta(tmem + kColO + 128u * uint32_t(g), tmem + kColS + 128u * uint32_t(g) + 8u * uint32_t(kk),
+                                   dv + uint64_t((kk * 2048) >> 4), kIdPV, uint32_t(v > 1 || kk > 0));
+                    if (!kTwo || g == 1) mma_commit(empty(v_slot));
+                    if (v + 2 < w.steps) {
+                        if (!qk(v + 2)) goto mma_done;
+                    } else {
+                        mma_commit(o_full(g));
+                    }
+                }
+            }
+        mma_done:
+            mma_commit(drain);   // everything issued, also after a wait that ran out
+            wait_drain(drain, 0u, status);
+        }
+    } else {
+        // ----------------------------------------------------------- softmax
+        const int g = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kColS + 128u * uint32_t(g), to = tmem + lanes + kColO + 128u * uint32_t(g);
+        T* const tag = nullptr;
+        uint32_t s_phase = 0, o_phase = 0;
+        for (int i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item w = get(i);
+            const int64_t r = w.r0 + (kTwo ? g * kRows : 0) + row;
+            const bool valid = r < rows;
+            const int64_t tok = valid ? r / a.group : 0;
+            const int head = int(w.h * a.group + (valid ? r - tok * a.group : 0));
+            // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + tok * p.q_stride + int64_t(head) * D);
+                const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kTile + row * 128);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    st_shared_v4(dst + uint32_t((c >> 3) * L::kPanel + (((c & 7) ^ (row & 7)) << 4)), v.x, v.y, v.z, v.w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full(g));
+            }
+            const int mine = kTwo ? w.steps >> 1 : (w.steps + 1 - g) >> 1;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int n = 0; n < mine && ok; ++n) {
+                ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
+                if (!ok) break;
+                s_phase ^= 1u;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), s[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+                const int64_t left = w.k1 - (w.k0 + int64_t(kTwo ? n : 2 * n + g) * kKeys);
+                if (left < kKeys) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= left) s[c][k] = 0xFF800000u;
+                }
+                float x0 = __uint_as_float(s[0][0]), x1 = __uint_as_float(s[1][0]), x2 = __uint_as_float(s[2][0]),
+                      x3 = __uint_as_float(s[3][0]);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    x0 = max3(x0, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
+                    x1 = max3(x1, __uint_as_float(s[1][k]), __uint_as_float(s[1][k + 1]));
+                    x2 = max3(x2, __uint_as_float(s[2][k]), __uint_as_float(s[2][k + 1]));
+                    x3 = max3(x3, __uint_as_float(s[3][k]), __uint_as_float(s[3][k + 1]));
+                }
+                const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
+                if (__any_sync(0xffffffffu, n == 0 || top > m + kGrow)) {
+                    const float was = m;
+                    m = fmaxf(m, top);
+                    if (n > 0) {
+                        // O is at rest: the product before this S has completed.
+                        const float f = was == m ? 1.f : ex2(was - m);
+                        l *= f;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st_32x32b_x32(to + 32u * uint32_t(c), o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const uint32_t* sc = s[2 * half + (k >> 4)];
+                        const float u = ex2(fmaf(__uint_as_float(sc[2 * (k & 15)]), a.scale_log2, -base));
+                        const float v = ex2(fmaf(__uint_as_float(sc[2 * (k & 15) + 1]), a.scale_log2, -base));
+                        l0 += u;
+                        l1 += v;
+                        pk[k] = pack16(u, v, tag);
+                    }
+                    tmem_st_32x32b_x32(ts + 32u * uint32_t(half), pk);
+                }
+                l += l0 + l1;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(g));
+            }
+            // The part's result.
+            const int part = kTwo ? w.part : 2 * w.part + g;
+            const int64_t at = (int64_t(part) * a.tokens + tok) * p.heads + head;
+            if (!ok) break;
+            if (mine > 0) {
+                ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
+                if (!ok) break;
+                o_phase ^= 1u;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+                    tmem_wait_ld(o);
+                    if (valid) {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                    }
+                }
+                tc_fence_before();
+            }
+            if (valid) a.part_ml[at] = make_float2(m, l);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+bool encode_prefix(CUtensorMap* m, const mmq_shared_prefix_attention_t& p, const void* base) {
+    auto fn = get_encode();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(p.head_dim), cuuint64_t(p.kv_heads), cuuint64_t(p.prefix)};
+    const cuuint64_t strides[2] = {cuuint64_t(p.prefix_head_stride) * 2, cuuint64_t(p.prefix_token_stride) * 2};
+    const cuuint32_t box[3] = {64, 1, kKeys}, estr[3] = {1, 1, 1};
+    return fn(m, p.type == MMQ_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool kTwo>
+cudaError_t launch(const AttnArgs& a, int nsm, cudaLaunchConfig_t cfg) {
+    Maps maps;
+    if (!encode_prefix(&maps.k, a.p, a.p.k_prefix) || !encode_prefix(&maps.v, a.p, a.p.v_prefix))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    constexpr int smem = Layout<D>::kBytes;
+    if ((e = cudaFuncSetAttribute(attn_prefix_kernel<T, D, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+        return e;
+    const int64_t per = kTwo ? 2 * kRows : kRows;
+    const int64_t items = (a.tokens * a.group + per - 1) / per * a.p.kv_heads * (a.prefix_parts / (kTwo ? 1 : 2));
+    cfg.gridDim = dim3(unsigned(items < nsm ? items : nsm));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, attn_prefix_kernel<T, D, kTwo>, maps, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const AttnArgs& a, int nsm, const cudaLaunchConfig_t& cfg) {
+    return a.prefix_tiles == 2 ? launch<T, D, true>(a, nsm, cfg) : launch<T, D, false>(a, nsm, cfg);
+}
+
+}  // namespace
+
+namespace mmq {
+
+cudaError_t launch_attention_prefix(const AttnArgs& a, int nsm, const cudaLaunchConfig_t& cfg) {
+    if (a.p.type == MMQ_TYPE_F16)
+        return a.p.head_dim == 64 ? launch_rows<__half, 64>(a, nsm, cfg) : launch_rows<__half, 128>(a, nsm, cfg);
+    return a.p.head_dim == 64 ? launch_rows<__nv_bfloat16, 64>(a, nsm, cfg) : launch_rows<__nv_bfloat16, 128>(a, nsm, cfg);
+}
+
+}  // namespace mmq
