@@ -49,6 +49,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -59,56 +64,62 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
 }
 
 // ------------------------------------------------------- few rows per key
-// One CTA: up to 16 rows that see the same keys (a token's heads of one kv
-// head over a part of its suffix; or any 16 rows over a part of the prefix).
-// Bound by the key / value bytes, so rows are padded to the 16 of one
-// mma.sync tile and the four warps take 16-key slabs in turn, each warp with
-// its own cp.async ring (4 warps x 3 stages x 16 keys x K and V, 96 KB at 128
-// dims, two CTAs per SM: 192 KB in flight), its own running maximum and sum,
-// joined through shared memory at the end.  Keys past the row's limit are
-// filled with zeros, not read, so what the cache holds there cannot matter.
-// Weights are rounded to the cache's type for the second product (their sum
-// is taken in f32 before that); both products accumulate in f32.
-constexpr int kWarps = 4, kSlab = 16, kStages = 3;
+// One warp, a CTA of its own: up to 16 rows that see the same keys (a token's
+// heads of one kv head over a part of its suffix; or any 16 rows over a part
+// of the prefix).  Bound by the key / value bytes: rows are padded to the 16 of
+// one mma.sync tile, keys come 16 at a time through a cp.async ring of three
+// (24 KB at 128 dims, nine such warps per SM: up to 144 KB in flight), and
+// warps that start, stream and finish on their own keep the memory busy where
+// suffixes are short.  Keys past the row's limit are filled with zeros, not
+// read, so what the cache holds there cannot matter.  Weights are rounded to
+// the cache's type for the second product (their sum is taken in f32 before
+// that); both products accumulate in f32.
+constexpr int kSlab = 16, kStages = 3;
 
 template <int D>
 constexpr int row_smem() {
-    return kWarps * kStages * 2 * kSlab * D * 2;
+    return kStages * 2 * kSlab * D * 2;
 }
+template <int D>
+constexpr int row_resident() {   // warps per SM that the launch plans for
+    return D == 128 ? 9 : 14;
+}
+enum class Keys { kPrefix, kPages, kSmallPages };   // kPages: pages of 16 and more, a slab lies on one
 
-template <typename T, int D, bool kPrefix>
-__global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArgs a) {
+template <typename T, int D, Keys kKeys>
+__global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const mmq_shared_prefix_attention_t& p = a.p;
     T* const tag = nullptr;
-    griddep_launch_dependents();
+    // No early trigger for the next kernel: its CTAs, one per SM, would take the
+    // room of the last third of these (170 against 150 us at 256 sequences).
     griddep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x;
     const int h = blockIdx.y, G = a.group;
     const int tiles_per_token = (G + 15) / 16;
 
-    // Rows [r0, r1) and keys [k0, k1) of this CTA.
+    // Rows [r0, r1) and keys [k0, k1) of this warp.
     int64_t r0, r1, k0, k1;
     int part = blockIdx.z;
     const int32_t* pages = nullptr;
-    if (kPrefix) {
+    if (kKeys == Keys::kPrefix) {
         r0 = int64_t(blockIdx.x) * 16;
         r1 = min(r0 + 16, a.tokens * G);
         k0 = part * a.part_keys;
         k1 = min(k0 + a.part_keys, p.prefix);
     } else {
-        const int64_t t = blockIdx.x / tiles_per_token;
-        const int b = int(t / p.q_len);
-        r0 = t * G + int64_t(blockIdx.x % tiles_per_token) * 16;
-        r1 = min(r0 + 16, t * G + G);
-        pages = p.page_table + int64_t(b) * p.table_width;
+        const int t = int(blockIdx.x) / tiles_per_token, tile = int(blockIdx.x) - t * tiles_per_token;
+        const int b = t / p.q_len;
+        r0 = int64_t(t) * G + tile * 16;
+        r1 = min(r0 + 16, int64_t(t) * G + G);
+        pages = p.page_table + b * p.table_width;
         const int64_t room = p.table_width << a.page_shift;
         int64_t len = p.lens[b];
         if (len > room) {
-            if (threadIdx.x == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+            if (lane == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
             len = room;
         }
-        len = max(int64_t(0), len - p.q_len + 1 + t % p.q_len);
+        len = max(int64_t(0), len - p.q_len + 1 + (t - b * p.q_len));
         const int64_t step = ((len + a.suffix_parts - 1) / a.suffix_parts + 63) & ~int64_t(63);
         k0 = min(part * step, len);
         k1 = min(k0 + step, len);
@@ -116,20 +127,79 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
     }
     const int64_t part_row = int64_t(part) * a.tokens;
     const int grow = lane >> 2, gcol = lane & 3;
-    auto token_head = [&](int64_t r) { return (r / G) * p.heads + int64_t(h) * G + r % G; };
+    auto token_head = [&](int64_t r) {   // row r's place among [tokens][heads]
+        const int64_t t = r / G;
+        return t * p.heads + int64_t(h) * G + (r - t * G);
+    };
 
     if (k0 >= k1) {
-        if (threadIdx.x < 16 && r0 + threadIdx.x < r1)
-            a.part_ml[part_row * p.heads + token_head(r0 + threadIdx.x)] = make_float2(-INFINITY, 0.f);
+        if (lane < 16 && r0 + lane < r1) a.part_ml[part_row * p.heads + token_head(r0 + lane)] = make_float2(-INFINITY, 0.f);
         return;
+    }
+
+    const uint32_t ring = smem_u32(smem);
+    constexpr uint32_t kHalfStage = kSlab * D * 2;
+    constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
+    constexpr int kRowsAtOnce = 32 / kChunks;
+    const int slabs = int((k1 - k0 + kSlab - 1) / kSlab);
+    bool bad_page = false;
+
+    const T* const keys = static_cast<const T*>(kKeys == Keys::kPrefix ? p.k_prefix : p.k_cache);
+    const T* const values = static_cast<const T*>(kKeys == Keys::kPrefix ? p.v_prefix : p.v_cache);
+    const int64_t step = kKeys == Keys::kPrefix ? p.prefix_token_stride : int64_t(p.kv_heads) * D;   // from key to key
+    const int64_t head = h * (kKeys == Keys::kPrefix ? p.prefix_head_stride : int64_t(D)) + (lane % kChunks) * 8;
+    const int64_t in_page = (int64_t(1) << a.page_shift) - 1;
+    int32_t next_id = kKeys == Keys::kPages ? pages[k0 >> a.page_shift] : 0;   // the next slab's page
+
+    // Slab i's rows: kRowsAtOnce rows of 16-byte chunks per instruction, chunk
+    // c of row r at c ^ (r & 7) (conflict-free for ldmatrix).
+    auto fetch = [&](int i, int stage) {
+        const int64_t first = k0 + int64_t(i) * kSlab;
+        int left = int(min(k1 - first, int64_t(kSlab)));   // rows to read
+        int64_t at = first;                                 // the first row's place in the cache
+        if (kKeys == Keys::kPages) {
+            const int32_t id = next_id;
+            if (id < 0 || id >= p.n_pages) {
+                bad_page = true;
+                left = 0;
+            }
+            at = (int64_t(id) << a.page_shift) + (first & in_page);
+            const int64_t then = first + kSlab;
+            if (then < k1) next_id = pages[then >> a.page_shift];
+        }
+        const uint32_t base = ring + uint32_t(stage) * 2 * kHalfStage;
+#pragma unroll
+        for (int j = 0; j < kSlab / kRowsAtOnce; ++j) {
+            const int r = j * kRowsAtOnce + lane / kChunks;
+            bool valid = r < left;
+            int64_t row = at + r;
+            if (kKeys == Keys::kSmallPages && valid) {
+                const int32_t id = pages[(first + r) >> a.page_shift];
+                if (id < 0 || id >= p.n_pages) {
+                    bad_page = true;
+                    valid = false;
+                }
+                row = (int64_t(id) << a.page_shift) + ((first + r) & in_page);
+            }
+            const int64_t off = row * step + head;
+            const uint32_t dst = base + uint32_t(r * D * 2 + (((lane % kChunks) ^ (r & 7)) << 4));
+            const T* none = static_cast<const T*>(p.q);   // an invalid row is filled with zeros, nothing is read
+            cp_async16(dst, valid ? keys + off : none, valid);
+            cp_async16(dst + kHalfStage, valid ? values + off : none, valid);
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (s < slabs) fetch(s, s);
+        cp_async_commit();
     }
 
     // Query fragments: rows grow and grow + 8, zero past r1.
     uint32_t qf[D / 16][4];
     {
-        const int64_t ra = r0 + grow, rb = ra + 8;
-        const T* qa = static_cast<const T*>(p.q) + (ra / G) * p.q_stride + (int64_t(h) * G + ra % G) * D;
-        const T* qb = static_cast<const T*>(p.q) + (rb / G) * p.q_stride + (int64_t(h) * G + rb % G) * D;
+        const int64_t ra = r0 + grow, rb = ra + 8, ta = ra / G, tb = rb / G;
+        const T* qa = static_cast<const T*>(p.q) + ta * p.q_stride + (int64_t(h) * G + (ra - ta * G)) * D;
+        const T* qb = static_cast<const T*>(p.q) + tb * p.q_stride + (int64_t(h) * G + (rb - tb * G)) * D;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const int c = kk * 16 + 2 * gcol;
@@ -140,70 +210,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
         }
     }
 
-    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages * 2 * kSlab * D * 2);
-    constexpr uint32_t kHalfStage = kSlab * D * 2;
-    constexpr int kChunks = D / 8;                 // 16-byte chunks of a row
-    const int64_t slabs = (k1 - k0 + kSlab - 1) / kSlab;
-    bool bad_page = false;
-
-    // Slab i's rows: 32 / kChunks rows of 16-byte chunks per step, chunk c of
-    // row r at c ^ (r & 7) (conflict-free for ldmatrix).
-    auto fetch = [&](int64_t i, int stage) {
-        const uint32_t base = ring + uint32_t(stage) * 2 * kHalfStage;
-        constexpr int kRows = 32 / kChunks;
-        const int c = lane % kChunks;
-#pragma unroll
-        for (int j = 0; j < kSlab / kRows; ++j) {
-            const int r = j * kRows + lane / kChunks;
-            const int64_t key = k0 + i * kSlab + r;
-            bool valid = key < k1;
-            int64_t off = 0;
-            if (valid) {
-                if (kPrefix) {
-                    off = key * p.prefix_token_stride + h * p.prefix_head_stride;
-                } else {
-                    const int32_t id = pages[key >> a.page_shift];
-                    if (id < 0 || id >= p.n_pages) {
-                        bad_page = true;
-                        valid = false;
-                    } else {
-                        off = ((((int64_t(id) << a.page_shift) + (key & ((int64_t(1) << a.page_shift) - 1))) *
-                                p.kv_heads) + h) * D;
-                    }
-                }
-            }
-            const uint32_t dst = base + uint32_t(r * D * 2 + ((c ^ (r & 7)) << 4));
-            const T* kp = static_cast<const T*>(kPrefix ? p.k_prefix : p.k_cache) + off + c * 8;
-            const T* vp = static_cast<const T*>(kPrefix ? p.v_prefix : p.v_cache) + off + c * 8;
-            cp_async16(dst, valid ? kp : static_cast<const T*>(p.q), valid);
-            cp_async16(dst + kHalfStage, valid ? vp : static_cast<const T*>(p.q), valid);
-        }
-    };
-
     float o[D / 8][4];
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const int m = lane >> 3, r7 = lane & 7;
+    const uint32_t krow = uint32_t(((m >> 1) * 8 + r7) * D * 2), vrow = uint32_t(((m & 1) * 8 + r7) * D * 2);
 
-    // This warp's slabs: warp, warp + 4, ...
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (warp + int64_t(s) * kWarps < slabs) fetch(warp + int64_t(s) * kWarps, s);
-        cp_async_commit();
-    }
     int stage = 0;
-    for (int64_t i = warp; i < slabs; i += kWarps) {
-        const int64_t ahead = i + int64_t(kStages - 1) * kWarps;
-        if (ahead < slabs) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+    for (int i = 0; i < slabs; ++i) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();   // slab i is here, and every lane is done with the stage before it
+        if (i + kStages - 1 < slabs) fetch(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
         cp_async_commit();
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
         const uint32_t kb = ring + uint32_t(stage) * 2 * kHalfStage, vb = kb + kHalfStage;
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-        const int m = lane >> 3, r7 = lane & 7;
-        const uint32_t krow = uint32_t(((m >> 1) * 8 + r7) * D * 2), vrow = uint32_t(((m & 1) * 8 + r7) * D * 2);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t b[4];
@@ -211,8 +234,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
             mma16816(s0, qf[kk], b[0], b[1], tag);
             mma16816(s1, qf[kk], b[2], b[3], tag);
         }
-        const int64_t left = k1 - (k0 + i * kSlab);   // keys of this slab: all from 16 on
         float x[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
+        const int left = int(min(k1 - k0 - int64_t(i) * kSlab, int64_t(kSlab)));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int key = (k & 2 ? 8 : 0) + 2 * gcol + (k & 1);
@@ -226,7 +249,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
         const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
         if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
             // (-inf) - (-inf) only where the sums are still zero
-            const float f0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0), f1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+            const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
             l0 *= f0;
             l1 *= f1;
 #pragma unroll
@@ -240,8 +263,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
         const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            x[k] = exp2f(x[k] - b0);
-            x[k + 4] = exp2f(x[k + 4] - b1);
+            x[k] = ex2(x[k] - b0);
+            x[k + 4] = ex2(x[k + 4] - b1);
         }
         l0 += (x[0] + x[1]) + (x[2] + x[3]);
         l1 += (x[4] + x[5]) + (x[6] + x[7]);
@@ -254,7 +277,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
             mma16816(o[2 * dc], pf, b[0], b[1], tag);
             mma16816(o[2 * dc + 1], pf, b[2], b[3], tag);
         }
-        __syncwarp();
         if (++stage == kStages) stage = 0;
     }
     cp_async_wait<0>();
@@ -263,43 +285,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_rows_kernel(const AttnArg
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-
-    // Join the four warps: their rows in shared memory, f32 [warp][16][D], and
-    // (m, l) [warp][16].
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);
-    __shared__ float2 sml[kWarps][16];
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<float2*>(so + (warp * 16 + grow) * D + n * 8 + 2 * gcol) = make_float2(o[n][0], o[n][1]);
-        *reinterpret_cast<float2*>(so + (warp * 16 + grow + 8) * D + n * 8 + 2 * gcol) = make_float2(o[n][2], o[n][3]);
-    }
-    if (gcol == 0) {
-        sml[warp][grow] = make_float2(m0, l0);
-        sml[warp][grow + 8] = make_float2(m1, l1);
-    }
-    __syncthreads();
-    constexpr int kLanes = D / 4, kRowsAtOnce = kWarps * 32 / kLanes;
-    const int c4 = (threadIdx.x % kLanes) * 4;
-    for (int r = threadIdx.x / kLanes; r < 16 && r0 + r < r1; r += kRowsAtOnce) {
-        float mm = -INFINITY;
+    for (int half = 0; half < 2; ++half) {
+        const int64_t r = r0 + grow + 8 * half;
+        if (r >= r1) continue;
+        const int64_t at = part_row * p.heads + token_head(r);
+        float* dst = a.part_o + at * D + 2 * gcol;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sml[w][r].x);
-        float ll = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float2 ml = sml[w][r];
-            // a warp without keys has l = 0 (and m = -inf)
-            const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - mm);
-            const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + c4);
-            ll = fmaf(f, ml.y, ll);
-            acc.x = fmaf(f, v.x, acc.x); acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z); acc.w = fmaf(f, v.w, acc.w);
-        }
-        const int64_t at = part_row * p.heads + token_head(r0 + r);
-        *reinterpret_cast<float4*>(a.part_o + at * D + c4) = acc;
-        if (c4 == 0) a.part_ml[at] = make_float2(mm, ll);
+        for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
+        if (gcol == 0) a.part_ml[at] = half ? make_float2(m1, l1) : make_float2(m0, l0);
     }
 }
 
@@ -378,7 +373,7 @@ int sm_count() {
 }
 
 // Parts for `units` independent pieces of up to `keys` keys each, on `slots`
-// resident CTAs: enough to give every slot a piece, none shorter than `least`.
+// resident warps: enough to give every slot a piece, none shorter than `least`.
 int split(int64_t units, int64_t keys, int64_t slots, int64_t least) {
     if (keys <= 0) return 0;
     int64_t n = (slots + units - 1) / units;
@@ -414,7 +409,7 @@ void plan(AttnArgs& a, int nsm) {
     a.page_shift = 0;
     while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
     const int64_t rows = a.tokens * a.group;
-    const int64_t slots = int64_t(nsm) * 2;
+    const int64_t slots = int64_t(nsm) * (p.head_dim == 128 ? row_resident<128>() : row_resident<64>());
     a.prefix_tiles = rows <= 16 ? 0 : rows <= 128 ? 1 : 2;
     a.prefix_parts = 0;
     a.part_keys = 0;
@@ -425,12 +420,13 @@ void plan(AttnArgs& a, int nsm) {
             const int64_t units = (rows + 128 * a.prefix_tiles - 1) / (128 * a.prefix_tiles) * p.kv_heads;
             n = tc_parts(units, (p.prefix + tile - 1) / tile, nsm);
         } else {
-            n = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 256);
+            n = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 64);
         }
         a.part_keys = ((p.prefix + n - 1) / n + tile - 1) / tile * tile;
         a.prefix_parts = int((p.prefix + a.part_keys - 1) / a.part_keys) * (a.prefix_tiles == 1 ? 2 : 1);
     }
-    a.suffix_parts = split(a.tokens * ((a.group + 15) / 16) * p.kv_heads, p.table_width << a.page_shift, slots, 256);
+    // ragged suffixes: several warps per slot, so that the longest do not end last alone
+    a.suffix_parts = split(a.tokens * ((a.group + 15) / 16) * p.kv_heads, p.table_width << a.page_shift, 3 * slots, 64);
 }
 
 size_t ml_bytes(const AttnArgs& a) {
@@ -450,21 +446,18 @@ cudaError_t launch(const AttnArgs& a, int nsm, cudaStream_t s) {
     };
     constexpr int smem = row_smem<D>();
     if (a.suffix_parts) {
-        if ((e = cudaFuncSetAttribute(attn_rows_kernel<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-            return e;
+        auto* kernel = a.p.page_size >= kSlab ? attn_rows_kernel<T, D, Keys::kPages> : attn_rows_kernel<T, D, Keys::kSmallPages>;
         const dim3 grid(unsigned(a.tokens * ((a.group + 15) / 16)), unsigned(a.p.kv_heads), unsigned(a.suffix_parts));
-        const cudaLaunchConfig_t cfg = config(grid, dim3(kWarps * 32), smem);
-        if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, false>, a))) return e;
+        const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
+        if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
     }
     if (a.prefix_parts && a.prefix_tiles) {
         const cudaLaunchConfig_t cfg = config(dim3(1), dim3(1), 0);
         if ((e = mmq::launch_attention_prefix(a, nsm, cfg))) return e;
     } else if (a.prefix_parts) {
-        if ((e = cudaFuncSetAttribute(attn_rows_kernel<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-            return e;
         const dim3 grid(unsigned((a.tokens * a.group + 15) / 16), unsigned(a.p.kv_heads), unsigned(a.prefix_parts));
-        const cudaLaunchConfig_t cfg = config(grid, dim3(kWarps * 32), smem);
-        if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, true>, a))) return e;
+        const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
+        if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, Keys::kPrefix>, a))) return e;
     }
     const cudaLaunchConfig_t cfg = config(dim3(unsigned((a.tokens * a.p.heads + 7) / 8)), dim3(256), 0);
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, a);
