@@ -13,7 +13,7 @@
 //                   lane): read S, keep the row's maximum and sum, write P over
 //                   S, and now and then scale O
 //   warp 8          TMA producer: key and value tiles (128 keys, 128-byte
-//                   swizzled panels of 64 values) through a ring of four
+//                   swizzled panels of 64 values) through a 128 KB ring
 //   warp 9          MMA issuer: S_i = Q_i K^T, O_i += P_i V, P from tensor memory
 // More than 128 rows: the groups hold two row tiles and share each key tile.
 // Up to 128: both hold the same rows and take key tiles in turn, as two parts.
@@ -39,7 +39,12 @@ using namespace mmq::tc;
 using mmq::AttnArgs;
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kThreads = 320, kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 384, kWarpTma = 8, kWarpMma = 9;
+// Registers: 168 per thread at launch (the launcher checks it), of which the
+// third warpgroup gives up 96 so that a softmax thread can hold its row of
+// 128 scores: 2 x 128 x 216 + 128 x 72 = 384 x 168.
+constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S_i at 128 i (P_i over its first 64 columns), O_i at 256 + 128 i
 constexpr float kGrow = 8.f;
@@ -53,8 +58,8 @@ struct Layout {
     static constexpr int kOffQ = 0;                          // two row tiles
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kSlots * kTile;
-    // barriers: full, empty per slot; q_full, s_full, p_full, o_full per group; drain
-    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 9) * 8;
+    // barriers: full, empty per slot; q_full, s_full, o_full per group, p_full per group and half; drain
+    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 11) * 8;
     static constexpr int kBytes = kOffMisc + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448, "shared memory budget");
@@ -101,9 +106,9 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     auto empty = [&](int s) { return bar0 + 8u * uint32_t(kSlots + s); };
     auto q_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + g); };
     auto s_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 2 + g); };
-    auto p_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 4 + g); };
-    auto o_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 6 + g); };
-    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 8);
+    auto o_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 4 + g); };
+    auto p_full = [&](int g, int half) { return bar0 + 8u * uint32_t(2 * kSlots + 6 + 2 * g + half); };
+    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 10);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     const AbortFlag abort_flag{sbase + L::kOffMisc + 4};
     const mmq_shared_prefix_attention_t& p = a.p;
@@ -118,7 +123,8 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         for (int g = 0; g < 2; ++g) {
             mbar_init(q_full(g), 4);
             mbar_init(s_full(g), 1);
-            mbar_init(p_full(g), 4);
+            mbar_init(p_full(g, 0), 4);
+            mbar_init(p_full(g, 1), 4);
             mbar_init(o_full(g), 1);
         }
         mbar_init(drain, 1);
@@ -162,103 +168,110 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         return w;
     };
 
-    if (warp == kWarpTma) {
-        // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            Ring<kSlots> r;
-            int issued[kSlots] = {};
-            uint32_t par[kSlots] = {};
-            auto load = [&](const CUtensorMap* map, int h, int64_t key) {
-                if (!wait_bounded(empty(r.slot), r.phase ^ 1u, abort_flag, status)) return false;
-                const uint32_t dst = sbase + uint32_t(L::kOffRing + r.slot * L::kTile);
-                mbar_arrive_expect_tx(full(r.slot), uint32_t(L::kTile));
+    if (warp >= 8) {
+        setmaxnreg_dec<kRegsOther>();
+        if (warp == kWarpTma) {
+            // ---------------------------------------------------------- producer
+            if (lane == 0) {
+                Ring<kSlots> r;
+                int issued[kSlots] = {};
+                uint32_t par[kSlots] = {};
+                auto load = [&](const CUtensorMap* map, int h, int64_t key) {
+                    if (!wait_bounded(empty(r.slot), r.phase ^ 1u, abort_flag, status)) return false;
+                    const uint32_t dst = sbase + uint32_t(L::kOffRing + r.slot * L::kTile);
+                    mbar_arrive_expect_tx(full(r.slot), uint32_t(L::kTile));
 #pragma unroll
-                for (int c = 0; c < L::kPanels; ++c)
-                    tma_load_3d(dst + uint32_t(c * L::kPanel), map, full(r.slot), 64 * c, h, int32_t(key));
-                issued[r.slot] = 1;
-                par[r.slot] = r.phase;
-                r.next();
-                return true;
-            };
-            for (int i = blockIdx.x; i < items; i += gridDim.x) {
-                const Item w = get(i);
-                // in the order the MMA warp takes them
-                auto key = [&](int v) { return w.k0 + int64_t(kTwo ? v >> 1 : v) * kKeys; };
-                auto want = [&](int v) { return v < w.steps && (!kTwo || !(v & 1)); };
-                if (want(0) && !load(&maps.k, w.h, key(0))) goto producer_done;
-                if (want(1) && !load(&maps.k, w.h, key(1))) goto producer_done;
-                for (int v = 0; v < w.steps; ++v) {
-                    if (want(v) && !load(&maps.v, w.h, key(v))) goto producer_done;
-                    if (want(v + 2) && !load(&maps.k, w.h, key(v + 2))) goto producer_done;
-                }
-            }
-        producer_done:
-            for (int s = 0; s < kSlots; ++s)
-                if (issued[s]) wait_drain(full(s), par[s], status);
-        }
-    } else if (warp == kWarpMma) {
-        // -------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            Ring<kSlots> r;
-            int k_slot = 0, v_slot = 0;
-            uint32_t q_phase = 0, p_phase[2] = {0, 0};
-            constexpr uint32_t kIdQK = idesc_16<T>(kKeys, false), kIdPV = idesc_16<T>(D, true);
-            auto take = [&](int& slot) {
-                if (!wait_bounded(full(r.slot), r.phase, abort_flag, status)) return false;
-                tc_fence_after();
-                slot = r.slot;
-                r.next();
-                return true;
-            };
-            auto qk = [&](int v) {
-                const int g = v & 1;
-                if (!kTwo || g == 0)
-                    if (!take(k_slot)) return false;
-                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
-                const uint64_t dk = smem_desc_sw128(sbase + uint32_t(L::kOffRing + k_slot * L::kTile));
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = uint64_t(((kk >> 2) * L::kPanel + (kk & 3) * 32) >> 4);
-                    mma_f16(tmem + kColS + 128u * uint32_t(g), dq + off, dk + off, kIdQK, uint32_t(kk > 0));
-                }
-                mma_commit(s_full(g));
-                if (!kTwo || g == 1) mma_commit(empty(k_slot));
-                return true;
-            };
-            for (int i = blockIdx.x; i < items; i += gridDim.x) {
-                const Item w = get(i);
-                for (int g = 0; g < 2; ++g)
-                    if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
-                q_phase ^= 1u;
-                tc_fence_after();
-                if (!qk(0)) goto mma_done;
-                if (w.steps > 1 && !qk(1)) goto mma_done;
-                for (int v = 0; v < w.steps; ++v) {
-                    const int g = v & 1;
-                    if ((!kTwo || g == 0) && !take(v_slot)) goto mma_done;
-                    if (!wait_bounded(p_full(g), p_phase[g], abort_flag, status)) goto mma_done;
-                    p_phase[g] ^= 1u;
-                    tc_fence_after();
-                    const uint64_t dv =
-                        smem_desc_mn_sw128(sbase + uint32_t(L::kOffRing + v_slot * L::kTile), uint32_t(L::kPanel));
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)   // 16 keys = 16 rows of 128 bytes
-                        mma_f16_ta(tmem + kColO + 128u * uint32_t(g), tmem + kColS + 128u * uint32_t(g) + 8u * uint32_t(kk),
-                                   dv + uint64_t((kk * 2048) >> 4), kIdPV, uint32_t(v > 1 || kk > 0));
-                    if (!kTwo || g == 1) mma_commit(empty(v_slot));
-                    if (v + 2 < w.steps) {
-                        if (!qk(v + 2)) goto mma_done;
-                    } else {
-                        mma_commit(o_full(g));
+                    for (int c = 0; c < L::kPanels; ++c)
+                        tma_load_3d(dst + uint32_t(c * L::kPanel), map, full(r.slot), 64 * c, h, int32_t(key));
+                    issued[r.slot] = 1;
+                    par[r.slot] = r.phase;
+                    r.next();
+                    return true;
+                };
+                for (int i = blockIdx.x; i < items; i += gridDim.x) {
+                    const Item w = get(i);
+                    // in the order the MMA warp takes them
+                    auto key = [&](int v) { return w.k0 + int64_t(kTwo ? v >> 1 : v) * kKeys; };
+                    auto want = [&](int v) { return v < w.steps && (!kTwo || !(v & 1)); };
+                    if (want(0) && !load(&maps.k, w.h, key(0))) goto producer_done;
+                    if (want(1) && !load(&maps.k, w.h, key(1))) goto producer_done;
+                    for (int v = 0; v < w.steps; ++v) {
+                        if (want(v) && !load(&maps.v, w.h, key(v))) goto producer_done;
+                        if (want(v + 2) && !load(&maps.k, w.h, key(v + 2))) goto producer_done;
                     }
                 }
+            producer_done:
+                for (int s = 0; s < kSlots; ++s)
+                    if (issued[s]) wait_drain(full(s), par[s], status);
             }
-        mma_done:
-            mma_commit(drain);   // everything issued, also after a wait that ran out
-            wait_drain(drain, 0u, status);
+        } else if (warp == kWarpMma) {
+            // -------------------------------------------------------- MMA issuer
+            if (lane == 0) {
+                Ring<kSlots> r;
+                int k_slot = 0, v_slot = 0;
+                uint32_t q_phase = 0, p_phase[2] = {0, 0};
+                constexpr uint32_t kIdQK = idesc_16<T>(kKeys, false), kIdPV = idesc_16<T>(D, true);
+                auto take = [&](int& slot) {
+                    if (!wait_bounded(full(r.slot), r.phase, abort_flag, status)) return false;
+                    tc_fence_after();
+                    slot = r.slot;
+                    r.next();
+                    return true;
+                };
+                auto qk = [&](int v) {
+                    const int g = v & 1;
+                    if (!kTwo || g == 0)
+                        if (!take(k_slot)) return false;
+                    const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
+                    const uint64_t dk = smem_desc_sw128(sbase + uint32_t(L::kOffRing + k_slot * L::kTile));
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = uint64_t(((kk >> 2) * L::kPanel + (kk & 3) * 32) >> 4);
+                        mma_f16(tmem + kColS + 128u * uint32_t(g), dq + off, dk + off, kIdQK, uint32_t(kk > 0));
+                    }
+                    mma_commit(s_full(g));
+                    if (!kTwo || g == 1) mma_commit(empty(k_slot));
+                    return true;
+                };
+                for (int i = blockIdx.x; i < items; i += gridDim.x) {
+                    const Item w = get(i);
+                    for (int g = 0; g < 2; ++g)
+                        if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
+                    q_phase ^= 1u;
+                    tc_fence_after();
+                    if (!qk(0)) goto mma_done;
+                    if (w.steps > 1 && !qk(1)) goto mma_done;
+                    for (int v = 0; v < w.steps; ++v) {
+                        const int g = v & 1;
+                        if ((!kTwo || g == 0) && !take(v_slot)) goto mma_done;
+                        const uint64_t dv =
+                            smem_desc_mn_sw128(sbase + uint32_t(L::kOffRing + v_slot * L::kTile), uint32_t(L::kPanel));
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk) {   // 16 keys = 16 rows of 128 bytes
+                            if ((kk & 3) == 0) {
+                                if (!wait_bounded(p_full(g, kk >> 2), p_phase[g], abort_flag, status)) goto mma_done;
+                                tc_fence_after();
+                            }
+                            mma_f16_ta(tmem + kColO + 128u * uint32_t(g), tmem + kColS + 128u * uint32_t(g) + 8u * uint32_t(kk),
+                                       dv + uint64_t((kk * 2048) >> 4), kIdPV, uint32_t(v > 1 || kk > 0));
+                        }
+                        p_phase[g] ^= 1u;
+                        if (!kTwo || g == 1) mma_commit(empty(v_slot));
+                        if (v + 2 < w.steps) {
+                            if (!qk(v + 2)) goto mma_done;
+                        } else {
+                            mma_commit(o_full(g));
+                        }
+                    }
+                }
+            mma_done:
+                mma_commit(drain);   // everything issued, also after a wait that ran out
+                wait_drain(drain, 0u, status);
+            }
         }
     } else {
         // ----------------------------------------------------------- softmax
+        setmaxnreg_inc<kRegsSoftmax>();
         const int g = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -334,26 +347,27 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : m;
-                float l0 = 0.f, l1 = 0.f;
+                const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const uint32_t* sc = s[2 * half + (k >> 4)];
-                        const float u = ex2(fmaf(__uint_as_float(sc[2 * (k & 15)]), a.scale_log2, -base));
-                        const float v = ex2(fmaf(__uint_as_float(sc[2 * (k & 15) + 1]), a.scale_log2, -base));
-                        l0 += u;
-                        l1 += v;
+                        const uint32_t* sc = &s[2 * half + (k >> 4)][2 * (k & 15)];
+                        const uint64_t e = ffma2(pack2u(sc[0], sc[1]), scale2, base2);
+                        const float u = ex2(lo_f(e)), v = ex2(hi_f(e));
+                        sum[k & 1] = fadd2(sum[k & 1], pack2(u, v));
                         pk[k] = pack16(u, v, tag);
                     }
                     tmem_st_32x32b_x32(ts + 32u * uint32_t(half), pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(g, half));
                 }
-                l += l0 + l1;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(g));
+                sum[0] = fadd2(sum[0], sum[1]);
+                l += lo_f(sum[0]) + hi_f(sum[0]);
             }
             // The part's result.
             const int part = kTwo ? w.part : 2 * w.part + g;
@@ -411,6 +425,11 @@ cudaError_t launch(const AttnArgs& a, int nsm, cudaLaunchConfig_t cfg) {
         return cudaErrorInvalidValue;
     cudaError_t e;
     constexpr int smem = Layout<D>::kBytes;
+    static const bool registers_ok = [] {   // else the split's increase would wait forever
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, attn_prefix_kernel<T, D, kTwo>) == cudaSuccess && f.numRegs == int(kRegsLaunch);
+    }();
+    if (!registers_ok) return cudaErrorLaunchOutOfResources;
     if ((e = cudaFuncSetAttribute(attn_prefix_kernel<T, D, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
         return e;
     const int64_t per = kTwo ? 2 * kRows : kRows;
