@@ -14,10 +14,16 @@
 //                   S, and now and then scale O
 //   warp 8          TMA producer: key and value tiles (128 keys, 128-byte
 //                   swizzled panels of 64 values) through a 128 KB ring
-//   warp 9          MMA issuer: S_i = Q_i K^T, O_i += P_i V, P from tensor memory
+//   warps 9, 10     MMA issuers of groups 0 and 1: S = Q K^T, O += P V, P from
+//                   tensor memory, taking turns batch by batch
 // More than 128 rows: the groups hold two row tiles and share each key tile.
 // Up to 128: both hold the same rows and take key tiles in turn, as two parts.
-// While one group does its softmax the tensor cores work for the other.
+// While one group does its softmax (1270 cycles a tile) the tensor cores work
+// for the other (16 products of 64 cycles).  The issuing thread is held for the
+// whole of its products, so one thread for both groups left the tensor cores
+// idle while it did anything else (2050 cycles a batch), and two free ones fell
+// into step, both groups at their softmax and then both at their products (1950
+// a batch); hence two that pass a turn.
 //
 // O is only scaled when a row's maximum has grown by more than 2^8 since the
 // last time (P then stays below 2^8, far inside fp16's range, and nothing is
@@ -39,11 +45,11 @@ using namespace mmq::tc;
 using mmq::AttnArgs;
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kThreads = 384, kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 384, kWarpTma = 8, kWarpMma = 9;   // and kWarpMma + 1
 // Registers: 168 per thread at launch (the launcher checks it), of which the
-// third warpgroup gives up 96 so that a softmax thread can hold its row of
-// 128 scores: 2 x 128 x 216 + 128 x 72 = 384 x 168.
-constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
+// third warpgroup gives up 80 so that a softmax thread can hold its row of
+// 128 scores: 2 x 128 x 208 + 128 x 88 = 384 x 168.
+constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S_i at 128 i (P_i over its first 64 columns), O_i at 256 + 128 i
@@ -58,8 +64,9 @@ struct Layout {
     static constexpr int kOffQ = 0;                          // two row tiles
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kSlots * kTile;
-    // barriers: full, empty per slot; q_full, s_full, o_full per group, p_full per group and half; drain
-    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 11) * 8;
+    // barriers: full, empty per slot; q_full, s_full, o_full per group, p_full per group and half; turn
+    // per group; drain
+    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 13) * 8;
     static constexpr int kBytes = kOffMisc + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448, "shared memory budget");
@@ -108,7 +115,8 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     auto s_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 2 + g); };
     auto o_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 4 + g); };
     auto p_full = [&](int g, int half) { return bar0 + 8u * uint32_t(2 * kSlots + 6 + 2 * g + half); };
-    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 10);
+    auto turn = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 10 + g); };
+    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 12);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     const AbortFlag abort_flag{sbase + L::kOffMisc + 4};
     const mmq_shared_prefix_attention_t& p = a.p;
@@ -118,7 +126,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+            mbar_init(empty(s), kTwo ? 2 : 1);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(q_full(g), 4);
@@ -126,8 +134,9 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             mbar_init(p_full(g, 0), 4);
             mbar_init(p_full(g, 1), 4);
             mbar_init(o_full(g), 1);
+            mbar_init(turn(g), 1);
         }
-        mbar_init(drain, 1);
+        mbar_init(drain, 2);
         abort_flag.set(0u);
         fence_barrier_init();
         prefetch_tmap(&maps.k);
@@ -152,7 +161,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     const int parts = a.prefix_parts / (kTwo ? 1 : 2);
     const int items = units * p.kv_heads * parts;
     struct Item {
-        int h, part, steps;   // steps: rounds of (S, P V), both groups' together
+        int h, part, tiles;   // tiles: of 128 keys
         int64_t r0, k0, k1;
     };
     auto get = [&](int i) {
@@ -163,8 +172,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         w.r0 = int64_t(u % units) * per_unit;
         w.k0 = w.part * a.part_keys;
         w.k1 = min(w.k0 + a.part_keys, p.prefix);
-        const int tiles = int((w.k1 - w.k0 + kKeys - 1) / kKeys);
-        w.steps = kTwo ? 2 * tiles : tiles;
+        w.tiles = int((w.k1 - w.k0 + kKeys - 1) / kKeys);
         return w;
     };
 
@@ -190,81 +198,96 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 };
                 for (int i = blockIdx.x; i < items; i += gridDim.x) {
                     const Item w = get(i);
-                    // in the order the MMA warp takes them
-                    auto key = [&](int v) { return w.k0 + int64_t(kTwo ? v >> 1 : v) * kKeys; };
-                    auto want = [&](int v) { return v < w.steps && (!kTwo || !(v & 1)); };
-                    if (want(0) && !load(&maps.k, w.h, key(0))) goto producer_done;
-                    if (want(1) && !load(&maps.k, w.h, key(1))) goto producer_done;
-                    for (int v = 0; v < w.steps; ++v) {
-                        if (want(v) && !load(&maps.v, w.h, key(v))) goto producer_done;
-                        if (want(v + 2) && !load(&maps.k, w.h, key(v + 2))) goto producer_done;
+                    const int tiles = w.tiles;
+                    auto key = [&](int t) { return w.k0 + int64_t(t) * kKeys; };
+                    if (kTwo) {   // K0 V0 K1 V1 ...
+                        for (int t = 0; t < tiles; ++t)
+                            if (!load(&maps.k, w.h, key(t)) || !load(&maps.v, w.h, key(t))) goto producer_done;
+                    } else {      // K0 K1 V0 V1 K2 K3 V2 V3 ..., an odd last tile alone
+                        for (int t = 0; t < tiles; t += 2) {
+                            const bool two = t + 1 < tiles;
+                            if (!load(&maps.k, w.h, key(t)) || (two && !load(&maps.k, w.h, key(t + 1))) ||
+                                !load(&maps.v, w.h, key(t)) || (two && !load(&maps.v, w.h, key(t + 1))))
+                                goto producer_done;
+                        }
                     }
                 }
             producer_done:
                 for (int s = 0; s < kSlots; ++s)
                     if (issued[s]) wait_drain(full(s), par[s], status);
             }
-        } else if (warp == kWarpMma) {
-            // -------------------------------------------------------- MMA issuer
+        } else if (warp < kWarpMma + 2) {
+            // ------------------------------------------------------- MMA issuers
             if (lane == 0) {
-                Ring<kSlots> r;
-                int k_slot = 0, v_slot = 0;
-                uint32_t q_phase = 0, p_phase[2] = {0, 0};
+                const int g = warp - kWarpMma;
+                uint32_t q_phase = 0, p_phase = 0, base = 0;   // base: ring position of the item's first tile
+                uint32_t t_phase = g == 0 ? 1u : 0u;           // group 0 has the first turn
                 constexpr uint32_t kIdQK = idesc_16<T>(kKeys, false), kIdPV = idesc_16<T>(D, true);
-                auto take = [&](int& slot) {
-                    if (!wait_bounded(full(r.slot), r.phase, abort_flag, status)) return false;
-                    tc_fence_after();
-                    slot = r.slot;
-                    r.next();
-                    return true;
-                };
-                auto qk = [&](int v) {
-                    const int g = v & 1;
-                    if (!kTwo || g == 0)
-                        if (!take(k_slot)) return false;
-                    const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
-                    const uint64_t dk = smem_desc_sw128(sbase + uint32_t(L::kOffRing + k_slot * L::kTile));
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = uint64_t(((kk >> 2) * L::kPanel + (kk & 3) * 32) >> 4);
-                        mma_f16(tmem + kColS + 128u * uint32_t(g), dq + off, dk + off, kIdQK, uint32_t(kk > 0));
-                    }
-                    mma_commit(s_full(g));
-                    if (!kTwo || g == 1) mma_commit(empty(k_slot));
-                    return true;
+                constexpr uint64_t kTileDesc = uint64_t(L::kTile >> 4), kPanelDesc = uint64_t(L::kPanel >> 4);
+                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
+                const uint64_t k_desc = smem_desc_sw128(sbase + uint32_t(L::kOffRing));
+                const uint64_t v_desc = smem_desc_mn_sw128(sbase + uint32_t(L::kOffRing), uint32_t(L::kPanel));
+                const uint32_t ts = tmem + kColS + 128u * uint32_t(g), to = tmem + kColO + 128u * uint32_t(g);
+                auto arrived = [&](uint32_t pos) {
+                    return wait_bounded(full(int(pos % kSlots)), (pos / kSlots) & 1u, abort_flag, status);
                 };
                 for (int i = blockIdx.x; i < items; i += gridDim.x) {
-                    const Item w = get(i);
-                    for (int g = 0; g < 2; ++g)
-                        if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
-                    q_phase ^= 1u;
-                    tc_fence_after();
-                    if (!qk(0)) goto mma_done;
-                    if (w.steps > 1 && !qk(1)) goto mma_done;
-                    for (int v = 0; v < w.steps; ++v) {
-                        const int g = v & 1;
-                        if ((!kTwo || g == 0) && !take(v_slot)) goto mma_done;
-                        const uint64_t dv =
-                            smem_desc_mn_sw128(sbase + uint32_t(L::kOffRing + v_slot * L::kTile), uint32_t(L::kPanel));
+                    const int tiles = get(i).tiles, mine = kTwo ? tiles : (tiles + 1 - g) >> 1;
+                    auto k_at = [&](int s) { return base + uint32_t(kTwo ? 2 * s : 4 * s + g); };
+                    auto v_at = [&](int s) {
+                        return base + uint32_t(kTwo ? 2 * s + 1 : 4 * s + (g == 1 ? 3 : 2 * s + 1 < tiles ? 2 : 1));
+                    };
+                    auto scores = [&](int s) {   // S = Q K^T; K has arrived
+                        const uint32_t slot = k_at(s) % kSlots;
+                        const uint64_t dk = k_desc + slot * kTileDesc;
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk) {   // 16 keys = 16 rows of 128 bytes
-                            if ((kk & 3) == 0) {
-                                if (!wait_bounded(p_full(g, kk >> 2), p_phase[g], abort_flag, status)) goto mma_done;
-                                tc_fence_after();
-                            }
-                            mma_f16_ta(tmem + kColO + 128u * uint32_t(g), tmem + kColS + 128u * uint32_t(g) + 8u * uint32_t(kk),
-                                       dv + uint64_t((kk * 2048) >> 4), kIdPV, uint32_t(v > 1 || kk > 0));
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = uint64_t(kk >> 2) * kPanelDesc + uint64_t((kk & 3) * 2);
+                            mma_f16(ts, dq + off, dk + off, kIdQK, uint32_t(kk > 0));
                         }
-                        p_phase[g] ^= 1u;
-                        if (!kTwo || g == 1) mma_commit(empty(v_slot));
-                        if (v + 2 < w.steps) {
-                            if (!qk(v + 2)) goto mma_done;
-                        } else {
-                            mma_commit(o_full(g));
-                        }
+                        mma_commit(s_full(g));
+                        mma_commit(empty(int(slot)));
+                    };
+                    if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
+                    q_phase ^= 1u;
+                    if (mine > 0) {
+                        if (!arrived(k_at(0))) goto mma_done;
+                        tc_fence_after();
+                        scores(0);
                     }
+                    const int rounds = kTwo ? tiles : (tiles + 1) >> 1;   // group 1 may have one tile less
+                    for (int s = 0; s < rounds; ++s) {
+                        if (s == mine) {
+                            if (!wait_bounded(turn(g), t_phase, abort_flag, status)) goto mma_done;
+                            t_phase ^= 1u;
+                            mbar_arrive(turn(g ^ 1));
+                            break;
+                        }
+                        // everything that can be waited for before the weights
+                        const bool more = s + 1 < mine;
+                        if (!arrived(v_at(s)) || (more && !arrived(k_at(s + 1)))) goto mma_done;
+                        const uint32_t slot = v_at(s) % kSlots;
+                        const uint64_t dv = v_desc + slot * kTileDesc;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (!wait_bounded(p_full(g, half), p_phase, abort_flag, status)) goto mma_done;
+                            if (half == 0 && !wait_bounded(turn(g), t_phase, abort_flag, status)) goto mma_done;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)   // 16 keys = 16 rows of 128 bytes
+                                mma_f16_ta(to, ts + 8u * uint32_t(kk), dv + uint64_t(kk * 128), kIdPV,
+                                           uint32_t(s > 0 || kk > 0));
+                        }
+                        p_phase ^= 1u;
+                        t_phase ^= 1u;
+                        if (more) scores(s + 1);
+                        mbar_arrive(turn(g ^ 1));
+                        mma_commit(empty(int(slot)));
+                        if (!more) mma_commit(o_full(g));
+                    }
+                    base += uint32_t(2 * tiles);
                 }
-            mma_done:
+        mma_done:
                 mma_commit(drain);   // everything issued, also after a wait that ran out
                 wait_drain(drain, 0u, status);
             }
@@ -297,7 +320,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full(g));
             }
-            const int mine = kTwo ? w.steps >> 1 : (w.steps + 1 - g) >> 1;
+            const int mine = kTwo ? w.tiles : (w.tiles + 1 - g) >> 1;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int n = 0; n < mine && ok; ++n) {
