@@ -91,9 +91,18 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
     extern __shared__ __align__(128) uint8_t smem[];
     const mmq_shared_prefix_attention_t& p = a.p;
     T* const tag = nullptr;
-    // No early trigger for the next kernel: its CTAs, one per SM, would take the
-    // room of the last third of these (170 against 150 us at 256 sequences).
-    griddep_wait();
+    if (kKeys == Keys::kPrefix) {
+        griddep_wait();
+        griddep_launch_dependents();
+    } else if (!a.beside) {
+        griddep_wait();
+    }
+    // Beside a prefix kernel, which was launched (and has seen to it that what
+    // precedes the call is complete) but need not have ended: only the last CTA
+    // waits for it, at its end, so that this grid's end is also the prefix
+    // kernel's for the join.  A wait in every CTA would hold their SMs' room.
+    const bool last = kKeys != Keys::kPrefix && a.beside && blockIdx.x == gridDim.x - 1 &&
+                      blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
     const int lane = threadIdx.x;
     const int h = blockIdx.y, G = a.group;
     const int tiles_per_token = (G + 15) / 16;
@@ -134,6 +143,7 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
 
     if (k0 >= k1) {
         if (lane < 16 && r0 + lane < r1) a.part_ml[part_row * p.heads + token_head(r0 + lane)] = make_float2(-INFINITY, 0.f);
+        if (last) griddep_wait();
         return;
     }
 
@@ -296,11 +306,13 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
             *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
         if (gcol == 0) a.part_ml[at] = half ? make_float2(m1, l1) : make_float2(m0, l0);
     }
+    if (last) griddep_wait();
 }
 
 // ------------------------------------------------------------------- join
-// One warp per (token, head): the parts' (m, l) give each part's factor, then
-// one pass over their sums; parts without keys are not read.
+// One warp per (token, head).  The parts' (m, l), one part per lane, give the
+// maximum and each part's factor; then the parts' sums, all loads in flight
+// together; parts without keys are not read.
 __device__ __forceinline__ void store_out(void* out, int type, int64_t at, float x, float y) {
     if (type == MMQ_TYPE_F32)
         *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = make_float2(x, y);
@@ -324,27 +336,38 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[i * rows + row].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f;
-    float2 acc[D / 64];
+    constexpr int kVec = D / 32;   // values per lane
+    float l = 0.f, acc[kVec] = {};
+    for (int first = 0; first < parts; first += 32) {
+        const int n = min(32, parts - first);
+        const float2 ml = lane < n ? a.part_ml[(first + lane) * rows + row] : make_float2(0.f, 0.f);
+        const float mine = ml.y == 0.f ? 0.f : ex2(ml.x - m);   // l = 0: no keys
+        l = fmaf(mine, ml.y, l);
+        const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float* src = a.part_o + ((first + i) * rows + row) * D + kVec * lane;
+            const float f = __shfl_sync(0xffffffffu, mine, i);
+            float v[kVec] = {};
+            if ((has >> i) & 1u) {
+                if (kVec == 4) {
+                    const float4 u = *reinterpret_cast<const float4*>(src);
+                    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[kVec - 1] = u.w;
+                } else {
+                    const float2 u = *reinterpret_cast<const float2*>(src);
+                    v[0] = u.x; v[kVec - 1] = u.y;
+                }
+            }
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) acc[c] = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const float2 ml = a.part_ml[i * rows + row];
-        if (ml.y == 0.f) continue;
-        const float f = exp2f(ml.x - m);
-        l = fmaf(f, ml.y, l);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const float2 v = *reinterpret_cast<const float2*>(a.part_o + (i * rows + row) * D + c * 64 + 2 * lane);
-            acc[c].x = fmaf(f, v.x, acc[c].x);
-            acc[c].y = fmaf(f, v.y, acc[c].y);
+            for (int k = 0; k < kVec; ++k) acc[k] = fmaf(f, v[k], acc[k]);
         }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float r = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-        store_out(a.p.out, a.p.out_type, row * D + c * 64 + 2 * lane, acc[c].x * r, acc[c].y * r);
+    for (int k = 0; k < kVec; k += 2)
+        store_out(a.p.out, a.p.out_type, row * D + kVec * lane + k, acc[k] * r, acc[k + 1] * r);
 }
 
 // A kernel of this call that follows another: it may be scheduled before the
@@ -384,15 +407,22 @@ int split(int64_t units, int64_t keys, int64_t slots, int64_t least) {
 }
 
 // Parts of the prefix for the tensor-core kernel: `units` row blocks over
-// `tiles` key tiles each, one CTA per SM.  A CTA's item costs its key tiles
-// and about three more for its queries, first scores and results; a part more
-// costs the join a little.
-int64_t tc_parts(int64_t units, int64_t tiles, int64_t nsm) {
+// `tiles` key tiles each, one CTA per SM.  Estimated in key tiles (about 1.7 us
+// each with two row tiles): a CTA's item costs its tiles and about four more
+// for its queries, first scores and results, a part costs the join a little,
+// and the suffix kernel, which follows but starts on the SMs that have no
+// item, reads about 140 KB per tile's time and SM there and 60 KB per SM with
+// all of them.
+int64_t tc_parts(int64_t units, int64_t tiles, int64_t nsm, double suffix_bytes) {
     int64_t best = 1;
     double least = 1e300;
     for (int64_t n = 1; n <= tiles && n <= 64; ++n) {
         const int64_t rounds = (units * n + nsm - 1) / nsm, each = (tiles + n - 1) / n;
-        const double cost = double(rounds * (each + 3)) + 0.25 * double(n);
+        const double prefix = double(rounds * (each + 4));
+        const double idle = rounds == 1 ? double(nsm - units * n) : 0.;
+        double left = suffix_bytes - idle * prefix * 140e3;
+        if (left < 0.) left = 0.;
+        const double cost = prefix + left / (double(nsm) * 60e3) + 0.25 * double(n);
         if (cost < least) {
             least = cost;
             best = n;
@@ -406,6 +436,7 @@ void plan(AttnArgs& a, int nsm) {
     a.tokens = int64_t(p.batch) * p.q_len;
     a.group = p.heads / p.kv_heads;
     a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.beside = p.prefix > 0;
     a.page_shift = 0;
     while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
     const int64_t rows = a.tokens * a.group;
@@ -418,7 +449,9 @@ void plan(AttnArgs& a, int nsm) {
         int64_t n;
         if (a.prefix_tiles) {
             const int64_t units = (rows + 128 * a.prefix_tiles - 1) / (128 * a.prefix_tiles) * p.kv_heads;
-            n = tc_parts(units, (p.prefix + tile - 1) / tile, nsm);
+            // on average a suffix fills half of its pages
+            const double suffix = 2. * double(a.tokens) * double(p.table_width << a.page_shift) * p.kv_heads * p.head_dim;
+            n = tc_parts(units, (p.prefix + tile - 1) / tile, nsm, suffix);
         } else {
             n = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 64);
         }
@@ -445,12 +478,6 @@ cudaError_t launch(const AttnArgs& a, int nsm, cudaStream_t s) {
         return f ? mmq::launch_config(grid, block, smem, s, attr) : follow_config(grid, block, smem, s, attr);
     };
     constexpr int smem = row_smem<D>();
-    if (a.suffix_parts) {
-        auto* kernel = a.p.page_size >= kSlab ? attn_rows_kernel<T, D, Keys::kPages> : attn_rows_kernel<T, D, Keys::kSmallPages>;
-        const dim3 grid(unsigned(a.tokens * ((a.group + 15) / 16)), unsigned(a.p.kv_heads), unsigned(a.suffix_parts));
-        const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
-        if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
-    }
     if (a.prefix_parts && a.prefix_tiles) {
         const cudaLaunchConfig_t cfg = config(dim3(1), dim3(1), 0);
         if ((e = mmq::launch_attention_prefix(a, nsm, cfg))) return e;
@@ -458,6 +485,12 @@ cudaError_t launch(const AttnArgs& a, int nsm, cudaStream_t s) {
         const dim3 grid(unsigned((a.tokens * a.group + 15) / 16), unsigned(a.p.kv_heads), unsigned(a.prefix_parts));
         const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
         if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, Keys::kPrefix>, a))) return e;
+    }
+    if (a.suffix_parts) {
+        auto* kernel = a.p.page_size >= kSlab ? attn_rows_kernel<T, D, Keys::kPages> : attn_rows_kernel<T, D, Keys::kSmallPages>;
+        const dim3 grid(unsigned(a.tokens * ((a.group + 15) / 16)), unsigned(a.p.kv_heads), unsigned(a.suffix_parts));
+        const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
+        if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
     }
     const cudaLaunchConfig_t cfg = config(dim3(unsigned((a.tokens * a.p.heads + 7) / 8)), dim3(256), 0);
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, a);

@@ -151,8 +151,10 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_launch_dependents();
+    // The suffix kernel may run beside this one (on the SMs this grid leaves
+    // free); what it reads is complete once this wait is over.
     griddep_wait();
+    griddep_launch_dependents();
 
     // Items: (row block, kv head, part), parts of one head's keys next to each other.
     const int64_t rows = a.tokens * a.group;
@@ -237,12 +239,13 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     auto v_at = [&](int s) {
                         return base + uint32_t(kTwo ? 2 * s + 1 : 4 * s + (g == 1 ? 3 : 2 * s + 1 < tiles ? 2 : 1));
                     };
-                    auto scores = [&](int s) {   // S = Q K^T; K has arrived
+                    auto scores = [&](int s, bool pass) {   // S = Q K^T; K has arrived
                         const uint32_t slot = k_at(s) % kSlots;
                         const uint64_t dk = k_desc + slot * kTileDesc;
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t off = uint64_t(kk >> 2) * kPanelDesc + uint64_t((kk & 3) * 2);
+                            if (kk == D / 16 - 2 && pass) mbar_arrive(turn(g ^ 1));   // the other thread needs a moment to start
                             mma_f16(ts, dq + off, dk + off, kIdQK, uint32_t(kk > 0));
                         }
                         mma_commit(s_full(g));
@@ -253,7 +256,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     if (mine > 0) {
                         if (!arrived(k_at(0))) goto mma_done;
                         tc_fence_after();
-                        scores(0);
+                        scores(0, false);
                     }
                     const int rounds = kTwo ? tiles : (tiles + 1) >> 1;   // group 1 may have one tile less
                     for (int s = 0; s < rounds; ++s) {
@@ -280,8 +283,8 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         }
                         p_phase ^= 1u;
                         t_phase ^= 1u;
-                        if (more) scores(s + 1);
-                        mbar_arrive(turn(g ^ 1));
+                        if (more) scores(s + 1, true);
+                        else mbar_arrive(turn(g ^ 1));
                         mma_commit(empty(int(slot)));
                         if (!more) mma_commit(o_full(g));
                     }
