@@ -64,9 +64,8 @@ struct Layout {
     static constexpr int kOffQ = 0;                          // two row tiles
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kSlots * kTile;
-    // barriers: full, empty per slot; q_full, s_full, o_full per group, p_full per group and half; turn
-    // per group; drain
-    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 13) * 8;
+    // barriers: full, empty per slot; q_full, s_full, o_full, p_full, turn per group; drain
+    static constexpr int kOffMisc = kOffBar + (2 * kSlots + 11) * 8;
     static constexpr int kBytes = kOffMisc + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448, "shared memory budget");
@@ -114,9 +113,9 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     auto q_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + g); };
     auto s_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 2 + g); };
     auto o_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 4 + g); };
-    auto p_full = [&](int g, int half) { return bar0 + 8u * uint32_t(2 * kSlots + 6 + 2 * g + half); };
-    auto turn = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 10 + g); };
-    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 12);
+    auto p_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 6 + g); };
+    auto turn = [&](int g) { return bar0 + 8u * uint32_t(2 * kSlots + 8 + g); };
+    const uint32_t drain = bar0 + 8u * uint32_t(2 * kSlots + 10);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     const AbortFlag abort_flag{sbase + L::kOffMisc + 4};
     const mmq_shared_prefix_attention_t& p = a.p;
@@ -131,8 +130,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         for (int g = 0; g < 2; ++g) {
             mbar_init(q_full(g), 4);
             mbar_init(s_full(g), 1);
-            mbar_init(p_full(g, 0), 4);
-            mbar_init(p_full(g, 1), 4);
+            mbar_init(p_full(g), 4);
             mbar_init(o_full(g), 1);
             mbar_init(turn(g), 1);
         }
@@ -239,8 +237,8 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     auto v_at = [&](int s) {
                         return base + uint32_t(kTwo ? 2 * s + 1 : 4 * s + (g == 1 ? 3 : 2 * s + 1 < tiles ? 2 : 1));
                     };
-                    auto scores = [&](int s, bool pass) {   // S = Q K^T; K has arrived
-                        const uint32_t slot = k_at(s) % kSlots;
+                    // S = Q K^T with K in `slot`, which has arrived
+                    auto scores = [&](uint32_t slot, bool pass) {
                         const uint64_t dk = k_desc + slot * kTileDesc;
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
@@ -256,37 +254,35 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     if (mine > 0) {
                         if (!arrived(k_at(0))) goto mma_done;
                         tc_fence_after();
-                        scores(0, false);
+                        scores(k_at(0) % kSlots, false);
                     }
                     const int rounds = kTwo ? tiles : (tiles + 1) >> 1;   // group 1 may have one tile less
                     for (int s = 0; s < rounds; ++s) {
-                        if (s == mine) {
-                            if (!wait_bounded(turn(g), t_phase, abort_flag, status)) goto mma_done;
-                            t_phase ^= 1u;
+                        const bool has = s < mine, more = s + 1 < mine;
+                        // everything that can be waited for before the turn
+                        if (has && (!arrived(v_at(s)) || (more && !arrived(k_at(s + 1))) ||
+                                    !wait_bounded(p_full(g), p_phase, abort_flag, status)))
+                            goto mma_done;
+                        const uint32_t v_slot = v_at(s) % kSlots, k_slot = k_at(s + 1) % kSlots;
+                        const uint64_t dv = v_desc + v_slot * kTileDesc;
+                        if (!wait_bounded(turn(g), t_phase, abort_flag, status)) goto mma_done;
+                        tc_fence_after();
+                        t_phase ^= 1u;
+                        if (!has) {
                             mbar_arrive(turn(g ^ 1));
                             break;
                         }
-                        // everything that can be waited for before the weights
-                        const bool more = s + 1 < mine;
-                        if (!arrived(v_at(s)) || (more && !arrived(k_at(s + 1)))) goto mma_done;
-                        const uint32_t slot = v_at(s) % kSlots;
-                        const uint64_t dv = v_desc + slot * kTileDesc;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (!wait_bounded(p_full(g, half), p_phase, abort_flag, status)) goto mma_done;
-                            if (half == 0 && !wait_bounded(turn(g), t_phase, abort_flag, status)) goto mma_done;
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)   // 16 keys = 16 rows of 128 bytes
-                                mma_f16_ta(to, ts + 8u * uint32_t(kk), dv + uint64_t(kk * 128), kIdPV,
-                                           uint32_t(s > 0 || kk > 0));
-                        }
                         p_phase ^= 1u;
-                        t_phase ^= 1u;
-                        if (more) scores(s + 1, true);
-                        else mbar_arrive(turn(g ^ 1));
-                        mma_commit(empty(int(slot)));
-                        if (!more) mma_commit(o_full(g));
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)   // 16 keys = 16 rows of 128 bytes
+                            mma_f16_ta(to, ts + 8u * uint32_t(kk), dv + uint64_t(kk * 128), kIdPV, uint32_t(s > 0 || kk > 0));
+                        if (more) {
+                            scores(k_slot, true);
+                        } else {
+                            mbar_arrive(turn(g ^ 1));
+                            mma_commit(o_full(g));
+                        }
+                        mma_commit(empty(int(v_slot)));
                     }
                     base += uint32_t(2 * tiles);
                 }
@@ -387,11 +383,11 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         pk[k] = pack16(u, v, tag);
                     }
                     tmem_st_32x32b_x32(ts + 32u * uint32_t(half), pk);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full(g, half));
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(g));
                 sum[0] = fadd2(sum[0], sum[1]);
                 l += lo_f(sum[0]) + hi_f(sum[0]);
             }
