@@ -30,14 +30,35 @@ using namespace mmq::tc;
 constexpr int kMaxTokens = MMQ_MOE_MAX_TOKENS;
 constexpr int kMaxExperts = MMQ_MOE_MAX_EXPERTS;
 constexpr int kMaxPairs = MMQ_MOE_MAX_PAIRS;
-constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kBlk = 144;     // bytes of a q4_K super-block
-// A weight tile is 32 rows x one super-block, one TMA box, two per warp in
-// flight: 32 boxes per SM.  Streaming 604 MB through such rings with no other
-// work takes 92 us (6.5 TB/s) with 32 boxes of 16 or of 32 rows in flight per
-// SM, but 127 us with 48 and 154 us with 64.
+constexpr int kSliceSb = 16;  // super-blocks of a row (or of a slice of it) that a CTA's warps hold together
+// A weight tile is 32 rows x a warp's super-blocks, one TMA box each, two
+// tiles per warp in flight: 32 boxes per SM.  Streaming 604 MB through such
+// rings with no other work takes 92 us (6.5 TB/s) with 32 boxes of 16 or of 32
+// rows in flight per SM, but 127 us with 48 and 154 us with 64.
 constexpr int kRows = 32, kStages = 2;
-constexpr int kTile = kRows * kBlk;
+constexpr int kBox = kRows * kBlk;
+constexpr int kRedPitch = kRows + 8;   // floats per token: the four lanes of a row on four banks
+constexpr int kLag = 3;                // batches between a warp's own tile of a batch and its adding the batch up
+
+// NG: groups of four tokens per pass.  One group: 16 warps with one
+// super-block each (more warps hide more).  Two: 8 warps with two super-blocks
+// each, since the activations of two groups and the rest of the state do not
+// fit 128 registers (655 -> 341 us for 32 tokens on 8 wide experts).
+template <int NG>
+struct Cfg {
+    static constexpr int kSub = NG;                                 // super-blocks per warp
+    static constexpr int kWarps = kSliceSb / kSub;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kTok = 4 * NG;
+    static constexpr int kTile = kSub * kBox;
+    static constexpr int kBuffers = 6;                              // batches of partial sums between the warps
+    static constexpr int kPart = kTok * kRedPitch;                  // floats of one warp's tile
+    static constexpr int kRed = kWarps * kPart * 4;                 // bytes of one buffer
+    static constexpr int kRing = kWarps * kStages * kTile;
+    static constexpr int kBytes = kRing + kBuffers * kRed + 128;    // + alignment
+};
+static_assert(Cfg<1>::kBytes <= 208 * 1024 && Cfg<2>::kBytes <= 208 * 1024, "shared memory budget");
 
 // Which tokens go to which expert: pair i = token i / top_k, its i % top_k-th
 // expert.  An active expert (one with a token) has its pairs in a row of
@@ -52,10 +73,11 @@ struct Plan {
 
 struct MoeArgs {
     mmq_q4K_moe_t p;
-    float* logits;   // [tokens][experts]
-    float* h;        // first product, rows in the plan's order: h [pairs][ffn], or if its sum is in
-                     // parts [gu_slices][pairs][2 ffn] of gate and up, alternating
-    float* y;        // second product [down_slices][pairs][model], rows by pair
+    float* logits;       // [tokens][experts]
+    float* h;            // first product, rows in the plan's order: h [pairs][ffn], or if its sum is in
+                         // parts [gu_slices][pairs][2 ffn] of gate and up, alternating
+    float* y;            // second product [down_slices][pairs][model], rows by pair
+    unsigned* arrived;   // [2] CTAs at the layer kernel's two barriers; zeroed by the router kernel
     int gu_slices, down_slices;
     int* status;
 };
@@ -65,9 +87,9 @@ struct MoeArgs {
 // so that a thread's loads are all in flight at once.
 constexpr int kRouterThreads = 256;
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
-    griddep_launch_dependents();
     griddep_wait();
     const mmq_q4K_moe_t& p = a.p;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.arrived[threadIdx.x] = 0u;
     __shared__ float part[kRouterThreads / 32][4];
     const int e = blockIdx.x, t0 = blockIdx.y * 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float4* w = reinterpret_cast<const float4*>(p.w_router + int64_t(e) * p.model);
@@ -169,17 +191,18 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* i
 struct PlanScratch {
     uint64_t tokens_of[kMaxExperts];   // one bit per token of an expert
     int ids[kMaxPairs];
-    int totals[3][kWarps];
+    int totals[3][kMaxExperts / 32];
 };
 
 // Fill `plan` (shared memory) from the logits, for passes of `pass_tokens`;
 // `store`: also the chosen experts and their weights to the caller.
-__device__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, int pass_tokens, bool store) {
+template <int kThreads>
+__device__ __forceinline__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, int pass_tokens, bool store) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
     static_assert(kMaxExperts <= kThreads && kMaxTokens <= 64, "one thread per expert, one bit per token");
     if (e < kMaxExperts) z->tokens_of[e] = 0;
     __syncthreads();
-    for (int t = warp; t < a.p.tokens; t += kWarps) choose(a, t, lane, z->ids, z->tokens_of, store);
+    for (int t = warp; t < a.p.tokens; t += kThreads / 32) choose(a, t, lane, z->ids, z->tokens_of, store);
     __syncthreads();
     uint64_t mine = e < kMaxExperts ? z->tokens_of[e] : 0;
     const int n = __popcll(mine), passes = (n + pass_tokens - 1) / pass_tokens;
@@ -194,33 +217,36 @@ __device__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, int pass
         }
     }
     const uint32_t live = __ballot_sync(0xffffffffu, n > 0);
-    if (lane == 31) {
+    if (lane == 31 && e < kMaxExperts) {
         z->totals[0][warp] = pairs;
         z->totals[1][warp] = pass;
         z->totals[2][warp] = __popc(live);
     }
     __syncthreads();
-    int at = pairs - n, first = pass - passes, rank = __popc(live & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) {
-        at += z->totals[0][w];
-        first += z->totals[1][w];
-        rank += z->totals[2][w];
-    }
-    if (n > 0) {
-        plan->expert[rank] = e;
-        plan->start[rank] = at;
-        plan->pass[rank] = first;
-        for (; mine; mine &= mine - 1) {
-            const int t = __ffsll(static_cast<long long>(mine)) - 1;
-            int j = 0;
-            while (z->ids[t * a.p.top_k + j] != e) ++j;
-            plan->order[at++] = t * a.p.top_k + j;
+    if (e < kMaxExperts) {
+        int at = pairs - n, first = pass - passes, rank = __popc(live & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) {
+            at += z->totals[0][w];
+            first += z->totals[1][w];
+            rank += z->totals[2][w];
         }
-    }
-    if (e == kThreads - 1) {
-        plan->active = rank;
-        plan->start[rank] = at;
-        plan->pass[rank] = first;
+        if (n > 0) {
+            plan->expert[rank] = e;
+            plan->start[rank] = at;
+            plan->pass[rank] = first;
+            for (; mine; mine &= mine - 1) {
+                const int t = __ffsll(static_cast<long long>(mine)) - 1;
+                int j = 0;
+                while (z->ids[t * a.p.top_k + j] != e) ++j;
+                plan->order[at++] = t * a.p.top_k + j;
+            }
+        }
+        if (e == kMaxExperts - 1) {
+            rank += n > 0;
+            plan->active = rank;
+            plan->start[rank] = at;
+            plan->pass[rank] = first + passes;
+        }
     }
     __syncthreads();
 }
@@ -237,10 +263,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with nothing to add to.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(b0));
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
@@ -335,17 +368,6 @@ __device__ __forceinline__ void make_act(Act& act, int lane, Load load) {
     act.up = __shfl_sync(0xffffffffu, __uint_as_float(uint32_t(127 + e) << 23), 8 * (lane & 3));
 }
 
-constexpr int kRedPitch = kRows + 8;   // floats per token: the four lanes of a row on four banks
-template <int NG>
-struct Smem {
-    static constexpr int kBuffers = 5 - NG;                         // batches of partial sums between the warps
-    static constexpr int kPart = 4 * NG * kRedPitch;                // floats of one warp's tile
-    static constexpr int kRed = kWarps * kPart * 4;                 // bytes of one buffer
-    static constexpr int kRing = kWarps * kStages * kTile;
-    static constexpr int kBytes = kRing + kBuffers * kRed + 128;    // + alignment
-};
-static_assert(Smem<2>::kBytes <= 208 * 1024, "shared memory budget");
-
 // A run of row tiles of one (active expert, slice, pass).
 struct Run {
     int a, slice, pass, first, count, left;   // left: tiles the CTA still has, this run's among them
@@ -363,327 +385,452 @@ struct Run {
     }
 };
 
-// Both products of the experts.  Activations are stationary: a warp keeps the
-// operand of one super-block for 4 NG tokens in registers and streams weight
-// tiles of that super-block through a ring of its own; the warps of a team hold the super-blocks of a row (or of a slice of
-// at most 16 of it), so a team reads whole rows.  The partial sums of a batch
-// (one tile per team) meet in shared memory: the warps take turns to add a
-// batch up, in a fixed order, and store it, and none of the others waits for
-// that unless it is a few batches ahead.  One CTA per SM; the row tiles of
-// all passes of all active experts are dealt out in equal consecutive parts.
-template <int NG, bool kDown>
-__global__ void __launch_bounds__(kThreads, 1)
-moe_expert_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    __shared__ Plan plan;
-    __shared__ PlanScratch scratch;
-    constexpr int kBuffers = Smem<NG>::kBuffers;
-    __shared__ uint64_t bars[kWarps * kStages + 2 * kBuffers];
-    __shared__ uint32_t abort_word;
-    __shared__ int start_at;
-    const mmq_q4K_moe_t& p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const AbortFlag abort_flag{smem_u32(&abort_word)};
-    const uint32_t bar0 = smem_u32(&bars[warp * kStages]), red_full = smem_u32(&bars[kWarps * kStages]);
-    const uint32_t red_empty = red_full + 8 * kBuffers;
-    constexpr int kTok = 4 * NG;
-    if (threadIdx.x == 0) {
-        abort_flag.set(0u);
-        for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(red_full + 8u * uint32_t(i), kWarps);
-            mbar_init(red_empty + 8u * uint32_t(i), 1);
-        }
-        prefetch_tmap(&map);
-    }
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(bar0 + 8u * uint32_t(i), 1);
-        fence_barrier_init();
-    }
-    // The logits are complete before the second product starts: the first one
-    // lets it be scheduled only after its own wait for the router.
-    if (!kDown) griddep_wait();
-    griddep_launch_dependents();
-    make_plan(a, &plan, &scratch, kTok, !kDown && blockIdx.x == 0);
-
-    const int rows = kDown ? p.model : 2 * p.ffn, nsb = (kDown ? p.ffn : p.model) / 256;
-    const int slices = kDown ? a.down_slices : a.gu_slices;
-    const int per = (nsb + slices - 1) / slices, teams = kWarps / per;
-    const int team = warp / per, ks = warp - team * per;
-    const int tiles = rows / kRows, each = slices * tiles;   // tiles of a pass
-    const uint32_t total = uint32_t(plan.pass[plan.active] * each);
-    const int i0 = int(uint64_t(total) * blockIdx.x / gridDim.x), i1 = int(uint64_t(total) * (blockIdx.x + 1) / gridDim.x);
-    if (i0 >= i1) return;
-    if (int(threadIdx.x) < plan.active) {
-        const int p0 = i0 / each;
-        if (plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1]) start_at = threadIdx.x;
-    }
-    __syncthreads();
+// A CTA's share of one product, and where its warps are in it.
+template <int NG>
+struct Product {
+    using C = Cfg<NG>;
+    const CUtensorMap* map;
+    int rows, nsb, slices, per, crew, teams, tiles;   // per: super-blocks of a slice; crew: warps of a team
+    int team, ks;                                      // this warp's team and first super-block
     Run run;
-    {
-        run.a = start_at;
-        const int local = i0 - plan.pass[run.a] * each, passes = plan.pass[run.a + 1] - plan.pass[run.a];
-        const int sp = local / tiles;
+    Run in;        // the run that lane 0 has issued up to, and its next tile
+    int in_tile;
+
+    __device__ __forceinline__ Product(const CUtensorMap* m, int rows_, int inner, int slices_, const Plan& plan, int* start_at)
+        : map(m), rows(rows_), nsb(inner / 256), slices(slices_) {
+        const int warp = threadIdx.x >> 5;
+        per = (nsb + slices - 1) / slices;
+        crew = (per + C::kSub - 1) / C::kSub;
+        teams = C::kWarps / crew;
+        team = warp / crew;
+        ks = (warp - team * crew) * C::kSub;
+        tiles = rows / kRows;
+        // equal consecutive parts of all passes' tiles
+        const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
+        const uint32_t i0 = uint32_t(uint64_t(total) * blockIdx.x / gridDim.x);
+        const uint32_t i1 = uint32_t(uint64_t(total) * (blockIdx.x + 1) / gridDim.x);
+        const int p0 = int(i0 / each);
+        __syncthreads();   // start_at may still be read for the product before
+        if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
+            *start_at = threadIdx.x;
+        __syncthreads();
+        run.left = int(i1 - i0);
+        run.a = run.left > 0 ? *start_at : 0;
+        const int passes = plan.pass[run.a + 1] - plan.pass[run.a];
+        const int local = run.left > 0 ? int(i0) - plan.pass[run.a] * int(each) : 0, sp = local / tiles;
         run.first = local - sp * tiles;
         run.slice = sp / passes;
         run.pass = sp - run.slice * passes;
-        run.left = i1 - i0;
         run.count = min(tiles - run.first, run.left);
+        in = run;
+        in_tile = team;
+        if (team >= teams) in.left = 0;
+        settle(plan);
     }
-
-    // The warp's weight stream: tiles team, team + teams, ... of each run.
-    Run in = run;
-    int in_tile = team, in_stage = 0, out_stage = 0, pending = 0;
-    uint32_t out_phase = 0;
-    const uint32_t ring = smem_u32(smem) + uint32_t(warp * kStages * kTile);
-    auto settle = [&]() {   // to a run with a tile for this warp
+    // To a run with a tile for this warp.
+    __device__ __forceinline__ void settle(const Plan& plan) {
         while (in.left > 0 && (in_tile >= in.count || in.slice * per + ks >= nsb)) {
             in.next(plan, slices, tiles);
             in_tile = team;
         }
-    };
-    auto issue = [&]() {
-        if (in.left <= 0 || abort_flag.raised()) return;
-        const uint32_t bar = bar0 + 8u * uint32_t(in_stage);
-        mbar_arrive_expect_tx(bar, kTile);
-        tma_load_2d(ring + uint32_t(in_stage * kTile), &map, bar, (in.slice * per + ks) * kBlk,
-                    plan.expert[in.a] * rows + (in.first + in_tile) * kRows);
+    }
+};
+
+template <int NG>
+struct Layer {
+    using C = Cfg<NG>;
+    const MoeArgs& a;
+    const Plan& plan;
+    AbortFlag abort_flag;
+    uint32_t bar0, red_full, red_empty, ring;
+    float* red0;
+    uint32_t magic;                        // fp16 1024 twice, in a register: one constant per instruction
+    int in_stage = 0, out_stage = 0, pending = 0, buffer = 0, turn = 0;
+    uint32_t out_phase = 0, red_phase = 0;
+    Act act[C::kSub][NG];
+
+    // Lane 0: the warp's next weight tile.
+    __device__ __forceinline__ void issue(Product<NG>& w) {
+        if (w.in.left <= 0 || abort_flag.raised()) return;
+        const uint32_t bar = bar0 + 8u * uint32_t(in_stage), dst = ring + uint32_t(in_stage * C::kTile);
+        const int sb = w.in.slice * w.per + w.ks, y = plan.expert[w.in.a] * w.rows + (w.in.first + w.in_tile) * kRows;
+        const bool two = C::kSub == 2 && w.ks + 1 < w.per && sb + 1 < w.nsb;
+        mbar_arrive_expect_tx(bar, two ? 2 * kBox : kBox);
+        tma_load_2d(dst, w.map, bar, sb * kBlk, y);
+        if (two) tma_load_2d(dst + kBox, w.map, bar, (sb + 1) * kBlk, y);
         ++pending;
         if (++in_stage == kStages) in_stage = 0;
-        in_tile += teams;
-        settle();
-    };
-    if (team >= teams) in.left = 0;
-    settle();
-    if (lane == 0)
-        for (int i = 0; i < kStages; ++i) issue();
-    if (kDown) griddep_wait();   // the first product
+        w.in_tile += w.teams;
+        w.settle(plan);
+    }
+    __device__ __forceinline__ void start(Product<NG>& w) {
+        if ((threadIdx.x & 31) == 0)
+            for (int i = 0; i < kStages; ++i) issue(w);
+    }
 
-    float* const red0 = reinterpret_cast<float*>(smem + Smem<NG>::kRing);
-    int buffer = 0, turn = 0;
-    uint32_t red_phase = 0, magic;   // fp16 1024 twice, kept in a register: one constant per instruction
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    for (; run.left > 0; run.next(plan, slices, tiles)) {
-        const int first = plan.start[run.a] + run.pass * kTok;
-        const int ntok = min(kTok, plan.start[run.a + 1] - first);
-        const int sb = run.slice * per + ks, held = min(per, nsb - run.slice * per);   // super-blocks of this slice
-        const bool works = team < teams && sb < nsb;
-        Act act[NG];
+    // This warp's operand: tokens first .. first + ntok - 1 of the plan's
+    // order; `all`: the tokens themselves.
+    template <bool kDown>
+    __device__ __forceinline__ void fill(const Product<NG>& w, int slice, int first, int ntok, bool all) {
+        const mmq_q4K_moe_t& p = a.p;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            const int tok = 4 * j + (g >> 1), pos = first + tok;
-            const bool have = works && tok < ntok;
-            const int64_t col = int64_t(sb) * 256 + 64 * t;
-            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!kDown) {
-                const float* x = p.x + (have ? int64_t(plan.order[pos] / p.top_k) * p.model + col : 0);
-                make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
-            } else if (a.gu_slices == 1) {
-                const float* x = a.h + (have ? int64_t(pos) * p.ffn + col : 0);
-                make_act(act[j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
-            } else {
-                const int64_t pairs = int64_t(p.tokens) * p.top_k;
-                make_act(act[j], lane, [&](int i) {
-                    float4 u = zero, v = zero;
-                    if (have) {
-                        for (int s = 0; s < a.gu_slices; ++s) {
-                            const float4* x =
-                                reinterpret_cast<const float4*>(a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
-                            const float4 c = x[0], d = x[1];
-                            u.x += c.x; u.y += c.y; u.z += c.z; u.w += c.w;
-                            v.x += d.x; v.y += d.y; v.z += d.z; v.w += d.w;
-                        }
-                    }
-                    return make_float4(silu_times(u.x, u.y), silu_times(u.z, u.w), silu_times(v.x, v.y),
-                                       silu_times(v.z, v.w));
-                });
-            }
-        }
-        for (int j0 = 0; j0 < run.count; j0 += teams) {
-            float* const red = red0 + buffer * (Smem<NG>::kRed / 4);
-            // The buffer's last batch has been added up (at first: passes at once).
-            if (!__all_sync(0xffffffffu, wait_bounded(red_empty + 8u * uint32_t(buffer), red_phase ^ 1u, abort_flag, a.status)))
-                break;
-            if (works && j0 + team < run.count) {
-                if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag, a.status)))
-                    break;
-                const uint32_t st = ring + uint32_t(out_stage * kTile);
-#pragma unroll 1
-                for (int m = 0; m < kRows; m += 16) {
-                    const uint32_t ra = st + uint32_t((m + g) * kBlk), rb = ra + 8 * kBlk;
-                    const RowScale r0 = row_scale(lds128(ra), t), r1 = row_scale(lds128(rb), t);
-                    float lo[NG][4], hi[NG][4];
+        for (int u = 0; u < C::kSub; ++u) {
+            const int sb = slice * w.per + w.ks + u;
+            const bool works = w.team < w.teams && w.ks + u < w.per && sb < w.nsb;
 #pragma unroll
-                    for (int j = 0; j < NG; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) lo[j][k] = hi[j][k] = 0.f;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint4 u = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
-                        const uint4 v = lds128(rb + uint32_t(16 + 32 * t + 16 * half));
-                        const uint32_t w0[4] = {u.x, u.y, u.z, u.w}, w1[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
-                            const uint32_t p0 = w0[i] >> 8, p1 = w1[i] >> 8;
-                            unpack_lo(w0[i], p0, r0, magic, x0, x2);
-                            unpack_lo(w1[i], p1, r1, magic, x1, x3);
-                            unpack_hi(w0[i], p0, r0, magic, y0, y2);
-                            unpack_hi(w1[i], p1, r1, magic, y1, y3);
-#pragma unroll
-                            for (int j = 0; j < NG; ++j) {
-                                const uint32_t* b = act[j].b[4 * half + i];
-                                mma16816(lo[j], x0, x1, x2, x3, b[0], b[1]);
-                                mma16816(hi[j], y0, y1, y2, y3, b[2], b[3]);
+            for (int j = 0; j < NG; ++j) {
+                const int tok = 4 * j + (g >> 1), pos = first + tok;
+                const bool have = works && tok < ntok;
+                const int64_t col = int64_t(sb) * 256 + 64 * t;
+                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!kDown || a.gu_slices == 1) {
+                    const float* x = nullptr;
+                    if (have)
+                        x = kDown ? a.h + int64_t(pos) * p.ffn + col
+                                  : p.x + int64_t(all ? tok : plan.order[pos] / p.top_k) * p.model + col;
+                    make_act(act[u][j], lane, [&](int i) { return have ? __ldcg(reinterpret_cast<const float4*>(x) + i) : zero; });
+                } else {
+                    const int64_t pairs = int64_t(p.tokens) * p.top_k;
+                    make_act(act[u][j], lane, [&](int i) {
+                        float4 c0 = zero, c1 = zero;
+                        if (have) {
+                            for (int s = 0; s < a.gu_slices; ++s) {
+                                const float4* x =
+                                    reinterpret_cast<const float4*>(a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
+                                const float4 c = __ldcg(x), d = __ldcg(x + 1);
+                                c0.x += c.x; c0.y += c.y; c0.z += c.z; c0.w += c.w;
+                                c1.x += d.x; c1.y += d.y; c1.z += d.z; c1.w += d.w;
                             }
                         }
-                    }
-                    float* mine = red + warp * Smem<NG>::kPart + t * kRedPitch + m + g;
+                        return make_float4(silu_times(c0.x, c0.y), silu_times(c0.z, c0.w), silu_times(c1.x, c1.y),
+                                           silu_times(c1.z, c1.w));
+                    });
+                }
+            }
+        }
+    }
+
+    // The warp's partial sums of the tile at shared address st, to `mine`.
+    __device__ __forceinline__ void tile(uint32_t st, int subs, float* mine) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+        for (int m = 0; m < kRows; m += 16) {
+            float tot[NG][2];
 #pragma unroll
-                    for (int j = 0; j < NG; ++j) {
-                        float mn[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma1688(mn, r0.m, r1.m, act[j].sums);
-                        const float s0 = (lo[j][0] + hi[j][0]) + (lo[j][1] + hi[j][1]);
-                        const float s1 = (lo[j][2] + hi[j][2]) + (lo[j][3] + hi[j][3]);
-                        mine[4 * j * kRedPitch] = act[j].up * (r0.d * s0 - r0.dmin * (mn[0] + mn[1]));
-                        mine[4 * j * kRedPitch + 8] = act[j].up * (r1.d * s1 - r1.dmin * (mn[2] + mn[3]));
+            for (int u = 0; u < C::kSub; ++u) {
+                if (u > 0 && u >= subs) break;
+                const uint32_t ra = st + uint32_t(u * kBox + (m + g) * kBlk), rb = ra + 8 * kBlk;
+                const RowScale r0 = row_scale(lds128(ra), t), r1 = row_scale(lds128(rb), t);
+                float acc[NG][4];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint4 c = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
+                    const uint4 d = lds128(rb + uint32_t(16 + 32 * t + 16 * half));
+                    const uint32_t w0[4] = {c.x, c.y, c.z, c.w}, w1[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+                        const uint32_t p0 = w0[i] >> 8, p1 = w1[i] >> 8;
+                        unpack_lo(w0[i], p0, r0, magic, x0, x2);
+                        unpack_lo(w1[i], p1, r1, magic, x1, x3);
+                        unpack_hi(w0[i], p0, r0, magic, y0, y2);
+                        unpack_hi(w1[i], p1, r1, magic, y1, y3);
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) {
+                            const uint32_t* b = act[u][j].b[4 * half + i];
+                            if (half + i == 0) mma16816_first(acc[j], x0, x1, x2, x3, b[0], b[1]);
+                            else mma16816(acc[j], x0, x1, x2, x3, b[0], b[1]);
+                            mma16816(acc[j], y0, y1, y2, y3, b[2], b[3]);
+                        }
                     }
                 }
-                // The stores above depend on every load from the stage, so
-                // those are done in every lane: the next copy may land in it.
-                __syncwarp();
-                if (lane == 0) {
-                    --pending;
-                    issue();
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    float mn[4];
+                    mma1688(mn, r0.m, r1.m, act[u][j].sums);
+                    const float v0 = act[u][j].up * (r0.d * (acc[j][0] + acc[j][1]) - r0.dmin * (mn[0] + mn[1]));
+                    const float v1 = act[u][j].up * (r1.d * (acc[j][2] + acc[j][3]) - r1.dmin * (mn[2] + mn[3]));
+                    tot[j][0] = u == 0 ? v0 : tot[j][0] + v0;
+                    tot[j][1] = u == 0 ? v1 : tot[j][1] + v1;
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                mine[(4 * j + t) * kRedPitch + m + g] = tot[j][0];
+                mine[(4 * j + t) * kRedPitch + m + g + 8] = tot[j][1];
+            }
+        }
+    }
+
+    // A batch of partial sums to be added up: tiles row_tile .. + tiles - 1 (one
+    // per team) for tokens first .. first + ntok - 1 of the plan's order.
+    struct Batch {
+        const float* red;
+        uint32_t full, empty, phase;
+        int first, ntok, held, slice, row_tile, tiles;
+    };
+    // One warp: two rows of one token per lane and step, the team's warps in order.
+    template <bool kDown>
+    __device__ __forceinline__ bool add(const Product<NG>& w, const Batch& d, bool all) {
+        const mmq_q4K_moe_t& p = a.p;
+        const int lane = threadIdx.x & 31;
+        if (!__all_sync(0xffffffffu, wait_bounded(d.full, d.phase, abort_flag, a.status))) return false;
+        constexpr int kLanes = kRows / 2;
+        const int r = 2 * (lane % kLanes);
+        for (int tm = 0; tm < d.tiles; ++tm) {
+            const int row = (d.row_tile + tm) * kRows + r;
+            for (int tok = lane / kLanes; tok < d.ntok; tok += 32 / kLanes) {
+                const int pos = d.first + tok, col = all ? plan.order[pos] / p.top_k : tok;
+                const float* from = d.red + tm * w.crew * C::kPart + col * kRedPitch + r;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll 8
+                for (int v = 0; v * C::kSub < d.held; ++v) {
+                    const float2 f = *reinterpret_cast<const float2*>(from + v * C::kPart);
+                    s0 += f.x;
+                    s1 += f.y;
+                }
+                const int64_t base = int64_t(d.slice) * p.tokens * p.top_k;
+                if (kDown)
+                    *reinterpret_cast<float2*>(a.y + (base + plan.order[pos]) * w.rows + row) = make_float2(s0, s1);
+                else if (w.slices > 1)
+                    *reinterpret_cast<float2*>(a.h + (base + pos) * w.rows + row) = make_float2(s0, s1);
+                else
+                    a.h[int64_t(pos) * p.ffn + (row >> 1)] = silu_times(s0, s1);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d.empty);
+        return true;
+    }
+
+    template <bool kDown>
+    __device__ __forceinline__ void go(Product<NG>& w) {
+        const mmq_q4K_moe_t& p = a.p;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        // Few tokens in all: every expert gets the columns of all of them
+        // (which the matrix instructions have room for anyway), made once.
+        const bool all = !kDown && p.tokens <= C::kTok && w.slices == 1;
+        if (all) fill<kDown>(w, 0, 0, p.tokens, true);
+        Batch due = {};
+        int wait = 0;   // batches until this warp adds `due` up
+        for (; w.run.left > 0; w.run.next(plan, w.slices, w.tiles)) {
+            const Run& run = w.run;
+            const int first = plan.start[run.a] + run.pass * C::kTok;
+            const int ntok = min(C::kTok, plan.start[run.a + 1] - first);
+            const int held = min(w.per, w.nsb - run.slice * w.per);   // super-blocks of this slice
+            const int subs = w.team < w.teams ? min(C::kSub, held - w.ks) : 0;
+            if (!all) fill<kDown>(w, run.slice, first, ntok, false);
+            for (int j0 = 0; j0 < run.count; j0 += w.teams) {
+                float* const red = red0 + buffer * (C::kRed / 4);
+                // The buffer's last batch has been added up (at first: passes at once).
+                if (!__all_sync(0xffffffffu, wait_bounded(red_empty + 8u * uint32_t(buffer), red_phase ^ 1u, abort_flag, a.status)))
+                    return;
+                if (subs > 0 && j0 + w.team < run.count) {
+                    if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag, a.status)))
+                        return;
+                    tile(ring + uint32_t(out_stage * C::kTile), subs, red + warp * C::kPart);
+                    // The stores depend on every load from the stage, so those
+                    // are done in every lane: the next copy may land in it.
+                    __syncwarp();
+                    if (lane == 0) {
+                        --pending;
+                        issue(w);
+                    }
+                    if (++out_stage == kStages) {
+                        out_stage = 0;
+                        out_phase ^= 1u;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(red_full + 8u * uint32_t(buffer));
+                if (turn == warp) {
+                    due = {red, red_full + 8u * uint32_t(buffer), red_empty + 8u * uint32_t(buffer), red_phase, first, ntok,
+                           held, run.slice, run.first + j0, min(w.teams, run.count - j0)};
+                    wait = kLag;
+                } else if (wait > 0 && --wait == 0) {
+                    if (!add<kDown>(w, due, all)) return;
+                }
+                if (++turn == C::kWarps) turn = 0;
+                if (++buffer == C::kBuffers) {
+                    buffer = 0;
+                    red_phase ^= 1u;
+                }
+            }
+        }
+        if (wait > 0) add<kDown>(w, due, all);
+    }
+
+    // Every CTA's writes before this are visible after it (a cooperative
+    // launch: all CTAs are resident).  False after a time-out.
+    __device__ __forceinline__ bool grid_barrier(unsigned* count) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+            const uint64_t t0 = globaltimer();
+            while (true) {
+                unsigned v;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+                if (v >= gridDim.x) break;
+                if (globaltimer() - t0 > kWaitLimitNs) {
+                    abort_flag.set(1u);
+                    atomicCAS(a.status, 0, MMQ_ERR_DEVICE_TIMEOUT);
+                    break;
+                }
+            }
+        }
+        __syncthreads();
+        return !abort_flag.raised();
+    }
+
+    // Only after a wait ran out is anything still in flight.
+    __device__ __forceinline__ void drain() {
+        if ((threadIdx.x & 31) == 0)
+            for (; pending > 0; --pending) {
+                wait_drain(bar0 + 8u * uint32_t(out_stage), out_phase, a.status);
                 if (++out_stage == kStages) {
                     out_stage = 0;
                     out_phase ^= 1u;
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(red_full + 8u * uint32_t(buffer));
-            if (turn == warp) {   // this warp adds the batch up: two rows of one token per lane and step
-                if (!__all_sync(0xffffffffu, wait_bounded(red_full + 8u * uint32_t(buffer), red_phase, abort_flag, a.status)))
-                    break;
-                const int batch = min(teams, run.count - j0);
-                const int r = 2 * (lane & 15);
-                for (int tm = 0; tm < batch; ++tm) {
-                    const int row = (run.first + j0 + tm) * kRows + r;
-                    for (int tok = lane >> 4; tok < ntok; tok += 2) {
-                        const float* from = red + tm * per * Smem<NG>::kPart + tok * kRedPitch + r;
-                        float s0 = 0.f, s1 = 0.f;
-#pragma unroll 8
-                        for (int w = 0; w < held; ++w) {
-                            const float2 f = *reinterpret_cast<const float2*>(from + w * Smem<NG>::kPart);
-                            s0 += f.x;
-                            s1 += f.y;
-                        }
-                        const int pos = first + tok;
-                        const int64_t base = int64_t(run.slice) * p.tokens * p.top_k;
-                        if (kDown)
-                            *reinterpret_cast<float2*>(a.y + (base + plan.order[pos]) * rows + row) = make_float2(s0, s1);
-                        else if (slices > 1)
-                            *reinterpret_cast<float2*>(a.h + (base + pos) * rows + row) = make_float2(s0, s1);
-                        else
-                            a.h[int64_t(pos) * p.ffn + (row >> 1)] = silu_times(s0, s1);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(red_empty + 8u * uint32_t(buffer));
-            }
-            if (++turn == kWarps) turn = 0;
-            if (++buffer == kBuffers) {
-                buffer = 0;
-                red_phase ^= 1u;
-            }
-        }
     }
-    // Only after a wait ran out is anything still in flight.
-    if (lane == 0)
-        for (; pending > 0; --pending) {
-            wait_drain(bar0 + 8u * uint32_t(out_stage), out_phase, a.status);
-            if (++out_stage == kStages) {
-                out_stage = 0;
-                out_phase ^= 1u;
-            }
-        }
-}
+};
 
-// ---------------------------------------------------------------- combine
-__global__ void __launch_bounds__(128) moe_combine_kernel(const MoeArgs a) {
-    griddep_launch_dependents();
-    griddep_wait();
+struct Maps {
+    CUtensorMap gu, down;
+};
+
+// Everything after the logits, one CTA per SM: the plan (in every CTA), both
+// products of the experts, the weighted sum; a grid-wide barrier after each
+// product.  In a product the activations are stationary: a warp keeps the
+// operand of its super-blocks for 4 NG tokens in registers and streams weight
+// tiles of those through a ring of its own; the warps of a team hold the
+// super-blocks of a row (or of a slice of at most 16 of it), so a team reads
+// whole rows.  The partial sums of a batch (one tile per team) meet in shared
+// memory: the warps take turns to add a batch up, in a fixed order, and store
+// it, each a few batches after its own tile of it, when the others have long
+// finished theirs.  (Adding at once makes every warp wait for the one before
+// it, which is late from its own adding: 4950 cycles a batch, of them 2100 of
+// products and 200 of waiting for weights.)
+// The row tiles of all passes of all active experts are dealt out in equal
+// consecutive parts.  The second product's first tiles are asked for before
+// the barrier that its activations wait for.
+template <int NG>
+__global__ void __launch_bounds__(Cfg<NG>::kThreads, 1)
+moe_layer_kernel(const __grid_constant__ Maps maps, const MoeArgs a) {
+    using C = Cfg<NG>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    __shared__ Plan plan;
+    __shared__ PlanScratch scratch;
+    __shared__ uint64_t bars[C::kWarps * kStages + 2 * C::kBuffers];
+    __shared__ uint32_t abort_word;
+    __shared__ int start_at;
     const mmq_q4K_moe_t& p = a.p;
-    const int t = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
-    if (c >= p.model) return;
-    const int64_t pairs = int64_t(p.tokens) * p.top_k;
-    const int64_t at = int64_t(t) * p.model + c;
-    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < p.top_k; ++k) {
-        const int64_t pair = int64_t(t) * p.top_k + k;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < a.down_slices; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(a.y + (i * pairs + pair) * p.model + c);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Layer<NG> layer{a, plan, AbortFlag{smem_u32(&abort_word)}, smem_u32(&bars[warp * kStages]),
+                    smem_u32(&bars[C::kWarps * kStages]), smem_u32(&bars[C::kWarps * kStages + C::kBuffers]),
+                    smem_u32(smem) + uint32_t(warp * kStages * C::kTile), reinterpret_cast<float*>(smem + C::kRing)};
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(layer.magic));
+    if (threadIdx.x == 0) {
+        layer.abort_flag.set(0u);
+        for (int i = 0; i < C::kBuffers; ++i) {
+            mbar_init(layer.red_full + 8u * uint32_t(i), C::kWarps);
+            mbar_init(layer.red_empty + 8u * uint32_t(i), 1);
         }
-        const float w = p.weights[pair];
-        r.x = fmaf(w, s.x, r.x); r.y = fmaf(w, s.y, r.y); r.z = fmaf(w, s.z, r.z); r.w = fmaf(w, s.w, r.w);
+        prefetch_tmap(&maps.gu);
+        prefetch_tmap(&maps.down);
     }
-    if (p.residual) {
-        const float4 v = *reinterpret_cast<const float4*>(p.residual + at);
-        r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(layer.bar0 + 8u * uint32_t(i), 1);
+        fence_barrier_init();
     }
-    *reinterpret_cast<float4*>(p.out + at) = r;
+    make_plan<C::kThreads>(a, &plan, &scratch, C::kTok, blockIdx.x == 0);
+    {
+        Product<NG> first(&maps.gu, 2 * p.ffn, p.model, a.gu_slices, plan, &start_at);
+        layer.start(first);
+        layer.template go<false>(first);
+    }
+    {
+        Product<NG> second(&maps.down, p.model, p.ffn, a.down_slices, plan, &start_at);
+        layer.start(second);
+        if (layer.grid_barrier(a.arrived)) layer.template go<true>(second);
+    }
+    layer.drain();
+    if (!layer.grid_barrier(a.arrived + 1)) return;
+
+    // out = residual + sum of the chosen experts' rows, four values per thread and step
+    const int n4 = p.model / 4;
+    const int64_t pairs = int64_t(p.tokens) * p.top_k;
+    for (int i = blockIdx.x * C::kThreads + threadIdx.x; i < p.tokens * n4; i += gridDim.x * C::kThreads) {
+        const int t = i / n4, c = (i - t * n4) * 4;
+        const int64_t at = int64_t(t) * p.model + c;
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < p.top_k; ++k) {
+            const int64_t pair = int64_t(t) * p.top_k + k;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < a.down_slices; ++j) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.y + (j * pairs + pair) * p.model + c));
+                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            }
+            const float w = __ldcg(p.weights + pair);
+            r.x = fmaf(w, s.x, r.x); r.y = fmaf(w, s.y, r.y); r.z = fmaf(w, s.z, r.z); r.w = fmaf(w, s.w, r.w);
+        }
+        if (p.residual) {
+            const float4 v = *reinterpret_cast<const float4*>(p.residual + at);
+            r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
+        }
+        *reinterpret_cast<float4*>(p.out + at) = r;
+    }
 }
 
-cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_t s, cudaLaunchAttribute* attr) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    return cfg;
-}
-
-// A row's super-blocks in slices of at most 16, one per warp of a team.
-int slices_of(int inner) { return (inner / 256 + kWarps - 1) / kWarps; }
+// A row's super-blocks in slices of at most 16.
+int slices_of(int inner) { return (inner / 256 + kSliceSb - 1) / kSliceSb; }
 
 struct Sizes {
-    size_t logits, h, y, bytes;
+    size_t arrived, logits, h, y, bytes;
 };
 Sizes sizes(const mmq_q4K_moe_t& p) {
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
     Sizes z;
     const size_t pairs = size_t(p.tokens) * size_t(p.top_k);
     const int gu = slices_of(p.model);
-    z.logits = 0;
+    z.arrived = 0;
+    z.logits = 256;
     z.h = z.logits + up(size_t(p.tokens) * size_t(p.experts) * 4);
     z.y = z.h + up(pairs * size_t(p.ffn) * 4 * (gu > 1 ? 2 * size_t(gu) : 1));
     z.bytes = z.y + size_t(slices_of(p.ffn)) * pairs * size_t(p.model) * 4;
     return z;
 }
 
-template <int NG, bool kDown>
-cudaError_t launch_expert(const MoeArgs& a, int nsm, cudaStream_t s) {
-    const int rows = kDown ? a.p.model : 2 * a.p.ffn;
-    const uint64_t pitch = uint64_t((kDown ? a.p.ffn : a.p.model) / 256) * kBlk;
-    CUtensorMap map;
-    if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
-                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
+bool encode_weights(CUtensorMap* m, const uint8_t* w, int experts, int rows, int inner) {
+    const uint64_t pitch = uint64_t(inner / 256) * kBlk;
+    return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, pitch, uint64_t(experts) * uint64_t(rows), pitch, kBlk, kRows,
+                     CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <int NG>
+cudaError_t launch_layer(const MoeArgs& a, int nsm, cudaStream_t s) {
+    const mmq_q4K_moe_t& p = a.p;
+    Maps maps;
+    if (!encode_weights(&maps.gu, p.w_gu, p.experts, 2 * p.ffn, p.model) ||
+        !encode_weights(&maps.down, p.w_down, p.experts, p.model, p.ffn))
         return cudaErrorInvalidValue;
-    constexpr int smem = Smem<NG>::kBytes;
+    constexpr int smem = Cfg<NG>::kBytes;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(moe_expert_kernel<NG, kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-        return e;
+    if ((e = cudaFuncSetAttribute(moe_layer_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(kThreads), smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_expert_kernel<NG, kDown>, map, a);
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(nsm));
+    cfg.blockDim = dim3(Cfg<NG>::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_layer_kernel<NG>, maps, a);
 }
 
 }  // namespace
@@ -700,6 +847,7 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     char* ws = static_cast<char*>(workspace);
     MoeArgs a;
     a.p = p;
+    a.arrived = reinterpret_cast<unsigned*>(ws + z.arrived);
     a.logits = reinterpret_cast<float*>(ws + z.logits);
     a.h = reinterpret_cast<float*>(ws + z.h);
     a.y = reinterpret_cast<float*>(ws + z.y);
@@ -712,11 +860,7 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
     // Four tokens at a time where an expert gets few on average, else eight.
     const bool few = p.tokens <= 4 || p.tokens * p.top_k <= 2 * p.experts;
-    if ((e = few ? launch_expert<1, false>(a, nsm, s) : launch_expert<2, false>(a, nsm, s))) return e;
-    if ((e = few ? launch_expert<1, true>(a, nsm, s) : launch_expert<2, true>(a, nsm, s))) return e;
-    cudaLaunchAttribute last_attr[1];
-    const cudaLaunchConfig_t last = follow_config(dim3(unsigned((p.model / 4 + 127) / 128), unsigned(p.tokens)), dim3(128), 0, s, last_attr);
-    return cudaLaunchKernelEx(&last, moe_combine_kernel, a);
+    return few ? launch_layer<1>(a, nsm, s) : launch_layer<2>(a, nsm, s);
 }
 
 }  // namespace mmq
