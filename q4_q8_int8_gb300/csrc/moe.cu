@@ -77,7 +77,6 @@ struct MoeArgs {
     float* h;            // first product, rows in the plan's order: h [pairs][ffn], or if its sum is in
                          // parts [gu_slices][pairs][2 ffn] of gate and up, alternating
     float* y;            // second product [down_slices][pairs][model], rows by pair
-    unsigned* arrived;   // [2] CTAs at the layer kernel's two barriers; zeroed by the router kernel
     int gu_slices, down_slices;
     int* status;
 };
@@ -87,9 +86,9 @@ struct MoeArgs {
 // so that a thread's loads are all in flight at once.
 constexpr int kRouterThreads = 256;
 __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a) {
+    griddep_launch_dependents();
     griddep_wait();
     const mmq_q4K_moe_t& p = a.p;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.arrived[threadIdx.x] = 0u;
     __shared__ float part[kRouterThreads / 32][4];
     const int e = blockIdx.x, t0 = blockIdx.y * 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float4* w = reinterpret_cast<const float4*>(p.w_router + int64_t(e) * p.model);
@@ -130,10 +129,12 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* ids, uint64_t* tokens_of, bool store) {
     const mmq_q4K_moe_t& p = a.p;
     constexpr int kPer = kMaxExperts / 32;
+    const int used = (p.experts + 31) / 32;   // of the kPer values per lane
     float v[kPer];
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+        if (j >= used) break;
         const int e = lane + 32 * j;
         v[j] = e < p.experts ? a.logits[int64_t(t) * p.experts + e] : -INFINITY;
         top = fmaxf(top, v[j]);
@@ -145,6 +146,7 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* i
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         key[j] = 0;
+        if (j >= used) break;
         if (lane + 32 * j < p.experts) {
             v[j] = expf(v[j] - top);
             sum += v[j];
@@ -157,17 +159,21 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* i
         uint32_t best = 0;
         int at = kMaxExperts;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
+        for (int j = 0; j < kPer; ++j) {
+            if (j >= used) break;
             if (key[j] > best) {
                 best = key[j];
                 at = lane + 32 * j;
             }
+        }
         const uint32_t most = __reduce_max_sync(0xffffffffu, best);
         at = __reduce_min_sync(0xffffffffu, best == most ? at : kMaxExperts);
         const float value = most > 1u ? __uint_as_float(most - 2u) : __int_as_float(0x7FC00000);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
+        for (int j = 0; j < kPer; ++j) {
+            if (j >= used) break;
             if (lane + 32 * j == at) key[j] = 0;
+        }
         picked += value;
         if (lane == i) {
             mine = value;
@@ -410,7 +416,6 @@ struct Product {
         const uint32_t i0 = uint32_t(uint64_t(total) * blockIdx.x / gridDim.x);
         const uint32_t i1 = uint32_t(uint64_t(total) * (blockIdx.x + 1) / gridDim.x);
         const int p0 = int(i0 / each);
-        __syncthreads();   // start_at may still be read for the product before
         if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
             *start_at = threadIdx.x;
         __syncthreads();
@@ -489,7 +494,7 @@ struct Layer {
                     if (have)
                         x = kDown ? a.h + int64_t(pos) * p.ffn + col
                                   : p.x + int64_t(all ? tok : plan.order[pos] / p.top_k) * p.model + col;
-                    make_act(act[u][j], lane, [&](int i) { return have ? __ldcg(reinterpret_cast<const float4*>(x) + i) : zero; });
+                    make_act(act[u][j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
                 } else {
                     const int64_t pairs = int64_t(p.tokens) * p.top_k;
                     make_act(act[u][j], lane, [&](int i) {
@@ -498,7 +503,7 @@ struct Layer {
                             for (int s = 0; s < a.gu_slices; ++s) {
                                 const float4* x =
                                     reinterpret_cast<const float4*>(a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
-                                const float4 c = __ldcg(x), d = __ldcg(x + 1);
+                                const float4 c = x[0], d = x[1];
                                 c0.x += c.x; c0.y += c.y; c0.z += c.z; c0.w += c.w;
                                 c1.x += d.x; c1.y += d.y; c1.z += d.z; c1.w += d.w;
                             }
@@ -661,28 +666,6 @@ struct Layer {
         if (wait > 0) add<kDown>(w, due, all);
     }
 
-    // Every CTA's writes before this are visible after it (a cooperative
-    // launch: all CTAs are resident).  False after a time-out.
-    __device__ __forceinline__ bool grid_barrier(unsigned* count) {
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
-            const uint64_t t0 = globaltimer();
-            while (true) {
-                unsigned v;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
-                if (v >= gridDim.x) break;
-                if (globaltimer() - t0 > kWaitLimitNs) {
-                    abort_flag.set(1u);
-                    atomicCAS(a.status, 0, MMQ_ERR_DEVICE_TIMEOUT);
-                    break;
-                }
-            }
-        }
-        __syncthreads();
-        return !abort_flag.raised();
-    }
-
     // Only after a wait ran out is anything still in flight.
     __device__ __forceinline__ void drain() {
         if ((threadIdx.x & 31) == 0)
@@ -696,28 +679,24 @@ struct Layer {
     }
 };
 
-struct Maps {
-    CUtensorMap gu, down;
-};
-
-// Everything after the logits, one CTA per SM: the plan (in every CTA), both
-// products of the experts, the weighted sum; a grid-wide barrier after each
-// product.  In a product the activations are stationary: a warp keeps the
-// operand of its super-blocks for 4 NG tokens in registers and streams weight
-// tiles of those through a ring of its own; the warps of a team hold the
-// super-blocks of a row (or of a slice of at most 16 of it), so a team reads
-// whole rows.  The partial sums of a batch (one tile per team) meet in shared
-// memory: the warps take turns to add a batch up, in a fixed order, and store
-// it, each a few batches after its own tile of it, when the others have long
-// finished theirs.  (Adding at once makes every warp wait for the one before
-// it, which is late from its own adding: 4950 cycles a batch, of them 2100 of
-// products and 200 of waiting for weights.)
-// The row tiles of all passes of all active experts are dealt out in equal
-// consecutive parts.  The second product's first tiles are asked for before
-// the barrier that its activations wait for.
-template <int NG>
+// One product of all active experts, one CTA per SM.  Activations are
+// stationary: a warp keeps the operand of its super-blocks for 4 NG tokens in
+// registers and streams weight tiles of those through a ring of its own; the
+// warps of a team hold the super-blocks of a row (or of a slice of at most 16
+// of it), so a team reads whole rows.  The partial sums of a batch (one tile
+// per team) meet in shared memory: the warps take turns to add a batch up, in
+// a fixed order, and store it, each a few batches after its own tile of it,
+// when the others have long finished theirs.  (Adding at once makes every warp
+// wait for the one before it, which is late from its own adding: 4950 cycles a
+// batch, of them 2100 of products and 200 of waiting for weights.)  The row
+// tiles of all passes of all active experts are dealt out in equal consecutive
+// parts.
+//
+// Every CTA makes the plan from the logits.  The second product does so, and
+// asks for its first weights, before it waits for the first one's results.
+template <int NG, bool kDown>
 __global__ void __launch_bounds__(Cfg<NG>::kThreads, 1)
-moe_layer_kernel(const __grid_constant__ Maps maps, const MoeArgs a) {
+moe_product_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
     using C = Cfg<NG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -738,99 +717,101 @@ moe_layer_kernel(const __grid_constant__ Maps maps, const MoeArgs a) {
             mbar_init(layer.red_full + 8u * uint32_t(i), C::kWarps);
             mbar_init(layer.red_empty + 8u * uint32_t(i), 1);
         }
-        prefetch_tmap(&maps.gu);
-        prefetch_tmap(&maps.down);
+        prefetch_tmap(&map);
     }
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(layer.bar0 + 8u * uint32_t(i), 1);
         fence_barrier_init();
     }
-    make_plan<C::kThreads>(a, &plan, &scratch, C::kTok, blockIdx.x == 0);
-    {
-        Product<NG> first(&maps.gu, 2 * p.ffn, p.model, a.gu_slices, plan, &start_at);
-        layer.start(first);
-        layer.template go<false>(first);
-    }
-    {
-        Product<NG> second(&maps.down, p.model, p.ffn, a.down_slices, plan, &start_at);
-        layer.start(second);
-        if (layer.grid_barrier(a.arrived)) layer.template go<true>(second);
-    }
+    // The logits are complete before the second product starts: the first one
+    // lets it be scheduled only after its own wait for the router.
+    if (!kDown) griddep_wait();
+    griddep_launch_dependents();
+    make_plan<C::kThreads>(a, &plan, &scratch, C::kTok, !kDown && blockIdx.x == 0);
+    Product<NG> w(&map, kDown ? p.model : 2 * p.ffn, kDown ? p.ffn : p.model, kDown ? a.down_slices : a.gu_slices, plan,
+                  &start_at);
+    layer.start(w);
+    if (kDown) griddep_wait();   // the first product
+    layer.template go<kDown>(w);
     layer.drain();
-    if (!layer.grid_barrier(a.arrived + 1)) return;
+}
 
-    // out = residual + sum of the chosen experts' rows, four values per thread and step
-    const int n4 = p.model / 4;
+// out = residual + the sum of the chosen experts' rows
+__global__ void __launch_bounds__(128) moe_combine_kernel(const MoeArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const mmq_q4K_moe_t& p = a.p;
+    const int t = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
+    if (c >= p.model) return;
     const int64_t pairs = int64_t(p.tokens) * p.top_k;
-    for (int i = blockIdx.x * C::kThreads + threadIdx.x; i < p.tokens * n4; i += gridDim.x * C::kThreads) {
-        const int t = i / n4, c = (i - t * n4) * 4;
-        const int64_t at = int64_t(t) * p.model + c;
-        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t at = int64_t(t) * p.model + c;
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = 0; k < p.top_k; ++k) {
-            const int64_t pair = int64_t(t) * p.top_k + k;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < a.down_slices; ++j) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.y + (j * pairs + pair) * p.model + c));
-                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-            }
-            const float w = __ldcg(p.weights + pair);
-            r.x = fmaf(w, s.x, r.x); r.y = fmaf(w, s.y, r.y); r.z = fmaf(w, s.z, r.z); r.w = fmaf(w, s.w, r.w);
+    for (int k = 0; k < p.top_k; ++k) {
+        const int64_t pair = int64_t(t) * p.top_k + k;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < a.down_slices; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(a.y + (j * pairs + pair) * p.model + c);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
-        if (p.residual) {
-            const float4 v = *reinterpret_cast<const float4*>(p.residual + at);
-            r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
-        }
-        *reinterpret_cast<float4*>(p.out + at) = r;
+        const float w = p.weights[pair];
+        r.x = fmaf(w, s.x, r.x); r.y = fmaf(w, s.y, r.y); r.z = fmaf(w, s.z, r.z); r.w = fmaf(w, s.w, r.w);
     }
+    if (p.residual) {
+        const float4 v = *reinterpret_cast<const float4*>(p.residual + at);
+        r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
+    }
+    *reinterpret_cast<float4*>(p.out + at) = r;
+}
+
+// A kernel of this call that follows another: it may be scheduled before the
+// other ends, and waits for it (griddep_wait) before it reads its results.
+cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_t s, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cfg;
 }
 
 // A row's super-blocks in slices of at most 16.
 int slices_of(int inner) { return (inner / 256 + kSliceSb - 1) / kSliceSb; }
 
 struct Sizes {
-    size_t arrived, logits, h, y, bytes;
+    size_t logits, h, y, bytes;
 };
 Sizes sizes(const mmq_q4K_moe_t& p) {
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
     Sizes z;
     const size_t pairs = size_t(p.tokens) * size_t(p.top_k);
     const int gu = slices_of(p.model);
-    z.arrived = 0;
-    z.logits = 256;
+    z.logits = 0;
     z.h = z.logits + up(size_t(p.tokens) * size_t(p.experts) * 4);
     z.y = z.h + up(pairs * size_t(p.ffn) * 4 * (gu > 1 ? 2 * size_t(gu) : 1));
     z.bytes = z.y + size_t(slices_of(p.ffn)) * pairs * size_t(p.model) * 4;
     return z;
 }
 
-bool encode_weights(CUtensorMap* m, const uint8_t* w, int experts, int rows, int inner) {
-    const uint64_t pitch = uint64_t(inner / 256) * kBlk;
-    return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, pitch, uint64_t(experts) * uint64_t(rows), pitch, kBlk, kRows,
-                     CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-template <int NG>
-cudaError_t launch_layer(const MoeArgs& a, int nsm, cudaStream_t s) {
-    const mmq_q4K_moe_t& p = a.p;
-    Maps maps;
-    if (!encode_weights(&maps.gu, p.w_gu, p.experts, 2 * p.ffn, p.model) ||
-        !encode_weights(&maps.down, p.w_down, p.experts, p.model, p.ffn))
+template <int NG, bool kDown>
+cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
+    const int rows = kDown ? a.p.model : 2 * a.p.ffn;
+    const uint64_t pitch = uint64_t((kDown ? a.p.ffn : a.p.model) / 256) * kBlk;
+    CUtensorMap map;
+    if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
+                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     constexpr int smem = Cfg<NG>::kBytes;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(moe_layer_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    if ((e = cudaFuncSetAttribute(moe_product_kernel<NG, kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+        return e;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(nsm));
-    cfg.blockDim = dim3(Cfg<NG>::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_layer_kernel<NG>, maps, a);
+    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(Cfg<NG>::kThreads), smem, s, attr);
+    return cudaLaunchKernelEx(&cfg, moe_product_kernel<NG, kDown>, map, a);
 }
 
 }  // namespace
@@ -847,7 +828,6 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     char* ws = static_cast<char*>(workspace);
     MoeArgs a;
     a.p = p;
-    a.arrived = reinterpret_cast<unsigned*>(ws + z.arrived);
     a.logits = reinterpret_cast<float*>(ws + z.logits);
     a.h = reinterpret_cast<float*>(ws + z.h);
     a.y = reinterpret_cast<float*>(ws + z.y);
@@ -860,7 +840,12 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
     // Four tokens at a time where an expert gets few on average, else eight.
     const bool few = p.tokens <= 4 || p.tokens * p.top_k <= 2 * p.experts;
-    return few ? launch_layer<1>(a, nsm, s) : launch_layer<2>(a, nsm, s);
+    if ((e = few ? launch_product<1, false>(a, nsm, s) : launch_product<2, false>(a, nsm, s))) return e;
+    if ((e = few ? launch_product<1, true>(a, nsm, s) : launch_product<2, true>(a, nsm, s))) return e;
+    cudaLaunchAttribute last_attr[1];
+    const cudaLaunchConfig_t last =
+        follow_config(dim3(unsigned((p.model / 4 + 127) / 128), unsigned(p.tokens)), dim3(128), 0, s, last_attr);
+    return cudaLaunchKernelEx(&last, moe_combine_kernel, a);
 }
 
 }  // namespace mmq
