@@ -391,30 +391,30 @@ struct Run {
     }
 };
 
+// The shape of one product.
+struct Shape {
+    int rows, nsb, slices, per, crew, teams, tiles;   // per: super-blocks of a slice; crew: warps of a team
+};
+
 // A CTA's share of one product, and where its warps are in it.
 template <int NG>
-struct Product {
+struct Product : Shape {
     using C = Cfg<NG>;
     const CUtensorMap* map;
-    int rows, nsb, slices, per, crew, teams, tiles;   // per: super-blocks of a slice; crew: warps of a team
-    int team, ks;                                      // this warp's team and first super-block
+    int team, ks;  // this warp's team and first super-block
     Run run;
     Run in;        // the run that lane 0 has issued up to, and its next tile
     int in_tile;
 
-    __device__ __forceinline__ Product(const CUtensorMap* m, int rows_, int inner, int slices_, const Plan& plan, int* start_at)
-        : map(m), rows(rows_), nsb(inner / 256), slices(slices_) {
+    __device__ __forceinline__ Product(const CUtensorMap* m, const Shape& shape, const Plan& plan, int* start_at)
+        : Shape(shape), map(m) {
         const int warp = threadIdx.x >> 5;
-        per = (nsb + slices - 1) / slices;
-        crew = (per + C::kSub - 1) / C::kSub;
-        teams = C::kWarps / crew;
         team = warp / crew;
         ks = (warp - team * crew) * C::kSub;
-        tiles = rows / kRows;
-        // equal consecutive parts of all passes' tiles
+        // equal consecutive parts of all passes' tiles, the first `more` one longer
         const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
-        const uint32_t i0 = uint32_t(uint64_t(total) * blockIdx.x / gridDim.x);
-        const uint32_t i1 = uint32_t(uint64_t(total) * (blockIdx.x + 1) / gridDim.x);
+        const uint32_t mine = total / gridDim.x, more = total - mine * gridDim.x;
+        const uint32_t i0 = blockIdx.x * mine + min(blockIdx.x, more), i1 = i0 + mine + (blockIdx.x < more ? 1u : 0u);
         const int p0 = int(i0 / each);
         if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
             *start_at = threadIdx.x;
@@ -696,7 +696,7 @@ struct Layer {
 // asks for its first weights, before it waits for the first one's results.
 template <int NG, bool kDown>
 __global__ void __launch_bounds__(Cfg<NG>::kThreads, 1)
-moe_product_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
+moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, const MoeArgs a) {
     using C = Cfg<NG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -728,8 +728,7 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
     if (!kDown) griddep_wait();
     griddep_launch_dependents();
     make_plan<C::kThreads>(a, &plan, &scratch, C::kTok, !kDown && blockIdx.x == 0);
-    Product<NG> w(&map, kDown ? p.model : 2 * p.ffn, kDown ? p.ffn : p.model, kDown ? a.down_slices : a.gu_slices, plan,
-                  &start_at);
+    Product<NG> w(&map, shape, plan, &start_at);
     layer.start(w);
     if (kDown) griddep_wait();   // the first product
     layer.template go<kDown>(w);
@@ -745,21 +744,20 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const MoeArgs a) {
     if (c >= p.model) return;
     const int64_t pairs = int64_t(p.tokens) * p.top_k;
     const int64_t at = int64_t(t) * p.model + c;
-    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < p.top_k; ++k) {
-        const int64_t pair = int64_t(t) * p.top_k + k;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < a.down_slices; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(a.y + (j * pairs + pair) * p.model + c);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    float4 r = p.residual ? *reinterpret_cast<const float4*>(p.residual + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* y = a.y + int64_t(t) * p.top_k * p.model + c;
+    // the chosen experts in order, the parts of each in order, loads ahead of the sums
+    const int n = p.top_k * a.down_slices;
+    int k = 0, part = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(y + (part * pairs + k) * p.model);
+        const float w = p.weights[t * p.top_k + k];
+        r.x = fmaf(w, v.x, r.x); r.y = fmaf(w, v.y, r.y); r.z = fmaf(w, v.z, r.z); r.w = fmaf(w, v.w, r.w);
+        if (++part == a.down_slices) {
+            part = 0;
+            ++k;
         }
-        const float w = p.weights[pair];
-        r.x = fmaf(w, s.x, r.x); r.y = fmaf(w, s.y, r.y); r.z = fmaf(w, s.z, r.z); r.w = fmaf(w, s.w, r.w);
-    }
-    if (p.residual) {
-        const float4 v = *reinterpret_cast<const float4*>(p.residual + at);
-        r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
     }
     *reinterpret_cast<float4*>(p.out + at) = r;
 }
@@ -800,7 +798,15 @@ Sizes sizes(const mmq_q4K_moe_t& p) {
 template <int NG, bool kDown>
 cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
     const int rows = kDown ? a.p.model : 2 * a.p.ffn;
-    const uint64_t pitch = uint64_t((kDown ? a.p.ffn : a.p.model) / 256) * kBlk;
+    Shape shape;
+    shape.rows = rows;
+    shape.nsb = (kDown ? a.p.ffn : a.p.model) / 256;
+    shape.slices = kDown ? a.down_slices : a.gu_slices;
+    shape.per = (shape.nsb + shape.slices - 1) / shape.slices;
+    shape.crew = (shape.per + Cfg<NG>::kSub - 1) / Cfg<NG>::kSub;
+    shape.teams = Cfg<NG>::kWarps / shape.crew;
+    shape.tiles = rows / kRows;
+    const uint64_t pitch = uint64_t(shape.nsb) * kBlk;
     CUtensorMap map;
     if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
                    uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -811,7 +817,7 @@ cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
         return e;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(Cfg<NG>::kThreads), smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_product_kernel<NG, kDown>, map, a);
+    return cudaLaunchKernelEx(&cfg, moe_product_kernel<NG, kDown>, map, shape, a);
 }
 
 }  // namespace
