@@ -39,7 +39,8 @@ constexpr int kSliceSb = 16;  // super-blocks of a row (or of a slice of it) tha
 constexpr int kRows = 32, kStages = 2;
 constexpr int kBox = kRows * kBlk;
 constexpr int kRedPitch = kRows + 8;   // floats per token: the four lanes of a row on four banks
-constexpr int kLag = 3;                // batches between a warp's own tile of a batch and its adding the batch up
+constexpr int kBatch = 2;              // tiles per team in a batch
+constexpr int kLag = 1;                // batches between a warp's own tiles of a batch and its adding the batch up
 
 // NG: groups of four tokens per pass.  One group: 16 warps with one
 // super-block each (more warps hide more).  Two: 8 warps with two super-blocks
@@ -52,9 +53,9 @@ struct Cfg {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTok = 4 * NG;
     static constexpr int kTile = kSub * kBox;
-    static constexpr int kBuffers = 6;                              // batches of partial sums between the warps
+    static constexpr int kBuffers = 3;                              // batches of partial sums between the warps
     static constexpr int kPart = kTok * kRedPitch;                  // floats of one warp's tile
-    static constexpr int kRed = kWarps * kPart * 4;                 // bytes of one buffer
+    static constexpr int kRed = kBatch * kWarps * kPart * 4;        // bytes of one buffer
     static constexpr int kRing = kWarps * kStages * kTile;
     static constexpr int kBytes = kRing + kBuffers * kRed + 128;    // + alignment
 };
@@ -292,20 +293,32 @@ struct RowScale {
     uint32_t m;                       // the two minima, fp16
     float d, dmin;
 };
-__device__ __forceinline__ RowScale row_scale(const uint4& head, int t) {
+// What a lane needs to know of its two sub-blocks' places among the 6-bit
+// scales: sub-blocks 0-3 are whole, the low six bits of bytes 0-3 (scales) and
+// 4-7 (minima); 4-7 have their low four bits in the nibbles of bytes 8-11 and
+// their high two on top of those bytes.
+struct Place {
+    uint32_t low, high, sel;   // masks of the low and of the high bits; bytes 2 (t & 1) and the next into halfwords
+    bool upper;                // sub-blocks 4-7
+    __device__ __forceinline__ explicit Place(int t)
+        : low(t < 2 ? 0x3F3F3F3Fu : 0x0F0F0F0Fu), high(t < 2 ? 0u : 0x30303030u), sel((t & 1) ? 0x4342u : 0x4140u),
+          upper(t >= 2) {}
+};
+__device__ __forceinline__ RowScale row_scale(const uint4& head, const Place& at) {
     RowScale r;
-    const uint32_t scw = t < 2 ? sc_lo4(head.y) : sc_hi4(head.y, head.w);
-    const uint32_t mw = t < 2 ? m_lo4(head.z) : m_hi4(head.z, head.w);
-    const uint32_t sel = (t & 1) ? 0x4342u : 0x4140u;   // bytes 2(t & 1), 2(t & 1) + 1 into halfwords
+    const uint32_t scw = ((at.upper ? head.w : head.y) & at.low) | ((head.y >> 2) & at.high);
+    const uint32_t mw = ((at.upper ? head.w >> 4 : head.z) & at.low) | ((head.z >> 2) & at.high);
     const __half2 k1024 = u2h(0x64006400u);
-    const __half2 sc = __hsub2(u2h(prmt(scw, 0x64646464u, sel)), k1024);
-    r.m = h2u(__hsub2(u2h(prmt(mw, 0x64646464u, sel)), k1024));
+    const __half2 sc = __hsub2(u2h(prmt(scw, 0x64646464u, at.sel)), k1024);
+    r.m = h2u(__hsub2(u2h(prmt(mw, 0x64646464u, at.sel)), k1024));
     r.s_lo = __low2half2(sc);
-    r.s_hi = __hmul2(__high2half2(sc), u2h(0x2C002C00u));             // / 16
-    r.b_lo = __hmul2(r.s_lo, u2h(0xE400E400u));                       // * -1024, at most 64512
-    r.b_hi = __hmul2(__high2half2(sc), u2h(0xD400D400u));             // * -64
-    r.d = __half2float(__ushort_as_half(uint16_t(head.x & 0xFFFFu)));
-    r.dmin = __half2float(__ushort_as_half(uint16_t(head.x >> 16)));
+    const __half2 hi = __high2half2(sc);
+    r.s_hi = __hmul2(hi, u2h(0x2C002C00u));             // / 16
+    r.b_lo = __hmul2(r.s_lo, u2h(0xE400E400u));         // * -1024, at most 64512
+    r.b_hi = __hmul2(hi, u2h(0xD400D400u));             // * -64
+    const float2 f = __half22float2(u2h(head.x));
+    r.d = f.x;
+    r.dmin = f.y;
     return r;
 }
 // (a & b) | c in one instruction.
@@ -403,8 +416,10 @@ struct Product : Shape {
     const CUtensorMap* map;
     int team, ks;  // this warp's team and first super-block
     Run run;
-    Run in;        // the run that lane 0 has issued up to, and its next tile
-    int in_tile;
+    Run in;             // the run that lane 0 has issued up to,
+    int in_left = 0;    // its tiles that are left for this warp's team,
+    int in_x = 0, in_y = 0;   // and the next one's place in the tensor map
+    bool in_two = false;      // with the warp's second super-block
 
     __device__ __forceinline__ Product(const CUtensorMap* m, const Shape& shape, const Plan& plan, int* start_at)
         : Shape(shape), map(m) {
@@ -428,16 +443,21 @@ struct Product : Shape {
         run.pass = sp - run.slice * passes;
         run.count = min(tiles - run.first, run.left);
         in = run;
-        in_tile = team;
         if (team >= teams) in.left = 0;
-        settle(plan);
+        enter(plan);
     }
-    // To a run with a tile for this warp.
-    __device__ __forceinline__ void settle(const Plan& plan) {
-        while (in.left > 0 && (in_tile >= in.count || in.slice * per + ks >= nsb)) {
-            in.next(plan, slices, tiles);
-            in_tile = team;
+    // The next run from `in` on that has a tile for this warp.
+    __device__ __forceinline__ void enter(const Plan& plan) {
+        for (; in.left > 0; in.next(plan, slices, tiles)) {
+            const int sb = in.slice * per + ks;
+            if (team >= in.count || sb >= nsb) continue;
+            in_left = (in.count - team + teams - 1) / teams;
+            in_x = sb * kBlk;
+            in_y = plan.expert[in.a] * rows + (in.first + team) * kRows;
+            in_two = C::kSub == 2 && ks + 1 < per && sb + 1 < nsb;
+            return;
         }
+        in_left = 0;
     }
 };
 
@@ -456,17 +476,18 @@ struct Layer {
 
     // Lane 0: the warp's next weight tile.
     __device__ __forceinline__ void issue(Product<NG>& w) {
-        if (w.in.left <= 0 || abort_flag.raised()) return;
+        if (w.in_left == 0 || abort_flag.raised()) return;
         const uint32_t bar = bar0 + 8u * uint32_t(in_stage), dst = ring + uint32_t(in_stage * C::kTile);
-        const int sb = w.in.slice * w.per + w.ks, y = plan.expert[w.in.a] * w.rows + (w.in.first + w.in_tile) * kRows;
-        const bool two = C::kSub == 2 && w.ks + 1 < w.per && sb + 1 < w.nsb;
-        mbar_arrive_expect_tx(bar, two ? 2 * kBox : kBox);
-        tma_load_2d(dst, w.map, bar, sb * kBlk, y);
-        if (two) tma_load_2d(dst + kBox, w.map, bar, (sb + 1) * kBlk, y);
+        mbar_arrive_expect_tx(bar, w.in_two ? 2 * kBox : kBox);
+        tma_load_2d(dst, w.map, bar, w.in_x, w.in_y);
+        if (w.in_two) tma_load_2d(dst + kBox, w.map, bar, w.in_x + kBlk, w.in_y);
         ++pending;
         if (++in_stage == kStages) in_stage = 0;
-        w.in_tile += w.teams;
-        w.settle(plan);
+        w.in_y += w.teams * kRows;
+        if (--w.in_left == 0) {
+            w.in.next(plan, w.slices, w.tiles);
+            w.enter(plan);
+        }
     }
     __device__ __forceinline__ void start(Product<NG>& w) {
         if ((threadIdx.x & 31) == 0)
@@ -519,6 +540,7 @@ struct Layer {
     // The warp's partial sums of the tile at shared address st, to `mine`.
     __device__ __forceinline__ void tile(uint32_t st, int subs, float* mine) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const Place place(t);
 #pragma unroll 1
         for (int m = 0; m < kRows; m += 16) {
             float tot[NG][2];
@@ -526,7 +548,7 @@ struct Layer {
             for (int u = 0; u < C::kSub; ++u) {
                 if (u > 0 && u >= subs) break;
                 const uint32_t ra = st + uint32_t(u * kBox + (m + g) * kBlk), rb = ra + 8 * kBlk;
-                const RowScale r0 = row_scale(lds128(ra), t), r1 = row_scale(lds128(rb), t);
+                const RowScale r0 = row_scale(lds128(ra), place), r1 = row_scale(lds128(rb), place);
                 float acc[NG][4];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -568,8 +590,9 @@ struct Layer {
         }
     }
 
-    // A batch of partial sums to be added up: tiles row_tile .. + tiles - 1 (one
-    // per team) for tokens first .. first + ntok - 1 of the plan's order.
+    // A batch of partial sums to be added up: tiles row_tile .. + tiles - 1
+    // (kBatch per team, team by team) for tokens first .. first + ntok - 1 of the
+    // plan's order.
     struct Batch {
         const float* red;
         uint32_t full, empty, phase;
@@ -583,11 +606,13 @@ struct Layer {
         if (!__all_sync(0xffffffffu, wait_bounded(d.full, d.phase, abort_flag, a.status))) return false;
         constexpr int kLanes = kRows / 2;
         const int r = 2 * (lane % kLanes);
-        for (int tm = 0; tm < d.tiles; ++tm) {
-            const int row = (d.row_tile + tm) * kRows + r;
+        for (int i = 0; i < d.tiles; ++i) {
+            const int row = (d.row_tile + i) * kRows + r;
+            const int nb = i >= w.teams ? 1 : 0, tm = i - nb * w.teams;
+            static_assert(kBatch == 2, "a team's first or second tile");
             for (int tok = lane / kLanes; tok < d.ntok; tok += 32 / kLanes) {
                 const int pos = d.first + tok, col = all ? plan.order[pos] / p.top_k : tok;
-                const float* from = d.red + tm * w.crew * C::kPart + col * kRedPitch + r;
+                const float* from = d.red + (nb * C::kWarps + tm * w.crew) * C::kPart + col * kRedPitch + r;
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll 8
                 for (int v = 0; v * C::kSub < d.held; ++v) {
@@ -626,15 +651,17 @@ struct Layer {
             const int held = min(w.per, w.nsb - run.slice * w.per);   // super-blocks of this slice
             const int subs = w.team < w.teams ? min(C::kSub, held - w.ks) : 0;
             if (!all) fill<kDown>(w, run.slice, first, ntok, false);
-            for (int j0 = 0; j0 < run.count; j0 += w.teams) {
+            for (int j0 = 0; j0 < run.count; j0 += kBatch * w.teams) {
                 float* const red = red0 + buffer * (C::kRed / 4);
                 // The buffer's last batch has been added up (at first: passes at once).
                 if (!__all_sync(0xffffffffu, wait_bounded(red_empty + 8u * uint32_t(buffer), red_phase ^ 1u, abort_flag, a.status)))
                     return;
-                if (subs > 0 && j0 + w.team < run.count) {
+#pragma unroll 1
+                for (int nb = 0; nb < kBatch; ++nb) {
+                    if (subs <= 0 || j0 + nb * w.teams + w.team >= run.count) break;
                     if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag, a.status)))
                         return;
-                    tile(ring + uint32_t(out_stage * C::kTile), subs, red + warp * C::kPart);
+                    tile(ring + uint32_t(out_stage * C::kTile), subs, red + (nb * C::kWarps + warp) * C::kPart);
                     // The stores depend on every load from the stage, so those
                     // are done in every lane: the next copy may land in it.
                     __syncwarp();
@@ -651,7 +678,7 @@ struct Layer {
                 if (lane == 0) mbar_arrive(red_full + 8u * uint32_t(buffer));
                 if (turn == warp) {
                     due = {red, red_full + 8u * uint32_t(buffer), red_empty + 8u * uint32_t(buffer), red_phase, first, ntok,
-                           held, run.slice, run.first + j0, min(w.teams, run.count - j0)};
+                           held, run.slice, run.first + j0, min(kBatch * w.teams, run.count - j0)};
                     wait = kLag;
                 } else if (wait > 0 && --wait == 0) {
                     if (!add<kDown>(w, due, all)) return;
@@ -683,10 +710,10 @@ struct Layer {
 // stationary: a warp keeps the operand of its super-blocks for 4 NG tokens in
 // registers and streams weight tiles of those through a ring of its own; the
 // warps of a team hold the super-blocks of a row (or of a slice of at most 16
-// of it), so a team reads whole rows.  The partial sums of a batch (one tile
-// per team) meet in shared memory: the warps take turns to add a batch up, in
-// a fixed order, and store it, each a few batches after its own tile of it,
-// when the others have long finished theirs.  (Adding at once makes every warp
+// of it), so a team reads whole rows.  The partial sums of a batch (two
+// tiles per team) meet in shared memory: the warps take turns to add a batch up, in
+// a fixed order, and store it, each a batch after its own tiles of it, when
+// the others have long finished theirs.  (Adding at once makes every warp
 // wait for the one before it, which is late from its own adding: 4950 cycles a
 // batch, of them 2100 of products and 200 of waiting for weights.)  The row
 // tiles of all passes of all active experts are dealt out in equal consecutive
