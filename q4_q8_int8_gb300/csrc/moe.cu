@@ -549,7 +549,11 @@ struct Layer {
                 if (u > 0 && u >= subs) break;
                 const uint32_t ra = st + uint32_t(u * kBox + (m + g) * kBlk), rb = ra + 8 * kBlk;
                 const RowScale r0 = row_scale(lds128(ra), place), r1 = row_scale(lds128(rb), place);
-                float acc[NG][4];
+                // One group: the low and the high nibbles apart, since the matrix
+                // instructions truncate each step of a sum (9.8e-7 -> 5e-7 of the
+                // result for one token; two groups have no registers for it).
+                constexpr int kApart = NG == 1 ? 2 : 1;
+                float acc[NG][kApart][4];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const uint4 c = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
@@ -566,9 +570,11 @@ struct Layer {
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
                             const uint32_t* b = act[u][j].b[4 * half + i];
-                            if (half + i == 0) mma16816_first(acc[j], x0, x1, x2, x3, b[0], b[1]);
-                            else mma16816(acc[j], x0, x1, x2, x3, b[0], b[1]);
-                            mma16816(acc[j], y0, y1, y2, y3, b[2], b[3]);
+                            const bool first = half + i == 0;
+                            if (first) mma16816_first(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
+                            else mma16816(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
+                            if (first && kApart == 2) mma16816_first(acc[j][kApart - 1], y0, y1, y2, y3, b[2], b[3]);
+                            else mma16816(acc[j][kApart - 1], y0, y1, y2, y3, b[2], b[3]);
                         }
                     }
                 }
@@ -576,8 +582,11 @@ struct Layer {
                 for (int j = 0; j < NG; ++j) {
                     float mn[4];
                     mma1688(mn, r0.m, r1.m, act[u][j].sums);
-                    const float v0 = act[u][j].up * (r0.d * (acc[j][0] + acc[j][1]) - r0.dmin * (mn[0] + mn[1]));
-                    const float v1 = act[u][j].up * (r1.d * (acc[j][2] + acc[j][3]) - r1.dmin * (mn[2] + mn[3]));
+                    if (kApart == 2)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[j][0][k] += acc[j][kApart - 1][k];
+                    const float v0 = act[u][j].up * (r0.d * (acc[j][0][0] + acc[j][0][1]) - r0.dmin * (mn[0] + mn[1]));
+                    const float v1 = act[u][j].up * (r1.d * (acc[j][0][2] + acc[j][0][3]) - r1.dmin * (mn[2] + mn[3]));
                     tot[j][0] = u == 0 ? v0 : tot[j][0] + v0;
                     tot[j][1] = u == 0 ? v1 : tot[j][1] + v1;
                 }
