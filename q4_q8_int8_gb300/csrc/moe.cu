@@ -365,25 +365,27 @@ __device__ __forceinline__ void make_act(Act& act, int lane, Load load) {
     e = e < -126 ? -126 : e;
     const float down = __uint_as_float(uint32_t(127 - e) << 23);
     const bool is_lo = (lane >> 2) & 1;
-    auto part = [&](float f) {
-        const __half hi = __float2half_rn(f);
-        return is_lo ? __float2half_rn(f - __half2float(hi)) : hi;
+    // two values' hi or lo; packed conversions (single ones take the slow pipe)
+    auto part = [&](float f, float h) {
+        const __half2 hi = __floats2half2_rn(f, h);
+        const float2 back = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(f - back.x, h - back.y);
+        return is_lo ? h2u(lo) : h2u(hi);
     };
-    __half sums[2];
+    float sums[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        float s = 0.f;
+        sums[c] = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             const float4 u = v[8 * c + w];
             const float f[4] = {u.x * down, u.y * down, u.z * down, u.w * down};
-            act.b[w][2 * c] = h2u(__halves2half2(part(f[0]), part(f[2])));
-            act.b[w][2 * c + 1] = h2u(__halves2half2(part(f[1]), part(f[3])));
-            s += (f[0] + f[1]) + (f[2] + f[3]);
+            act.b[w][2 * c] = part(f[0], f[2]);
+            act.b[w][2 * c + 1] = part(f[1], f[3]);
+            sums[c] += (f[0] + f[1]) + (f[2] + f[3]);
         }
-        sums[c] = part(s);
     }
-    act.sums = h2u(__halves2half2(sums[0], sums[1]));
+    act.sums = part(sums[0], sums[1]);
     act.up = __shfl_sync(0xffffffffu, __uint_as_float(uint32_t(127 + e) << 23), 8 * (lane & 3));
 }
 
