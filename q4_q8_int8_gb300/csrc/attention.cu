@@ -310,9 +310,12 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
 }
 
 // ------------------------------------------------------------------- join
-// One warp per (token, head).  The parts' (m, l), one part per lane, give the
-// maximum and each part's factor; then the parts' sums, all loads in flight
-// together; parts without keys are not read.
+// kWarpsPerRow warps per (token, head).  The parts' (m, l), one part per lane,
+// give the maximum and each part's factor; then the parts' sums, the warps
+// taking parts in turn with up to eight loads in flight each; parts without
+// keys are not read.  Bound by the latency of those three steps where rows are
+// few: 34 parts of 128 rows take one warp per row 10.5 us.
+constexpr int kJoinWarps = 8;
 __device__ __forceinline__ void store_out(void* out, int type, int64_t at, float x, float y) {
     if (type == MMQ_TYPE_F32)
         *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = make_float2(x, y);
@@ -323,20 +326,20 @@ __device__ __forceinline__ void store_out(void* out, int type, int64_t at, float
             pack16(x, y, static_cast<__nv_bfloat16*>(nullptr));
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+template <int D, int kWarpsPerRow>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31;
+    constexpr int kVec = D / 32;   // values per lane
+    __shared__ float sums[kWarpsPerRow > 1 ? kJoinWarps : 1][kVec][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, turn = warp % kWarpsPerRow;
     const int64_t rows = a.tokens * a.p.heads;
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int parts = a.prefix_parts + a.suffix_parts;
+    const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / kWarpsPerRow) + warp / kWarpsPerRow;
+    const int parts = row < rows ? a.prefix_parts + a.suffix_parts : 0;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[i * rows + row].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    constexpr int kVec = D / 32;   // values per lane
     float l = 0.f, acc[kVec] = {};
     for (int first = 0; first < parts; first += 32) {
         const int n = min(32, parts - first);
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
         l = fmaf(mine, ml.y, l);
         const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
 #pragma unroll 8
-        for (int i = 0; i < n; ++i) {
+        for (int i = turn; i < n; i += kWarpsPerRow) {
             const float* src = a.part_o + ((first + i) * rows + row) * D + kVec * lane;
             const float f = __shfl_sync(0xffffffffu, mine, i);
             float v[kVec] = {};
@@ -362,6 +365,17 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
             for (int k = 0; k < kVec; ++k) acc[k] = fmaf(f, v[k], acc[k]);
         }
     }
+    if (kWarpsPerRow > 1) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sums[warp][k][lane] = acc[k];
+        __syncthreads();
+        if (turn != 0) return;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+#pragma unroll
+            for (int w = 1; w < kWarpsPerRow; ++w) acc[k] += sums[warp + w][k][lane];
+    }
+    if (row >= rows) return;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float r = l == 0.f ? 0.f : 1.f / l;
@@ -492,8 +506,11 @@ cudaError_t launch(const AttnArgs& a, int nsm, cudaStream_t s) {
         const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
         if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
     }
-    const cudaLaunchConfig_t cfg = config(dim3(unsigned((a.tokens * a.p.heads + 7) / 8)), dim3(256), 0);
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, a);
+    // Many parts of few rows: the parts of a row over four warps.
+    const bool many = a.prefix_parts + a.suffix_parts > 8;
+    const int64_t each = many ? kJoinWarps / 4 : kJoinWarps;
+    const cudaLaunchConfig_t cfg = config(dim3(unsigned((a.tokens * a.p.heads + each - 1) / each)), dim3(kJoinWarps * 32), 0);
+    return many ? cudaLaunchKernelEx(&cfg, attn_join_kernel<D, 4>, a) : cudaLaunchKernelEx(&cfg, attn_join_kernel<D, 1>, a);
 }
 
 }  // namespace
