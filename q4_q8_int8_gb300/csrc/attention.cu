@@ -336,33 +336,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
     const int64_t rows = a.tokens * a.p.heads;
     const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / kWarpsPerRow) + warp / kWarpsPerRow;
     const int parts = row < rows ? a.prefix_parts + a.suffix_parts : 0;
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[i * rows + row].x);
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 ml0 = lane < parts ? a.part_ml[lane * rows + row] : none;
+    float m = ml0.x;
+    for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, a.part_ml[i * rows + row].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float l = 0.f, acc[kVec] = {};
     for (int first = 0; first < parts; first += 32) {
         const int n = min(32, parts - first);
-        const float2 ml = lane < n ? a.part_ml[(first + lane) * rows + row] : make_float2(0.f, 0.f);
+        const float2 ml = first == 0 ? ml0 : lane < n ? a.part_ml[(first + lane) * rows + row] : none;
         const float mine = ml.y == 0.f ? 0.f : ex2(ml.x - m);   // l = 0: no keys
         l = fmaf(mine, ml.y, l);
         const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
-#pragma unroll 8
-        for (int i = turn; i < n; i += kWarpsPerRow) {
-            const float* src = a.part_o + ((first + i) * rows + row) * D + kVec * lane;
-            const float f = __shfl_sync(0xffffffffu, mine, i);
-            float v[kVec] = {};
-            if ((has >> i) & 1u) {
-                if (kVec == 4) {
-                    const float4 u = *reinterpret_cast<const float4*>(src);
-                    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[kVec - 1] = u.w;
-                } else {
-                    const float2 u = *reinterpret_cast<const float2*>(src);
-                    v[0] = u.x; v[kVec - 1] = u.y;
+        constexpr int kFlight = 8;
+        for (int i0 = turn; i0 < n; i0 += kFlight * kWarpsPerRow) {
+            float v[kFlight][kVec];
+#pragma unroll
+            for (int q = 0; q < kFlight; ++q) {
+                const int i = i0 + q * kWarpsPerRow;
+                const float* src = a.part_o + (int64_t(first + i) * rows + row) * D + kVec * lane;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) v[q][k] = 0.f;
+                if (i < n && ((has >> i) & 1u)) {
+                    if (kVec == 4) {
+                        const float4 u = *reinterpret_cast<const float4*>(src);
+                        v[q][0] = u.x; v[q][1] = u.y; v[q][2] = u.z; v[q][kVec - 1] = u.w;
+                    } else {
+                        const float2 u = *reinterpret_cast<const float2*>(src);
+                        v[q][0] = u.x; v[q][kVec - 1] = u.y;
+                    }
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) acc[k] = fmaf(f, v[k], acc[k]);
+            for (int q = 0; q < kFlight; ++q) {
+                const float f = __shfl_sync(0xffffffffu, mine, (i0 + q * kWarpsPerRow) & 31);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) acc[k] = fmaf(f, v[q][k], acc[k]);
+            }
         }
     }
     if (kWarpsPerRow > 1) {
