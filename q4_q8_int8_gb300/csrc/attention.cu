@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
         const float mine = ml.y == 0.f ? 0.f : ex2(ml.x - m);   // l = 0: no keys
         l = fmaf(mine, ml.y, l);
         const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
-        constexpr int kFlight = 8;
+        constexpr int kFlight = kWarpsPerRow == 1 ? 4 : 8;
         for (int i0 = turn; i0 < n; i0 += kFlight * kWarpsPerRow) {
             float v[kFlight][kVec];
 #pragma unroll
