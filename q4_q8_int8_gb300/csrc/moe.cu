@@ -539,24 +539,23 @@ struct Layer {
         }
     }
 
-    // The warp's partial sums of the tile at shared address st, to `mine`, for
-    // the first kGroups groups of four tokens.
-    template <int kGroups>
+    // The warp's partial sums of the tile at shared address st, to `mine`.
     __device__ __forceinline__ void tile(uint32_t st, int subs, float* mine) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const Place place(t);
-#pragma unroll 1
-        for (int m = 0; m < kRows; m += 16) {
-            float tot[kGroups][2];
 #pragma unroll
-            for (int u = 0; u < C::kSub; ++u) {
-                if (u > 0 && u >= subs) break;
+        for (int u = 0; u < C::kSub; ++u) {
+            if (u > 0 && u >= subs) break;
+            // Rolled: with two super-blocks the instructions of a tile are many
+            // enough to be waited for.
+#pragma unroll 1
+            for (int m = 0; m < kRows; m += 16) {
                 const uint32_t ra = st + uint32_t(u * kBox + (m + g) * kBlk), rb = ra + 8 * kBlk;
                 const RowScale r0 = row_scale(lds128(ra), place), r1 = row_scale(lds128(rb), place);
                 // The low and the high nibbles apart, since the matrix instructions
                 // truncate each step of a sum (9.8e-7 -> 5e-7 of the result for one
                 // token).
-                float acc[kGroups][2][4];
+                float acc[NG][2][4];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const uint4 c = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
@@ -571,32 +570,30 @@ struct Layer {
                         unpack_hi(w0[i], p0, r0, magic, y0, y2);
                         unpack_hi(w1[i], p1, r1, magic, y1, y3);
 #pragma unroll
-                        for (int j = 0; j < kGroups; ++j) {
+                        for (int j = 0; j < NG; ++j) {
                             const uint32_t* b = act[u][j].b[4 * half + i];
-                            const bool first = half + i == 0;
-                            if (first) mma16816_first(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
-                            else mma16816(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
-                            if (first) mma16816_first(acc[j][1], y0, y1, y2, y3, b[2], b[3]);
-                            else mma16816(acc[j][1], y0, y1, y2, y3, b[2], b[3]);
+                            if (half + i == 0) {
+                                mma16816_first(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
+                                mma16816_first(acc[j][1], y0, y1, y2, y3, b[2], b[3]);
+                            } else {
+                                mma16816(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
+                                mma16816(acc[j][1], y0, y1, y2, y3, b[2], b[3]);
+                            }
                         }
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
+                for (int j = 0; j < NG; ++j) {
                     float mn[4];
                     mma1688(mn, r0.m, r1.m, act[u][j].sums);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[j][0][k] += acc[j][1][k];
-                    const float v0 = act[u][j].up * (r0.d * (acc[j][0][0] + acc[j][0][1]) - r0.dmin * (mn[0] + mn[1]));
-                    const float v1 = act[u][j].up * (r1.d * (acc[j][0][2] + acc[j][0][3]) - r1.dmin * (mn[2] + mn[3]));
-                    tot[j][0] = u == 0 ? v0 : tot[j][0] + v0;
-                    tot[j][1] = u == 0 ? v1 : tot[j][1] + v1;
+                    const float s0 = (acc[j][0][0] + acc[j][1][0]) + (acc[j][0][1] + acc[j][1][1]);
+                    const float s1 = (acc[j][0][2] + acc[j][1][2]) + (acc[j][0][3] + acc[j][1][3]);
+                    const float v0 = act[u][j].up * (r0.d * s0 - r0.dmin * (mn[0] + mn[1]));
+                    const float v1 = act[u][j].up * (r1.d * s1 - r1.dmin * (mn[2] + mn[3]));
+                    float* out = mine + (4 * j + t) * kRedPitch + m + g;
+                    out[0] = u == 0 ? v0 : out[0] + v0;
+                    out[8] = u == 0 ? v1 : out[8] + v1;
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                mine[(4 * j + t) * kRedPitch + m + g] = tot[j][0];
-                mine[(4 * j + t) * kRedPitch + m + g + 8] = tot[j][1];
             }
         }
     }
@@ -662,7 +659,6 @@ struct Layer {
             const int held = min(w.per, w.nsb - run.slice * w.per);   // super-blocks of this slice
             const int subs = w.team < w.teams ? min(C::kSub, held - w.ks) : 0;
             if (!all) fill<kDown>(w, run.slice, first, ntok, false);
-            const int columns = all ? p.tokens : ntok;   // a pass may have few tokens left
             for (int j0 = 0; j0 < run.count; j0 += kBatch * w.teams) {
                 float* const red = red0 + buffer * (C::kRed / 4);
                 // The buffer's last batch has been added up (at first: passes at once).
@@ -675,8 +671,7 @@ struct Layer {
                         return;
                     float* const mine = red + (nb * C::kWarps + warp) * C::kPart;
                     const uint32_t st = ring + uint32_t(out_stage * C::kTile);
-                    if (NG == 1 || columns > 4) tile<NG>(st, subs, mine);
-                    else tile<1>(st, subs, mine);
+                    tile(st, subs, mine);
                     // The stores depend on every load from the stage, so those
                     // are done in every lane: the next copy may land in it.
                     __syncwarp();
