@@ -427,16 +427,20 @@ int mmq_gguf_write(const char* path, int64_t n, const char* const* names,
 
 /* Synchronizes `stream`, then returns and clears the current device's status
  * word: MMQ_OK, or MMQ_ERR_DEVICE_TIMEOUT if a kernel's bounded wait gave up
- * since the last call (that kernel's output is then invalid), or
- * MMQ_ERR_CUDA if the synchronization itself failed. */
+ * since the last call (that kernel's output is then invalid), or MMQ_ERR_ARG
+ * if a kernel met a position, slot, page or length out of range (the calls
+ * that read such say what became of them), or MMQ_ERR_CUDA if the
+ * synchronization itself failed. */
 int mmq_status(void* stream);
 
 /* Static text for an MMQ_* code. */
 const char* mmq_strerror(int code);
 
 /* Programmatic dependent launch (process-wide, default off): when enabled,
- * the q8_1 prepass and the GEMM kernels (few-token and tcgen05) are launched
+ * the q8_1 prepass, the GEMM kernels (few-token and tcgen05), the head norms
+ * and the first kernel of an attention or mixture-of-experts call are launched
  * so that each may start while the previous kernel on its stream finishes.
+ * (The later kernels of such a call always are; they belong to the call.)
  * A kernel so launched issues only its weight loads (or, for the tcgen05
  * kernel, only its set-up) before it waits for the previous grid to
  * complete; it reads activations and writes its outputs only after that
@@ -534,9 +538,11 @@ size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t
  * and zeros for a token that sees no key.  Scores, the running maximum and
  * sum and the values' sum are f32; the weights are rounded to `type` for the
  * product with the values (a relative 2^-11 or 2^-8 per weight, unbiased), so
- * an f32 out is no more precise than that.  The prefix is read once per 128 or
- * so rows of the batch rather than once per sequence.  What the caches hold
- * past a token's last key is never read.  Results are bitwise the same run to
+ * an f32 out is no more precise than that.  The prefix is read once for all:
+ * per kv head, 128 or 256 rows (a token and a head of the group each) share each
+ * key tile.  Each token reads its own suffix by itself: q_len is meant for the
+ * few tokens of a speculative step, not for a prefill.  What the caches hold
+ * past a token's last key is never used, whatever it is.  Results are bitwise the same run to
  * run on one device and build.  A length over table_width * page_size is cut
  * to it, and a page number outside [0, n_pages) stands for a page of zeros;
  * either sets the device status word to MMQ_ERR_ARG.
@@ -580,7 +586,8 @@ size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p);
  * sum of two fp16 values (within 2^-22 of the value or 2^-32 of the largest of
  * its 256 neighbours) against the weights' exact integers, with f32 sums, so
  * the result is that of f32 arithmetic on the dequantized weights.  Only the
- * chosen experts' weights are read, once per 4 to 16 tokens of an expert.
+ * chosen experts' weights are read, once per four tokens of an expert, or per
+ * eight where an expert gets more than two on average.
  * Results are bitwise the same run to run on one device and build.
  * tokens 1..64 (0 does nothing), experts 1..256, top_k 1..16 and at most
  * experts, tokens * top_k at most 512, model and ffn multiples of 256;

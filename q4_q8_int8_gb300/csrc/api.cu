@@ -490,11 +490,11 @@ static int check_attention_sizes(const mmq_shared_prefix_attention_t* p) {
     if (p->type != MMQ_TYPE_F16 && p->type != MMQ_TYPE_BF16) return MMQ_ERR_ARG;
     if (p->out_type != p->type && p->out_type != MMQ_TYPE_F32) return MMQ_ERR_ARG;
     if (!(p->scale > 0.f && p->scale < 1e30f)) return MMQ_ERR_ARG;
-    const int64_t kStride = int64_t(1) << 40;
+    const int64_t kStride = int64_t(1) << 38;   // a tensor map's strides are below 2^40 bytes
     if (p->q_stride < int64_t(p->heads) * p->head_dim || p->q_stride % 8 || p->q_stride > kStride) return MMQ_ERR_ARG;
     if (p->prefix > 0) {
         const int64_t ts = p->prefix_token_stride, hs = p->prefix_head_stride;
-        if (ts < p->head_dim || hs < p->head_dim || ts % 8 || hs % 8 || ts > kStride / 2 || hs > kStride / 2)
+        if (ts < p->head_dim || hs < p->head_dim || ts % 8 || hs % 8 || ts > kStride || hs > kStride)
             return MMQ_ERR_ARG;
     }
     return MMQ_OK;
@@ -524,7 +524,9 @@ int mmq_shared_prefix_attention(const mmq_shared_prefix_attention_t* p, void* wo
     if (workspace_bytes < need) return MMQ_ERR_ARG;
     int* status = mmq::status_word_ptr();
     if (!status) return MMQ_ERR_CUDA;
-    return from_cuda(mmq::launch_shared_prefix_attention(*p, workspace, status, static_cast<cudaStream_t>(stream)));
+    const cudaError_t e = mmq::launch_shared_prefix_attention(*p, workspace, status, static_cast<cudaStream_t>(stream));
+    // the tensor-core kernel's register split does not fit this build of it
+    return e == cudaErrorLaunchOutOfResources ? MMQ_ERR_RESOURCE : from_cuda(e);
 }
 
 // The sizes of a mixture-of-experts call (no pointers): MMQ_OK or MMQ_ERR_ARG.

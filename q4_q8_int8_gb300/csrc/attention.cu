@@ -73,7 +73,9 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
 // suffixes are short.  Keys past the row's limit are filled with zeros, not
 // read, so what the cache holds there cannot matter.  Weights are rounded to
 // the cache's type for the second product (their sum is taken in f32 before
-// that); both products accumulate in f32.
+// that); both products accumulate in f32.  Measured: 256 suffixes of 1 to 512
+// tokens, 8 kv heads x 128 (261 MB): 50 us, 5.2 TB/s, 77 % of the copy rate (as
+// CTAs of four warps that join in shared memory: 66 us).
 constexpr int kSlab = 16, kStages = 3;
 
 template <int D>

@@ -25,9 +25,18 @@
 // into step, both groups at their softmax and then both at their products (1950
 // a batch); hence two that pass a turn.
 //
-// O is only scaled when a row's maximum has grown by more than 2^8 since the
-// last time (P then stays below 2^8, far inside fp16's range, and nothing is
-// lost: the factor is common to P, the sum and O).
+// Measured: 1024 rows per kv head x 16384 keys x 8 kv heads, D = 128 (68.7
+// GFLOP): 62 us on the 128 CTAs that four parts make, 1.1 PFLOP/s, 59 % of the
+// measured bf16 rate.  A pair of tiles takes 2980 cycles of which the products
+// are 2048: a group's chain of scores, softmax (1230), hand-over (230) and its
+// own products (2 x 512, and the waits between) is what is left to shorten.
+// Tried and no faster: half of P handed over early, the maximum of the tile
+// before as the reference so that the exponentials need not wait for this
+// one's, polling instead of suspended waits.
+//
+// O is only scaled when a row's largest score (in units of log2) has grown by
+// more than 8 since the last time: P then stays below 2^8, far inside fp16's
+// range, and nothing is lost, since the factor is common to P, the sum and O.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -16,6 +16,18 @@
 //   S = sum (sc q) x,  M = sum over the eight 32-value sub-blocks of m X, X the
 // sub-block's sum of activations (split in the same way).  So the experts see
 // f32 activations (no q8_1 rounding of x or h) at fp16 matrix rates.
+//
+// Measured: 16 tokens, 64 experts of 4096 x 2048, 6 per token (50 of them
+// active): the first product streams 478 MB in 82 us (5.8 TB/s, 86 % of the
+// copy rate), the second 239 MB in 42 us, and 35 us go into the router (4), the
+// plans and first tiles (8 each), the spread of the CTAs' ends and the combine.
+// 32 tokens on 8 experts of 4096 x 11008 take 290 us where the weights' bytes
+// need 90: at eight tokens a pass a tile costs twice the instructions, an SM
+// holds 8 warps of 255 registers, too few to hide them behind each other, and
+// experts with more than eight tokens are read twice.  Tried and slower: the
+// second group's activations in shared memory and 16 warps (304 us), the whole
+// layer as one cooperative kernel with barriers (329 us; one token 38 us
+// instead of 30).
 #include <cuda_fp16.h>
 
 #include "mmq_internal.h"
@@ -45,7 +57,8 @@ constexpr int kLag = 1;                // batches between a warp's own tiles of 
 // NG: groups of four tokens per pass.  One group: 16 warps with one
 // super-block each (more warps hide more).  Two: 8 warps with two super-blocks
 // each, since the activations of two groups and the rest of the state do not
-// fit 128 registers (655 -> 341 us for 32 tokens on 8 wide experts).
+// fit 128 registers (453 us with 16 warps, 290 with 8, for 32 tokens on 8 wide
+// experts).
 template <int NG>
 struct Cfg {
     static constexpr int kSub = NG;                                 // super-blocks per warp
@@ -881,7 +894,10 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     const cudaLaunchConfig_t first = launch_config(dim3(unsigned(p.experts), unsigned((p.tokens + 3) / 4)),
                                                    dim3(kRouterThreads), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
-    // Four tokens at a time where an expert gets few on average, else eight.
+    // Four tokens at a time where an expert gets few on average, else eight: a
+    // pass of eight costs less than two of four, but more than one (16 tokens, 6
+    // of 64 experts each: 162 us by fours, 234 us for the first product alone by
+    // eights; 32 tokens, 2 of 8: 290 us by eights, 2947 us by fours at first).
     const bool few = p.tokens <= 4 || p.tokens * p.top_k <= 2 * p.experts;
     if ((e = few ? launch_product<1, false>(a, nsm, s) : launch_product<2, false>(a, nsm, s))) return e;
     if ((e = few ? launch_product<1, true>(a, nsm, s) : launch_product<2, true>(a, nsm, s))) return e;
