@@ -586,8 +586,7 @@ size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p);
  * sum of two fp16 values (within 2^-22 of the value or 2^-32 of the largest of
  * its 256 neighbours) against the weights' exact integers, with f32 sums, so
  * the result is that of f32 arithmetic on the dequantized weights.  Only the
- * chosen experts' weights are read, once per four tokens of an expert, or per
- * eight where an expert gets more than two on average.
+ * chosen experts' weights are read, once per four tokens of an expert.
  * Results are bitwise the same run to run on one device and build.
  * tokens 1..64 (0 does nothing), experts 1..256, top_k 1..16 and at most
  * experts, tokens * top_k at most 512, model and ffn multiples of 256;

@@ -21,13 +21,14 @@
 // active): the first product streams 478 MB in 82 us (5.8 TB/s, 86 % of the
 // copy rate), the second 239 MB in 42 us, and 35 us go into the router (4), the
 // plans and first tiles (8 each), the spread of the CTAs' ends and the combine.
-// 32 tokens on 8 experts of 4096 x 11008 take 290 us where the weights' bytes
-// need 90: at eight tokens a pass a tile costs twice the instructions, an SM
-// holds 8 warps of 255 registers, too few to hide them behind each other, and
-// experts with more than eight tokens are read twice.  Tried and slower: the
-// second group's activations in shared memory and 16 warps (304 us), the whole
-// layer as one cooperative kernel with barriers (329 us; one token 38 us
-// instead of 30).
+// The instructions that unpack and multiply a tile take 2100 cycles on an SM's
+// 16 warps, its bytes 3200 at the copy rate, so an expert with more than four
+// tokens, whose weights are unpacked once per four, is bound by them: 32 tokens
+// on 8 experts of 4096 x 11008 take 305 us where the bytes need 90.  Tried and
+// no faster: an expert's passes side by side, so that all but one find the
+// weights in the L2 (310 us); eight tokens a pass; the whole layer as one
+// cooperative kernel with barriers (32 tokens 329 us, one token 38 instead of
+// 30).
 #include <cuda_fp16.h>
 
 #include "mmq_internal.h"
@@ -43,36 +44,27 @@ constexpr int kMaxTokens = MMQ_MOE_MAX_TOKENS;
 constexpr int kMaxExperts = MMQ_MOE_MAX_EXPERTS;
 constexpr int kMaxPairs = MMQ_MOE_MAX_PAIRS;
 constexpr int kBlk = 144;     // bytes of a q4_K super-block
-constexpr int kSliceSb = 16;  // super-blocks of a row (or of a slice of it) that a CTA's warps hold together
-// A weight tile is 32 rows x a warp's super-blocks, one TMA box each, two
-// tiles per warp in flight: 32 boxes per SM.  Streaming 604 MB through such
-// rings with no other work takes 92 us (6.5 TB/s) with 32 boxes of 16 or of 32
-// rows in flight per SM, but 127 us with 48 and 154 us with 64.
+// A warp holds one super-block of a row at a time, a CTA's warps up to 16 (a
+// row, or a slice of it), for four tokens.  (Eight tokens at a time halve the
+// passes of an expert that many chose, but want twice the registers, so half
+// the warps: 32 tokens, 2 of 8 experts each, 150 us instead of 127; 24 tokens,
+// 2 of 16: 123 instead of 77.)
+constexpr int kWarps = 16, kThreads = 32 * kWarps, kTok = 4;
+// A weight tile is 32 rows x one super-block, one TMA box, two per warp in
+// flight: 32 boxes per SM.  Streaming 604 MB through such rings with no other
+// work takes 92 us (6.5 TB/s) with 32 boxes of 16 or of 32 rows in flight per
+// SM, but 127 us with 48 and 154 us with 64.
 constexpr int kRows = 32, kStages = 2;
-constexpr int kBox = kRows * kBlk;
+constexpr int kTile = kRows * kBlk;
 constexpr int kRedPitch = kRows + 8;   // floats per token: the four lanes of a row on four banks
 constexpr int kBatch = 2;              // tiles per team in a batch
 constexpr int kLag = 1;                // batches between a warp's own tiles of a batch and its adding the batch up
-
-// NG: groups of four tokens per pass.  One group: 16 warps with one
-// super-block each (more warps hide more).  Two: 8 warps with two super-blocks
-// each, since the activations of two groups and the rest of the state do not
-// fit 128 registers (453 us with 16 warps, 290 with 8, for 32 tokens on 8 wide
-// experts).
-template <int NG>
-struct Cfg {
-    static constexpr int kSub = NG;                                 // super-blocks per warp
-    static constexpr int kWarps = kSliceSb / kSub;
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTok = 4 * NG;
-    static constexpr int kTile = kSub * kBox;
-    static constexpr int kBuffers = 3;                              // batches of partial sums between the warps
-    static constexpr int kPart = kTok * kRedPitch;                  // floats of one warp's tile
-    static constexpr int kRed = kBatch * kWarps * kPart * 4;        // bytes of one buffer
-    static constexpr int kRing = kWarps * kStages * kTile;
-    static constexpr int kBytes = kRing + kBuffers * kRed + 128;    // + alignment
-};
-static_assert(Cfg<1>::kBytes <= 208 * 1024 && Cfg<2>::kBytes <= 208 * 1024, "shared memory budget");
+constexpr int kBuffers = 3;                                // batches of partial sums between the warps
+constexpr int kPart = kTok * kRedPitch;                    // floats of one warp's tile
+constexpr int kRed = kBatch * kWarps * kPart * 4;          // bytes of one buffer
+constexpr int kRing = kWarps * kStages * kTile;
+constexpr int kSmemBytes = kRing + kBuffers * kRed + 128;  // + alignment
+static_assert(kSmemBytes <= 212 * 1024, "shared memory budget");
 
 // Which tokens go to which expert: pair i = token i / top_k, its i % top_k-th
 // expert.  An active expert (one with a token) has its pairs in a row of
@@ -214,10 +206,9 @@ struct PlanScratch {
     int totals[3][kMaxExperts / 32];
 };
 
-// Fill `plan` (shared memory) from the logits, for passes of `pass_tokens`;
-// `store`: also the chosen experts and their weights to the caller.
-template <int kThreads>
-__device__ __forceinline__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, int pass_tokens, bool store) {
+// Fill `plan` (shared memory) from the logits; `store`: also the chosen
+// experts and their weights to the caller.
+__device__ __forceinline__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, bool store) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
     static_assert(kMaxExperts <= kThreads && kMaxTokens <= 64, "one thread per expert, one bit per token");
     if (e < kMaxExperts) z->tokens_of[e] = 0;
@@ -225,7 +216,7 @@ __device__ __forceinline__ void make_plan(const MoeArgs& a, Plan* plan, PlanScra
     for (int t = warp; t < a.p.tokens; t += kThreads / 32) choose(a, t, lane, z->ids, z->tokens_of, store);
     __syncthreads();
     uint64_t mine = e < kMaxExperts ? z->tokens_of[e] : 0;
-    const int n = __popcll(mine), passes = (n + pass_tokens - 1) / pass_tokens;
+    const int n = __popcll(mine), passes = (n + kTok - 1) / kTok;
     // prefixes over the experts: of their pairs, their passes, and the active ones
     int pairs = n, pass = passes;
 #pragma unroll
@@ -421,26 +412,23 @@ struct Run {
 
 // The shape of one product.
 struct Shape {
-    int rows, nsb, slices, per, crew, teams, tiles;   // per: super-blocks of a slice; crew: warps of a team
+    int rows, nsb, slices, per, teams, tiles;   // per: super-blocks of a slice and warps of a team
 };
 
 // A CTA's share of one product, and where its warps are in it.
-template <int NG>
 struct Product : Shape {
-    using C = Cfg<NG>;
     const CUtensorMap* map;
-    int team, ks;  // this warp's team and first super-block
+    int team, ks;  // this warp's team and its super-block of a slice
     Run run;
     Run in;             // the run that lane 0 has issued up to,
     int in_left = 0;    // its tiles that are left for this warp's team,
     int in_x = 0, in_y = 0;   // and the next one's place in the tensor map
-    bool in_two = false;      // with the warp's second super-block
 
     __device__ __forceinline__ Product(const CUtensorMap* m, const Shape& shape, const Plan& plan, int* start_at)
         : Shape(shape), map(m) {
         const int warp = threadIdx.x >> 5;
-        team = warp / crew;
-        ks = (warp - team * crew) * C::kSub;
+        team = warp / per;
+        ks = warp - team * per;
         // equal consecutive parts of all passes' tiles, the first `more` one longer
         const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
         const uint32_t mine = total / gridDim.x, more = total - mine * gridDim.x;
@@ -469,16 +457,13 @@ struct Product : Shape {
             in_left = (in.count - team + teams - 1) / teams;
             in_x = sb * kBlk;
             in_y = plan.expert[in.a] * rows + (in.first + team) * kRows;
-            in_two = C::kSub == 2 && ks + 1 < per && sb + 1 < nsb;
             return;
         }
         in_left = 0;
     }
 };
 
-template <int NG>
 struct Layer {
-    using C = Cfg<NG>;
     const MoeArgs& a;
     const Plan& plan;
     AbortFlag abort_flag;
@@ -487,15 +472,14 @@ struct Layer {
     uint32_t magic;                        // fp16 1024 twice, in a register: one constant per instruction
     int in_stage = 0, out_stage = 0, pending = 0, buffer = 0, turn = 0;
     uint32_t out_phase = 0, red_phase = 0;
-    Act act[C::kSub][NG];
+    Act act;
 
     // Lane 0: the warp's next weight tile.
-    __device__ __forceinline__ void issue(Product<NG>& w) {
+    __device__ __forceinline__ void issue(Product& w) {
         if (w.in_left == 0 || abort_flag.raised()) return;
-        const uint32_t bar = bar0 + 8u * uint32_t(in_stage), dst = ring + uint32_t(in_stage * C::kTile);
-        mbar_arrive_expect_tx(bar, w.in_two ? 2 * kBox : kBox);
-        tma_load_2d(dst, w.map, bar, w.in_x, w.in_y);
-        if (w.in_two) tma_load_2d(dst + kBox, w.map, bar, w.in_x + kBlk, w.in_y);
+        const uint32_t bar = bar0 + 8u * uint32_t(in_stage);
+        mbar_arrive_expect_tx(bar, kTile);
+        tma_load_2d(ring + uint32_t(in_stage * kTile), w.map, bar, w.in_x, w.in_y);
         ++pending;
         if (++in_stage == kStages) in_stage = 0;
         w.in_y += w.teams * kRows;
@@ -504,7 +488,7 @@ struct Layer {
             w.enter(plan);
         }
     }
-    __device__ __forceinline__ void start(Product<NG>& w) {
+    __device__ __forceinline__ void start(Product& w) {
         if ((threadIdx.x & 31) == 0)
             for (int i = 0; i < kStages; ++i) issue(w);
     }
@@ -512,102 +496,76 @@ struct Layer {
     // This warp's operand: tokens first .. first + ntok - 1 of the plan's
     // order; `all`: the tokens themselves.
     template <bool kDown>
-    __device__ __forceinline__ void fill(const Product<NG>& w, int slice, int first, int ntok, bool all) {
+    __device__ __forceinline__ void fill(const Product& w, int slice, int first, int ntok, bool all) {
         const mmq_q4K_moe_t& p = a.p;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int u = 0; u < C::kSub; ++u) {
-            const int sb = slice * w.per + w.ks + u;
-            const bool works = w.team < w.teams && w.ks + u < w.per && sb < w.nsb;
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const int tok = 4 * j + (g >> 1), pos = first + tok;
-                const bool have = works && tok < ntok;
-                const int64_t col = int64_t(sb) * 256 + 64 * t;
-                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!kDown || a.gu_slices == 1) {
-                    const float* x = nullptr;
-                    if (have)
-                        x = kDown ? a.h + int64_t(pos) * p.ffn + col
-                                  : p.x + int64_t(all ? tok : plan.order[pos] / p.top_k) * p.model + col;
-                    make_act(act[u][j], lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
-                } else {
-                    const int64_t pairs = int64_t(p.tokens) * p.top_k;
-                    make_act(act[u][j], lane, [&](int i) {
-                        float4 c0 = zero, c1 = zero;
-                        if (have) {
-                            for (int s = 0; s < a.gu_slices; ++s) {
-                                const float4* x =
-                                    reinterpret_cast<const float4*>(a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
-                                const float4 c = x[0], d = x[1];
-                                c0.x += c.x; c0.y += c.y; c0.z += c.z; c0.w += c.w;
-                                c1.x += d.x; c1.y += d.y; c1.z += d.z; c1.w += d.w;
-                            }
-                        }
-                        return make_float4(silu_times(c0.x, c0.y), silu_times(c0.z, c0.w), silu_times(c1.x, c1.y),
-                                           silu_times(c1.z, c1.w));
-                    });
+        const int sb = slice * w.per + w.ks, tok = g >> 1, pos = first + tok;
+        const bool have = w.team < w.teams && sb < w.nsb && tok < ntok;
+        const int64_t col = int64_t(sb) * 256 + 64 * t;
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!kDown || a.gu_slices == 1) {
+            const float* x = nullptr;
+            if (have)
+                x = kDown ? a.h + int64_t(pos) * p.ffn + col
+                          : p.x + int64_t(all ? tok : plan.order[pos] / p.top_k) * p.model + col;
+            make_act(act, lane, [&](int i) { return have ? reinterpret_cast<const float4*>(x)[i] : zero; });
+        } else {
+            const int64_t pairs = int64_t(p.tokens) * p.top_k;
+            make_act(act, lane, [&](int i) {
+                float4 c0 = zero, c1 = zero;
+                if (have) {
+                    for (int s = 0; s < a.gu_slices; ++s) {
+                        const float4* x = reinterpret_cast<const float4*>(a.h + ((s * pairs + pos) * p.ffn + col + 4 * i) * 2);
+                        const float4 c = x[0], d = x[1];
+                        c0.x += c.x; c0.y += c.y; c0.z += c.z; c0.w += c.w;
+                        c1.x += d.x; c1.y += d.y; c1.z += d.z; c1.w += d.w;
+                    }
                 }
-            }
+                return make_float4(silu_times(c0.x, c0.y), silu_times(c0.z, c0.w), silu_times(c1.x, c1.y),
+                                   silu_times(c1.z, c1.w));
+            });
         }
     }
 
     // The warp's partial sums of the tile at shared address st, to `mine`.
-    __device__ __forceinline__ void tile(uint32_t st, int subs, float* mine) {
+    __device__ __forceinline__ void tile(uint32_t st, float* mine) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const Place place(t);
-#pragma unroll
-        for (int u = 0; u < C::kSub; ++u) {
-            if (u > 0 && u >= subs) break;
-            // Rolled: with two super-blocks the instructions of a tile are many
-            // enough to be waited for.
 #pragma unroll 1
-            for (int m = 0; m < kRows; m += 16) {
-                const uint32_t ra = st + uint32_t(u * kBox + (m + g) * kBlk), rb = ra + 8 * kBlk;
-                const RowScale r0 = row_scale(lds128(ra), place), r1 = row_scale(lds128(rb), place);
-                // The low and the high nibbles apart, since the matrix instructions
-                // truncate each step of a sum (9.8e-7 -> 5e-7 of the result for one
-                // token).
-                float acc[NG][2][4];
+        for (int m = 0; m < kRows; m += 16) {
+            const uint32_t ra = st + uint32_t((m + g) * kBlk), rb = ra + 8 * kBlk;
+            const RowScale r0 = row_scale(lds128(ra), place), r1 = row_scale(lds128(rb), place);
+            // The low and the high nibbles apart, since the matrix instructions
+            // truncate each step of a sum (9.8e-7 -> 5e-7 of the result for one
+            // token).
+            float lo[4], hi[4], mn[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint4 c = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
-                    const uint4 d = lds128(rb + uint32_t(16 + 32 * t + 16 * half));
-                    const uint32_t w0[4] = {c.x, c.y, c.z, c.w}, w1[4] = {d.x, d.y, d.z, d.w};
+            for (int half = 0; half < 2; ++half) {
+                const uint4 c = lds128(ra + uint32_t(16 + 32 * t + 16 * half));
+                const uint4 d = lds128(rb + uint32_t(16 + 32 * t + 16 * half));
+                const uint32_t w0[4] = {c.x, c.y, c.z, c.w}, w1[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
-                        const uint32_t p0 = w0[i] >> 8, p1 = w1[i] >> 8;
-                        unpack_lo(w0[i], p0, r0, magic, x0, x2);
-                        unpack_lo(w1[i], p1, r1, magic, x1, x3);
-                        unpack_hi(w0[i], p0, r0, magic, y0, y2);
-                        unpack_hi(w1[i], p1, r1, magic, y1, y3);
-#pragma unroll
-                        for (int j = 0; j < NG; ++j) {
-                            const uint32_t* b = act[u][j].b[4 * half + i];
-                            if (half + i == 0) {
-                                mma16816_first(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
-                                mma16816_first(acc[j][1], y0, y1, y2, y3, b[2], b[3]);
-                            } else {
-                                mma16816(acc[j][0], x0, x1, x2, x3, b[0], b[1]);
-                                mma16816(acc[j][1], y0, y1, y2, y3, b[2], b[3]);
-                            }
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+                    const uint32_t p0 = w0[i] >> 8, p1 = w1[i] >> 8;
+                    unpack_lo(w0[i], p0, r0, magic, x0, x2);
+                    unpack_lo(w1[i], p1, r1, magic, x1, x3);
+                    unpack_hi(w0[i], p0, r0, magic, y0, y2);
+                    unpack_hi(w1[i], p1, r1, magic, y1, y3);
+                    const uint32_t* b = act.b[4 * half + i];
+                    if (half + i == 0) {
+                        mma16816_first(lo, x0, x1, x2, x3, b[0], b[1]);
+                        mma16816_first(hi, y0, y1, y2, y3, b[2], b[3]);
+                    } else {
+                        mma16816(lo, x0, x1, x2, x3, b[0], b[1]);
+                        mma16816(hi, y0, y1, y2, y3, b[2], b[3]);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    float mn[4];
-                    mma1688(mn, r0.m, r1.m, act[u][j].sums);
-                    const float s0 = (acc[j][0][0] + acc[j][1][0]) + (acc[j][0][1] + acc[j][1][1]);
-                    const float s1 = (acc[j][0][2] + acc[j][1][2]) + (acc[j][0][3] + acc[j][1][3]);
-                    const float v0 = act[u][j].up * (r0.d * s0 - r0.dmin * (mn[0] + mn[1]));
-                    const float v1 = act[u][j].up * (r1.d * s1 - r1.dmin * (mn[2] + mn[3]));
-                    float* out = mine + (4 * j + t) * kRedPitch + m + g;
-                    out[0] = u == 0 ? v0 : out[0] + v0;
-                    out[8] = u == 0 ? v1 : out[8] + v1;
-                }
             }
+            mma1688(mn, r0.m, r1.m, act.sums);
+            const float s0 = (lo[0] + hi[0]) + (lo[1] + hi[1]), s1 = (lo[2] + hi[2]) + (lo[3] + hi[3]);
+            mine[t * kRedPitch + m + g] = act.up * (r0.d * s0 - r0.dmin * (mn[0] + mn[1]));
+            mine[t * kRedPitch + m + g + 8] = act.up * (r1.d * s1 - r1.dmin * (mn[2] + mn[3]));
         }
     }
 
@@ -621,7 +579,7 @@ struct Layer {
     };
     // One warp: two rows of one token per lane and step, the team's warps in order.
     template <bool kDown>
-    __device__ __forceinline__ bool add(const Product<NG>& w, const Batch& d, bool all) {
+    __device__ __forceinline__ bool add(const Product& w, const Batch& d, bool all) {
         const mmq_q4K_moe_t& p = a.p;
         const int lane = threadIdx.x & 31;
         if (!__all_sync(0xffffffffu, wait_bounded(d.full, d.phase, abort_flag, a.status))) return false;
@@ -633,11 +591,11 @@ struct Layer {
             static_assert(kBatch == 2, "a team's first or second tile");
             for (int tok = lane / kLanes; tok < d.ntok; tok += 32 / kLanes) {
                 const int pos = d.first + tok, col = all ? plan.order[pos] / p.top_k : tok;
-                const float* from = d.red + (nb * C::kWarps + tm * w.crew) * C::kPart + col * kRedPitch + r;
+                const float* from = d.red + (nb * kWarps + tm * w.per) * kPart + col * kRedPitch + r;
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll 8
-                for (int v = 0; v * C::kSub < d.held; ++v) {
-                    const float2 f = *reinterpret_cast<const float2*>(from + v * C::kPart);
+                for (int v = 0; v < d.held; ++v) {
+                    const float2 f = *reinterpret_cast<const float2*>(from + v * kPart);
                     s0 += f.x;
                     s1 += f.y;
                 }
@@ -656,35 +614,35 @@ struct Layer {
     }
 
     template <bool kDown>
-    __device__ __forceinline__ void go(Product<NG>& w) {
+    __device__ __forceinline__ void go(Product& w) {
         const mmq_q4K_moe_t& p = a.p;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         // Few tokens in all: every expert gets the columns of all of them
         // (which the matrix instructions have room for anyway), made once.
-        const bool all = !kDown && p.tokens <= C::kTok && w.slices == 1;
+        const bool all = !kDown && p.tokens <= kTok && w.slices == 1;
         if (all) fill<kDown>(w, 0, 0, p.tokens, true);
         Batch due = {};
         int wait = 0;   // batches until this warp adds `due` up
         for (; w.run.left > 0; w.run.next(plan, w.slices, w.tiles)) {
             const Run& run = w.run;
-            const int first = plan.start[run.a] + run.pass * C::kTok;
-            const int ntok = min(C::kTok, plan.start[run.a + 1] - first);
+            const int first = plan.start[run.a] + run.pass * kTok;
+            const int ntok = min(kTok, plan.start[run.a + 1] - first);
             const int held = min(w.per, w.nsb - run.slice * w.per);   // super-blocks of this slice
-            const int subs = w.team < w.teams ? min(C::kSub, held - w.ks) : 0;
+            const bool works = w.team < w.teams && w.ks < held;
             if (!all) fill<kDown>(w, run.slice, first, ntok, false);
             for (int j0 = 0; j0 < run.count; j0 += kBatch * w.teams) {
-                float* const red = red0 + buffer * (C::kRed / 4);
+                float* const red = red0 + buffer * (kRed / 4);
                 // The buffer's last batch has been added up (at first: passes at once).
                 if (!__all_sync(0xffffffffu, wait_bounded(red_empty + 8u * uint32_t(buffer), red_phase ^ 1u, abort_flag, a.status)))
                     return;
 #pragma unroll 1
                 for (int nb = 0; nb < kBatch; ++nb) {
-                    if (subs <= 0 || j0 + nb * w.teams + w.team >= run.count) break;
+                    if (!works || j0 + nb * w.teams + w.team >= run.count) break;
                     if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8u * uint32_t(out_stage), out_phase, abort_flag, a.status)))
                         return;
-                    float* const mine = red + (nb * C::kWarps + warp) * C::kPart;
-                    const uint32_t st = ring + uint32_t(out_stage * C::kTile);
-                    tile(st, subs, mine);
+                    float* const mine = red + (nb * kWarps + warp) * kPart;
+                    const uint32_t st = ring + uint32_t(out_stage * kTile);
+                    tile(st, mine);
                     // The stores depend on every load from the stage, so those
                     // are done in every lane: the next copy may land in it.
                     __syncwarp();
@@ -706,8 +664,8 @@ struct Layer {
                 } else if (wait > 0 && --wait == 0) {
                     if (!add<kDown>(w, due, all)) return;
                 }
-                if (++turn == C::kWarps) turn = 0;
-                if (++buffer == C::kBuffers) {
+                if (++turn == kWarps) turn = 0;
+                if (++buffer == kBuffers) {
                     buffer = 0;
                     red_phase ^= 1u;
                 }
@@ -730,10 +688,10 @@ struct Layer {
 };
 
 // One product of all active experts, one CTA per SM.  Activations are
-// stationary: a warp keeps the operand of its super-blocks for 4 NG tokens in
-// registers and streams weight tiles of those through a ring of its own; the
-// warps of a team hold the super-blocks of a row (or of a slice of at most 16
-// of it), so a team reads whole rows.  The partial sums of a batch (two
+// stationary: a warp keeps the operand of one super-block for four tokens in
+// registers and streams weight tiles of it through a ring of its own; the warps
+// of a team hold the super-blocks of a row (or of a slice of at most 16 of it),
+// so a team reads whole rows.  The partial sums of a batch (two
 // tiles per team) meet in shared memory: the warps take turns to add a batch up, in
 // a fixed order, and store it, each a batch after its own tiles of it, when
 // the others have long finished theirs.  (Adding at once makes every warp
@@ -744,27 +702,25 @@ struct Layer {
 //
 // Every CTA makes the plan from the logits.  The second product does so, and
 // asks for its first weights, before it waits for the first one's results.
-template <int NG, bool kDown>
-__global__ void __launch_bounds__(Cfg<NG>::kThreads, 1)
+template <bool kDown>
+__global__ void __launch_bounds__(kThreads, 1)
 moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, const MoeArgs a) {
-    using C = Cfg<NG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ Plan plan;
     __shared__ PlanScratch scratch;
-    __shared__ uint64_t bars[C::kWarps * kStages + 2 * C::kBuffers];
+    __shared__ uint64_t bars[kWarps * kStages + 2 * kBuffers];
     __shared__ uint32_t abort_word;
     __shared__ int start_at;
-    const mmq_q4K_moe_t& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Layer<NG> layer{a, plan, AbortFlag{smem_u32(&abort_word)}, smem_u32(&bars[warp * kStages]),
-                    smem_u32(&bars[C::kWarps * kStages]), smem_u32(&bars[C::kWarps * kStages + C::kBuffers]),
-                    smem_u32(smem) + uint32_t(warp * kStages * C::kTile), reinterpret_cast<float*>(smem + C::kRing)};
+    Layer layer{a, plan, AbortFlag{smem_u32(&abort_word)}, smem_u32(&bars[warp * kStages]),
+                    smem_u32(&bars[kWarps * kStages]), smem_u32(&bars[kWarps * kStages + kBuffers]),
+                    smem_u32(smem) + uint32_t(warp * kStages * kTile), reinterpret_cast<float*>(smem + kRing)};
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(layer.magic));
     if (threadIdx.x == 0) {
         layer.abort_flag.set(0u);
-        for (int i = 0; i < C::kBuffers; ++i) {
-            mbar_init(layer.red_full + 8u * uint32_t(i), C::kWarps);
+        for (int i = 0; i < kBuffers; ++i) {
+            mbar_init(layer.red_full + 8u * uint32_t(i), kWarps);
             mbar_init(layer.red_empty + 8u * uint32_t(i), 1);
         }
         prefetch_tmap(&map);
@@ -777,11 +733,11 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, c
     // lets it be scheduled only after its own wait for the router.
     if (!kDown) griddep_wait();
     griddep_launch_dependents();
-    make_plan<C::kThreads>(a, &plan, &scratch, C::kTok, !kDown && blockIdx.x == 0);
-    Product<NG> w(&map, shape, plan, &start_at);
+    make_plan(a, &plan, &scratch, !kDown && blockIdx.x == 0);
+    Product w(&map, shape, plan, &start_at);
     layer.start(w);
     if (kDown) griddep_wait();   // the first product
-    layer.template go<kDown>(w);
+    layer.go<kDown>(w);
     layer.drain();
 }
 
@@ -828,7 +784,7 @@ cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_
 }
 
 // A row's super-blocks in slices of at most 16.
-int slices_of(int inner) { return (inner / 256 + kSliceSb - 1) / kSliceSb; }
+int slices_of(int inner) { return (inner / 256 + kWarps - 1) / kWarps; }
 
 struct Sizes {
     size_t logits, h, y, bytes;
@@ -845,7 +801,7 @@ Sizes sizes(const mmq_q4K_moe_t& p) {
     return z;
 }
 
-template <int NG, bool kDown>
+template <bool kDown>
 cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
     const int rows = kDown ? a.p.model : 2 * a.p.ffn;
     Shape shape;
@@ -853,21 +809,19 @@ cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
     shape.nsb = (kDown ? a.p.ffn : a.p.model) / 256;
     shape.slices = kDown ? a.down_slices : a.gu_slices;
     shape.per = (shape.nsb + shape.slices - 1) / shape.slices;
-    shape.crew = (shape.per + Cfg<NG>::kSub - 1) / Cfg<NG>::kSub;
-    shape.teams = Cfg<NG>::kWarps / shape.crew;
+    shape.teams = kWarps / shape.per;
     shape.tiles = rows / kRows;
     const uint64_t pitch = uint64_t(shape.nsb) * kBlk;
     CUtensorMap map;
     if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
                    uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
-    constexpr int smem = Cfg<NG>::kBytes;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(moe_product_kernel<NG, kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+    if ((e = cudaFuncSetAttribute(moe_product_kernel<kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)))
         return e;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(Cfg<NG>::kThreads), smem, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_product_kernel<NG, kDown>, map, shape, a);
+    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(kThreads), kSmemBytes, s, attr);
+    return cudaLaunchKernelEx(&cfg, moe_product_kernel<kDown>, map, shape, a);
 }
 
 }  // namespace
@@ -894,13 +848,8 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     const cudaLaunchConfig_t first = launch_config(dim3(unsigned(p.experts), unsigned((p.tokens + 3) / 4)),
                                                    dim3(kRouterThreads), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
-    // Four tokens at a time where an expert gets few on average, else eight: a
-    // pass of eight costs less than two of four, but more than one (16 tokens, 6
-    // of 64 experts each: 162 us by fours, 234 us for the first product alone by
-    // eights; 32 tokens, 2 of 8: 290 us by eights, 2947 us by fours at first).
-    const bool few = p.tokens <= 4 || p.tokens * p.top_k <= 2 * p.experts;
-    if ((e = few ? launch_product<1, false>(a, nsm, s) : launch_product<2, false>(a, nsm, s))) return e;
-    if ((e = few ? launch_product<1, true>(a, nsm, s) : launch_product<2, true>(a, nsm, s))) return e;
+    if ((e = launch_product<false>(a, nsm, s))) return e;
+    if ((e = launch_product<true>(a, nsm, s))) return e;
     cudaLaunchAttribute last_attr[1];
     const cudaLaunchConfig_t last =
         follow_config(dim3(unsigned((p.model / 4 + 127) / 128), unsigned(p.tokens)), dim3(128), 0, s, last_attr);
