@@ -63,11 +63,10 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// ------------------------------------------------------- few rows per key
+// ----------------------------------------------------------------- suffix
 // One warp, a CTA of its own: up to 16 rows that see the same keys (a token's
-// heads of one kv head over a part of its suffix; or any 16 rows over a part
-// of the prefix).  Bound by the key / value bytes: rows are padded to the 16 of
-// one mma.sync tile, keys come 16 at a time through a cp.async ring of three
+// heads of one kv head, over a part of its suffix).  Bound by the key / value
+// bytes: rows are padded to the 16 of one mma.sync tile, keys come 16 at a time through a cp.async ring of three
 // (24 KB at 128 dims, nine such warps per SM: up to 144 KB in flight), and
 // warps that start, stream and finish on their own keep the memory busy where
 // suffixes are short.  Keys past the row's limit are filled with zeros, not
@@ -86,56 +85,38 @@ template <int D>
 constexpr int row_resident() {   // warps per SM that the launch plans for
     return D == 128 ? 9 : 14;
 }
-enum class Keys { kPrefix, kPages, kSmallPages };   // kPages: pages of 16 and more, a slab lies on one
 
-template <typename T, int D, Keys kKeys>
-__global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const AttnArgs a) {
+template <typename T, int D, bool kSmallPages>   // small: less than a slab, which else lies on one page
+__global__ void __launch_bounds__(32, row_resident<D>()) attn_suffix_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const mmq_shared_prefix_attention_t& p = a.p;
     T* const tag = nullptr;
-    if (kKeys == Keys::kPrefix) {
-        griddep_wait();
-        griddep_launch_dependents();
-    } else if (!a.beside) {
-        griddep_wait();
-    }
+    if (!a.beside) griddep_wait();
     // Beside a prefix kernel, which was launched (and has seen to it that what
     // precedes the call is complete) but need not have ended: only the last CTA
     // waits for it, at its end, so that this grid's end is also the prefix
     // kernel's for the join.  A wait in every CTA would hold their SMs' room.
-    const bool last = kKeys != Keys::kPrefix && a.beside && blockIdx.x == gridDim.x - 1 &&
+    const bool last = a.beside && blockIdx.x == gridDim.x - 1 &&
                       blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
     const int lane = threadIdx.x;
     const int h = blockIdx.y, G = a.group;
     const int tiles_per_token = (G + 15) / 16;
 
     // Rows [r0, r1) and keys [k0, k1) of this warp.
-    int64_t r0, r1, k0, k1;
-    int part = blockIdx.z;
-    const int32_t* pages = nullptr;
-    if (kKeys == Keys::kPrefix) {
-        r0 = int64_t(blockIdx.x) * 16;
-        r1 = min(r0 + 16, a.tokens * G);
-        k0 = part * a.part_keys;
-        k1 = min(k0 + a.part_keys, p.prefix);
-    } else {
-        const int t = int(blockIdx.x) / tiles_per_token, tile = int(blockIdx.x) - t * tiles_per_token;
-        const int b = t / p.q_len;
-        r0 = int64_t(t) * G + tile * 16;
-        r1 = min(r0 + 16, int64_t(t) * G + G);
-        pages = p.page_table + b * p.table_width;
-        const int64_t room = p.table_width << a.page_shift;
-        int64_t len = p.lens[b];
-        if (len > room) {
-            if (lane == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
-            len = room;
-        }
-        len = max(int64_t(0), len - p.q_len + 1 + (t - b * p.q_len));
-        const int64_t step = ((len + a.suffix_parts - 1) / a.suffix_parts + 63) & ~int64_t(63);
-        k0 = min(part * step, len);
-        k1 = min(k0 + step, len);
-        part += a.prefix_parts;
+    const int t = int(blockIdx.x) / tiles_per_token, tile = int(blockIdx.x) - t * tiles_per_token;
+    const int b = t / p.q_len;
+    const int64_t r0 = int64_t(t) * G + tile * 16, r1 = min(r0 + 16, int64_t(t) * G + G);
+    const int32_t* pages = p.page_table + b * p.table_width;
+    const int64_t room = p.table_width << a.page_shift;
+    int64_t len = p.lens[b];
+    if (len > room) {
+        if (lane == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+        len = room;
     }
+    len = max(int64_t(0), len - p.q_len + 1 + (t - b * p.q_len));
+    const int64_t share = ((len + a.suffix_parts - 1) / a.suffix_parts + 63) & ~int64_t(63);
+    const int64_t k0 = min(int64_t(blockIdx.z) * share, len), k1 = min(k0 + share, len);
+    const int part = a.prefix_parts + int(blockIdx.z);
     const int64_t part_row = int64_t(part) * a.tokens;
     const int grow = lane >> 2, gcol = lane & 3;
     auto token_head = [&](int64_t r) {   // row r's place among [tokens][heads]
@@ -156,12 +137,12 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
     const int slabs = int((k1 - k0 + kSlab - 1) / kSlab);
     bool bad_page = false;
 
-    const T* const keys = static_cast<const T*>(kKeys == Keys::kPrefix ? p.k_prefix : p.k_cache);
-    const T* const values = static_cast<const T*>(kKeys == Keys::kPrefix ? p.v_prefix : p.v_cache);
-    const int64_t step = kKeys == Keys::kPrefix ? p.prefix_token_stride : int64_t(p.kv_heads) * D;   // from key to key
-    const int64_t head = h * (kKeys == Keys::kPrefix ? p.prefix_head_stride : int64_t(D)) + (lane % kChunks) * 8;
+    const T* const keys = static_cast<const T*>(p.k_cache);
+    const T* const values = static_cast<const T*>(p.v_cache);
+    const int64_t step = int64_t(p.kv_heads) * D;   // from key to key
+    const int64_t head = int64_t(h) * D + (lane % kChunks) * 8;
     const int64_t in_page = (int64_t(1) << a.page_shift) - 1;
-    int32_t next_id = kKeys == Keys::kPages ? pages[k0 >> a.page_shift] : 0;   // the next slab's page
+    int32_t next_id = kSmallPages ? 0 : pages[k0 >> a.page_shift];   // the next slab's page
 
     // Slab i's rows: kRowsAtOnce rows of 16-byte chunks per instruction, chunk
     // c of row r at c ^ (r & 7) (conflict-free for ldmatrix).
@@ -169,7 +150,7 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
         const int64_t first = k0 + int64_t(i) * kSlab;
         int left = int(min(k1 - first, int64_t(kSlab)));   // rows to read
         int64_t at = first;                                 // the first row's place in the cache
-        if (kKeys == Keys::kPages) {
+        if (!kSmallPages) {
             const int32_t id = next_id;
             if (id < 0 || id >= p.n_pages) {
                 bad_page = true;
@@ -185,7 +166,7 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_rows_kernel(const 
             const int r = j * kRowsAtOnce + lane / kChunks;
             bool valid = r < left;
             int64_t row = at + r;
-            if (kKeys == Keys::kSmallPages && valid) {
+            if (kSmallPages && valid) {
                 const int32_t id = pages[(first + r) >> a.page_shift];
                 if (id < 0 || id >= p.n_pages) {
                     bad_page = true;
@@ -433,23 +414,31 @@ int split(int64_t units, int64_t keys, int64_t slots, int64_t least) {
     return int(n < 1 ? 1 : n);
 }
 
-// Parts of the prefix for the tensor-core kernel: `units` row blocks over
-// `tiles` key tiles each, one CTA per SM.  Estimated in key tiles (about 1.7 us
-// each with two row tiles): a CTA's item costs its tiles and about four more
-// for its queries, first scores and results, a part costs the join a little,
-// and the suffix kernel, which follows but starts on the SMs that have no
-// item, reads about 140 KB per tile's time and SM there and 60 KB per SM with
-// all of them.
-int64_t tc_parts(int64_t units, int64_t tiles, int64_t nsm, double suffix_bytes) {
+// The prefix kernel's row tiles per CTA: two, one of them empty for up to 128
+// rows, but for few rows one, the two groups taking key tiles in turn.  (8192
+// keys of 8 kv heads x 128: 32 rows 15.2 us with one, 15.7 with two; 64 rows
+// 17.6 and 16.9; 128 rows 23.9 and 20.7, where twice as many parts and twice the
+// bytes per time cost more than the empty tile; 24 rows, 4096 keys of 32 kv heads x
+// 64: 17.1 and 20.2.)
+int prefix_tiles(int64_t rows) { return rows <= 48 ? 1 : 2; }
+
+// And its parts: `units` row blocks over `keys` key tiles each.  Estimated in
+// units of 1.7 us, the time of a key tile for two row tiles: with one it is half
+// of that; every item takes about four more for its queries, first scores and
+// results; the kernel writes and the join reads `part` bytes per part, 6.8 MB per
+// unit; and the suffix kernel, which follows but starts on the SMs that have no
+// item, reads about 140 KB per unit and SM there and 60 KB per SM with all.
+// (256 sequences, 1024 rows per kv head x 16384 keys: 122 us with 2 parts, 104 with
+// the 3 this gives, 113 with 4.)
+int64_t prefix_parts(int tiles, int64_t units, int64_t keys, int64_t nsm, double part, double suffix) {
     int64_t best = 1;
     double least = 1e300;
-    for (int64_t n = 1; n <= tiles && n <= 64; ++n) {
-        const int64_t rounds = (units * n + nsm - 1) / nsm, each = (tiles + n - 1) / n;
-        const double prefix = double(rounds * (each + 4));
+    for (int64_t n = 1; n <= keys && n <= 64; ++n) {
+        const int64_t rounds = (units * n + nsm - 1) / nsm, each = (keys + n - 1) / n;
+        const double prefix = double(rounds) * (double(tiles == 2 ? each : (each + 1) / 2) + 4.);
         const double idle = rounds == 1 ? double(nsm - units * n) : 0.;
-        double left = suffix_bytes - idle * prefix * 140e3;
-        if (left < 0.) left = 0.;
-        const double cost = prefix + left / (double(nsm) * 60e3) + 0.25 * double(n);
+        const double left = suffix - idle * prefix * 140e3;
+        const double cost = prefix + (left > 0. ? left / (double(nsm) * 60e3) : 0.) + part * double(n) / 6.8e6;
         if (cost < least) {
             least = cost;
             best = n;
@@ -466,24 +455,21 @@ void plan(AttnArgs& a, int nsm) {
     a.beside = p.prefix > 0;
     a.page_shift = 0;
     while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
-    const int64_t rows = a.tokens * a.group;
     const int64_t slots = int64_t(nsm) * (p.head_dim == 128 ? row_resident<128>() : row_resident<64>());
-    a.prefix_tiles = rows <= 16 ? 0 : rows <= 128 ? 1 : 2;
+    a.prefix_tiles = 0;
     a.prefix_parts = 0;
     a.part_keys = 0;
     if (p.prefix > 0) {
-        const int64_t tile = a.prefix_tiles ? 128 : 64;
-        int64_t n;
-        if (a.prefix_tiles) {
-            const int64_t units = (rows + 128 * a.prefix_tiles - 1) / (128 * a.prefix_tiles) * p.kv_heads;
-            // on average a suffix fills half of its pages
-            const double suffix = 2. * double(a.tokens) * double(p.table_width << a.page_shift) * p.kv_heads * p.head_dim;
-            n = tc_parts(units, (p.prefix + tile - 1) / tile, nsm, suffix);
-        } else {
-            n = split((rows + 15) / 16 * p.kv_heads, p.prefix, slots, 64);
-        }
-        a.part_keys = ((p.prefix + n - 1) / n + tile - 1) / tile * tile;
-        a.prefix_parts = int((p.prefix + a.part_keys - 1) / a.part_keys) * (a.prefix_tiles == 1 ? 2 : 1);
+        const int64_t rows = a.tokens * a.group;
+        a.prefix_tiles = prefix_tiles(rows);
+        const int per_item = a.prefix_tiles == 1 ? 2 : 1;   // parts
+        // on average a suffix fills half of its pages
+        const double suffix = 2. * double(a.tokens) * double(p.table_width << a.page_shift) * p.kv_heads * p.head_dim;
+        const double part = 8. * double(a.tokens) * p.heads * p.head_dim * per_item;   // written and read
+        const int64_t n = prefix_parts(a.prefix_tiles, (rows + 128 * a.prefix_tiles - 1) / (128 * a.prefix_tiles) * p.kv_heads,
+                                       (p.prefix + 127) / 128, nsm, part, suffix);
+        a.part_keys = ((p.prefix + n - 1) / n + 127) / 128 * 128;
+        a.prefix_parts = int((p.prefix + a.part_keys - 1) / a.part_keys) * per_item;
     }
     // ragged suffixes: several warps per slot, so that the longest do not end last alone
     a.suffix_parts = split(a.tokens * ((a.group + 15) / 16) * p.kv_heads, p.table_width << a.page_shift, 3 * slots, 64);
@@ -505,16 +491,12 @@ cudaError_t launch(const AttnArgs& a, int nsm, cudaStream_t s) {
         return f ? mmq::launch_config(grid, block, smem, s, attr) : follow_config(grid, block, smem, s, attr);
     };
     constexpr int smem = row_smem<D>();
-    if (a.prefix_parts && a.prefix_tiles) {
+    if (a.prefix_parts) {
         const cudaLaunchConfig_t cfg = config(dim3(1), dim3(1), 0);
         if ((e = mmq::launch_attention_prefix(a, nsm, cfg))) return e;
-    } else if (a.prefix_parts) {
-        const dim3 grid(unsigned((a.tokens * a.group + 15) / 16), unsigned(a.p.kv_heads), unsigned(a.prefix_parts));
-        const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
-        if ((e = cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, D, Keys::kPrefix>, a))) return e;
     }
     if (a.suffix_parts) {
-        auto* kernel = a.p.page_size >= kSlab ? attn_rows_kernel<T, D, Keys::kPages> : attn_rows_kernel<T, D, Keys::kSmallPages>;
+        auto* kernel = a.p.page_size >= kSlab ? attn_suffix_kernel<T, D, false> : attn_suffix_kernel<T, D, true>;
         const dim3 grid(unsigned(a.tokens * ((a.group + 15) / 16)), unsigned(a.p.kv_heads), unsigned(a.suffix_parts));
         const cudaLaunchConfig_t cfg = config(grid, dim3(32), smem);
         if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;

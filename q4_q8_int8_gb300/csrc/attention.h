@@ -20,7 +20,7 @@ struct AttnArgs {
     int* status;
     int64_t tokens;       // batch * q_len
     int group;            // heads per kv head
-    int prefix_tiles;     // 128-row tiles per CTA of the tensor-core prefix kernel; 0: the few-row kernel
+    int prefix_tiles;     // the prefix kernel's 128-row tiles per CTA
     int prefix_parts;     // parts 0 .. prefix_parts - 1
     int64_t part_keys;    // prefix keys per part, a multiple of the kernel's key tile
     int suffix_parts;     // the parts after them
