@@ -68,7 +68,7 @@ static_assert(kSmemBytes <= 212 * 1024, "shared memory budget");
 
 // Which tokens go to which expert: pair i = token i / top_k, its i % top_k-th
 // expert.  An active expert (one with a token) has its pairs in a row of
-// `order`, and one pass over its weights per kTok of them.
+// `order`, and one pass over its weights per 4 of them (16 in the wide form).
 struct Plan {
     int active;
     int expert[kMaxExperts];
@@ -82,6 +82,7 @@ struct MoeArgs {
     float* logits;       // [tokens][experts]
     float* h;            // first product, rows in the plan's order: h [pairs][ffn], or if its sum is in
                          // parts [gu_slices][pairs][2 ffn] of gate and up, alternating
+    float* parts;        // wide form: first product [gu_slices][pairs][2 ffn], gate and up alternating
     float* y;            // second product [down_slices][pairs][model], rows by pair
     int gu_slices, down_slices;
     int* status;
@@ -206,17 +207,18 @@ struct PlanScratch {
     int totals[3][kMaxExperts / 32];
 };
 
-// Fill `plan` (shared memory) from the logits; `store`: also the chosen
-// experts and their weights to the caller.
+// Fill `plan` (shared memory) from the logits, a pass for every tok tokens of
+// an expert; `store`: also the chosen experts and their weights to the caller.
+template <int threads, int tok>
 __device__ __forceinline__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, bool store) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
-    static_assert(kMaxExperts <= kThreads && kMaxTokens <= 64, "one thread per expert, one bit per token");
+    static_assert(kMaxExperts <= threads && kMaxTokens <= 64, "one thread per expert, one bit per token");
     if (e < kMaxExperts) z->tokens_of[e] = 0;
     __syncthreads();
-    for (int t = warp; t < a.p.tokens; t += kThreads / 32) choose(a, t, lane, z->ids, z->tokens_of, store);
+    for (int t = warp; t < a.p.tokens; t += threads / 32) choose(a, t, lane, z->ids, z->tokens_of, store);
     __syncthreads();
     uint64_t mine = e < kMaxExperts ? z->tokens_of[e] : 0;
-    const int n = __popcll(mine), passes = (n + kTok - 1) / kTok;
+    const int n = __popcll(mine), passes = (n + tok - 1) / tok;
     // prefixes over the experts: of their pairs, their passes, and the active ones
     int pairs = n, pass = passes;
 #pragma unroll
@@ -410,6 +412,28 @@ struct Run {
     }
 };
 
+// The first run of a CTA's share: equal consecutive parts of all passes' tiles,
+// the first `more` one longer.  start_at: a word of shared memory.
+__device__ __forceinline__ Run first_run(const Plan& plan, int slices, int tiles, int* start_at) {
+    const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
+    const uint32_t mine = total / gridDim.x, more = total - mine * gridDim.x;
+    const uint32_t i0 = blockIdx.x * mine + min(blockIdx.x, more), i1 = i0 + mine + (blockIdx.x < more ? 1u : 0u);
+    const int p0 = int(i0 / each);
+    if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
+        *start_at = threadIdx.x;
+    __syncthreads();
+    Run run;
+    run.left = int(i1 - i0);
+    run.a = run.left > 0 ? *start_at : 0;
+    const int passes = plan.pass[run.a + 1] - plan.pass[run.a];
+    const int local = run.left > 0 ? int(i0) - plan.pass[run.a] * int(each) : 0, sp = local / tiles;
+    run.first = local - sp * tiles;
+    run.slice = sp / passes;
+    run.pass = sp - run.slice * passes;
+    run.count = min(tiles - run.first, run.left);
+    return run;
+}
+
 // The shape of one product.
 struct Shape {
     int rows, nsb, slices, per, teams, tiles;   // per: super-blocks of a slice and warps of a team
@@ -429,22 +453,7 @@ struct Product : Shape {
         const int warp = threadIdx.x >> 5;
         team = warp / per;
         ks = warp - team * per;
-        // equal consecutive parts of all passes' tiles, the first `more` one longer
-        const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
-        const uint32_t mine = total / gridDim.x, more = total - mine * gridDim.x;
-        const uint32_t i0 = blockIdx.x * mine + min(blockIdx.x, more), i1 = i0 + mine + (blockIdx.x < more ? 1u : 0u);
-        const int p0 = int(i0 / each);
-        if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
-            *start_at = threadIdx.x;
-        __syncthreads();
-        run.left = int(i1 - i0);
-        run.a = run.left > 0 ? *start_at : 0;
-        const int passes = plan.pass[run.a + 1] - plan.pass[run.a];
-        const int local = run.left > 0 ? int(i0) - plan.pass[run.a] * int(each) : 0, sp = local / tiles;
-        run.first = local - sp * tiles;
-        run.slice = sp / passes;
-        run.pass = sp - run.slice * passes;
-        run.count = min(tiles - run.first, run.left);
+        run = first_run(plan, slices, tiles, start_at);
         in = run;
         if (team >= teams) in.left = 0;
         enter(plan);
@@ -733,12 +742,383 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, c
     // lets it be scheduled only after its own wait for the router.
     if (!kDown) griddep_wait();
     griddep_launch_dependents();
-    make_plan(a, &plan, &scratch, !kDown && blockIdx.x == 0);
+    make_plan<kThreads, kTok>(a, &plan, &scratch, !kDown && blockIdx.x == 0);
     Product w(&map, shape, plan, &start_at);
     layer.start(w);
     if (kDown) griddep_wait();   // the first product
     layer.go<kDown>(w);
     layer.drain();
+}
+
+// ------------------------------------------------------------- many tokens
+// The same product where experts have many tokens: up to 16 of them per pass,
+// so that the weights are unpacked once for all, on tcgen05.
+//
+// A tile is 128 rows x one super-block.  Two groups of four warps take row
+// tiles in turn, thread = row: a thread turns its row's 144 bytes into 256
+// values sc q (and the eight minima m) in tensor memory, the A operand; B, in
+// shared memory, has a row per token's hi and one per its lo, K in the order in
+// which unpacking leaves the values; 16 + 1 products per super-block give
+// the row's sums for all tokens, which the thread reads back, scales and adds
+// up over the (at most four) super-blocks of a slice of the row.
+//   warps 0-3, 4-7  groups 0 and 1
+//   warp 8          TMA producer, a ring of tiles for both groups
+//   warps 9, 10     MMA issuers of groups 0 and 1
+constexpr int kWideTok = 16, kWideThreads = 384, kWideRows = 128, kWideStages = 7, kWideSlice = 4;
+constexpr int kWideTile = kWideRows * kBlk;
+constexpr int kWideN = 2 * kWideTok;                  // columns: tokens' hi, tokens' lo
+constexpr int kWidePanel = kWideN * 128;              // 64 k of all columns, 128-byte swizzle
+constexpr int kWideOffB = kWideStages * kWideTile;    // [kWideSlice][4] panels
+constexpr int kWideOffX = kWideOffB + kWideSlice * 4 * kWidePanel;   // sub-block sums: 16 k per super-block
+constexpr int kWideOffUp = kWideOffX + kWidePanel;    // float [kWideSlice][kWideTok]: 2^e
+constexpr int kWideOffTo = kWideOffUp + kWideSlice * kWideTok * 4;    // int [kWideTok]: a token's row of the result
+constexpr int kWideSmem = kWideOffTo + kWideTok * 4 + 1024;
+static_assert(kWideTile % 1024 == 0 && kWideSmem <= 208 * 1024, "shared memory layout");
+// Of a group's 256 columns: A from 0, the minima, the sums of the values of two
+// super-blocks in turn, the sums of the minima.
+constexpr uint32_t kWideColX = 128, kWideColS = 160, kWideColM = 224;
+
+template <bool kDown>
+__global__ void __launch_bounds__(kWideThreads, 1)
+moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, const MoeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ Plan plan;
+    __shared__ PlanScratch scratch;
+    __shared__ uint64_t bars[2 * kWideStages + 11];
+    __shared__ uint32_t abort_word, tmem_slot;
+    __shared__ int start_at;
+    const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+    auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty = [&](uint32_t s) { return bar0 + 8u * (kWideStages + s); };
+    auto a_full = [&](int g, int half) { return bar0 + 8u * uint32_t(2 * kWideStages + 2 * g + half); };
+    auto sums_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kWideStages + 4 + g); };
+    auto a_free = [&](int g) { return bar0 + 8u * uint32_t(2 * kWideStages + 6 + g); };   // its first half
+    const uint32_t b_full = bar0 + 8u * (2 * kWideStages + 8), b_empty = b_full + 8u, drain = b_full + 16u;
+    const AbortFlag abort_flag{smem_u32(&abort_word)};
+    int* const status = a.status;
+    const mmq_q4K_moe_t& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < kWideStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 4);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(a_full(g, 0), 4);
+            mbar_init(a_full(g, 1), 4);
+            mbar_init(a_free(g), 1);
+            mbar_init(sums_full(g), 1);
+        }
+        mbar_init(b_full, 8);
+        mbar_init(b_empty, 10);   // eight warps and the two issuers
+        mbar_init(drain, 2);
+        abort_flag.set(0u);
+        fence_barrier_init();
+        prefetch_tmap(&map);
+    }
+    __syncwarp();
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    // As in moe_product_kernel: the logits are complete before the second product starts.
+    if (!kDown) griddep_wait();
+    griddep_launch_dependents();
+    make_plan<kWideThreads, kWideTok>(a, &plan, &scratch, !kDown && blockIdx.x == 0);
+    Run run = first_run(plan, shape.slices, shape.tiles, &start_at);
+    auto held_of = [&](const Run& r) { return min(shape.per, shape.nsb - r.slice * shape.per); };
+    // Ring position of super-block s of the run's row tile u: the two groups'
+    // tiles in turn, an odd last one alone.
+    auto position = [&](uint32_t base, int u, int s, int count, int held) {
+        return base + uint32_t((u & ~1) * held + ((u | 1) < count ? 2 * s + (u & 1) : s));
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            uint32_t pos = 0;
+            auto load = [&](int x, int y) {
+                const uint32_t slot = pos % kWideStages, par = (pos / kWideStages) & 1u;
+                if (!wait_bounded(empty(slot), par ^ 1u, abort_flag, status)) return false;
+                mbar_arrive_expect_tx(full(slot), kWideTile);
+                tma_load_2d(sbase + slot * kWideTile, &map, full(slot), x, y);
+                ++pos;
+                return true;
+            };
+            for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
+                const int held = held_of(run);
+                const int y = plan.expert[run.a] * shape.rows + run.first * kWideRows, x = run.slice * shape.per * kBlk;
+                for (int u = 0; u < run.count; u += 2)
+                    for (int s = 0; s < held; ++s)
+                        for (int v = u; v < min(u + 2, run.count); ++v)
+                            if (!load(x + s * kBlk, y + v * kWideRows)) goto producer_done;
+            }
+        producer_done:
+            for (uint32_t i = pos > kWideStages ? pos - kWideStages : 0; i < pos; ++i)
+                wait_drain(full(i % kWideStages), (i / kWideStages) & 1u, status);
+        }
+    } else if (warp == 9 || warp == 10) {
+        if (lane == 0) {
+            const int g = warp - 9;
+            const uint32_t t = tmem + 256u * uint32_t(g);
+            constexpr uint32_t id = idesc_f16_f32(kWideRows, kWideN);
+            const uint64_t b_desc = smem_desc_sw128(sbase + kWideOffB), x_desc = smem_desc_sw128(sbase + kWideOffX);
+            uint32_t run_phase = 0, phase = 0;
+            for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
+                const int held = held_of(run);
+                if (!wait_bounded(b_full, run_phase, abort_flag, status)) goto mma_done;
+                run_phase ^= 1u;
+                for (int u = g; u < run.count; u += 2)
+                    for (int s = 0; s < held; ++s) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (!wait_bounded(a_full(g, half), phase, abort_flag, status)) goto mma_done;
+                            tc_fence_after();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int k = 8 * half + i;   // 16 values each, a panel of 64
+                                mma_f16_ta(t + kWideColS + 32u * phase, t + 8u * uint32_t(k),
+                                           b_desc + uint64_t((s * 4 + (k >> 2)) * (kWidePanel >> 4) + (k & 3) * 2), id,
+                                           uint32_t(k > 0));
+                            }
+                            if (half == 0) mma_commit(a_free(g));
+                        }
+                        mma_f16_ta(t + kWideColM, t + kWideColX, x_desc + uint64_t(s * 2), id, 0u);
+                        mma_commit(sums_full(g));
+                        phase ^= 1u;
+                    }
+                mbar_arrive(b_empty);
+            }
+        mma_done:
+            mma_commit(drain);   // everything issued, also after a wait that ran out
+            wait_drain(drain, 0u, status);
+        }
+    } else if (warp < 8) {
+        const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t t = tmem + 256u * uint32_t(g) + (uint32_t((warp & 3) * 32) << 16);
+        float* const ups = reinterpret_cast<float*>(smem + kWideOffUp);
+        const int* const to = reinterpret_cast<const int*>(smem + kWideOffTo);
+        uint32_t run_phase = 0, tiles = 0, base = 0, magic;   // tiles: the group's, so far
+        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+        const int64_t pairs = int64_t(p.tokens) * p.top_k;
+        if (kDown) griddep_wait();   // the first product's h
+        for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
+            const int held = held_of(run);
+            const int first = plan.start[run.a] + run.pass * kWideTok;
+            const int ntok = min(kWideTok, plan.start[run.a + 1] - first);
+            // B: a warp per token and super-block, 8 consecutive values per lane.
+            if (!__all_sync(0xffffffffu, wait_bounded(b_empty, run_phase ^ 1u, abort_flag, status))) break;
+            // Two tokens of every super-block, all loads ahead.
+            float4 ahead[kWideSlice][2][2];
+#pragma unroll
+            for (int s = 0; s < kWideSlice; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int n = warp + 8 * j;
+                    ahead[s][j][0] = ahead[s][j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (s < held && n < ntok) {
+                        const int64_t col = int64_t(run.slice * shape.per + s) * 256 + 8 * lane;
+                        const float4* x = reinterpret_cast<const float4*>(
+                            kDown ? a.h + int64_t(first + n) * p.ffn + col
+                                  : p.x + int64_t(plan.order[first + n] / p.top_k) * p.model + col);
+                        ahead[s][j][0] = x[0];
+                        ahead[s][j][1] = x[1];
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < 2 * kWideSlice; ++i) {
+                const int s = i >> 1, n = warp + 8 * (i & 1);
+                if (s >= held) break;
+                const float4 c = ahead[s][i & 1][0], d = ahead[s][i & 1][1];
+                float v[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
+                const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // not negative: bits order as values
+                // 2^e with top 2^-e in [128, 256), e from -126 on
+                int e = int(bits >> 23) - 127 - 7;
+                e = e < -126 ? -126 : e;
+                const float down = __uint_as_float(uint32_t(127 - e) << 23);
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    v[k] *= down;
+                    sum += v[k];
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // elements 0 2, 1 3, 4 6, 5 7
+                    const int j = (k & 1) + 4 * (k >> 1);
+                    const __half2 h = __floats2half2_rn(v[j], v[j + 2]);
+                    const float2 back = __half22float2(h);
+                    hi[k] = h2u(h);
+                    lo[k] = h2u(__floats2half2_rn(v[j] - back.x, v[j + 2] - back.y));
+                }
+                const uint32_t panel = sbase + uint32_t(kWideOffB + (s * 4 + (lane >> 3)) * kWidePanel);
+                const uint32_t swizzled = uint32_t(((lane & 7) ^ (n & 7)) << 4);   // rows n and 16 + n alike
+                st_shared_v4(panel + uint32_t(n * 128) + swizzled, hi[0], hi[1], hi[2], hi[3]);
+                st_shared_v4(panel + uint32_t((kWideTok + n) * 128) + swizzled, lo[0], lo[1], lo[2], lo[3]);
+                // the eight sub-blocks' sums, and eight zeros
+                const __half2 h = __floats2half2_rn(sum, sum);
+                const __half2 l = __floats2half2_rn(sum - __low2float(h), 0.f);
+                uint8_t* const xs = smem + kWideOffX;
+                const int chunk = ((2 * s) ^ (n & 7)) << 4, zeros = ((2 * s + 1) ^ (n & 7)) << 4;
+                if ((lane & 3) == 0) {
+                    *reinterpret_cast<__half*>(xs + n * 128 + chunk + 2 * (lane >> 2)) = __low2half(h);
+                    *reinterpret_cast<__half*>(xs + (kWideTok + n) * 128 + chunk + 2 * (lane >> 2)) = __low2half(l);
+                } else if (lane < 3) {
+                    *reinterpret_cast<uint4*>(xs + (lane == 1 ? n : kWideTok + n) * 128 + zeros) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (lane == 0) ups[s * kWideTok + n] = __uint_as_float(uint32_t(127 + e) << 23);
+                if (s == 0 && lane == 0)
+                    reinterpret_cast<int*>(smem + kWideOffTo)[n] = !kDown ? first + n : n < ntok ? plan.order[first + n] : 0;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_full);
+            bool ok = __all_sync(0xffffffffu, wait_bounded(b_full, run_phase, abort_flag, status));
+            run_phase ^= 1u;
+            // The group's tiles one after the other; the sums of each are read
+            // between the halves of the next.
+            const int mine = (run.count + 1 - g) / 2 * held;
+            float acc[kWideTok];
+#pragma unroll
+            for (int k = 0; k < kWideTok; ++k) acc[k] = 0.f;
+            float2 scales = make_float2(0.f, 0.f);   // d, dmin of the tile before
+            for (int i = 0, u = g, s = 0, was_s = 0; ok && i <= mine; ++i) {
+                uint32_t at = 0, slot = 0;
+                __half2 sc[4];
+                uint4 head = make_uint4(0u, 0u, 0u, 0u);
+                // 64 values from two 16-byte loads: sub-blocks 2 j and 2 j + 1
+                auto unpack = [&](int j) {
+                    RowScale r;
+                    const __half2 high = __high2half2(sc[j]);
+                    r.s_lo = __low2half2(sc[j]);
+                    r.s_hi = __hmul2(high, u2h(0x2C002C00u));      // / 16
+                    r.b_lo = __hmul2(r.s_lo, u2h(0xE400E400u));    // * -1024
+                    r.b_hi = __hmul2(high, u2h(0xD400D400u));      // * -64
+                    const uint4 c = lds128(at + uint32_t(16 + 32 * j)), d = lds128(at + uint32_t(32 + 32 * j));
+                    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+                    uint32_t x[32];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t w8 = w[q] >> 8;
+                        unpack_lo(w[q], w8, r, magic, x[2 * q], x[2 * q + 1]);
+                        unpack_hi(w[q], w8, r, magic, x[16 + 2 * q], x[17 + 2 * q]);
+                    }
+                    tmem_st_32x32b_x32(t + 32u * uint32_t(j), x);
+                };
+                auto hand_over = [&](int half) {
+                    tmem_wait_st();   // and with the stores the loads that they depend on
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(a_full(g, half));
+                        if (half == 1) mbar_arrive(empty(slot));
+                    }
+                };
+                const __half2 k1024 = u2h(0x64006400u);
+                if (i < mine) {
+                    const uint32_t pos = position(base, u, s, run.count, held);
+                    slot = pos % kWideStages;
+                    at = sbase + slot * kWideTile + uint32_t(row * kBlk);
+                    ok = __all_sync(0xffffffffu, wait_bounded(full(slot), (pos / kWideStages) & 1u, abort_flag, status) &&
+                                                     (tiles == 0 || wait_bounded(a_free(g), (tiles - 1) & 1u, abort_flag, status)));
+                    if (!ok) break;
+                    head = lds128(at);
+                    const uint32_t sa = sc_lo4(head.y), sb = sc_hi4(head.y, head.w);
+                    sc[0] = __hsub2(u2h(prmt(sa, 0x64646464u, 0x4140u)), k1024);
+                    sc[1] = __hsub2(u2h(prmt(sa, 0x64646464u, 0x4342u)), k1024);
+                    sc[2] = __hsub2(u2h(prmt(sb, 0x64646464u, 0x4140u)), k1024);
+                    sc[3] = __hsub2(u2h(prmt(sb, 0x64646464u, 0x4342u)), k1024);
+                    tc_fence_after();
+                    unpack(0);
+                    unpack(1);
+                    hand_over(0);
+                }
+                if (i > 0) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(sums_full(g), (tiles - 1) & 1u, abort_flag, status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t sum[32], mn[32];
+                    tmem_ld_32x32b_x32(t + kWideColS + 32u * ((tiles - 1) & 1u), sum);
+                    tmem_ld_32x32b_x32(t + kWideColM, mn);
+                    tmem_wait_ld(sum);
+                    tmem_wait_ld(mn);
+#pragma unroll
+                    for (int k = 0; k < kWideTok; ++k) {
+                        auto of = [](uint32_t v) { return __uint_as_float(v); };
+                        acc[k] = fmaf(ups[was_s * kWideTok + k],
+                                      scales.x * (of(sum[k]) + of(sum[kWideTok + k])) - scales.y * (of(mn[k]) + of(mn[kWideTok + k])),
+                                      acc[k]);
+                    }
+                }
+                if (i < mine) {
+                    const uint32_t ma = m_lo4(head.z), mb = m_hi4(head.z, head.w);
+                    const uint32_t mins[8] = {h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4140u)), k1024)),
+                                              h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4342u)), k1024)),
+                                              h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4140u)), k1024)),
+                                              h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4342u)), k1024)), 0u, 0u, 0u, 0u};
+                    tmem_st_32x32b_x8(t + kWideColX, mins);
+                    unpack(2);
+                    unpack(3);
+                    hand_over(1);
+                    scales = __half22float2(u2h(head.x));
+                    ++tiles;
+                }
+                if (i > 0 && was_s == held - 1) {   // the row is complete; u is the next one by now
+                    const int was_u = i < mine ? u - 2 : u;
+                    const int64_t part = int64_t(run.slice) * pairs;
+                    float* const out = (kDown ? a.y : a.parts) + int64_t(run.first + was_u) * kWideRows + row;
+#pragma unroll
+                    for (int k = 0; k < kWideTok; ++k) {
+                        const int64_t to_row = part + to[k];
+                        if (k < ntok) out[to_row * shape.rows] = acc[k];
+                        acc[k] = 0.f;
+                    }
+                }
+                was_s = s;
+                if (i + 1 < mine && ++s == held) {
+                    s = 0;
+                    u += 2;
+                }
+            }
+            if (!ok) break;
+            base += uint32_t(run.count * held);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_empty);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// h = silu(gate) * up of the wide form, gate and up each a sum of parts; rows in the plan's order.
+__global__ void __launch_bounds__(256) moe_act_kernel(const MoeArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const mmq_q4K_moe_t& p = a.p;
+    const int f = (blockIdx.x * 256 + threadIdx.x) * 2;
+    if (f >= p.ffn) return;
+    const int64_t pairs = int64_t(p.tokens) * p.top_k;
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);   // gate, up, gate, up
+#pragma unroll 4
+    for (int s = 0; s < a.gu_slices; ++s) {
+        const float4 v = *reinterpret_cast<const float4*>(a.parts + ((s * pairs + blockIdx.y) * p.ffn + f) * 2);
+        c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+    }
+    *reinterpret_cast<float2*>(a.h + int64_t(blockIdx.y) * p.ffn + f) = make_float2(silu_times(c.x, c.y), silu_times(c.z, c.w));
 }
 
 // out = residual + the sum of the chosen experts' rows
@@ -783,45 +1163,55 @@ cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_
     return cfg;
 }
 
-// A row's super-blocks in slices of at most 16.
-int slices_of(int inner) { return (inner / 256 + kWarps - 1) / kWarps; }
+// The wide form, by what an expert gets on average.
+bool wide(const mmq_q4K_moe_t& p) { return p.tokens * p.top_k > 4 * p.experts; }
+
+// A row's super-blocks in slices of at most 16, or 4 in the wide form.
+int slices_of(const mmq_q4K_moe_t& p, int inner) {
+    const int most = wide(p) ? kWideSlice : kWarps;
+    return (inner / 256 + most - 1) / most;
+}
 
 struct Sizes {
-    size_t logits, h, y, bytes;
+    size_t logits, h, parts, y, bytes;
 };
 Sizes sizes(const mmq_q4K_moe_t& p) {
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
     Sizes z;
     const size_t pairs = size_t(p.tokens) * size_t(p.top_k);
-    const int gu = slices_of(p.model);
+    const size_t gu = size_t(slices_of(p, p.model)), h = pairs * size_t(p.ffn) * 4;
     z.logits = 0;
     z.h = z.logits + up(size_t(p.tokens) * size_t(p.experts) * 4);
-    z.y = z.h + up(pairs * size_t(p.ffn) * 4 * (gu > 1 ? 2 * size_t(gu) : 1));
-    z.bytes = z.y + size_t(slices_of(p.ffn)) * pairs * size_t(p.model) * 4;
+    z.parts = z.h + up(wide(p) || gu == 1 ? h : 2 * gu * h);
+    z.y = z.parts + (wide(p) ? up(2 * gu * h) : 0);
+    z.bytes = z.y + size_t(slices_of(p, p.ffn)) * pairs * size_t(p.model) * 4;
     return z;
 }
 
 template <bool kDown>
 cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
-    const int rows = kDown ? a.p.model : 2 * a.p.ffn;
+    const bool is_wide = wide(a.p);
+    const int rows = kDown ? a.p.model : 2 * a.p.ffn, tile_rows = is_wide ? kWideRows : kRows;
     Shape shape;
     shape.rows = rows;
     shape.nsb = (kDown ? a.p.ffn : a.p.model) / 256;
     shape.slices = kDown ? a.down_slices : a.gu_slices;
     shape.per = (shape.nsb + shape.slices - 1) / shape.slices;
     shape.teams = kWarps / shape.per;
-    shape.tiles = rows / kRows;
+    shape.tiles = rows / tile_rows;
     const uint64_t pitch = uint64_t(shape.nsb) * kBlk;
     CUtensorMap map;
     if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
-                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
+                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, uint32_t(tile_rows), CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
+    auto* const kernel = is_wide ? moe_wide_kernel<kDown> : moe_product_kernel<kDown>;
+    const int smem = is_wide ? kWideSmem : kSmemBytes;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(moe_product_kernel<kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)))
-        return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(kThreads), kSmemBytes, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_product_kernel<kDown>, map, shape, a);
+    const cudaLaunchConfig_t cfg =
+        follow_config(dim3(unsigned(nsm)), dim3(is_wide ? kWideThreads : kThreads), size_t(smem), s, attr);
+    return cudaLaunchKernelEx(&cfg, kernel, map, shape, a);
 }
 
 }  // namespace
@@ -840,15 +1230,22 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     a.p = p;
     a.logits = reinterpret_cast<float*>(ws + z.logits);
     a.h = reinterpret_cast<float*>(ws + z.h);
+    a.parts = reinterpret_cast<float*>(ws + z.parts);
     a.y = reinterpret_cast<float*>(ws + z.y);
-    a.gu_slices = slices_of(p.model);
-    a.down_slices = slices_of(p.ffn);
+    a.gu_slices = slices_of(p, p.model);
+    a.down_slices = slices_of(p, p.ffn);
     a.status = status;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t first = launch_config(dim3(unsigned(p.experts), unsigned((p.tokens + 3) / 4)),
                                                    dim3(kRouterThreads), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
     if ((e = launch_product<false>(a, nsm, s))) return e;
+    if (wide(p)) {
+        cudaLaunchAttribute act_attr[1];
+        const cudaLaunchConfig_t act = follow_config(dim3(unsigned((p.ffn / 2 + 255) / 256), unsigned(p.tokens * p.top_k)),
+                                                     dim3(256), 0, s, act_attr);
+        if ((e = cudaLaunchKernelEx(&act, moe_act_kernel, a))) return e;
+    }
     if ((e = launch_product<true>(a, nsm, s))) return e;
     cudaLaunchAttribute last_attr[1];
     const cudaLaunchConfig_t last =
