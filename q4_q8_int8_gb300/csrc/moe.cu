@@ -754,29 +754,35 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, c
 // The same product where experts have many tokens: up to 16 of them per pass,
 // so that the weights are unpacked once for all, on tcgen05.
 //
-// A tile is 128 rows x one super-block.  Two groups of four warps take row
-// tiles in turn, thread = row: a thread turns its row's 144 bytes into 256
-// values sc q (and the eight minima m) in tensor memory, the A operand; B, in
-// shared memory, has a row per token's hi and one per its lo, K in the order in
-// which unpacking leaves the values; 16 + 1 products per super-block give
-// the row's sums for all tokens, which the thread reads back, scales and adds
-// up over the (at most four) super-blocks of a slice of the row.
-//   warps 0-3, 4-7  groups 0 and 1
-//   warp 8          TMA producer, a ring of tiles for both groups
-//   warps 9, 10     MMA issuers of groups 0 and 1
-constexpr int kWideTok = 16, kWideThreads = 384, kWideRows = 128, kWideStages = 7, kWideSlice = 4;
+// A tile is 128 rows x one super-block.  Two groups of eight warps take row
+// tiles in turn, two threads per row, one for either half of the super-block:
+// a thread turns its share of the row's 144 bytes into 128 values sc q in
+// tensor memory, the A operand (and one of them adds the eight minima m, twice);
+// B, in shared memory, has a row per token's hi and one per its lo, K in the
+// order in which unpacking leaves the values; a second B has the sub-blocks'
+// sums, hi and lo one after the other.  16 + 1 products per super-block give
+// the row's sums for all tokens, which its two threads read back, eight tokens
+// each, scale and add up over the (at most four) super-blocks of a slice of the
+// row.  Values are unpacked while the products of the tile before run, into the
+// half of A that those are through with; sums are double.
+//   warps 0-7, 8-15  groups 0 and 1: four warps per half
+//   warp 16          TMA producer, a ring of tiles for both groups
+//   warps 17, 18     MMA issuers of groups 0 and 1 (a thread issues a product
+//                    every 45 cycles, whatever its width up to 64)
+constexpr int kWideTok = 16, kWideThreads = 19 * 32, kWideRows = 128, kWideStages = 7, kWideSlice = 4;
 constexpr int kWideTile = kWideRows * kBlk;
 constexpr int kWideN = 2 * kWideTok;                  // columns: tokens' hi, tokens' lo
 constexpr int kWidePanel = kWideN * 128;              // 64 k of all columns, 128-byte swizzle
 constexpr int kWideOffB = kWideStages * kWideTile;    // [kWideSlice][4] panels
-constexpr int kWideOffX = kWideOffB + kWideSlice * 4 * kWidePanel;   // sub-block sums: 16 k per super-block
-constexpr int kWideOffUp = kWideOffX + kWidePanel;    // float [kWideSlice][kWideTok]: 2^e
+constexpr int kWideOffX = kWideOffB + kWideSlice * 4 * kWidePanel;   // sub-block sums: 16 k per super-block, a row per token
+constexpr int kWideOffUp = kWideOffX + kWideTok * 128;    // float [kWideSlice][kWideTok]: 2^e
 constexpr int kWideOffTo = kWideOffUp + kWideSlice * kWideTok * 4;    // int [kWideTok]: a token's row of the result
 constexpr int kWideSmem = kWideOffTo + kWideTok * 4 + 1024;
 static_assert(kWideTile % 1024 == 0 && kWideSmem <= 208 * 1024, "shared memory layout");
-// Of a group's 256 columns: A from 0, the minima, the sums of the values of two
-// super-blocks in turn, the sums of the minima.
-constexpr uint32_t kWideColX = 128, kWideColS = 160, kWideColM = 224;
+// Of a group's 256 columns: A from 0, the minima, and for two tiles in turn the
+// sums of the values and of the minima.
+constexpr uint32_t kWideColX = 128, kWideColM = 144, kWideColS = 192;
+constexpr int kWideHalf = kWideTok / 2;   // tokens per thread
 
 template <bool kDown>
 __global__ void __launch_bounds__(kWideThreads, 1)
@@ -785,16 +791,16 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Plan plan;
     __shared__ PlanScratch scratch;
-    __shared__ uint64_t bars[2 * kWideStages + 11];
+    __shared__ uint64_t bars[2 * kWideStages + 13];
     __shared__ uint32_t abort_word, tmem_slot;
     __shared__ int start_at;
     const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
     auto full = [&](uint32_t s) { return bar0 + 8u * s; };
     auto empty = [&](uint32_t s) { return bar0 + 8u * (kWideStages + s); };
     auto a_full = [&](int g, int half) { return bar0 + 8u * uint32_t(2 * kWideStages + 2 * g + half); };
-    auto sums_full = [&](int g) { return bar0 + 8u * uint32_t(2 * kWideStages + 4 + g); };
-    auto a_free = [&](int g) { return bar0 + 8u * uint32_t(2 * kWideStages + 6 + g); };   // its first half
-    const uint32_t b_full = bar0 + 8u * (2 * kWideStages + 8), b_empty = b_full + 8u, drain = b_full + 16u;
+    auto a_free = [&](int g) { return bar0 + 8u * uint32_t(2 * kWideStages + 4 + g); };   // its first half
+    auto sums_full = [&](int g, uint32_t n) { return bar0 + 8u * (2 * kWideStages + 6 + 2 * uint32_t(g) + (n & 1u)); };
+    const uint32_t b_full = bar0 + 8u * (2 * kWideStages + 10), b_empty = b_full + 8u, drain = b_full + 16u;
     const AbortFlag abort_flag{smem_u32(&abort_word)};
     int* const status = a.status;
     const mmq_q4K_moe_t& p = a.p;
@@ -802,23 +808,24 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < kWideStages; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 4);
+            mbar_init(empty(s), 8);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(a_full(g, 0), 4);
             mbar_init(a_full(g, 1), 4);
             mbar_init(a_free(g), 1);
-            mbar_init(sums_full(g), 1);
+            mbar_init(sums_full(g, 0), 1);
+            mbar_init(sums_full(g, 1), 1);
         }
-        mbar_init(b_full, 8);
-        mbar_init(b_empty, 10);   // eight warps and the two issuers
+        mbar_init(b_full, 16);
+        mbar_init(b_empty, 18);   // sixteen warps and the two issuers
         mbar_init(drain, 2);
         abort_flag.set(0u);
         fence_barrier_init();
         prefetch_tmap(&map);
     }
     __syncwarp();
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(smem_u32(&tmem_slot), 512);
         tmem_relinquish();
     }
@@ -838,7 +845,7 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
         return base + uint32_t((u & ~1) * held + ((u | 1) < count ? 2 * s + (u & 1) : s));
     };
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             uint32_t pos = 0;
             auto load = [&](int x, int y) {
@@ -861,19 +868,20 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
             for (uint32_t i = pos > kWideStages ? pos - kWideStages : 0; i < pos; ++i)
                 wait_drain(full(i % kWideStages), (i / kWideStages) & 1u, status);
         }
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == 17 || warp == 18) {
         if (lane == 0) {
-            const int g = warp - 9;
+            const int g = warp - 17;
             const uint32_t t = tmem + 256u * uint32_t(g);
-            constexpr uint32_t id = idesc_f16_f32(kWideRows, kWideN);
+            constexpr uint32_t id = idesc_f16_f32(kWideRows, kWideN), id_x = idesc_f16_f32(kWideRows, kWideTok);
             const uint64_t b_desc = smem_desc_sw128(sbase + kWideOffB), x_desc = smem_desc_sw128(sbase + kWideOffX);
-            uint32_t run_phase = 0, phase = 0;
+            uint32_t run_phase = 0, tiles = 0;
             for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
                 const int held = held_of(run);
                 if (!wait_bounded(b_full, run_phase, abort_flag, status)) goto mma_done;
                 run_phase ^= 1u;
                 for (int u = g; u < run.count; u += 2)
                     for (int s = 0; s < held; ++s) {
+                        const uint32_t phase = tiles & 1u;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             if (!wait_bounded(a_full(g, half), phase, abort_flag, status)) goto mma_done;
@@ -887,9 +895,9 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
                             }
                             if (half == 0) mma_commit(a_free(g));
                         }
-                        mma_f16_ta(t + kWideColM, t + kWideColX, x_desc + uint64_t(s * 2), id, 0u);
-                        mma_commit(sums_full(g));
-                        phase ^= 1u;
+                        mma_f16_ta(t + kWideColM + 16u * phase, t + kWideColX, x_desc + uint64_t(s * 2), id_x, 0u);
+                        mma_commit(sums_full(g, tiles));
+                        ++tiles;
                     }
                 mbar_arrive(b_empty);
             }
@@ -897,11 +905,11 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
             mma_commit(drain);   // everything issued, also after a wait that ran out
             wait_drain(drain, 0u, status);
         }
-    } else if (warp < 8) {
-        const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+    } else {
+        const int g = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
         const uint32_t t = tmem + 256u * uint32_t(g) + (uint32_t((warp & 3) * 32) << 16);
         float* const ups = reinterpret_cast<float*>(smem + kWideOffUp);
-        const int* const to = reinterpret_cast<const int*>(smem + kWideOffTo);
+        int* const to = reinterpret_cast<int*>(smem + kWideOffTo);
         uint32_t run_phase = 0, tiles = 0, base = 0, magic;   // tiles: the group's, so far
         asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
         const int64_t pairs = int64_t(p.tokens) * p.top_k;
@@ -910,30 +918,29 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
             const int held = held_of(run);
             const int first = plan.start[run.a] + run.pass * kWideTok;
             const int ntok = min(kWideTok, plan.start[run.a + 1] - first);
-            // B: a warp per token and super-block, 8 consecutive values per lane.
+            // B: a warp per token, 8 consecutive values of a super-block per lane, all loads ahead.
             if (!__all_sync(0xffffffffu, wait_bounded(b_empty, run_phase ^ 1u, abort_flag, status))) break;
-            // Two tokens of every super-block, all loads ahead.
-            float4 ahead[kWideSlice][2][2];
+            const int n = warp;
+            float4 ahead[kWideSlice][2];
+            {
+                const int64_t col = int64_t(run.slice * shape.per) * 256 + 8 * lane;
+                const bool have = n < ntok;
+                const float* x = !have ? nullptr
+                                 : kDown ? a.h + int64_t(first + n) * p.ffn + col
+                                         : p.x + int64_t(plan.order[first + n] / p.top_k) * p.model + col;
 #pragma unroll
-            for (int s = 0; s < kWideSlice; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int n = warp + 8 * j;
-                    ahead[s][j][0] = ahead[s][j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (s < held && n < ntok) {
-                        const int64_t col = int64_t(run.slice * shape.per + s) * 256 + 8 * lane;
-                        const float4* x = reinterpret_cast<const float4*>(
-                            kDown ? a.h + int64_t(first + n) * p.ffn + col
-                                  : p.x + int64_t(plan.order[first + n] / p.top_k) * p.model + col);
-                        ahead[s][j][0] = x[0];
-                        ahead[s][j][1] = x[1];
+                for (int s = 0; s < kWideSlice; ++s) {
+                    ahead[s][0] = ahead[s][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (have && s < held) {
+                        ahead[s][0] = reinterpret_cast<const float4*>(x + 256 * s)[0];
+                        ahead[s][1] = reinterpret_cast<const float4*>(x + 256 * s)[1];
                     }
                 }
+            }
 #pragma unroll
-            for (int i = 0; i < 2 * kWideSlice; ++i) {
-                const int s = i >> 1, n = warp + 8 * (i & 1);
+            for (int s = 0; s < kWideSlice; ++s) {
                 if (s >= held) break;
-                const float4 c = ahead[s][i & 1][0], d = ahead[s][i & 1][1];
+                const float4 c = ahead[s][0], d = ahead[s][1];
                 float v[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
                 float top = 0.f;
 #pragma unroll
@@ -964,122 +971,120 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
                 const uint32_t swizzled = uint32_t(((lane & 7) ^ (n & 7)) << 4);   // rows n and 16 + n alike
                 st_shared_v4(panel + uint32_t(n * 128) + swizzled, hi[0], hi[1], hi[2], hi[3]);
                 st_shared_v4(panel + uint32_t((kWideTok + n) * 128) + swizzled, lo[0], lo[1], lo[2], lo[3]);
-                // the eight sub-blocks' sums, and eight zeros
+                // the eight sub-blocks' sums, hi and lo
                 const __half2 h = __floats2half2_rn(sum, sum);
                 const __half2 l = __floats2half2_rn(sum - __low2float(h), 0.f);
-                uint8_t* const xs = smem + kWideOffX;
-                const int chunk = ((2 * s) ^ (n & 7)) << 4, zeros = ((2 * s + 1) ^ (n & 7)) << 4;
                 if ((lane & 3) == 0) {
-                    *reinterpret_cast<__half*>(xs + n * 128 + chunk + 2 * (lane >> 2)) = __low2half(h);
-                    *reinterpret_cast<__half*>(xs + (kWideTok + n) * 128 + chunk + 2 * (lane >> 2)) = __low2half(l);
-                } else if (lane < 3) {
-                    *reinterpret_cast<uint4*>(xs + (lane == 1 ? n : kWideTok + n) * 128 + zeros) = make_uint4(0u, 0u, 0u, 0u);
+                    uint8_t* const xs = smem + kWideOffX + n * 128 + 2 * (lane >> 2);
+                    *reinterpret_cast<__half*>(xs + (((2 * s) ^ (n & 7)) << 4)) = __low2half(h);
+                    *reinterpret_cast<__half*>(xs + (((2 * s + 1) ^ (n & 7)) << 4)) = __low2half(l);
                 }
                 if (lane == 0) ups[s * kWideTok + n] = __uint_as_float(uint32_t(127 + e) << 23);
-                if (s == 0 && lane == 0)
-                    reinterpret_cast<int*>(smem + kWideOffTo)[n] = !kDown ? first + n : n < ntok ? plan.order[first + n] : 0;
             }
+            if (lane == 0) to[n] = run.slice * int(pairs) + (!kDown ? first + n : n < ntok ? plan.order[first + n] : 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_full);
             bool ok = __all_sync(0xffffffffu, wait_bounded(b_full, run_phase, abort_flag, status));
             run_phase ^= 1u;
-            // The group's tiles one after the other; the sums of each are read
-            // between the halves of the next.
+            // The group's tiles one after the other, the sums of each during the next.
             const int mine = (run.count + 1 - g) / 2 * held;
-            float acc[kWideTok];
+            float acc[kWideHalf];
 #pragma unroll
-            for (int k = 0; k < kWideTok; ++k) acc[k] = 0.f;
+            for (int k = 0; k < kWideHalf; ++k) acc[k] = 0.f;
             float2 scales = make_float2(0.f, 0.f);   // d, dmin of the tile before
-            for (int i = 0, u = g, s = 0, was_s = 0; ok && i <= mine; ++i) {
-                uint32_t at = 0, slot = 0;
-                __half2 sc[4];
-                uint4 head = make_uint4(0u, 0u, 0u, 0u);
-                // 64 values from two 16-byte loads: sub-blocks 2 j and 2 j + 1
-                auto unpack = [&](int j) {
-                    RowScale r;
-                    const __half2 high = __high2half2(sc[j]);
-                    r.s_lo = __low2half2(sc[j]);
-                    r.s_hi = __hmul2(high, u2h(0x2C002C00u));      // / 16
-                    r.b_lo = __hmul2(r.s_lo, u2h(0xE400E400u));    // * -1024
-                    r.b_hi = __hmul2(high, u2h(0xD400D400u));      // * -64
-                    const uint4 c = lds128(at + uint32_t(16 + 32 * j)), d = lds128(at + uint32_t(32 + 32 * j));
-                    const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
-                    uint32_t x[32];
+            int was_s = 0;
+            auto add_sums = [&](uint32_t tile) {
+                if (!__all_sync(0xffffffffu, wait_bounded(sums_full(g, tile), (tile >> 1) & 1u, abort_flag, status))) return false;
+                tc_fence_after();
+                uint32_t hi[8], lo[8], mn[8];
+                const uint32_t ts = t + kWideColS + 32u * (tile & 1u) + uint32_t(kWideHalf * half);
+                tmem_ld_32x32b_x8(ts, hi);
+                tmem_ld_32x32b_x8(ts + kWideTok, lo);
+                tmem_ld_32x32b_x8(t + kWideColM + 16u * (tile & 1u) + uint32_t(kWideHalf * half), mn);
+                tmem_wait_ld(hi);
+                tmem_wait_ld(lo);
+                tmem_wait_ld(mn);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint32_t w8 = w[q] >> 8;
-                        unpack_lo(w[q], w8, r, magic, x[2 * q], x[2 * q + 1]);
-                        unpack_hi(w[q], w8, r, magic, x[16 + 2 * q], x[17 + 2 * q]);
+                for (int k = 0; k < kWideHalf; ++k) {
+                    auto of = [](uint32_t v) { return __uint_as_float(v); };
+                    acc[k] = fmaf(ups[was_s * kWideTok + kWideHalf * half + k],
+                                  scales.x * (of(hi[k]) + of(lo[k])) - scales.y * of(mn[k]), acc[k]);
+                }
+                return true;
+            };
+            for (int i = 0, u = g, s = 0; ok && i <= mine; ++i) {
+                if (half == 1 && i > 0) {   // A's second half is free, too
+                    ok = add_sums(tiles - 1);
+                    if (!ok) break;
+                }
+                float2 next_scales = scales;
+                if (i < mine) {
+                    const uint32_t pos = position(base, u, s, run.count, held), slot = pos % kWideStages;
+                    const uint32_t at = sbase + slot * kWideTile + uint32_t(row * kBlk);
+                    ok = __all_sync(0xffffffffu, wait_bounded(full(slot), (pos / kWideStages) & 1u, abort_flag, status) &&
+                                                     (half == 1 || tiles == 0 ||
+                                                      wait_bounded(a_free(g), (tiles - 1) & 1u, abort_flag, status)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint4 head = lds128(at);
+                    const __half2 k1024 = u2h(0x64006400u);
+                    // sub-blocks 4 half .. 4 half + 3
+                    const uint32_t four = half ? sc_hi4(head.y, head.w) : sc_lo4(head.y);
+                    const __half2 sc[2] = {__hsub2(u2h(prmt(four, 0x64646464u, 0x4140u)), k1024),
+                                           __hsub2(u2h(prmt(four, 0x64646464u, 0x4342u)), k1024)};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {   // 64 values from two 16-byte loads
+                        RowScale r;
+                        const __half2 high = __high2half2(sc[j]);
+                        r.s_lo = __low2half2(sc[j]);
+                        r.s_hi = __hmul2(high, u2h(0x2C002C00u));      // / 16
+                        r.b_lo = __hmul2(r.s_lo, u2h(0xE400E400u));    // * -1024
+                        r.b_hi = __hmul2(high, u2h(0xD400D400u));      // * -64
+                        const uint32_t from = at + uint32_t(16 + 64 * half + 32 * j);
+                        const uint4 c = lds128(from), d = lds128(from + 16u);
+                        const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+                        uint32_t x[32];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint32_t w8 = w[q] >> 8;
+                            unpack_lo(w[q], w8, r, magic, x[2 * q], x[2 * q + 1]);
+                            unpack_hi(w[q], w8, r, magic, x[16 + 2 * q], x[17 + 2 * q]);
+                        }
+                        tmem_st_32x32b_x32(t + uint32_t(64 * half + 32 * j), x);
                     }
-                    tmem_st_32x32b_x32(t + 32u * uint32_t(j), x);
-                };
-                auto hand_over = [&](int half) {
+                    if (half == 1) {
+                        const uint32_t ma = m_lo4(head.z), mb = m_hi4(head.z, head.w);
+                        const uint32_t m0 = h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4140u)), k1024)),
+                                       m1 = h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4342u)), k1024)),
+                                       m2 = h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4140u)), k1024)),
+                                       m3 = h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4342u)), k1024));
+                        const uint32_t mins[8] = {m0, m1, m2, m3, m0, m1, m2, m3};
+                        tmem_st_32x32b_x8(t + kWideColX, mins);
+                    }
                     tmem_wait_st();   // and with the stores the loads that they depend on
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(a_full(g, half));
-                        if (half == 1) mbar_arrive(empty(slot));
+                        mbar_arrive(empty(slot));
                     }
-                };
-                const __half2 k1024 = u2h(0x64006400u);
-                if (i < mine) {
-                    const uint32_t pos = position(base, u, s, run.count, held);
-                    slot = pos % kWideStages;
-                    at = sbase + slot * kWideTile + uint32_t(row * kBlk);
-                    ok = __all_sync(0xffffffffu, wait_bounded(full(slot), (pos / kWideStages) & 1u, abort_flag, status) &&
-                                                     (tiles == 0 || wait_bounded(a_free(g), (tiles - 1) & 1u, abort_flag, status)));
-                    if (!ok) break;
-                    head = lds128(at);
-                    const uint32_t sa = sc_lo4(head.y), sb = sc_hi4(head.y, head.w);
-                    sc[0] = __hsub2(u2h(prmt(sa, 0x64646464u, 0x4140u)), k1024);
-                    sc[1] = __hsub2(u2h(prmt(sa, 0x64646464u, 0x4342u)), k1024);
-                    sc[2] = __hsub2(u2h(prmt(sb, 0x64646464u, 0x4140u)), k1024);
-                    sc[3] = __hsub2(u2h(prmt(sb, 0x64646464u, 0x4342u)), k1024);
-                    tc_fence_after();
-                    unpack(0);
-                    unpack(1);
-                    hand_over(0);
-                }
-                if (i > 0) {
-                    ok = __all_sync(0xffffffffu, wait_bounded(sums_full(g), (tiles - 1) & 1u, abort_flag, status));
-                    if (!ok) break;
-                    tc_fence_after();
-                    uint32_t sum[32], mn[32];
-                    tmem_ld_32x32b_x32(t + kWideColS + 32u * ((tiles - 1) & 1u), sum);
-                    tmem_ld_32x32b_x32(t + kWideColM, mn);
-                    tmem_wait_ld(sum);
-                    tmem_wait_ld(mn);
-#pragma unroll
-                    for (int k = 0; k < kWideTok; ++k) {
-                        auto of = [](uint32_t v) { return __uint_as_float(v); };
-                        acc[k] = fmaf(ups[was_s * kWideTok + k],
-                                      scales.x * (of(sum[k]) + of(sum[kWideTok + k])) - scales.y * (of(mn[k]) + of(mn[kWideTok + k])),
-                                      acc[k]);
-                    }
-                }
-                if (i < mine) {
-                    const uint32_t ma = m_lo4(head.z), mb = m_hi4(head.z, head.w);
-                    const uint32_t mins[8] = {h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4140u)), k1024)),
-                                              h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4342u)), k1024)),
-                                              h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4140u)), k1024)),
-                                              h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4342u)), k1024)), 0u, 0u, 0u, 0u};
-                    tmem_st_32x32b_x8(t + kWideColX, mins);
-                    unpack(2);
-                    unpack(3);
-                    hand_over(1);
-                    scales = __half22float2(u2h(head.x));
+                    next_scales = __half22float2(u2h(head.x));
                     ++tiles;
                 }
+                if (half == 0 && i > 0) {
+                    ok = add_sums(i < mine ? tiles - 2 : tiles - 1);
+                    if (!ok) break;
+                }
+                scales = next_scales;
                 if (i > 0 && was_s == held - 1) {   // the row is complete; u is the next one by now
                     const int was_u = i < mine ? u - 2 : u;
-                    const int64_t part = int64_t(run.slice) * pairs;
                     float* const out = (kDown ? a.y : a.parts) + int64_t(run.first + was_u) * kWideRows + row;
+                    const int4 t0 = reinterpret_cast<const int4*>(to)[2 * half], t1 = reinterpret_cast<const int4*>(to)[2 * half + 1];
+                    const int rows_to[kWideHalf] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
 #pragma unroll
-                    for (int k = 0; k < kWideTok; ++k) {
-                        const int64_t to_row = part + to[k];
-                        if (k < ntok) out[to_row * shape.rows] = acc[k];
+                    for (int k = 0; k < kWideHalf; ++k) {
+                        if (kWideHalf * half + k < ntok) out[int64_t(rows_to[k]) * shape.rows] = acc[k];
                         acc[k] = 0.f;
                     }
                 }
@@ -1097,7 +1102,7 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
