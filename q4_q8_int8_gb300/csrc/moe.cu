@@ -767,8 +767,7 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, c
 // half of A that those are through with; sums are double.
 //   warps 0-7, 8-15  groups 0 and 1: four warps per half
 //   warp 16          TMA producer, a ring of tiles for both groups
-//   warps 17, 18     MMA issuers of groups 0 and 1 (a thread issues a product
-//                    every 45 cycles, whatever its width up to 64)
+//   warps 17, 18     MMA issuers of groups 0 and 1
 constexpr int kWideTok = 16, kWideThreads = 19 * 32, kWideRows = 128, kWideStages = 7, kWideSlice = 4;
 constexpr int kWideTile = kWideRows * kBlk;
 constexpr int kWideN = 2 * kWideTok;                  // columns: tokens' hi, tokens' lo
@@ -869,9 +868,9 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
                 wait_drain(full(i % kWideStages), (i / kWideStages) & 1u, status);
         }
     } else if (warp == 17 || warp == 18) {
-        if (lane == 0) {
-            const int g = warp - 17;
-            const uint32_t t = tmem + 256u * uint32_t(g);
+        const int g = __shfl_sync(0xffffffffu, warp, 0) - 17;
+        const uint32_t t = __shfl_sync(0xffffffffu, tmem, 0) + 256u * uint32_t(g);
+        if (elect_one()) {
             constexpr uint32_t id = idesc_f16_f32(kWideRows, kWideN), id_x = idesc_f16_f32(kWideRows, kWideTok);
             const uint64_t b_desc = smem_desc_sw128(sbase + kWideOffB), x_desc = smem_desc_sw128(sbase + kWideOffX);
             uint32_t run_phase = 0, tiles = 0;
@@ -881,7 +880,8 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
                 run_phase ^= 1u;
                 for (int u = g; u < run.count; u += 2)
                     for (int s = 0; s < held; ++s) {
-                        const uint32_t phase = tiles & 1u;
+                        const uint32_t phase = tiles & 1u, ts = t + kWideColS + 32u * phase;
+                        const uint64_t bs = b_desc + uint64_t(s * 4 * (kWidePanel >> 4));
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             if (!wait_bounded(a_full(g, half), phase, abort_flag, status)) goto mma_done;
@@ -889,9 +889,8 @@ moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, cons
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int k = 8 * half + i;   // 16 values each, a panel of 64
-                                mma_f16_ta(t + kWideColS + 32u * phase, t + 8u * uint32_t(k),
-                                           b_desc + uint64_t((s * 4 + (k >> 2)) * (kWidePanel >> 4) + (k & 3) * 2), id,
-                                           uint32_t(k > 0));
+                                mma_f16_ta(ts, t + 8u * uint32_t(k), bs + uint64_t((k >> 2) * (kWidePanel >> 4) + (k & 3) * 2),
+                                           id, uint32_t(k > 0));
                             }
                             if (half == 0) mma_commit(a_free(g));
                         }
