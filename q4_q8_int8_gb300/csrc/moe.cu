@@ -68,7 +68,7 @@ static_assert(kSmemBytes <= 212 * 1024, "shared memory budget");
 
 // Which tokens go to which expert: pair i = token i / top_k, its i % top_k-th
 // expert.  An active expert (one with a token) has its pairs in a row of
-// `order`, and one pass over its weights per 4 of them (16 in the wide form).
+// `order`, and one pass over its weights per kTok of them.
 struct Plan {
     int active;
     int expert[kMaxExperts];
@@ -82,7 +82,6 @@ struct MoeArgs {
     float* logits;       // [tokens][experts]
     float* h;            // first product, rows in the plan's order: h [pairs][ffn], or if its sum is in
                          // parts [gu_slices][pairs][2 ffn] of gate and up, alternating
-    float* parts;        // wide form: first product [gu_slices][pairs][2 ffn], gate and up alternating
     float* y;            // second product [down_slices][pairs][model], rows by pair
     int gu_slices, down_slices;
     int* status;
@@ -207,18 +206,17 @@ struct PlanScratch {
     int totals[3][kMaxExperts / 32];
 };
 
-// Fill `plan` (shared memory) from the logits, a pass for every tok tokens of
-// an expert; `store`: also the chosen experts and their weights to the caller.
-template <int threads, int tok>
+// Fill `plan` (shared memory) from the logits; `store`: also the chosen
+// experts and their weights to the caller.
 __device__ __forceinline__ void make_plan(const MoeArgs& a, Plan* plan, PlanScratch* z, bool store) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
-    static_assert(kMaxExperts <= threads && kMaxTokens <= 64, "one thread per expert, one bit per token");
+    static_assert(kMaxExperts <= kThreads && kMaxTokens <= 64, "one thread per expert, one bit per token");
     if (e < kMaxExperts) z->tokens_of[e] = 0;
     __syncthreads();
-    for (int t = warp; t < a.p.tokens; t += threads / 32) choose(a, t, lane, z->ids, z->tokens_of, store);
+    for (int t = warp; t < a.p.tokens; t += kThreads / 32) choose(a, t, lane, z->ids, z->tokens_of, store);
     __syncthreads();
     uint64_t mine = e < kMaxExperts ? z->tokens_of[e] : 0;
-    const int n = __popcll(mine), passes = (n + tok - 1) / tok;
+    const int n = __popcll(mine), passes = (n + kTok - 1) / kTok;
     // prefixes over the experts: of their pairs, their passes, and the active ones
     int pairs = n, pass = passes;
 #pragma unroll
@@ -412,28 +410,6 @@ struct Run {
     }
 };
 
-// The first run of a CTA's share: equal consecutive parts of all passes' tiles,
-// the first `more` one longer.  start_at: a word of shared memory.
-__device__ __forceinline__ Run first_run(const Plan& plan, int slices, int tiles, int* start_at) {
-    const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
-    const uint32_t mine = total / gridDim.x, more = total - mine * gridDim.x;
-    const uint32_t i0 = blockIdx.x * mine + min(blockIdx.x, more), i1 = i0 + mine + (blockIdx.x < more ? 1u : 0u);
-    const int p0 = int(i0 / each);
-    if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
-        *start_at = threadIdx.x;
-    __syncthreads();
-    Run run;
-    run.left = int(i1 - i0);
-    run.a = run.left > 0 ? *start_at : 0;
-    const int passes = plan.pass[run.a + 1] - plan.pass[run.a];
-    const int local = run.left > 0 ? int(i0) - plan.pass[run.a] * int(each) : 0, sp = local / tiles;
-    run.first = local - sp * tiles;
-    run.slice = sp / passes;
-    run.pass = sp - run.slice * passes;
-    run.count = min(tiles - run.first, run.left);
-    return run;
-}
-
 // The shape of one product.
 struct Shape {
     int rows, nsb, slices, per, teams, tiles;   // per: super-blocks of a slice and warps of a team
@@ -453,7 +429,22 @@ struct Product : Shape {
         const int warp = threadIdx.x >> 5;
         team = warp / per;
         ks = warp - team * per;
-        run = first_run(plan, slices, tiles, start_at);
+        // equal consecutive parts of all passes' tiles, the first `more` one longer
+        const uint32_t each = uint32_t(slices * tiles), total = uint32_t(plan.pass[plan.active]) * each;
+        const uint32_t mine = total / gridDim.x, more = total - mine * gridDim.x;
+        const uint32_t i0 = blockIdx.x * mine + min(blockIdx.x, more), i1 = i0 + mine + (blockIdx.x < more ? 1u : 0u);
+        const int p0 = int(i0 / each);
+        if (int(threadIdx.x) < plan.active && plan.pass[threadIdx.x] <= p0 && p0 < plan.pass[threadIdx.x + 1])
+            *start_at = threadIdx.x;
+        __syncthreads();
+        run.left = int(i1 - i0);
+        run.a = run.left > 0 ? *start_at : 0;
+        const int passes = plan.pass[run.a + 1] - plan.pass[run.a];
+        const int local = run.left > 0 ? int(i0) - plan.pass[run.a] * int(each) : 0, sp = local / tiles;
+        run.first = local - sp * tiles;
+        run.slice = sp / passes;
+        run.pass = sp - run.slice * passes;
+        run.count = min(tiles - run.first, run.left);
         in = run;
         if (team >= teams) in.left = 0;
         enter(plan);
@@ -742,387 +733,12 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, c
     // lets it be scheduled only after its own wait for the router.
     if (!kDown) griddep_wait();
     griddep_launch_dependents();
-    make_plan<kThreads, kTok>(a, &plan, &scratch, !kDown && blockIdx.x == 0);
+    make_plan(a, &plan, &scratch, !kDown && blockIdx.x == 0);
     Product w(&map, shape, plan, &start_at);
     layer.start(w);
     if (kDown) griddep_wait();   // the first product
     layer.go<kDown>(w);
     layer.drain();
-}
-
-// ------------------------------------------------------------- many tokens
-// The same product where experts have many tokens: up to 16 of them per pass,
-// so that the weights are unpacked once for all, on tcgen05.
-//
-// A tile is 128 rows x one super-block.  Two groups of eight warps take row
-// tiles in turn, two threads per row, one for either half of the super-block:
-// a thread turns its share of the row's 144 bytes into 128 values sc q in
-// tensor memory, the A operand (and one of them adds the eight minima m, twice);
-// B, in shared memory, has a row per token's hi and one per its lo, K in the
-// order in which unpacking leaves the values; a second B has the sub-blocks'
-// sums, hi and lo one after the other.  16 + 1 products per super-block give
-// the row's sums for all tokens, which its two threads read back, eight tokens
-// each, scale and add up over the (at most four) super-blocks of a slice of the
-// row.  Values are unpacked while the products of the tile before run, into the
-// half of A that those are through with; sums are double.
-//   warps 0-7, 8-15  groups 0 and 1: four warps per half
-//   warp 16          TMA producer, a ring of tiles for both groups
-//   warps 17, 18     MMA issuers of groups 0 and 1
-constexpr int kWideTok = 16, kWideThreads = 19 * 32, kWideRows = 128, kWideStages = 7, kWideSlice = 4;
-constexpr int kWideTile = kWideRows * kBlk;
-constexpr int kWideN = 2 * kWideTok;                  // columns: tokens' hi, tokens' lo
-constexpr int kWidePanel = kWideN * 128;              // 64 k of all columns, 128-byte swizzle
-constexpr int kWideOffB = kWideStages * kWideTile;    // [kWideSlice][4] panels
-constexpr int kWideOffX = kWideOffB + kWideSlice * 4 * kWidePanel;   // sub-block sums: 16 k per super-block, a row per token
-constexpr int kWideOffUp = kWideOffX + kWideTok * 128;    // float [kWideSlice][kWideTok]: 2^e
-constexpr int kWideOffTo = kWideOffUp + kWideSlice * kWideTok * 4;    // int [kWideTok]: a token's row of the result
-constexpr int kWideSmem = kWideOffTo + kWideTok * 4 + 1024;
-static_assert(kWideTile % 1024 == 0 && kWideSmem <= 208 * 1024, "shared memory layout");
-// Of a group's 256 columns: A from 0, the minima, and for two tiles in turn the
-// sums of the values and of the minima.
-constexpr uint32_t kWideColX = 128, kWideColM = 144, kWideColS = 192;
-constexpr int kWideHalf = kWideTok / 2;   // tokens per thread
-
-template <bool kDown>
-__global__ void __launch_bounds__(kWideThreads, 1)
-moe_wide_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, const MoeArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ Plan plan;
-    __shared__ PlanScratch scratch;
-    __shared__ uint64_t bars[2 * kWideStages + 13];
-    __shared__ uint32_t abort_word, tmem_slot;
-    __shared__ int start_at;
-    const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
-    auto full = [&](uint32_t s) { return bar0 + 8u * s; };
-    auto empty = [&](uint32_t s) { return bar0 + 8u * (kWideStages + s); };
-    auto a_full = [&](int g, int half) { return bar0 + 8u * uint32_t(2 * kWideStages + 2 * g + half); };
-    auto a_free = [&](int g) { return bar0 + 8u * uint32_t(2 * kWideStages + 4 + g); };   // its first half
-    auto sums_full = [&](int g, uint32_t n) { return bar0 + 8u * (2 * kWideStages + 6 + 2 * uint32_t(g) + (n & 1u)); };
-    const uint32_t b_full = bar0 + 8u * (2 * kWideStages + 10), b_empty = b_full + 8u, drain = b_full + 16u;
-    const AbortFlag abort_flag{smem_u32(&abort_word)};
-    int* const status = a.status;
-    const mmq_q4K_moe_t& p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (uint32_t s = 0; s < kWideStages; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 8);
-        }
-        for (int g = 0; g < 2; ++g) {
-            mbar_init(a_full(g, 0), 4);
-            mbar_init(a_full(g, 1), 4);
-            mbar_init(a_free(g), 1);
-            mbar_init(sums_full(g, 0), 1);
-            mbar_init(sums_full(g, 1), 1);
-        }
-        mbar_init(b_full, 16);
-        mbar_init(b_empty, 18);   // sixteen warps and the two issuers
-        mbar_init(drain, 2);
-        abort_flag.set(0u);
-        fence_barrier_init();
-        prefetch_tmap(&map);
-    }
-    __syncwarp();
-    if (warp == 17) {
-        tmem_alloc(smem_u32(&tmem_slot), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    // As in moe_product_kernel: the logits are complete before the second product starts.
-    if (!kDown) griddep_wait();
-    griddep_launch_dependents();
-    make_plan<kWideThreads, kWideTok>(a, &plan, &scratch, !kDown && blockIdx.x == 0);
-    Run run = first_run(plan, shape.slices, shape.tiles, &start_at);
-    auto held_of = [&](const Run& r) { return min(shape.per, shape.nsb - r.slice * shape.per); };
-    // Ring position of super-block s of the run's row tile u: the two groups'
-    // tiles in turn, an odd last one alone.
-    auto position = [&](uint32_t base, int u, int s, int count, int held) {
-        return base + uint32_t((u & ~1) * held + ((u | 1) < count ? 2 * s + (u & 1) : s));
-    };
-
-    if (warp == 16) {
-        if (lane == 0) {
-            uint32_t pos = 0;
-            auto load = [&](int x, int y) {
-                const uint32_t slot = pos % kWideStages, par = (pos / kWideStages) & 1u;
-                if (!wait_bounded(empty(slot), par ^ 1u, abort_flag, status)) return false;
-                mbar_arrive_expect_tx(full(slot), kWideTile);
-                tma_load_2d(sbase + slot * kWideTile, &map, full(slot), x, y);
-                ++pos;
-                return true;
-            };
-            for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
-                const int held = held_of(run);
-                const int y = plan.expert[run.a] * shape.rows + run.first * kWideRows, x = run.slice * shape.per * kBlk;
-                for (int u = 0; u < run.count; u += 2)
-                    for (int s = 0; s < held; ++s)
-                        for (int v = u; v < min(u + 2, run.count); ++v)
-                            if (!load(x + s * kBlk, y + v * kWideRows)) goto producer_done;
-            }
-        producer_done:
-            for (uint32_t i = pos > kWideStages ? pos - kWideStages : 0; i < pos; ++i)
-                wait_drain(full(i % kWideStages), (i / kWideStages) & 1u, status);
-        }
-    } else if (warp == 17 || warp == 18) {
-        const int g = __shfl_sync(0xffffffffu, warp, 0) - 17;
-        const uint32_t t = __shfl_sync(0xffffffffu, tmem, 0) + 256u * uint32_t(g);
-        if (elect_one()) {
-            constexpr uint32_t id = idesc_f16_f32(kWideRows, kWideN), id_x = idesc_f16_f32(kWideRows, kWideTok);
-            const uint64_t b_desc = smem_desc_sw128(sbase + kWideOffB), x_desc = smem_desc_sw128(sbase + kWideOffX);
-            uint32_t run_phase = 0, tiles = 0;
-            for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
-                const int held = held_of(run);
-                if (!wait_bounded(b_full, run_phase, abort_flag, status)) goto mma_done;
-                run_phase ^= 1u;
-                for (int u = g; u < run.count; u += 2)
-                    for (int s = 0; s < held; ++s) {
-                        const uint32_t phase = tiles & 1u, ts = t + kWideColS + 32u * phase;
-                        const uint64_t bs = b_desc + uint64_t(s * 4 * (kWidePanel >> 4));
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (!wait_bounded(a_full(g, half), phase, abort_flag, status)) goto mma_done;
-                            tc_fence_after();
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int k = 8 * half + i;   // 16 values each, a panel of 64
-                                mma_f16_ta(ts, t + 8u * uint32_t(k), bs + uint64_t((k >> 2) * (kWidePanel >> 4) + (k & 3) * 2),
-                                           id, uint32_t(k > 0));
-                            }
-                            if (half == 0) mma_commit(a_free(g));
-                        }
-                        mma_f16_ta(t + kWideColM + 16u * phase, t + kWideColX, x_desc + uint64_t(s * 2), id_x, 0u);
-                        mma_commit(sums_full(g, tiles));
-                        ++tiles;
-                    }
-                mbar_arrive(b_empty);
-            }
-        mma_done:
-            mma_commit(drain);   // everything issued, also after a wait that ran out
-            wait_drain(drain, 0u, status);
-        }
-    } else {
-        const int g = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
-        const uint32_t t = tmem + 256u * uint32_t(g) + (uint32_t((warp & 3) * 32) << 16);
-        float* const ups = reinterpret_cast<float*>(smem + kWideOffUp);
-        int* const to = reinterpret_cast<int*>(smem + kWideOffTo);
-        uint32_t run_phase = 0, tiles = 0, base = 0, magic;   // tiles: the group's, so far
-        asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-        const int64_t pairs = int64_t(p.tokens) * p.top_k;
-        if (kDown) griddep_wait();   // the first product's h
-        for (; run.left > 0; run.next(plan, shape.slices, shape.tiles)) {
-            const int held = held_of(run);
-            const int first = plan.start[run.a] + run.pass * kWideTok;
-            const int ntok = min(kWideTok, plan.start[run.a + 1] - first);
-            // B: a warp per token, 8 consecutive values of a super-block per lane, all loads ahead.
-            if (!__all_sync(0xffffffffu, wait_bounded(b_empty, run_phase ^ 1u, abort_flag, status))) break;
-            const int n = warp;
-            float4 ahead[kWideSlice][2];
-            {
-                const int64_t col = int64_t(run.slice * shape.per) * 256 + 8 * lane;
-                const bool have = n < ntok;
-                const float* x = !have ? nullptr
-                                 : kDown ? a.h + int64_t(first + n) * p.ffn + col
-                                         : p.x + int64_t(plan.order[first + n] / p.top_k) * p.model + col;
-#pragma unroll
-                for (int s = 0; s < kWideSlice; ++s) {
-                    ahead[s][0] = ahead[s][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (have && s < held) {
-                        ahead[s][0] = reinterpret_cast<const float4*>(x + 256 * s)[0];
-                        ahead[s][1] = reinterpret_cast<const float4*>(x + 256 * s)[1];
-                    }
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < kWideSlice; ++s) {
-                if (s >= held) break;
-                const float4 c = ahead[s][0], d = ahead[s][1];
-                float v[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
-                float top = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[k]));
-                const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // not negative: bits order as values
-                // 2^e with top 2^-e in [128, 256), e from -126 on
-                int e = int(bits >> 23) - 127 - 7;
-                e = e < -126 ? -126 : e;
-                const float down = __uint_as_float(uint32_t(127 - e) << 23);
-                float sum = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    v[k] *= down;
-                    sum += v[k];
-                }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {   // elements 0 2, 1 3, 4 6, 5 7
-                    const int j = (k & 1) + 4 * (k >> 1);
-                    const __half2 h = __floats2half2_rn(v[j], v[j + 2]);
-                    const float2 back = __half22float2(h);
-                    hi[k] = h2u(h);
-                    lo[k] = h2u(__floats2half2_rn(v[j] - back.x, v[j + 2] - back.y));
-                }
-                const uint32_t panel = sbase + uint32_t(kWideOffB + (s * 4 + (lane >> 3)) * kWidePanel);
-                const uint32_t swizzled = uint32_t(((lane & 7) ^ (n & 7)) << 4);   // rows n and 16 + n alike
-                st_shared_v4(panel + uint32_t(n * 128) + swizzled, hi[0], hi[1], hi[2], hi[3]);
-                st_shared_v4(panel + uint32_t((kWideTok + n) * 128) + swizzled, lo[0], lo[1], lo[2], lo[3]);
-                // the eight sub-blocks' sums, hi and lo
-                const __half2 h = __floats2half2_rn(sum, sum);
-                const __half2 l = __floats2half2_rn(sum - __low2float(h), 0.f);
-                if ((lane & 3) == 0) {
-                    uint8_t* const xs = smem + kWideOffX + n * 128 + 2 * (lane >> 2);
-                    *reinterpret_cast<__half*>(xs + (((2 * s) ^ (n & 7)) << 4)) = __low2half(h);
-                    *reinterpret_cast<__half*>(xs + (((2 * s + 1) ^ (n & 7)) << 4)) = __low2half(l);
-                }
-                if (lane == 0) ups[s * kWideTok + n] = __uint_as_float(uint32_t(127 + e) << 23);
-            }
-            if (lane == 0) to[n] = run.slice * int(pairs) + (!kDown ? first + n : n < ntok ? plan.order[first + n] : 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_full);
-            bool ok = __all_sync(0xffffffffu, wait_bounded(b_full, run_phase, abort_flag, status));
-            run_phase ^= 1u;
-            // The group's tiles one after the other, the sums of each during the next.
-            const int mine = (run.count + 1 - g) / 2 * held;
-            float acc[kWideHalf];
-#pragma unroll
-            for (int k = 0; k < kWideHalf; ++k) acc[k] = 0.f;
-            float2 scales = make_float2(0.f, 0.f);   // d, dmin of the tile before
-            int was_s = 0;
-            auto add_sums = [&](uint32_t tile) {
-                if (!__all_sync(0xffffffffu, wait_bounded(sums_full(g, tile), (tile >> 1) & 1u, abort_flag, status))) return false;
-                tc_fence_after();
-                uint32_t hi[8], lo[8], mn[8];
-                const uint32_t ts = t + kWideColS + 32u * (tile & 1u) + uint32_t(kWideHalf * half);
-                tmem_ld_32x32b_x8(ts, hi);
-                tmem_ld_32x32b_x8(ts + kWideTok, lo);
-                tmem_ld_32x32b_x8(t + kWideColM + 16u * (tile & 1u) + uint32_t(kWideHalf * half), mn);
-                tmem_wait_ld(hi);
-                tmem_wait_ld(lo);
-                tmem_wait_ld(mn);
-#pragma unroll
-                for (int k = 0; k < kWideHalf; ++k) {
-                    auto of = [](uint32_t v) { return __uint_as_float(v); };
-                    acc[k] = fmaf(ups[was_s * kWideTok + kWideHalf * half + k],
-                                  scales.x * (of(hi[k]) + of(lo[k])) - scales.y * of(mn[k]), acc[k]);
-                }
-                return true;
-            };
-            for (int i = 0, u = g, s = 0; ok && i <= mine; ++i) {
-                if (half == 1 && i > 0) {   // A's second half is free, too
-                    ok = add_sums(tiles - 1);
-                    if (!ok) break;
-                }
-                float2 next_scales = scales;
-                if (i < mine) {
-                    const uint32_t pos = position(base, u, s, run.count, held), slot = pos % kWideStages;
-                    const uint32_t at = sbase + slot * kWideTile + uint32_t(row * kBlk);
-                    ok = __all_sync(0xffffffffu, wait_bounded(full(slot), (pos / kWideStages) & 1u, abort_flag, status) &&
-                                                     (half == 1 || tiles == 0 ||
-                                                      wait_bounded(a_free(g), (tiles - 1) & 1u, abort_flag, status)));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint4 head = lds128(at);
-                    const __half2 k1024 = u2h(0x64006400u);
-                    // sub-blocks 4 half .. 4 half + 3
-                    const uint32_t four = half ? sc_hi4(head.y, head.w) : sc_lo4(head.y);
-                    const __half2 sc[2] = {__hsub2(u2h(prmt(four, 0x64646464u, 0x4140u)), k1024),
-                                           __hsub2(u2h(prmt(four, 0x64646464u, 0x4342u)), k1024)};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {   // 64 values from two 16-byte loads
-                        RowScale r;
-                        const __half2 high = __high2half2(sc[j]);
-                        r.s_lo = __low2half2(sc[j]);
-                        r.s_hi = __hmul2(high, u2h(0x2C002C00u));      // / 16
-                        r.b_lo = __hmul2(r.s_lo, u2h(0xE400E400u));    // * -1024
-                        r.b_hi = __hmul2(high, u2h(0xD400D400u));      // * -64
-                        const uint32_t from = at + uint32_t(16 + 64 * half + 32 * j);
-                        const uint4 c = lds128(from), d = lds128(from + 16u);
-                        const uint32_t w[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
-                        uint32_t x[32];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const uint32_t w8 = w[q] >> 8;
-                            unpack_lo(w[q], w8, r, magic, x[2 * q], x[2 * q + 1]);
-                            unpack_hi(w[q], w8, r, magic, x[16 + 2 * q], x[17 + 2 * q]);
-                        }
-                        tmem_st_32x32b_x32(t + uint32_t(64 * half + 32 * j), x);
-                    }
-                    if (half == 1) {
-                        const uint32_t ma = m_lo4(head.z), mb = m_hi4(head.z, head.w);
-                        const uint32_t m0 = h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4140u)), k1024)),
-                                       m1 = h2u(__hsub2(u2h(prmt(ma, 0x64646464u, 0x4342u)), k1024)),
-                                       m2 = h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4140u)), k1024)),
-                                       m3 = h2u(__hsub2(u2h(prmt(mb, 0x64646464u, 0x4342u)), k1024));
-                        const uint32_t mins[8] = {m0, m1, m2, m3, m0, m1, m2, m3};
-                        tmem_st_32x32b_x8(t + kWideColX, mins);
-                    }
-                    tmem_wait_st();   // and with the stores the loads that they depend on
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(a_full(g, half));
-                        mbar_arrive(empty(slot));
-                    }
-                    next_scales = __half22float2(u2h(head.x));
-                    ++tiles;
-                }
-                if (half == 0 && i > 0) {
-                    ok = add_sums(i < mine ? tiles - 2 : tiles - 1);
-                    if (!ok) break;
-                }
-                scales = next_scales;
-                if (i > 0 && was_s == held - 1) {   // the row is complete; u is the next one by now
-                    const int was_u = i < mine ? u - 2 : u;
-                    float* const out = (kDown ? a.y : a.parts) + int64_t(run.first + was_u) * kWideRows + row;
-                    const int4 t0 = reinterpret_cast<const int4*>(to)[2 * half], t1 = reinterpret_cast<const int4*>(to)[2 * half + 1];
-                    const int rows_to[kWideHalf] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
-#pragma unroll
-                    for (int k = 0; k < kWideHalf; ++k) {
-                        if (kWideHalf * half + k < ntok) out[int64_t(rows_to[k]) * shape.rows] = acc[k];
-                        acc[k] = 0.f;
-                    }
-                }
-                was_s = s;
-                if (i + 1 < mine && ++s == held) {
-                    s = 0;
-                    u += 2;
-                }
-            }
-            if (!ok) break;
-            base += uint32_t(run.count * held);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_empty);
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 17) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
-}
-
-// h = silu(gate) * up of the wide form, gate and up each a sum of parts; rows in the plan's order.
-__global__ void __launch_bounds__(256) moe_act_kernel(const MoeArgs a) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const mmq_q4K_moe_t& p = a.p;
-    const int f = (blockIdx.x * 256 + threadIdx.x) * 2;
-    if (f >= p.ffn) return;
-    const int64_t pairs = int64_t(p.tokens) * p.top_k;
-    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);   // gate, up, gate, up
-#pragma unroll 4
-    for (int s = 0; s < a.gu_slices; ++s) {
-        const float4 v = *reinterpret_cast<const float4*>(a.parts + ((s * pairs + blockIdx.y) * p.ffn + f) * 2);
-        c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
-    }
-    *reinterpret_cast<float2*>(a.h + int64_t(blockIdx.y) * p.ffn + f) = make_float2(silu_times(c.x, c.y), silu_times(c.z, c.w));
 }
 
 // out = residual + the sum of the chosen experts' rows
@@ -1167,55 +783,45 @@ cudaLaunchConfig_t follow_config(dim3 grid, dim3 block, size_t smem, cudaStream_
     return cfg;
 }
 
-// The wide form, by what an expert gets on average.
-bool wide(const mmq_q4K_moe_t& p) { return p.tokens * p.top_k > 4 * p.experts; }
-
-// A row's super-blocks in slices of at most 16, or 4 in the wide form.
-int slices_of(const mmq_q4K_moe_t& p, int inner) {
-    const int most = wide(p) ? kWideSlice : kWarps;
-    return (inner / 256 + most - 1) / most;
-}
+// A row's super-blocks in slices of at most 16.
+int slices_of(int inner) { return (inner / 256 + kWarps - 1) / kWarps; }
 
 struct Sizes {
-    size_t logits, h, parts, y, bytes;
+    size_t logits, h, y, bytes;
 };
 Sizes sizes(const mmq_q4K_moe_t& p) {
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
     Sizes z;
     const size_t pairs = size_t(p.tokens) * size_t(p.top_k);
-    const size_t gu = size_t(slices_of(p, p.model)), h = pairs * size_t(p.ffn) * 4;
+    const int gu = slices_of(p.model);
     z.logits = 0;
     z.h = z.logits + up(size_t(p.tokens) * size_t(p.experts) * 4);
-    z.parts = z.h + up(wide(p) || gu == 1 ? h : 2 * gu * h);
-    z.y = z.parts + (wide(p) ? up(2 * gu * h) : 0);
-    z.bytes = z.y + size_t(slices_of(p, p.ffn)) * pairs * size_t(p.model) * 4;
+    z.y = z.h + up(pairs * size_t(p.ffn) * 4 * (gu > 1 ? 2 * size_t(gu) : 1));
+    z.bytes = z.y + size_t(slices_of(p.ffn)) * pairs * size_t(p.model) * 4;
     return z;
 }
 
 template <bool kDown>
 cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
-    const bool is_wide = wide(a.p);
-    const int rows = kDown ? a.p.model : 2 * a.p.ffn, tile_rows = is_wide ? kWideRows : kRows;
+    const int rows = kDown ? a.p.model : 2 * a.p.ffn;
     Shape shape;
     shape.rows = rows;
     shape.nsb = (kDown ? a.p.ffn : a.p.model) / 256;
     shape.slices = kDown ? a.down_slices : a.gu_slices;
     shape.per = (shape.nsb + shape.slices - 1) / shape.slices;
     shape.teams = kWarps / shape.per;
-    shape.tiles = rows / tile_rows;
+    shape.tiles = rows / kRows;
     const uint64_t pitch = uint64_t(shape.nsb) * kBlk;
     CUtensorMap map;
     if (!encode_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, kDown ? a.p.w_down : a.p.w_gu, pitch,
-                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, uint32_t(tile_rows), CU_TENSOR_MAP_SWIZZLE_NONE))
+                   uint64_t(a.p.experts) * uint64_t(rows), pitch, kBlk, kRows, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
-    auto* const kernel = is_wide ? moe_wide_kernel<kDown> : moe_product_kernel<kDown>;
-    const int smem = is_wide ? kWideSmem : kSmemBytes;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
+    if ((e = cudaFuncSetAttribute(moe_product_kernel<kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)))
+        return e;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg =
-        follow_config(dim3(unsigned(nsm)), dim3(is_wide ? kWideThreads : kThreads), size_t(smem), s, attr);
-    return cudaLaunchKernelEx(&cfg, kernel, map, shape, a);
+    const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(kThreads), kSmemBytes, s, attr);
+    return cudaLaunchKernelEx(&cfg, moe_product_kernel<kDown>, map, shape, a);
 }
 
 }  // namespace
@@ -1234,22 +840,15 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     a.p = p;
     a.logits = reinterpret_cast<float*>(ws + z.logits);
     a.h = reinterpret_cast<float*>(ws + z.h);
-    a.parts = reinterpret_cast<float*>(ws + z.parts);
     a.y = reinterpret_cast<float*>(ws + z.y);
-    a.gu_slices = slices_of(p, p.model);
-    a.down_slices = slices_of(p, p.ffn);
+    a.gu_slices = slices_of(p.model);
+    a.down_slices = slices_of(p.ffn);
     a.status = status;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t first = launch_config(dim3(unsigned(p.experts), unsigned((p.tokens + 3) / 4)),
                                                    dim3(kRouterThreads), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
     if ((e = launch_product<false>(a, nsm, s))) return e;
-    if (wide(p)) {
-        cudaLaunchAttribute act_attr[1];
-        const cudaLaunchConfig_t act = follow_config(dim3(unsigned((p.ffn / 2 + 255) / 256), unsigned(p.tokens * p.top_k)),
-                                                     dim3(256), 0, s, act_attr);
-        if ((e = cudaLaunchKernelEx(&act, moe_act_kernel, a))) return e;
-    }
     if ((e = launch_product<true>(a, nsm, s))) return e;
     cudaLaunchAttribute last_attr[1];
     const cudaLaunchConfig_t last =
