@@ -24,7 +24,7 @@
 // The instructions that unpack and multiply a tile take 2100 cycles on an SM's
 // 16 warps, its bytes 3200 at the copy rate, so an expert with more than four
 // tokens, whose weights are unpacked once per four, is bound by them: 32 tokens
-// on 8 experts of 4096 x 11008 take 305 us where the bytes need 90.  Tried and
+// on 8 experts of 4096 x 11008 take 296 to 304 us where the bytes need 90.  Tried and
 // no faster: an expert's passes side by side, so that all but one find the
 // weights in the L2 (310 us); eight tokens a pass; the whole layer as one
 // cooperative kernel with barriers (32 tokens 329 us, one token 38 instead of
