@@ -537,8 +537,9 @@ size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t
  *     out = sum_i exp(s_i - max s) v_i / sum_i exp(s_i - max s)
  * and zeros for a token that sees no key.  Scores, the running maximum and
  * sum and the values' sum are f32; the weights are rounded to `type` for the
- * product with the values (a relative 2^-11 or 2^-8 per weight, unbiased), so
- * an f32 out is no more precise than that.  The prefix is read once for all:
+ * product with the values (a relative 2^-11 or 2^-8 per weight; f16 weights under
+ * 2^-21 of the row's largest instead by up to 2^-32 of it each), so an f32 out is
+ * no more precise than that.  The prefix is read once for all:
  * per kv head, 128 or 256 rows (a token and a head of the group each) share each
  * key tile.  Each token reads its own suffix by itself: q_len is meant for the
  * few tokens of a speculative step, not for a prefill.  What the caches hold

@@ -1,12 +1,15 @@
 // Attention of a batch whose sequences share one prefix: softmax over the
 // prefix keys, then each token's own paged suffix, in f32, computed in parts
 // and joined by the running maximum and sum:
-//   part p of a row:  m_p = max s,  l_p = sum 2^(s - m_p),  o_p = sum 2^(s - m_p) v
+//   part p of a row:  l_p = sum 2^(s - m_p),  o_p = sum 2^(s - m_p) v,  m_p a
+//                     reference near its largest s
 //   row:              out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p,  m = max m_p
 // with s = q.k * scale * log2(e).  A row with no key at all (an empty prefix
 // and an empty suffix) is zero.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "attention.h"
 #include "mmq_internal.h"
@@ -72,10 +75,14 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
 // suffixes are short.  Keys past the row's limit are filled with zeros, not
 // read, so what the cache holds there cannot matter.  Weights are rounded to
 // the cache's type for the second product (their sum is taken in f32 before
-// that); both products accumulate in f32.  Measured: 256 suffixes of 1 to 512
+// that); as fp16 their reference is 15 (in units of log2) under the largest
+// score, so that the largest is 2^15 and those down to 2^-29 of it are normal
+// numbers.  Both products accumulate in f32.  Measured: 256 suffixes of 1 to 512
 // tokens, 8 kv heads x 128 (261 MB): 50 us, 5.2 TB/s, 77 % of the copy rate (as
 // CTAs of four warps that join in shared memory: 66 us).
 constexpr int kSlab = 16, kStages = 3;
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f;   // of the weights, in units of log2
 
 template <int D>
 constexpr int row_smem() {
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_suffix_kernel(cons
             m0 = n0;
             m1 = n1;
         }
-        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+        const float b0 = m0 == -INFINITY ? 0.f : m0 - kLift<T>, b1 = m1 == -INFINITY ? 0.f : m1 - kLift<T>;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             x[k] = ex2(x[k] - b0);
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_suffix_kernel(cons
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
-        if (gcol == 0) a.part_ml[at] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+        if (gcol == 0) a.part_ml[at] = half ? make_float2(m1 - kLift<T>, l1) : make_float2(m0 - kLift<T>, l0);
     }
     if (last) griddep_wait();
 }

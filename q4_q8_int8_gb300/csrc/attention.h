@@ -11,8 +11,9 @@ namespace mmq {
 // row r of kv head h being token r / group, head h * group + r % group.  Each
 // part (a range of prefix keys, or a range of a token's own suffix) leaves
 // per (token, head) its unnormalised sum of weights x values, f32
-// [part][token][head][dim], and (m, l): its largest score in units of log2
-// and its sum of weights 2^(score - m); (-inf, 0) and no values for no keys.
+// [part][token][head][dim], and (m, l): a reference near its largest score, in
+// units of log2, and its sum of weights 2^(score - m); (-inf, 0) and no values
+// for no keys.
 struct AttnArgs {
     mmq_shared_prefix_attention_t p;
     float* part_o;

@@ -35,8 +35,12 @@
 // one's, polling instead of suspended waits.
 //
 // O is only scaled when a row's largest score (in units of log2) has grown by
-// more than 8 since the last time: P then stays below 2^8, far inside fp16's
-// range, and nothing is lost, since the factor is common to P, the sum and O.
+// more than 8 since the last time: nothing is lost, since the factor is common
+// to P, the sum and O.  P then stays below 2^8, and as fp16 below 2^15: its
+// reference is 7 under the score, which the rest of fp16's range has room for,
+// so that weights of down to 2^-21 of the largest are normal numbers and those
+// below it are off by at most 2^-32 of the largest.  (With P at most 2^8 the
+// last was 2^-25, and many keys that far under one that takes all were lost.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -63,6 +67,9 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S_i at 128 i (P_i over its first 64 columns), O_i at 256 + 128 i
 constexpr float kGrow = 8.f;
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;   // of P, in units of log2
+static_assert(kGrow + kLift<__half> < 16.f, "P within fp16's range");
 
 template <int D>
 struct Layout {
@@ -377,7 +384,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m;
+                const float base = m == -INFINITY ? 0.f : m - kLift<T>;
                 const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -424,7 +431,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 }
                 tc_fence_before();
             }
-            if (valid) a.part_ml[at] = make_float2(m, l);
+            if (valid) a.part_ml[at] = make_float2(m - kLift<T>, l);
         }
     }
 
