@@ -271,6 +271,16 @@ def _stream_ptr(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the current one), from that stream's own pool: a block that another
+    stream's pool has free may still be in use by work queued there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def q8_1_struct(qs, da, sa) -> mmq_q8_1_t:
     return mmq_q8_1_t(qs.data_ptr(), da.data_ptr(), sa.data_ptr())
 
@@ -652,6 +662,7 @@ def _torch():
 
 # One new token costs these calls a few microseconds on the device, so each
 # checks its arguments in a few flat expressions and calls the library once.
+# What a call with `stream` allocates, results among it, belongs to that stream.
 def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
                  eps: float = 1e-6, interleaved: bool = False, sections=None, out=None, stream=None):
     """Head norms, rotary positions and the cache write after a fused q/k/v projection.
@@ -697,7 +708,7 @@ def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, 
         if w is not None and (w.dtype is not f32 or not w.is_contiguous() or w.numel() != D or w.get_device() != dev):
             _refuse("qk_norm_rope: a norm weight must be float32 [D] on qkv's device")
     if out is None:
-        out = torch.empty((T, heads, D), dtype=dt, device=qkv.device)
+        out = _empty((T, heads, D), dt, qkv.device, stream)
     elif (out.dtype is not dt or not out.is_contiguous() or out.shape != (T, heads, D) or out.get_device() != dev):
         _refuse("qk_norm_rope: out must be contiguous [T][heads][D] of the cache's type, on qkv's device")
     p = mmq_qk_norm_rope_t(
@@ -765,7 +776,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
             or lens.dtype is not i32 or not lens.is_contiguous() or lens.numel() != batch or lens.get_device() != dev):
         _refuse("shared_prefix_attention: page_table must be int32 [batch][width], lens int32 [batch], on q's device")
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=q.device)
+        out = _empty(qs, dt, q.device, stream)
         out_kind = kind
     else:
         out_kind = MMQ_TYPE_F32 if out.dtype is torch.float32 else kind
@@ -796,10 +807,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
 def _workspace(need: int, device, stream, what: str):
     if not need:
         _refuse(f"{what}: sizes")
-    ws = _t.empty(need, dtype=_t.uint8, device=device)
-    if stream is not None:   # the allocator knows the current stream only
-        ws.record_stream(stream)
-    return ws
+    return _empty(need, _t.uint8, device, stream)
 
 
 def mmq_q4K_moe_workspace(p):
@@ -841,11 +849,11 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
                                  or residual.get_device() != dev):
         _refuse("q4K_moe: residual must be contiguous float32 [T][model] on x's device")
     if out is None:
-        out = torch.empty(xs, dtype=f32, device=device)
+        out = _empty(xs, f32, device, stream)
     elif out.dtype is not f32 or not out.is_contiguous() or out.shape != xs or out.get_device() != dev:
         _refuse("q4K_moe: out must be contiguous float32 [T][model] on x's device")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
-    weights = torch.empty((T, top_k), dtype=f32, device=device)
+    ids = _empty((T, top_k), torch.int32, device, stream)
+    weights = _empty((T, top_k), f32, device, stream)
     if T == 0:
         return out, ids, weights
     p = mmq_q4K_moe_t(x.data_ptr(), w_router.data_ptr(), w_gu.data_ptr(), w_down.data_ptr(),

@@ -1,0 +1,133 @@
+"""Memory that a call with stream= allocates comes from that stream's pool.
+
+The current stream's pool may hand out a block that work queued on the current
+stream still uses (the workspace of the call before, say), and the given stream
+does not wait for that work.  Shown without a GPU: stand-ins for the tensors,
+the library and the allocator, which notes the stream each block is for.
+"""
+import contextlib
+import types
+
+import pytest
+
+import q4_q8_int8_gb300 as mmq
+
+torch = pytest.importorskip("torch")
+
+
+class Tensor:
+    """What the binding asks of a CUDA tensor; no memory."""
+    made = 0
+
+    def __init__(self, shape, dtype, stride=None):
+        self.shape = torch.Size(shape if isinstance(shape, (tuple, list)) else (shape,))
+        self.dtype, self.device = dtype, "cuda:0"
+        Tensor.made += 1
+        self.at = Tensor.made << 32
+        steps, n = [], 1
+        for d in reversed(self.shape):
+            steps.insert(0, n)
+            n *= d
+        self.steps, self.n = stride or tuple(steps), n
+        self.contiguous = stride is None
+
+    def get_device(self):
+        return 0
+
+    def stride(self, i=None):
+        return self.steps if i is None else self.steps[i]
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return self.n
+
+    def dim(self):
+        return len(self.shape)
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return self.at
+
+    def record_stream(self, stream):
+        pass
+
+
+class Library:
+    """Every entry point: a size where one is asked for, else success."""
+    calls = None
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return 4096 if name.endswith(("workspace", "bytes")) else 0
+        return entry
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """(streams that blocks were allocated for, the library's calls)."""
+    now, blocks, lib = [None], [], Library()
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, now[0] = now[0], s
+        yield
+        now[0] = before
+
+    def empty(shape, dtype=None, device=None, pin_memory=False):
+        if not pin_memory:
+            blocks.append(now[0])
+        return Tensor(shape, dtype)
+
+    current = types.SimpleNamespace(cuda_stream=1, device_index=0, synchronize=lambda: None)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(mmq, "_lib", lib)
+    monkeypatch.setattr(mmq, "load_library", lambda *a: lib)
+    return types.SimpleNamespace(blocks=blocks, lib=lib, side=types.SimpleNamespace(
+        cuda_stream=77, device_index=0, synchronize=lambda: None))
+
+
+f16, f32, i32, u8 = torch.float16, torch.float32, torch.int32, torch.uint8
+
+
+def rope(**more):
+    mmq.qk_norm_rope(Tensor((3, 6 * 64), f32), 4, Tensor((9, 32), f32), Tensor((9, 32), f32), Tensor(3, i32),
+                     Tensor(3, i32), Tensor((8, 1, 64), f16), Tensor((8, 1, 64), f16), **more)
+
+
+def attention(**more):
+    mmq.shared_prefix_attention(Tensor((3, 4, 64), f16), Tensor((50, 2, 64), f16), Tensor((50, 2, 64), f16),
+                                Tensor((8, 16, 2, 64), f16), Tensor((8, 16, 2, 64), f16), Tensor((3, 2), i32),
+                                Tensor(3, i32), **more)
+
+
+def moe(**more):
+    mmq.q4K_moe(Tensor((3, 512), f32), Tensor((8, 512), f32), Tensor((8, 512, 2, 144), u8), Tensor((8, 512, 1, 144), u8), 2,
+                **more)
+
+
+OPERATORS = [(rope, 1), (attention, 2), (moe, 4)]
+
+
+@pytest.mark.parametrize("call,blocks", OPERATORS, ids=lambda v: getattr(v, "__name__", None))
+def test_layer_operators_allocate_on_the_given_stream(world, call, blocks):
+    call(stream=world.side)
+    assert world.blocks == [world.side] * blocks
+    name, args = world.lib.calls[-1]
+    assert args[-1] == 77
+    world.blocks.clear()
+    call()
+    assert world.blocks == [None] * blocks
+    assert world.lib.calls[-1][1][-1] == 1
