@@ -285,24 +285,24 @@ def q8_1_struct(qs, da, sa) -> mmq_q8_1_t:
     return mmq_q8_1_t(qs.data_ptr(), da.data_ptr(), sa.data_ptr())
 
 
-def empty_q8_1(M: int, K: int, device="cuda"):
+def empty_q8_1(M: int, K: int, device="cuda", stream=None):
     """Allocate (qs int8 [M][K], da f32 [M][K/32], sa int32 [M][K/32])."""
     import torch
-    return (torch.empty((M, K), dtype=torch.int8, device=device),
-            torch.empty((M, K // 32), dtype=torch.float32, device=device),
-            torch.empty((M, K // 32), dtype=torch.int32, device=device))
+    return (_empty((M, K), torch.int8, device, stream),
+            _empty((M, K // 32), torch.float32, device, stream),
+            _empty((M, K // 32), torch.int32, device, stream))
 
 
 def quantize_q8_1(x, out=None, stream=None):
     """x float32 [M][K] (CUDA, contiguous) -> (qs, da, sa) CUDA tensors."""
     M, K = x.shape
-    qs, da, sa = out if out is not None else empty_q8_1(M, K, x.device)
+    qs, da, sa = out if out is not None else empty_q8_1(M, K, x.device, stream)
     _check(mmq_quantize_q8_1(ctypes.c_void_p(x.data_ptr()), M, K, q8_1_struct(qs, da, sa),
                              _stream_ptr(stream)), "mmq_quantize_q8_1")
     return qs, da, sa
 
 
-def empty_tcop(M: int, K: int, device="cuda"):
+def empty_tcop(M: int, K: int, device="cuda", stream=None):
     """Allocate the tensor-core operand plane of M x K activations (uint8,
     mmq_q8_1_tcop_bytes(M, K) bytes; the caching allocator's blocks are
     256-byte aligned, which the call checks)."""
@@ -310,15 +310,15 @@ def empty_tcop(M: int, K: int, device="cuda"):
     n = mmq_q8_1_tcop_bytes(M, K)
     if n == 0:
         raise MMQError(MMQ_ERR_ARG, "mmq_q8_1_tcop_bytes")
-    return torch.empty((n,), dtype=torch.uint8, device=device)
+    return _empty((n,), torch.uint8, device, stream)
 
 
 def quantize_q8_1_tcop(x, out=None, tcop=None, stream=None):
     """x float32 [M][K] (CUDA) -> ((qs, da, sa), tcop): the q8_1 prepass that
     also writes the operand plane for q4K_gemm_tcop."""
     M, K = x.shape
-    qs, da, sa = out if out is not None else empty_q8_1(M, K, x.device)
-    tcop = tcop if tcop is not None else empty_tcop(M, K, x.device)
+    qs, da, sa = out if out is not None else empty_q8_1(M, K, x.device, stream)
+    tcop = tcop if tcop is not None else empty_tcop(M, K, x.device, stream)
     _check(mmq_quantize_q8_1_tcop(ctypes.c_void_p(x.data_ptr()), M, K, q8_1_struct(qs, da, sa),
                                   ctypes.c_void_p(tcop.data_ptr()), _stream_ptr(stream)),
            "mmq_quantize_q8_1_tcop")
@@ -328,7 +328,7 @@ def quantize_q8_1_tcop(x, out=None, tcop=None, stream=None):
 def q4K_gemm_tcop(tcop, w, M: int, N: int, K: int, out=None, stream=None):
     """The super-block tcgen05 GEMM on an operand plane -> C float32 [M][N]."""
     import torch
-    C = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=w.device)
+    C = out if out is not None else _empty((M, N), torch.float32, w.device, stream)
     _check(mmq_q4K_gemm_tcop(ctypes.c_void_p(tcop.data_ptr()), ctypes.c_void_p(w.data_ptr()),
                              ctypes.c_void_p(C.data_ptr()), M, N, K, _stream_ptr(stream)),
            "mmq_q4K_gemm_tcop")
@@ -340,7 +340,7 @@ def q4K_gemm(aq, w, N: int, path: int = MMQ_PATH_AUTO, out=None, stream=None):
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    C = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=qs.device)
+    C = out if out is not None else _empty((M, N), torch.float32, qs.device, stream)
     _check(mmq_q4K_gemm_path(q8_1_struct(qs, da, sa), ctypes.c_void_p(w.data_ptr()),
                              ctypes.c_void_p(C.data_ptr()), M, N, K, path, _stream_ptr(stream)),
            "mmq_q4K_gemm")
@@ -360,7 +360,7 @@ def q4K_gemm_host(x_host, w, N: int, out=None, workspace=None, stream=None):
     need = mmq_q4K_gemm_host_workspace(M, N, K)
     own = workspace is None
     if own:
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=w.device)
+        workspace = _empty(need + 256, torch.uint8, w.device, stream)
     base = (workspace.data_ptr() + 255) // 256 * 256
     avail = workspace.numel() - (base - workspace.data_ptr())
     sp = _stream_ptr(stream)
@@ -378,8 +378,8 @@ def q4K_gemm_q8_1(aq, w, N: int, with_c: bool = True, out=None, stream=None):
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    C = torch.empty((M, N), dtype=torch.float32, device=qs.device) if with_c else None
-    o = out if out is not None else empty_q8_1(M, N, qs.device)
+    C = _empty((M, N), torch.float32, qs.device, stream) if with_c else None
+    o = out if out is not None else empty_q8_1(M, N, qs.device, stream)
     _check(mmq_q4K_gemm_q8_1(q8_1_struct(qs, da, sa), ctypes.c_void_p(w.data_ptr()),
                              ctypes.c_void_p(C.data_ptr() if C is not None else 0), q8_1_struct(*o),
                              M, N, K, _stream_ptr(stream)),
@@ -392,7 +392,7 @@ def q4K_block_dots(aq, w, N: int, path: int = MMQ_PATH_AUTO, out=None, stream=No
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    S = out if out is not None else torch.empty((M, N, K // 32), dtype=torch.int32, device=qs.device)
+    S = out if out is not None else _empty((M, N, K // 32), torch.int32, qs.device, stream)
     _check(mmq_q4K_block_dots(q8_1_struct(qs, da, sa), ctypes.c_void_p(w.data_ptr()),
                               ctypes.c_void_p(S.data_ptr()), M, N, K, path, _stream_ptr(stream)),
            "mmq_q4K_block_dots")
@@ -404,7 +404,7 @@ def q4K_scaled_block_dots(aq, w, N: int, out=None, stream=None):
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    S = out if out is not None else torch.empty((M, N, K // 32), dtype=torch.int32, device=qs.device)
+    S = out if out is not None else _empty((M, N, K // 32), torch.int32, qs.device, stream)
     _check(mmq_q4K_scaled_block_dots(q8_1_struct(qs, da, sa), ctypes.c_void_p(w.data_ptr()),
                                      ctypes.c_void_p(S.data_ptr()), M, N, K, _stream_ptr(stream)),
            "mmq_q4K_scaled_block_dots")
@@ -439,7 +439,7 @@ def mmq_interleave_rows_q4K(gate, up, out, F, K, stream):
 def interleave_rows_q4K(gate, up, F: int, K: int, out=None, stream=None):
     """gate, up: q4_K bytes of F x K matrices (CUDA uint8) -> rows interleaved (2F x K)."""
     import torch
-    o = out if out is not None else torch.empty(2 * gate.numel(), dtype=torch.uint8, device=gate.device)
+    o = out if out is not None else _empty(2 * gate.numel(), torch.uint8, gate.device, stream)
     _check(mmq_interleave_rows_q4K(ctypes.c_void_p(gate.data_ptr()), ctypes.c_void_p(up.data_ptr()),
                                    ctypes.c_void_p(o.data_ptr()), F, K, _stream_ptr(stream)),
            "mmq_interleave_rows_q4K")
@@ -452,8 +452,8 @@ def q4K_gemm_swiglu_q8_1(aq, w_gu, F: int, with_h: bool = False, out=None, strea
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    h = torch.empty((M, F), dtype=torch.float32, device=qs.device) if with_h else None
-    o = out if out is not None else empty_q8_1(M, F, qs.device)
+    h = _empty((M, F), torch.float32, qs.device, stream) if with_h else None
+    o = out if out is not None else empty_q8_1(M, F, qs.device, stream)
     _check(mmq_q4K_gemm_swiglu_q8_1(q8_1_struct(qs, da, sa), ctypes.c_void_p(w_gu.data_ptr()),
                                     ctypes.c_void_p(h.data_ptr() if h is not None else 0), q8_1_struct(*o),
                                     M, F, K, _stream_ptr(stream)),
@@ -513,7 +513,7 @@ def pack_q6K(q, sc, d_bits):
 def repack_q6K(w, N: int, K: int, out=None, stream=None):
     """Customary q6_K bytes (CUDA uint8) -> the device layout the q6_K GEMM reads."""
     import torch
-    o = out if out is not None else torch.empty(N * (K // 256) * 224, dtype=torch.uint8, device=w.device)
+    o = out if out is not None else _empty(N * (K // 256) * 224, torch.uint8, w.device, stream)
     _check(mmq_repack_q6K(ctypes.c_void_p(w.data_ptr()), ctypes.c_void_p(o.data_ptr()), N, K,
                           _stream_ptr(stream)), "mmq_repack_q6K")
     return o
@@ -524,7 +524,7 @@ def q6K_gemm(aq, w_dev, N: int, path: int = MMQ_PATH_AUTO, out=None, stream=None
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    C = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=qs.device)
+    C = out if out is not None else _empty((M, N), torch.float32, qs.device, stream)
     _check(mmq_q6K_gemm_path(q8_1_struct(qs, da, sa), ctypes.c_void_p(w_dev.data_ptr()),
                              ctypes.c_void_p(C.data_ptr()), M, N, K, path, _stream_ptr(stream)), "mmq_q6K_gemm")
     return C
@@ -535,7 +535,7 @@ def q6K_block_dots(aq, w_dev, N: int, out=None, stream=None):
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    S = out if out is not None else torch.empty((M, N, K // 16), dtype=torch.int32, device=qs.device)
+    S = out if out is not None else _empty((M, N, K // 16), torch.int32, qs.device, stream)
     _check(mmq_q6K_block_dots(q8_1_struct(qs, da, sa), ctypes.c_void_p(w_dev.data_ptr()),
                               ctypes.c_void_p(S.data_ptr()), M, N, K, _stream_ptr(stream)), "mmq_q6K_block_dots")
     return S
@@ -547,7 +547,7 @@ def q6K_scaled_block_dots(aq, w_dev, N: int, out=None, stream=None):
     import torch
     qs, da, sa = aq
     M, K = qs.shape
-    S = out if out is not None else torch.empty((M, N, K // 32), dtype=torch.int32, device=qs.device)
+    S = out if out is not None else _empty((M, N, K // 32), torch.int32, qs.device, stream)
     _check(mmq_q6K_scaled_block_dots(q8_1_struct(qs, da, sa), ctypes.c_void_p(w_dev.data_ptr()),
                                      ctypes.c_void_p(S.data_ptr()), M, N, K, _stream_ptr(stream)),
            "mmq_q6K_scaled_block_dots")
@@ -595,7 +595,7 @@ def gguf_read(path: str):
 def dequantize_q4K_f16(w, N: int, K: int, out=None, stream=None):
     """q4_K bytes of an N x K matrix (CUDA uint8) -> float16 [N][K]."""
     import torch
-    wh = out if out is not None else torch.empty((N, K), dtype=torch.float16, device=w.device)
+    wh = out if out is not None else _empty((N, K), torch.float16, w.device, stream)
     _check(mmq_dequantize_q4K_f16(ctypes.c_void_p(w.data_ptr()), ctypes.c_void_p(wh.data_ptr()), N, K,
                                   _stream_ptr(stream)), "mmq_dequantize_q4K_f16")
     return wh
@@ -604,7 +604,7 @@ def dequantize_q4K_f16(w, N: int, K: int, out=None, stream=None):
 def convert_f16(x, out=None, stream=None):
     """float32 CUDA tensor -> float16 of the same shape (round to nearest even)."""
     import torch
-    xh = out if out is not None else torch.empty(x.shape, dtype=torch.float16, device=x.device)
+    xh = out if out is not None else _empty(x.shape, torch.float16, x.device, stream)
     _check(mmq_convert_f32_f16(ctypes.c_void_p(x.data_ptr()), ctypes.c_void_p(xh.data_ptr()), x.numel(),
                                _stream_ptr(stream)), "mmq_convert_f32_f16")
     return xh
@@ -615,7 +615,7 @@ def gemm_f16(a, b, out=None, stream=None):
     import torch
     M, K = a.shape
     N = b.shape[0]
-    C = out if out is not None else torch.empty((M, N), dtype=torch.float32, device=a.device)
+    C = out if out is not None else _empty((M, N), torch.float32, a.device, stream)
     _check(mmq_gemm_f16(ctypes.c_void_p(a.data_ptr()), ctypes.c_void_p(b.data_ptr()),
                         ctypes.c_void_p(C.data_ptr()), M, N, K, _stream_ptr(stream)), "mmq_gemm_f16")
     return C

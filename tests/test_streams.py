@@ -131,3 +131,40 @@ def test_layer_operators_allocate_on_the_given_stream(world, call, blocks):
     call()
     assert world.blocks == [None] * blocks
     assert world.lib.calls[-1][1][-1] == 1
+
+
+def q8(M, K):
+    return Tensor((M, K), torch.int8), Tensor((M, K // 32), f32), Tensor((M, K // 32), i32)
+
+
+W = 512 * 256 // 256 * 144      # bytes of a q4_K matrix, 512 x 256
+GEMMS = [
+    ("quantize_q8_1", lambda **m: mmq.quantize_q8_1(Tensor((4, 256), f32), **m), 3),
+    ("quantize_q8_1_tcop", lambda **m: mmq.quantize_q8_1_tcop(Tensor((4, 256), f32), **m), 4),
+    ("q4K_gemm_tcop", lambda **m: mmq.q4K_gemm_tcop(Tensor(4096, u8), Tensor(W, u8), 4, 512, 256, **m), 1),
+    ("q4K_gemm", lambda **m: mmq.q4K_gemm(q8(4, 256), Tensor(W, u8), 512, **m), 1),
+    ("q4K_gemm_host", lambda **m: mmq.q4K_gemm_host(Tensor((4, 256), f32), Tensor(W, u8), 512, **m), 1),
+    ("q4K_gemm_q8_1", lambda **m: mmq.q4K_gemm_q8_1(q8(4, 256), Tensor(W, u8), 512, **m), 4),
+    ("q4K_block_dots", lambda **m: mmq.q4K_block_dots(q8(4, 256), Tensor(W, u8), 512, **m), 1),
+    ("q4K_scaled_block_dots", lambda **m: mmq.q4K_scaled_block_dots(q8(4, 256), Tensor(W, u8), 512, **m), 1),
+    ("interleave_rows_q4K", lambda **m: mmq.interleave_rows_q4K(Tensor(W, u8), Tensor(W, u8), 512, 256, **m), 1),
+    ("q4K_gemm_swiglu_q8_1", lambda **m: mmq.q4K_gemm_swiglu_q8_1(q8(4, 256), Tensor(W, u8), 256, with_h=True, **m), 4),
+    ("repack_q6K", lambda **m: mmq.repack_q6K(Tensor(512 * 210, u8), 512, 256, **m), 1),
+    ("q6K_gemm", lambda **m: mmq.q6K_gemm(q8(4, 256), Tensor(512 * 224, u8), 512, **m), 1),
+    ("q6K_block_dots", lambda **m: mmq.q6K_block_dots(q8(4, 256), Tensor(512 * 224, u8), 512, **m), 1),
+    ("q6K_scaled_block_dots", lambda **m: mmq.q6K_scaled_block_dots(q8(4, 256), Tensor(512 * 224, u8), 512, **m), 1),
+    ("dequantize_q4K_f16", lambda **m: mmq.dequantize_q4K_f16(Tensor(W, u8), 512, 256, **m), 1),
+    ("convert_f16", lambda **m: mmq.convert_f16(Tensor((4, 256), f32), **m), 1),
+    ("gemm_f16", lambda **m: mmq.gemm_f16(Tensor((4, 256), f16), Tensor((512, 256), f16), **m), 1),
+]
+
+
+@pytest.mark.parametrize("call,blocks", [g[1:] for g in GEMMS], ids=[g[0] for g in GEMMS])
+def test_projections_allocate_on_the_given_stream(world, call, blocks):
+    call(stream=world.side)
+    assert world.blocks == [world.side] * blocks
+    assert world.lib.calls[-1][1][-1].value == 77
+    world.blocks.clear()
+    call()
+    assert world.blocks == [None] * blocks
+    assert world.lib.calls[-1][1][-1].value == 1
