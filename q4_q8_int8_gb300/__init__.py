@@ -650,6 +650,11 @@ def _refuse(what: str):
     raise MMQError(MMQ_ERR_ARG, what)
 
 
+# The library launches on the current device; a stream of another would be as wrong as memory of another.
+def _elsewhere(dev: int, stream) -> bool:
+    return dev < 0 or dev != _t._C._cuda_getDevice() or (stream is not None and stream.device_index != dev)
+
+
 _t = None   # torch, imported by the first call of one of these
 
 
@@ -687,8 +692,10 @@ def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, 
         kind = MMQ_TYPE_BF16
     else:
         _refuse("qk_norm_rope: the caches must be float16 or bfloat16")
-    if dev < 0 or qkv.dtype is not f32 or step != 1 or width != (heads + 2 * kv_heads) * D:
-        _refuse("qk_norm_rope: qkv must be float32 [T][(heads + 2 kv_heads) D] on the GPU")
+    if _elsewhere(dev, stream):
+        _refuse("qk_norm_rope: qkv and the stream must be on the current GPU")
+    if qkv.dtype is not f32 or step != 1 or width != (heads + 2 * kv_heads) * D:
+        _refuse("qk_norm_rope: qkv must be float32 [T][(heads + 2 kv_heads) D]")
     if (v_cache.dtype is not dt or v_cache.shape != kc or not k_cache.is_contiguous() or not v_cache.is_contiguous()
             or k_cache.get_device() != dev or v_cache.get_device() != dev):
         _refuse("qk_norm_rope: k_cache and v_cache must be alike and contiguous, on qkv's device")
@@ -761,8 +768,10 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     batch, width = page_table.shape
     q_step, q_head, q_one = q.stride()
     k_step, k_head, k_one = k_prefix.stride()
-    if dev < 0 or q_one != 1 or q_head != D or T != batch * q_len:
-        _refuse("shared_prefix_attention: q must be [batch q_len][heads][D] on the GPU, its heads contiguous")
+    if _elsewhere(dev, stream):
+        _refuse("shared_prefix_attention: q and the stream must be on the current GPU")
+    if q_one != 1 or q_head != D or T != batch * q_len:
+        _refuse("shared_prefix_attention: q must be [batch q_len][heads][D], its heads contiguous")
     if (k_prefix.dtype is not dt or v_prefix.dtype is not dt or v_prefix.shape != k_prefix.shape or pd != D
             or k_prefix.get_device() != dev or v_prefix.get_device() != dev
             or (P and (k_one != 1 or v_prefix.stride() != (k_step, k_head, 1)))):
@@ -837,8 +846,10 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
     E, rm = w_router.shape
     ge, gf, gs, gb = w_gu.shape
     de, dm, ds, db = w_down.shape
-    if dev < 0 or x.dtype is not f32 or not x.is_contiguous():
-        _refuse("q4K_moe: x must be contiguous float32 [T][model] on the GPU")
+    if _elsewhere(dev, stream):
+        _refuse("q4K_moe: x and the stream must be on the current GPU")
+    if x.dtype is not f32 or not x.is_contiguous():
+        _refuse("q4K_moe: x must be contiguous float32 [T][model]")
     if w_router.dtype is not f32 or not w_router.is_contiguous() or rm != model or w_router.get_device() != dev:
         _refuse("q4K_moe: w_router must be contiguous float32 [E][model] on x's device")
     if (w_gu.dtype is not u8 or not w_gu.is_contiguous() or ge != E or gf != 512 * ds or gs * 256 != model or gb != 144
