@@ -361,6 +361,8 @@ def q4K_gemm_host(x_host, w, N: int, out=None, workspace=None, stream=None):
     own = workspace is None
     if own:
         workspace = _empty(need + 256, torch.uint8, w.device, stream)
+    elif not workspace.is_contiguous():
+        raise MMQError(MMQ_ERR_ARG, "q4K_gemm_host: workspace must be contiguous")
     base = (workspace.data_ptr() + 255) // 256 * 256
     avail = workspace.numel() - (base - workspace.data_ptr())
     sp = _stream_ptr(stream)
@@ -803,8 +805,8 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     lib = _lib or load_library()
     if workspace is None:
         workspace = _workspace(lib.mmq_shared_prefix_attention_workspace(p), q.device, stream, "shared_prefix_attention")
-    elif workspace.get_device() != dev:
-        _refuse("shared_prefix_attention: workspace must be on q's device")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("shared_prefix_attention: workspace must be contiguous, on q's device")
     rc = lib.mmq_shared_prefix_attention(
         p, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
@@ -873,8 +875,8 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
     lib = _lib or load_library()
     if workspace is None:
         workspace = _workspace(lib.mmq_q4K_moe_workspace(p), device, stream, "q4K_moe")
-    elif workspace.get_device() != dev:
-        _refuse("q4K_moe: workspace must be on x's device")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("q4K_moe: workspace must be contiguous, on x's device")
     rc = lib.mmq_q4K_moe(p, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                          torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if rc:

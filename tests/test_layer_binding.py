@@ -39,3 +39,15 @@ def test_a_stream_of_another_device(world, call):  # noqa: F811
 def test_tensors_on_the_host(world, call, monkeypatch):  # noqa: F811
     monkeypatch.setattr(Tensor, "get_device", lambda self: -1)
     refused(world, call)
+
+
+def host_gemm(**more):
+    mmq.q4K_gemm_host(Tensor((4, 256), torch.float32), Tensor(512 * 144, torch.uint8), 512, **more)
+
+
+@pytest.mark.parametrize("call", [attention, moe, host_gemm], ids=lambda c: c.__name__)
+def test_a_workspace_that_is_not_contiguous(world, call):  # noqa: F811
+    """Its values reach past its storage (expanded), or lie between another's (strided)."""
+    for stride in ((0,), (2,)):
+        refused(world, call, workspace=Tensor(1 << 20, torch.uint8, stride=stride))
+    call(workspace=Tensor(1 << 20, torch.uint8))
