@@ -274,7 +274,7 @@ def _stream_ptr(stream=None):
 def _empty(shape, dtype, device, stream):
     """Memory for a call on `stream` (None: the current one), from that stream's own pool: a block that another
     stream's pool has free may still be in use by work queued there."""
-    import torch
+    torch = _t or _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
