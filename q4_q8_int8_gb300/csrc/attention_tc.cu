@@ -265,9 +265,9 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         mma_commit(s_full(g));
                         mma_commit(empty(int(slot)));
                     };
-                    if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
-                    q_phase ^= 1u;
-                    if (mine > 0) {
+                    if (kTwo || mine > 0) {
+                        if (!wait_bounded(q_full(g), q_phase, abort_flag, status)) goto mma_done;
+                        q_phase ^= 1u;
                         if (!arrived(k_at(0))) goto mma_done;
                         tc_fence_after();
                         scores(k_at(0) % kSlots, false);
@@ -322,6 +322,15 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             const bool valid = r < rows;
             const int64_t tok = valid ? r / a.group : 0;
             const int head = int(w.h * a.group + (valid ? r - tok * a.group : 0));
+            const int mine = kTwo ? w.tiles : (w.tiles + 1 - g) >> 1;
+            const int part = kTwo ? w.part : 2 * w.part + g;
+            const int64_t at = (int64_t(part) * a.tokens + tok) * p.heads + head;
+            // An item of one tile has none for group 1, which does not arrive on q_full for it either: it would wait
+            // for nothing here, and be a phase of that barrier ahead before the issuer has seen this one.
+            if (!kTwo && mine == 0) {
+                if (valid) a.part_ml[at] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
             // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.
             {
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + tok * p.q_stride + int64_t(head) * D);
@@ -335,7 +344,6 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full(g));
             }
-            const int mine = kTwo ? w.tiles : (w.tiles + 1 - g) >> 1;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int n = 0; n < mine && ok; ++n) {
@@ -408,29 +416,25 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 l += lo_f(sum[0]) + hi_f(sum[0]);
             }
             // The part's result.
-            const int part = kTwo ? w.part : 2 * w.part + g;
-            const int64_t at = (int64_t(part) * a.tokens + tok) * p.heads + head;
             if (!ok) break;
-            if (mine > 0) {
-                ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
-                if (!ok) break;
-                o_phase ^= 1u;
-                tc_fence_after();
+            ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
+            if (!ok) break;
+            o_phase ^= 1u;
+            tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
-                    tmem_wait_ld(o);
-                    if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + 32 * c);
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+                tmem_wait_ld(o);
+                if (valid) {
+                    float4* dst = reinterpret_cast<float4*>(a.part_o + at * D + 32 * c);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                             __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
                 }
-                tc_fence_before();
             }
+            tc_fence_before();
             if (valid) a.part_ml[at] = make_float2(m - kLift<T>, l);
         }
     }
