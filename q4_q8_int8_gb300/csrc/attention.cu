@@ -525,8 +525,9 @@ size_t shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t& p)
     AttnArgs a;
     a.p = p;
     plan(a, nsm);
-    return ml_bytes(a) + size_t(a.prefix_parts + a.suffix_parts) * size_t(a.tokens) * size_t(p.heads) *
-                             size_t(p.head_dim) * sizeof(float);
+    const size_t need = ml_bytes(a) + size_t(a.prefix_parts + a.suffix_parts) * size_t(a.tokens) * size_t(p.heads) *
+                                          size_t(p.head_dim) * sizeof(float);
+    return need ? need : 256;   // no prefix and no page: no parts, but 0 stands for an error
 }
 
 cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& p, void* workspace, int* status,
