@@ -326,6 +326,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
     const int64_t rows = a.tokens * a.p.heads;
     const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / kWarpsPerRow) + warp / kWarpsPerRow;
     const int parts = row < rows ? a.prefix_parts + a.suffix_parts : 0;
+    // An empty page table has no suffix kernel to say that a length is past it.
+    if (a.suffix_parts == 0 && lane == 0 && row < rows && a.p.lens[row / a.p.heads / a.p.q_len] > 0)
+        atomicCAS(a.status, 0, MMQ_ERR_ARG);
     const float2 none = make_float2(-INFINITY, 0.f);
     const float2 ml0 = lane < parts ? a.part_ml[lane * rows + row] : none;
     float m = ml0.x;
