@@ -427,7 +427,7 @@ int mmq_gguf_write(const char* path, int64_t n, const char* const* names,
 
 /* Synchronizes `stream`, then returns and clears the current device's status
  * word: MMQ_OK, or MMQ_ERR_DEVICE_TIMEOUT if a kernel's bounded wait gave up
- * since the last call (that kernel's output is then invalid), or MMQ_ERR_ARG
+ * since the last call (that kernel's output is then invalid), or else MMQ_ERR_ARG
  * if a kernel met a position, slot, page or length out of range (the calls
  * that read such say what became of them), or MMQ_ERR_CUDA if the
  * synchronization itself failed. */

@@ -113,7 +113,8 @@ struct AbortFlag {
 
 // Wait for phase `parity` of `bar`.  Returns false (without waiting further)
 // if another thread of the CTA already aborted, or after kWaitLimitNs, in
-// which case it raises the CTA's abort flag and the device status word.
+// which case it raises the CTA's abort flag and the device status word, there
+// over whatever another kernel found wrong in its arguments.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, AbortFlag abort_flag,
                                              int* status) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -123,7 +124,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, Abor
         if (abort_flag.raised()) return false;
         if (globaltimer() - t0 > kWaitLimitNs) {
             abort_flag.set(1u);
-            atomicCAS(status, 0, MMQ_ERR_DEVICE_TIMEOUT);
+            atomicExch(status, MMQ_ERR_DEVICE_TIMEOUT);
             return false;
         }
     }
@@ -140,7 +141,7 @@ __device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t pari
         if (abort_flag.raised()) return false;
         if (globaltimer() - t0 > kWaitLimitNs) {
             abort_flag.set(1u);
-            atomicCAS(status, 0, MMQ_ERR_DEVICE_TIMEOUT);
+            atomicExch(status, MMQ_ERR_DEVICE_TIMEOUT);
             return false;
         }
     }
@@ -152,7 +153,7 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, int* s
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(bar, parity)) {
         if (globaltimer() - t0 > kWaitLimitNs) {
-            atomicCAS(status, 0, MMQ_ERR_DEVICE_TIMEOUT);
+            atomicExch(status, MMQ_ERR_DEVICE_TIMEOUT);
             return false;
         }
     }
