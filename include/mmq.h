@@ -579,8 +579,8 @@ typedef struct {
 size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p);
 
 /* Per token: p = softmax(x . w_router^T); the top_k experts with the largest
- * p (ties: the lower number; a NaN ranks last); w their p, or p over the
- * chosen p's sum; and
+ * p (ties: the lower number, so also where a logit of NaN or +Inf makes all of
+ * a token's p NaN); w their p, or p over the chosen p's sum; and
  *     out = residual + sum over the chosen e of w_e * h_e . Wd_e^T,
  *     h_e = silu(x . Wg_e^T) * (x . Wu_e^T),  silu(g) = g / (1 + exp(-g)).
  * The activations x and h are not quantized: each product takes them as the

@@ -130,8 +130,9 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 
 // One warp: token t's softmax and its top_k experts, best first.  A choice is
 // two warp reductions over keys that order the values e^(logit - max), from 0
-// to 1 and so by their bits; NaN ranks below every number, so the chosen
-// experts are always distinct and in range.
+// to 1 and so by their bits.  A NaN or +Inf among the logits makes the sum and
+// with it every softmax value NaN: all keys are equal then, the lowest experts
+// are taken, distinct and in range as always, with weights of NaN.
 __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* ids, uint64_t* tokens_of, bool store) {
     const mmq_q4K_moe_t& p = a.p;
     constexpr int kPer = kMaxExperts / 32;
@@ -156,8 +157,12 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, int lane, int* i
         if (lane + 32 * j < p.experts) {
             v[j] = expf(v[j] - top);
             sum += v[j];
-            key[j] = v[j] == v[j] ? __float_as_uint(v[j]) + 2u : 1u;
+            key[j] = __float_as_uint(v[j]) + 2u;
         }
+    }
+    if (__any_sync(0xffffffffu, sum != sum)) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) key[j] = key[j] ? 1u : 0u;
     }
     float picked = 0.f, mine = 0.f;   // lane i keeps the i-th choice
     int chosen = 0;
