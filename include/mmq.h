@@ -604,8 +604,9 @@ int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes,
  * integer dots and the tolerance do not. */
 int mmq_debug_force_gemv_split(int ks);
 
-/* Test hook: when nonzero, the next tensor-core GEMM launch on this host
- * thread withholds one producer arrival so that its consumers' bounded
+/* Test hook: when nonzero, the next launch on this host thread of a
+ * tensor-core GEMM, an attention call with a prefix or a mixture of experts
+ * withholds one producer arrival so that its consumers' bounded
  * waits run out; the kernel then records MMQ_ERR_DEVICE_TIMEOUT and returns
  * without hanging.  Used only to test the failure path. */
 void mmq_debug_inject_timeout(int enable);

@@ -524,7 +524,13 @@ int mmq_shared_prefix_attention(const mmq_shared_prefix_attention_t* p, void* wo
     if (workspace_bytes < need) return MMQ_ERR_ARG;
     int* status = mmq::status_word_ptr();
     if (!status) return MMQ_ERR_CUDA;
-    const cudaError_t e = mmq::launch_shared_prefix_attention(*p, workspace, status, static_cast<cudaStream_t>(stream));
+    int inject = 0;
+    if (p->prefix > 0) {   // the suffix kernel and the join wait for nothing
+        inject = t_inject_timeout;
+        t_inject_timeout = 0;
+    }
+    const cudaError_t e =
+        mmq::launch_shared_prefix_attention(*p, workspace, status, inject, static_cast<cudaStream_t>(stream));
     // the tensor-core kernel's register split does not fit this build of it
     return e == cudaErrorLaunchOutOfResources ? MMQ_ERR_RESOURCE : from_cuda(e);
 }
@@ -571,7 +577,9 @@ int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes,
     if (workspace_bytes < need) return MMQ_ERR_ARG;
     int* status = mmq::status_word_ptr();
     if (!status) return MMQ_ERR_CUDA;
-    return from_cuda(mmq::launch_q4K_moe(*p, workspace, status, static_cast<cudaStream_t>(stream)));
+    const int inject = t_inject_timeout;
+    t_inject_timeout = 0;
+    return from_cuda(mmq::launch_q4K_moe(*p, workspace, status, inject, static_cast<cudaStream_t>(stream)));
 }
 
 int mmq_status(void* stream) {

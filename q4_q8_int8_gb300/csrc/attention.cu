@@ -534,13 +534,14 @@ size_t shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t& p)
 }
 
 cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& p, void* workspace, int* status,
-                                           cudaStream_t s) {
+                                           int inject_timeout, cudaStream_t s) {
     const int nsm = sm_count();
     if (!nsm) return cudaErrorInvalidDevice;
     AttnArgs a;
     a.p = p;
     plan(a, nsm);
     a.status = status;
+    a.inject = inject_timeout;
     a.part_ml = static_cast<float2*>(workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a));
     if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);

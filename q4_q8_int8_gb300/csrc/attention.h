@@ -25,6 +25,7 @@ struct AttnArgs {
     int prefix_parts;     // parts 0 .. prefix_parts - 1
     int64_t part_keys;    // prefix keys per part, a multiple of the kernel's key tile
     int suffix_parts;     // the parts after them
+    int inject;           // test hook: the prefix kernel's first CTA withholds one key tile
     bool beside;          // the suffix kernel follows a prefix kernel, which it does not depend on
     int page_shift;
     float scale_log2;     // scale * log2(e)

@@ -200,15 +200,19 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 Ring<kSlots> r;
                 int issued[kSlots] = {};
                 uint32_t par[kSlots] = {};
+                bool withhold = a.inject && blockIdx.x == 0;
                 auto load = [&](const CUtensorMap* map, int h, int64_t key) {
                     if (!wait_bounded(empty(r.slot), r.phase ^ 1u, abort_flag, status)) return false;
                     const uint32_t dst = sbase + uint32_t(L::kOffRing + r.slot * L::kTile);
-                    mbar_arrive_expect_tx(full(r.slot), uint32_t(L::kTile));
+                    if (!withhold) {
+                        mbar_arrive_expect_tx(full(r.slot), uint32_t(L::kTile));
 #pragma unroll
-                    for (int c = 0; c < L::kPanels; ++c)
-                        tma_load_3d(dst + uint32_t(c * L::kPanel), map, full(r.slot), 64 * c, h, int32_t(key));
-                    issued[r.slot] = 1;
-                    par[r.slot] = r.phase;
+                        for (int c = 0; c < L::kPanels; ++c)
+                            tma_load_3d(dst + uint32_t(c * L::kPanel), map, full(r.slot), 64 * c, h, int32_t(key));
+                        issued[r.slot] = 1;
+                        par[r.slot] = r.phase;
+                    }
+                    withhold = false;
                     r.next();
                     return true;
                 };

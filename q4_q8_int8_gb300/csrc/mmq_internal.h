@@ -154,10 +154,10 @@ cudaError_t launch_qk_norm_rope(const mmq_qk_norm_rope_t& p, int* status, cudaSt
 // Shared-prefix attention (attention.cu); batch >= 1.
 size_t shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t& p);   // 0 on a CUDA error
 cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& p, void* workspace, int* status,
-                                           cudaStream_t s);
+                                           int inject_timeout, cudaStream_t s);
 // Mixture of q4_K experts for a few tokens (moe.cu); tokens >= 1.
 size_t q4K_moe_workspace(const mmq_q4K_moe_t& p);   // 0 on a CUDA error
-cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status, cudaStream_t s);
+cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status, int inject_timeout, cudaStream_t s);
 int small_m_launch_count(int64_t M, int64_t N, int64_t K);   // kernels per call, -1 on a CUDA error
 constexpr int64_t kSmallMMax = 64;
 

@@ -707,9 +707,11 @@ struct Layer {
 //
 // Every CTA makes the plan from the logits.  The second product does so, and
 // asks for its first weights, before it waits for the first one's results.
+// `inject`, a test hook: 1 more arrival than there will be on the first CTA's
+// barriers for full batches.
 template <bool kDown>
 __global__ void __launch_bounds__(kThreads, 1)
-moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, const MoeArgs a) {
+moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, const MoeArgs a, const int inject) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ Plan plan;
@@ -725,7 +727,7 @@ moe_product_kernel(const __grid_constant__ CUtensorMap map, const Shape shape, c
     if (threadIdx.x == 0) {
         layer.abort_flag.set(0u);
         for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(layer.red_full + 8u * uint32_t(i), kWarps);
+            mbar_init(layer.red_full + 8u * uint32_t(i), kWarps + (!kDown && blockIdx.x == 0 ? inject : 0));
             mbar_init(layer.red_empty + 8u * uint32_t(i), 1);
         }
         prefetch_tmap(&map);
@@ -807,7 +809,7 @@ Sizes sizes(const mmq_q4K_moe_t& p) {
 }
 
 template <bool kDown>
-cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
+cudaError_t launch_product(const MoeArgs& a, int nsm, int inject, cudaStream_t s) {
     const int rows = kDown ? a.p.model : 2 * a.p.ffn;
     Shape shape;
     shape.rows = rows;
@@ -826,7 +828,7 @@ cudaError_t launch_product(const MoeArgs& a, int nsm, cudaStream_t s) {
         return e;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = follow_config(dim3(unsigned(nsm)), dim3(kThreads), kSmemBytes, s, attr);
-    return cudaLaunchKernelEx(&cfg, moe_product_kernel<kDown>, map, shape, a);
+    return cudaLaunchKernelEx(&cfg, moe_product_kernel<kDown>, map, shape, a, inject);
 }
 
 }  // namespace
@@ -835,7 +837,7 @@ namespace mmq {
 
 size_t q4K_moe_workspace(const mmq_q4K_moe_t& p) { return sizes(p).bytes; }
 
-cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status, cudaStream_t s) {
+cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status, int inject_timeout, cudaStream_t s) {
     int dev = 0, nsm = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) || (e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev))) return e;
@@ -853,8 +855,8 @@ cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status,
     const cudaLaunchConfig_t first = launch_config(dim3(unsigned(p.experts), unsigned((p.tokens + 3) / 4)),
                                                    dim3(kRouterThreads), 0, s, attr);
     if ((e = cudaLaunchKernelEx(&first, moe_router_kernel, a))) return e;
-    if ((e = launch_product<false>(a, nsm, s))) return e;
-    if ((e = launch_product<true>(a, nsm, s))) return e;
+    if ((e = launch_product<false>(a, nsm, inject_timeout, s))) return e;
+    if ((e = launch_product<true>(a, nsm, 0, s))) return e;
     cudaLaunchAttribute last_attr[1];
     const cudaLaunchConfig_t last =
         follow_config(dim3(unsigned((p.model / 4 + 127) / 128), unsigned(p.tokens)), dim3(128), 0, s, last_attr);
