@@ -320,15 +320,16 @@ template <int D, int kWarpsPerRow>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnArgs a) {
     griddep_launch_dependents();
     griddep_wait();
+    if (a.suffix_parts == 0) {   // an empty page table: no suffix kernel says that a length is past it
+        const int64_t b = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;   // at least one thread per sequence
+        if (b < a.p.batch && a.p.lens[b] > 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+    }
     constexpr int kVec = D / 32;   // values per lane
     __shared__ float sums[kWarpsPerRow > 1 ? kJoinWarps : 1][kVec][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, turn = warp % kWarpsPerRow;
     const int64_t rows = a.tokens * a.p.heads;
     const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / kWarpsPerRow) + warp / kWarpsPerRow;
     const int parts = row < rows ? a.prefix_parts + a.suffix_parts : 0;
-    // An empty page table has no suffix kernel to say that a length is past it.
-    if (a.suffix_parts == 0 && lane == 0 && row < rows && a.p.lens[row / a.p.heads / a.p.q_len] > 0)
-        atomicCAS(a.status, 0, MMQ_ERR_ARG);
     const float2 none = make_float2(-INFINITY, 0.f);
     const float2 ml0 = lane < parts ? a.part_ml[lane * rows + row] : none;
     float m = ml0.x;
