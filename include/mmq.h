@@ -538,8 +538,8 @@ size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t
  * and zeros for a token that sees no key.  Scores, the running maximum and
  * sum and the values' sum are f32; the weights are rounded to `type` for the
  * product with the values (a relative 2^-11 or 2^-8 per weight; f16 weights under
- * 2^-21 of the row's largest instead by up to 2^-32 of it each), so an f32 out is
- * no more precise than that.  The prefix is read once for all:
+ * 2^-21 of the row's largest instead by up to 2^-32 of it each; with scores past
+ * 2^20, under 2^-14 by up to 2^-25), so an f32 out is no more precise than that.  The prefix is read once for all:
  * per kv head, 128 or 256 rows (a token and a head of the group each) share each
  * key tile.  Each token reads its own suffix by itself: q_len is meant for the
  * few tokens of a speculative step, not for a prefill.  What the caches hold

@@ -75,14 +75,14 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
 // suffixes are short.  Keys past the row's limit are filled with zeros, not
 // read, so what the cache holds there cannot matter.  Weights are rounded to
 // the cache's type for the second product (their sum is taken in f32 before
-// that); as fp16 their reference is 15 (in units of log2) under the largest
-// score, so that the largest is 2^15 and those down to 2^-29 of it are normal
-// numbers.  Both products accumulate in f32.  Measured: 256 suffixes of 1 to 512
+// that); as fp16 their reference is 7 (in units of log2) under the largest
+// score, so that those down to 2^-21 of the largest are normal numbers, and for
+// no score, however it is rounded, more than 8.  Both products accumulate in f32.  Measured: 256 suffixes of 1 to 512
 // tokens, 8 kv heads x 128 (261 MB): 50 us, 5.2 TB/s, 77 % of the copy rate (as
 // CTAs of four warps that join in shared memory: 66 us).
 constexpr int kSlab = 16, kStages = 3;
 template <typename T>
-constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f;   // of the weights, in units of log2
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;   // of the weights, in units of log2
 
 template <int D>
 constexpr int row_smem() {
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_suffix_kernel(cons
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int key = (k & 2 ? 8 : 0) + 2 * gcol + (k & 1);
-            x[k] = key < left ? x[k] * a.scale_log2 : -INFINITY;
+            x[k] = key < left ? __fmul_rn(x[k], a.scale_log2) : -INFINITY;
         }
         float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), t1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(32, row_resident<D>()) attn_suffix_kernel(cons
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
         const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
         if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-            // (-inf) - (-inf) only where the sums are still zero
-            const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+            // (-inf) - (-inf) only where the sums are still zero; m - kLift as it is rounded below
+            const float f0 = n0 == -INFINITY ? 1.f : ex2((m0 - kLift<T>) - (n0 - kLift<T>));
+            const float f1 = n1 == -INFINITY ? 1.f : ex2((m1 - kLift<T>) - (n1 - kLift<T>));
             l0 *= f0;
             l1 *= f1;
 #pragma unroll

@@ -70,6 +70,12 @@ constexpr float kGrow = 8.f;
 template <typename T>
 constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;   // of P, in units of log2
 static_assert(kGrow + kLift<__half> < 16.f, "P within fp16's range");
+constexpr float kWide = 0x1p20f;
+// What is subtracted from a row's scores, for a largest one of m, or none yet.
+template <typename T>
+__device__ __forceinline__ float reference(float m) {
+    return m == -INFINITY ? 0.f : fabsf(m) < kWide ? m - kLift<T> : m;
+}
 
 template <int D>
 struct Layout {
@@ -349,8 +355,21 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (lane == 0) mbar_arrive(q_full(g));
             }
             float m = -INFINITY, l = 0.f;
-            bool ok = true;
-            for (int n = 0; n < mine && ok; ++n) {
+            bool ok = true, wide = false;
+            int n = 0;
+            auto scale_o = [&](float f) {   // at rest: the product before this S has completed
+                l *= f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st_32x32b_x32(to + 32u * uint32_t(c), o);
+                }
+            };
+            for (; n < mine && ok; ++n) {
                 ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
                 if (!ok) break;
                 s_phase ^= 1u;
@@ -380,23 +399,12 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
                 if (__any_sync(0xffffffffu, n == 0 || top > m + kGrow)) {
                     const float was = m;
+                    wide = __any_sync(0xffffffffu, !(fabsf(fmaxf(m, top)) < kWide));
+                    if (wide) break;
                     m = fmaxf(m, top);
-                    if (n > 0) {
-                        // O is at rest: the product before this S has completed.
-                        const float f = was == m ? 1.f : ex2(was - m);
-                        l *= f;
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
-                            tmem_wait_ld(o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st_32x32b_x32(to + 32u * uint32_t(c), o);
-                        }
-                    }
+                    if (n > 0) scale_o(was == m ? 1.f : ex2(was - m));
                 }
-                const float base = m == -INFINITY ? 0.f : m - kLift<T>;
+                const float base = m - kLift<T>;
                 const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -419,6 +427,53 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 sum[0] = fadd2(sum[0], sum[1]);
                 l += lo_f(sum[0]) + hi_f(sum[0]);
             }
+            // S scale - m in one step, as above, is past zero by what m lost in its rounding, half a unit in its last
+            // place: from 2^20 on too much for P's range.  From the first tile where a row of the warp gets there the
+            // products are rounded first, as m was, and m is neither lifted nor let behind (nor is a row left out that
+            // has no score above -Inf).  No usual call comes here, so short loops over S where it lies.
+            for (bool here = true; wide && n < mine; ++n, here = false) {
+                if (!here) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
+                    if (!ok) break;
+                    s_phase ^= 1u;
+                    tc_fence_after();
+                }
+                const int64_t left = w.k1 - (w.k0 + int64_t(kTwo ? n : 2 * n + g) * kKeys);
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
+                    tmem_wait_ld(x);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * c + k < left) top = fmaxf(top, __uint_as_float(x[k]));
+                }
+                const float was = m;
+                m = fmaxf(m, __fmul_rn(top, a.scale_log2));
+                const float base = reference<T>(m);
+                if (n > 0) scale_o(was == -INFINITY ? 0.f : ex2(reference<T>(was) - base));
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32], pk[16];
+                    tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
+                    tmem_wait_ld(x);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float y = __fmul_rn(__uint_as_float(x[k]), a.scale_log2);
+                        x[k] = 32 * c + k < left ? __float_as_uint(ex2(__fsub_rn(y, base))) : 0u;
+                        sum += __uint_as_float(x[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) pk[k] = pack16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), tag);
+                    tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);   // over what has been read
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(g));
+                l += sum;
+            }
             // The part's result.
             if (!ok) break;
             ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
@@ -439,7 +494,7 @@ attn_prefix_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 }
             }
             tc_fence_before();
-            if (valid) a.part_ml[at] = make_float2(m - kLift<T>, l);
+            if (valid) a.part_ml[at] = make_float2(m == -INFINITY ? m : reference<T>(m), l);
         }
     }
 
