@@ -770,13 +770,14 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     batch, width = page_table.shape
     q_step, q_head, q_one = q.stride()
     k_step, k_head, k_one = k_prefix.stride()
+    v_step, v_head, v_one = v_prefix.stride() if v_prefix.dim() == 3 else (0, 0, 0)
     if _elsewhere(dev, stream):
         _refuse("shared_prefix_attention: q and the stream must be on the current GPU")
-    if q_one != 1 or q_head != D or T != batch * q_len:
+    if q_one != 1 or (q_head != D and heads > 1) or T != batch * q_len:
         _refuse("shared_prefix_attention: q must be [batch q_len][heads][D], its heads contiguous")
     if (k_prefix.dtype is not dt or v_prefix.dtype is not dt or v_prefix.shape != k_prefix.shape or pd != D
             or k_prefix.get_device() != dev or v_prefix.get_device() != dev
-            or (P and (k_one != 1 or v_prefix.stride() != (k_step, k_head, 1)))):
+            or (P and (k_one != 1 or v_one != 1 or (P > 1 and v_step != k_step) or (kv_heads > 1 and v_head != k_head)))):
         _refuse("shared_prefix_attention: k_prefix and v_prefix must be alike, [P][kv_heads][D] in q's type, on q's device")
     if (k_cache.dtype is not dt or v_cache.dtype is not dt or v_cache.shape != k_cache.shape or ch != kv_heads or cd != D
             or not k_cache.is_contiguous() or not v_cache.is_contiguous() or k_cache.get_device() != dev
