@@ -652,11 +652,6 @@ def _refuse(what: str):
     raise MMQError(MMQ_ERR_ARG, what)
 
 
-# The library launches on the current device; a stream of another would be as wrong as memory of another.
-def _elsewhere(dev: int, stream) -> bool:
-    return dev < 0 or dev != _t._C._cuda_getDevice() or (stream is not None and stream.device_index != dev)
-
-
 _t = None   # torch, imported by the first call of one of these
 
 
@@ -669,6 +664,8 @@ def _torch():
 
 # One new token costs these calls a few microseconds on the device, so each
 # checks its arguments in a few flat expressions and calls the library once.
+# The library launches on the current device, so memory and streams of another
+# are refused.
 # What a call with `stream` allocates, results among it, belongs to that stream.
 def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
                  eps: float = 1e-6, interleaved: bool = False, sections=None, out=None, stream=None):
@@ -694,7 +691,7 @@ def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, 
         kind = MMQ_TYPE_BF16
     else:
         _refuse("qk_norm_rope: the caches must be float16 or bfloat16")
-    if _elsewhere(dev, stream):
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
         _refuse("qk_norm_rope: qkv and the stream must be on the current GPU")
     if qkv.dtype is not f32 or step != 1 or width != (heads + 2 * kv_heads) * D:
         _refuse("qk_norm_rope: qkv must be float32 [T][(heads + 2 kv_heads) D]")
@@ -717,7 +714,7 @@ def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, 
         if w is not None and (w.dtype is not f32 or not w.is_contiguous() or w.numel() != D or w.get_device() != dev):
             _refuse("qk_norm_rope: a norm weight must be float32 [D] on qkv's device")
     if out is None:
-        out = _empty((T, heads, D), dt, qkv.device, stream)
+        out = torch.empty((T, heads, D), dtype=dt, device=qkv.device) if stream is None else _empty((T, heads, D), dt, qkv.device, stream)
     elif (out.dtype is not dt or not out.is_contiguous() or out.shape != (T, heads, D) or out.get_device() != dev):
         _refuse("qk_norm_rope: out must be contiguous [T][heads][D] of the cache's type, on qkv's device")
     p = mmq_qk_norm_rope_t(
@@ -771,7 +768,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     q_step, q_head, q_one = q.stride()
     k_step, k_head, k_one = k_prefix.stride()
     v_step, v_head, v_one = v_prefix.stride() if v_prefix.dim() == 3 else (0, 0, 0)
-    if _elsewhere(dev, stream):
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
         _refuse("shared_prefix_attention: q and the stream must be on the current GPU")
     if q_one != 1 or (q_head != D and heads > 1) or T != batch * q_len:
         _refuse("shared_prefix_attention: q must be [batch q_len][heads][D], its heads contiguous")
@@ -788,7 +785,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
             or lens.dtype is not i32 or not lens.is_contiguous() or lens.numel() != batch or lens.get_device() != dev):
         _refuse("shared_prefix_attention: page_table must be int32 [batch][width], lens int32 [batch], on q's device")
     if out is None:
-        out = _empty(qs, dt, q.device, stream)
+        out = torch.empty(qs, dtype=dt, device=q.device) if stream is None else _empty(qs, dt, q.device, stream)
         out_kind = kind
     else:
         out_kind = MMQ_TYPE_F32 if out.dtype is torch.float32 else kind
@@ -849,7 +846,7 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
     E, rm = w_router.shape
     ge, gf, gs, gb = w_gu.shape
     de, dm, ds, db = w_down.shape
-    if _elsewhere(dev, stream):
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
         _refuse("q4K_moe: x and the stream must be on the current GPU")
     if x.dtype is not f32 or not x.is_contiguous():
         _refuse("q4K_moe: x must be contiguous float32 [T][model]")
@@ -863,7 +860,7 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
                                  or residual.get_device() != dev):
         _refuse("q4K_moe: residual must be contiguous float32 [T][model] on x's device")
     if out is None:
-        out = _empty(xs, f32, device, stream)
+        out = torch.empty(xs, dtype=f32, device=device) if stream is None else _empty(xs, f32, device, stream)
     elif out.dtype is not f32 or not out.is_contiguous() or out.shape != xs or out.get_device() != dev:
         _refuse("q4K_moe: out must be contiguous float32 [T][model] on x's device")
     ids = _empty((T, top_k), torch.int32, device, stream)
