@@ -547,7 +547,7 @@ size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t
  * run on one device and build.  A length over table_width * page_size is cut
  * to it, and a page number outside [0, n_pages) stands for a page of zeros;
  * either sets the device status word to MMQ_ERR_ARG.
- * head_dim 64 or 128; heads a multiple of kv_heads; strides multiples of 8;
+ * scale > 0; head_dim 64 or 128; heads a multiple of kv_heads; strides multiples of 8;
  * pointers 16-byte aligned (page_table, lens: 4-byte); batch == 0 does
  * nothing.  MMQ_ERR_ARG (a small workspace included) / MMQ_ERR_ALIGN /
  * MMQ_ERR_DEVICE / MMQ_ERR_RESOURCE / MMQ_ERR_CUDA. */
@@ -586,7 +586,8 @@ size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p);
  * The activations x and h are not quantized: each product takes them as the
  * sum of two fp16 values (within 2^-22 of the value or 2^-32 of the largest of
  * its 256 neighbours) against the weights' exact integers, with f32 sums, so
- * the result is that of f32 arithmetic on the dequantized weights.  Only the
+ * the result is that of f32 arithmetic on the dequantized weights (but an h that
+ * overflows f32 gives NaN, not Inf: the split has no Inf).  Only the
  * chosen experts' weights are read, once per four tokens of an expert.
  * Results are bitwise the same run to run on one device and build.
  * tokens 1..64 (0 does nothing), experts 1..256, top_k 1..16 and at most

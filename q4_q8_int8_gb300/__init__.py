@@ -4,7 +4,8 @@ Thin ctypes binding over the C-ABI library ``lib/libmmq.so`` (declared in
 ``include/mmq.h``).  Functions named ``mmq_*`` mirror the C entry points
 one to one and take raw pointers; the snake-case helpers below them only
 allocate outputs with PyTorch and pass ``data_ptr()`` and the current CUDA
-stream.  Every step of the computation runs in the library's CUDA kernels;
+stream, or the one given as ``stream``, which what the call allocates then
+belongs to.  Every step of the computation runs in the library's CUDA kernels;
 if the library is missing, every call raises.
 """
 from __future__ import annotations
@@ -750,8 +751,8 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, page_table,
     [batch]: the tokens of each sequence's suffix, its q_len new ones among
     them (token j sees lens - q_len + 1 + j of them).  scale: 1/sqrt(D) by
     default.  Returns [batch q_len][heads][D] in q's type, or into `out`
-    (which may also be float32).  `workspace`: a CUDA uint8 tensor of
-    mmq_shared_prefix_attention_workspace bytes, allocated per call if None."""
+    (which may also be float32).  `workspace`: a contiguous CUDA uint8 tensor
+    of mmq_shared_prefix_attention_workspace bytes, allocated per call if None."""
     torch = _t or _torch()
     dt, dev, i32 = q.dtype, q.get_device(), torch.int32
     if dt is torch.float16:
@@ -837,8 +838,8 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
     float32 [T][model] or None.  Returns (out float32 [T][model], the chosen
     experts int32 [T][top_k], best first, and their weights float32
     [T][top_k]: softmax values, divided by their sum if `renormalize`).
-    `workspace`: a CUDA uint8 tensor of mmq_q4K_moe_workspace bytes, allocated
-    per call if None."""
+    `workspace`: a contiguous CUDA uint8 tensor of mmq_q4K_moe_workspace bytes,
+    allocated per call if None."""
     torch = _t or _torch()
     f32, u8, dev, device = torch.float32, torch.uint8, x.get_device(), x.device
     xs = x.shape

@@ -69,17 +69,18 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
 // ----------------------------------------------------------------- suffix
 // One warp, a CTA of its own: up to 16 rows that see the same keys (a token's
 // heads of one kv head, over a part of its suffix).  Bound by the key / value
-// bytes: rows are padded to the 16 of one mma.sync tile, keys come 16 at a time through a cp.async ring of three
-// (24 KB at 128 dims, nine such warps per SM: up to 144 KB in flight), and
-// warps that start, stream and finish on their own keep the memory busy where
-// suffixes are short.  Keys past the row's limit are filled with zeros, not
+// bytes: rows are padded to the 16 of one mma.sync tile, keys come 16 at a time
+// through a cp.async ring of three (24 KB at 128 dims, nine such warps per SM:
+// up to 144 KB in flight), and warps that start, stream and finish on their own
+// keep the memory busy where suffixes are short.  Keys past the row's limit are filled with zeros, not
 // read, so what the cache holds there cannot matter.  Weights are rounded to
 // the cache's type for the second product (their sum is taken in f32 before
 // that); as fp16 their reference is 7 (in units of log2) under the largest
 // score, so that those down to 2^-21 of the largest are normal numbers, and for
-// no score, however it is rounded, more than 8.  Both products accumulate in f32.  Measured: 256 suffixes of 1 to 512
-// tokens, 8 kv heads x 128 (261 MB): 50 us, 5.2 TB/s, 77 % of the copy rate (as
-// CTAs of four warps that join in shared memory: 66 us).
+// no score, however it is rounded, more than 8.  Both products accumulate in
+// f32.  Measured: 256 suffixes of 1 to 512 tokens, 8 kv heads x 128 (261 MB):
+// 50 us, 5.2 TB/s, 77 % of the copy rate (as CTAs of four warps that join in
+// shared memory: 66 us).
 constexpr int kSlab = 16, kStages = 3;
 template <typename T>
 constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;   // of the weights, in units of log2

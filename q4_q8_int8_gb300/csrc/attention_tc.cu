@@ -16,8 +16,9 @@
 //                   swizzled panels of 64 values) through a 128 KB ring
 //   warps 9, 10     MMA issuers of groups 0 and 1: S = Q K^T, O += P V, P from
 //                   tensor memory, taking turns batch by batch
-// More than 128 rows: the groups hold two row tiles and share each key tile.
-// Up to 128: both hold the same rows and take key tiles in turn, as two parts.
+// More than 48 rows: the groups hold two row tiles, of which the second may be
+// empty, and share each key tile.  Up to 48: both hold the same rows and take key
+// tiles in turn, as two parts (times at prefix_tiles in attention.cu).
 // While one group does its softmax (1270 cycles a tile) the tensor cores work
 // for the other (16 products of 64 cycles).  The issuing thread is held for the
 // whole of its products, so one thread for both groups left the tensor cores
@@ -34,13 +35,24 @@
 // before as the reference so that the exponentials need not wait for this
 // one's, polling instead of suspended waits.
 //
-// O is only scaled when a row's largest score (in units of log2) has grown by
-// more than 8 since the last time: nothing is lost, since the factor is common
-// to P, the sum and O.  P then stays below 2^8, and as fp16 below 2^15: its
-// reference is 7 under the score, which the rest of fp16's range has room for,
-// so that weights of down to 2^-21 of the largest are normal numbers and those
-// below it are off by at most 2^-32 of the largest.  (With P at most 2^8 the
-// last was 2^-25, and many keys that far under one that takes all were lost.)
+// P is rounded to 16 bits because the second product takes both operands of one
+// type.  As the sum of two such values, a second product each, a whole call's
+// results have the errors of f32 weights (2.1e-4 instead of 2.9e-4 of the norm
+// with an f16 output, whose own rounding is 2.1e-4; 1.65e-3 instead of 2.35e-3 with
+// bf16), for 103 -> 125 us here (256 sequences) and 69 -> 78 us (64 sequences x
+// 32768 keys): not kept.
+//
+// The running maximum and sum are the online softmax of Milakov and Gimelshein
+// (2018); two groups that alternate between softmax and products, and a maximum
+// that may lag, are known from the published work on attention since.  O is only
+// scaled when a row's largest score (in units of log2) has grown by more than 8
+// since the last time: nothing is lost, since the factor is common to P, the sum
+// and O.  P then stays below 2^8, and as fp16 below 2^15: its reference is 7
+// under the score, which the rest of fp16's range has room for, so that weights
+// of down to 2^-21 of the largest are normal numbers and those below it are off
+// by at most 2^-32 of the largest.  (With P at most 2^8 the last was 2^-25, and
+// many keys that far under one that takes all were lost.)  Scores past 2^20 have
+// a loop of their own, where the reference is the score.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -22,13 +22,15 @@
 // copy rate), the second 239 MB in 42 us, and 35 us go into the router (4), the
 // plans and first tiles (8 each), the spread of the CTAs' ends and the combine.
 // The instructions that unpack and multiply a tile take 2100 cycles on an SM's
-// 16 warps, its bytes 3200 at the copy rate, so an expert with more than four
-// tokens, whose weights are unpacked once per four, is bound by them: 32 tokens
-// on 8 experts of 4096 x 11008 take 296 to 304 us where the bytes need 90.  Tried and
-// no faster: an expert's passes side by side, so that all but one find the
-// weights in the L2 (310 us); eight tokens a pass; the whole layer as one
-// cooperative kernel with barriers (32 tokens 329 us, one token 38 instead of
-// 30).
+// 16 warps, its bytes 3200 at the copy rate, so a pass is bound by its bytes; an
+// expert with more than four tokens takes a pass per four, and each streams its
+// weights again: 32 tokens on 8 experts of 4096 x 11008 read 994 + 427 MB from
+// DRAM where the weights are 406 + 203 MB, in 296 to 306 us where those need 90
+// (the first product at 5.2 TB/s with the issue slots 63 % busy, the second at
+// 3.5).  Tried and no faster: an expert's passes side by side, so that all but
+// one find the weights in the L2 (310 us); eight tokens a pass; the whole layer
+// as one cooperative kernel with barriers (32 tokens 329 us, one token 38
+// instead of 30).
 #include <cuda_fp16.h>
 
 #include "mmq_internal.h"
