@@ -668,6 +668,8 @@ def _torch():
 # The library launches on the current device, so memory and streams of another
 # are refused.
 # What a call with `stream` allocates, results among it, belongs to that stream.
+# As with any work on a stream, its inputs have to be complete there, and memory
+# of another stream's pool has to stay until it is done (Tensor.record_stream).
 def qk_norm_rope(qkv, heads: int, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
                  eps: float = 1e-6, interleaved: bool = False, sections=None, out=None, stream=None):
     """Head norms, rotary positions and the cache write after a fused q/k/v projection.
