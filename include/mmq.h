@@ -596,6 +596,102 @@ size_t mmq_q4K_moe_workspace(const mmq_q4K_moe_t* p);
  * workspace included) / MMQ_ERR_ALIGN / MMQ_ERR_DEVICE / MMQ_ERR_CUDA. */
 int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- a key/value cache held in 4 bits ----
+ *
+ * A cache is [n_pages][kv_heads][page_size / 16] tiles of 18 head_dim bytes:
+ * 16 tokens' keys and values of one head, 4 bits per value and a float16 scale
+ * per 32 values of a token, so 4.5 bits per value.  The bytes' order inside a
+ * tile is the library's (keys' codes, their scales, values' codes, their
+ * scales); mmq_kv4_write and mmq_kv4_read are the way in and out.  A tile of
+ * zero bytes holds zeros.  Slot s is place s % page_size of page s / page_size.
+ * page_size a power of two from 16 to 2^20, head_dim 64 or 128, the cache
+ * 16-byte aligned. */
+
+/* Bytes of one page; 0 for sizes the calls refuse. */
+size_t mmq_kv4_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size);
+
+typedef struct {
+    const void* k;           /* [tokens][kv_heads][head_dim], type; strides in */
+    const void* v;           /* values between tokens and heads below          */
+    uint8_t* cache;
+    const int32_t* slots;    /* [tokens]; negative: the token is not cached    */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t tokens, n_slots; /* n_slots = n_pages * page_size                  */
+    int32_t kv_heads, head_dim, page_size;
+    int32_t type;            /* MMQ_TYPE_F16, MMQ_TYPE_BF16 or MMQ_TYPE_F32    */
+} mmq_kv4_write_t;
+
+/* Quantizes keys and values into their slots.  Per block of 32 values x of a
+ * token and head, m the one of largest magnitude (the positive one of two):
+ *     d = float16(bfloat16(-m / 8)), its magnitude at most 8160,
+ *     code k = clamp(rint(x / d), -8, 7), ties to even;  0 where d is zero,
+ * and the cache holds k * d, which is a float16 (d has 8 significant bits, k
+ * at most 8).  Bit for bit reproducible.  A block with a NaN or an infinity
+ * holds NaN.  Two tokens with the same slot race.  A slot >= n_slots writes
+ * nothing and sets the device status word to MMQ_ERR_ARG.  tokens == 0 does
+ * nothing.  Strides multiples of 8 values, k, v and cache 16-byte aligned
+ * (slots: 4-byte).  MMQ_ERR_ARG / MMQ_ERR_ALIGN / MMQ_ERR_DEVICE /
+ * MMQ_ERR_CUDA.  Takes part in programmatic launch. */
+int mmq_kv4_write(const mmq_kv4_write_t* p, void* stream);
+
+typedef struct {
+    const uint8_t* cache;
+    const int32_t* slots;    /* [tokens]                                       */
+    void* k;                 /* [tokens][kv_heads][head_dim], type             */
+    void* v;                 /* the same                                       */
+    int64_t tokens, n_slots;
+    int32_t kv_heads, head_dim, page_size;
+    int32_t type;            /* MMQ_TYPE_F16, MMQ_TYPE_BF16 or MMQ_TYPE_F32    */
+} mmq_kv4_read_t;
+
+/* Expands the slots' keys and values, exactly as float16 or float32, rounded
+ * once to bfloat16.  The outputs are contiguous: what mmq_shared_prefix_attention
+ * takes as a prefix.  A negative slot gives zeros, a slot >= n_slots too and
+ * the device status word MMQ_ERR_ARG.  Rules and errors as mmq_kv4_write. */
+int mmq_kv4_read(const mmq_kv4_read_t* p, void* stream);
+
+typedef struct {
+    const void* q;           /* [tokens][heads][head_dim], type; q_stride      */
+                             /* values between tokens                          */
+    void* out;               /* [tokens][heads][head_dim], out_type            */
+    const uint8_t* cache;
+    const int32_t* page_table;/* [batch][table_width] page numbers             */
+    const int32_t* lens;     /* [batch] tokens of each sequence, its new ones
+                              * among them (already written)                   */
+    const int32_t* q_starts; /* [batch + 1]: sequence b's new tokens are rows
+                              * q_starts[b] .. q_starts[b + 1] - 1 of q; NULL:
+                              * tokens / batch of them each                    */
+    int64_t q_stride, tokens, n_pages, table_width;
+    int32_t batch, heads, kv_heads, head_dim;
+    int32_t page_size;
+    int32_t type, out_type;  /* MMQ_TYPE_F16 / BF16; out_type also F32         */
+    float scale;
+} mmq_kv4_attention_t;
+
+/* Device workspace of one call (its sizes only; 0 for sizes the call
+ * refuses).  256-byte aligned, caller-owned, not used by anything else until
+ * the stream passes the call. */
+size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
+
+/* Causal attention of a batch over its pages of a 4-bit cache.  With n the new
+ * tokens of sequence b, the j-th (0 .. n - 1) sees the first lens[b] - n + 1 + j
+ * keys of the sequence (key i on page page_table[b][i / page_size], place i %
+ * page_size); head h uses kv head h / (heads / kv_heads); s = scale * q.k,
+ *     out = sum_i exp(s_i - max s) v_i / sum_i exp(s_i - max s)
+ * and zeros for a token that sees no key.  n may differ from sequence to
+ * sequence and be zero.  Rows of q that belong to no sequence are not read and
+ * those of out are left as they were.  What the cache holds past a token's last
+ * key is never used, whatever it is.  Results are bitwise the same run to run
+ * on one device and build.  A length over table_width * page_size is cut to
+ * it, a page number outside [0, n_pages) stands for a page of zeros, and a
+ * sequence whose q_starts do not lie in order within [0, tokens] is left out;
+ * each sets the device status word to MMQ_ERR_ARG.
+ * scale > 0; heads a multiple of kv_heads; q_stride a multiple of 8; pointers
+ * 16-byte aligned (page_table, lens, q_starts: 4-byte); batch == 0 or tokens ==
+ * 0 does nothing.  MMQ_ERR_ARG (a small workspace included) / MMQ_ERR_ALIGN /
+ * MMQ_ERR_DEVICE / MMQ_ERR_RESOURCE / MMQ_ERR_CUDA. */
+int mmq_kv4_attention(const mmq_kv4_attention_t* p, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test hook: force the K split of the dot-product kernels (q4_K, M <= 4;
  * q6_K, M <= 16) for later calls on this host thread: ks = 1, 2 or 4 warps
  * per row group (the SwiGLU epilogue takes 1 or 2; a forced 4 makes its

@@ -46,6 +46,7 @@ EXPORTS = (
     "mmq_gguf_read", "mmq_gguf_write",
     "mmq_qk_norm_rope", "mmq_shared_prefix_attention", "mmq_shared_prefix_attention_workspace",
     "mmq_q4K_moe", "mmq_q4K_moe_workspace",
+    "mmq_kv4_page_bytes", "mmq_kv4_write", "mmq_kv4_read", "mmq_kv4_attention", "mmq_kv4_attention_workspace",
     "mmq_status", "mmq_strerror", "mmq_debug_inject_timeout", "mmq_debug_force_gemv_split",
     "mmq_set_programmatic_launch",
 )
@@ -88,6 +89,28 @@ class mmq_q4K_moe_t(ctypes.Structure):
     _fields_ = [("x", _P), ("w_router", _P), ("w_gu", _P), ("w_down", _P), ("residual", _P), ("out", _P), ("ids", _P),
                 ("weights", _P), ("tokens", _I32), ("model", _I32), ("ffn", _I32), ("experts", _I32), ("top_k", _I32),
                 ("renormalize", _I32)]
+
+
+class mmq_kv4_write_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("k", _P), ("v", _P), ("cache", _P), ("slots", _P),
+                ("k_token_stride", _I64), ("k_head_stride", _I64), ("v_token_stride", _I64), ("v_head_stride", _I64),
+                ("tokens", _I64), ("n_slots", _I64),
+                ("kv_heads", _I32), ("head_dim", _I32), ("page_size", _I32), ("type", _I32)]
+
+
+class mmq_kv4_read_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("cache", _P), ("slots", _P), ("k", _P), ("v", _P), ("tokens", _I64), ("n_slots", _I64),
+                ("kv_heads", _I32), ("head_dim", _I32), ("page_size", _I32), ("type", _I32)]
+
+
+class mmq_kv4_attention_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("q", _P), ("out", _P), ("cache", _P), ("page_table", _P), ("lens", _P), ("q_starts", _P),
+                ("q_stride", _I64), ("tokens", _I64), ("n_pages", _I64), ("table_width", _I64),
+                ("batch", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("page_size", _I32),
+                ("type", _I32), ("out_type", _I32), ("scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -153,6 +176,11 @@ def load_library(path: str = LIB_PATH):
                                                 ctypes.c_int),
                 "mmq_q4K_moe_workspace": ([ctypes.POINTER(mmq_q4K_moe_t)], S),
                 "mmq_q4K_moe": ([ctypes.POINTER(mmq_q4K_moe_t), P, S, P], ctypes.c_int),
+                "mmq_kv4_page_bytes": ([_I32, _I32, _I32], S),
+                "mmq_kv4_write": ([ctypes.POINTER(mmq_kv4_write_t), P], ctypes.c_int),
+                "mmq_kv4_read": ([ctypes.POINTER(mmq_kv4_read_t), P], ctypes.c_int),
+                "mmq_kv4_attention_workspace": ([ctypes.POINTER(mmq_kv4_attention_t)], S),
+                "mmq_kv4_attention": ([ctypes.POINTER(mmq_kv4_attention_t), P, S, P], ctypes.c_int),
                 "mmq_status": ([P], ctypes.c_int),
                 "mmq_strerror": ([ctypes.c_int], ctypes.c_char_p),
                 "mmq_debug_inject_timeout": ([ctypes.c_int], None),
@@ -883,3 +911,179 @@ def q4K_moe(x, w_router, w_gu, w_down, top_k: int, renormalize: bool = True, res
     if rc:
         _check(rc, "mmq_q4K_moe")
     return out, ids, weights
+
+
+# ---- a key/value cache held in 4 bits ----------------------------------------
+def mmq_kv4_page_bytes(kv_heads, head_dim, page_size):
+    return load_library().mmq_kv4_page_bytes(kv_heads, head_dim, page_size)
+
+
+def mmq_kv4_write(p, stream):
+    return load_library().mmq_kv4_write(ctypes.byref(p), stream)
+
+
+def mmq_kv4_read(p, stream):
+    return load_library().mmq_kv4_read(ctypes.byref(p), stream)
+
+
+def mmq_kv4_attention_workspace(p):
+    return load_library().mmq_kv4_attention_workspace(ctypes.byref(p))
+
+
+def mmq_kv4_attention(p, workspace, workspace_bytes, stream):
+    return load_library().mmq_kv4_attention(ctypes.byref(p), workspace, workspace_bytes, stream)
+
+
+def empty_kv4_cache(pages: int, kv_heads: int, D: int, page_size: int = 16, device="cuda", stream=None):
+    """Allocate a 4-bit key/value cache: uint8 [pages][kv_heads][page_size / 16][18 D] of undefined contents (what lies
+    past a sequence's tokens is never used)."""
+    torch = _t or _torch()
+    if not mmq_kv4_page_bytes(kv_heads, D, page_size):
+        _refuse("empty_kv4_cache: sizes")
+    return _empty((pages, kv_heads, page_size // 16, 18 * D), torch.uint8, device, stream)
+
+
+def kv4_write(k, v, slots, cache, stream=None):
+    """Quantize new keys and values into their slots of a 4-bit cache.
+
+    k, v float16, bfloat16 or float32 [T][kv_heads][D] (tokens and heads may be
+    strided, each its own way), D 64 or 128; slots int32 [T] (negative: not
+    cached); cache uint8 [pages][kv_heads][page_size / 16][18 D], contiguous
+    (empty_kv4_cache), slot s being place s % page_size of page s / page_size.
+    The cache then holds, per block of 32 values x with m the largest in
+    magnitude, clamp(rint(x / d), -8, 7) * d with d = -m / 8 rounded to
+    bfloat16, then float16.  A slot out of range shows in status()."""
+    torch = _t or _torch()
+    dt, dev = k.dtype, k.get_device()
+    T, heads, D = ks = k.shape
+    pages, kv_heads, tiles, size = cache.shape
+    kt, kh, k1 = k.stride()
+    vt, vh, v1 = v.stride() if v.dim() == 3 else (0, 0, 0)
+    kind = MMQ_TYPE_F16 if dt is torch.float16 else MMQ_TYPE_BF16 if dt is torch.bfloat16 else MMQ_TYPE_F32
+    if kind == MMQ_TYPE_F32 and dt is not torch.float32:
+        _refuse("kv4_write: k must be float16, bfloat16 or float32")
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        _refuse("kv4_write: k and the stream must be on the current GPU")
+    if v.dtype is not dt or v.shape != ks or v.get_device() != dev or (T and (k1 != 1 or v1 != 1)):
+        _refuse("kv4_write: k and v must be alike, [T][kv_heads][D], on one device")
+    if (cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.get_device() != dev or heads != kv_heads
+            or size != 18 * D):
+        _refuse("kv4_write: cache must be contiguous uint8 [pages][kv_heads][page_size / 16][18 D] on k's device")
+    if slots.dtype is not torch.int32 or not slots.is_contiguous() or slots.numel() != T or slots.get_device() != dev:
+        _refuse("kv4_write: slots must be int32 [T] on k's device")
+    p = mmq_kv4_write_t(k.data_ptr(), v.data_ptr(), cache.data_ptr(), slots.data_ptr(),
+                        kt if T > 1 else heads * D, kh if heads > 1 else D, vt if T > 1 else heads * D,
+                        vh if heads > 1 else D, T, pages * tiles * 16, heads, D, tiles * 16, kind)
+    rc = (_lib or load_library()).mmq_kv4_write(
+        p, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_kv4_write")
+
+
+def kv4_read(cache, slots, dtype=None, out=None, stream=None):
+    """Expand slots of a 4-bit cache -> (k, v) [T][kv_heads][D] in `dtype`: float16 (the default) or float32, exactly, or
+    bfloat16, rounded once.
+
+    cache and slots as in kv4_write (a negative slot gives zeros); `out`: two
+    contiguous tensors of that shape, of one type.  What comes back can be the
+    prefix of shared_prefix_attention."""
+    torch = _t or _torch()
+    dev, device = cache.get_device(), cache.device
+    pages, kv_heads, tiles, size = cache.shape
+    D, T = size // 18, slots.numel()
+    shape = (T, kv_heads, D)
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        _refuse("kv4_read: the cache and the stream must be on the current GPU")
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous() or size != 18 * D:
+        _refuse("kv4_read: cache must be contiguous uint8 [pages][kv_heads][page_size / 16][18 D]")
+    if slots.dtype is not torch.int32 or not slots.is_contiguous() or slots.get_device() != dev:
+        _refuse("kv4_read: slots must be int32 [T] on the cache's device")
+    if out is None:
+        dt = torch.float16 if dtype is None else dtype
+        if stream is None:
+            k, v = torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device)
+        else:
+            k, v = _empty(shape, dt, device, stream), _empty(shape, dt, device, stream)
+    else:
+        k, v = out
+        dt = k.dtype
+        if (v.dtype is not dt or (dtype is not None and dtype is not dt) or k.shape != shape or v.shape != shape
+                or not k.is_contiguous() or not v.is_contiguous() or k.get_device() != dev or v.get_device() != dev):
+            _refuse("kv4_read: out must be two contiguous tensors [T][kv_heads][D] of one type on the cache's device")
+    kind = MMQ_TYPE_F16 if dt is torch.float16 else MMQ_TYPE_BF16 if dt is torch.bfloat16 else MMQ_TYPE_F32
+    if kind == MMQ_TYPE_F32 and dt is not torch.float32:
+        _refuse("kv4_read: the outputs are float16, bfloat16 or float32")
+    p = mmq_kv4_read_t(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), T, pages * tiles * 16, kv_heads, D,
+                       tiles * 16, kind)
+    rc = (_lib or load_library()).mmq_kv4_read(
+        p, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_kv4_read")
+    return k, v
+
+
+def kv4_attention(q, cache, page_table, lens, q_starts=None, scale=None, out=None, workspace=None, stream=None):
+    """Causal attention of a ragged batch over its pages of a 4-bit key/value cache.
+
+    q float16 or bfloat16 [T][heads][D] (tokens may be strided), D 64 or 128:
+    the new tokens of all sequences, whose keys and values are in the cache
+    already; cache uint8 [pages][kv_heads][page_size / 16][18 D] as in kv4_write;
+    page_table int32 [batch][width]; lens int32 [batch]: each sequence's tokens,
+    its new ones among them; q_starts int32 [batch + 1]: sequence b's rows of q
+    are q_starts[b] .. q_starts[b + 1] - 1 (rows of none are left alone in
+    `out`), or None for T / batch of them each.  scale: 1/sqrt(D) by default.
+    Returns [T][heads][D] in q's type, or into `out` (which may also be
+    float32).  `workspace`: a contiguous CUDA uint8 tensor of
+    mmq_kv4_attention_workspace bytes, allocated per call if None."""
+    torch = _t or _torch()
+    dt, dev, i32 = q.dtype, q.get_device(), torch.int32
+    if dt is torch.float16:
+        kind = MMQ_TYPE_F16
+    elif dt is torch.bfloat16:
+        kind = MMQ_TYPE_BF16
+    else:
+        _refuse("kv4_attention: q must be float16 or bfloat16")
+    T, heads, D = qs = q.shape
+    pages, kv_heads, tiles, size = cache.shape
+    batch, width = page_table.shape
+    q_step, q_head, q_one = q.stride()
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        _refuse("kv4_attention: q and the stream must be on the current GPU")
+    if q_one != 1 or (q_head != D and heads > 1):
+        _refuse("kv4_attention: q must be [T][heads][D], its heads contiguous")
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.get_device() != dev or size != 18 * D:
+        _refuse("kv4_attention: cache must be contiguous uint8 [pages][kv_heads][page_size / 16][18 D] on q's device")
+    if (page_table.dtype is not i32 or not page_table.is_contiguous() or page_table.get_device() != dev
+            or lens.dtype is not i32 or not lens.is_contiguous() or lens.numel() != batch or lens.get_device() != dev):
+        _refuse("kv4_attention: page_table must be int32 [batch][width], lens int32 [batch], on q's device")
+    if q_starts is None:
+        if T % batch if batch else T:
+            _refuse("kv4_attention: without q_starts, T must be a multiple of the batch")
+    elif (q_starts.dtype is not i32 or not q_starts.is_contiguous() or q_starts.numel() != batch + 1
+          or q_starts.get_device() != dev):
+        _refuse("kv4_attention: q_starts must be int32 [batch + 1] on q's device")
+    if out is None:
+        out = torch.empty(qs, dtype=dt, device=q.device) if stream is None else _empty(qs, dt, q.device, stream)
+        out_kind = kind
+    else:
+        out_kind = MMQ_TYPE_F32 if out.dtype is torch.float32 else kind
+        if (out.shape != qs or not out.is_contiguous() or out.get_device() != dev
+                or (out.dtype is not dt and out_kind != MMQ_TYPE_F32)):
+            _refuse("kv4_attention: out must be contiguous [T][heads][D] in q's type or float32")
+    if batch == 0 or T == 0:
+        return out
+    p = mmq_kv4_attention_t(
+        q.data_ptr(), out.data_ptr(), cache.data_ptr(), page_table.data_ptr(), lens.data_ptr(),
+        None if q_starts is None else q_starts.data_ptr(), q_step if T > 1 else heads * D, T, pages, width,
+        batch, heads, kv_heads, D, tiles * 16, kind, out_kind, D ** -0.5 if scale is None else scale)
+    lib = _lib or load_library()
+    if workspace is None:
+        workspace = _workspace(lib.mmq_kv4_attention_workspace(p), q.device, stream, "kv4_attention")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("kv4_attention: workspace must be contiguous, on q's device")
+    rc = lib.mmq_kv4_attention(
+        p, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_kv4_attention")
+    return out

@@ -582,6 +582,107 @@ int mmq_q4K_moe(const mmq_q4K_moe_t* p, void* workspace, size_t workspace_bytes,
     return from_cuda(mmq::launch_q4K_moe(*p, workspace, status, inject, static_cast<cudaStream_t>(stream)));
 }
 
+// Sizes that every call on a 4-bit cache has: MMQ_OK or MMQ_ERR_ARG.
+static int check_kv4_cache(int32_t kv_heads, int32_t head_dim, int32_t page_size) {
+    if (kv_heads < 1 || kv_heads > 65535 || (head_dim != 64 && head_dim != 128)) return MMQ_ERR_ARG;
+    if (page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1))) return MMQ_ERR_ARG;
+    return MMQ_OK;
+}
+
+size_t mmq_kv4_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size) {
+    if (check_kv4_cache(kv_heads, head_dim, page_size)) return 0;
+    return size_t(kv_heads) * size_t(page_size / 16) * 18 * size_t(head_dim);
+}
+
+// Tokens and slots of a write or read.
+static int check_kv4_slots(int64_t tokens, int64_t n_slots, int32_t page_size, int32_t type) {
+    const int64_t kMax = (int64_t(1) << 31) - 1;
+    if (tokens < 0 || tokens > kMax - 31 || n_slots < 0 || n_slots > kMax || n_slots % page_size) return MMQ_ERR_ARG;
+    if (type != MMQ_TYPE_F16 && type != MMQ_TYPE_BF16 && type != MMQ_TYPE_F32) return MMQ_ERR_ARG;
+    return MMQ_OK;
+}
+
+int mmq_kv4_write(const mmq_kv4_write_t* p, void* stream) {
+    if (!p || check_kv4_cache(p->kv_heads, p->head_dim, p->page_size) ||
+        check_kv4_slots(p->tokens, p->n_slots, p->page_size, p->type))
+        return MMQ_ERR_ARG;
+    for (const int64_t n : {p->k_token_stride, p->k_head_stride, p->v_token_stride, p->v_head_stride})
+        if (n < 0 || n % 8 || n > (int64_t(1) << 38)) return MMQ_ERR_ARG;
+    if (p->tokens == 0) return check_device();
+    if (!p->k || !p->v || !p->slots || (p->n_slots > 0 && !p->cache)) return MMQ_ERR_ARG;
+    for (const void* v : {p->k, p->v, static_cast<const void*>(p->cache)})
+        if (!aligned16(v)) return MMQ_ERR_ALIGN;
+    if (!aligned4(p->slots)) return MMQ_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_kv4_write(*p, status, static_cast<cudaStream_t>(stream)));
+}
+
+int mmq_kv4_read(const mmq_kv4_read_t* p, void* stream) {
+    if (!p || check_kv4_cache(p->kv_heads, p->head_dim, p->page_size) ||
+        check_kv4_slots(p->tokens, p->n_slots, p->page_size, p->type))
+        return MMQ_ERR_ARG;
+    if (p->tokens == 0) return check_device();
+    if (!p->k || !p->v || !p->slots || (p->n_slots > 0 && !p->cache)) return MMQ_ERR_ARG;
+    for (const void* v : {static_cast<const void*>(p->k), static_cast<const void*>(p->v), static_cast<const void*>(p->cache)})
+        if (!aligned16(v)) return MMQ_ERR_ALIGN;
+    if (!aligned4(p->slots)) return MMQ_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_kv4_read(*p, status, static_cast<cudaStream_t>(stream)));
+}
+
+// The sizes of a 4-bit attention call (no pointers but q_starts): MMQ_OK or MMQ_ERR_ARG.
+static int check_kv4_attention_sizes(const mmq_kv4_attention_t* p) {
+    if (!p || check_kv4_cache(p->kv_heads, p->head_dim, p->page_size)) return MMQ_ERR_ARG;
+    const int64_t kMax = (int64_t(1) << 31) - 1;
+    if (p->batch < 0 || p->batch > (1 << 20) || p->heads < 1 || p->heads > 65535 || p->heads % p->kv_heads)
+        return MMQ_ERR_ARG;
+    if (p->tokens < 0 || p->tokens > kMax / p->heads) return MMQ_ERR_ARG;
+    if (!p->q_starts && (p->batch == 0 ? p->tokens != 0 : p->tokens % p->batch != 0)) return MMQ_ERR_ARG;
+    if (p->n_pages < 0 || p->n_pages > kMax) return MMQ_ERR_ARG;
+    if (p->table_width < 0 || p->table_width > kMax / p->page_size) return MMQ_ERR_ARG;
+    if (p->type != MMQ_TYPE_F16 && p->type != MMQ_TYPE_BF16) return MMQ_ERR_ARG;
+    if (p->out_type != p->type && p->out_type != MMQ_TYPE_F32) return MMQ_ERR_ARG;
+    if (!(p->scale > 0.f && p->scale < 1e30f)) return MMQ_ERR_ARG;
+    if (p->q_stride < int64_t(p->heads) * p->head_dim || p->q_stride % 8 || p->q_stride > (int64_t(1) << 38))
+        return MMQ_ERR_ARG;
+    return MMQ_OK;
+}
+
+size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p) {
+    if (check_kv4_attention_sizes(p) || p->batch == 0 || p->tokens == 0 || check_device()) return 0;
+    return mmq::kv4_attention_workspace(*p);
+}
+
+int mmq_kv4_attention(const mmq_kv4_attention_t* p, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_kv4_attention_sizes(p);
+    if (rc) return rc;
+    if (p->batch == 0 || p->tokens == 0) return check_device();
+    if (!p->q || !p->out || !p->lens || !workspace) return MMQ_ERR_ARG;
+    if (p->table_width > 0 && !p->page_table) return MMQ_ERR_ARG;
+    if (p->table_width > 0 && p->n_pages > 0 && !p->cache) return MMQ_ERR_ARG;
+    for (const void* v : {p->q, static_cast<const void*>(p->out), static_cast<const void*>(p->cache)})
+        if (!aligned16(v)) return MMQ_ERR_ALIGN;
+    if (!aligned4(p->page_table) || !aligned4(p->lens) || !aligned4(p->q_starts)) return MMQ_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return MMQ_ERR_ALIGN;
+    if ((rc = check_device())) return rc;
+    const size_t need = mmq::kv4_attention_workspace(*p);
+    if (need == 0) return MMQ_ERR_CUDA;
+    if (workspace_bytes < need) return MMQ_ERR_ARG;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    const int inject = t_inject_timeout;
+    t_inject_timeout = 0;
+    const cudaError_t e = mmq::launch_kv4_attention(*p, workspace, status, inject, static_cast<cudaStream_t>(stream));
+    // a tensor-core kernel's register split does not fit this build of it
+    return e == cudaErrorLaunchOutOfResources ? MMQ_ERR_RESOURCE : from_cuda(e);
+}
+
 int mmq_status(void* stream) {
     int* p = mmq::status_word_ptr();
     if (!p) return MMQ_ERR_CUDA;

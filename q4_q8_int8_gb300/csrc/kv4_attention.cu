@@ -1,0 +1,808 @@
+// Attention of a ragged batch over a 4-bit paged cache: few rows per sequence.
+//
+// With k the codes less 8, d the scales, g the blocks of 32 dimensions of a head:
+//   s_t = f sum_g dk_tg sum_{x in g} q'_x k_tx      q' = 2^e q as fp16, f = scale log2(e) 2^-e
+//   out = sum_t 2^(s_t - m) dv_t k_t / sum_t 2^(s_t - m)
+// in parts joined by their references m and sums, as in attention.cu.
+//
+// Rows are the (new token, head of the group) pairs of one kv head, R = 8 NT of
+// them to a unit, which needs every tile of 16 keys that its last row sees.
+// All units' tiles, one after the other, are cut into equal runs, one per warp:
+// ragged lengths and few long sequences fill the machine alike.  A warp's run
+// may hold the end of one unit, some whole ones and the start of another; parts
+// of a unit that lie in one CTA join in shared memory, those over several in
+// the workspace, joined by a second kernel.
+//
+// Per tile a warp takes two products on the tensor cores with 16 x 16 blocks of
+// codes as the A operand: S^T = K Q^T and O^T = V^T P^T, whose 8 columns are the
+// rows, so that a group of up to 8 heads fills a product that would be half
+// empty with rows as M.  The cache's bytes are in the A operand's order: a tile
+// is one asynchronous bulk copy into the warp's own ring, and a lane's words
+// need masks only.
+//   Keys: a code masked out of its word is an fp16 subnormal, n 2^-24 (or 2^-20
+//   from the upper nibble, for which q' is 2^-4 times smaller); the 8 is taken
+//   off by the accumulator's start, -8 sum q', and the block's scale multiplies
+//   the f32 sum.  q' has its row's largest element in [2^13, 2^14): nothing of
+//   a bfloat16's or float16's eleven bits is lost down to 2^-28 of it.
+//   Values: (n - 8) d, exact in fp16, because here the scale's index is summed
+//   over.  Weights are the sum of two fp16 values (22 bits, 2^-25 of the
+//   reference at worst), a product each: one alone would double the error of a
+//   float16 result.
+// The reference m of a row is only raised when a score is more than 8 (in
+// log2) above it: weights stay below 2^8.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kv4.cuh"
+#include "mmq_internal.h"
+#include "sm103_ptx.cuh"
+#include "tc_common.cuh"
+
+namespace {
+
+using namespace mmq::ptx;
+using namespace mmq::kv4;
+using mmq::tc::ld_shared_v4;
+
+constexpr int kWarps = 8;
+constexpr float kGrow = 8.f;
+constexpr int kLeast = 2;   // tiles to a run, where there are too few for all warps
+
+struct Kv4Args {
+    mmq_kv4_attention_t p;
+    float* parts;       // [ctas][2] units' sums and (m, l): a CTA's first and last
+    struct Mark* marks; // [ctas]
+    int* status;
+    int inject;
+    int page_shift, group;
+    float scale_log2;
+};
+// What a CTA leaves of units that it shares with other CTAs: the start of a
+// unit's run of tiles is its name.
+struct Mark {
+    int64_t head, tail;      // -1: none
+    int head_ends;           // the head's unit has its last tile here
+    int b, h, tile;          // the tail's unit
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ bool finite16(uint32_t bits) { return (bits & 0x7C00u) != 0x7C00u; }   // low half
+
+// --------------------------------------------------------------- sequences
+struct Sequence {
+    int n, len;       // new tokens, tokens
+    int64_t start;    // first row of q
+};
+// Checked: a sequence's rows lie in [0, tokens), its keys in its pages.
+__device__ __forceinline__ Sequence sequence(const Kv4Args& a, int b, bool tell) {
+    const mmq_kv4_attention_t& p = a.p;
+    Sequence s;
+    bool bad = false;
+    if (p.q_starts) {
+        const int64_t lo = p.q_starts[b], hi = p.q_starts[b + 1];
+        bad = lo < 0 || hi < lo || hi > p.tokens;
+        s.start = lo;
+        s.n = bad ? 0 : int(hi - lo);
+    } else {
+        s.n = int(p.tokens / p.batch);
+        s.start = int64_t(b) * s.n;
+    }
+    const int64_t room = p.table_width << a.page_shift, len = p.lens[b];
+    bad = bad || len > room;
+    s.len = int(max(int64_t(0), min(len, room)));
+    if (tell && bad) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+    return s;
+}
+// Keys that new token j of a sequence sees.
+__device__ __forceinline__ int seen(const Sequence& s, int j) { return max(0, s.len - s.n + 1 + j); }
+
+template <int R>
+__device__ __forceinline__ int units(const Sequence& s, int group) {
+    return int((int64_t(s.n) * group + R - 1) / R);
+}
+// Tiles of one unit, at least one: a unit without keys still has zeros to write.
+template <int R>
+__device__ __forceinline__ int unit_tiles(const Sequence& s, int group, int u) {
+    const int last = int(min(int64_t(s.n) - 1, (int64_t(u) * R + R - 1) / group));
+    return max(1, (seen(s, last) + kTokens - 1) / kTokens);
+}
+template <int R>
+__device__ __forceinline__ int64_t sequence_tiles(const Sequence& s, int group) {
+    int64_t n = 0;
+    const int m = units<R>(s, group);
+    for (int u = 0; u < m; ++u) n += unit_tiles<R>(s, group, u);
+    return n;
+}
+
+// ------------------------------------------------------------------ output
+__device__ __forceinline__ void store_value(void* out, int type, int64_t at, float x) {
+    if (type == MMQ_TYPE_F32) static_cast<float*>(out)[at] = x;
+    else if (type == MMQ_TYPE_F16) static_cast<__half*>(out)[at] = __float2half_rn(x);
+    else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
+}
+
+template <int D, int NT>
+struct Rows {
+    static constexpr int R = 8 * NT;
+    static constexpr int kRegs = D / 16 * 4 * NT;         // accumulators per lane
+    static constexpr int kPart = kRegs * 32 + 2 * R;      // floats of a part: sums [reg][lane], then m, l [row]
+    static constexpr int kCtas = NT == 1 ? 2 : 1;         // per SM
+    static constexpr int kStages = D == 128 && NT == 1 ? 4 : D == 128 ? 6 : 8;
+    static constexpr int kRing = kStages * tile_bytes(D); // a warp's; its last part lies over it
+    static constexpr int kOffFirst = kWarps * kRing;      // and its first part here
+    static constexpr int kOffBar = kOffFirst + kWarps * kPart * 4;
+    static constexpr int kBytes = kOffBar + kWarps * kStages * 8;
+    static_assert(kRing >= kPart * 4 && kRing % 16 == 0, "a part fits the ring");
+    static_assert(kCtas * (kBytes + 2048) <= 228 * 1024, "shared memory");
+};
+
+// Register k = (block i, half of 16 dimensions, column) of lane: its dimension and row.
+template <int NT>
+__device__ __forceinline__ void element(int k, int lane, int& dim, int& row) {
+    const int nt = (k >> 2) % NT, i = (k >> 2) / NT;
+    dim = 16 * i + 8 * ((k >> 1) & 1) + (lane >> 2);
+    row = 8 * nt + 2 * (lane & 3) + (k & 1);
+}
+
+struct Unit {
+    int b, h, tile;
+};
+template <int D, int R>
+__device__ __forceinline__ void store_row(const Kv4Args& a, const Unit& u, const Sequence& s, int row, int dim, float x) {
+    const int64_t r = int64_t(u.tile) * R + row;
+    const int64_t j = r / a.group;
+    if (j >= s.n) return;
+    const int head = u.h * a.group + int(r - j * a.group);
+    store_value(a.p.out, a.p.out_type, ((s.start + j) * a.p.heads + head) * D + dim, x);
+}
+
+// Parts of one unit, added up by a CTA: warp w and lane have registers w, w + 8, ... of all lanes, which are of one row.
+template <int D, int NT>
+struct Join {
+    using W = Rows<D, NT>;
+    static constexpr int kMine = W::kRegs / kWarps;
+    float acc[kMine] = {}, m = -INFINITY, l = 0.f;
+    int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, dim, row;
+
+    __device__ __forceinline__ Join() { element<NT>(warp, lane, dim, row); }
+    __device__ __forceinline__ void add(const float* part) {
+        const float pm = part[W::kRegs * 32 + row], pl = part[W::kRegs * 32 + W::R + row];
+        if (pl == 0.f) return;   // no key
+        const float top = fmaxf(m, pm);
+        const float mine = l == 0.f ? 0.f : ex2(m - top), its = ex2(pm - top);
+        m = top;
+        l = l * mine + pl * its;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) acc[i] = acc[i] * mine + part[(warp + kWarps * i) * 32 + lane] * its;
+    }
+    __device__ __forceinline__ void finish(const Kv4Args& a, const Unit& u, const Sequence& s) const {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            int at, same;
+            element<NT>(warp + kWarps * i, lane, at, same);
+            store_row<D, W::R>(a, u, s, row, at, acc[i] * inv);
+        }
+    }
+    __device__ __forceinline__ void keep(float* part) const {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) part[(warp + kWarps * i) * 32 + lane] = acc[i];
+        // one lane of those that have the row, for the first registers' warps
+        if (lane < 4 && warp < 4 * NT && (warp & 2) == 0) {
+            part[W::kRegs * 32 + row] = m;
+            part[W::kRegs * 32 + W::R + row] = l;
+        }
+    }
+};
+
+// ------------------------------------------------------------------ kernel
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(const Kv4Args a) {
+    using W = Rows<D, NT>;
+    constexpr int R = W::R, kStages = W::kStages, kGroups = D / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ struct {
+        int64_t total[kWarps];
+        int64_t first[kWarps + 1];      // each warp's first tile of all
+        int b[kWarps];                  // the sequence it lies in
+        int64_t offset[kWarps];         // and its place there
+        // the parts of each warp, its first and its last: the unit's name or -1, whether it starts and ends there
+        int64_t name[2 * kWarps];
+        int whole[2 * kWarps];          // bit 0: starts, bit 1: ends
+        Unit unit[2 * kWarps];
+        uint32_t aborted;
+    } sh;
+    static_assert(sizeof(sh) <= 1024, "counted in Rows");
+    const mmq_kv4_attention_t& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
+    const AbortFlag abort_flag{smem_u32(&sh.aborted)};
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp * W::kRing);
+    const uint32_t bars = smem_u32(smem) + uint32_t(W::kOffBar + warp * kStages * 8);
+
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) mbar_init(bars + 8u * uint32_t(i), 1);
+    if (threadIdx.x == 0) sh.aborted = 0;
+    if (threadIdx.x < 2 * kWarps) sh.name[threadIdx.x] = -1;
+    fence_barrier_init();
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // ---- who does what: a scan over the sequences' tiles
+    const int per = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
+    const int b0 = min(p.batch, int(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += sequence_tiles<R>(sequence(a, b, blockIdx.x == 0), a.group) * p.kv_heads;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) sh.total[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh.total[w];
+        total += sh.total[w];
+    }
+    const int64_t x1 = before + upto, x0 = x1 - mine;
+    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kWarps, total / kLeast));
+    auto first_of = [&](int64_t run) {   // runs < 2^16
+        return run >= runs ? total : total / runs * run + total % runs * run / runs;
+    };
+    for (int w = 0; w <= kWarps; ++w) {
+        const int64_t at = first_of(int64_t(blockIdx.x) * kWarps + w);
+        if (threadIdx.x == 0) sh.first[w] = at;
+        if (w < kWarps && x0 <= at && at < x1) {   // of one thread
+            int64_t x = x0;
+            for (int b = b0; b < b1; ++b) {
+                const int64_t n = sequence_tiles<R>(sequence(a, b, false), a.group) * p.kv_heads;
+                if (at < x + n) {
+                    sh.b[w] = b;
+                    sh.offset[w] = at - x;
+                    break;
+                }
+                x += n;
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- this warp's run
+    int64_t at = sh.first[warp];
+    const int64_t end = sh.first[warp + 1];
+    int b = at < end ? sh.b[warp] : 0;
+    int64_t offset = at < end ? sh.offset[warp] : 0;
+    auto part_at = [&](int slot) {
+        return reinterpret_cast<float*>(smem + (slot & 1 ? (slot >> 1) * W::kRing : W::kOffFirst + (slot >> 1) * W::kPart * 4));
+    };
+    uint32_t pos = 0;              // copies taken so far
+    uint32_t sent = 0;             // copies issued so far
+    bool ok = true, bad_page = false;
+    float o[W::kRegs / 4][4];
+    float m[NT][2], l[NT][2];      // of rows 2 c, 2 c + 1
+
+    while (at < end && ok) {
+        const Sequence s = sequence(a, b, false);
+        const int64_t each = sequence_tiles<R>(s, a.group);
+        if (offset >= each * p.kv_heads) {   // also a sequence without rows
+            ++b;
+            offset = 0;
+            continue;
+        }
+        Unit u;
+        u.b = b;
+        u.h = int(offset / each);
+        int64_t in_head = offset - u.h * each;
+        u.tile = 0;
+        int tiles;
+        while (in_head >= (tiles = unit_tiles<R>(s, a.group, u.tile))) {
+            in_head -= tiles;
+            ++u.tile;
+        }
+        const int t0 = int(in_head), t1 = int(min(int64_t(tiles), t0 + (end - at)));
+        const int64_t name = at - t0;        // the unit's first tile of all
+        const int row0 = u.tile * R;   // first row of the unit
+
+        // Queries: lane's row is r8 (of each eight), its dimensions 2 c, 2 c + 1 and those + 8 of every 16.
+        uint32_t qf[NT][D / 16][2];
+        float off8[NT][kGroups][2];    // -8 sum q' of rows 2 c, 2 c + 1, in units of the products
+        float f[NT][2];
+        int see[NT][2], most = 0, least = 0x7FFFFFFF;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row0 + 8 * nt + r8, j = row / a.group;
+            const bool has = j < s.n;
+            const T* src = static_cast<const T*>(p.q) + (s.start + (has ? j : 0)) * p.q_stride +
+                           (int64_t(u.h) * a.group + (has ? row - j * a.group : 0)) * D + 2 * c4;
+            float x[D / 16][4];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t lo = has ? *reinterpret_cast<const uint32_t*>(src + 16 * i) : 0u;
+                const uint32_t hi = has ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8) : 0u;
+                if (std::is_same<T, __half>::value) {
+                    const float2 u0 = __half22float2(u2h(lo)), u1 = __half22float2(u2h(hi));
+                    x[i][0] = u0.x; x[i][1] = u0.y; x[i][2] = u1.x; x[i][3] = u1.y;
+                } else {
+                    x[i][0] = __uint_as_float(lo << 16); x[i][1] = __uint_as_float(lo & 0xFFFF0000u);
+                    x[i][2] = __uint_as_float(hi << 16); x[i][3] = __uint_as_float(hi & 0xFFFF0000u);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[i][k]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // top in [2^e, 2^(e+1)) -> [2^13, 2^14); a row of zeros or tiny values as if it had 2^-100
+            const int e = max(-100, int((__float_as_uint(top) >> 23) & 0xFF) - 127);
+            const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+            float sum[kGroups];
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) sum[g] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const __half2 v0 = __floats2half2_rn(x[i][0] * up, x[i][1] * up);
+                const __half2 v1 = __floats2half2_rn(x[i][2] * up * 0.0625f, x[i][3] * up * 0.0625f);
+                qf[nt][i][0] = h2u(v0);
+                qf[nt][i][1] = h2u(v1);
+                const float2 w0 = __half22float2(v0), w1 = __half22float2(v1);
+                sum[i / 2] += (w0.x + w0.y) + 16.f * (w1.x + w1.y);
+            }
+            // The products carry 2^-24 from the codes.  Held below infinity: all scores of the row are too large by
+            // then for it to matter, but zeros stay zeros.
+            const float mine_f = fminf(a.scale_log2 * __uint_as_float(uint32_t(127 + e - 13) << 23) * 0x1p24f, 3.4e38f);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+                sum[g] *= -8.f * 0x1p-24f;
+            }
+            const int mine_see = has ? min(seen(s, j), t1 * kTokens) : 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int from = (2 * c4 + k) * 4;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) off8[nt][g][k] = __shfl_sync(0xffffffffu, sum[g], from);
+                f[nt][k] = __shfl_sync(0xffffffffu, mine_f, from);
+                see[nt][k] = __shfl_sync(0xffffffffu, mine_see, from);
+                m[nt][k] = -INFINITY;
+                l[nt][k] = 0.f;
+            }
+            most = max(most, mine_see);
+            if (has) least = min(least, mine_see);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+        }
+#pragma unroll
+        for (int i = 0; i < W::kRegs / 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+
+        const int last = min(t1, (most + kTokens - 1) / kTokens);   // tiles with a key
+        // Tile t's copy.  The pages of 32 tiles at a time are in the lanes.
+        const int32_t* const table = p.page_table + int64_t(b) * p.table_width;
+        const int tile_shift = a.page_shift - 4;
+        int32_t ids = -1;
+        uint32_t zeros = 0;            // stages that stand for a page of zeros
+        int next = t0;
+        auto fetch = [&]() {
+            const int i = (next - t0) & 31;
+            if (i == 0) {
+                ids = -1;
+                if (next + lane < last) {
+                    ids = table[(next + lane) >> tile_shift];
+                    if (ids < 0 || ids >= p.n_pages) {
+                        ids = -1;
+                        bad_page = true;
+                    }
+                }
+            }
+            const int32_t id = __shfl_sync(0xffffffffu, ids, i);
+            const int stage = int(sent % kStages);
+            ++sent;
+            zeros = id < 0 ? zeros | (1u << stage) : zeros & ~(1u << stage);
+            const int64_t place = (((int64_t(id) * p.kv_heads + u.h) << tile_shift) + (next & ((1 << tile_shift) - 1)));
+            ++next;
+            if (lane == 0) {
+                const uint32_t bar = bars + 8u * uint32_t(stage);
+                if (id < 0) {
+                    mbar_arrive(bar);
+                } else if (a.inject && blockIdx.x == 0 && warp == 0 && sent == 1) {
+                    // test hook: this copy never comes
+                } else {
+                    mbar_arrive_expect_tx(bar, tile_bytes(D));
+                    bulk_load(ring + uint32_t(stage * tile_bytes(D)), p.cache + place * tile_bytes(D), tile_bytes(D), bar);
+                }
+            }
+        };
+        for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
+
+        for (int t = t0; t < last; ++t) {
+            const int stage = int(pos % kStages);
+            ok = __all_sync(0xffffffffu, wait_bounded(bars + 8u * uint32_t(stage), (pos / kStages) & 1u, abort_flag, a.status));
+            if (!ok) break;
+            ++pos;
+            if (next < last) fetch();   // into the tile's before this one, whose words the products have taken
+            const uint32_t base = ring + uint32_t(stage * tile_bytes(D));
+            const bool zero = (zeros >> stage) & 1u;
+
+            // ---- scores of tokens r8, r8 + 8 against rows 2 c, 2 c + 1
+            uint32_t kw[D / 16], ks[kGroups];   // ks: blocks of token r8, then of r8 + 8, two to a word
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 w = ld_shared_v4(base + uint32_t(512 * i + 16 * lane));
+                kw[4 * i] = w.x; kw[4 * i + 1] = w.y; kw[4 * i + 2] = w.z; kw[4 * i + 3] = w.w;
+            }
+            {
+                const uint32_t from = base + uint32_t(key_scales(D) + r8 * (D / 8));
+                if (D == 128) {
+                    const uint4 w = ld_shared_v4(from);
+                    ks[0] = w.x; ks[1] = w.y; ks[kGroups / 2] = w.z; ks[kGroups - 1] = w.w;
+                } else {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ks[0]), "=r"(ks[1]) : "r"(from) : "memory");
+                }
+                if (zero) {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) ks[g] = 0;
+                }
+            }
+            float y[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[nt][k] = 0.f;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                float acc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    acc[nt][0] = acc[nt][2] = off8[nt][g][0];
+                    acc[nt][1] = acc[nt][3] = off8[nt][g][1];
+                }
+#pragma unroll
+                for (int i = 2 * g; i < 2 * g + 2; ++i) {
+                    const uint32_t w8 = kw[i] >> 8;
+                    const uint32_t A[4] = {kw[i] & 0x000F000Fu, w8 & 0x000F000Fu, kw[i] & 0x00F000F0u, w8 & 0x00F000F0u};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt], A, qf[nt][i][0], qf[nt][i][1]);
+                }
+                const float2 lo = __half22float2(u2h(ks[g / 2])), hi = __half22float2(u2h(ks[kGroups / 2 + g / 2]));
+                const float d0 = g & 1 ? lo.y : lo.x, d1 = g & 1 ? hi.y : hi.x;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    y[nt][0] = fmaf(d0, acc[nt][0], y[nt][0]);
+                    y[nt][1] = fmaf(d0, acc[nt][1], y[nt][1]);
+                    y[nt][2] = fmaf(d1, acc[nt][2], y[nt][2]);
+                    y[nt][3] = fmaf(d1, acc[nt][3], y[nt][3]);
+                }
+            }
+            const int key = t * kTokens + r8;
+            const bool ragged = t * kTokens + kTokens > least;   // some row does not see all of it
+            bool rises = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    y[nt][k] = __fmul_rn(y[nt][k], f[nt][k & 1]);
+                    if (ragged && key + (k & 2 ? 8 : 0) >= see[nt][k & 1]) y[nt][k] = -INFINITY;
+                    rises |= y[nt][k] > m[nt][k & 1] + kGrow;
+                }
+            if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float top = fmaxf(y[nt][k], y[nt][k + 2]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float now = fmaxf(m[nt][k], top);
+                        // (-inf) - (-inf) only where the sums are still zero
+                        const float by = now == -INFINITY ? 1.f : ex2(m[nt][k] - now);
+                        m[nt][k] = now;
+                        l[nt][k] *= by;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[i * NT + nt][k] *= by;
+                            o[i * NT + nt][k + 2] *= by;
+                        }
+                    }
+            }
+            // ---- weights, as the B operand: tokens 2 c, 2 c + 1 and those + 8 of row r8
+            uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float ref = m[nt][k & 1] == -INFINITY ? 0.f : m[nt][k & 1];
+                    y[nt][k] = ex2(__fsub_rn(y[nt][k], ref));
+                    l[nt][k & 1] += y[nt][k];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const __half2 v = __floats2half2_rn(y[nt][2 * k], y[nt][2 * k + 1]);
+                    const float2 back = __half22float2(v);
+                    const __half2 rest = __floats2half2_rn(y[nt][2 * k] - back.x, y[nt][2 * k + 1] - back.y);
+                    hi[nt][k] = transpose8x8(h2u(v));
+                    lo[nt][k] = transpose8x8(h2u(rest));
+                }
+            }
+
+            // ---- values
+            uint32_t vs[kGroups][2];   // scales of tokens 2 c, 2 c + 1 and those + 8
+#pragma unroll
+            for (int g = 0; g < kGroups; g += 2) {
+                const uint4 w = ld_shared_v4(base + uint32_t(value_scales(D) + c4 * (D / 4) + 8 * g));
+                vs[g][0] = w.x; vs[g][1] = w.y; vs[g + 1][0] = w.z; vs[g + 1][1] = w.w;
+            }
+            if (zero) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) vs[g][0] = vs[g][1] = 0;
+            }
+            uint32_t off[kGroups];   // ragged tiles: tokens whose scale is no number, as bits
+            bool any_off = false;
+            if (ragged) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    off[g] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int token = 2 * c4 + (k & 1) + (k & 2 ? 8 : 0);
+                        const uint32_t bits = k & 1 ? vs[g][k >> 1] >> 16 : vs[g][k >> 1] & 0xFFFFu;
+                        const bool past = t * kTokens + token >= most;
+                        if (past || !finite16(bits)) vs[g][k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        if (!past && !finite16(bits)) off[g] |= 1u << token;
+                    }
+                    off[g] |= __shfl_xor_sync(0xffffffffu, off[g], 1);
+                    off[g] |= __shfl_xor_sync(0xffffffffu, off[g], 2);
+                    any_off |= off[g] != 0;
+                }
+            }
+            const __half2 bias_lo = __float2half2_rn(1032.f), bias_hi = __float2half2_rn(72.f);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t w;
+                if (i % 4 == 0) {
+                    const uint4 v = ld_shared_v4(base + uint32_t(value_codes(D) + 512 * (i / 4) + 16 * lane));
+                    kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
+                }
+                w = kw[i % 4];
+                const uint32_t w8 = w >> 8;
+                const __half2 d0 = u2h(vs[i / 2][0]), d1 = u2h(vs[i / 2][1]);
+                const uint32_t A[4] = {h2u(__hmul2(__hsub2(u2h((w & 0x000F000Fu) | 0x64006400u), bias_lo), d0)),
+                                       h2u(__hmul2(__hsub2(u2h((w & 0x00F000F0u) | 0x54005400u), bias_hi), d0)),
+                                       h2u(__hmul2(__hsub2(u2h((w8 & 0x000F000Fu) | 0x64006400u), bias_lo), d1)),
+                                       h2u(__hmul2(__hsub2(u2h((w8 & 0x00F000F0u) | 0x54005400u), bias_hi), d1))};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(o[i * NT + nt], A, lo[nt][0], lo[nt][1]);
+                    mma16816(o[i * NT + nt], A, hi[nt][0], hi[nt][1]);
+                }
+            }
+            if (ragged && any_off) {   // such a token's block is no number for the rows that see it, and only for them
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int n = min(16, max(0, see[nt][k] - t * kTokens));
+                        const uint32_t sees = (1u << n) - 1u;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+                            if (off[i / 2] & sees) o[i * NT + nt][k] = o[i * NT + nt][k + 2] = __int_as_float(0x7FC00000);
+                    }
+            }
+        }
+        if (!ok) break;
+
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], d);
+
+        at += t1 - t0;
+        offset += t1 - t0;
+        const bool starts = t0 == 0, ends = t1 == tiles;
+        if (starts && ends) {
+            float inv[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) inv[nt][k] = l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k];
+#pragma unroll
+            for (int k = 0; k < W::kRegs; ++k) {
+                int dim, row;
+                element<NT>(k, lane, dim, row);
+                store_row<D, R>(a, u, s, row, dim, o[k >> 2][k & 3] * inv[(k >> 2) % NT][k & 1]);
+            }
+            continue;
+        }
+        // A part of a unit: the warp's last, or its first.
+        const int slot = 2 * warp + (at == end ? 1 : 0);
+        float* const part = part_at(slot);
+#pragma unroll
+        for (int k = 0; k < W::kRegs; ++k) part[k * 32 + lane] = o[k >> 2][k & 3];
+        if (r8 == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    part[W::kRegs * 32 + 8 * nt + 2 * c4 + k] = m[nt][k];
+                    part[W::kRegs * 32 + R + 8 * nt + 2 * c4 + k] = l[nt][k];
+                }
+        if (lane == 0) {
+            sh.name[slot] = name;
+            sh.whole[slot] = (starts ? 1 : 0) | (ends ? 2 : 0);
+            sh.unit[slot] = u;
+        }
+    }
+    if (bad_page) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+    // After a wait that ran out: the copies still in flight.
+    for (; pos < sent; ++pos)
+        if (!(a.inject && blockIdx.x == 0 && warp == 0 && pos == 0))
+            wait_drain(bars + 8u * (pos % kStages), (pos / kStages) & 1u, a.status);
+    __syncthreads();
+
+    // ---- units of several warps: joined, finished or left for the join over CTAs
+    Mark mark{-1, -1, 0, 0, 0, 0};
+    if (!abort_flag.raised()) {
+        for (int i = 0; i < 2 * kWarps;) {
+            if (sh.name[i] < 0) {
+                ++i;
+                continue;
+            }
+            const int64_t name = sh.name[i];
+            int upto = i + 1, ends = sh.whole[i] & 2;
+            for (int j = i + 1; j < 2 * kWarps; ++j)
+                if (sh.name[j] == name) {
+                    upto = j + 1;
+                    ends = sh.whole[j] & 2;
+                } else if (sh.name[j] >= 0) {
+                    break;
+                }
+            const bool starts = sh.whole[i] & 1;
+            Join<D, NT> join;
+            for (int j = i; j < upto; ++j)
+                if (sh.name[j] >= 0) join.add(part_at(j));
+            if (starts && ends) {
+                join.finish(a, sh.unit[i], sequence(a, sh.unit[i].b, false));
+            } else {
+                join.keep(a.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * W::kPart);
+                if (starts) {
+                    mark.tail = name;
+                    mark.b = sh.unit[i].b;
+                    mark.h = sh.unit[i].h;
+                    mark.tile = sh.unit[i].tile;
+                } else {
+                    mark.head = name;
+                    mark.head_ends = ends;
+                }
+            }
+            i = upto;
+        }
+    }
+    if (threadIdx.x == 0) a.marks[blockIdx.x] = mark;
+}
+
+// Units of several CTAs: CTA i joins the one that starts in CTA i and does not end there.
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32) kv4_join_kernel(const Kv4Args a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    using W = Rows<D, NT>;
+    const Mark mark = a.marks[blockIdx.x];
+    if (mark.tail < 0) return;
+    Join<D, NT> join;
+    join.add(a.parts + (int64_t(blockIdx.x) * 2 + 1) * W::kPart);
+    for (unsigned j = blockIdx.x + 1; j < gridDim.x; ++j) {
+        const int64_t name = a.marks[j].head;
+        if (name < 0) {      // no tile at all, or an aborted CTA
+            continue;
+        }
+        if (name != mark.tail) break;
+        join.add(a.parts + int64_t(j) * 2 * W::kPart);
+        if (a.marks[j].head_ends) break;
+    }
+    join.finish(a, Unit{mark.b, mark.h, mark.tile}, sequence(a, mark.b, false));
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// Eight rows to a unit where a sequence has no more on average, else sixteen.
+bool narrow(const mmq_kv4_attention_t& p) { return p.tokens * (p.heads / p.kv_heads) <= int64_t(8) * p.batch; }
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <int D, int NT>
+size_t part_bytes(int nsm) {
+    return up256(size_t(nsm) * Rows<D, NT>::kCtas * 2 * Rows<D, NT>::kPart * 4);
+}
+size_t part_bytes(const mmq_kv4_attention_t& p, int nsm) {
+    if (p.head_dim == 64) return narrow(p) ? part_bytes<64, 1>(nsm) : part_bytes<64, 2>(nsm);
+    return narrow(p) ? part_bytes<128, 1>(nsm) : part_bytes<128, 2>(nsm);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
+    using W = Rows<D, NT>;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(kv4_rows_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes)))
+        return e;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned(nsm * W::kCtas)), dim3(kWarps * 32), W::kBytes, s, attr);
+    if ((e = cudaLaunchKernelEx(&cfg, kv4_rows_kernel<T, D, NT>, a))) return e;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a);
+}
+template <typename T, int D>
+cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
+    return narrow(a.p) ? launch<T, D, 1>(a, nsm, s) : launch<T, D, 2>(a, nsm, s);
+}
+
+}  // namespace
+
+namespace mmq {
+
+size_t kv4_attention_workspace(const mmq_kv4_attention_t& p) {
+    const int nsm = sm_count();
+    return nsm ? part_bytes(p, nsm) + up256(size_t(nsm) * 2 * sizeof(Mark)) : 0;
+}
+
+cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, int* status, int inject_timeout,
+                                 cudaStream_t s) {
+    const int nsm = sm_count();
+    if (!nsm) return cudaErrorInvalidDevice;
+    Kv4Args a;
+    a.p = p;
+    a.parts = static_cast<float*>(workspace);
+    a.marks = reinterpret_cast<Mark*>(static_cast<char*>(workspace) + part_bytes(p, nsm));
+    a.status = status;
+    a.inject = inject_timeout;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
+    a.group = p.heads / p.kv_heads;
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);
+    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, nsm, s) : launch<__nv_bfloat16, 128>(a, nsm, s);
+}
+
+}  // namespace mmq

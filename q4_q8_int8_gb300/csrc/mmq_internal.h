@@ -158,6 +158,12 @@ cudaError_t launch_shared_prefix_attention(const mmq_shared_prefix_attention_t& 
 // Mixture of q4_K experts for a few tokens (moe.cu); tokens >= 1.
 size_t q4K_moe_workspace(const mmq_q4K_moe_t& p);   // 0 on a CUDA error
 cudaError_t launch_q4K_moe(const mmq_q4K_moe_t& p, void* workspace, int* status, int inject_timeout, cudaStream_t s);
+// The 4-bit key/value cache (kv4.cu, kv4_attention.cu); tokens >= 1.
+cudaError_t launch_kv4_write(const mmq_kv4_write_t& p, int* status, cudaStream_t s);
+cudaError_t launch_kv4_read(const mmq_kv4_read_t& p, int* status, cudaStream_t s);
+size_t kv4_attention_workspace(const mmq_kv4_attention_t& p);   // 0 on a CUDA error
+cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, int* status, int inject_timeout,
+                                 cudaStream_t s);
 int small_m_launch_count(int64_t M, int64_t N, int64_t K);   // kernels per call, -1 on a CUDA error
 constexpr int64_t kSmallMMax = 64;
 
