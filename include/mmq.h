@@ -692,6 +692,62 @@ size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
  * MMQ_ERR_DEVICE / MMQ_ERR_RESOURCE / MMQ_ERR_CUDA. */
 int mmq_kv4_attention(const mmq_kv4_attention_t* p, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- pages of a key/value cache, of 16 bits or of 4 ----
+ *
+ * A pool is one cache or several (keys and values of every layer, say) that
+ * share their page numbers: n_pages pages of page_bytes bytes each, one after
+ * the other from each cache's pointer. */
+#define MMQ_PAGES_MAX_CACHES 256
+#define MMQ_PAGES_MAX (1 << 20)   /* pages of a pool that is compacted */
+
+typedef struct {
+    void* const* caches;     /* host array of n_caches device pointers         */
+    const int32_t* src;      /* [pairs] page numbers, device                   */
+    const int32_t* dst;      /* [pairs]                                        */
+    int64_t pairs, n_pages, page_bytes;
+    int32_t n_caches;
+} mmq_pages_copy_t;
+
+/* Page dst[i] = page src[i] in every cache, as a sequence that forks needs for
+ * the page it shares in part.  A pair with a negative number is left out, one
+ * with a number >= n_pages too and sets the device status word to MMQ_ERR_ARG.
+ * All pairs are copied at once: a page that is the destination of two, or of
+ * one and the source of another, is undefined.  page_bytes a multiple of 16,
+ * n_caches 1..256, caches 16-byte aligned (src, dst: 4-byte); pairs == 0 does
+ * nothing.  MMQ_ERR_ARG / MMQ_ERR_ALIGN / MMQ_ERR_DEVICE / MMQ_ERR_CUDA.
+ * Takes part in programmatic launch. */
+int mmq_pages_copy(const mmq_pages_copy_t* p, void* stream);
+
+typedef struct {
+    void* const* caches;     /* host array of n_caches device pointers (NULL:
+                              * none, only the tables are compacted)           */
+    const int32_t* page_table;/* [batch][table_width]                          */
+    const int32_t* lens;     /* [batch] tokens                                 */
+    int32_t* table_out;      /* [batch][table_width]; may be page_table        */
+    int32_t* page_map;       /* [n_pages]                                      */
+    int32_t* live;           /* [1]                                            */
+    int64_t n_pages, page_bytes, table_width;
+    int32_t batch, n_caches;
+    int32_t page_size;       /* tokens of a page, a power of two               */
+} mmq_pages_compact_t;
+
+/* Device workspace of one call (n_pages alone counts; 0 if refused). */
+size_t mmq_pages_compact_workspace(const mmq_pages_compact_t* p);
+
+/* Moves the live pages to the front of the pool.  A page is live if a
+ * sequence's table names it among its first ceil(lens / page_size) entries (a
+ * page of several sequences is one page).  With n of them, live pages below n
+ * stay and the k-th of the others goes to the k-th free place below n, in every
+ * cache.  page_map[p] is the page's new number, or -1 if it is free; table_out
+ * the table in new numbers, -1 past a sequence's pages; live[0] = n, so that
+ * pages n .. n_pages - 1 are free afterwards (what they hold is left there).  A
+ * length over table_width * page_size is cut to it, a page number outside [0,
+ * n_pages) becomes -1; either sets the device status word to MMQ_ERR_ARG.
+ * n_pages up to 2^20; page_size up to 2^20; otherwise as mmq_pages_copy.
+ * Workspace 256-byte aligned, caller-owned, not used by anything else until
+ * the stream passes the call. */
+int mmq_pages_compact(const mmq_pages_compact_t* p, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Test hook: force the K split of the dot-product kernels (q4_K, M <= 4;
  * q6_K, M <= 16) for later calls on this host thread: ks = 1, 2 or 4 warps
  * per row group (the SwiGLU epilogue takes 1 or 2; a forced 4 makes its

@@ -47,6 +47,7 @@ EXPORTS = (
     "mmq_qk_norm_rope", "mmq_shared_prefix_attention", "mmq_shared_prefix_attention_workspace",
     "mmq_q4K_moe", "mmq_q4K_moe_workspace",
     "mmq_kv4_page_bytes", "mmq_kv4_write", "mmq_kv4_read", "mmq_kv4_attention", "mmq_kv4_attention_workspace",
+    "mmq_pages_copy", "mmq_pages_compact", "mmq_pages_compact_workspace",
     "mmq_status", "mmq_strerror", "mmq_debug_inject_timeout", "mmq_debug_force_gemv_split",
     "mmq_set_programmatic_launch",
 )
@@ -111,6 +112,19 @@ class mmq_kv4_attention_t(ctypes.Structure):
                 ("q_stride", _I64), ("tokens", _I64), ("n_pages", _I64), ("table_width", _I64),
                 ("batch", _I32), ("heads", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("page_size", _I32),
                 ("type", _I32), ("out_type", _I32), ("scale", ctypes.c_float)]
+
+
+class mmq_pages_copy_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("caches", ctypes.POINTER(_P)), ("src", _P), ("dst", _P), ("pairs", _I64), ("n_pages", _I64),
+                ("page_bytes", _I64), ("n_caches", _I32)]
+
+
+class mmq_pages_compact_t(ctypes.Structure):
+    """Mirror of the C struct."""
+    _fields_ = [("caches", ctypes.POINTER(_P)), ("page_table", _P), ("lens", _P), ("table_out", _P), ("page_map", _P),
+                ("live", _P), ("n_pages", _I64), ("page_bytes", _I64), ("table_width", _I64), ("batch", _I32),
+                ("n_caches", _I32), ("page_size", _I32)]
 
 
 _lock = threading.Lock()
@@ -181,6 +195,9 @@ def load_library(path: str = LIB_PATH):
                 "mmq_kv4_read": ([ctypes.POINTER(mmq_kv4_read_t), P], ctypes.c_int),
                 "mmq_kv4_attention_workspace": ([ctypes.POINTER(mmq_kv4_attention_t)], S),
                 "mmq_kv4_attention": ([ctypes.POINTER(mmq_kv4_attention_t), P, S, P], ctypes.c_int),
+                "mmq_pages_copy": ([ctypes.POINTER(mmq_pages_copy_t), P], ctypes.c_int),
+                "mmq_pages_compact_workspace": ([ctypes.POINTER(mmq_pages_compact_t)], S),
+                "mmq_pages_compact": ([ctypes.POINTER(mmq_pages_compact_t), P, S, P], ctypes.c_int),
                 "mmq_status": ([P], ctypes.c_int),
                 "mmq_strerror": ([ctypes.c_int], ctypes.c_char_p),
                 "mmq_debug_inject_timeout": ([ctypes.c_int], None),
@@ -1087,3 +1104,111 @@ def kv4_attention(q, cache, page_table, lens, q_starts=None, scale=None, out=Non
     if rc:
         _check(rc, "mmq_kv4_attention")
     return out
+
+
+# ---- pages of a key/value cache ------------------------------------------------
+MMQ_PAGES_MAX_CACHES = 256
+
+
+def mmq_pages_copy(p, stream):
+    return load_library().mmq_pages_copy(ctypes.byref(p), stream)
+
+
+def mmq_pages_compact_workspace(p):
+    return load_library().mmq_pages_compact_workspace(ctypes.byref(p))
+
+
+def mmq_pages_compact(p, workspace, workspace_bytes, stream):
+    return load_library().mmq_pages_compact(ctypes.byref(p), workspace, workspace_bytes, stream)
+
+
+def _pool(caches, dev: int, what: str):
+    """(host array of the caches' pointers, pages, bytes of one page); refuses caches that are not alike."""
+    first = caches[0]
+    shape, dt = first.shape, first.dtype
+    pages = shape[0]
+    for c in caches:
+        if c.shape != shape or c.dtype is not dt or not c.is_contiguous() or c.get_device() != dev:
+            _refuse(f"{what}: the caches must be contiguous and alike, [pages][...], on one device")
+    n = len(caches)
+    if n > MMQ_PAGES_MAX_CACHES:
+        _refuse(f"{what}: at most {MMQ_PAGES_MAX_CACHES} caches")
+    size = first.element_size()
+    for d in shape[1:]:
+        size *= d
+    return (_P * n)(*[c.data_ptr() for c in caches]), pages, size
+
+
+def pages_copy(caches, src, dst, stream=None):
+    """Copy whole pages in every cache of a pool: page dst[i] = page src[i].
+
+    caches: up to 256 tensors that share their page numbers (keys and values of
+    every layer, say, of any type: a 4-bit cache too), contiguous and alike,
+    [pages][...], a page a multiple of 16 bytes; src, dst int32 [n] (a pair with
+    a negative number is left out).  All pairs are copied at once: no page may
+    be the destination of two, or of one and the source of another.  A number
+    out of range shows in status()."""
+    torch = _t or _torch()
+    dev, i32, n = src.get_device(), torch.int32, src.numel()
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        _refuse("pages_copy: src and the stream must be on the current GPU")
+    if (src.dtype is not i32 or dst.dtype is not i32 or not src.is_contiguous() or not dst.is_contiguous()
+            or dst.numel() != n or dst.get_device() != dev):
+        _refuse("pages_copy: src and dst must be int32 [n] on one device")
+    if not caches:
+        return
+    pointers, pages, size = _pool(caches, dev, "pages_copy")
+    p = mmq_pages_copy_t(pointers, src.data_ptr(), dst.data_ptr(), n, pages, size, len(caches))
+    rc = (_lib or load_library()).mmq_pages_copy(
+        p, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_pages_copy")
+
+
+def pages_compact(caches, page_table, lens, page_size: int, pages: int | None = None, table_out=None, workspace=None,
+                  stream=None):
+    """Move the live pages of a pool to its front, in every cache.
+
+    caches as in pages_copy (or none, with `pages` their number, up to 2^20
+    either way); page_table int32 [batch][width], lens int32 [batch]: a page is
+    live if it is among the first ceil(lens / page_size) of a row.  Returns (the
+    table in new page numbers, int32 [batch][width], -1 past a sequence's pages,
+    or into `table_out`, which may be page_table; int32 [pages]: each page's new
+    number or -1; int32 [1]: how many are live, so that the pages from there on
+    are free).  Live pages move only where they have to, into free places.
+    `workspace`: a contiguous CUDA uint8 tensor of mmq_pages_compact_workspace
+    bytes, allocated per call if None."""
+    torch = _t or _torch()
+    dev, i32, device = page_table.get_device(), torch.int32, page_table.device
+    batch, width = shape = page_table.shape
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        _refuse("pages_compact: page_table and the stream must be on the current GPU")
+    if (page_table.dtype is not i32 or not page_table.is_contiguous() or lens.dtype is not i32 or not lens.is_contiguous()
+            or lens.numel() != batch or lens.get_device() != dev):
+        _refuse("pages_compact: page_table must be int32 [batch][width], lens int32 [batch], on one device")
+    if caches:
+        pointers, n, size = _pool(caches, dev, "pages_compact")
+        if pages is not None and pages != n:
+            _refuse("pages_compact: pages must be the caches' number")
+    elif pages is None:
+        _refuse("pages_compact: without caches, pages must be given")
+    else:
+        pointers, n, size = None, pages, 16
+    if table_out is None:
+        table_out = _empty(shape, i32, device, stream)
+    elif (table_out.dtype is not i32 or table_out.shape != shape or not table_out.is_contiguous()
+          or table_out.get_device() != dev):
+        _refuse("pages_compact: table_out must be int32 [batch][width] on page_table's device")
+    page_map, live = _empty((n,), i32, device, stream), _empty((1,), i32, device, stream)
+    p = mmq_pages_compact_t(pointers, page_table.data_ptr(), lens.data_ptr(), table_out.data_ptr(), page_map.data_ptr(),
+                            live.data_ptr(), n, size, width, batch, len(caches) if caches else 0, page_size)
+    lib = _lib or load_library()
+    if workspace is None:
+        workspace = _workspace(lib.mmq_pages_compact_workspace(p), device, stream, "pages_compact")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("pages_compact: workspace must be contiguous, on page_table's device")
+    rc = lib.mmq_pages_compact(p, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mmq_pages_compact")
+    return table_out, page_map, live

@@ -683,6 +683,62 @@ int mmq_kv4_attention(const mmq_kv4_attention_t* p, void* workspace, size_t work
     return e == cudaErrorLaunchOutOfResources ? MMQ_ERR_RESOURCE : from_cuda(e);
 }
 
+// The caches of a pool: MMQ_OK, MMQ_ERR_ARG or MMQ_ERR_ALIGN.
+static int check_pool(void* const* caches, int32_t n_caches, int64_t n_pages, int64_t page_bytes) {
+    if (n_caches < 0 || n_caches > MMQ_PAGES_MAX_CACHES || n_pages < 0 || n_pages > (int64_t(1) << 31) - 1) return MMQ_ERR_ARG;
+    if (n_caches > 0 && !caches) return MMQ_ERR_ARG;
+    if (page_bytes < 16 || page_bytes % 16 || page_bytes > (int64_t(1) << 32)) return MMQ_ERR_ARG;
+    for (int i = 0; i < n_caches; ++i) {
+        if (!caches[i] && n_pages > 0) return MMQ_ERR_ARG;
+        if (!aligned16(caches[i])) return MMQ_ERR_ALIGN;
+    }
+    return MMQ_OK;
+}
+
+int mmq_pages_copy(const mmq_pages_copy_t* p, void* stream) {
+    if (!p || p->pairs < 0 || p->pairs > (int64_t(1) << 31) - 1 || p->n_caches < 1) return MMQ_ERR_ARG;
+    int rc = check_pool(p->caches, p->n_caches, p->n_pages, p->page_bytes);
+    if (rc) return rc;
+    if (p->pairs == 0) return check_device();
+    if (!p->src || !p->dst) return MMQ_ERR_ARG;
+    if (!aligned4(p->src) || !aligned4(p->dst)) return MMQ_ERR_ALIGN;
+    if ((rc = check_device())) return rc;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_pages_copy(*p, status, static_cast<cudaStream_t>(stream)));
+}
+
+// The sizes of a compaction (no device pointers): MMQ_OK or MMQ_ERR_ARG.
+static int check_compact_sizes(const mmq_pages_compact_t* p) {
+    if (!p || p->n_pages < 0 || p->n_pages > MMQ_PAGES_MAX || p->batch < 0 || p->batch > (1 << 20)) return MMQ_ERR_ARG;
+    if (p->page_size < 1 || p->page_size > (1 << 20) || (p->page_size & (p->page_size - 1))) return MMQ_ERR_ARG;
+    if (p->table_width < 0 || p->table_width > ((int64_t(1) << 31) - 1) / p->page_size) return MMQ_ERR_ARG;
+    return MMQ_OK;
+}
+
+size_t mmq_pages_compact_workspace(const mmq_pages_compact_t* p) {
+    return check_compact_sizes(p) ? 0 : mmq::pages_compact_workspace(*p);
+}
+
+int mmq_pages_compact(const mmq_pages_compact_t* p, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_compact_sizes(p);
+    if (rc) return rc;
+    if ((rc = check_pool(p->caches, p->n_caches, p->n_pages, p->n_caches ? p->page_bytes : 16))) return rc;
+    const bool entries = p->batch > 0 && p->table_width > 0;
+    if (!p->live || !workspace || (p->n_pages > 0 && !p->page_map) || (p->batch > 0 && !p->lens) ||
+        (entries && (!p->page_table || !p->table_out)))
+        return MMQ_ERR_ARG;
+    for (const int32_t* v : {p->page_table, p->lens, static_cast<const int32_t*>(p->table_out),
+                             static_cast<const int32_t*>(p->page_map), static_cast<const int32_t*>(p->live)})
+        if (!aligned4(v)) return MMQ_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return MMQ_ERR_ALIGN;
+    if ((rc = check_device())) return rc;
+    if (workspace_bytes < mmq::pages_compact_workspace(*p)) return MMQ_ERR_ARG;
+    int* status = mmq::status_word_ptr();
+    if (!status) return MMQ_ERR_CUDA;
+    return from_cuda(mmq::launch_pages_compact(*p, workspace, status, static_cast<cudaStream_t>(stream)));
+}
+
 int mmq_status(void* stream) {
     int* p = mmq::status_word_ptr();
     if (!p) return MMQ_ERR_CUDA;

@@ -164,6 +164,10 @@ cudaError_t launch_kv4_read(const mmq_kv4_read_t& p, int* status, cudaStream_t s
 size_t kv4_attention_workspace(const mmq_kv4_attention_t& p);   // 0 on a CUDA error
 cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, int* status, int inject_timeout,
                                  cudaStream_t s);
+// Page copies and compaction (pages.cu); pairs >= 1, n_pages >= 1.
+cudaError_t launch_pages_copy(const mmq_pages_copy_t& p, int* status, cudaStream_t s);
+size_t pages_compact_workspace(const mmq_pages_compact_t& p);
+cudaError_t launch_pages_compact(const mmq_pages_compact_t& p, void* workspace, int* status, cudaStream_t s);
 int small_m_launch_count(int64_t M, int64_t N, int64_t K);   // kernels per call, -1 on a CUDA error
 constexpr int64_t kSmallMMax = 64;
 

@@ -1,4 +1,6 @@
 """Refusals of the 4-bit cache's entry points, before any device work."""
+import ctypes
+
 import pytest
 
 import q4_q8_int8_gb300 as mmq
@@ -84,3 +86,56 @@ def test_null_structs():
 def test_page_bytes():
     assert mmq.mmq_kv4_page_bytes(8, 128, 16) == 8 * 18 * 128 and mmq.mmq_kv4_page_bytes(2, 64, 64) == 2 * 4 * 18 * 64
     assert not any((mmq.mmq_kv4_page_bytes(0, 128, 16), mmq.mmq_kv4_page_bytes(8, 96, 16), mmq.mmq_kv4_page_bytes(8, 64, 12)))
+
+
+def pointers(*at):
+    return (ctypes.c_void_p * len(at))(*at)
+
+
+def copy(caches=(0x10000, 0x20000), **change):
+    f = dict(caches=None if caches is None else pointers(*caches), src=0x30000, dst=0x40000, pairs=3, n_pages=10,
+             page_bytes=64, n_caches=2 if caches is None else len(caches))
+    f.update(change)
+    return mmq.mmq_pages_copy(mmq.mmq_pages_copy_t(**f), None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(caches=None), dict(caches=(0x10000, None)), dict(caches=()), dict(caches=(0x10000,) * 257), dict(src=None),
+    dict(dst=None), dict(pairs=-1), dict(pairs=2 ** 31), dict(n_pages=-1), dict(n_pages=2 ** 31), dict(page_bytes=0),
+    dict(page_bytes=24), dict(page_bytes=-16), dict(page_bytes=2 ** 32 + 16), dict(n_caches=-1)])
+def test_copy_refuses_arguments(change):
+    assert copy(**change) == mmq.MMQ_ERR_ARG
+
+
+@pytest.mark.parametrize("change", [dict(caches=(0x10000, 0x20008)), dict(src=0x30002), dict(dst=0x40001)])
+def test_copy_refuses_alignment(change):
+    assert copy(**change) == mmq.MMQ_ERR_ALIGN
+
+
+def compact(caches=(0x10000,), workspace=0x100, ws_bytes=1 << 30, **change):
+    f = dict(caches=None if caches is None else pointers(*caches), page_table=0x20000, lens=0x30000, table_out=0x40000,
+             page_map=0x50000, live=0x60000, n_pages=10, page_bytes=64, table_width=4, batch=3,
+             n_caches=1 if caches is None else len(caches), page_size=16)
+    f.update(change)
+    return mmq.mmq_pages_compact(mmq.mmq_pages_compact_t(**f), workspace, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(caches=None), dict(caches=(None,)), dict(caches=(0x10000,) * 257), dict(page_table=None), dict(lens=None),
+    dict(table_out=None), dict(page_map=None), dict(live=None), dict(workspace=None), dict(n_pages=-1),
+    dict(n_pages=(1 << 20) + 1), dict(page_bytes=40), dict(table_width=-1), dict(table_width=1 << 28), dict(batch=-1),
+    dict(batch=(1 << 20) + 1), dict(page_size=0), dict(page_size=12), dict(page_size=1 << 21), dict(n_caches=-1)])
+def test_compact_refuses_arguments(change):
+    assert compact(**change) == mmq.MMQ_ERR_ARG
+
+
+@pytest.mark.parametrize("change", [dict(caches=(0x10004,)), dict(page_table=2), dict(lens=1), dict(table_out=0x40002),
+                                    dict(page_map=0x50001), dict(live=0x60002), dict(workspace=0x180)])
+def test_compact_refuses_alignment(change):
+    assert compact(**change) == mmq.MMQ_ERR_ALIGN
+
+
+def test_pages_null_structs():
+    lib = mmq.load_library()
+    assert lib.mmq_pages_copy(None, None) == lib.mmq_pages_compact(None, None, 0, None) == mmq.MMQ_ERR_ARG
+    assert lib.mmq_pages_compact_workspace(None) == 0

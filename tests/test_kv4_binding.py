@@ -111,3 +111,52 @@ def test_what_is_passed_on(world):  # noqa: F811
     assert (p.tokens, p.batch, p.q_stride, p.scale, bool(p.q_starts)) == (7, 3, 999 * 8, 0.5, True)
     attend()
     assert not world.lib.calls[-1][1][0].q_starts
+
+
+def copy(caches=None, src=None, dst=None, **more):
+    caches = [Tensor((8, 64), u8), Tensor((8, 64), u8)] if caches is None else caches
+    mmq.pages_copy(caches, Tensor(3, i32) if src is None else src, Tensor(3, i32) if dst is None else dst, **more)
+
+
+def compact(caches=None, table=None, lens=None, **more):
+    caches = [Tensor((8, 64), u8), Tensor((8, 64), u8)] if caches is None else caches
+    mmq.pages_compact(caches, Tensor((3, 2), i32) if table is None else table, Tensor(3, i32) if lens is None else lens, 16, **more)
+
+
+@pytest.mark.parametrize("call", [copy, compact])
+def test_pages_devices(world, call, monkeypatch):  # noqa: F811
+    test_devices(world, call, monkeypatch)
+
+
+@pytest.mark.parametrize("call", [copy, compact])
+@pytest.mark.parametrize("caches", [
+    [Tensor((8, 64), u8), Tensor((9, 64), u8)], [Tensor((8, 64), u8), Tensor((8, 64), f16)],
+    [Tensor((8, 64), u8, stride=(128, 1))], [Tensor((8, 64), u8)] * 257])
+def test_caches_that_are_not_alike(world, call, caches):  # noqa: F811
+    refused(world, call, caches=caches)
+
+
+@pytest.mark.parametrize("change", [dict(src=Tensor(3, torch.int64)), dict(dst=Tensor(2, i32)), dict(dst=Tensor(3, i32, stride=(2,)))])
+def test_copy_refuses(world, change):  # noqa: F811
+    refused(world, copy, **change)
+
+
+@pytest.mark.parametrize("change", [
+    dict(table=Tensor((3, 2), torch.int64)), dict(lens=Tensor(2, i32)), dict(lens=Tensor(3, torch.int64)), dict(pages=9),
+    dict(caches=[]), dict(table_out=Tensor((3, 2), torch.int64)), dict(table_out=Tensor((2, 3), i32)),
+    dict(workspace=Tensor(1 << 20, u8, stride=(2,)))])
+def test_compact_refuses(world, change):  # noqa: F811
+    refused(world, compact, **change)
+
+
+def test_pages_allocations_and_what_is_passed_on(world):  # noqa: F811
+    compact(stream=world.side)
+    assert world.blocks == [world.side] * 4 and world.lib.calls[-1][1][-1] == 77
+    p = world.lib.calls[-1][1][0]
+    assert (p.n_pages, p.page_bytes, p.table_width, p.batch, p.n_caches, p.page_size) == (8, 64, 2, 3, 2, 16)
+    compact(caches=[], pages=5)
+    p = world.lib.calls[-1][1][0]
+    assert (p.n_pages, p.n_caches) == (5, 0) and not p.caches
+    copy(caches=[Tensor((8, 16, 4), torch.float32)])
+    p = world.lib.calls[-1][1][0]
+    assert (p.pairs, p.n_pages, p.page_bytes, p.n_caches) == (3, 8, 256, 1)
