@@ -46,8 +46,10 @@ using namespace mmq::ptx;
 using namespace mmq::kv4;
 using mmq::tc::ld_shared_v4;
 
-constexpr int kWarps = 8;
-constexpr float kGrow = 8.f;
+constexpr int kWarps = 4;
+constexpr int kStep = 2 * kTokens;   // keys that a warp takes at a time
+constexpr float kLift = 7.f, kSpan = 14.f;   // a row's reference is 7 (in log2) under its largest score at first, 14 at most
+constexpr float kNone = -3.402823466e38f;   // the reference before any score: no score is under it but -Inf
 constexpr int kLeast = 2;   // tiles to a run, where there are too few for all warps
 
 struct Kv4Args {
@@ -58,6 +60,7 @@ struct Kv4Args {
     int inject;
     int page_shift, group;
     float scale_log2;
+    uint32_t low, high;   // masks of codes: 0x000F000F, 0x00F000F0
 };
 // What a CTA leaves of units that it shares with other CTAs: the start of a
 // unit's run of tiles is its name.
@@ -76,6 +79,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same without an accumulator, and with bfloat16 operands.
+__device__ __forceinline__ void mma16816_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma16816_bf16_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (v & mask) | bits
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+    return d;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t d;
@@ -127,7 +147,7 @@ __device__ __forceinline__ int units(const Sequence& s, int group) {
 template <int R>
 __device__ __forceinline__ int unit_tiles(const Sequence& s, int group, int u) {
     const int last = int(min(int64_t(s.n) - 1, (int64_t(u) * R + R - 1) / group));
-    return max(1, (seen(s, last) + kTokens - 1) / kTokens);
+    return max(1, (seen(s, last) + kStep - 1) / kStep);
 }
 template <int R>
 __device__ __forceinline__ int64_t sequence_tiles(const Sequence& s, int group) {
@@ -149,9 +169,9 @@ struct Rows {
     static constexpr int R = 8 * NT;
     static constexpr int kRegs = D / 16 * 4 * NT;         // accumulators per lane
     static constexpr int kPart = kRegs * 32 + 2 * R;      // floats of a part: sums [reg][lane], then m, l [row]
-    static constexpr int kCtas = NT == 1 ? 2 : 1;         // per SM
-    static constexpr int kStages = D == 128 && NT == 1 ? 4 : D == 128 ? 6 : 8;
-    static constexpr int kRing = kStages * tile_bytes(D); // a warp's; its last part lies over it
+    static constexpr int kCtas = NT == 1 ? 3 : 2;         // per SM
+    static constexpr int kStages = D == 128 && NT == 1 ? 3 : 4;   // steps of two tiles
+    static constexpr int kRing = kStages * 2 * tile_bytes(D); // a warp's; its last part lies over it
     static constexpr int kOffFirst = kWarps * kRing;      // and its first part here
     static constexpr int kOffBar = kOffFirst + kWarps * kPart * 4;
     static constexpr int kBytes = kOffBar + kWarps * kStages * 8;
@@ -170,6 +190,7 @@ __device__ __forceinline__ void element(int k, int lane, int& dim, int& row) {
 struct Unit {
     int b, h, tile;
 };
+__device__ __align__(16) const uint8_t zero_tile[tile_bytes(128)] = {};   // of a page that does not exist
 template <int D, int R>
 __device__ __forceinline__ void store_row(const Kv4Args& a, const Unit& u, const Sequence& s, int row, int dim, float x) {
     const int64_t r = int64_t(u.tile) * R + row;
@@ -179,39 +200,44 @@ __device__ __forceinline__ void store_row(const Kv4Args& a, const Unit& u, const
     store_value(a.p.out, a.p.out_type, ((s.start + j) * a.p.heads + head) * D + dim, x);
 }
 
-// Parts of one unit, added up by a CTA: warp w and lane have registers w, w + 8, ... of all lanes, which are of one row.
+// Parts of one unit, added up by a CTA: a thread has some registers of its lane, all of one row.
 template <int D, int NT>
 struct Join {
     using W = Rows<D, NT>;
-    static constexpr int kMine = W::kRegs / kWarps;
-    float acc[kMine] = {}, m = -INFINITY, l = 0.f;
-    int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, dim, row;
+    static constexpr int kMine = W::kRegs / kWarps, kSame = kWarps / 2 / NT;   // warps of the same row
+    static_assert(kSame >= 1, "a row per thread");
+    float acc[kMine] = {}, m = kNone, l = 0.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = warp & 1, nt = (warp >> 1) % NT, rest = (warp >> 1) / NT;
+    const int row = 8 * nt + 2 * (lane & 3) + col;
 
-    __device__ __forceinline__ Join() { element<NT>(warp, lane, dim, row); }
+    __device__ __forceinline__ int reg(int i) const {   // as element() has it
+        const int c = rest + kSame * i;
+        return 4 * ((c >> 1) * NT + nt) + 2 * (c & 1) + col;
+    }
     __device__ __forceinline__ void add(const float* part) {
         const float pm = part[W::kRegs * 32 + row], pl = part[W::kRegs * 32 + W::R + row];
         if (pl == 0.f) return;   // no key
         const float top = fmaxf(m, pm);
-        const float mine = l == 0.f ? 0.f : ex2(m - top), its = ex2(pm - top);
+        const float mine = ex2(m - top), its = ex2(pm - top);
         m = top;
         l = l * mine + pl * its;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) acc[i] = acc[i] * mine + part[(warp + kWarps * i) * 32 + lane] * its;
+        for (int i = 0; i < kMine; ++i) acc[i] = acc[i] * mine + part[reg(i) * 32 + lane] * its;
     }
     __device__ __forceinline__ void finish(const Kv4Args& a, const Unit& u, const Sequence& s) const {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            int at, same;
-            element<NT>(warp + kWarps * i, lane, at, same);
-            store_row<D, W::R>(a, u, s, row, at, acc[i] * inv);
+            int dim, same;
+            element<NT>(reg(i), lane, dim, same);
+            store_row<D, W::R>(a, u, s, row, dim, acc[i] * inv);
         }
     }
     __device__ __forceinline__ void keep(float* part) const {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) part[(warp + kWarps * i) * 32 + lane] = acc[i];
-        // one lane of those that have the row, for the first registers' warps
-        if (lane < 4 && warp < 4 * NT && (warp & 2) == 0) {
+        for (int i = 0; i < kMine; ++i) part[reg(i) * 32 + lane] = acc[i];
+        if (lane < 4 && rest == 0) {
             part[W::kRegs * 32 + row] = m;
             part[W::kRegs * 32 + W::R + row] = l;
         }
@@ -219,8 +245,9 @@ struct Join {
 };
 
 // ------------------------------------------------------------------ kernel
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(const Kv4Args a) {
+// kFine: weights as two fp16 values, for a result that shows it.
+template <typename T, int D, int NT, bool kFine>
+__global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kernel(const Kv4Args a) {
     using W = Rows<D, NT>;
     constexpr int R = W::R, kStages = W::kStages, kGroups = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -243,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
     const uint32_t bars = smem_u32(smem) + uint32_t(W::kOffBar + warp * kStages * 8);
 
     if (lane == 0)
-        for (int i = 0; i < kStages; ++i) mbar_init(bars + 8u * uint32_t(i), 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(bars + 8u * uint32_t(i), 2);
     if (threadIdx.x == 0) sh.aborted = 0;
     if (threadIdx.x < 2 * kWarps) sh.name[threadIdx.x] = -1;
     fence_barrier_init();
@@ -300,9 +327,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
     auto part_at = [&](int slot) {
         return reinterpret_cast<float*>(smem + (slot & 1 ? (slot >> 1) * W::kRing : W::kOffFirst + (slot >> 1) * W::kPart * 4));
     };
-    uint32_t pos = 0;              // copies taken so far
-    uint32_t sent = 0;             // copies issued so far
+    int stage = 0, fill = 0, flying = 0;   // the ring's next step to take, to fill, and those under way
+    uint32_t phase = 0;
+    bool withheld = a.inject && blockIdx.x == 0 && warp == 0;   // test hook: the first copies never come
     bool ok = true, bad_page = false;
+    // The masks are kernel arguments so that they stay in registers: an instruction takes one constant, the other bits.
+    const uint32_t low = a.low, high = a.high;   // 0x000F000F, 0x00F000F0
     float o[W::kRegs / 4][4];
     float m[NT][2], l[NT][2];      // of rows 2 c, 2 c + 1
 
@@ -330,7 +360,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
 
         // Queries: lane's row is r8 (of each eight), its dimensions 2 c, 2 c + 1 and those + 8 of every 16.
         uint32_t qf[NT][D / 16][2];
-        float off8[NT][kGroups][2];    // -8 sum q' of rows 2 c, 2 c + 1, in units of the products
+        uint32_t qs[NT][2];            // -8 sum q' of each block, times 2^112, as an operand
         float f[NT][2];
         int see[NT][2], most = 0, least = 0x7FFFFFFF;
 #pragma unroll
@@ -372,24 +402,42 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
                 const float2 w0 = __half22float2(v0), w1 = __half22float2(v1);
                 sum[i / 2] += (w0.x + w0.y) + 16.f * (w1.x + w1.y);
             }
-            // The products carry 2^-24 from the codes.  Held below infinity: all scores of the row are too large by
-            // then for it to matter, but zeros stay zeros.
-            const float mine_f = fminf(a.scale_log2 * __uint_as_float(uint32_t(127 + e - 13) << 23) * 0x1p24f, 3.4e38f);
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-                sum[g] *= -8.f * 0x1p-24f;
+                sum[g] *= -8.f * 0x1p-24f * 0x1p112f;
             }
-            const int mine_see = has ? min(seen(s, j), t1 * kTokens) : 0;
+            // As three bfloat16 each, in the order in which take() has the scales: of 16 places, lane c has 2 c, 2 c + 1
+            // (first word) and those + 8 (second), the scales of blocks 2 c, 2 c + 1 modulo their number.
+            uint32_t part[3][kGroups / 2];
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int g = 0; g < kGroups; g += 2) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(sum[g], sum[g + 1]);
+                    sum[g] -= __low2float(v);
+                    sum[g + 1] -= __high2float(v);
+                    part[k][g / 2] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+            if (D == 128) {
+                const uint32_t one = c4 & 1 ? part[0][kGroups / 2 - 1] : part[0][0], two = c4 & 1 ? part[1][kGroups / 2 - 1] : part[1][0];
+                qs[nt][0] = c4 & 2 ? two : one;
+                qs[nt][1] = c4 & 2 ? 0u : c4 & 1 ? part[2][kGroups / 2 - 1] : part[2][0];
+            } else {
+                qs[nt][0] = c4 == 0 ? part[0][0] : c4 == 1 ? part[1][0] : c4 == 2 ? part[2][0] : 0u;
+                qs[nt][1] = 0u;
+            }
+            // The products carry 2^-24 from the codes.  Held below infinity: all scores of the row are too large by
+            // then for it to matter, but zeros stay zeros.
+            const float mine_f = fminf(a.scale_log2 * __uint_as_float(uint32_t(127 + e - 13) << 23) * 0x1p24f, 3.4e38f);
+            const int mine_see = has ? min(seen(s, j), t1 * kStep) : 0;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int from = (2 * c4 + k) * 4;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) off8[nt][g][k] = __shfl_sync(0xffffffffu, sum[g], from);
                 f[nt][k] = __shfl_sync(0xffffffffu, mine_f, from);
                 see[nt][k] = __shfl_sync(0xffffffffu, mine_see, from);
-                m[nt][k] = -INFINITY;
+                m[nt][k] = kNone;
                 l[nt][k] = 0.f;
             }
             most = max(most, mine_see);
@@ -405,127 +453,123 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 
-        const int last = min(t1, (most + kTokens - 1) / kTokens);   // tiles with a key
-        // Tile t's copy.  The pages of 32 tiles at a time are in the lanes.
+        const int last = min(t1, (most + kStep - 1) / kStep);   // steps with a key
+        // Copies, of two tiles a step.  Lanes 2 i and 2 i + 1 have the places of step i of the next 16 and issue its copies.
         const int32_t* const table = p.page_table + int64_t(b) * p.table_width;
         const int tile_shift = a.page_shift - 4;
-        int32_t ids = -1;
-        uint32_t zeros = 0;            // stages that stand for a page of zeros
+        const uint8_t* src = zero_tile;
         int next = t0;
         auto fetch = [&]() {
-            const int i = (next - t0) & 31;
+            const int i = (next - t0) & 15;
             if (i == 0) {
-                ids = -1;
-                if (next + lane < last) {
-                    ids = table[(next + lane) >> tile_shift];
-                    if (ids < 0 || ids >= p.n_pages) {
-                        ids = -1;
+                const int tile = 2 * next + lane;
+                src = zero_tile;
+                if (tile * kTokens < most) {
+                    const int32_t id = table[tile >> tile_shift];
+                    if (id < 0 || id >= p.n_pages)
                         bad_page = true;
-                    }
+                    else
+                        src = p.cache + (((int64_t(id) * p.kv_heads + u.h) << tile_shift) + (tile & ((1 << tile_shift) - 1))) *
+                                            tile_bytes(D);
                 }
             }
-            const int32_t id = __shfl_sync(0xffffffffu, ids, i);
-            const int stage = int(sent % kStages);
-            ++sent;
-            zeros = id < 0 ? zeros | (1u << stage) : zeros & ~(1u << stage);
-            const int64_t place = (((int64_t(id) * p.kv_heads + u.h) << tile_shift) + (next & ((1 << tile_shift) - 1)));
+            const uint32_t bar = bars + 8u * uint32_t(fill), dst = ring + uint32_t(fill * 2 * tile_bytes(D)) + uint32_t(lane & 1) * tile_bytes(D);
+            if (lane >> 1 == i && !withheld) {
+                mbar_arrive_expect_tx(bar, tile_bytes(D));
+                bulk_load(dst, src, tile_bytes(D), bar);
+            }
+            withheld = false;
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+            ++flying;
             ++next;
-            if (lane == 0) {
-                const uint32_t bar = bars + 8u * uint32_t(stage);
-                if (id < 0) {
-                    mbar_arrive(bar);
-                } else if (a.inject && blockIdx.x == 0 && warp == 0 && sent == 1) {
-                    // test hook: this copy never comes
-                } else {
-                    mbar_arrive_expect_tx(bar, tile_bytes(D));
-                    bulk_load(ring + uint32_t(stage * tile_bytes(D)), p.cache + place * tile_bytes(D), tile_bytes(D), bar);
-                }
-            }
         };
         for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
 
-        for (int t = t0; t < last; ++t) {
-            const int stage = int(pos % kStages);
-            ok = __all_sync(0xffffffffu, wait_bounded(bars + 8u * uint32_t(stage), (pos / kStages) & 1u, abort_flag, a.status));
-            if (!ok) break;
-            ++pos;
-            if (next < last) fetch();   // into the tile's before this one, whose words the products have taken
-            const uint32_t base = ring + uint32_t(stage * tile_bytes(D));
-            const bool zero = (zeros >> stage) & 1u;
+        // One step; kRagged: not all rows see all of it.
+        auto take = [&](int t, auto ragged) {
+            constexpr bool kRagged = decltype(ragged)::value;
+            const uint32_t base = ring + uint32_t(stage * 2 * tile_bytes(D));
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            phase ^= stage == 0 ? 1u : 0u;
+            --flying;
+            if (next < last) fetch();   // into the step's before this one, whose words the products have taken
 
-            // ---- scores of tokens r8, r8 + 8 against rows 2 c, 2 c + 1
-            uint32_t kw[D / 16], ks[kGroups];   // ks: blocks of token r8, then of r8 + 8, two to a word
+            // ---- scores of tokens r8, r8 + 8 of each tile against rows 2 c, 2 c + 1
+            float y[2][NT][4];
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 w = ld_shared_v4(base + uint32_t(512 * i + 16 * lane));
-                kw[4 * i] = w.x; kw[4 * i + 1] = w.y; kw[4 * i + 2] = w.z; kw[4 * i + 3] = w.w;
-            }
-            {
-                const uint32_t from = base + uint32_t(key_scales(D) + r8 * (D / 8));
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t at = base + uint32_t(j * tile_bytes(D));
+                uint32_t kw[D / 16], ks[kGroups];   // ks: blocks of token r8, then of r8 + 8, two to a word
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const uint4 w = ld_shared_v4(at + uint32_t(512 * i + 16 * lane));
+                    kw[4 * i] = w.x; kw[4 * i + 1] = w.y; kw[4 * i + 2] = w.z; kw[4 * i + 3] = w.w;
+                }
+                const uint32_t from = at + uint32_t(key_scales(D) + r8 * (D / 8));
                 if (D == 128) {
                     const uint4 w = ld_shared_v4(from);
                     ks[0] = w.x; ks[1] = w.y; ks[kGroups / 2] = w.z; ks[kGroups - 1] = w.w;
                 } else {
                     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ks[0]), "=r"(ks[1]) : "r"(from) : "memory");
                 }
-                if (zero) {
+                // What the codes' 8 takes off: the scales, as bfloat16 of 2^-112 their value (float16's bits moved by
+                // three), times the blocks' sums.
+                {
+                    const uint32_t w0 = D == 128 && (c4 & 1) ? ks[kGroups / 2 - 1] : ks[0];
+                    const uint32_t w1 = D == 128 && (c4 & 1) ? ks[kGroups - 1] : ks[kGroups / 2];
+                    const uint32_t d0 = and_or(w0, 0x80008000u, (w0 >> 3) & 0x0FFF0FFFu), d1 = and_or(w1, 0x80008000u, (w1 >> 3) & 0x0FFF0FFFu);
+                    const uint32_t A[4] = {d0, d1, d0, d1};
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) ks[g] = 0;
+                    for (int nt = 0; nt < NT; ++nt) mma16816_bf16_0(y[j][nt], A, qs[nt][0], qs[nt][1]);
+                }
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    float acc[NT][4];
+#pragma unroll
+                    for (int i = 2 * g; i < 2 * g + 2; ++i) {
+                        const uint32_t w8 = kw[i] >> 8;
+                        const uint32_t A[4] = {kw[i] & low, w8 & low, kw[i] & high, w8 & high};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (i % 2 == 0) mma16816_0(acc[nt], A, qf[nt][i][0], qf[nt][i][1]);
+                            else mma16816(acc[nt], A, qf[nt][i][0], qf[nt][i][1]);
+                        }
+                    }
+                    const float2 lo = __half22float2(u2h(ks[g / 2])), hi = __half22float2(u2h(ks[kGroups / 2 + g / 2]));
+                    const float d0 = g & 1 ? lo.y : lo.x, d1 = g & 1 ? hi.y : hi.x;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[j][nt][k] = fmaf(k & 2 ? d1 : d0, acc[nt][k], y[j][nt][k]);
                 }
             }
-            float y[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[nt][k] = 0.f;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                float acc[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    acc[nt][0] = acc[nt][2] = off8[nt][g][0];
-                    acc[nt][1] = acc[nt][3] = off8[nt][g][1];
-                }
-#pragma unroll
-                for (int i = 2 * g; i < 2 * g + 2; ++i) {
-                    const uint32_t w8 = kw[i] >> 8;
-                    const uint32_t A[4] = {kw[i] & 0x000F000Fu, w8 & 0x000F000Fu, kw[i] & 0x00F000F0u, w8 & 0x00F000F0u};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt], A, qf[nt][i][0], qf[nt][i][1]);
-                }
-                const float2 lo = __half22float2(u2h(ks[g / 2])), hi = __half22float2(u2h(ks[kGroups / 2 + g / 2]));
-                const float d0 = g & 1 ? lo.y : lo.x, d1 = g & 1 ? hi.y : hi.x;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    y[nt][0] = fmaf(d0, acc[nt][0], y[nt][0]);
-                    y[nt][1] = fmaf(d0, acc[nt][1], y[nt][1]);
-                    y[nt][2] = fmaf(d1, acc[nt][2], y[nt][2]);
-                    y[nt][3] = fmaf(d1, acc[nt][3], y[nt][3]);
-                }
-            }
-            const int key = t * kTokens + r8;
-            const bool ragged = t * kTokens + kTokens > least;   // some row does not see all of it
             bool rises = false;
+            float top[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    y[nt][k] = __fmul_rn(y[nt][k], f[nt][k & 1]);
-                    if (ragged && key + (k & 2 ? 8 : 0) >= see[nt][k & 1]) y[nt][k] = -INFINITY;
-                    rises |= y[nt][k] > m[nt][k & 1] + kGrow;
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y[j][nt][k] = __fmul_rn(y[j][nt][k], f[nt][k & 1]);
+                        if (kRagged && t * kStep + kTokens * j + r8 + (k & 2 ? 8 : 0) >= see[nt][k & 1]) y[j][nt][k] = -INFINITY;
+                    }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    top[nt][k] = fmaxf(fmaxf(y[0][nt][k], y[0][nt][k + 2]), fmaxf(y[1][nt][k], y[1][nt][k + 2]));
+                    rises |= top[nt][k] - m[nt][k] > kSpan;   // exact where it matters, however large they are
                 }
+            }
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float top = fmaxf(y[nt][k], y[nt][k + 2]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const float now = fmaxf(m[nt][k], top);
-                        // (-inf) - (-inf) only where the sums are still zero
-                        const float by = now == -INFINITY ? 1.f : ex2(m[nt][k] - now);
+                        float now = fmaxf(top[nt][k], __shfl_xor_sync(0xffffffffu, top[nt][k], 4));
+                        now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
+                        now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+                        now = fmaxf(m[nt][k], now - kLift);
+                        const float by = ex2(m[nt][k] - now);
                         m[nt][k] = now;
                         l[nt][k] *= by;
 #pragma unroll
@@ -536,88 +580,97 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
                     }
             }
             // ---- weights, as the B operand: tokens 2 c, 2 c + 1 and those + 8 of row r8
-            uint32_t hi[NT][2], lo[NT][2];
+            uint32_t hi[2][NT][2], lo[2][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float ref = m[nt][k & 1] == -INFINITY ? 0.f : m[nt][k & 1];
-                    y[nt][k] = ex2(__fsub_rn(y[nt][k], ref));
-                    l[nt][k & 1] += y[nt][k];
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const __half2 v = __floats2half2_rn(y[nt][2 * k], y[nt][2 * k + 1]);
-                    const float2 back = __half22float2(v);
-                    const __half2 rest = __floats2half2_rn(y[nt][2 * k] - back.x, y[nt][2 * k + 1] - back.y);
-                    hi[nt][k] = transpose8x8(h2u(v));
-                    lo[nt][k] = transpose8x8(h2u(rest));
-                }
-            }
-
-            // ---- values
-            uint32_t vs[kGroups][2];   // scales of tokens 2 c, 2 c + 1 and those + 8
-#pragma unroll
-            for (int g = 0; g < kGroups; g += 2) {
-                const uint4 w = ld_shared_v4(base + uint32_t(value_scales(D) + c4 * (D / 4) + 8 * g));
-                vs[g][0] = w.x; vs[g][1] = w.y; vs[g + 1][0] = w.z; vs[g + 1][1] = w.w;
-            }
-            if (zero) {
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) vs[g][0] = vs[g][1] = 0;
-            }
-            uint32_t off[kGroups];   // ragged tiles: tokens whose scale is no number, as bits
-            bool any_off = false;
-            if (ragged) {
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    off[g] = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int token = 2 * c4 + (k & 1) + (k & 2 ? 8 : 0);
-                        const uint32_t bits = k & 1 ? vs[g][k >> 1] >> 16 : vs[g][k >> 1] & 0xFFFFu;
-                        const bool past = t * kTokens + token >= most;
-                        if (past || !finite16(bits)) vs[g][k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                        if (!past && !finite16(bits)) off[g] |= 1u << token;
-                    }
-                    off[g] |= __shfl_xor_sync(0xffffffffu, off[g], 1);
-                    off[g] |= __shfl_xor_sync(0xffffffffu, off[g], 2);
-                    any_off |= off[g] != 0;
-                }
-            }
-            const __half2 bias_lo = __float2half2_rn(1032.f), bias_hi = __float2half2_rn(72.f);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t w;
-                if (i % 4 == 0) {
-                    const uint4 v = ld_shared_v4(base + uint32_t(value_codes(D) + 512 * (i / 4) + 16 * lane));
-                    kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
-                }
-                w = kw[i % 4];
-                const uint32_t w8 = w >> 8;
-                const __half2 d0 = u2h(vs[i / 2][0]), d1 = u2h(vs[i / 2][1]);
-                const uint32_t A[4] = {h2u(__hmul2(__hsub2(u2h((w & 0x000F000Fu) | 0x64006400u), bias_lo), d0)),
-                                       h2u(__hmul2(__hsub2(u2h((w & 0x00F000F0u) | 0x54005400u), bias_hi), d0)),
-                                       h2u(__hmul2(__hsub2(u2h((w8 & 0x000F000Fu) | 0x64006400u), bias_lo), d1)),
-                                       h2u(__hmul2(__hsub2(u2h((w8 & 0x00F000F0u) | 0x54005400u), bias_hi), d1))};
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(o[i * NT + nt], A, lo[nt][0], lo[nt][1]);
-                    mma16816(o[i * NT + nt], A, hi[nt][0], hi[nt][1]);
-                }
-            }
-            if (ragged && any_off) {   // such a token's block is no number for the rows that see it, and only for them
+                    float* const x = y[j][nt];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int k = 0; k < 4; ++k) x[k] = ex2(__fsub_rn(x[k], m[nt][k & 1]));
+                    l[nt][0] += x[0] + x[2];
+                    l[nt][1] += x[1] + x[3];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int n = min(16, max(0, see[nt][k] - t * kTokens));
-                        const uint32_t sees = (1u << n) - 1u;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
-                            if (off[i / 2] & sees) o[i * NT + nt][k] = o[i * NT + nt][k + 2] = __int_as_float(0x7FC00000);
+                        const __half2 v = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+                        const float2 back = __half22float2(v);
+                        hi[j][nt][k] = transpose8x8(h2u(v));
+                        if (kFine) {
+                            const __half2 rest = __floats2half2_rn(x[2 * k] - back.x, x[2 * k + 1] - back.y);
+                            lo[j][nt][k] = transpose8x8(h2u(rest));
+                        }
                     }
+                }
+
+            // ---- values
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t at = base + uint32_t(j * tile_bytes(D));
+                uint32_t vs[kGroups][2];   // scales of tokens 2 c, 2 c + 1 and those + 8
+#pragma unroll
+                for (int g = 0; g < kGroups; g += 2) {
+                    const uint4 w = ld_shared_v4(at + uint32_t(value_scales(D) + c4 * (D / 4) + 8 * g));
+                    vs[g][0] = w.x; vs[g][1] = w.y; vs[g + 1][0] = w.z; vs[g + 1][1] = w.w;
+                }
+                const int first = t * kStep + kTokens * j;
+                uint32_t off[kGroups];   // ragged steps: tokens whose scale is no number, as bits
+                bool any_off = false;
+                if (kRagged) {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        off[g] = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int token = 2 * c4 + (k & 1) + (k & 2 ? 8 : 0);
+                            const uint32_t bits = k & 1 ? vs[g][k >> 1] >> 16 : vs[g][k >> 1] & 0xFFFFu;
+                            const bool past = first + token >= most;
+                            if (past || !finite16(bits)) vs[g][k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            if (!past && !finite16(bits)) off[g] |= 1u << token;
+                        }
+                        off[g] |= __shfl_xor_sync(0xffffffffu, off[g], 1);
+                        off[g] |= __shfl_xor_sync(0xffffffffu, off[g], 2);
+                        any_off |= off[g] != 0;
+                    }
+                }
+                const __half2 bias_lo = __float2half2_rn(1032.f), bias_hi = __float2half2_rn(72.f);
+#pragma unroll
+                for (int i4 = 0; i4 < D / 64; ++i4) {
+                    const uint4 v = ld_shared_v4(at + uint32_t(value_codes(D) + 512 * i4 + 16 * lane));
+                    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 4 * i4; i < 4 * i4 + 4; ++i) {
+                        const uint32_t w = word[i % 4], w8 = w >> 8;
+                        const __half2 d0 = u2h(vs[i / 2][0]), d1 = u2h(vs[i / 2][1]);
+                        const uint32_t A[4] = {h2u(__hmul2(__hsub2(u2h(and_or(w, low, 0x64006400u)), bias_lo), d0)),
+                                               h2u(__hmul2(__hsub2(u2h(and_or(w, high, 0x54005400u)), bias_hi), d0)),
+                                               h2u(__hmul2(__hsub2(u2h(and_or(w8, low, 0x64006400u)), bias_lo), d1)),
+                                               h2u(__hmul2(__hsub2(u2h(and_or(w8, high, 0x54005400u)), bias_hi), d1))};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (kFine) mma16816(o[i * NT + nt], A, lo[j][nt][0], lo[j][nt][1]);
+                            mma16816(o[i * NT + nt], A, hi[j][nt][0], hi[j][nt][1]);
+                        }
+                    }
+                }
+                if (kRagged && any_off) {   // such a token's block is no number for the rows that see it, and only for them
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int n = min(16, max(0, see[nt][k] - first));
+                            const uint32_t sees = (1u << n) - 1u;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                if (off[i / 2] & sees) o[i * NT + nt][k] = o[i * NT + nt][k + 2] = __int_as_float(0x7FC00000);
+                        }
+                }
             }
+        };
+        for (int t = t0; t < last; ++t) {
+            ok = __all_sync(0xffffffffu, wait_bounded(bars + 8u * uint32_t(stage), phase, abort_flag, a.status));
+            if (!ok) break;
+            if (t * kStep + kStep > least) take(t, std::true_type{});
+            else take(t, std::false_type{});
         }
         if (!ok) break;
 
@@ -666,9 +719,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_rows_kernel(
     }
     if (bad_page) atomicCAS(a.status, 0, MMQ_ERR_ARG);
     // After a wait that ran out: the copies still in flight.
-    for (; pos < sent; ++pos)
-        if (!(a.inject && blockIdx.x == 0 && warp == 0 && pos == 0))
-            wait_drain(bars + 8u * (pos % kStages), (pos / kStages) & 1u, a.status);
+    for (bool never = a.inject && blockIdx.x == 0 && warp == 0; flying > 0; --flying, never = false) {
+        if (!never) wait_drain(bars + 8u * uint32_t(stage), phase, a.status);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        phase ^= stage == 0 ? 1u : 0u;
+    }
     __syncthreads();
 
     // ---- units of several warps: joined, finished or left for the join over CTAs
@@ -761,12 +816,13 @@ size_t part_bytes(const mmq_kv4_attention_t& p, int nsm) {
 template <typename T, int D, int NT>
 cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
     using W = Rows<D, NT>;
+    const bool fine = std::is_same<T, __half>::value || a.p.out_type == MMQ_TYPE_F32;
+    auto* kernel = fine ? kv4_rows_kernel<T, D, NT, true> : kv4_rows_kernel<T, D, NT, std::is_same<T, __half>::value>;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(kv4_rows_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes)))
-        return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes))) return e;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned(nsm * W::kCtas)), dim3(kWarps * 32), W::kBytes, s, attr);
-    if ((e = cudaLaunchKernelEx(&cfg, kv4_rows_kernel<T, D, NT>, a))) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
@@ -801,6 +857,8 @@ cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, 
     while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
     a.group = p.heads / p.kv_heads;
     a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.low = 0x000F000Fu;
+    a.high = 0x00F000F0u;
     if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);
     return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, nsm, s) : launch<__nv_bfloat16, 128>(a, nsm, s);
 }
