@@ -35,7 +35,7 @@
 
 #include <type_traits>
 
-#include "kv4.cuh"
+#include "kv4_attention.cuh"
 #include "mmq_internal.h"
 #include "sm103_ptx.cuh"
 #include "tc_common.cuh"
@@ -46,29 +46,12 @@ using namespace mmq::ptx;
 using namespace mmq::kv4;
 using mmq::tc::ld_shared_v4;
 
+__device__ __align__(16) const uint8_t zero_tile[tile_bytes(128)] = {};   // of a page that does not exist
 constexpr int kWarps = 4;
 constexpr int kStep = 2 * kTokens;   // keys that a warp takes at a time
 constexpr float kLift = 7.f, kSpan = 14.f;   // a row's reference is 7 (in log2) under its largest score at first, 14 at most
 constexpr float kNone = -3.402823466e38f;   // the reference before any score: no score is under it but -Inf
 constexpr int kLeast = 2;   // tiles to a run, where there are too few for all warps
-
-struct Kv4Args {
-    mmq_kv4_attention_t p;
-    float* parts;       // [ctas][2] units' sums and (m, l): a CTA's first and last
-    struct Mark* marks; // [ctas]
-    int* status;
-    int inject;
-    int page_shift, group;
-    float scale_log2;
-    uint32_t low, high;   // masks of codes: 0x000F000F, 0x00F000F0
-};
-// What a CTA leaves of units that it shares with other CTAs: the start of a
-// unit's run of tiles is its name.
-struct Mark {
-    int64_t head, tail;      // -1: none
-    int head_ends;           // the head's unit has its last tile here
-    int b, h, tile;          // the tail's unit
-};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -102,60 +85,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
-__device__ __forceinline__ bool finite16(uint32_t bits) { return (bits & 0x7C00u) != 0x7C00u; }   // low half
-
-// --------------------------------------------------------------- sequences
-struct Sequence {
-    int n, len;       // new tokens, tokens
-    int64_t start;    // first row of q
-};
-// Checked: a sequence's rows lie in [0, tokens), its keys in its pages.
-__device__ __forceinline__ Sequence sequence(const Kv4Args& a, int b, bool tell) {
-    const mmq_kv4_attention_t& p = a.p;
-    Sequence s;
-    bool bad = false;
-    if (p.q_starts) {
-        const int64_t lo = p.q_starts[b], hi = p.q_starts[b + 1];
-        bad = lo < 0 || hi < lo || hi > p.tokens;
-        s.start = lo;
-        s.n = bad ? 0 : int(hi - lo);
-    } else {
-        s.n = int(p.tokens / p.batch);
-        s.start = int64_t(b) * s.n;
-    }
-    const int64_t room = p.table_width << a.page_shift, len = p.lens[b];
-    bad = bad || len > room;
-    s.len = int(max(int64_t(0), min(len, room)));
-    if (tell && bad) atomicCAS(a.status, 0, MMQ_ERR_ARG);
-    return s;
-}
-// Keys that new token j of a sequence sees.
-__device__ __forceinline__ int seen(const Sequence& s, int j) { return max(0, s.len - s.n + 1 + j); }
-
-template <int R>
-__device__ __forceinline__ int units(const Sequence& s, int group) {
-    return int((int64_t(s.n) * group + R - 1) / R);
-}
-// Tiles of one unit, at least one: a unit without keys still has zeros to write.
-template <int R>
-__device__ __forceinline__ int unit_tiles(const Sequence& s, int group, int u) {
-    const int last = int(min(int64_t(s.n) - 1, (int64_t(u) * R + R - 1) / group));
-    return max(1, (seen(s, last) + kStep - 1) / kStep);
-}
-template <int R>
-__device__ __forceinline__ int64_t sequence_tiles(const Sequence& s, int group) {
-    int64_t n = 0;
-    const int m = units<R>(s, group);
-    for (int u = 0; u < m; ++u) n += unit_tiles<R>(s, group, u);
-    return n;
-}
 
 // ------------------------------------------------------------------ output
 __device__ __forceinline__ void store_value(void* out, int type, int64_t at, float x) {
@@ -187,10 +118,6 @@ __device__ __forceinline__ void element(int k, int lane, int& dim, int& row) {
     row = 8 * nt + 2 * (lane & 3) + (k & 1);
 }
 
-struct Unit {
-    int b, h, tile;
-};
-__device__ __align__(16) const uint8_t zero_tile[tile_bytes(128)] = {};   // of a page that does not exist
 template <int D, int R>
 __device__ __forceinline__ void store_row(const Kv4Args& a, const Unit& u, const Sequence& s, int row, int dim, float x) {
     const int64_t r = int64_t(u.tile) * R + row;
@@ -280,34 +207,20 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     // ---- who does what: a scan over the sequences' tiles
     const int per = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
     const int b0 = min(p.batch, int(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += sequence_tiles<R>(sequence(a, b, blockIdx.x == 0), a.group) * p.kv_heads;
-    int64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-    }
-    if (lane == 31) sh.total[warp] = upto;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh.total[w];
-        total += sh.total[w];
-    }
-    const int64_t x1 = before + upto, x0 = x1 - mine;
-    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kWarps, total / kLeast));
-    auto first_of = [&](int64_t run) {   // runs < 2^16
-        return run >= runs ? total : total / runs * run + total % runs * run / runs;
+    auto steps_of = [&](const Sequence& s) {   // of one head
+        return int64_t(s.n) * a.group > a.few ? 0 : head_steps<R, kStep>(s, a.group);
     };
+    int64_t mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
+    const int64_t x1 = cta_scan<kWarps>(mine, sh.total, total), x0 = x1 - mine;
+    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kWarps, total / kLeast));
     for (int w = 0; w <= kWarps; ++w) {
-        const int64_t at = first_of(int64_t(blockIdx.x) * kWarps + w);
+        const int64_t at = run_start(int64_t(blockIdx.x) * kWarps + w, runs, total);
         if (threadIdx.x == 0) sh.first[w] = at;
         if (w < kWarps && x0 <= at && at < x1) {   // of one thread
             int64_t x = x0;
             for (int b = b0; b < b1; ++b) {
-                const int64_t n = sequence_tiles<R>(sequence(a, b, false), a.group) * p.kv_heads;
+                const int64_t n = steps_of(sequence(a, b, false)) * p.kv_heads;
                 if (at < x + n) {
                     sh.b[w] = b;
                     sh.offset[w] = at - x;
@@ -338,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
 
     while (at < end && ok) {
         const Sequence s = sequence(a, b, false);
-        const int64_t each = sequence_tiles<R>(s, a.group);
+        const int64_t each = steps_of(s);
         if (offset >= each * p.kv_heads) {   // also a sequence without rows
             ++b;
             offset = 0;
@@ -350,7 +263,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
         int64_t in_head = offset - u.h * each;
         u.tile = 0;
         int tiles;
-        while (in_head >= (tiles = unit_tiles<R>(s, a.group, u.tile))) {
+        while (in_head >= (tiles = unit_steps<R, kStep>(s, a.group, u.tile))) {
             in_head -= tiles;
             ++u.tile;
         }
@@ -836,11 +749,33 @@ cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+
+// A sequence of up to so many rows is the few-row kernel's.
+constexpr int kFew = 16;
+
+struct Forms {
+    bool few, many, two;   // which kernels a call may need; two: units of 256 rows
+};
+Forms forms(const mmq_kv4_attention_t& p) {
+    const int64_t group = p.heads / p.kv_heads, rows = p.tokens * group;   // of all sequences
+    const int64_t most = p.q_starts ? rows : rows / p.batch;               // of one, at most
+    return Forms{p.q_starts || most <= kFew, most > kFew, rows > int64_t(128) * p.batch};
+}
+size_t all_part_bytes(const mmq_kv4_attention_t& p, int nsm) {
+    const Forms f = forms(p);
+    const size_t few = f.few ? part_bytes(p, nsm) : 0, many = f.many ? up256(mmq::kv4_attention_tc_part_bytes(p.head_dim, nsm)) : 0;
+    return few > many ? few : many;
+}
+constexpr int kMostRuns = 3;   // marks per SM, of either kernel
+
+}  // namespace
+
 namespace mmq {
 
 size_t kv4_attention_workspace(const mmq_kv4_attention_t& p) {
     const int nsm = sm_count();
-    return nsm ? part_bytes(p, nsm) + up256(size_t(nsm) * 2 * sizeof(Mark)) : 0;
+    return nsm ? all_part_bytes(p, nsm) + up256(size_t(nsm) * kMostRuns * sizeof(Mark)) : 0;
 }
 
 cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, int* status, int inject_timeout,
@@ -850,7 +785,7 @@ cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, 
     Kv4Args a;
     a.p = p;
     a.parts = static_cast<float*>(workspace);
-    a.marks = reinterpret_cast<Mark*>(static_cast<char*>(workspace) + part_bytes(p, nsm));
+    a.marks = reinterpret_cast<Mark*>(static_cast<char*>(workspace) + all_part_bytes(p, nsm));
     a.status = status;
     a.inject = inject_timeout;
     a.page_shift = 0;
@@ -859,8 +794,16 @@ cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, 
     a.scale_log2 = p.scale * 1.4426950408889634f;
     a.low = 0x000F000Fu;
     a.high = 0x00F000F0u;
-    if (p.type == MMQ_TYPE_F16) return p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);
-    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, nsm, s) : launch<__nv_bfloat16, 128>(a, nsm, s);
+    a.few = kFew;
+    const Forms f = forms(p);
+    if (f.few) {
+        cudaError_t e;
+        if (p.type == MMQ_TYPE_F16) e = p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);
+        else e = p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, nsm, s) : launch<__nv_bfloat16, 128>(a, nsm, s);
+        if (e || !f.many) return e;
+    }
+    cudaLaunchAttribute attr[1];
+    return launch_kv4_attention_tc(a, f.two, nsm, mmq::launch_config(dim3(1), dim3(1), 0, s, attr));
 }
 
 }  // namespace mmq

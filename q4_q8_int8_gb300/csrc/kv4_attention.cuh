@@ -1,0 +1,129 @@
+// What the kernels of the 4-bit cache's attention share: their arguments, the
+// sequences as they are after their checks, and how the work is cut up.
+//
+// Rows are the (new token, head of the group) pairs of one kv head, row r of a
+// sequence being token r / group.  R rows make a unit, which needs every step
+// of kStep keys that its last row sees.  All units' steps, sequence by
+// sequence, head by head, unit by unit, are cut into runs of equal length.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mmq.h"
+#include "kv4.cuh"
+
+namespace mmq {
+namespace kv4 {
+
+struct Kv4Args {
+    mmq_kv4_attention_t p;
+    float* parts;       // [ctas][2] units' sums and (m, l): a CTA's first and last
+    struct Mark* marks; // [ctas]
+    int* status;
+    int inject;
+    int page_shift, group;
+    float scale_log2;
+    uint32_t low, high;   // masks of codes: 0x000F000F, 0x00F000F0
+    int few;              // sequences of up to so many rows are the few-row kernel's, others the tensor-core kernel's
+};
+// What a CTA leaves of units that it shares with other CTAs: the start of a
+// unit's run of tiles is its name.
+struct Mark {
+    int64_t head, tail;      // -1: none
+    int head_ends;           // the head's unit has its last tile here
+    int b, h, tile;          // the tail's unit
+};
+
+// The unit of the sequence's head.
+struct Unit {
+    int b, h, tile;
+};
+
+__device__ __forceinline__ bool finite16(uint32_t bits) { return (bits & 0x7C00u) != 0x7C00u; }   // low half
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// --------------------------------------------------------------- sequences
+struct Sequence {
+    int n, len;       // new tokens, tokens
+    int64_t start;    // first row of q
+};
+// Checked: a sequence's rows lie in [0, tokens), its keys in its pages.
+__device__ __forceinline__ Sequence sequence(const Kv4Args& a, int b, bool tell) {
+    const mmq_kv4_attention_t& p = a.p;
+    Sequence s;
+    bool bad = false;
+    if (p.q_starts) {
+        const int64_t lo = p.q_starts[b], hi = p.q_starts[b + 1];
+        bad = lo < 0 || hi < lo || hi > p.tokens;
+        s.start = lo;
+        s.n = bad ? 0 : int(hi - lo);
+    } else {
+        s.n = int(p.tokens / p.batch);
+        s.start = int64_t(b) * s.n;
+    }
+    const int64_t room = p.table_width << a.page_shift, len = p.lens[b];
+    bad = bad || len > room;
+    s.len = int(max(int64_t(0), min(len, room)));
+    if (tell && bad) atomicCAS(a.status, 0, MMQ_ERR_ARG);
+    return s;
+}
+// Keys that new token j of a sequence sees.
+__device__ __forceinline__ int seen(const Sequence& s, int j) { return max(0, s.len - s.n + 1 + j); }
+
+template <int R>
+__device__ __forceinline__ int units(const Sequence& s, int group) {
+    return int((int64_t(s.n) * group + R - 1) / R);
+}
+// Keys that the unit's last row sees, the most of all.
+template <int R>
+__device__ __forceinline__ int unit_keys(const Sequence& s, int group, int u) {
+    return seen(s, int(min(int64_t(s.n) - 1, (int64_t(u) * R + R - 1) / group)));
+}
+// Steps of kStep keys of one unit, at least one: a unit without keys still has zeros to write.
+template <int R, int kStep>
+__device__ __forceinline__ int unit_steps(const Sequence& s, int group, int u) {
+    return max(1, (unit_keys<R>(s, group, u) + kStep - 1) / kStep);
+}
+template <int R, int kStep>
+__device__ __forceinline__ int64_t head_steps(const Sequence& s, int group) {
+    int64_t n = 0;
+    const int m = units<R>(s, group);
+    for (int u = 0; u < m; ++u) n += unit_steps<R, kStep>(s, group, u);
+    return n;
+}
+// The first step of run `run` of `runs` that share `total` steps alike (total < 2^47, runs < 2^16).
+__device__ __forceinline__ int64_t run_start(int64_t run, int64_t runs, int64_t total) {
+    return run >= runs ? total : total / runs * run + total % runs * run / runs;
+}
+// An inclusive sum over the threads of a CTA of kWarps warps, and the whole sum; sums: kWarps words of shared memory.
+template <int kWarps>
+__device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t* sums, int64_t& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+    }
+    return upto;
+}
+
+}  // namespace kv4
+
+// The tensor-core kernel (kv4_attention_tc.cu) and its join; two: 256 rows to a unit, not 128.
+size_t kv4_attention_tc_part_bytes(int head_dim, int nsm);
+cudaError_t launch_kv4_attention_tc(const kv4::Kv4Args& a, bool two, int nsm, const cudaLaunchConfig_t& cfg);
+
+}  // namespace mmq

@@ -1,0 +1,834 @@
+// Attention over a 4-bit paged cache on the tensor cores: sequences with many
+// rows (a chunk of a prompt, or a speculative step of a wide group).
+//
+// A unit is 128 or 256 rows of one sequence's kv head.  Per 128 keys it takes
+// two products of 128 rows x 128 keys x D for each 128 rows, S = Q K^T and
+// O += P V with P = 2^(S f - m) as fp16, the rest f32; the keys and values, (code
+// - 8) * scale, are exact in fp16, so that P's rounding is the only one beside the
+// result's.  Q is fp16: a bfloat16 row with its largest element in [2^13,
+// 2^14), of which fp16 loses nothing down to 2^-28 of it, and 2^-e in f.
+//
+// One CTA per SM:
+//   warps 0-3, 4-7  softmax groups 0 and 1, thread = row (its tensor-memory
+//                   lane): read S, keep the row's maximum and sum, write P over
+//                   S, now and then scale O
+//   warps 8-11      expand raw tiles to operand tiles (128-byte swizzle): keys
+//                   [key][dimension], values transposed, [dimension][key]
+//   warp 12         fetches raw tiles: 8 bulk copies for 128 keys' half
+//   warps 13, 14    MMA issuers of groups 0 and 1
+// Runs of equal length of all units' key tiles are the CTAs' work, as in the
+// few-row kernel; the parts of units that lie in several runs are joined by a
+// second kernel.  kTwo: 256 rows to a unit, both groups share each key tile,
+// expanded once, and their issuers take turns (as in attention_tc.cu, where the
+// reason is measured).  Else 128 rows, and each group has a run of its own.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kv4_attention.cuh"
+#include "mmq_internal.h"
+#include "sm103_ptx.cuh"
+#include "tc_common.cuh"
+
+namespace {
+
+using namespace mmq::ptx;
+using namespace mmq::tc;
+using namespace mmq::kv4;
+
+constexpr int kKeys = 128, kRows = 128;
+constexpr int kThreads = 512;
+constexpr int kWarpExpand = 8, kWarpFetch = 12, kWarpMma = 13;   // and kWarpMma + 1
+// Registers: 128 per thread at launch (the launcher checks it): 256 x 192 + 128 x 72 + 128 x 56 = 512 x 128.
+constexpr uint32_t kRegsLaunch = 128, kRegsSoftmax = 192, kRegsExpand = 72, kRegsOther = 56;
+static_assert(256 * kRegsSoftmax + 128 * kRegsExpand + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;   // S_g at 128 g (P_g over its first 64 columns), O_g at 256 + 128 g
+constexpr float kGrow = 8.f, kLift = 7.f;    // P at most 2^15
+constexpr float kNone = -3.402823466e38f;    // the maximum before any score
+constexpr float kWide = 0x1p20f;
+__device__ __forceinline__ float reference(float m) { return fabsf(m) < kWide ? m - kLift : m; }
+
+__device__ __align__(16) const uint8_t zero_tile[tile_bytes(128)] = {};   // of a page that does not exist
+
+// Where a run starts: tile t of unit u of head h of sequence b, and its length.
+struct Start {
+    int64_t steps, first;   // first: the run's first step of all
+    int b, h, u, t;
+};
+
+// A run's units one after the other, each with the key tiles [t, t1) that the run has of it.
+template <int R>
+struct Walk {
+    const Kv4Args& a;
+    int64_t left, name;   // steps after this piece; the unit's first step of all
+    Sequence s;
+    int b, h, u, t, t1, steps;
+    bool starts;          // the unit's first tile is this piece's
+
+    __device__ __forceinline__ Walk(const Kv4Args& args, const Start& from) : a(args) {
+        left = from.steps;
+        b = from.b;
+        h = from.h;
+        u = from.u;
+        t = t1 = from.t;
+        name = from.first - from.t;
+        if (left > 0) {
+            s = sequence(a, b, false);
+            begin(from.t);
+        }
+    }
+    __device__ __forceinline__ bool valid() const { return t < t1; }
+    __device__ __forceinline__ bool ends() const { return t1 == steps; }
+    __device__ __forceinline__ int most() const { return unit_keys<R>(s, a.group, u); }     // keys that its last row sees
+    __device__ __forceinline__ int least() const { return seen(s, u * R / a.group); }       // and its first
+    __device__ __forceinline__ void begin(int from) {
+        steps = unit_steps<R, kKeys>(s, a.group, u);
+        starts = from == 0;
+        t = from;
+        t1 = int(min(int64_t(steps), from + left));
+        left -= t1 - t;
+    }
+    __device__ __forceinline__ void next() {   // the next piece
+        t = t1;
+        if (left == 0) return;
+        name += steps;
+        if (++u == units<R>(s, a.group)) {
+            u = 0;
+            if (++h == a.p.kv_heads) {
+                h = 0;
+                do s = sequence(a, ++b, false);
+                while (int64_t(s.n) * a.group <= a.few);
+            }
+        }
+        begin(0);
+    }
+    __device__ __forceinline__ void step() {   // the next tile
+        if (++t == t1) next();
+    }
+};
+
+template <int D, bool kTwo>
+struct Layout {
+    static constexpr int kStreams = kTwo ? 1 : 2;
+    static constexpr int kTile = kKeys * D * 2;              // of keys, values or queries as fp16
+    static constexpr int kSlots = 512 / D;
+    static constexpr int kBufs = kSlots / 2 / kStreams;      // per stream, of keys and of values
+    static constexpr int kRaw = 8 * 9 * D;                   // 128 keys or values in 4 bits
+    static constexpr int kRawSlots = 384 / D;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffSlots = 2 * kTile;
+    static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
+    static constexpr int kOffSums = kOffRaw + kRawSlots * kRaw;
+    static constexpr int kOffStart = kOffSums + 16 * 8;
+    static constexpr int kOffBar = kOffStart + 2 * int(sizeof(Start));
+    // barriers: raw_full, raw_empty; full, empty per slot; q_full, s_full, p_full, o_full, turn per group; drain
+    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 11) * 8;
+    static constexpr int kBytes = kOffMisc + 32 + 1024;
+    static constexpr int kR = kTwo ? 2 * kRows : kRows;      // rows of a unit
+};
+static_assert(Layout<128, true>::kBytes <= 232448 && Layout<128, false>::kBytes <= 232448, "shared memory budget");
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+// Two codes in the lower nibbles, or the upper ones, of v's bytes 0 and 2, less 8, times the scales.
+__device__ __forceinline__ uint32_t expand_low(uint32_t v, uint32_t scales) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(d) : "r"(v));
+    return h2u(__hmul2(__hsub2(u2h(d), __float2half2_rn(1032.f)), u2h(scales)));
+}
+__device__ __forceinline__ uint32_t expand_high(uint32_t v, uint32_t scales) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(d) : "r"(v));
+    return h2u(__hmul2(__hsub2(u2h(d), __float2half2_rn(72.f)), u2h(scales)));
+}
+template <int N>
+__device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t* w) {
+    if (N == 4) {
+        const uint4 v = ld_shared_v4(addr);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    }
+}
+
+template <typename T, int D, bool kTwo>
+__global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
+    using L = Layout<D, kTwo>;
+    constexpr int kSlots = L::kSlots, kRawSlots = L::kRawSlots, kStreams = L::kStreams, kBufs = L::kBufs, kR = L::kR;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::kOffBar;
+    auto raw_full = [&](int s) { return bar0 + 8u * uint32_t(s); };
+    auto raw_empty = [&](int s) { return bar0 + 8u * uint32_t(kRawSlots + s); };
+    auto full = [&](int s) { return bar0 + 8u * uint32_t(2 * kRawSlots + s); };
+    auto empty = [&](int s) { return bar0 + 8u * uint32_t(2 * kRawSlots + kSlots + s); };
+    const uint32_t bar1 = bar0 + 8u * uint32_t(2 * kRawSlots + 2 * kSlots);
+    auto q_full = [&](int g) { return bar1 + 8u * uint32_t(g); };
+    auto s_full = [&](int g) { return bar1 + 8u * uint32_t(2 + g); };
+    auto o_full = [&](int g) { return bar1 + 8u * uint32_t(4 + g); };
+    auto p_full = [&](int g) { return bar1 + 8u * uint32_t(6 + g); };
+    auto turn = [&](int g) { return bar1 + 8u * uint32_t(8 + g); };
+    const uint32_t drain = bar1 + 8u * 10u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+    const AbortFlag abort_flag{sbase + L::kOffMisc + 4};
+    const AbortFlag no_number{sbase + L::kOffMisc + 8};   // a value scale that is none was met where not all rows see it
+    Start* const from = reinterpret_cast<Start*>(smem + L::kOffStart);   // of each stream's run
+    int64_t* const sums = reinterpret_cast<int64_t*>(smem + L::kOffSums);
+    const mmq_kv4_attention_t& p = a.p;
+    int* const status = a.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRawSlots; ++s) {
+            mbar_init(raw_full(s), 1);
+            mbar_init(raw_empty(s), 4);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(full(s), 4);
+            mbar_init(empty(s), kTwo ? 2 : 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(q_full(g), 4);
+            mbar_init(s_full(g), 1);
+            mbar_init(p_full(g), 4);
+            mbar_init(o_full(g), 1);
+            mbar_init(turn(g), 1);
+        }
+        mbar_init(drain, 2);
+        abort_flag.set(0u);
+        no_number.set(0u);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // ---- who does what
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int b0 = min(p.batch, int(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+    auto steps_of = [&](const Sequence& s) {   // of one head
+        return int64_t(s.n) * a.group <= a.few ? 0 : head_steps<kR, kKeys>(s, a.group);
+    };
+    int64_t mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
+    const int64_t x1 = cta_scan<kThreads / 32>(mine, sums, total), x0 = x1 - mine;
+    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kStreams, total));
+    if (threadIdx.x < kStreams) a.marks[blockIdx.x + threadIdx.x * gridDim.x] = Mark{-1, -1, 0, 0, 0, 0};
+
+#pragma unroll
+    for (int st = 0; st < kStreams; ++st) {
+        const int64_t run = blockIdx.x + int64_t(st) * gridDim.x;
+        const int64_t lo = run_start(run, runs, total), hi = run_start(run + 1, runs, total);
+        if (threadIdx.x == 0) {
+            from[st].steps = hi - lo;
+            from[st].first = lo;
+        }
+        if (lo < hi && x0 <= lo && lo < x1) {   // of one thread
+            int64_t x = x0;
+            for (int b = b0; b < b1; ++b) {
+                const Sequence s = sequence(a, b, false);
+                const int64_t each = steps_of(s);
+                if (lo < x + each * p.kv_heads) {
+                    int64_t in_head = (lo - x) % each;
+                    int u = 0, steps;
+                    while (in_head >= (steps = unit_steps<kR, kKeys>(s, a.group, u))) {
+                        in_head -= steps;
+                        ++u;
+                    }
+                    from[st].b = b;
+                    from[st].h = int((lo - x) / each);
+                    from[st].u = u;
+                    from[st].t = int(in_head);
+                    break;
+                }
+                x += each * p.kv_heads;
+            }
+        }
+    }
+    __syncthreads();
+    auto slot_of = [&](int st, int kind, uint32_t no) { return (st * 2 + kind) * kBufs + int(no % kBufs); };
+    auto phase_of = [&](uint32_t no) { return (no / kBufs) & 1u; };
+
+    // Tiles in the order K, V (kTwo) or K of both streams, V of both; job(stream, kind, its place).
+    auto jobs = [&](auto&& job) {
+        Walk<kR> one(a, from[0]), two(a, from[kStreams - 1]);
+        while (one.valid() || (!kTwo && two.valid())) {
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {
+                if (one.valid() && !job(0, kind, one)) return;
+                if (!kTwo && two.valid() && !job(1, kind, two)) return;
+            }
+            if (one.valid()) one.step();
+            if (!kTwo && two.valid()) two.step();
+        }
+    };
+    if (warp >= kWarpExpand && warp < kWarpFetch) {
+        // ------------------------------------------------------------ expand
+        setmaxnreg_dec<kRegsExpand>();
+        Ring<kRawSlots> raw;
+        uint32_t tile_no[2] = {0, 0};   // tiles of each stream so far
+        // Thread: tile of 16 tokens, a row of eight in it (tokens r, r + 8 of keys, dimensions r, r + 8 of 16
+        // of values), and the blocks of 16 dimensions of every second (or the one) 64.
+        constexpr int kJ = D / 32;
+        const int id = threadIdx.x - kWarpExpand * 32;
+        const int tile = id >> 4, r = id & 7, part = (id >> 3) & 1;
+        const uint32_t words = uint32_t(tile * 9 * D + r * 64) + (D == 128 ? part * 512u : part * 8u);
+        jobs([&](int st, int kind, const Walk<kR>& q) {
+            const uint32_t no = tile_no[st];
+            const int slot = slot_of(st, kind, no);
+            if (kind == 1) ++tile_no[st];
+            if (!__all_sync(0xffffffffu, wait_bounded(raw_full(raw.slot), raw.phase, abort_flag, status) &&
+                                             wait_bounded(empty(slot), phase_of(no) ^ 1u, abort_flag, status)))
+                return false;
+            const uint32_t raw_at = sbase + uint32_t(L::kOffRaw + raw.slot * L::kRaw);
+            const uint32_t to = sbase + uint32_t(L::kOffSlots + slot * L::kTile);
+            uint32_t w[4][kJ];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ld_shared_words<kJ>(raw_at + words + 16u * c, w[c]);
+            if (kind == 0) {
+                uint32_t ks[2][kJ / 2];   // tokens r, r + 8: this part's blocks of 32, two to a word
+                const uint32_t at = raw_at + uint32_t(tile * 9 * D + key_scales(D) + r * (D / 8));
+                if (D == 128) {
+                    ks[0][0] = ld_shared_u32(at + 4u * part);
+                    ks[1][0] = ld_shared_u32(at + 8u + 4u * part);
+                } else {
+                    ks[0][0] = ld_shared_u32(at);
+                    ks[1][0] = ld_shared_u32(at + 4u);
+                }
+                const uint32_t row = uint32_t(tile * 16 + r) * 128u;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int i = part * kJ + j;
+                    // block i / 2 of 32: 2 part, 2 part + 1 of D = 128, part of D = 64
+                    const uint32_t sel = D == 128 ? (j >> 1 ? 0x3232u : 0x1010u) : (part ? 0x3232u : 0x1010u);
+                    const uint32_t d0 = prmt(ks[0][0], 0u, sel), d1 = prmt(ks[1][0], 0u, sel);
+                    const uint32_t dst = to + uint32_t(i >> 2) * (kKeys * 128) + row;
+                    const uint32_t c0 = uint32_t((2 * (i & 3)) ^ r) << 4, c1 = uint32_t((2 * (i & 3) + 1) ^ r) << 4;
+                    st_shared_v4(dst + c0, expand_low(w[0][j], d0), expand_low(w[1][j], d0), expand_low(w[2][j], d0), expand_low(w[3][j], d0));
+                    st_shared_v4(dst + c1, expand_high(w[0][j], d0), expand_high(w[1][j], d0), expand_high(w[2][j], d0), expand_high(w[3][j], d0));
+                    st_shared_v4(dst + 1024u + c0, expand_low(w[0][j] >> 8, d1), expand_low(w[1][j] >> 8, d1), expand_low(w[2][j] >> 8, d1), expand_low(w[3][j] >> 8, d1));
+                    st_shared_v4(dst + 1024u + c1, expand_high(w[0][j] >> 8, d1), expand_high(w[1][j] >> 8, d1), expand_high(w[2][j] >> 8, d1), expand_high(w[3][j] >> 8, d1));
+                }
+            } else {
+                constexpr int kG = D == 128 ? 2 : 1;    // blocks of 32 dimensions here
+                uint32_t vs[4][kG][2];                  // tokens 2 c, 2 c + 1 and those + 8
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    ld_shared_words<2 * kG>(raw_at + uint32_t(tile * 9 * D + value_scales(D) - value_codes(D) + c * (D / 4) + part * kG * 8), vs[c][0]);
+                if (q.t * kKeys + kKeys > q.least()) {
+                    // tokens that some rows of the unit do not see: what is no number must not reach those,
+                    // and what lies past the last must reach none
+                    const int left = q.most() - (q.t * kKeys + tile * 16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int token = 2 * c + (k & 1) + (k & 2 ? 8 : 0);
+#pragma unroll
+                            for (int g = 0; g < kG; ++g) {
+                                const uint32_t v = vs[c][g][k >> 1], bits = k & 1 ? v >> 16 : v & 0xFFFFu;
+                                if (token >= left || !finite16(bits)) vs[c][g][k >> 1] = v & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u);
+                                if (token < left && !finite16(bits)) no_number.set(1u);
+                            }
+                        }
+                }
+                const uint32_t col = uint32_t(tile >> 2) * (D * 128);
+                const uint32_t c0 = uint32_t((2 * (tile & 3)) ^ r) << 4, c1 = uint32_t((2 * (tile & 3) + 1) ^ r) << 4;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int i = part * kJ + j, g = j >> 1;
+                    const uint32_t dst = to + col + uint32_t(16 * i + r) * 128u;
+                    st_shared_v4(dst + c0, expand_low(w[0][j], vs[0][g][0]), expand_low(w[1][j], vs[1][g][0]), expand_low(w[2][j], vs[2][g][0]), expand_low(w[3][j], vs[3][g][0]));
+                    st_shared_v4(dst + 1024u + c0, expand_high(w[0][j], vs[0][g][0]), expand_high(w[1][j], vs[1][g][0]), expand_high(w[2][j], vs[2][g][0]), expand_high(w[3][j], vs[3][g][0]));
+                    st_shared_v4(dst + c1, expand_low(w[0][j] >> 8, vs[0][g][1]), expand_low(w[1][j] >> 8, vs[1][g][1]), expand_low(w[2][j] >> 8, vs[2][g][1]), expand_low(w[3][j] >> 8, vs[3][g][1]));
+                    st_shared_v4(dst + 1024u + c1, expand_high(w[0][j] >> 8, vs[0][g][1]), expand_high(w[1][j] >> 8, vs[1][g][1]), expand_high(w[2][j] >> 8, vs[2][g][1]), expand_high(w[3][j] >> 8, vs[3][g][1]));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(full(slot));
+                mbar_arrive(raw_empty(raw.slot));   // the stores above have taken what was loaded
+            }
+            raw.next();
+            return true;
+        });
+    } else if (warp >= kWarpFetch) {
+        setmaxnreg_dec<kRegsOther>();
+        if (warp == kWarpFetch) {
+            // ------------------------------------------------------ raw tiles
+            Ring<kRawSlots> raw;
+            uint32_t issued = 0, parity = 0;   // slots with a copy, the parity of its arrival
+            bool withhold = a.inject && blockIdx.x == 0;
+            const uint8_t* src[kStreams];
+            const int tile_shift = a.page_shift - 4;
+            jobs([&](int st, int kind, const Walk<kR>& q) {
+                if (kind == 0) {
+                    src[st] = zero_tile;
+                    const int tile = 8 * q.t + lane;
+                    if (lane < 8 && tile * kTokens < q.most()) {
+                        const int32_t id = p.page_table[int64_t(q.b) * p.table_width + (tile >> tile_shift)];
+                        if (id < 0 || id >= p.n_pages) atomicCAS(status, 0, MMQ_ERR_ARG);
+                        else
+                            src[st] = p.cache + (((int64_t(id) * p.kv_heads + q.h) << tile_shift) +
+                                                 (tile & ((1 << tile_shift) - 1))) * tile_bytes(D);
+                    }
+                }
+                if (!__all_sync(0xffffffffu, wait_bounded(raw_empty(raw.slot), raw.phase ^ 1u, abort_flag, status))) return false;
+                if (!withhold) {
+                    if (lane == 0) mbar_arrive_expect_tx(raw_full(raw.slot), uint32_t(L::kRaw));
+                    __syncwarp();
+                    if (lane < 8)
+                        bulk_load(sbase + uint32_t(L::kOffRaw + raw.slot * L::kRaw + lane * 9 * D),
+                                  src[st] + (kind ? value_codes(D) : 0), 9 * D, raw_full(raw.slot));
+                    issued |= 1u << raw.slot;
+                    parity = (parity & ~(1u << raw.slot)) | (raw.phase << raw.slot);
+                }
+                withhold = false;
+                raw.next();
+                return true;
+            });
+            // copies still in flight, also after a wait that ran out
+            if (lane == 0)
+                for (int s = 0; s < kRawSlots; ++s)
+                    if ((issued >> s) & 1u) wait_drain(raw_full(s), (parity >> s) & 1u, status);
+        } else if (warp <= kWarpMma + 1) {
+            // ---------------------------------------------------- MMA issuers
+            if (lane == 0) {
+                const int g = warp - kWarpMma, st = kTwo ? 0 : g;
+                constexpr uint32_t kIdQK = idesc_f16_f32(kRows, kKeys), kIdPV = idesc_f16_f32(kRows, D);
+                constexpr uint64_t kTileDesc = uint64_t(L::kTile >> 4);
+                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
+                const uint64_t slots = smem_desc_sw128(sbase + uint32_t(L::kOffSlots));
+                const uint32_t ts = tmem + kColS + 128u * uint32_t(g), to = tmem + kColO + 128u * uint32_t(g);
+                auto arrived = [&](int kind, uint32_t no) {
+                    return wait_bounded(full(slot_of(st, kind, no)), phase_of(no), abort_flag, status);
+                };
+                // A tile's descriptor, opaque so that the loop does not keep one for every product: this thread has few
+                // registers, and of those that went to local memory (128 rows, D = 128) the upper words, which hold the
+                // swizzle and strides, did not reach the products.
+                auto described = [](uint64_t d) {
+                    asm volatile("" : "+l"(d));
+                    return d;
+                };
+                // S = Q K^T with tile `no` of keys, which has arrived
+                auto scores = [&](uint32_t no, bool pass) {
+                    const int slot = slot_of(st, 0, no);
+                    const uint64_t dk = described(slots + uint64_t(slot) * kTileDesc), dq_now = described(dq);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = uint64_t(kk >> 2) * uint64_t(kKeys * 128 >> 4) + uint64_t((kk & 3) * 2);
+                        if (kTwo && kk == D / 16 - 2 && pass) mbar_arrive(turn(g ^ 1));   // the other thread needs a moment
+                        mma_f16(ts, dq_now + off, dk + off, kIdQK, uint32_t(kk > 0));
+                    }
+                    mma_commit(s_full(g));
+                    mma_commit(empty(slot));
+                };
+                uint32_t no = 0;   // tiles so far
+                uint32_t q_phase = 0, p_phase = 0, t_phase = g == 0 ? 1u : 0u;   // group 0 has the first turn
+                bool ok = true;
+                for (Walk<kR> q(a, from[st]); q.valid() && ok; q.next()) {
+                    const int tiles = q.t1 - q.t;
+                    ok = wait_bounded(q_full(g), q_phase, abort_flag, status) && arrived(0, no);
+                    if (!ok) break;
+                    q_phase ^= 1u;
+                    tc_fence_after();
+                    scores(no, false);
+                    for (int s = 0; s < tiles; ++s, ++no) {
+                        const bool more = s + 1 < tiles;
+                        ok = arrived(1, no) && (!more || arrived(0, no + 1)) &&
+                             wait_bounded(p_full(g), p_phase, abort_flag, status) &&
+                             (!kTwo || wait_bounded(turn(g), t_phase, abort_flag, status));
+                        if (!ok) break;
+                        tc_fence_after();
+                        t_phase ^= 1u;
+                        p_phase ^= 1u;
+                        const int slot = slot_of(st, 1, no);
+                        const uint64_t dv = described(slots + uint64_t(slot) * kTileDesc);
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_f16_ta(to, ts + 8u * uint32_t(kk),
+                                       dv + uint64_t(kk >> 2) * uint64_t(D * 128 >> 4) + uint64_t((kk & 3) * 2), kIdPV,
+                                       uint32_t(s > 0 || kk > 0));
+                        if (more) {
+                            scores(no + 1, true);
+                        } else {
+                            if (kTwo) mbar_arrive(turn(g ^ 1));
+                            mma_commit(o_full(g));
+                        }
+                        mma_commit(empty(slot));
+                    }
+                }
+                mma_commit(drain);   // everything issued, also after a wait that ran out
+                wait_drain(drain, 0u, status);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        setmaxnreg_inc<kRegsSoftmax>();
+        const int g = warp >> 2, st = kTwo ? 0 : g;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kColS + 128u * uint32_t(g), to = tmem + lanes + kColO + 128u * uint32_t(g);
+        uint32_t s_phase = 0, o_phase = 0;
+        bool ok = true;
+        for (Walk<kR> q(a, from[st]); q.valid() && ok; q.next()) {
+            const int r = q.u * kR + (kTwo ? g * kRows : 0) + row;
+            const int j = r / a.group;
+            const bool valid = j < q.s.n;
+            const int head = q.h * a.group + r - j * a.group;
+            const int see = valid ? seen(q.s, j) : 0x7FFFFFFF;
+            // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.
+            float scale = a.scale_log2;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (valid ? (q.s.start + j) * p.q_stride + int64_t(head) * D : 0));
+                const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kTile + row * 128);
+                uint4 v[D / 8];
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                if (std::is_same<T, __nv_bfloat16>::value) {
+                    uint32_t top = 0;   // magnitudes order as integers; NaN's as the largest
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+                    }
+                    // top in [2^e, 2^(e+1)) -> [2^13, 2^14); a row of zeros or tiny values as if it had 2^-100
+                    const int e = max(-100, int(top >> 23) - 127);
+                    const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+                    scale = fminf(scale * __uint_as_float(uint32_t(127 + e - 13) << 23), 3.4e38f);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint32_t* const w[4] = {&v[c].x, &v[c].y, &v[c].z, &v[c].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *w[k] = pack16(__uint_as_float(*w[k] << 16) * up, __uint_as_float(*w[k] & 0xFFFF0000u) * up);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    st_shared_v4(dst + uint32_t((c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)), v[c].x, v[c].y, v[c].z, v[c].w);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full(g));
+            }
+            float m = kNone, l = 0.f;
+            bool wide = false;
+            const int tiles = q.t1 - q.t;
+            int n = 0;
+            auto scale_o = [&](float f) {   // at rest: the product before this S has completed
+                l *= f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st_32x32b_x32(to + 32u * uint32_t(c), o);
+                }
+            };
+            for (; n < tiles; ++n) {
+                ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
+                if (!ok) break;
+                s_phase ^= 1u;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), s[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+                const int left = see - (q.t + n) * kKeys;
+                if (left < kKeys) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= left) s[c][k] = 0xFF800000u;
+                }
+                float x0 = __uint_as_float(s[0][0]), x1 = __uint_as_float(s[1][0]), x2 = __uint_as_float(s[2][0]),
+                      x3 = __uint_as_float(s[3][0]);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    x0 = max3(x0, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
+                    x1 = max3(x1, __uint_as_float(s[1][k]), __uint_as_float(s[1][k + 1]));
+                    x2 = max3(x2, __uint_as_float(s[2][k]), __uint_as_float(s[2][k + 1]));
+                    x3 = max3(x3, __uint_as_float(s[3][k]), __uint_as_float(s[3][k + 1]));
+                }
+                const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * scale;
+                const bool rises = top > m + kGrow;
+                if (__any_sync(0xffffffffu, rises)) {
+                    const float was = m;
+                    wide = __any_sync(0xffffffffu, rises && !(fabsf(top) < kWide));
+                    if (wide) break;
+                    m = fmaxf(m, top);
+                    if (n > 0) scale_o(ex2(was - m));
+                }
+                const float base = m - kLift;
+                const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const uint32_t* sc = &s[2 * half + (k >> 4)][2 * (k & 15)];
+                        const uint64_t e = ffma2(pack2u(sc[0], sc[1]), scale2, base2);
+                        const float u = ex2(lo_f(e)), v = ex2(hi_f(e));
+                        sum[k & 1] = fadd2(sum[k & 1], pack2(u, v));
+                        pk[k] = pack16(u, v);
+                    }
+                    tmem_st_32x32b_x32(ts + 32u * uint32_t(half), pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(g));
+                sum[0] = fadd2(sum[0], sum[1]);
+                l += lo_f(sum[0]) + hi_f(sum[0]);
+            }
+            // S scale - m in one step, as above, is past zero by what m lost in its rounding, half a unit in its
+            // last place: from 2^20 on too much for P's range.  From the first tile where a row of the warp gets
+            // there the products are rounded first, as m was, and m is neither lifted nor let behind.  No usual
+            // call comes here, so short loops over S where it lies.
+            for (bool here = true; ok && wide && n < tiles; ++n, here = false) {
+                if (!here) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
+                    if (!ok) break;
+                    s_phase ^= 1u;
+                    tc_fence_after();
+                }
+                const int left = see - (q.t + n) * kKeys;
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
+                    tmem_wait_ld(x);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * c + k < left) top = fmaxf(top, __uint_as_float(x[k]));
+                }
+                const float was = m;
+                m = fmaxf(m, __fmul_rn(top, scale));
+                const float base = reference(m);
+                if (n > 0) scale_o(ex2(reference(was) - base));
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32], pk[16];
+                    tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
+                    tmem_wait_ld(x);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float y = __fmul_rn(__uint_as_float(x[k]), scale);
+                        x[k] = 32 * c + k < left ? __float_as_uint(ex2(__fsub_rn(y, base))) : 0u;
+                        sum += __uint_as_float(x[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) pk[k] = pack16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                    tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);   // over what has been read
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(g));
+                l += sum;
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
+            if (!ok) break;
+            o_phase ^= 1u;
+            tc_fence_after();
+            // Where a value scale is no number and not all rows see its token: the rows that do, block by block.
+            uint32_t none = 0;
+            if (no_number.raised() && valid) {
+                const int tile_shift = a.page_shift - 4;
+                for (int key = max(q.t, q.least() / kKeys) * kKeys; key < min(see, q.t1 * kKeys); ++key) {
+                    const int32_t id = p.page_table[int64_t(q.b) * p.table_width + (key >> a.page_shift)];
+                    if (id < 0 || id >= p.n_pages) continue;
+                    const uint8_t* at = p.cache + (((int64_t(id) * p.kv_heads + q.h) << tile_shift) +
+                                                   ((key >> 4) & ((1 << tile_shift) - 1))) * tile_bytes(D);
+                    for (int b = 0; b < D / 32; ++b)
+                        if (!finite16(*reinterpret_cast<const uint16_t*>(at + value_scale<D>(key & 15, b)))) none |= 1u << b;
+                }
+            }
+            const bool done = q.starts && q.ends();
+            const float factor = done ? l == 0.f ? 0.f : 1.f / l : 1.f;
+            const int64_t run = blockIdx.x + int64_t(st) * gridDim.x;
+            const int64_t at = (run * 2 + (q.starts ? 1 : 0)) * kR + (r - q.u * kR);   // a part's row
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+                tmem_wait_ld(o);
+                if (!valid) continue;
+                const float by = (none >> c) & 1u ? __int_as_float(0x7FC00000) : factor;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                const int64_t out = ((q.s.start + j) * p.heads + head) * D + 32 * c;
+                if (!done || p.out_type == MMQ_TYPE_F32) {
+                    uint4* dst = reinterpret_cast<uint4*>(done ? static_cast<float*>(p.out) + out : a.parts + at * D + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float u = __uint_as_float(o[2 * k]), v = __uint_as_float(o[2 * k + 1]);
+                        if (std::is_same<T, __half>::value) {
+                            pk[k] = pack16(u, v);
+                        } else {
+                            const __nv_bfloat162 w = __floats2bfloat162_rn(u, v);
+                            pk[k] = *reinterpret_cast<const uint32_t*>(&w);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                }
+            }
+            tc_fence_before();
+            if (!done && row == 0 && (g == 0 || !kTwo)) {
+                Mark& mark = a.marks[run];
+                if (q.starts) {
+                    mark.tail = q.name;
+                    mark.b = q.b;
+                    mark.h = q.h;
+                    mark.tile = q.u;
+                } else {
+                    mark.head = q.name;
+                    mark.head_ends = q.ends();
+                }
+            }
+            if (!done && valid)
+                reinterpret_cast<float2*>(a.parts + int64_t(gridDim.x) * kStreams * 2 * kR * D)[at] = make_float2(reference(m), l);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Units of several runs: blocks (i, *) join the one that starts in run i and does not end there, a warp per row.
+template <typename T, int D, bool kTwo>
+__global__ void __launch_bounds__(256) kv4_tc_join_kernel(const Kv4Args a) {
+    constexpr int kR = Layout<D, kTwo>::kR, kVec = D / 32;
+    griddep_launch_dependents();
+    griddep_wait();
+    const Mark mark = a.marks[blockIdx.x];
+    if (mark.tail < 0) return;
+    const int lane = threadIdx.x & 31, row = int(blockIdx.y) * 8 + (threadIdx.x >> 5);
+    const Sequence s = sequence(a, mark.b, false);
+    const int r = mark.tile * kR + row, j = r / a.group;
+    if (j >= s.n) return;
+    const float2* const mls = reinterpret_cast<const float2*>(a.parts + int64_t(gridDim.x) * 2 * kR * D);
+    float acc[kVec] = {}, m = kNone, l = 0.f;
+    auto add = [&](int64_t part) {
+        const float2 ml = mls[part * kR + row];
+        float v[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; k += 2) {
+            const float2 u = *reinterpret_cast<const float2*>(a.parts + (part * kR + row) * D + kVec * lane + k);
+            v[k] = u.x;
+            v[k + 1] = u.y;
+        }
+        if (ml.y == 0.f) return;   // no key
+        const float top = fmaxf(m, ml.x), mine = ex2(m - top), its = ex2(ml.x - top);
+        m = top;
+        l = l * mine + ml.y * its;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * mine + v[k] * its;
+    };
+    add(int64_t(blockIdx.x) * 2 + 1);
+    for (unsigned i = blockIdx.x + 1; i < gridDim.x; ++i) {
+        const int64_t name = a.marks[i].head;
+        if (name < 0) continue;   // no tile at all
+        if (name != mark.tail) break;
+        add(int64_t(i) * 2);
+        if (a.marks[i].head_ends) break;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = ((s.start + j) * a.p.heads + mark.h * a.group + (r - j * a.group)) * D + kVec * lane;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        const float x = acc[k] * inv;
+        if (a.p.out_type == MMQ_TYPE_F32) static_cast<float*>(a.p.out)[at + k] = x;
+        else if (std::is_same<T, __half>::value) static_cast<__half*>(a.p.out)[at + k] = __float2half_rn(x);
+        else static_cast<__nv_bfloat16*>(a.p.out)[at + k] = __float2bfloat16_rn(x);
+    }
+}
+
+template <typename T, int D, bool kTwo>
+cudaError_t launch(const Kv4Args& a, int nsm, cudaLaunchConfig_t cfg) {
+    using L = Layout<D, kTwo>;
+    static const bool registers_ok = [] {   // else the split's increase would wait forever
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kv4_tc_kernel<T, D, kTwo>) == cudaSuccess && f.numRegs == int(kRegsLaunch);
+    }();
+    if (!registers_ok) return cudaErrorLaunchOutOfResources;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(kv4_tc_kernel<T, D, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes))) return e;
+    cfg.gridDim = dim3(unsigned(nsm));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    if ((e = cudaLaunchKernelEx(&cfg, kv4_tc_kernel<T, D, kTwo>, a))) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(unsigned(nsm * L::kStreams), unsigned(L::kR / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv4_tc_join_kernel<T, D, kTwo>, a);
+}
+template <typename T, int D>
+cudaError_t launch(const Kv4Args& a, bool two, int nsm, const cudaLaunchConfig_t& cfg) {
+    return two ? launch<T, D, true>(a, nsm, cfg) : launch<T, D, false>(a, nsm, cfg);
+}
+
+}  // namespace
+
+namespace mmq {
+
+// Parts of 2 x nsm x 256 rows either way (two runs of 128 rows per CTA, or one of 256).
+size_t kv4_attention_tc_part_bytes(int head_dim, int nsm) { return size_t(nsm) * 2 * 256 * size_t(head_dim + 2) * 4; }
+
+cudaError_t launch_kv4_attention_tc(const kv4::Kv4Args& a, bool two, int nsm, const cudaLaunchConfig_t& cfg) {
+    if (a.p.type == MMQ_TYPE_F16)
+        return a.p.head_dim == 64 ? launch<__half, 64>(a, two, nsm, cfg) : launch<__half, 128>(a, two, nsm, cfg);
+    return a.p.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, two, nsm, cfg) : launch<__nv_bfloat16, 128>(a, two, nsm, cfg);
+}
+
+}  // namespace mmq
