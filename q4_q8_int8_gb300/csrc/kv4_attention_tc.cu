@@ -16,6 +16,7 @@
 //                   [key][dimension], values transposed, [dimension][key]
 //   warp 12         fetches raw tiles: 8 bulk copies for 128 keys' half
 //   warps 13, 14    MMA issuers of groups 0 and 1
+//   warp 15         tells the others which pieces of units their run has
 // Runs of equal length of all units' key tiles are the CTAs' work, as in the
 // few-row kernel; the parts of units that lie in several runs are joined by a
 // second kernel.  kTwo: 256 rows to a unit, both groups share each key tile,
@@ -40,8 +41,8 @@ using namespace mmq::kv4;
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kThreads = 512;
 constexpr int kWarpExpand = 8, kWarpFetch = 12, kWarpMma = 13;   // and kWarpMma + 1
-// Registers: 128 per thread at launch (the launcher checks it): 256 x 192 + 128 x 72 + 128 x 56 = 512 x 128.
-constexpr uint32_t kRegsLaunch = 128, kRegsSoftmax = 192, kRegsExpand = 72, kRegsOther = 56;
+// Registers: 128 per thread at launch (the launcher checks it): 256 x 200 + 128 x 72 + 128 x 40 = 512 x 128.
+constexpr uint32_t kRegsLaunch = 128, kRegsSoftmax = 200, kRegsExpand = 72, kRegsOther = 40;
 static_assert(256 * kRegsSoftmax + 128 * kRegsExpand + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S_g at 128 g (P_g over its first 64 columns), O_g at 256 + 128 g
@@ -109,6 +110,14 @@ struct Walk {
     }
 };
 
+// What the roles are told of a piece: tiles [t0, t1) of a unit; none: the run's end.
+struct Piece {
+    int64_t start, name;             // the sequence's first row of q; the unit's first step of all
+    int b, h, u, t0, t1, starts, ends;
+    int n, len, most, least;         // of the sequence; keys that the unit's last and first row see
+};
+constexpr int kPieces = 4;           // told ahead
+
 template <int D, bool kTwo>
 struct Layout {
     static constexpr int kStreams = kTwo ? 1 : 2;
@@ -122,9 +131,11 @@ struct Layout {
     static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
     static constexpr int kOffSums = kOffRaw + kRawSlots * kRaw;
     static constexpr int kOffStart = kOffSums + 16 * 8;
-    static constexpr int kOffBar = kOffStart + 2 * int(sizeof(Start));
-    // barriers: raw_full, raw_empty; full, empty per slot; q_full, s_full, p_full, o_full, turn per group; drain
-    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 11) * 8;
+    static constexpr int kOffPieces = kOffStart + 2 * int(sizeof(Start));
+    static constexpr int kOffBar = kOffPieces + 2 * kPieces * int(sizeof(Piece));
+    // barriers: raw_full, raw_empty; full, empty per slot; q_full, s_full, p_full, o_full, turn per group; drain;
+    // told, done per piece
+    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 11 + 4 * kPieces) * 8;
     static constexpr int kBytes = kOffMisc + 32 + 1024;
     static constexpr int kR = kTwo ? 2 * kRows : kRows;      // rows of a unit
 };
@@ -186,6 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     auto p_full = [&](int g) { return bar1 + 8u * uint32_t(6 + g); };
     auto turn = [&](int g) { return bar1 + 8u * uint32_t(8 + g); };
     const uint32_t drain = bar1 + 8u * 10u;
+    auto told = [&](int st, uint32_t i) { return bar1 + 8u * (11u + uint32_t(st * kPieces) + i % kPieces); };
+    auto done_with = [&](int st, uint32_t i) { return told(st, i) + 8u * 2u * kPieces; };
+    Piece* const pieces = reinterpret_cast<Piece*>(smem + L::kOffPieces);
+    auto piece_at = [&](int st, uint32_t i) -> Piece& { return pieces[st * kPieces + int(i % kPieces)]; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     const AbortFlag abort_flag{sbase + L::kOffMisc + 4};
     const AbortFlag no_number{sbase + L::kOffMisc + 8};   // a value scale that is none was met where not all rows see it
@@ -212,6 +227,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             mbar_init(turn(g), 1);
         }
         mbar_init(drain, 2);
+        for (int st = 0; st < kStreams; ++st)
+            for (int i = 0; i < kPieces; ++i) {
+                mbar_init(told(st, i), 1);
+                mbar_init(done_with(st, i), kTwo ? 1 + 4 + 2 + 8 : 1 + 4 + 1 + 4);   // fetch, expand, MMA, softmax
+            }
         abort_flag.set(0u);
         no_number.set(0u);
         fence_barrier_init();
@@ -274,17 +294,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     auto slot_of = [&](int st, int kind, uint32_t no) { return (st * 2 + kind) * kBufs + int(no % kBufs); };
     auto phase_of = [&](uint32_t no) { return (no / kBufs) & 1u; };
 
-    // Tiles in the order K, V (kTwo) or K of both streams, V of both; job(stream, kind, its place).
+    // Piece i of stream st, once it is told; false after a wait that ran out.
+    auto await_piece = [&](int st, uint32_t i) { return wait_bounded(told(st, i), (i / kPieces) & 1u, abort_flag, status); };
+    // A warp's tiles in the order K, V (kTwo) or K of both streams, V of both; job(stream, kind, piece, tile).
     auto jobs = [&](auto&& job) {
-        Walk<kR> one(a, from[0]), two(a, from[kStreams - 1]);
-        while (one.valid() || (!kTwo && two.valid())) {
+        uint32_t no[kStreams] = {};
+        int t[kStreams];
+        bool live[kStreams], any = false, ok = true;
+        auto load = [&](int st) {
+            ok = __all_sync(0xffffffffu, await_piece(st, no[st]));
+            const Piece& q = piece_at(st, no[st]);
+            live[st] = ok && q.t0 < q.t1;
+            t[st] = q.t0;
+        };
 #pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {
-                if (one.valid() && !job(0, kind, one)) return;
-                if (!kTwo && two.valid() && !job(1, kind, two)) return;
+        for (int st = 0; st < kStreams; ++st) {
+            load(st);
+            if (!ok) return;
+            any |= live[st];
+        }
+        while (any) {
+#pragma unroll 1
+            for (int kind = 0; kind < 2; ++kind)
+#pragma unroll 1
+                for (int st = 0; st < kStreams; ++st)
+                    if (live[st] && !job(st, kind, piece_at(st, no[st]), t[st])) return;
+            any = false;
+#pragma unroll
+            for (int st = 0; st < kStreams; ++st) {
+                if (live[st] && ++t[st] == piece_at(st, no[st]).t1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(done_with(st, no[st]));
+                    ++no[st];
+                    load(st);
+                    if (!ok) return;
+                }
+                any |= live[st];
             }
-            if (one.valid()) one.step();
-            if (!kTwo && two.valid()) two.step();
         }
     };
     if (warp >= kWarpExpand && warp < kWarpFetch) {
@@ -298,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         const int id = threadIdx.x - kWarpExpand * 32;
         const int tile = id >> 4, r = id & 7, part = (id >> 3) & 1;
         const uint32_t words = uint32_t(tile * 9 * D + r * 64) + (D == 128 ? part * 512u : part * 8u);
-        jobs([&](int st, int kind, const Walk<kR>& q) {
+        jobs([&](int st, int kind, const Piece& q, int t) {
             const uint32_t no = tile_no[st];
             const int slot = slot_of(st, kind, no);
             if (kind == 1) ++tile_no[st];
@@ -340,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     ld_shared_words<2 * kG>(raw_at + uint32_t(tile * 9 * D + value_scales(D) - value_codes(D) + c * (D / 4) + part * kG * 8), vs[c][0]);
-                if (q.t * kKeys + kKeys > q.least()) {
+                if (t * kKeys + kKeys > q.least) {
                     // tokens that some rows of the unit do not see: what is no number must not reach those,
                     // and what lies past the last must reach none
-                    const int left = q.most() - (q.t * kKeys + tile * 16);
+                    const int left = q.most - (t * kKeys + tile * 16);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -387,11 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             bool withhold = a.inject && blockIdx.x == 0;
             const uint8_t* src[kStreams];
             const int tile_shift = a.page_shift - 4;
-            jobs([&](int st, int kind, const Walk<kR>& q) {
+            jobs([&](int st, int kind, const Piece& q, int t) {
                 if (kind == 0) {
                     src[st] = zero_tile;
-                    const int tile = 8 * q.t + lane;
-                    if (lane < 8 && tile * kTokens < q.most()) {
+                    const int tile = 8 * t + lane;
+                    if (lane < 8 && tile * kTokens < q.most) {
                         const int32_t id = p.page_table[int64_t(q.b) * p.table_width + (tile >> tile_shift)];
                         if (id < 0 || id >= p.n_pages) atomicCAS(status, 0, MMQ_ERR_ARG);
                         else
@@ -452,8 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 uint32_t no = 0;   // tiles so far
                 uint32_t q_phase = 0, p_phase = 0, t_phase = g == 0 ? 1u : 0u;   // group 0 has the first turn
                 bool ok = true;
-                for (Walk<kR> q(a, from[st]); q.valid() && ok; q.next()) {
-                    const int tiles = q.t1 - q.t;
+                for (uint32_t i = 0;; ++i) {
+                    ok = await_piece(st, i);
+                    const int tiles = piece_at(st, i).t1 - piece_at(st, i).t0;
+                    if (!ok || tiles == 0) break;
+                    mbar_arrive(done_with(st, i));
                     ok = wait_bounded(q_full(g), q_phase, abort_flag, status) && arrived(0, no);
                     if (!ok) break;
                     q_phase ^= 1u;
@@ -483,9 +532,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                         }
                         mma_commit(empty(slot));
                     }
+                    if (!ok) break;
                 }
                 mma_commit(drain);   // everything issued, also after a wait that ran out
                 wait_drain(drain, 0u, status);
+            }
+        } else if (lane < kStreams) {
+            // ---------------------------------------------- the runs' pieces
+            Walk<kR> q(a, from[lane]);
+            for (uint32_t i = 0;; ++i) {
+                if (!wait_bounded(done_with(lane, i), ((i / kPieces) & 1u) ^ 1u, abort_flag, status)) break;
+                Piece& to = piece_at(lane, i);
+                to.t0 = q.t;
+                to.t1 = q.t1;
+                if (q.valid()) {
+                    to.start = q.s.start;
+                    to.name = q.name;
+                    to.b = q.b;
+                    to.h = q.h;
+                    to.u = q.u;
+                    to.starts = q.starts;
+                    to.ends = q.ends();
+                    to.n = q.s.n;
+                    to.len = q.s.len;
+                    to.most = q.most();
+                    to.least = q.least();
+                }
+                mbar_arrive(told(lane, i));
+                if (!q.valid()) break;
+                q.next();
             }
         }
     } else {
@@ -497,16 +572,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         const uint32_t ts = tmem + lanes + kColS + 128u * uint32_t(g), to = tmem + lanes + kColO + 128u * uint32_t(g);
         uint32_t s_phase = 0, o_phase = 0;
         bool ok = true;
-        for (Walk<kR> q(a, from[st]); q.valid() && ok; q.next()) {
-            const int r = q.u * kR + (kTwo ? g * kRows : 0) + row;
-            const int j = r / a.group;
-            const bool valid = j < q.s.n;
-            const int head = q.h * a.group + r - j * a.group;
-            const int see = valid ? seen(q.s, j) : 0x7FFFFFFF;
-            // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.
+        for (uint32_t piece_no = 0;; ++piece_no) {
+            ok = __all_sync(0xffffffffu, await_piece(st, piece_no));
+            const Piece& q = piece_at(st, piece_no);
+            const int tiles = q.t1 - q.t0;
+            if (!ok || tiles == 0) break;
+            int left;   // keys that the row sees from the next tile on
             float scale = a.scale_log2;
+            // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.
             {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (valid ? (q.s.start + j) * p.q_stride + int64_t(head) * D : 0));
+                const int r = q.u * kR + (kTwo ? g * kRows : 0) + row, j = r / a.group, head = q.h * a.group + r - j * a.group;
+                const bool valid = j < q.n;
+                left = (valid ? max(0, q.len - q.n + 1 + j) : 0x7FFFFFFF) - q.t0 * kKeys;
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (valid ? (q.start + j) * p.q_stride + int64_t(head) * D : 0));
                 const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kTile + row * 128);
                 uint4 v[D / 8];
 #pragma unroll
@@ -540,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             }
             float m = kNone, l = 0.f;
             bool wide = false;
-            const int tiles = q.t1 - q.t;
             int n = 0;
             auto scale_o = [&](float f) {   // at rest: the product before this S has completed
                 l *= f;
@@ -564,7 +641,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), s[c]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-                const int left = see - (q.t + n) * kKeys;
                 if (left < kKeys) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -612,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 if (lane == 0) mbar_arrive(p_full(g));
                 sum[0] = fadd2(sum[0], sum[1]);
                 l += lo_f(sum[0]) + hi_f(sum[0]);
+                left -= kKeys;
             }
             // S scale - m in one step, as above, is past zero by what m lost in its rounding, half a unit in its
             // last place: from 2^20 on too much for P's range.  From the first tile where a row of the warp gets
@@ -624,7 +701,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     s_phase ^= 1u;
                     tc_fence_after();
                 }
-                const int left = see - (q.t + n) * kKeys;
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -659,17 +735,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(g));
                 l += sum;
+                left -= kKeys;
             }
             if (!ok) break;
             ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
             if (!ok) break;
             o_phase ^= 1u;
             tc_fence_after();
+            const int r = q.u * kR + (kTwo ? g * kRows : 0) + row, j = r / a.group, head = q.h * a.group + r - j * a.group;
+            const bool valid = j < q.n, done = q.starts && q.ends;
             // Where a value scale is no number and not all rows see its token: the rows that do, block by block.
             uint32_t none = 0;
             if (no_number.raised() && valid) {
-                const int tile_shift = a.page_shift - 4;
-                for (int key = max(q.t, q.least() / kKeys) * kKeys; key < min(see, q.t1 * kKeys); ++key) {
+                const int tile_shift = a.page_shift - 4, see = max(0, q.len - q.n + 1 + j);
+                for (int key = max(q.t0, q.least / kKeys) * kKeys; key < min(see, q.t1 * kKeys); ++key) {
                     const int32_t id = p.page_table[int64_t(q.b) * p.table_width + (key >> a.page_shift)];
                     if (id < 0 || id >= p.n_pages) continue;
                     const uint8_t* at = p.cache + (((int64_t(id) * p.kv_heads + q.h) << tile_shift) +
@@ -678,7 +757,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                         if (!finite16(*reinterpret_cast<const uint16_t*>(at + value_scale<D>(key & 15, b)))) none |= 1u << b;
                 }
             }
-            const bool done = q.starts && q.ends();
             const float factor = done ? l == 0.f ? 0.f : 1.f / l : 1.f;
             const int64_t run = blockIdx.x + int64_t(st) * gridDim.x;
             const int64_t at = (run * 2 + (q.starts ? 1 : 0)) * kR + (r - q.u * kR);   // a part's row
@@ -691,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 const float by = (none >> c) & 1u ? __int_as_float(0x7FC00000) : factor;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
-                const int64_t out = ((q.s.start + j) * p.heads + head) * D + 32 * c;
+                const int64_t out = ((q.start + j) * p.heads + head) * D + 32 * c;
                 if (!done || p.out_type == MMQ_TYPE_F32) {
                     uint4* dst = reinterpret_cast<uint4*>(done ? static_cast<float*>(p.out) + out : a.parts + at * D + 32 * c);
 #pragma unroll
@@ -723,11 +801,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     mark.tile = q.u;
                 } else {
                     mark.head = q.name;
-                    mark.head_ends = q.ends();
+                    mark.head_ends = q.ends;
                 }
             }
             if (!done && valid)
                 reinterpret_cast<float2*>(a.parts + int64_t(gridDim.x) * kStreams * 2 * kR * D)[at] = make_float2(reference(m), l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(done_with(st, piece_no));
         }
     }
 
