@@ -161,13 +161,15 @@ struct Join {
             store_row<D, W::R>(a, u, s, row, dim, acc[i] * inv);
         }
     }
-    __device__ __forceinline__ void keep(float* part) const {
+    __device__ __forceinline__ void keep(const Kv4Args& a, int64_t part) const {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) part[reg(i) * 32 + lane] = acc[i];
-        if (lane < 4 && rest == 0) {
-            part[W::kRegs * 32 + row] = m;
-            part[W::kRegs * 32 + W::R + row] = l;
+        for (int i = 0; i < kMine; ++i) {
+            int dim, same;
+            element<NT>(reg(i), lane, dim, same);
+            a.parts[(part * W::R + row) * D + dim] = acc[i];
         }
+        if (lane < 4 && rest == 0)
+            reinterpret_cast<float2*>(a.parts + int64_t(gridDim.x) * 2 * W::R * D)[part * W::R + row] = make_float2(m, l);
     }
 };
 
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     __syncthreads();
 
     // ---- units of several warps: joined, finished or left for the join over CTAs
-    Mark mark{-1, -1, 0, 0, 0, 0};
+    Mark mark{-1, 0, 0, 0};
     if (!abort_flag.raised()) {
         for (int i = 0; i < 2 * kWarps;) {
             if (sh.name[i] < 0) {
@@ -657,21 +659,17 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
                     break;
                 }
             const bool starts = sh.whole[i] & 1;
+            const Unit u = sh.unit[i];
             Join<D, NT> join;
             for (int j = i; j < upto; ++j)
                 if (sh.name[j] >= 0) join.add(part_at(j));
             if (starts && ends) {
-                join.finish(a, sh.unit[i], sequence(a, sh.unit[i].b, false));
+                join.finish(a, u, sequence(a, u.b, false));
             } else {
-                join.keep(a.parts + (int64_t(blockIdx.x) * 2 + (starts ? 1 : 0)) * W::kPart);
+                join.keep(a, int64_t(blockIdx.x) * 2 + (starts ? 1 : 0));
                 if (starts) {
-                    mark.tail = name;
-                    mark.b = sh.unit[i].b;
-                    mark.h = sh.unit[i].h;
-                    mark.tile = sh.unit[i].tile;
-                } else {
-                    mark.head = name;
-                    mark.head_ends = ends;
+                    const int64_t end = name + unit_steps<R, kStep>(sequence(a, u.b, false), a.group, u.tile);
+                    mark = Mark{int(run_of(end - 1, runs, total) / kWarps), u.b, u.h, u.tile};
                 }
             }
             i = upto;
@@ -680,26 +678,99 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     if (threadIdx.x == 0) a.marks[blockIdx.x] = mark;
 }
 
-// Units of several CTAs: CTA i joins the one that starts in CTA i and does not end there.
-template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) kv4_join_kernel(const Kv4Args a) {
+// Units of several runs: block (i, rows) joins eight rows of the unit that starts in run i and does not end there.
+// Few parts: a warp per row.  Many: the warps share a row's parts, row after row.
+constexpr int kJoinRows = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * 32) kv4_join_kernel(const Kv4Args a, int R) {
+    constexpr int kVec = D / 32, kFlight = 4;
+    __shared__ float sums[kJoinRows][D + 1];
     griddep_launch_dependents();
     griddep_wait();
-    using W = Rows<D, NT>;
     const Mark mark = a.marks[blockIdx.x];
-    if (mark.tail < 0) return;
-    Join<D, NT> join;
-    join.add(a.parts + (int64_t(blockIdx.x) * 2 + 1) * W::kPart);
-    for (unsigned j = blockIdx.x + 1; j < gridDim.x; ++j) {
-        const int64_t name = a.marks[j].head;
-        if (name < 0) {      // no tile at all, or an aborted CTA
-            continue;
+    if (mark.last < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Sequence s = sequence(a, mark.b, false);
+    const float2* const mls = reinterpret_cast<const float2*>(a.parts + int64_t(gridDim.x) * 2 * R * D);
+    const int parts = mark.last - int(blockIdx.x) + 1;
+    auto at = [&](int k) { return (k == 0 ? int64_t(blockIdx.x) * 2 + 1 : (int64_t(blockIdx.x) + k) * 2) * R; };   // of row 0
+    // Row `row`'s parts first, first + step, ...: their weighted sum, from the row's reference on
+    auto gather = [&](int row, int first, int step, float (&acc)[kVec], float& l) {
+        float m = kNone;
+        for (int k = lane; k < parts; k += 32) {
+            const float2 ml = mls[at(k) + row];
+            if (ml.y != 0.f) m = fmaxf(m, ml.x);   // else no key
         }
-        if (name != mark.tail) break;
-        join.add(a.parts + int64_t(j) * 2 * W::kPart);
-        if (a.marks[j].head_ends) break;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+        for (int k0 = first; k0 < parts; k0 += kFlight * step) {
+            float v[kFlight][kVec];
+            float2 ml[kFlight];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const int k = k0 + f * step;
+                ml[f] = make_float2(kNone, 0.f);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) v[f][c] = 0.f;
+                if (k < parts) {
+                    ml[f] = mls[at(k) + row];
+#pragma unroll
+                    for (int c = 0; c < kVec; c += 2) {
+                        const float2 u = *reinterpret_cast<const float2*>(a.parts + (at(k) + row) * D + kVec * lane + c);
+                        v[f][c] = u.x;
+                        v[f][c + 1] = u.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                if (ml[f].y == 0.f) continue;
+                const float by = ex2(ml[f].x - m);
+                l = fmaf(by, ml[f].y, l);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) acc[c] = fmaf(by, v[f][c], acc[c]);
+            }
+        }
+    };
+    auto store = [&](int row, const float (&acc)[kVec], float l) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t r = int64_t(mark.tile) * R + row, j = r / a.group;
+        const int64_t out = ((s.start + j) * a.p.heads + mark.h * a.group + (r - j * a.group)) * D + kVec * lane;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) store_value(a.p.out, a.p.out_type, out + c, acc[c] * inv);
+    };
+    const int64_t rows = int64_t(s.n) * a.group - int64_t(mark.tile) * R;   // of the unit, from its first on
+    const int row0 = int(blockIdx.y) * kJoinRows;
+    if (row0 >= rows) return;
+    float acc[kVec], l;
+    if (parts <= 8) {
+        if (row0 + warp >= rows) return;
+        gather(row0 + warp, 0, 1, acc, l);
+        store(row0 + warp, acc, l);
+        return;
     }
-    join.finish(a, Unit{mark.b, mark.h, mark.tile}, sequence(a, mark.b, false));
+    for (int row = row0; row < row0 + kJoinRows && row < rows; ++row) {
+        gather(row, warp, kJoinRows, acc, l);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) sums[warp][kVec * lane + c] = acc[c];
+        if (lane == 0) sums[warp][D] = l;
+        __syncthreads();
+        if (warp == (row & (kJoinRows - 1))) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) acc[c] = 0.f;
+            l = 0.f;
+            for (int w = 0; w < kJoinRows; ++w) {
+                l += sums[w][D];
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) acc[c] += sums[w][kVec * lane + c];
+            }
+            store(row, acc, l);
+        }
+        __syncthreads();
+    }
 }
 
 int sm_count() {
@@ -719,7 +790,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 template <int D, int NT>
 size_t part_bytes(int nsm) {
-    return up256(size_t(nsm) * Rows<D, NT>::kCtas * 2 * Rows<D, NT>::kPart * 4);
+    return up256(size_t(nsm) * Rows<D, NT>::kCtas * 2 * Rows<D, NT>::R * (D + 2) * 4);
 }
 size_t part_bytes(const mmq_kv4_attention_t& p, int nsm) {
     if (p.head_dim == 64) return narrow(p) ? part_bytes<64, 1>(nsm) : part_bytes<64, 2>(nsm);
@@ -734,13 +805,9 @@ cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
     cudaError_t e;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes))) return e;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned(nsm * W::kCtas)), dim3(kWarps * 32), W::kBytes, s, attr);
+    const cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned(nsm * W::kCtas)), dim3(kWarps * 32), W::kBytes, s, attr);
     if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a);
+    return mmq::launch_kv4_join(a, W::R, nsm * W::kCtas, s);
 }
 template <typename T, int D>
 cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
@@ -772,6 +839,19 @@ constexpr int kMostRuns = 3;   // marks per SM, of either kernel
 }  // namespace
 
 namespace mmq {
+
+cudaError_t launch_kv4_join(const Kv4Args& a, int R, int runs, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the kernel before it
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = s;
+    cfg.gridDim = dim3(unsigned(runs), unsigned((R + kJoinRows - 1) / kJoinRows));
+    cfg.blockDim = dim3(kJoinRows * 32);
+    return a.p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<64>, a, R) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<128>, a, R);
+}
 
 size_t kv4_attention_workspace(const mmq_kv4_attention_t& p) {
     const int nsm = sm_count();

@@ -15,10 +15,11 @@
 namespace mmq {
 namespace kv4 {
 
+struct Mark;
 struct Kv4Args {
     mmq_kv4_attention_t p;
-    float* parts;       // [ctas][2] units' sums and (m, l): a CTA's first and last
-    struct Mark* marks; // [ctas]
+    float* parts;         // see Mark
+    Mark* marks;          // one per run (of a CTA, or a stream of it)
     int* status;
     int inject;
     int page_shift, group;
@@ -26,12 +27,12 @@ struct Kv4Args {
     uint32_t low, high;   // masks of codes: 0x000F000F, 0x00F000F0
     int few;              // sequences of up to so many rows are the few-row kernel's, others the tensor-core kernel's
 };
-// What a CTA leaves of units that it shares with other CTAs: the start of a
-// unit's run of tiles is its name.
+// A unit that starts in a run and does not end there: runs up to `last` (-1: no
+// such unit) have a part of it.  A run leaves two parts at most, of a unit that
+// started before it (0) and of one that does not end in it (1): sums f32
+// [run][part][row][dim], and after those (reference, sum of weights) [run][part][row].
 struct Mark {
-    int64_t head, tail;      // -1: none
-    int head_ends;           // the head's unit has its last tile here
-    int b, h, tile;          // the tail's unit
+    int last, b, h, tile;
 };
 
 // The unit of the sequence's head.
@@ -99,6 +100,13 @@ __device__ __forceinline__ int64_t head_steps(const Sequence& s, int group) {
 __device__ __forceinline__ int64_t run_start(int64_t run, int64_t runs, int64_t total) {
     return run >= runs ? total : total / runs * run + total % runs * run / runs;
 }
+// The run that step `at` lies in.
+__device__ __forceinline__ int64_t run_of(int64_t at, int64_t runs, int64_t total) {
+    int64_t r = min(runs - 1, int64_t(double(at) * double(runs) / double(total)));
+    while (run_start(r, runs, total) > at) --r;
+    while (run_start(r + 1, runs, total) <= at) ++r;
+    return r;
+}
 // An inclusive sum over the threads of a CTA of kWarps warps, and the whole sum; sums: kWarps words of shared memory.
 template <int kWarps>
 __device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t* sums, int64_t& total) {
@@ -123,6 +131,8 @@ __device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t* sums, int64_t
 }  // namespace kv4
 
 // The tensor-core kernel (kv4_attention_tc.cu) and its join; two: 256 rows to a unit, not 128.
+// Joins what `runs` runs of units of R rows have left (kv4_attention.cu).
+cudaError_t launch_kv4_join(const kv4::Kv4Args& a, int R, int runs, cudaStream_t s);
 size_t kv4_attention_tc_part_bytes(int head_dim, int nsm);
 cudaError_t launch_kv4_attention_tc(const kv4::Kv4Args& a, bool two, int nsm, const cudaLaunchConfig_t& cfg);
 

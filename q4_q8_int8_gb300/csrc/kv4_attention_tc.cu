@@ -112,8 +112,9 @@ struct Walk {
 
 // What the roles are told of a piece: tiles [t0, t1) of a unit; none: the run's end.
 struct Piece {
-    int64_t start, name;             // the sequence's first row of q; the unit's first step of all
+    int64_t start;                   // the sequence's first row of q
     int b, h, u, t0, t1, starts, ends;
+    int last;                        // the run that the unit ends in
     int n, len, most, least;         // of the sequence; keys that the unit's last and first row see
 };
 constexpr int kPieces = 4;           // told ahead
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
     const int64_t x1 = cta_scan<kThreads / 32>(mine, sums, total), x0 = x1 - mine;
     const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kStreams, total));
-    if (threadIdx.x < kStreams) a.marks[blockIdx.x + threadIdx.x * gridDim.x] = Mark{-1, -1, 0, 0, 0, 0};
+    if (threadIdx.x < kStreams) a.marks[blockIdx.x + threadIdx.x * gridDim.x] = Mark{-1, 0, 0, 0};
 
 #pragma unroll
     for (int st = 0; st < kStreams; ++st) {
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 to.t1 = q.t1;
                 if (q.valid()) {
                     to.start = q.s.start;
-                    to.name = q.name;
+                    to.last = int(run_of(q.name + q.steps - 1, runs, total));
                     to.b = q.b;
                     to.h = q.h;
                     to.u = q.u;
@@ -792,18 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 }
             }
             tc_fence_before();
-            if (!done && row == 0 && (g == 0 || !kTwo)) {
-                Mark& mark = a.marks[run];
-                if (q.starts) {
-                    mark.tail = q.name;
-                    mark.b = q.b;
-                    mark.h = q.h;
-                    mark.tile = q.u;
-                } else {
-                    mark.head = q.name;
-                    mark.head_ends = q.ends;
-                }
-            }
+            if (!done && q.starts && row == 0 && (g == 0 || !kTwo)) a.marks[run] = Mark{q.last, q.b, q.h, q.u};
             if (!done && valid)
                 reinterpret_cast<float2*>(a.parts + int64_t(gridDim.x) * kStreams * 2 * kR * D)[at] = make_float2(reference(m), l);
             __syncwarp();
@@ -817,55 +807,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
-    }
-}
-
-// Units of several runs: blocks (i, *) join the one that starts in run i and does not end there, a warp per row.
-template <typename T, int D, bool kTwo>
-__global__ void __launch_bounds__(256) kv4_tc_join_kernel(const Kv4Args a) {
-    constexpr int kR = Layout<D, kTwo>::kR, kVec = D / 32;
-    griddep_launch_dependents();
-    griddep_wait();
-    const Mark mark = a.marks[blockIdx.x];
-    if (mark.tail < 0) return;
-    const int lane = threadIdx.x & 31, row = int(blockIdx.y) * 8 + (threadIdx.x >> 5);
-    const Sequence s = sequence(a, mark.b, false);
-    const int r = mark.tile * kR + row, j = r / a.group;
-    if (j >= s.n) return;
-    const float2* const mls = reinterpret_cast<const float2*>(a.parts + int64_t(gridDim.x) * 2 * kR * D);
-    float acc[kVec] = {}, m = kNone, l = 0.f;
-    auto add = [&](int64_t part) {
-        const float2 ml = mls[part * kR + row];
-        float v[kVec];
-#pragma unroll
-        for (int k = 0; k < kVec; k += 2) {
-            const float2 u = *reinterpret_cast<const float2*>(a.parts + (part * kR + row) * D + kVec * lane + k);
-            v[k] = u.x;
-            v[k + 1] = u.y;
-        }
-        if (ml.y == 0.f) return;   // no key
-        const float top = fmaxf(m, ml.x), mine = ex2(m - top), its = ex2(ml.x - top);
-        m = top;
-        l = l * mine + ml.y * its;
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * mine + v[k] * its;
-    };
-    add(int64_t(blockIdx.x) * 2 + 1);
-    for (unsigned i = blockIdx.x + 1; i < gridDim.x; ++i) {
-        const int64_t name = a.marks[i].head;
-        if (name < 0) continue;   // no tile at all
-        if (name != mark.tail) break;
-        add(int64_t(i) * 2);
-        if (a.marks[i].head_ends) break;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = ((s.start + j) * a.p.heads + mark.h * a.group + (r - j * a.group)) * D + kVec * lane;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-        const float x = acc[k] * inv;
-        if (a.p.out_type == MMQ_TYPE_F32) static_cast<float*>(a.p.out)[at + k] = x;
-        else if (std::is_same<T, __half>::value) static_cast<__half*>(a.p.out)[at + k] = __float2half_rn(x);
-        else static_cast<__nv_bfloat16*>(a.p.out)[at + k] = __float2bfloat16_rn(x);
     }
 }
 
@@ -883,15 +824,7 @@ cudaError_t launch(const Kv4Args& a, int nsm, cudaLaunchConfig_t cfg) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = L::kBytes;
     if ((e = cudaLaunchKernelEx(&cfg, kv4_tc_kernel<T, D, kTwo>, a))) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(unsigned(nsm * L::kStreams), unsigned(L::kR / 8));
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv4_tc_join_kernel<T, D, kTwo>, a);
+    return mmq::launch_kv4_join(a, L::kR, nsm * L::kStreams, cfg.stream);
 }
 template <typename T, int D>
 cudaError_t launch(const Kv4Args& a, bool two, int nsm, const cudaLaunchConfig_t& cfg) {
