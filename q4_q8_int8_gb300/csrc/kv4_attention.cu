@@ -118,13 +118,11 @@ __device__ __forceinline__ void element(int k, int lane, int& dim, int& row) {
     row = 8 * nt + 2 * (lane & 3) + (k & 1);
 }
 
+// Where a unit's row goes, in values; -1 past its sequence's last.
 template <int D, int R>
-__device__ __forceinline__ void store_row(const Kv4Args& a, const Unit& u, const Sequence& s, int row, int dim, float x) {
-    const int64_t r = int64_t(u.tile) * R + row;
-    const int64_t j = r / a.group;
-    if (j >= s.n) return;
-    const int head = u.h * a.group + int(r - j * a.group);
-    store_value(a.p.out, a.p.out_type, ((s.start + j) * a.p.heads + head) * D + dim, x);
+__device__ __forceinline__ int64_t out_row(const Kv4Args& a, const Unit& u, const Sequence& s, int row) {
+    const int r = u.tile * R + row, j = r / a.group;
+    return j < s.n ? ((s.start + j) * a.p.heads + u.h * a.group + (r - j * a.group)) * D : -1;
 }
 
 // Parts of one unit, added up by a CTA: a thread has some registers of its lane, all of one row.
@@ -154,11 +152,13 @@ struct Join {
     }
     __device__ __forceinline__ void finish(const Kv4Args& a, const Unit& u, const Sequence& s) const {
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t out = out_row<D, W::R>(a, u, s, row);
+        if (out < 0) return;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             int dim, same;
             element<NT>(reg(i), lane, dim, same);
-            store_row<D, W::R>(a, u, s, row, dim, acc[i] * inv);
+            store_value(a.p.out, a.p.out_type, out + dim, acc[i] * inv);
         }
     }
     __device__ __forceinline__ void keep(const Kv4Args& a, int64_t part) const {
@@ -215,9 +215,9 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     int64_t mine = 0, total;
     for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
     const int64_t x1 = cta_scan<kWarps>(mine, sh.total, total), x0 = x1 - mine;
-    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kWarps, total / kLeast));
+    const Runs runs(total, max(int64_t(1), min(int64_t(gridDim.x) * kWarps, total / kLeast)));
     for (int w = 0; w <= kWarps; ++w) {
-        const int64_t at = run_start(int64_t(blockIdx.x) * kWarps + w, runs, total);
+        const int64_t at = runs.start(int64_t(blockIdx.x) * kWarps + w);
         if (threadIdx.x == 0) sh.first[w] = at;
         if (w < kWarps && x0 <= at && at < x1) {   // of one thread
             int64_t x = x0;
@@ -273,11 +273,49 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
         const int64_t name = at - t0;        // the unit's first tile of all
         const int row0 = u.tile * R;   // first row of the unit
 
+        const int most = min(unit_keys<R>(s, a.group, u.tile), t1 * kStep);   // that the unit's last row sees of these
+        const int least = min(seen(s, row0 / a.group), t1 * kStep);           // and its first
+        const int last = min(t1, (most + kStep - 1) / kStep);   // steps with a key
+        // Copies, of two tiles a step.  Lanes 2 i and 2 i + 1 have the places of step i of the next 16 and issue its copies.
+        const int32_t* const table = p.page_table + int64_t(b) * p.table_width;
+        const int tile_shift = a.page_shift - 4;
+        const uint8_t* src = zero_tile;
+        int next = t0;
+        int32_t ahead = -1;            // the page of this lane's tile of the 16 steps after those
+        auto page_of = [&](int step) {
+            const int tile = 2 * step + lane;
+            return tile * kTokens < most ? table[tile >> tile_shift] : -1;
+        };
+        auto fetch = [&]() {
+            const int i = (next - t0) & 15;
+            if (i == 0) {
+                const int tile = 2 * next + lane;
+                const int32_t id = next == t0 ? page_of(next) : ahead;
+                const bool good = id >= 0 && id < p.n_pages;
+                src = zero_tile;
+                if (good)
+                    src = p.cache + (((int64_t(id) * p.kv_heads + u.h) << tile_shift) + (tile & ((1 << tile_shift) - 1))) * tile_bytes(D);
+                bad_page |= !good && tile * kTokens < most;
+            } else if (i == 8) {
+                ahead = page_of(next + 8);
+            }
+            const uint32_t bar = bars + 8u * uint32_t(fill), dst = ring + uint32_t(fill * 2 * tile_bytes(D)) + uint32_t(lane & 1) * tile_bytes(D);
+            if (lane >> 1 == i && !withheld) {
+                mbar_arrive_expect_tx(bar, tile_bytes(D));
+                bulk_load(dst, src, tile_bytes(D), bar);
+            }
+            withheld = false;
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+            ++flying;
+            ++next;
+        };
+        for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
+
         // Queries: lane's row is r8 (of each eight), its dimensions 2 c, 2 c + 1 and those + 8 of every 16.
         uint32_t qf[NT][D / 16][2];
         uint32_t qs[NT][2];            // -8 sum q' of each block, times 2^112, as an operand
         float f[NT][2];
-        int see[NT][2], most = 0, least = 0x7FFFFFFF;
+        int see[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = row0 + 8 * nt + r8, j = row / a.group;
@@ -355,50 +393,11 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
                 m[nt][k] = kNone;
                 l[nt][k] = 0.f;
             }
-            most = max(most, mine_see);
-            if (has) least = min(least, mine_see);
-        }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-            least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
         }
 #pragma unroll
         for (int i = 0; i < W::kRegs / 4; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-
-        const int last = min(t1, (most + kStep - 1) / kStep);   // steps with a key
-        // Copies, of two tiles a step.  Lanes 2 i and 2 i + 1 have the places of step i of the next 16 and issue its copies.
-        const int32_t* const table = p.page_table + int64_t(b) * p.table_width;
-        const int tile_shift = a.page_shift - 4;
-        const uint8_t* src = zero_tile;
-        int next = t0;
-        auto fetch = [&]() {
-            const int i = (next - t0) & 15;
-            if (i == 0) {
-                const int tile = 2 * next + lane;
-                src = zero_tile;
-                if (tile * kTokens < most) {
-                    const int32_t id = table[tile >> tile_shift];
-                    if (id < 0 || id >= p.n_pages)
-                        bad_page = true;
-                    else
-                        src = p.cache + (((int64_t(id) * p.kv_heads + u.h) << tile_shift) + (tile & ((1 << tile_shift) - 1))) *
-                                            tile_bytes(D);
-                }
-            }
-            const uint32_t bar = bars + 8u * uint32_t(fill), dst = ring + uint32_t(fill * 2 * tile_bytes(D)) + uint32_t(lane & 1) * tile_bytes(D);
-            if (lane >> 1 == i && !withheld) {
-                mbar_arrive_expect_tx(bar, tile_bytes(D));
-                bulk_load(dst, src, tile_bytes(D), bar);
-            }
-            withheld = false;
-            fill = fill + 1 == kStages ? 0 : fill + 1;
-            ++flying;
-            ++next;
-        };
-        for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
 
         // One step; kRagged: not all rows see all of it.
         auto take = [&](int t, auto ragged) {
@@ -605,11 +604,37 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) inv[nt][k] = l[nt][k] == 0.f ? 0.f : 1.f / l[nt][k];
+            for (int nt = 0; nt < NT; ++nt) {
+                if (p.out_type == MMQ_TYPE_F32) {
 #pragma unroll
-            for (int k = 0; k < W::kRegs; ++k) {
-                int dim, row;
-                element<NT>(k, lane, dim, row);
-                store_row<D, R>(a, u, s, row, dim, o[k >> 2][k & 3] * inv[(k >> 2) % NT][k & 1]);
+                    for (int k = 0; k < 2; ++k) {
+                        const int64_t out = out_row<D, R>(a, u, s, 8 * nt + 2 * c4 + k);
+                        if (out < 0) continue;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            static_cast<float*>(p.out)[out + 16 * i + r8] = o[i * NT + nt][k] * inv[nt][k];
+                            static_cast<float*>(p.out)[out + 16 * i + 8 + r8] = o[i * NT + nt][k + 2] * inv[nt][k];
+                        }
+                    }
+                    continue;
+                }
+                // 8 x 8 blocks turned round: row r8, dimensions 2 c, 2 c + 1
+                const int64_t out = out_row<D, R>(a, u, s, 8 * nt + r8);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float x = o[i * NT + nt][2 * half] * inv[nt][0], y = o[i * NT + nt][2 * half + 1] * inv[nt][1];
+                        uint32_t w;
+                        if (std::is_same<T, __half>::value) {
+                            w = h2u(__floats2half2_rn(x, y));
+                        } else {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                            w = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        w = transpose8x8(w);
+                        if (out >= 0) *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out + 16 * i + 8 * half + 2 * c4) = w;
+                    }
             }
             continue;
         }
@@ -669,7 +694,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
                 join.keep(a, int64_t(blockIdx.x) * 2 + (starts ? 1 : 0));
                 if (starts) {
                     const int64_t end = name + unit_steps<R, kStep>(sequence(a, u.b, false), a.group, u.tile);
-                    mark = Mark{int(run_of(end - 1, runs, total) / kWarps), u.b, u.h, u.tile};
+                    mark = Mark{int(runs.of(end - 1) / kWarps), u.b, u.h, u.tile};
                 }
             }
             i = upto;

@@ -96,17 +96,17 @@ __device__ __forceinline__ int64_t head_steps(const Sequence& s, int group) {
     for (int u = 0; u < m; ++u) n += unit_steps<R, kStep>(s, group, u);
     return n;
 }
-// The first step of run `run` of `runs` that share `total` steps alike (total < 2^47, runs < 2^16).
-__device__ __forceinline__ int64_t run_start(int64_t run, int64_t runs, int64_t total) {
-    return run >= runs ? total : total / runs * run + total % runs * run / runs;
-}
-// The run that step `at` lies in.
-__device__ __forceinline__ int64_t run_of(int64_t at, int64_t runs, int64_t total) {
-    int64_t r = min(runs - 1, int64_t(double(at) * double(runs) / double(total)));
-    while (run_start(r, runs, total) > at) --r;
-    while (run_start(r + 1, runs, total) <= at) ++r;
-    return r;
-}
+// Runs that share `total` steps: the first `longer` of them have one more than the others.
+struct Runs {
+    int64_t total, each, longer;
+    __device__ __forceinline__ Runs(int64_t total, int64_t runs) : total(total), each(total / runs), longer(total - each * runs) {}
+    __device__ __forceinline__ int64_t start(int64_t run) const { return min(total, run * each + min(run, longer)); }
+    // The run that step `at` lies in.
+    __device__ __forceinline__ int64_t of(int64_t at) const {
+        const int64_t first = longer * (each + 1);
+        return at < first ? at / (each + 1) : longer + (at - first) / each;
+    }
+};
 // An inclusive sum over the threads of a CTA of kWarps warps, and the whole sum; sums: kWarps words of shared memory.
 template <int kWarps>
 __device__ __forceinline__ int64_t cta_scan(int64_t mine, int64_t* sums, int64_t& total) {

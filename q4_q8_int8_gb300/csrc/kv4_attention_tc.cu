@@ -258,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     int64_t mine = 0, total;
     for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
     const int64_t x1 = cta_scan<kThreads / 32>(mine, sums, total), x0 = x1 - mine;
-    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x) * kStreams, total));
+    const Runs runs(total, max(int64_t(1), min(int64_t(gridDim.x) * kStreams, total)));
     if (threadIdx.x < kStreams) a.marks[blockIdx.x + threadIdx.x * gridDim.x] = Mark{-1, 0, 0, 0};
 
 #pragma unroll
     for (int st = 0; st < kStreams; ++st) {
         const int64_t run = blockIdx.x + int64_t(st) * gridDim.x;
-        const int64_t lo = run_start(run, runs, total), hi = run_start(run + 1, runs, total);
+        const int64_t lo = runs.start(run), hi = runs.start(run + 1);
         if (threadIdx.x == 0) {
             from[st].steps = hi - lo;
             from[st].first = lo;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 to.t1 = q.t1;
                 if (q.valid()) {
                     to.start = q.s.start;
-                    to.last = int(run_of(q.name + q.steps - 1, runs, total));
+                    to.last = int(runs.of(q.name + q.steps - 1));
                     to.b = q.b;
                     to.h = q.h;
                     to.u = q.u;
