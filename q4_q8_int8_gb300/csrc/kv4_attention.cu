@@ -703,13 +703,13 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     if (threadIdx.x == 0) a.marks[blockIdx.x] = mark;
 }
 
-// Units of several runs: block (i, rows) joins eight rows of the unit that starts in run i and does not end there.
-// Few parts: a warp per row.  Many: the warps share a row's parts, row after row.
+// Units of several runs: blocks (i, *) join the one that starts in run i and does not end there.  kShare: a block per
+// row, whose warps share the row's parts (one sequence of 32k tokens has 57 of them); else a warp per row, eight rows.
 constexpr int kJoinRows = 8;
-template <int D>
+template <int D, bool kShare>
 __global__ void __launch_bounds__(kJoinRows * 32) kv4_join_kernel(const Kv4Args a, int R) {
     constexpr int kVec = D / 32, kFlight = 4;
-    __shared__ float sums[kJoinRows][D + 1];
+    __shared__ float sums[kShare ? kJoinRows : 1][D + 1];
     griddep_launch_dependents();
     griddep_wait();
     const Mark mark = a.marks[blockIdx.x];
@@ -768,34 +768,23 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv4_join_kernel(const Kv4Args 
         for (int c = 0; c < kVec; ++c) store_value(a.p.out, a.p.out_type, out + c, acc[c] * inv);
     };
     const int64_t rows = int64_t(s.n) * a.group - int64_t(mark.tile) * R;   // of the unit, from its first on
-    const int row0 = int(blockIdx.y) * kJoinRows;
-    if (row0 >= rows) return;
     float acc[kVec], l;
-    if (parts <= 8) {
-        if (row0 + warp >= rows) return;
-        gather(row0 + warp, 0, 1, acc, l);
-        store(row0 + warp, acc, l);
-        return;
-    }
-    for (int row = row0; row < row0 + kJoinRows && row < rows; ++row) {
-        gather(row, warp, kJoinRows, acc, l);
+    const int row = kShare ? int(blockIdx.y) : int(blockIdx.y) * kJoinRows + warp;
+    if (row >= rows) return;   // the whole block, if it shares
+    gather(row, kShare ? warp : 0, kShare ? kJoinRows : 1, acc, l);
+    if (kShare) {
 #pragma unroll
         for (int c = 0; c < kVec; ++c) sums[warp][kVec * lane + c] = acc[c];
         if (lane == 0) sums[warp][D] = l;
         __syncthreads();
-        if (warp == (row & (kJoinRows - 1))) {
+        if (warp) return;
+        for (int w = 1; w < kJoinRows; ++w) {
+            l += sums[w][D];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) acc[c] = 0.f;
-            l = 0.f;
-            for (int w = 0; w < kJoinRows; ++w) {
-                l += sums[w][D];
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) acc[c] += sums[w][kVec * lane + c];
-            }
-            store(row, acc, l);
+            for (int c = 0; c < kVec; ++c) acc[c] += sums[w][kVec * lane + c];
         }
-        __syncthreads();
     }
+    store(row, acc, l);
 }
 
 int sm_count() {
@@ -873,9 +862,12 @@ cudaError_t launch_kv4_join(const Kv4Args& a, int R, int runs, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = s;
-    cfg.gridDim = dim3(unsigned(runs), unsigned((R + kJoinRows - 1) / kJoinRows));
+    const bool share = R <= 16;
+    cfg.gridDim = dim3(unsigned(runs), unsigned(share ? R : R / kJoinRows));
     cfg.blockDim = dim3(kJoinRows * 32);
-    return a.p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<64>, a, R) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<128>, a, R);
+    if (a.p.head_dim == 64)
+        return share ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<64, true>, a, R) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<64, false>, a, R);
+    return share ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<128, true>, a, R) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<128, false>, a, R);
 }
 
 size_t kv4_attention_workspace(const mmq_kv4_attention_t& p) {

@@ -12,11 +12,11 @@
 //   warps 0-3, 4-7  softmax groups 0 and 1, thread = row (its tensor-memory
 //                   lane): read S, keep the row's maximum and sum, write P over
 //                   S, now and then scale O
-//   warps 8-11      expand raw tiles to operand tiles (128-byte swizzle): keys
-//                   [key][dimension], values transposed, [dimension][key]
-//   warp 12         fetches raw tiles: 8 bulk copies for 128 keys' half
-//   warps 13, 14    MMA issuers of groups 0 and 1
-//   warp 15         tells the others which pieces of units their run has
+//   warps 8-11      expand raw keys to operand tiles (128-byte swizzle), [key][dimension]
+//   warps 12-15     and raw values, transposed, [dimension][key]
+//   warp 16         fetches raw tiles: 8 bulk copies for 128 keys' half
+//   warps 17, 18    MMA issuers of groups 0 and 1
+//   warp 19         tells the others which pieces of units their run has
 // Runs of equal length of all units' key tiles are the CTAs' work, as in the
 // few-row kernel; the parts of units that lie in several runs are joined by a
 // second kernel.  kTwo: 256 rows to a unit, both groups share each key tile,
@@ -39,11 +39,11 @@ using namespace mmq::tc;
 using namespace mmq::kv4;
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kThreads = 512;
-constexpr int kWarpExpand = 8, kWarpFetch = 12, kWarpMma = 13;   // and kWarpMma + 1
-// Registers: 128 per thread at launch (the launcher checks it): 256 x 200 + 128 x 72 + 128 x 40 = 512 x 128.
-constexpr uint32_t kRegsLaunch = 128, kRegsSoftmax = 200, kRegsExpand = 72, kRegsOther = 40;
-static_assert(256 * kRegsSoftmax + 128 * kRegsExpand + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr int kThreads = 640;
+constexpr int kWarpExpand = 8, kWarpFetch = 16, kWarpMma = 17;   // and kWarpMma + 1; four expand keys, four values
+// Registers: 96 per thread at launch (the launcher checks it): 256 x 128 + 256 x 80 + 128 x 64 = 640 x 96.
+constexpr uint32_t kRegsLaunch = 96, kRegsSoftmax = 128, kRegsExpand = 80, kRegsOther = 64;
+static_assert(256 * kRegsSoftmax + 256 * kRegsExpand + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S_g at 128 g (P_g over its first 64 columns), O_g at 256 + 128 g
 constexpr float kGrow = 8.f, kLift = 7.f;    // P at most 2^15
@@ -131,7 +131,7 @@ struct Layout {
     static constexpr int kOffSlots = 2 * kTile;
     static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
     static constexpr int kOffSums = kOffRaw + kRawSlots * kRaw;
-    static constexpr int kOffStart = kOffSums + 16 * 8;
+    static constexpr int kOffStart = kOffSums + (kThreads / 32) * 8;
     static constexpr int kOffPieces = kOffStart + 2 * int(sizeof(Start));
     static constexpr int kOffBar = kOffPieces + 2 * kPieces * int(sizeof(Piece));
     // barriers: raw_full, raw_empty; full, empty per slot; q_full, s_full, p_full, o_full, turn per group; drain;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         for (int st = 0; st < kStreams; ++st)
             for (int i = 0; i < kPieces; ++i) {
                 mbar_init(told(st, i), 1);
-                mbar_init(done_with(st, i), kTwo ? 1 + 4 + 2 + 8 : 1 + 4 + 1 + 4);   // fetch, expand, MMA, softmax
+                mbar_init(done_with(st, i), kTwo ? 1 + 8 + 2 + 8 : 1 + 8 + 1 + 4);   // fetch, expand, MMA, softmax
             }
         abort_flag.set(0u);
         no_number.set(0u);
@@ -339,82 +339,89 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         setmaxnreg_dec<kRegsExpand>();
         Ring<kRawSlots> raw;
         uint32_t tile_no[2] = {0, 0};   // tiles of each stream so far
-        // Thread: tile of 16 tokens, a row of eight in it (tokens r, r + 8 of keys, dimensions r, r + 8 of 16
-        // of values), and the blocks of 16 dimensions of every second (or the one) 64.
-        constexpr int kJ = D / 32;
-        const int id = threadIdx.x - kWarpExpand * 32;
+        // Thread: tile of 16 tokens, a row of eight in it (tokens r, r + 8 of keys, dimensions r, r + 8 of 16 of
+        // values), and the blocks of 16 dimensions of every second (or the one) 64.  A block's four words there give
+        // four 16-byte chunks: the lower nibbles, the upper, and both after a shift by 8.
+        constexpr int kJ = D / 32, kG = D / 64;   // blocks of 16 and of 32 dimensions
+        const bool values = warp >= kWarpExpand + 4;
+        const int id = threadIdx.x & 127;
         const int tile = id >> 4, r = id & 7, part = (id >> 3) & 1;
         const uint32_t words = uint32_t(tile * 9 * D + r * 64) + (D == 128 ? part * 512u : part * 8u);
+        const uint32_t scales = uint32_t(tile * 9 * D + 8 * D) + (values ? uint32_t(part * kG * 8) : uint32_t(r * (D / 8)) + (D == 128 ? 4u * part : 0u));
+        // Keys: blocks along the row, shift by 8 rows.  Values: blocks by 16 rows, upper nibbles 8 rows on.
+        const uint32_t row0 = values ? uint32_t((tile >> 2) * (D * 128) + (16 * part * kJ + r) * 128)
+                                     : uint32_t((D == 128 ? part * kKeys * 128 : 0) + (tile * 16 + r) * 128);
         jobs([&](int st, int kind, const Piece& q, int t) {
-            const uint32_t no = tile_no[st];
+            if ((kind == 1) != values) {
+                raw.next();
+                return true;
+            }
+            const uint32_t no = tile_no[st]++;
             const int slot = slot_of(st, kind, no);
-            if (kind == 1) ++tile_no[st];
             if (!__all_sync(0xffffffffu, wait_bounded(raw_full(raw.slot), raw.phase, abort_flag, status) &&
                                              wait_bounded(empty(slot), phase_of(no) ^ 1u, abort_flag, status)))
                 return false;
             const uint32_t raw_at = sbase + uint32_t(L::kOffRaw + raw.slot * L::kRaw);
-            const uint32_t to = sbase + uint32_t(L::kOffSlots + slot * L::kTile);
-            uint32_t w[4][kJ];
+            const uint32_t to = sbase + uint32_t(L::kOffSlots + slot * L::kTile) + row0;
+            uint32_t w[4][kJ], sc[kG][4][2];   // sc: of the lower and the upper tokens, for each word
 #pragma unroll
             for (int c = 0; c < 4; ++c) ld_shared_words<kJ>(raw_at + words + 16u * c, w[c]);
-            if (kind == 0) {
-                uint32_t ks[2][kJ / 2];   // tokens r, r + 8: this part's blocks of 32, two to a word
-                const uint32_t at = raw_at + uint32_t(tile * 9 * D + key_scales(D) + r * (D / 8));
-                if (D == 128) {
-                    ks[0][0] = ld_shared_u32(at + 4u * part);
-                    ks[1][0] = ld_shared_u32(at + 8u + 4u * part);
-                } else {
-                    ks[0][0] = ld_shared_u32(at);
-                    ks[1][0] = ld_shared_u32(at + 4u);
-                }
-                const uint32_t row = uint32_t(tile * 16 + r) * 128u;
+            if (values) {
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) {
-                    const int i = part * kJ + j;
-                    // block i / 2 of 32: 2 part, 2 part + 1 of D = 128, part of D = 64
-                    const uint32_t sel = D == 128 ? (j >> 1 ? 0x3232u : 0x1010u) : (part ? 0x3232u : 0x1010u);
-                    const uint32_t d0 = prmt(ks[0][0], 0u, sel), d1 = prmt(ks[1][0], 0u, sel);
-                    const uint32_t dst = to + uint32_t(i >> 2) * (kKeys * 128) + row;
-                    const uint32_t c0 = uint32_t((2 * (i & 3)) ^ r) << 4, c1 = uint32_t((2 * (i & 3) + 1) ^ r) << 4;
-                    st_shared_v4(dst + c0, expand_low(w[0][j], d0), expand_low(w[1][j], d0), expand_low(w[2][j], d0), expand_low(w[3][j], d0));
-                    st_shared_v4(dst + c1, expand_high(w[0][j], d0), expand_high(w[1][j], d0), expand_high(w[2][j], d0), expand_high(w[3][j], d0));
-                    st_shared_v4(dst + 1024u + c0, expand_low(w[0][j] >> 8, d1), expand_low(w[1][j] >> 8, d1), expand_low(w[2][j] >> 8, d1), expand_low(w[3][j] >> 8, d1));
-                    st_shared_v4(dst + 1024u + c1, expand_high(w[0][j] >> 8, d1), expand_high(w[1][j] >> 8, d1), expand_high(w[2][j] >> 8, d1), expand_high(w[3][j] >> 8, d1));
-                }
-            } else {
-                constexpr int kG = D == 128 ? 2 : 1;    // blocks of 32 dimensions here
-                uint32_t vs[4][kG][2];                  // tokens 2 c, 2 c + 1 and those + 8
+                for (int c = 0; c < 4; ++c) {   // tokens 2 c, 2 c + 1 and those + 8
+                    uint32_t v[2 * kG];
+                    ld_shared_words<2 * kG>(raw_at + scales + uint32_t(c * (D / 4)), v);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    ld_shared_words<2 * kG>(raw_at + uint32_t(tile * 9 * D + value_scales(D) - value_codes(D) + c * (D / 4) + part * kG * 8), vs[c][0]);
+                    for (int g = 0; g < kG; ++g) {
+                        sc[g][c][0] = v[2 * g];
+                        sc[g][c][1] = v[2 * g + 1];
+                    }
+                }
                 if (t * kKeys + kKeys > q.least) {
-                    // tokens that some rows of the unit do not see: what is no number must not reach those,
-                    // and what lies past the last must reach none
+                    // tokens that some rows of the unit do not see: what is no number must not reach those, and what
+                    // lies past the last must reach none
                     const int left = q.most - (t * kKeys + tile * 16);
+                    bool none = false;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int token = 2 * c + (k & 1) + (k & 2 ? 8 : 0);
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
                             for (int g = 0; g < kG; ++g) {
-                                const uint32_t v = vs[c][g][k >> 1], bits = k & 1 ? v >> 16 : v & 0xFFFFu;
-                                if (token >= left || !finite16(bits)) vs[c][g][k >> 1] = v & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u);
-                                if (token < left && !finite16(bits)) no_number.set(1u);
+                                const bool past = 2 * c + (k & 1) + (k & 2 ? 8 : 0) >= left;
+                                uint32_t& v = sc[g][c][k >> 1];
+                                const bool good = finite16(k & 1 ? v >> 16 : v);
+                                if (past || !good) v &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                                none |= !past && !good;
                             }
-                        }
+                    if (none) no_number.set(1u);
                 }
-                const uint32_t col = uint32_t(tile >> 2) * (D * 128);
-                const uint32_t c0 = uint32_t((2 * (tile & 3)) ^ r) << 4, c1 = uint32_t((2 * (tile & 3) + 1) ^ r) << 4;
+            } else {
+                // tokens r and r + 8: this part's blocks of 32, two to a word (D = 128), or the part's of the two
+                const uint32_t lo = ld_shared_u32(raw_at + scales), hi = ld_shared_u32(raw_at + scales + (D == 128 ? 8u : 4u));
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) {
-                    const int i = part * kJ + j, g = j >> 1;
-                    const uint32_t dst = to + col + uint32_t(16 * i + r) * 128u;
-                    st_shared_v4(dst + c0, expand_low(w[0][j], vs[0][g][0]), expand_low(w[1][j], vs[1][g][0]), expand_low(w[2][j], vs[2][g][0]), expand_low(w[3][j], vs[3][g][0]));
-                    st_shared_v4(dst + 1024u + c0, expand_high(w[0][j], vs[0][g][0]), expand_high(w[1][j], vs[1][g][0]), expand_high(w[2][j], vs[2][g][0]), expand_high(w[3][j], vs[3][g][0]));
-                    st_shared_v4(dst + c1, expand_low(w[0][j] >> 8, vs[0][g][1]), expand_low(w[1][j] >> 8, vs[1][g][1]), expand_low(w[2][j] >> 8, vs[2][g][1]), expand_low(w[3][j] >> 8, vs[3][g][1]));
-                    st_shared_v4(dst + 1024u + c1, expand_high(w[0][j] >> 8, vs[0][g][1]), expand_high(w[1][j] >> 8, vs[1][g][1]), expand_high(w[2][j] >> 8, vs[2][g][1]), expand_high(w[3][j] >> 8, vs[3][g][1]));
+                for (int g = 0; g < kG; ++g) {
+                    const uint32_t sel = (D == 128 ? g : part) ? 0x3232u : 0x1010u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        sc[g][c][0] = prmt(lo, 0u, sel);
+                        sc[g][c][1] = prmt(hi, 0u, sel);
+                    }
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                const int g = D == 128 ? j >> 1 : 0;
+                const int chunk = 2 * (values ? tile & 3 : D == 128 ? j : 2 * part + j);
+                const uint32_t at = to + (values ? uint32_t(j * 2048) : 0u);
+                const uint32_t x0 = uint32_t(chunk ^ r) << 4, x1 = uint32_t((chunk + 1) ^ r) << 4;
+                const uint32_t y1 = values ? 1024u + x0 : x1, y2 = values ? x1 : 1024u + x0;
+                st_shared_v4(at + x0, expand_low(w[0][j], sc[g][0][0]), expand_low(w[1][j], sc[g][1][0]), expand_low(w[2][j], sc[g][2][0]), expand_low(w[3][j], sc[g][3][0]));
+                st_shared_v4(at + y1, expand_high(w[0][j], sc[g][0][0]), expand_high(w[1][j], sc[g][1][0]), expand_high(w[2][j], sc[g][2][0]), expand_high(w[3][j], sc[g][3][0]));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c][j] >>= 8;
+                st_shared_v4(at + y2, expand_low(w[0][j], sc[g][0][1]), expand_low(w[1][j], sc[g][1][1]), expand_low(w[2][j], sc[g][2][1]), expand_low(w[3][j], sc[g][3][1]));
+                st_shared_v4(at + 1024u + x1, expand_high(w[0][j], sc[g][0][1]), expand_high(w[1][j], sc[g][1][1]), expand_high(w[2][j], sc[g][2][1]), expand_high(w[3][j], sc[g][3][1]));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -637,26 +644,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 if (!ok) break;
                 s_phase ^= 1u;
                 tc_fence_after();
-                uint32_t s[4][32];
+                // 64 keys at a time: the second half's scores stay for the weights, the first half's are read again.
+                uint32_t s[2][32];
+                auto read = [&](int half) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), s[c]);
+                    for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(ts + uint32_t(64 * half + 32 * c), s[c]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-                if (left < kKeys) {
+                    for (int c = 0; c < 2; ++c) tmem_wait_ld(s[c]);
+                    if (left < 64 * half + 64) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * c + k >= left) s[c][k] = 0xFF800000u;
-                }
-                float x0 = __uint_as_float(s[0][0]), x1 = __uint_as_float(s[1][0]), x2 = __uint_as_float(s[2][0]),
-                      x3 = __uint_as_float(s[3][0]);
+                            for (int k = 0; k < 32; ++k)
+                                if (64 * half + 32 * c + k >= left) s[c][k] = 0xFF800000u;
+                    }
+                };
+                float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    x0 = max3(x0, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
-                    x1 = max3(x1, __uint_as_float(s[1][k]), __uint_as_float(s[1][k + 1]));
-                    x2 = max3(x2, __uint_as_float(s[2][k]), __uint_as_float(s[2][k + 1]));
-                    x3 = max3(x3, __uint_as_float(s[3][k]), __uint_as_float(s[3][k + 1]));
+                for (int half = 0; half < 2; ++half) {
+                    read(half);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        x0 = max3(x0, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
+                        x1 = max3(x1, __uint_as_float(s[0][k + 2]), __uint_as_float(s[0][k + 3]));
+                        x2 = max3(x2, __uint_as_float(s[1][k]), __uint_as_float(s[1][k + 1]));
+                        x3 = max3(x3, __uint_as_float(s[1][k + 2]), __uint_as_float(s[1][k + 3]));
+                    }
                 }
                 const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * scale;
                 const bool rises = top > m + kGrow;
@@ -666,21 +679,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     if (wide) break;
                     m = fmaxf(m, top);
                     if (n > 0) scale_o(ex2(was - m));
+                    read(1);   // scale_o() needs registers
                 }
                 const float base = m - kLift;
                 const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int half = 1; half >= 0; --half) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const uint32_t* sc = &s[2 * half + (k >> 4)][2 * (k & 15)];
+                        const uint32_t* sc = &s[k >> 4][2 * (k & 15)];
                         const uint64_t e = ffma2(pack2u(sc[0], sc[1]), scale2, base2);
                         const float u = ex2(lo_f(e)), v = ex2(hi_f(e));
                         sum[k & 1] = fadd2(sum[k & 1], pack2(u, v));
                         pk[k] = pack16(u, v);
                     }
+                    if (half == 1) read(0);   // before P takes its place
                     tmem_st_32x32b_x32(ts + 32u * uint32_t(half), pk);
                 }
                 tmem_wait_st();
