@@ -14,7 +14,7 @@
 //                   S, now and then scale O
 //   warps 8-11      expand raw keys to operand tiles (128-byte swizzle), [key][dimension]
 //   warps 12-15     and raw values, transposed, [dimension][key]
-//   warp 16         fetches raw tiles: 8 bulk copies for 128 keys' half
+//   warp 16         fetches raw tiles: one to four bulk copies for 64 keys, by the page's size
 //   warps 17, 18    MMA issuers of groups 0 and 1
 //   warp 19         tells the others which pieces of units their run has
 // Runs of equal length of all units' key tiles are the CTAs' work, as in the
@@ -38,20 +38,20 @@ using namespace mmq::ptx;
 using namespace mmq::tc;
 using namespace mmq::kv4;
 
-constexpr int kKeys = 128, kRows = 128;
+constexpr int kKeys = 64, kRows = 128;   // keys of a tile
 constexpr int kThreads = 640;
 constexpr int kWarpExpand = 8, kWarpFetch = 16, kWarpMma = 17;   // and kWarpMma + 1; four expand keys, four values
-// Registers: 96 per thread at launch (the launcher checks it): 256 x 128 + 256 x 80 + 128 x 64 = 640 x 96.
-constexpr uint32_t kRegsLaunch = 96, kRegsSoftmax = 128, kRegsExpand = 80, kRegsOther = 64;
+// Registers: 96 per thread at launch (the launcher checks it): 256 x 144 + 256 x 64 + 128 x 64 = 640 x 96.
+constexpr uint32_t kRegsLaunch = 96, kRegsSoftmax = 144, kRegsExpand = 64, kRegsOther = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsExpand + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // S_g at 128 g (P_g over its first 64 columns), O_g at 256 + 128 g
+constexpr uint32_t kColS = 0, kColO = 256;   // S_g at 128 g and 64 on, in turn (P over its first 32 columns), O_g at 256 + 128 g
 constexpr float kGrow = 8.f, kLift = 7.f;    // P at most 2^15
 constexpr float kNone = -3.402823466e38f;    // the maximum before any score
 constexpr float kWide = 0x1p20f;
 __device__ __forceinline__ float reference(float m) { return fabsf(m) < kWide ? m - kLift : m; }
 
-__device__ __align__(16) const uint8_t zero_tile[tile_bytes(128)] = {};   // of a page that does not exist
+__device__ __align__(16) const uint8_t zero_tiles[kKeys / kTokens * tile_bytes(128)] = {};   // of a page that does not exist
 
 // Where a run starts: tile t of unit u of head h of sequence b, and its length.
 struct Start {
@@ -122,21 +122,22 @@ constexpr int kPieces = 4;           // told ahead
 template <int D, bool kTwo>
 struct Layout {
     static constexpr int kStreams = kTwo ? 1 : 2;
-    static constexpr int kTile = kKeys * D * 2;              // of keys, values or queries as fp16
-    static constexpr int kSlots = 512 / D;
+    static constexpr int kTile = kKeys * D * 2;              // of keys or values as fp16
+    static constexpr int kQ = kRows * D * 2;
+    static constexpr int kSlots = 1024 / D;
     static constexpr int kBufs = kSlots / 2 / kStreams;      // per stream, of keys and of values
-    static constexpr int kRaw = 8 * 9 * D;                   // 128 keys or values in 4 bits
+    static constexpr int kRaw = kKeys / kTokens * tile_bytes(D);   // a tile's keys and values in 4 bits
     static constexpr int kRawSlots = 384 / D;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffSlots = 2 * kTile;
+    static constexpr int kOffSlots = 2 * kQ;
     static constexpr int kOffRaw = kOffSlots + kSlots * kTile;
     static constexpr int kOffSums = kOffRaw + kRawSlots * kRaw;
     static constexpr int kOffStart = kOffSums + (kThreads / 32) * 8;
     static constexpr int kOffPieces = kOffStart + 2 * int(sizeof(Start));
     static constexpr int kOffBar = kOffPieces + 2 * kPieces * int(sizeof(Piece));
-    // barriers: raw_full, raw_empty; full, empty per slot; q_full, s_full, p_full, o_full, turn per group; drain;
-    // told, done per piece
-    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 11 + 4 * kPieces) * 8;
+    // barriers: raw_full, raw_empty; full, empty per slot; q_full, o_done per group, s_full, p_full per group and
+    // buffer; drain; told, done per piece
+    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 13 + 4 * kPieces) * 8;
     static constexpr int kBytes = kOffMisc + 32 + 1024;
     static constexpr int kR = kTwo ? 2 * kRows : kRows;      // rows of a unit
 };
@@ -171,12 +172,8 @@ __device__ __forceinline__ uint32_t expand_high(uint32_t v, uint32_t scales) {
 }
 template <int N>
 __device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t* w) {
-    if (N == 4) {
-        const uint4 v = ld_shared_v4(addr);
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-    }
+    if (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    else w[0] = ld_shared_u32(addr);
 }
 
 template <typename T, int D, bool kTwo>
@@ -193,12 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     auto empty = [&](int s) { return bar0 + 8u * uint32_t(2 * kRawSlots + kSlots + s); };
     const uint32_t bar1 = bar0 + 8u * uint32_t(2 * kRawSlots + 2 * kSlots);
     auto q_full = [&](int g) { return bar1 + 8u * uint32_t(g); };
-    auto s_full = [&](int g) { return bar1 + 8u * uint32_t(2 + g); };
-    auto o_full = [&](int g) { return bar1 + 8u * uint32_t(4 + g); };
-    auto p_full = [&](int g) { return bar1 + 8u * uint32_t(6 + g); };
-    auto turn = [&](int g) { return bar1 + 8u * uint32_t(8 + g); };
-    const uint32_t drain = bar1 + 8u * 10u;
-    auto told = [&](int st, uint32_t i) { return bar1 + 8u * (11u + uint32_t(st * kPieces) + i % kPieces); };
+    auto o_done = [&](int g) { return bar1 + 8u * uint32_t(2 + g); };
+    auto s_full = [&](int g, uint32_t no) { return bar1 + 8u * (4u + 2u * uint32_t(g) + (no & 1u)); };
+    auto p_full = [&](int g, uint32_t no) { return bar1 + 8u * (8u + 2u * uint32_t(g) + (no & 1u)); };
+    const uint32_t drain = bar1 + 8u * 12u;
+    auto told = [&](int st, uint32_t i) { return bar1 + 8u * (13u + uint32_t(st * kPieces) + i % kPieces); };
     auto done_with = [&](int st, uint32_t i) { return told(st, i) + 8u * 2u * kPieces; };
     Piece* const pieces = reinterpret_cast<Piece*>(smem + L::kOffPieces);
     auto piece_at = [&](int st, uint32_t i) -> Piece& { return pieces[st * kPieces + int(i % kPieces)]; };
@@ -214,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRawSlots; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_empty(s), 4);
+            mbar_init(raw_empty(s), 8);
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(full(s), 4);
@@ -222,10 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(q_full(g), 4);
-            mbar_init(s_full(g), 1);
-            mbar_init(p_full(g), 4);
-            mbar_init(o_full(g), 1);
-            mbar_init(turn(g), 1);
+            mbar_init(o_done(g), 1);
+            for (uint32_t i = 0; i < 2; ++i) {
+                mbar_init(s_full(g, i), 1);
+                mbar_init(p_full(g, i), 4);
+            }
         }
         mbar_init(drain, 2);
         for (int st = 0; st < kStreams; ++st)
@@ -297,86 +294,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
 
     // Piece i of stream st, once it is told; false after a wait that ran out.
     auto await_piece = [&](int st, uint32_t i) { return wait_bounded(told(st, i), (i / kPieces) & 1u, abort_flag, status); };
-    // A warp's tiles in the order K, V (kTwo) or K of both streams, V of both; job(stream, kind, piece, tile).
-    auto jobs = [&](auto&& job) {
-        uint32_t no[kStreams] = {};
-        int t[kStreams];
-        bool live[kStreams], any = false, ok = true;
-        auto load = [&](int st) {
-            ok = __all_sync(0xffffffffu, await_piece(st, no[st]));
-            const Piece& q = piece_at(st, no[st]);
-            live[st] = ok && q.t0 < q.t1;
-            t[st] = q.t0;
-        };
-#pragma unroll
-        for (int st = 0; st < kStreams; ++st) {
-            load(st);
-            if (!ok) return;
-            any |= live[st];
-        }
-        while (any) {
-#pragma unroll 1
-            for (int kind = 0; kind < 2; ++kind)
-#pragma unroll 1
-                for (int st = 0; st < kStreams; ++st)
-                    if (live[st] && !job(st, kind, piece_at(st, no[st]), t[st])) return;
-            any = false;
-#pragma unroll
-            for (int st = 0; st < kStreams; ++st) {
-                if (live[st] && ++t[st] == piece_at(st, no[st]).t1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(done_with(st, no[st]));
-                    ++no[st];
-                    load(st);
-                    if (!ok) return;
-                }
-                any |= live[st];
-            }
-        }
+    // A warp's way through the streams' tiles, a tile of each per step.  (No arrays: they would lie in local memory.)
+    struct Place {
+        uint32_t piece = 0, no = 0;   // pieces and tiles before
+        int t = 0;
+        bool live = false;
     };
+    Place one, two;
+    uint32_t raw_no = 0;              // raw tiles before this step
+    auto load = [&](int st, Place& at) {   // the next piece
+        if (!__all_sync(0xffffffffu, await_piece(st, at.piece))) return false;
+        const Piece& q = piece_at(st, at.piece);
+        at.live = q.t0 < q.t1;
+        at.t = q.t0;
+        return true;
+    };
+    auto begin = [&]() { return load(0, one) && (kTwo || load(1, two)); };
+    auto advance = [&](int st, Place& at) {
+        if (!at.live) return true;
+        ++at.no;
+        if (++at.t < piece_at(st, at.piece).t1) return true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done_with(st, at.piece));
+        ++at.piece;
+        return load(st, at);
+    };
+    auto step = [&]() {
+        raw_no += uint32_t(one.live) + uint32_t(two.live);
+        return advance(0, one) && (kTwo || advance(1, two));
+    };
+    auto more = [&]() { return one.live || two.live; };
+    auto raw_of = [&](int st) { return raw_no + (st ? uint32_t(one.live) : 0u); };   // of stream st in this step
+    auto raw_slot = [&](uint32_t i) { return int(i % uint32_t(kRawSlots)); };
+    auto raw_phase = [&](uint32_t i) { return (i / uint32_t(kRawSlots)) & 1u; };
     if (warp >= kWarpExpand && warp < kWarpFetch) {
         // ------------------------------------------------------------ expand
         setmaxnreg_dec<kRegsExpand>();
-        Ring<kRawSlots> raw;
-        uint32_t tile_no[2] = {0, 0};   // tiles of each stream so far
-        // Thread: tile of 16 tokens, a row of eight in it (tokens r, r + 8 of keys, dimensions r, r + 8 of 16 of
-        // values), and the blocks of 16 dimensions of every second (or the one) 64.  A block's four words there give
-        // four 16-byte chunks: the lower nibbles, the upper, and both after a shift by 8.
-        constexpr int kJ = D / 32, kG = D / 64;   // blocks of 16 and of 32 dimensions
+        // Thread: tile of 16 tokens (one per warp), a row of eight in it (tokens r, r + 8 of keys, dimensions r, r + 8 of
+        // 16 of values), and a quarter of the dimensions.  A block of 16's four words there give four 16-byte chunks: the
+        // lower nibbles, the upper, and both after a shift by 8.
+        constexpr int kJ = D / 64;   // blocks of 16 dimensions
         const bool values = warp >= kWarpExpand + 4;
-        const int id = threadIdx.x & 127;
-        const int tile = id >> 4, r = id & 7, part = (id >> 3) & 1;
-        const uint32_t words = uint32_t(tile * 9 * D + r * 64) + (D == 128 ? part * 512u : part * 8u);
-        const uint32_t scales = uint32_t(tile * 9 * D + 8 * D) + (values ? uint32_t(part * kG * 8) : uint32_t(r * (D / 8)) + (D == 128 ? 4u * part : 0u));
+        const uint32_t scratch = sbase + uint32_t(L::kOffMisc + 16 + 4 * (warp & 3));
+        const int tile = warp & 3, r = lane & 7, part = lane >> 3;
+        const int block32 = D == 128 ? part : part >> 1;
+        const uint32_t half = uint32_t(tile * tile_bytes(D) + (values ? value_codes(D) : 0));
+        const uint32_t words = half + uint32_t(r * 64) + (D == 128 ? (part >> 1) * 512u + (part & 1) * 8u : part * 4u);
+        const uint32_t scales = half + uint32_t(8 * D) + (values ? uint32_t(block32 * 8) : uint32_t(r * (D / 8) + 4 * (block32 >> 1)));
         // Keys: blocks along the row, shift by 8 rows.  Values: blocks by 16 rows, upper nibbles 8 rows on.
-        const uint32_t row0 = values ? uint32_t((tile >> 2) * (D * 128) + (16 * part * kJ + r) * 128)
-                                     : uint32_t((D == 128 ? part * kKeys * 128 : 0) + (tile * 16 + r) * 128);
-        jobs([&](int st, int kind, const Piece& q, int t) {
-            if ((kind == 1) != values) {
-                raw.next();
-                return true;
-            }
-            const uint32_t no = tile_no[st]++;
-            const int slot = slot_of(st, kind, no);
-            if (!__all_sync(0xffffffffu, wait_bounded(raw_full(raw.slot), raw.phase, abort_flag, status) &&
-                                             wait_bounded(empty(slot), phase_of(no) ^ 1u, abort_flag, status)))
-                return false;
-            const uint32_t raw_at = sbase + uint32_t(L::kOffRaw + raw.slot * L::kRaw);
+        const uint32_t row0 = values ? uint32_t((16 * part * kJ + r) * 128)
+                                     : uint32_t((D == 128 ? (part >> 1) * kKeys * 128 : 0) + (tile * 16 + r) * 128);
+        auto expand = [&](int st, const Place& place) {
+            const Piece& q = piece_at(st, place.piece);
+            const int t = place.t;
+            const uint32_t raw = raw_of(st);
+            const int slot = slot_of(st, values, place.no), raw_at_slot = raw_slot(raw);
+            if (!__all_sync(0xffffffffu, wait_bounded(raw_full(raw_at_slot), raw_phase(raw), abort_flag, status))) return false;
+            const uint32_t raw_at = sbase + uint32_t(L::kOffRaw + raw_at_slot * L::kRaw);
             const uint32_t to = sbase + uint32_t(L::kOffSlots + slot * L::kTile) + row0;
-            uint32_t w[4][kJ], sc[kG][4][2];   // sc: of the lower and the upper tokens, for each word
+            uint32_t w[4][kJ], sc[4][2];   // sc: of the lower and the upper tokens, for each word
+            // Word c of rows r is at 64 r + 16 c: lane r takes them from r / 2 on, so that eight lanes hit all banks.
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ld_shared_words<kJ>(raw_at + words + 16u * c, w[c]);
+            for (int c = 0; c < 4; ++c) ld_shared_words<kJ>(raw_at + words + ((16u * c + 8u * uint32_t(r & 6)) & 48u), w[c]);
             if (values) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {   // tokens 2 c, 2 c + 1 and those + 8
-                    uint32_t v[2 * kG];
-                    ld_shared_words<2 * kG>(raw_at + scales + uint32_t(c * (D / 4)), v);
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) {
-                        sc[g][c][0] = v[2 * g];
-                        sc[g][c][1] = v[2 * g + 1];
-                    }
-                }
+                for (int c = 0; c < 4; ++c)   // tokens 2 c, 2 c + 1 and those + 8
+                    ld_shared_words<2>(raw_at + scales + uint32_t(c * (D / 4)), sc[c]);
                 if (t * kKeys + kKeys > q.least) {
                     // tokens that some rows of the unit do not see: what is no number must not reach those, and what
                     // lies past the last must reach none
@@ -385,88 +368,123 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int g = 0; g < kG; ++g) {
-                                const bool past = 2 * c + (k & 1) + (k & 2 ? 8 : 0) >= left;
-                                uint32_t& v = sc[g][c][k >> 1];
-                                const bool good = finite16(k & 1 ? v >> 16 : v);
-                                if (past || !good) v &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                                none |= !past && !good;
-                            }
+                        for (int k = 0; k < 4; ++k) {
+                            const bool past = 2 * c + (k & 1) + (k & 2 ? 8 : 0) >= left;
+                            uint32_t& v = sc[c][k >> 1];
+                            const bool good = finite16(k & 1 ? v >> 16 : v);
+                            if (past || !good) v &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            none |= !past && !good;
+                        }
                     if (none) no_number.set(1u);
                 }
             } else {
-                // tokens r and r + 8: this part's blocks of 32, two to a word (D = 128), or the part's of the two
-                const uint32_t lo = ld_shared_u32(raw_at + scales), hi = ld_shared_u32(raw_at + scales + (D == 128 ? 8u : 4u));
+                // tokens r and r + 8: two blocks of 32 to a word
+                const uint32_t lo = ld_shared_u32(raw_at + scales), hi = ld_shared_u32(raw_at + scales + uint32_t(D / 16));
+                const uint32_t sel = block32 & 1 ? 0x3232u : 0x1010u;
 #pragma unroll
-                for (int g = 0; g < kG; ++g) {
-                    const uint32_t sel = (D == 128 ? g : part) ? 0x3232u : 0x1010u;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        sc[g][c][0] = prmt(lo, 0u, sel);
-                        sc[g][c][1] = prmt(hi, 0u, sel);
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    sc[c][0] = prmt(lo, 0u, sel);
+                    sc[c][1] = prmt(hi, 0u, sel);
                 }
+            }
+            // all loads are back (each is in the sum) before the raw slot is handed on
+            loads_done(scratch, sc[0][0] ^ sc[0][1] ^ sc[1][0] ^ sc[2][0] ^ sc[3][0] ^ w[0][0] ^ w[1][0] ^ w[2][0] ^ w[3][0]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_empty(raw_at_slot));
+            if (!__all_sync(0xffffffffu, wait_bounded(empty(slot), phase_of(place.no) ^ 1u, abort_flag, status))) return false;
+            // words back in order: w[c] is word c + r / 2
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                const uint32_t a0 = w[0][j], a1 = w[1][j], a2 = w[2][j], a3 = w[3][j];
+                const bool one = r & 2, two = r & 4;
+                const uint32_t b0 = one ? a3 : a0, b1 = one ? a0 : a1, b2 = one ? a1 : a2, b3 = one ? a2 : a3;
+                w[0][j] = two ? b2 : b0;
+                w[1][j] = two ? b3 : b1;
+                w[2][j] = two ? b0 : b2;
+                w[3][j] = two ? b1 : b3;
             }
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-                const int g = D == 128 ? j >> 1 : 0;
-                const int chunk = 2 * (values ? tile & 3 : D == 128 ? j : 2 * part + j);
+                const int chunk = 2 * (values ? tile : (part * kJ + j) & 3);
                 const uint32_t at = to + (values ? uint32_t(j * 2048) : 0u);
                 const uint32_t x0 = uint32_t(chunk ^ r) << 4, x1 = uint32_t((chunk + 1) ^ r) << 4;
                 const uint32_t y1 = values ? 1024u + x0 : x1, y2 = values ? x1 : 1024u + x0;
-                st_shared_v4(at + x0, expand_low(w[0][j], sc[g][0][0]), expand_low(w[1][j], sc[g][1][0]), expand_low(w[2][j], sc[g][2][0]), expand_low(w[3][j], sc[g][3][0]));
-                st_shared_v4(at + y1, expand_high(w[0][j], sc[g][0][0]), expand_high(w[1][j], sc[g][1][0]), expand_high(w[2][j], sc[g][2][0]), expand_high(w[3][j], sc[g][3][0]));
+                st_shared_v4(at + x0, expand_low(w[0][j], sc[0][0]), expand_low(w[1][j], sc[1][0]), expand_low(w[2][j], sc[2][0]), expand_low(w[3][j], sc[3][0]));
+                st_shared_v4(at + y1, expand_high(w[0][j], sc[0][0]), expand_high(w[1][j], sc[1][0]), expand_high(w[2][j], sc[2][0]), expand_high(w[3][j], sc[3][0]));
 #pragma unroll
                 for (int c = 0; c < 4; ++c) w[c][j] >>= 8;
-                st_shared_v4(at + y2, expand_low(w[0][j], sc[g][0][1]), expand_low(w[1][j], sc[g][1][1]), expand_low(w[2][j], sc[g][2][1]), expand_low(w[3][j], sc[g][3][1]));
-                st_shared_v4(at + 1024u + x1, expand_high(w[0][j], sc[g][0][1]), expand_high(w[1][j], sc[g][1][1]), expand_high(w[2][j], sc[g][2][1]), expand_high(w[3][j], sc[g][3][1]));
+                st_shared_v4(at + y2, expand_low(w[0][j], sc[0][1]), expand_low(w[1][j], sc[1][1]), expand_low(w[2][j], sc[2][1]), expand_low(w[3][j], sc[3][1]));
+                st_shared_v4(at + 1024u + x1, expand_high(w[0][j], sc[0][1]), expand_high(w[1][j], sc[1][1]), expand_high(w[2][j], sc[2][1]), expand_high(w[3][j], sc[3][1]));
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(full(slot));
-                mbar_arrive(raw_empty(raw.slot));   // the stores above have taken what was loaded
-            }
-            raw.next();
+            if (lane == 0) mbar_arrive(full(slot));
             return true;
-        });
+        };
+        bool ok = begin();
+        while (ok && more()) {
+#pragma unroll 1
+            for (int st = 0; st < kStreams && ok; ++st) {
+                const Place& place = !kTwo && st ? two : one;
+                const Place copy = place;
+                if (copy.live) ok = expand(st, copy);
+            }
+            ok = ok && step();
+        }
     } else if (warp >= kWarpFetch) {
         setmaxnreg_dec<kRegsOther>();
         if (warp == kWarpFetch) {
             // ------------------------------------------------------ raw tiles
-            Ring<kRawSlots> raw;
             uint32_t issued = 0, parity = 0;   // slots with a copy, the parity of its arrival
             bool withhold = a.inject && blockIdx.x == 0;
-            const uint8_t* src[kStreams];
             const int tile_shift = a.page_shift - 4;
-            jobs([&](int st, int kind, const Piece& q, int t) {
-                if (kind == 0) {
-                    src[st] = zero_tile;
-                    const int tile = 8 * t + lane;
-                    if (lane < 8 && tile * kTokens < q.most) {
-                        const int32_t id = p.page_table[int64_t(q.b) * p.table_width + (tile >> tile_shift)];
-                        if (id < 0 || id >= p.n_pages) atomicCAS(status, 0, MMQ_ERR_ARG);
-                        else
-                            src[st] = p.cache + (((int64_t(id) * p.kv_heads + q.h) << tile_shift) +
-                                                 (tile & ((1 << tile_shift) - 1))) * tile_bytes(D);
-                    }
-                }
-                if (!__all_sync(0xffffffffu, wait_bounded(raw_empty(raw.slot), raw.phase ^ 1u, abort_flag, status))) return false;
+            constexpr int kOf = kKeys / kTokens;   // tiles of 16
+            // A copy takes as many of a key tile's tiles of 16 as lie on one page, up to all; lane i issues the i-th.
+            const int of_page = min(kOf, 1 << tile_shift), copies = kOf / of_page;
+            const uint32_t bytes = uint32_t(of_page * tile_bytes(D)), into = uint32_t(lane) * bytes;
+            // The page of this lane's copy, looked up a step ahead; what lies past the unit's keys is no page.
+            auto page_of = [&](int st, const Place& at) {
+                if (!at.live) return -1;
+                const Piece& q = piece_at(st, at.piece);
+                const int tile = kOf * at.t + of_page * lane;
+                return lane < copies && tile * kTokens < q.most ? p.page_table[int64_t(q.b) * p.table_width + (tile >> tile_shift)] : -1;
+            };
+            auto place_of = [&](int st, const Place& at, int32_t id) -> const uint8_t* {
+                const Piece& q = piece_at(st, at.piece);
+                const int tile = kOf * at.t + of_page * lane;
+                if (id >= 0 && id < p.n_pages)
+                    return p.cache + (((int64_t(id) * p.kv_heads + q.h) << tile_shift) + (tile & ((1 << tile_shift) - 1))) * tile_bytes(D);
+                if (lane < copies && tile * kTokens < q.most) atomicCAS(status, 0, MMQ_ERR_ARG);
+                return zero_tiles;
+            };
+            auto copy = [&](const uint8_t* src, uint32_t i) {
+                const int slot = raw_slot(i);
+                if (!__all_sync(0xffffffffu, wait_bounded(raw_empty(slot), raw_phase(i) ^ 1u, abort_flag, status))) return false;
                 if (!withhold) {
-                    if (lane == 0) mbar_arrive_expect_tx(raw_full(raw.slot), uint32_t(L::kRaw));
+                    if (lane == 0) mbar_arrive_expect_tx(raw_full(slot), uint32_t(L::kRaw));
                     __syncwarp();
-                    if (lane < 8)
-                        bulk_load(sbase + uint32_t(L::kOffRaw + raw.slot * L::kRaw + lane * 9 * D),
-                                  src[st] + (kind ? value_codes(D) : 0), 9 * D, raw_full(raw.slot));
-                    issued |= 1u << raw.slot;
-                    parity = (parity & ~(1u << raw.slot)) | (raw.phase << raw.slot);
+                    if (lane < copies) bulk_load(sbase + uint32_t(L::kOffRaw + slot * L::kRaw) + into, src, bytes, raw_full(slot));
+                    issued |= 1u << slot;
+                    parity = (parity & ~(1u << slot)) | (raw_phase(i) << slot);
                 }
                 withhold = false;
-                raw.next();
                 return true;
-            });
+            };
+            bool ok = begin();
+            int32_t id0 = ok ? page_of(0, one) : -1, id1 = ok && !kTwo ? page_of(1, two) : -1;
+            while (ok && more()) {
+                const uint8_t* src0 = one.live ? place_of(0, one, id0) : zero_tiles;
+                const uint8_t* src1 = two.live ? place_of(1, two, id1) : zero_tiles;
+                const bool has0 = one.live, has1 = two.live;
+                const uint32_t raw0 = raw_of(0), raw1 = raw_of(1);
+                ok = step();
+                if (ok) {
+                    id0 = page_of(0, one);
+                    if (!kTwo) id1 = page_of(1, two);
+                }
+                // (a piece that has been stepped past is not looked at again)
+                ok = (!has0 || copy(src0, raw0)) && (!has1 || copy(src1, raw1)) && ok;
+            }
             // copies still in flight, also after a wait that ran out
             if (lane == 0)
                 for (int s = 0; s < kRawSlots; ++s)
@@ -477,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 const int g = warp - kWarpMma, st = kTwo ? 0 : g;
                 constexpr uint32_t kIdQK = idesc_f16_f32(kRows, kKeys), kIdPV = idesc_f16_f32(kRows, D);
                 constexpr uint64_t kTileDesc = uint64_t(L::kTile >> 4);
-                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kTile));
+                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kQ));
                 const uint64_t slots = smem_desc_sw128(sbase + uint32_t(L::kOffSlots));
                 const uint32_t ts = tmem + kColS + 128u * uint32_t(g), to = tmem + kColO + 128u * uint32_t(g);
                 auto arrived = [&](int kind, uint32_t no) {
@@ -490,57 +508,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     asm volatile("" : "+l"(d));
                     return d;
                 };
-                // S = Q K^T with tile `no` of keys, which has arrived
-                auto scores = [&](uint32_t no, bool pass) {
-                    const int slot = slot_of(st, 0, no);
+                uint32_t no = 0;   // tiles so far, the buffer of S in turn
+                // S = Q K^T with tile i of keys, once it is there
+                auto scores = [&](uint32_t i) {
+                    if (!arrived(0, i)) return false;
+                    tc_fence_after();
+                    const int slot = slot_of(st, 0, i);
                     const uint64_t dk = described(slots + uint64_t(slot) * kTileDesc), dq_now = described(dq);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = uint64_t(kk >> 2) * uint64_t(kKeys * 128 >> 4) + uint64_t((kk & 3) * 2);
-                        if (kTwo && kk == D / 16 - 2 && pass) mbar_arrive(turn(g ^ 1));   // the other thread needs a moment
-                        mma_f16(ts, dq_now + off, dk + off, kIdQK, uint32_t(kk > 0));
-                    }
-                    mma_commit(s_full(g));
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_f16(ts + 64u * (i & 1u), dq_now + uint64_t(kk >> 2) * uint64_t(kRows * 128 >> 4) + uint64_t((kk & 3) * 2),
+                                dk + uint64_t(kk >> 2) * uint64_t(kKeys * 128 >> 4) + uint64_t((kk & 3) * 2), kIdQK, uint32_t(kk > 0));
+                    mma_commit(s_full(g, i));
                     mma_commit(empty(slot));
+                    return true;
                 };
-                uint32_t no = 0;   // tiles so far
-                uint32_t q_phase = 0, p_phase = 0, t_phase = g == 0 ? 1u : 0u;   // group 0 has the first turn
+                uint32_t q_phase = 0;
                 bool ok = true;
-                for (uint32_t i = 0;; ++i) {
+                for (uint32_t i = 0; ok; ++i) {
                     ok = await_piece(st, i);
                     const int tiles = piece_at(st, i).t1 - piece_at(st, i).t0;
                     if (!ok || tiles == 0) break;
                     mbar_arrive(done_with(st, i));
-                    ok = wait_bounded(q_full(g), q_phase, abort_flag, status) && arrived(0, no);
-                    if (!ok) break;
+                    ok = wait_bounded(q_full(g), q_phase, abort_flag, status) && scores(no) && (tiles == 1 || scores(no + 1));
                     q_phase ^= 1u;
-                    tc_fence_after();
-                    scores(no, false);
-                    for (int s = 0; s < tiles; ++s, ++no) {
-                        const bool more = s + 1 < tiles;
-                        ok = arrived(1, no) && (!more || arrived(0, no + 1)) &&
-                             wait_bounded(p_full(g), p_phase, abort_flag, status) &&
-                             (!kTwo || wait_bounded(turn(g), t_phase, abort_flag, status));
+                    for (int s = 0; s < tiles && ok; ++s, ++no) {
+                        ok = arrived(1, no) && wait_bounded(p_full(g, no), (no >> 1) & 1u, abort_flag, status);
                         if (!ok) break;
                         tc_fence_after();
-                        t_phase ^= 1u;
-                        p_phase ^= 1u;
                         const int slot = slot_of(st, 1, no);
                         const uint64_t dv = described(slots + uint64_t(slot) * kTileDesc);
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_f16_ta(to, ts + 8u * uint32_t(kk),
-                                       dv + uint64_t(kk >> 2) * uint64_t(D * 128 >> 4) + uint64_t((kk & 3) * 2), kIdPV,
-                                       uint32_t(s > 0 || kk > 0));
-                        if (more) {
-                            scores(no + 1, true);
-                        } else {
-                            if (kTwo) mbar_arrive(turn(g ^ 1));
-                            mma_commit(o_full(g));
-                        }
+                            mma_f16_ta(to, ts + 64u * (no & 1u) + 8u * uint32_t(kk), dv + uint64_t(kk * 2), kIdPV, uint32_t(s > 0 || kk > 0));
+                        mma_commit(o_done(g));
                         mma_commit(empty(slot));
+                        if (s + 2 < tiles) ok = scores(no + 2);
                     }
-                    if (!ok) break;
                 }
                 mma_commit(drain);   // everything issued, also after a wait that ran out
                 wait_drain(drain, 0u, status);
@@ -577,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         const int g = warp >> 2, st = kTwo ? 0 : g;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + kColS + 128u * uint32_t(g), to = tmem + lanes + kColO + 128u * uint32_t(g);
-        uint32_t s_phase = 0, o_phase = 0;
+        const uint32_t ts0 = tmem + lanes + kColS + 128u * uint32_t(g), to = tmem + lanes + kColO + 128u * uint32_t(g);
+        uint32_t no = 0;   // tiles so far
         bool ok = true;
         for (uint32_t piece_no = 0;; ++piece_no) {
             ok = __all_sync(0xffffffffu, await_piece(st, piece_no));
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 const bool valid = j < q.n;
                 left = (valid ? max(0, q.len - q.n + 1 + j) : 0x7FFFFFFF) - q.t0 * kKeys;
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (valid ? (q.start + j) * p.q_stride + int64_t(head) * D : 0));
-                const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kTile + row * 128);
+                const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kQ + row * 128);
                 uint4 v[D / 8];
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
@@ -627,49 +631,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             float m = kNone, l = 0.f;
             bool wide = false;
             int n = 0;
-            auto scale_o = [&](float f) {   // at rest: the product before this S has completed
+            // The product of the tile before.  Every tile waits for it before it hands P on, long after it has been, so
+            // that o_done is never more than a phase ahead or behind.
+            auto await_product = [&]() {
+                ok = __all_sync(0xffffffffu, wait_bounded(o_done(g), (no & 1u) ^ 1u, abort_flag, status));
+                tc_fence_after();
+            };
+            auto scale_o = [&](float f) {   // O at rest
+                await_product();
+                if (!ok) return;
                 l *= f;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {   // few registers beside the scores
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(to + 16u * uint32_t(c), o);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st_32x32b_x32(to + 32u * uint32_t(c), o);
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st_32x32b_x16(to + 16u * uint32_t(c), o);
                 }
             };
-            for (; n < tiles; ++n) {
-                ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
+            for (; n < tiles; ++n, ++no) {
+                ok = __all_sync(0xffffffffu, wait_bounded(s_full(g, no), (no >> 1) & 1u, abort_flag, status));
                 if (!ok) break;
-                s_phase ^= 1u;
                 tc_fence_after();
-                // 64 keys at a time: the second half's scores stay for the weights, the first half's are read again.
+                const uint32_t ts = ts0 + 64u * (no & 1u);
                 uint32_t s[2][32];
-                auto read = [&](int half) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(ts + uint32_t(64 * half + 32 * c), s[c]);
+                for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), s[c]);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_wait_ld(s[c]);
-                    if (left < 64 * half + 64) {
+                for (int c = 0; c < 2; ++c) tmem_wait_ld(s[c]);
+                if (left < kKeys) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (64 * half + 32 * c + k >= left) s[c][k] = 0xFF800000u;
-                    }
-                };
-                float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= left) s[c][k] = 0xFF800000u;
+                }
+                float x0 = __uint_as_float(s[0][0]), x1 = __uint_as_float(s[0][1]), x2 = __uint_as_float(s[1][0]),
+                      x3 = __uint_as_float(s[1][1]);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    read(half);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        x0 = max3(x0, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
-                        x1 = max3(x1, __uint_as_float(s[0][k + 2]), __uint_as_float(s[0][k + 3]));
-                        x2 = max3(x2, __uint_as_float(s[1][k]), __uint_as_float(s[1][k + 1]));
-                        x3 = max3(x3, __uint_as_float(s[1][k + 2]), __uint_as_float(s[1][k + 3]));
-                    }
+                for (int k = 0; k < 32; k += 4) {
+                    x0 = max3(x0, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
+                    x1 = max3(x1, __uint_as_float(s[0][k + 2]), __uint_as_float(s[0][k + 3]));
+                    x2 = max3(x2, __uint_as_float(s[1][k]), __uint_as_float(s[1][k + 1]));
+                    x3 = max3(x3, __uint_as_float(s[1][k + 2]), __uint_as_float(s[1][k + 3]));
                 }
                 const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * scale;
                 const bool rises = top > m + kGrow;
@@ -679,29 +685,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     if (wide) break;
                     m = fmaxf(m, top);
                     if (n > 0) scale_o(ex2(was - m));
-                    read(1);   // scale_o() needs registers
+                    if (!ok) break;
                 }
                 const float base = m - kLift;
                 const uint64_t scale2 = pack2(scale, scale), base2 = pack2(-base, -base);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int half = 1; half >= 0; --half) {
-                    uint32_t pk[32];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const uint32_t* sc = &s[k >> 4][2 * (k & 15)];
-                        const uint64_t e = ffma2(pack2u(sc[0], sc[1]), scale2, base2);
+                    for (int k = 0; k < 16; ++k) {
+                        const uint64_t e = ffma2(pack2u(s[c][2 * k], s[c][2 * k + 1]), scale2, base2);
                         const float u = ex2(lo_f(e)), v = ex2(hi_f(e));
                         sum[k & 1] = fadd2(sum[k & 1], pack2(u, v));
                         pk[k] = pack16(u, v);
                     }
-                    if (half == 1) read(0);   // before P takes its place
-                    tmem_st_32x32b_x32(ts + 32u * uint32_t(half), pk);
+                    tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);
                 }
+                if (n > 0) await_product();
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(g));
+                if (lane == 0) mbar_arrive(p_full(g, no));
                 sum[0] = fadd2(sum[0], sum[1]);
                 l += lo_f(sum[0]) + hi_f(sum[0]);
                 left -= kKeys;
@@ -710,16 +716,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             // last place: from 2^20 on too much for P's range.  From the first tile where a row of the warp gets
             // there the products are rounded first, as m was, and m is neither lifted nor let behind.  No usual
             // call comes here, so short loops over S where it lies.
-            for (bool here = true; ok && wide && n < tiles; ++n, here = false) {
+            for (bool here = true; ok && wide && n < tiles; ++n, ++no, here = false) {
                 if (!here) {
-                    ok = __all_sync(0xffffffffu, wait_bounded(s_full(g), s_phase, abort_flag, status));
+                    ok = __all_sync(0xffffffffu, wait_bounded(s_full(g, no), (no >> 1) & 1u, abort_flag, status));
                     if (!ok) break;
-                    s_phase ^= 1u;
                     tc_fence_after();
                 }
+                const uint32_t ts = ts0 + 64u * (no & 1u);
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t x[32];
                     tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
                     tmem_wait_ld(x);
@@ -731,8 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 m = fmaxf(m, __fmul_rn(top, scale));
                 const float base = reference(m);
                 if (n > 0) scale_o(ex2(reference(was) - base));
+                if (!ok) break;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t x[32], pk[16];
                     tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
                     tmem_wait_ld(x);
@@ -746,17 +753,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     for (int k = 0; k < 16; ++k) pk[k] = pack16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
                     tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);   // over what has been read
                 }
+                if (n > 0) await_product();
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(g));
+                if (lane == 0) mbar_arrive(p_full(g, no));
                 l += sum;
                 left -= kKeys;
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, wait_bounded(o_full(g), o_phase, abort_flag, status));
+            await_product();
             if (!ok) break;
-            o_phase ^= 1u;
             tc_fence_after();
             const int r = q.u * kR + (kTwo ? g * kRows : 0) + row, j = r / a.group, head = q.h * a.group + r - j * a.group;
             const bool valid = j < q.n, done = q.starts && q.ends;
