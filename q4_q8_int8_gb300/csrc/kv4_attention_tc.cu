@@ -591,39 +591,90 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             if (!ok || tiles == 0) break;
             int left;   // keys that the row sees from the next tile on
             float scale = a.scale_log2;
-            // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.
+            // The group's query rows, swizzled (16-byte chunk c of row n at c ^ (n & 7)); zeros past the last row.  Of 256
+            // rows a warp takes kLanes lanes to a row, each lane one chunk of each of kTurns rows, and the results go out
+            // the same way; of at most 128, which are few as a rule, each thread takes its own row.  Own rows for the many:
+            // 70 -> 80 us (64 tokens of 8 sequences), 390 -> 409 (4096 of 2); together for the few: 21 rows of 33
+            // sequences 63 -> 70, 35 rows 70 -> 77.
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
+            const int in_row = lane % kLanes, of_turn = lane / kLanes;
+            const uint32_t q_rows = sbase + uint32_t(L::kOffQ + g * L::kQ + (in_row >> 3) * (kRows * 128) + (warp & 3) * 32 * 128);
+            auto q_chunk = [&](int r) { return q_rows + uint32_t(r * 128 + (((in_row & 7) ^ (r & 7)) << 4)); };
             {
                 const int r = q.u * kR + (kTwo ? g * kRows : 0) + row, j = r / a.group, head = q.h * a.group + r - j * a.group;
                 const bool valid = j < q.n;
                 left = (valid ? max(0, q.len - q.n + 1 + j) : 0x7FFFFFFF) - q.t0 * kKeys;
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (valid ? (q.start + j) * p.q_stride + int64_t(head) * D : 0));
-                const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kQ + row * 128);
-                uint4 v[D / 8];
+                if constexpr (kTwo) {
+                    const int64_t at = valid ? (q.start + j) * p.q_stride + int64_t(head) * D : -1;
+                    const uint32_t some = __ballot_sync(0xffffffffu, valid);
+                    uint4 v[kTurns];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                if (std::is_same<T, __nv_bfloat16>::value) {
-                    uint32_t top = 0;   // magnitudes order as integers; NaN's as the largest
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+                    for (int i = 0; i < kTurns; ++i) {
+                        const int64_t from_row = __shfl_sync(0xffffffffu, at, i * kAtOnce + of_turn);
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (from_row >= 0) v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + from_row + 8 * in_row);
                     }
-                    // top in [2^e, 2^(e+1)) -> [2^13, 2^14); a row of zeros or tiny values as if it had 2^-100
-                    const int e = max(-100, int(top >> 23) - 127);
-                    const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
-                    scale = fminf(scale * __uint_as_float(uint32_t(127 + e - 13) << 23), 3.4e38f);
+                    if (std::is_same<T, __nv_bfloat16>::value && some) {
+                        int e[kTurns];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint32_t* const w[4] = {&v[c].x, &v[c].y, &v[c].z, &v[c].w};
+                        for (int i = 0; i < kTurns; ++i) {
+                            uint32_t top = 0;   // magnitudes order as integers; NaN's as the largest
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *w[k] = pack16(__uint_as_float(*w[k] << 16) * up, __uint_as_float(*w[k] & 0xFFFF0000u) * up);
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t w = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
+                                top = max(top, max((w << 16) & 0x7FFF0000u, w & 0x7FFF0000u));
+                            }
+                            // top in [2^e, 2^(e+1)) -> [2^13, 2^14); a row of zeros or tiny values as if it had 2^-100
+                            e[i] = max(-100, int(top >> 23) - 127);
+                        }
+#pragma unroll
+                        for (int d = 1; d < kLanes; d <<= 1) {
+#pragma unroll
+                            for (int i = 0; i < kTurns; ++i) e[i] = max(e[i], __shfl_xor_sync(0xffffffffu, e[i], d));
+                        }
+#pragma unroll
+                        for (int i = 0; i < kTurns; ++i) {
+                            const float up = __uint_as_float(uint32_t(127 + 13 - e[i]) << 23);
+                            uint32_t* const w[4] = {&v[i].x, &v[i].y, &v[i].z, &v[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *w[k] = pack16(__uint_as_float(*w[k] << 16) * up, __uint_as_float(*w[k] & 0xFFFF0000u) * up);
+                            const int of_mine = __shfl_sync(0xffffffffu, e[i], lane % kAtOnce * kLanes);
+                            if (lane / kAtOnce == i) scale = fminf(a.scale_log2 * __uint_as_float(uint32_t(127 + of_mine - 13) << 23), 3.4e38f);
+                        }
                     }
+#pragma unroll
+                    for (int i = 0; i < kTurns; ++i) st_shared_v4(q_chunk(i * kAtOnce + of_turn), v[i].x, v[i].y, v[i].z, v[i].w);
+                } else {
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (valid ? (q.start + j) * p.q_stride + int64_t(head) * D : 0));
+                    const uint32_t dst = sbase + uint32_t(L::kOffQ + g * L::kQ + row * 128);
+                    uint4 v[D / 8];
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) v[c] = valid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    if (std::is_same<T, __nv_bfloat16>::value) {
+                        uint32_t top = 0;   // magnitudes order as integers; NaN's as the largest
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) top = max(top, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+                        }
+                        // top in [2^e, 2^(e+1)) -> [2^13, 2^14); a row of zeros or tiny values as if it had 2^-100
+                        const int e = max(-100, int(top >> 23) - 127);
+                        const float up = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+                        scale = fminf(scale * __uint_as_float(uint32_t(127 + e - 13) << 23), 3.4e38f);
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            uint32_t* const w[4] = {&v[c].x, &v[c].y, &v[c].z, &v[c].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *w[k] = pack16(__uint_as_float(*w[k] << 16) * up, __uint_as_float(*w[k] & 0xFFFF0000u) * up);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        st_shared_v4(dst + uint32_t((c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)), v[c].x, v[c].y, v[c].z, v[c].w);
                 }
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    st_shared_v4(dst + uint32_t((c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)), v[c].x, v[c].y, v[c].z, v[c].w);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full(g));
@@ -784,22 +835,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             const float factor = done ? l == 0.f ? 0.f : 1.f / l : 1.f;
             const int64_t run = blockIdx.x + int64_t(st) * gridDim.x;
             const int64_t at = (run * 2 + (q.starts ? 1 : 0)) * kR + (r - q.u * kR);   // a part's row
+            const int64_t out = !valid ? -1 : done ? ((q.start + j) * p.heads + head) * D : at * D;
+            const bool narrow = done && p.out_type != MMQ_TYPE_F32;
+            float* const out32 = done ? static_cast<float*>(p.out) : a.parts;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(to + 32u * uint32_t(c), o);
                 tmem_wait_ld(o);
-                if (!valid) continue;
                 const float by = (none >> c) & 1u ? __int_as_float(0x7FC00000) : factor;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
-                const int64_t out = ((q.start + j) * p.heads + head) * D + 32 * c;
-                if (!done || p.out_type == MMQ_TYPE_F32) {
-                    uint4* dst = reinterpret_cast<uint4*>(done ? static_cast<float*>(p.out) + out : a.parts + at * D + 32 * c);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out);
+                if (narrow) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -811,9 +858,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                             pk[k] = *reinterpret_cast<const uint32_t*>(&w);
                         }
                     }
+                    if constexpr (kTwo) {   // through the queries' place, which is free now
+                        const uint32_t mine = sbase + uint32_t(L::kOffQ + g * L::kQ + (c >> 1) * (kRows * 128) + row * 128);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(mine + uint32_t(((4 * (c & 1) + k) ^ (row & 7)) << 4), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                    } else if (valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + out + 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+                    }
+                } else if constexpr (kTwo) {
+                    const uint32_t rows = sbase + uint32_t(L::kOffQ + g * L::kQ + (warp & 3) * 32 * 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_shared_v4(rows + uint32_t(lane * 128 + ((k ^ (lane & 7)) << 4)), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int of = 4 * k + (lane >> 3);
+                        const int64_t to_row = __shfl_sync(0xffffffffu, out, of);
+                        const uint4 v = ld_shared_v4(rows + uint32_t(of * 128 + (((lane ^ of) & 7) << 4)));
+                        if (to_row >= 0) *reinterpret_cast<uint4*>(out32 + to_row + 32 * c + 4 * (lane & 7)) = v;
+                    }
+                    __syncwarp();
+                } else if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(out32 + out + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
+            }
+            if (kTwo && narrow) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int64_t to_row = __shfl_sync(0xffffffffu, out, i * kAtOnce + of_turn);
+                    const uint4 v = ld_shared_v4(q_chunk(i * kAtOnce + of_turn));
+                    if (to_row >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to_row + 8 * in_row) = v;
+                }
+                __syncwarp();
             }
             tc_fence_before();
             if (!done && q.starts && row == 0 && (g == 0 || !kTwo)) a.marks[run] = Mark{q.last, q.b, q.h, q.u};
