@@ -51,172 +51,360 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return d;
 }
 
+// The lanes of a tile: D / 4 of them, lane 4 i + c with dimensions 16 i to
+// 16 i + 15 of the keys of tokens c, c + 4, c + 8, c + 12 and of the values of
+// tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9.  These are 32 contiguous bytes of 16-bit
+// values each and all that the lane's eight words of key codes and eight of
+// value codes hold.
+__device__ __forceinline__ int key_token(int c, int k) { return c + 4 * k; }
+__device__ __forceinline__ int value_token(int c, int k) { return 2 * c + (k & 1) + 8 * (k >> 1); }
+
+constexpr int kThreads = 128;
+
+// A lane's place: item (16 tokens of a head, heads fastest) and the token that
+// group 0 starts with, at most 0: groups start where the first token's tile
+// does, so that the tokens of one long chunk fill whole tiles.
+template <int D>
+struct Lane {
+    static constexpr int kLanes = D / 4;
+    int i, c, h;
+    int64_t t0;
+    __device__ __forceinline__ Lane(const int32_t* slots, int64_t tokens, int kv_heads) {
+        const uint32_t item = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;   // below 2^31 and a block's
+        i = threadIdx.x % kLanes >> 2;
+        c = threadIdx.x & 3;
+        h = int(item % uint32_t(kv_heads));
+        const int first = slots[0];
+        t0 = int64_t(item / uint32_t(kv_heads)) * kTokens - (first < 0 ? 0 : first & 15);
+    }
+};
+
+// The slot of a token: lane l of the first 16 of an item's holds that of token
+// l.  whole: all the warp's items are a tile each, in order.
+template <int D>
+struct Slots {
+    int mine, first;
+    bool whole;
+    template <typename P>
+    __device__ __forceinline__ Slots(const P& p, const Lane<D>& lane, int* status) {
+        const int l = threadIdx.x & 15;
+        const int64_t t = lane.t0 + l;
+        mine = t >= 0 && t < p.tokens ? p.slots[t] : -1;
+        if (mine >= p.n_slots) {
+            if (lane.h == 0) atomicCAS(status, 0, MMQ_ERR_ARG);
+            mine = -1;
+        }
+        first = __shfl_sync(0xffffffffu, mine, 0, Lane<D>::kLanes);
+        whole = __all_sync(0xffffffffu, mine >= 0 && (first & 15) == 0 && mine == first + l);
+    }
+    __device__ __forceinline__ int of(int l) const { return __shfl_sync(0xffffffffu, mine, l, Lane<D>::kLanes); }
+};
+
+// Sixteen values of a token, and what the block's scale needs of them.
 template <typename T>
-__device__ __forceinline__ void load8(const void* base, int64_t at, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const void* base, int64_t at, float (&x)[8]) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__half>(const void* base, int64_t at, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __half*>(base) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Values;
+template <typename T>
+struct Values16 {
+    uint4 u[2];
+    __device__ __forceinline__ void load(const void* base, int64_t at, bool here) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
+        for (int k = 0; k < 2; ++k) u[k] = here ? src[k] : make_uint4(0u, 0u, 0u, 0u);
     }
-}
+    __device__ __forceinline__ uint32_t word(int k) const {
+        const uint4& v = u[k >> 2];
+        return (k & 3) == 0 ? v.x : (k & 3) == 1 ? v.y : (k & 3) == 2 ? v.z : v.w;
+    }
+};
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const void* base, int64_t at, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+struct Values<__half> : Values16<__half> {
+    __device__ __forceinline__ float get(int k) const {
+        const uint32_t w = word(k >> 1);
+        const __half2 h = *reinterpret_cast<const __half2*>(&w);
+        return k & 1 ? __high2float(h) : __low2float(h);
     }
+    __device__ __forceinline__ void ends(float& most, float& least) const {
+        uint32_t w = word(0);
+        __half2 a = *reinterpret_cast<__half2*>(&w), b = a;
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            w = word(k);
+            a = __hmax2_nan(a, *reinterpret_cast<__half2*>(&w));
+            b = __hmin2_nan(b, *reinterpret_cast<__half2*>(&w));
+        }
+        most = max_nan(__low2float(a), __high2float(a));
+        least = min_nan(__low2float(b), __high2float(b));
+    }
+};
+template <>
+struct Values<__nv_bfloat16> : Values16<__nv_bfloat16> {
+    __device__ __forceinline__ float get(int k) const {
+        return __uint_as_float(k & 1 ? word(k >> 1) & 0xFFFF0000u : word(k >> 1) << 16);
+    }
+    __device__ __forceinline__ void ends(float& most, float& least) const {
+        uint32_t w = word(0);
+        __nv_bfloat162 a = *reinterpret_cast<__nv_bfloat162*>(&w), b = a;
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            w = word(k);
+            a = __hmax2_nan(a, *reinterpret_cast<__nv_bfloat162*>(&w));
+            b = __hmin2_nan(b, *reinterpret_cast<__nv_bfloat162*>(&w));
+        }
+        most = max_nan(__low2float(a), __high2float(a));
+        least = min_nan(__low2float(b), __high2float(b));
+    }
+};
+template <>
+struct Values<float> {
+    float4 f[4];
+    __device__ __forceinline__ void load(const void* base, int64_t at, bool here) {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = here ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ float get(int k) const {
+        const float4& v = f[k >> 2];
+        return (k & 3) == 0 ? v.x : (k & 3) == 1 ? v.y : (k & 3) == 2 ? v.z : v.w;
+    }
+    __device__ __forceinline__ void ends(float& most, float& least) const {
+        most = least = get(0);
+#pragma unroll
+        for (int k = 1; k < 16; ++k) {
+            most = max_nan(most, get(k));
+            least = min_nan(least, get(k));
+        }
+    }
+};
+
+// code - 8 of x / d as bits whose lowest four are the code and whose others,
+// up to the 22nd, are zero.
+//
+// 16-bit types: a quotient that is no tie (an odd multiple of 1/2) is at least
+// 2^-12 from one, x having at most 11 bits, d at most 8, and |x| >= |d| / 2
+// there.  x times the rounded 1 / d is off by at most 12.5 * 2^-24.  So the
+// product rounded to multiples of 2^-14, which adding 768 does, is the tie where
+// the quotient is one and on its side of it where not, and the second sum rounds
+// it to an integer, ties to even.
+template <typename T>
+__device__ __forceinline__ uint32_t code_of(float x, float d, float inverse) {
+    const float t = fminf(fmaxf(fmaf(x, inverse, 768.f), 760.f), 775.f);
+    return __float_as_uint(t + (12582912.f + 8.f - 768.f));
+}
+// float: within one of the quotient; then the exact remainder decides.
+template <>
+__device__ __forceinline__ uint32_t code_of<float>(float x, float d, float inverse) {
+    float n = rintf(fminf(fmaxf(x * inverse, -8.f), 7.f));
+    const float rest = fmaf(-n, d, x), twice = 2.f * fabsf(rest);
+    const bool odd = int(n) & 1;
+    if (twice > fabsf(d) || (twice == fabsf(d) && odd)) n += (rest < 0.f) == (d < 0.f) ? 1.f : -1.f;
+    return uint32_t(int(fminf(fmaxf(n, -8.f), 7.f)) + 8);
 }
 
-// The scale of a block whose values four neighbouring lanes hold, and this
-// lane's eight codes, one per nibble (value k in bits 4k).
-__device__ __forceinline__ uint32_t quantize(const float (&x)[8], __half& scale) {
-    float most = x[0], least = x[0];
-#pragma unroll
-    for (int k = 1; k < 8; ++k) {
-        most = max_nan(most, x[k]);
-        least = min_nan(least, x[k]);
-    }
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-        most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, d));
-        least = min_nan(least, __shfl_xor_sync(0xffffffffu, least, d));
-    }
+// The scale of a block, half of whose values a lane holds, the other half its
+// neighbour of i ^ 1, and the lane's codes: byte x the dimensions x (low) and
+// x + 8 (high) of its sixteen.
+template <typename T>
+__device__ __forceinline__ uint2 quantize(const Values<T>& x, __half& scale) {
+    float most, least;
+    x.ends(most, least);
+    most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 4));
+    least = min_nan(least, __shfl_xor_sync(0xffffffffu, least, 4));
     const float top = most >= -least ? most : least;   // NaN: least, which is NaN too
     float d = __bfloat162float(__float2bfloat16_rn(__fmul_rn(top, -0.125f)));
     if (fabsf(d) > kTop) d = copysignf(kTop, d);
     if (!(fabsf(top) <= 3.402823466e38f)) d = __int_as_float(0x7FC00000);
     scale = __float2half_rn(d);
     d = __half2float(scale);
-    const float inverse = d == 0.f ? 0.f : 1.f / d;
-    uint32_t codes = 0;
+    const bool none = d == 0.f || d != d;
+    const float inverse = none ? 0.f : 1.f / d;
+    uint32_t w[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        // within one of the quotient; then the exact remainder decides, ties to even
-        float n = rintf(fminf(fmaxf(x[k] * inverse, -8.f), 7.f));
-        const float rest = fmaf(-n, d, x[k]), twice = 2.f * fabsf(rest);
-        const bool odd = int(n) & 1;
-        if (twice > fabsf(d) || (twice == fabsf(d) && odd)) n += (rest < 0.f) == (d < 0.f) ? 1.f : -1.f;
-        n = fminf(fmaxf(n, -8.f), 7.f);
-        if (d == 0.f || d != d) n = 0.f;
-        codes |= uint32_t(int(n) + 8) << (4 * k);
+    for (int half = 0; half < 2; ++half) {
+        uint32_t b[4];   // the low byte
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            b[k] = code_of<T>(x.get(4 * half + k), d, inverse) + 16u * code_of<T>(x.get(4 * half + k + 8), d, inverse);
+        w[half] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     }
-    return codes;
+    return none ? make_uint2(0x88888888u, 0x88888888u) : make_uint2(w[0], w[1]);
 }
 
-// Bytes x = 0..3 (even lanes) or 4..7 (odd lanes) of the 16 dimensions that
-// lanes 2 i and 2 i + 1 hold: the even lane's codes low, the odd lane's high.
-__device__ __forceinline__ uint32_t pair_bytes(uint32_t codes, bool odd) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 1);
-    const uint32_t lo = odd ? other >> 16 : codes & 0xFFFFu, hi = odd ? codes >> 16 : other & 0xFFFFu;
-    uint32_t w = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w |= (((lo >> (4 * k)) & 15u) | (((hi >> (4 * k)) & 15u) << 4)) << (8 * k);
-    return w;
-}
-
+// Bound by what it reads and writes where there are many tokens (see the
+// launch's figures), by its latency where there are few.
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D) kv4_write_kernel(const WriteArgs a) {
-    __shared__ __align__(16) uint8_t tile[tile_bytes(D)];
-    __shared__ int64_t first;   // slot of the group's first token
+__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const WriteArgs a) {
     const mmq_kv4_write_t& p = a.p;
     griddep_launch_dependents();
     griddep_wait();
-    constexpr int kLanes = D / 8;   // threads per token
-    // Groups of 16 start where the first token's tile does, so that the tokens
-    // of one long chunk fill whole tiles.
-    const int shift = p.slots[0] < 0 ? 0 : p.slots[0] & 15;
-    const int i16 = threadIdx.x / kLanes, e = threadIdx.x % kLanes;
-    const int64_t t = int64_t(blockIdx.x) * kTokens - shift + i16;
-    const int h = blockIdx.y;
-    const bool here = t >= 0 && t < p.tokens;
-    const int64_t slot = here ? p.slots[t] : -1;
-    const bool good = slot >= 0 && slot < p.n_slots;
-    if (slot >= p.n_slots && e == 0 && h == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
-    float k[8] = {}, v[8] = {};
-    if (good) {
-        load8<T>(p.k, t * p.k_token_stride + h * p.k_head_stride + 8 * e, k);
-        load8<T>(p.v, t * p.v_token_stride + h * p.v_head_stride + 8 * e, v);
-    }
-    __half ks, vs;
-    const bool odd = e & 1;
-    const uint32_t kb = pair_bytes(quantize(k, ks), odd), vb = pair_bytes(quantize(v, vs), odd);
-    // All 16 tokens of one tile, in order: the tile is put together first.
-    if (threadIdx.x == 0) first = slot;
-    __syncthreads();
-    const bool whole = __syncthreads_and(good && (first & 15) == 0 && slot == first + i16);
-    uint8_t* const dst = whole ? tile : good ? tile_of<D>(p.cache, slot, h, p.kv_heads, a.page_shift) : nullptr;
-    if (whole || good) {
-        const int place = int(slot & 15);
+    const Lane<D> lane(p.slots, p.tokens, p.kv_heads);
+    uint2 kb[4], vb[4];
+    __half ks[4], vs[4];
+    const Slots<D> slots(p, lane, a.status);
+    {
+        Values<T> k[4], v[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const int x = n + (odd ? 4 : 0);
-            dst[key_byte(place, e >> 1, x)] = uint8_t(kb >> (8 * n));
-            dst[value_byte<D>(place, e >> 1, x)] = uint8_t(vb >> (8 * n));
+            const int64_t t = lane.t0 + key_token(lane.c, n), u = lane.t0 + value_token(lane.c, n);
+            k[n].load(p.k, t * p.k_token_stride + lane.h * p.k_head_stride + 16 * lane.i, t >= 0 && t < p.tokens);
+            v[n].load(p.v, u * p.v_token_stride + lane.h * p.v_head_stride + 16 * lane.i, u >= 0 && u < p.tokens);
         }
-        if ((e & 3) == 0) {
-            *reinterpret_cast<__half*>(dst + key_scale<D>(place, e >> 2)) = ks;
-            *reinterpret_cast<__half*>(dst + value_scale<D>(place, e >> 2)) = vs;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            kb[n] = quantize<T>(k[n], ks[n]);
+            vb[n] = quantize<T>(v[n], vs[n]);
         }
     }
-    if (!whole) return;
-    __syncthreads();
-    if (threadIdx.x < tile_bytes(D) / 16) {
-        const uint4 w = reinterpret_cast<const uint4*>(tile)[threadIdx.x];
-        reinterpret_cast<uint4*>(tile_of<D>(p.cache, slot, h, p.kv_heads, a.page_shift))[threadIdx.x] = w;
+    const int i = lane.i, c = lane.c;
+    if (slots.whole) {
+        uint8_t* const dst = tile_of<D>(p.cache, slots.first, lane.h, p.kv_heads, a.page_shift);
+        // keys: word x / 2 of token t and t + 8 takes two bytes of each
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 8; x += 2) {
+                const uint32_t lo = x < 4 ? kb[n].x : kb[n].y, hi = x < 4 ? kb[n + 2].x : kb[n + 2].y;
+                *reinterpret_cast<uint32_t*>(dst + key_byte(key_token(c, n), i, x)) = __byte_perm(lo, hi, x & 2 ? 0x7362 : 0x5140);
+            }
+        // values: word x takes a byte of each of the four tokens
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) w[n] = x < 4 ? vb[n].x : vb[n].y;
+            const uint32_t sel = uint32_t(x & 3) | uint32_t(4 + (x & 3)) << 4;
+            *reinterpret_cast<uint32_t*>(dst + value_byte<D>(2 * c, i, x)) =
+                __byte_perm(__byte_perm(w[0], w[2], sel), __byte_perm(w[1], w[3], sel), 0x5410);
+        }
+        if ((i & 1) == 0) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) *reinterpret_cast<__half*>(dst + key_scale<D>(key_token(c, n), i >> 1)) = ks[n];
+            const __half2 s0 = __halves2half2(vs[0], vs[1]), s1 = __halves2half2(vs[2], vs[3]);
+            *reinterpret_cast<uint2*>(dst + value_scale<D>(2 * c, i >> 1)) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&s0), *reinterpret_cast<const uint32_t*>(&s1));
+        }
+        return;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int k = slots.of(key_token(c, n)), v = slots.of(value_token(c, n));
+        if (k >= 0) {
+            uint8_t* const dst = tile_of<D>(p.cache, k, lane.h, p.kv_heads, a.page_shift);
+            const int place = int(k & 15);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[key_byte(place, i, x)] = uint8_t((x < 4 ? kb[n].x : kb[n].y) >> (8 * (x & 3)));
+            if ((i & 1) == 0) *reinterpret_cast<__half*>(dst + key_scale<D>(place, i >> 1)) = ks[n];
+        }
+        if (v >= 0) {
+            uint8_t* const dst = tile_of<D>(p.cache, v, lane.h, p.kv_heads, a.page_shift);
+            const int place = int(v & 15);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[value_byte<D>(place, i, x)] = uint8_t((x < 4 ? vb[n].x : vb[n].y) >> (8 * (x & 3)));
+            if ((i & 1) == 0) *reinterpret_cast<__half*>(dst + value_scale<D>(place, i >> 1)) = vs[n];
+        }
     }
 }
 
 // -------------------------------------------------------------------- read
-__device__ __forceinline__ void store2(__half* at, float x, float y) { *reinterpret_cast<__half2*>(at) = __floats2half2_rn(x, y); }
-__device__ __forceinline__ void store2(__nv_bfloat16* at, float x, float y) {
-    *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(x, y);
+// A pair of codes in the low nibbles of two halves, less 8 and times a scale.
+// Exact: 1024 + code and the difference are, and so is the product, by the
+// layout's bound on scales.
+__device__ __forceinline__ __half2 expand(uint32_t pair, __half2 scale) {
+    const uint32_t w = (pair & 0x000F000Fu) | 0x64006400u;
+    return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1032.f)), scale);
 }
-__device__ __forceinline__ void store2(float* at, float x, float y) { *reinterpret_cast<float2*>(at) = make_float2(x, y); }
+__device__ __forceinline__ uint32_t as_words(__half2 x, const __half*) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ uint32_t as_words(__half2 x, const __nv_bfloat16*) {
+    const float2 f = __half22float2(x);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint2 as_words(__half2 x, const float*) {
+    const float2 f = __half22float2(x);
+    return make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
+}
+__device__ __forceinline__ void store4(void* at, const uint32_t (&w)[4]) { *static_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]); }
+__device__ __forceinline__ void store4(void* at, const uint2 (&w)[4]) {
+    static_cast<uint4*>(at)[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+    static_cast<uint4*>(at)[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+}
+// A token's sixteen values from four words, each with two neighbouring
+// dimensions in its halves' low nibbles and those + 8 in the next.
+template <typename T>
+__device__ __forceinline__ void store16(T* at, const uint32_t (&pairs)[4], __half scale) {
+    const __half2 s = __half2half2(scale);
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi) {
+        decltype(as_words(s, at)) w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = as_words(expand(pairs[k] >> (4 * hi), s), at);
+        store4(at + 8 * hi, w);
+    }
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D) kv4_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     const mmq_kv4_read_t& p = a.p;
     griddep_launch_dependents();
     griddep_wait();
-    constexpr int kLanes = D / 8;
-    const int e = threadIdx.x % kLanes, h = blockIdx.y;
-    const int64_t t = int64_t(blockIdx.x) * kTokens + threadIdx.x / kLanes;
-    if (t >= p.tokens) return;
-    const int64_t slot = p.slots[t];
-    const bool good = slot >= 0 && slot < p.n_slots;
-    if (slot >= p.n_slots && e == 0 && h == 0) atomicCAS(a.status, 0, MMQ_ERR_ARG);
-    float k[8] = {}, v[8] = {};
-    if (good) {
-        const uint8_t* src = tile_of<D>(p.cache, slot, h, p.kv_heads, a.page_shift);
-        const int place = int(slot & 15), nibble = 4 * (e & 1);
-        const float ks = __half2float(*reinterpret_cast<const __half*>(src + key_scale<D>(place, e >> 2)));
-        const float vs = __half2float(*reinterpret_cast<const __half*>(src + value_scale<D>(place, e >> 2)));
+    const Lane<D> lane(p.slots, p.tokens, p.kv_heads);
+    const Slots<D> slots(p, lane, a.status);
+    const int i = lane.i, c = lane.c;
+    auto out = [&](void* base, int n) {
+        return static_cast<T*>(base) + ((lane.t0 + n) * p.kv_heads + lane.h) * D + 16 * i;
+    };
+    if (slots.whole) {
+        const uint8_t* const src = tile_of<D>(p.cache, slots.first, lane.h, p.kv_heads, a.page_shift);
+        uint32_t k[2][4], v[8];
+        __half ks[4];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            k[x] = float(int((src[key_byte(place, e >> 1, x)] >> nibble) & 15) - 8) * ks;
-            v[x] = float(int((src[value_byte<D>(place, e >> 1, x)] >> nibble) & 15) - 8) * vs;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) k[n][x] = *reinterpret_cast<const uint32_t*>(src + key_byte(key_token(c, n), i, 2 * x));
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint32_t*>(src + value_byte<D>(2 * c, i, x));
+#pragma unroll
+        for (int n = 0; n < 4; ++n) ks[n] = *reinterpret_cast<const __half*>(src + key_scale<D>(key_token(c, n), i >> 1));
+        const uint2 scales = *reinterpret_cast<const uint2*>(src + value_scale<D>(2 * c, i >> 1));
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            uint32_t pairs[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) pairs[x] = k[n & 1][x] >> (8 * (n >> 1));
+            store16(out(p.k, key_token(c, n)), pairs, ks[n]);
         }
-    }
-    const int64_t at = (t * p.kv_heads + h) * D + 8 * e;
 #pragma unroll
-    for (int x = 0; x < 8; x += 2) {
-        store2(static_cast<T*>(p.k) + at + x, k[x], k[x + 1]);
-        store2(static_cast<T*>(p.v) + at + x, v[x], v[x + 1]);
+        for (int n = 0; n < 4; ++n) {   // token 2 c + n % 2 + 8 (n / 2), byte n / 2 + 2 (n % 2)
+            uint32_t pairs[4];
+            const uint32_t b = uint32_t((n >> 1) + 2 * (n & 1));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) pairs[x] = __byte_perm(v[2 * x], v[2 * x + 1], b | (4 + b) << 8);
+            const __half2 s = *reinterpret_cast<const __half2*>(n < 2 ? &scales.x : &scales.y);
+            store16(out(p.v, value_token(c, n)), pairs, n & 1 ? __high2half(s) : __low2half(s));
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int n = 0; n < 8; ++n) {
+        const int t = n < 4 ? key_token(c, n) : value_token(c, n - 4);
+        const int slot = slots.of(t);
+        if (lane.t0 + t < 0 || lane.t0 + t >= p.tokens) continue;
+        uint32_t pairs[4] = {};
+        __half scale = __float2half_rn(0.f);
+        if (slot >= 0) {
+            const uint8_t* const src = tile_of<D>(p.cache, slot, lane.h, p.kv_heads, a.page_shift);
+            const int place = int(slot & 15);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint8_t b = src[n < 4 ? key_byte(place, i, x) : value_byte<D>(place, i, x)];
+                pairs[x >> 1] |= uint32_t(b) << (16 * (x & 1));
+            }
+            scale = *reinterpret_cast<const __half*>(src + (n < 4 ? key_scale<D>(place, i >> 1) : value_scale<D>(place, i >> 1)));
+        }
+        if (slot < 0) {   // zeros, without the sign that codes of 0 would give
+#pragma unroll
+            for (int x = 0; x < 4; ++x) pairs[x] = 0x00880088u;
+        }
+        store16(out(n < 4 ? p.k : p.v, t), pairs, scale);
     }
 }
 
@@ -226,20 +414,23 @@ int shift_of(int page_size) {
     return s;
 }
 
+template <int D, typename Args>
+cudaError_t launch(void (*kernel)(Args), const Args& a, cudaStream_t s) {
+    // one group more than the tokens fill: the first may hold as little as one
+    const int64_t items = (int64_t(a.p.tokens) + 15 + kTokens - 1) / kTokens * a.p.kv_heads;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    constexpr int kItems = kThreads / Lane<D>::kLanes;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned((items + kItems - 1) / kItems)), dim3(kThreads), 0, s, attr);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
 template <typename T, int D>
 cudaError_t write(const WriteArgs& a, cudaStream_t s) {
-    cudaLaunchAttribute attr[1];
-    // one group more than the tokens fill: the first may hold as little as one token
-    const dim3 grid(unsigned((a.p.tokens + 15 + kTokens - 1) / kTokens), unsigned(a.p.kv_heads));
-    const cudaLaunchConfig_t cfg = mmq::launch_config(grid, dim3(2 * D), 0, s, attr);
-    return cudaLaunchKernelEx(&cfg, kv4_write_kernel<T, D>, a);
+    return launch<D>(kv4_write_kernel<T, D>, a, s);
 }
 template <typename T, int D>
 cudaError_t read(const ReadArgs& a, cudaStream_t s) {
-    cudaLaunchAttribute attr[1];
-    const dim3 grid(unsigned((a.p.tokens + kTokens - 1) / kTokens), unsigned(a.p.kv_heads));
-    const cudaLaunchConfig_t cfg = mmq::launch_config(grid, dim3(2 * D), 0, s, attr);
-    return cudaLaunchKernelEx(&cfg, kv4_read_kernel<T, D>, a);
+    return launch<D>(kv4_read_kernel<T, D>, a, s);
 }
 
 }  // namespace
