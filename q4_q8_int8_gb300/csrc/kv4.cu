@@ -91,7 +91,7 @@ struct Slots {
         const int64_t t = lane.t0 + l;
         mine = t >= 0 && t < p.tokens ? p.slots[t] : -1;
         if (mine >= p.n_slots) {
-            if (lane.h == 0) atomicCAS(status, 0, MMQ_ERR_ARG);
+            if (lane.h == 0 && blockIdx.y == 0) atomicCAS(status, 0, MMQ_ERR_ARG);
             mine = -1;
         }
         first = __shfl_sync(0xffffffffu, mine, 0, Lane<D>::kLanes);
@@ -237,70 +237,66 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const WriteArgs a) 
     griddep_launch_dependents();
     griddep_wait();
     const Lane<D> lane(p.slots, p.tokens, p.kv_heads);
-    uint2 kb[4], vb[4];
-    __half ks[4], vs[4];
     const Slots<D> slots(p, lane, a.status);
-    {
-        Values<T> k[4], v[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int64_t t = lane.t0 + key_token(lane.c, n), u = lane.t0 + value_token(lane.c, n);
-            k[n].load(p.k, t * p.k_token_stride + lane.h * p.k_head_stride + 16 * lane.i, t >= 0 && t < p.tokens);
-            v[n].load(p.v, u * p.v_token_stride + lane.h * p.v_head_stride + 16 * lane.i, u >= 0 && u < p.tokens);
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            kb[n] = quantize<T>(k[n], ks[n]);
-            vb[n] = quantize<T>(v[n], vs[n]);
-        }
-    }
     const int i = lane.i, c = lane.c;
+    const bool keys = blockIdx.y == 0;
+    auto token = [&](int n) { return keys ? key_token(c, n) : value_token(c, n); };
+    const void* const from = keys ? p.k : p.v;
+    const int64_t token_stride = keys ? p.k_token_stride : p.v_token_stride;
+    const int64_t column = lane.h * (keys ? p.k_head_stride : p.v_head_stride) + 16 * i;
+    Values<T> x[4];
+    uint2 b[4];
+    __half s[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int64_t t = lane.t0 + token(n);
+        x[n].load(from, t * token_stride + column, t >= 0 && t < p.tokens);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) b[n] = quantize<T>(x[n], s[n]);
     if (slots.whole) {
         uint8_t* const dst = tile_of<D>(p.cache, slots.first, lane.h, p.kv_heads, a.page_shift);
-        // keys: word x / 2 of token t and t + 8 takes two bytes of each
+        if (keys) {   // word x / 2 of tokens t and t + 8 takes two bytes of each
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int x = 0; x < 8; x += 2) {
-                const uint32_t lo = x < 4 ? kb[n].x : kb[n].y, hi = x < 4 ? kb[n + 2].x : kb[n + 2].y;
-                *reinterpret_cast<uint32_t*>(dst + key_byte(key_token(c, n), i, x)) = __byte_perm(lo, hi, x & 2 ? 0x7362 : 0x5140);
+                for (int x = 0; x < 8; x += 2) {
+                    const uint32_t lo = x < 4 ? b[n].x : b[n].y, hi = x < 4 ? b[n + 2].x : b[n + 2].y;
+                    *reinterpret_cast<uint32_t*>(dst + key_byte(key_token(c, n), i, x)) = __byte_perm(lo, hi, x & 2 ? 0x7362 : 0x5140);
+                }
+            if ((i & 1) == 0) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) *reinterpret_cast<__half*>(dst + key_scale<D>(key_token(c, n), i >> 1)) = s[n];
             }
-        // values: word x takes a byte of each of the four tokens
+        } else {   // word x takes a byte of each of the four tokens
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            uint32_t w[4];
+            for (int x = 0; x < 8; ++x) {
+                uint32_t w[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) w[n] = x < 4 ? vb[n].x : vb[n].y;
-            const uint32_t sel = uint32_t(x & 3) | uint32_t(4 + (x & 3)) << 4;
-            *reinterpret_cast<uint32_t*>(dst + value_byte<D>(2 * c, i, x)) =
-                __byte_perm(__byte_perm(w[0], w[2], sel), __byte_perm(w[1], w[3], sel), 0x5410);
-        }
-        if ((i & 1) == 0) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) *reinterpret_cast<__half*>(dst + key_scale<D>(key_token(c, n), i >> 1)) = ks[n];
-            const __half2 s0 = __halves2half2(vs[0], vs[1]), s1 = __halves2half2(vs[2], vs[3]);
-            *reinterpret_cast<uint2*>(dst + value_scale<D>(2 * c, i >> 1)) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&s0), *reinterpret_cast<const uint32_t*>(&s1));
+                for (int n = 0; n < 4; ++n) w[n] = x < 4 ? b[n].x : b[n].y;
+                const uint32_t sel = uint32_t(x & 3) | uint32_t(4 + (x & 3)) << 4;
+                *reinterpret_cast<uint32_t*>(dst + value_byte<D>(2 * c, i, x)) =
+                    __byte_perm(__byte_perm(w[0], w[2], sel), __byte_perm(w[1], w[3], sel), 0x5410);
+            }
+            if ((i & 1) == 0) {
+                const __half2 s0 = __halves2half2(s[0], s[1]), s1 = __halves2half2(s[2], s[3]);
+                *reinterpret_cast<uint2*>(dst + value_scale<D>(2 * c, i >> 1)) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&s0), *reinterpret_cast<const uint32_t*>(&s1));
+            }
         }
         return;
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        const int k = slots.of(key_token(c, n)), v = slots.of(value_token(c, n));
-        if (k >= 0) {
-            uint8_t* const dst = tile_of<D>(p.cache, k, lane.h, p.kv_heads, a.page_shift);
-            const int place = int(k & 15);
+        const int slot = slots.of(token(n));
+        if (slot < 0) continue;
+        uint8_t* const dst = tile_of<D>(p.cache, slot, lane.h, p.kv_heads, a.page_shift);
+        const int place = int(slot & 15);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) dst[key_byte(place, i, x)] = uint8_t((x < 4 ? kb[n].x : kb[n].y) >> (8 * (x & 3)));
-            if ((i & 1) == 0) *reinterpret_cast<__half*>(dst + key_scale<D>(place, i >> 1)) = ks[n];
-        }
-        if (v >= 0) {
-            uint8_t* const dst = tile_of<D>(p.cache, v, lane.h, p.kv_heads, a.page_shift);
-            const int place = int(v & 15);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) dst[value_byte<D>(place, i, x)] = uint8_t((x < 4 ? vb[n].x : vb[n].y) >> (8 * (x & 3)));
-            if ((i & 1) == 0) *reinterpret_cast<__half*>(dst + value_scale<D>(place, i >> 1)) = vs[n];
-        }
+        for (int x = 0; x < 8; ++x)
+            dst[keys ? key_byte(place, i, x) : value_byte<D>(place, i, x)] = uint8_t((x < 4 ? b[n].x : b[n].y) >> (8 * (x & 3)));
+        if ((i & 1) == 0)
+            *reinterpret_cast<__half*>(dst + (keys ? key_scale<D>(place, i >> 1) : value_scale<D>(place, i >> 1))) = s[n];
     }
 }
 
@@ -349,62 +345,60 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     const Lane<D> lane(p.slots, p.tokens, p.kv_heads);
     const Slots<D> slots(p, lane, a.status);
     const int i = lane.i, c = lane.c;
-    auto out = [&](void* base, int n) {
-        return static_cast<T*>(base) + ((lane.t0 + n) * p.kv_heads + lane.h) * D + 16 * i;
+    const bool keys = blockIdx.y == 0;
+    auto out = [&](int t) {
+        return static_cast<T*>(keys ? p.k : p.v) + ((lane.t0 + t) * p.kv_heads + lane.h) * D + 16 * i;
     };
     if (slots.whole) {
         const uint8_t* const src = tile_of<D>(p.cache, slots.first, lane.h, p.kv_heads, a.page_shift);
-        uint32_t k[2][4], v[8];
-        __half ks[4];
+        uint32_t w[8];
+        if (keys) {
+            __half s[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+            for (int x = 0; x < 8; ++x)
+                w[x] = *reinterpret_cast<const uint32_t*>(src + key_byte(key_token(c, x >> 2), i, 2 * (x & 3)));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) k[n][x] = *reinterpret_cast<const uint32_t*>(src + key_byte(key_token(c, n), i, 2 * x));
+            for (int n = 0; n < 4; ++n) s[n] = *reinterpret_cast<const __half*>(src + key_scale<D>(key_token(c, n), i >> 1));
 #pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint32_t*>(src + value_byte<D>(2 * c, i, x));
+            for (int n = 0; n < 4; ++n) {
+                uint32_t pairs[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) ks[n] = *reinterpret_cast<const __half*>(src + key_scale<D>(key_token(c, n), i >> 1));
-        const uint2 scales = *reinterpret_cast<const uint2*>(src + value_scale<D>(2 * c, i >> 1));
+                for (int x = 0; x < 4; ++x) pairs[x] = w[4 * (n & 1) + x] >> (8 * (n >> 1));
+                store16(out(key_token(c, n)), pairs, s[n]);
+            }
+        } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            uint32_t pairs[4];
+            for (int x = 0; x < 8; ++x) w[x] = *reinterpret_cast<const uint32_t*>(src + value_byte<D>(2 * c, i, x));
+            const uint2 s = *reinterpret_cast<const uint2*>(src + value_scale<D>(2 * c, i >> 1));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) pairs[x] = k[n & 1][x] >> (8 * (n >> 1));
-            store16(out(p.k, key_token(c, n)), pairs, ks[n]);
-        }
+            for (int n = 0; n < 4; ++n) {   // token 2 c + n % 2 + 8 (n / 2), byte n / 2 + 2 (n % 2)
+                uint32_t pairs[4];
+                const uint32_t b = uint32_t((n >> 1) + 2 * (n & 1));
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {   // token 2 c + n % 2 + 8 (n / 2), byte n / 2 + 2 (n % 2)
-            uint32_t pairs[4];
-            const uint32_t b = uint32_t((n >> 1) + 2 * (n & 1));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pairs[x] = __byte_perm(v[2 * x], v[2 * x + 1], b | (4 + b) << 8);
-            const __half2 s = *reinterpret_cast<const __half2*>(n < 2 ? &scales.x : &scales.y);
-            store16(out(p.v, value_token(c, n)), pairs, n & 1 ? __high2half(s) : __low2half(s));
+                for (int x = 0; x < 4; ++x) pairs[x] = __byte_perm(w[2 * x], w[2 * x + 1], b | (4 + b) << 8);
+                const __half2 two = *reinterpret_cast<const __half2*>(n < 2 ? &s.x : &s.y);
+                store16(out(value_token(c, n)), pairs, n & 1 ? __high2half(two) : __low2half(two));
+            }
         }
         return;
     }
 #pragma unroll 1
-    for (int n = 0; n < 8; ++n) {
-        const int t = n < 4 ? key_token(c, n) : value_token(c, n - 4);
+    for (int n = 0; n < 4; ++n) {
+        const int t = keys ? key_token(c, n) : value_token(c, n);
         const int slot = slots.of(t);
         if (lane.t0 + t < 0 || lane.t0 + t >= p.tokens) continue;
-        uint32_t pairs[4] = {};
+        uint32_t pairs[4] = {0x00880088u, 0x00880088u, 0x00880088u, 0x00880088u};   // zeros
         __half scale = __float2half_rn(0.f);
         if (slot >= 0) {
             const uint8_t* const src = tile_of<D>(p.cache, slot, lane.h, p.kv_heads, a.page_shift);
             const int place = int(slot & 15);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint8_t b = src[n < 4 ? key_byte(place, i, x) : value_byte<D>(place, i, x)];
-                pairs[x >> 1] |= uint32_t(b) << (16 * (x & 1));
-            }
-            scale = *reinterpret_cast<const __half*>(src + (n < 4 ? key_scale<D>(place, i >> 1) : value_scale<D>(place, i >> 1)));
+            for (int x = 0; x < 8; x += 2)
+                pairs[x >> 1] = uint32_t(src[keys ? key_byte(place, i, x) : value_byte<D>(place, i, x)]) |
+                                uint32_t(src[keys ? key_byte(place, i, x + 1) : value_byte<D>(place, i, x + 1)]) << 16;
+            scale = *reinterpret_cast<const __half*>(src + (keys ? key_scale<D>(place, i >> 1) : value_scale<D>(place, i >> 1)));
         }
-        if (slot < 0) {   // zeros, without the sign that codes of 0 would give
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pairs[x] = 0x00880088u;
-        }
-        store16(out(n < 4 ? p.k : p.v, t), pairs, scale);
+        store16(out(t), pairs, scale);
     }
 }
 
@@ -421,7 +415,7 @@ cudaError_t launch(void (*kernel)(Args), const Args& a, cudaStream_t s) {
     if (items > INT32_MAX) return cudaErrorInvalidValue;
     constexpr int kItems = kThreads / Lane<D>::kLanes;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned((items + kItems - 1) / kItems)), dim3(kThreads), 0, s, attr);
+    const cudaLaunchConfig_t cfg = mmq::launch_config(dim3(unsigned((items + kItems - 1) / kItems), 2), dim3(kThreads), 0, s, attr);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 template <typename T, int D>
