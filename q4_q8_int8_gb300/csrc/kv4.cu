@@ -11,6 +11,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "mmq_internal.h"
 #include "sm103_ptx.cuh"
@@ -28,6 +30,7 @@ struct WriteArgs {
 struct ReadArgs {
     mmq_kv4_read_t p;
     int page_shift;
+    bool aligned;   // k and v to 32 bytes
     int* status;
 };
 
@@ -308,33 +311,42 @@ __device__ __forceinline__ __half2 expand(uint32_t pair, __half2 scale) {
     const uint32_t w = (pair & 0x000F000Fu) | 0x64006400u;
     return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1032.f)), scale);
 }
-__device__ __forceinline__ uint32_t as_words(__half2 x, const __half*) { return *reinterpret_cast<const uint32_t*>(&x); }
-__device__ __forceinline__ uint32_t as_words(__half2 x, const __nv_bfloat16*) {
-    const float2 f = __half22float2(x);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-__device__ __forceinline__ uint2 as_words(__half2 x, const float*) {
-    const float2 f = __half22float2(x);
-    return make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
-}
-__device__ __forceinline__ void store4(void* at, const uint32_t (&w)[4]) { *static_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]); }
-__device__ __forceinline__ void store4(void* at, const uint2 (&w)[4]) {
-    static_cast<uint4*>(at)[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
-    static_cast<uint4*>(at)[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+// 32 bytes, a whole sector, in one store where the address allows it.
+__device__ __forceinline__ void store8(void* at, const uint32_t* w, bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 // A token's sixteen values from four words, each with two neighbouring
 // dimensions in its halves' low nibbles and those + 8 in the next.
 template <typename T>
-__device__ __forceinline__ void store16(T* at, const uint32_t (&pairs)[4], __half scale) {
+__device__ __forceinline__ void store16(T* at, const uint32_t (&pairs)[4], __half scale, bool aligned) {
     const __half2 s = __half2half2(scale);
+    constexpr int kWords = sizeof(T) / 2;   // of a pair
+    uint32_t w[8 * kWords];
 #pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-        decltype(as_words(s, at)) w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = as_words(expand(pairs[k] >> (4 * hi), s), at);
-        store4(at + 8 * hi, w);
+    for (int k = 0; k < 8; ++k) {
+        const __half2 x = expand(pairs[k & 3] >> (4 * (k >> 2)), s);
+        if (std::is_same<T, __half>::value) {
+            w[k] = *reinterpret_cast<const uint32_t*>(&x);
+        } else {
+            const float2 f = __half22float2(x);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+            if (std::is_same<T, float>::value) {
+                w[kWords * k] = __float_as_uint(f.x);
+                w[kWords * k + kWords - 1] = __float_as_uint(f.y);
+            } else {
+                w[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
     }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) store8(at + 16 / kWords * k, w + 8 * k, aligned);
 }
 
 template <typename T, int D>
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     const Lane<D> lane(p.slots, p.tokens, p.kv_heads);
     const Slots<D> slots(p, lane, a.status);
     const int i = lane.i, c = lane.c;
-    const bool keys = blockIdx.y == 0;
+    const bool keys = blockIdx.y == 0, aligned = a.aligned;
     auto out = [&](int t) {
         return static_cast<T*>(keys ? p.k : p.v) + ((lane.t0 + t) * p.kv_heads + lane.h) * D + 16 * i;
     };
@@ -364,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
                 uint32_t pairs[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) pairs[x] = w[4 * (n & 1) + x] >> (8 * (n >> 1));
-                store16(out(key_token(c, n)), pairs, s[n]);
+                store16(out(key_token(c, n)), pairs, s[n], aligned);
             }
         } else {
 #pragma unroll
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) pairs[x] = __byte_perm(w[2 * x], w[2 * x + 1], b | (4 + b) << 8);
                 const __half2 two = *reinterpret_cast<const __half2*>(n < 2 ? &s.x : &s.y);
-                store16(out(value_token(c, n)), pairs, n & 1 ? __high2half(two) : __low2half(two));
+                store16(out(value_token(c, n)), pairs, n & 1 ? __high2half(two) : __low2half(two), aligned);
             }
         }
         return;
@@ -398,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
                                 uint32_t(src[keys ? key_byte(place, i, x + 1) : value_byte<D>(place, i, x + 1)]) << 16;
             scale = *reinterpret_cast<const __half*>(src + (keys ? key_scale<D>(place, i >> 1) : value_scale<D>(place, i >> 1)));
         }
-        store16(out(t), pairs, scale);
+        store16(out(t), pairs, scale, aligned);
     }
 }
 
@@ -442,7 +454,8 @@ cudaError_t launch_kv4_write(const mmq_kv4_write_t& p, int* status, cudaStream_t
 }
 
 cudaError_t launch_kv4_read(const mmq_kv4_read_t& p, int* status, cudaStream_t s) {
-    const ReadArgs a{p, shift_of(p.page_size), status};
+    const bool aligned = (reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) % 32 == 0;
+    const ReadArgs a{p, shift_of(p.page_size), aligned, status};
     const bool wide = p.head_dim == 128;
     switch (p.type) {
         case MMQ_TYPE_F16: return wide ? read<__half, 128>(a, s) : read<__half, 64>(a, s);
