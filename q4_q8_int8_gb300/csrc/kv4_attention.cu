@@ -6,8 +6,8 @@
 // in parts joined by their references m and sums, as in attention.cu.
 //
 // Rows are the (new token, head of the group) pairs of one kv head, R = 8 NT of
-// them to a unit, which needs every tile of 16 keys that its last row sees.
-// All units' tiles, one after the other, are cut into equal runs, one per warp:
+// them to a unit, which needs every step of 32 keys (two tiles) that its last
+// row sees.  All units' steps, one after the other, are cut into equal runs, one per warp:
 // ragged lengths and few long sequences fill the machine alike.  A warp's run
 // may hold the end of one unit, some whole ones and the start of another; parts
 // of a unit that lie in one CTA join in shared memory, those over several in
@@ -20,16 +20,30 @@
 // is one asynchronous bulk copy into the warp's own ring, and a lane's words
 // need masks only.
 //   Keys: a code masked out of its word is an fp16 subnormal, n 2^-24 (or 2^-20
-//   from the upper nibble, for which q' is 2^-4 times smaller); the 8 is taken
-//   off by the accumulator's start, -8 sum q', and the block's scale multiplies
-//   the f32 sum.  q' has its row's largest element in [2^13, 2^14): nothing of
-//   a bfloat16's or float16's eleven bits is lost down to 2^-28 of it.
+//   from the upper nibble, for which q' is 2^-4 times smaller), and the block's
+//   scale multiplies the f32 sum.  The 8 is taken off in one more product,
+//   scales times -8 sum q' of their blocks: a scale's bits, shifted by three,
+//   are a bfloat16 (times 2^-112), and each f32 sum is three of them.  q' has
+//   its row's largest element in [2^13, 2^14): nothing of a bfloat16's or
+//   float16's eleven bits is lost down to 2^-28 of it.
 //   Values: (n - 8) d, exact in fp16, because here the scale's index is summed
-//   over.  Weights are the sum of two fp16 values (22 bits, 2^-25 of the
-//   reference at worst), a product each: one alone would double the error of a
-//   float16 result.
-// The reference m of a row is only raised when a score is more than 8 (in
-// log2) above it: weights stay below 2^8.
+//   over.  kFine (float16 queries, float32 results): weights are the sum of two
+//   fp16 values (22 bits, 2^-25 of the reference at worst), a product each; one
+//   alone would double the error of a float16 result.  For a bfloat16 result,
+//   rounded eight times as coarsely, one is taken, and the sum of weights is
+//   that of the rounded ones.
+// The reference m of a row starts kLift (in log2) under its first largest score
+// and is raised when a score is more than kSpan above it: weights stay below
+// 2^14, and what they lose in fp16 is small against the largest.
+//
+// Bound: a decode step of 64 sequences of up to 32k tokens, 8 heads of keys,
+// reads 1.26 GB in 233 us, 5.4 TB/s, 80 % of a copy's rate (float16 results: 262
+// us, for their second product).  There the warps' instructions bound it as much
+// as memory does: what cut instructions cut time (347 us at first; 250 with
+// scales by pairs of tiles, the offset by a product and steps of two tiles; 244
+// and 233 with fewer stores and pages looked up ahead).  Four warps to a CTA,
+// three CTAs to an SM for eight rows, two for sixteen; a ring of three or four
+// steps for each warp.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -51,7 +65,7 @@ constexpr int kWarps = 4;
 constexpr int kStep = 2 * kTokens;   // keys that a warp takes at a time
 constexpr float kLift = 7.f, kSpan = 14.f;   // a row's reference is 7 (in log2) under its largest score at first, 14 at most
 constexpr float kNone = -3.402823466e38f;   // the reference before any score: no score is under it but -Inf
-constexpr int kLeast = 2;   // tiles to a run, where there are too few for all warps
+constexpr int kLeast = 2;   // steps to a run, where there are too few for all warps
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -797,7 +811,9 @@ int sm_count() {
     return n;
 }
 
-// Eight rows to a unit where a sequence has no more on average, else sixteen.
+// Eight rows to a unit where a sequence has no more on average, else sixteen.  33 sequences of 5001 tokens, four heads
+// of keys, seven rows each: 35 us, and 47 by units of sixteen; 14 rows: 50 us by twice as many units of eight, and 45.
+// 64 sequences of 32k tokens, four rows: 235 and 327; sixteen rows: 466 and 336.
 bool narrow(const mmq_kv4_attention_t& p) { return p.tokens * (p.heads / p.kv_heads) <= int64_t(8) * p.batch; }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -832,16 +848,22 @@ cudaError_t launch(const Kv4Args& a, int nsm, cudaStream_t s) {
 
 namespace {
 
-// A sequence of up to so many rows is the few-row kernel's.
-constexpr int kFew = 16;
-
 struct Forms {
     bool few, many, two;   // which kernels a call may need; two: units of 256 rows
+    int most_few;          // a sequence of up to so many rows is the few-row kernel's
 };
 Forms forms(const mmq_kv4_attention_t& p) {
     const int64_t group = p.heads / p.kv_heads, rows = p.tokens * group;   // of all sequences
     const int64_t most = p.q_starts ? rows : rows / p.batch;               // of one, at most
-    return Forms{p.q_starts || most <= kFew, most > kFew, rows > int64_t(128) * p.batch};
+    // 33 sequences of 5001 tokens, four heads of keys, alike: 14 rows 43 us by units of sixteen and 62 by the other kernel;
+    // 21 rows 56 and 63, 35 rows 143 and 70.  A ragged batch costs the time of two kernels where it has rows for both: one
+    // to five tokens (7 to 35 rows) 86 us cut at 16 rows, 100 at 24, 80 at 40.  So where the average tells that most are
+    // few, the cut is high.
+    const bool mostly_few = rows <= int64_t(24) * p.batch;
+    const int most_few = p.q_starts ? mostly_few ? 40 : 16 : 24;
+    // 256 rows: chunks of 2047 tokens 684 us, and 1082 by units of 128; 64 tokens of 8 sequences, 256 rows each, 70 and 95.
+    // Up to 128 rows: 128 rows 99 us, and 110 by a unit of 256 that is half empty; 35 rows 70 and 99.
+    return Forms{p.q_starts || most <= most_few, most > most_few, rows > int64_t(128) * p.batch, most_few};
 }
 size_t all_part_bytes(const mmq_kv4_attention_t& p, int nsm) {
     const Forms f = forms(p);
@@ -862,7 +884,10 @@ cudaError_t launch_kv4_join(const Kv4Args& a, int R, int runs, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = s;
-    const bool share = R <= 16;
+    // Many parts to a unit (its share of the runs), so that a warp alone would take them one after the other: one sequence
+    // of 32k tokens 27 us, and 36 by a warp per row.  Else a warp per row is the faster: 33 sequences of one to five
+    // tokens 82 us shared and 78 not, 64 of 32k tokens 235 and 233.
+    const bool share = R <= 16 && int64_t(a.p.batch) * a.p.kv_heads * 4 <= runs;
     cfg.gridDim = dim3(unsigned(runs), unsigned(share ? R : R / kJoinRows));
     cfg.blockDim = dim3(kJoinRows * 32);
     if (a.p.head_dim == 64)
@@ -891,8 +916,8 @@ cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, 
     a.scale_log2 = p.scale * 1.4426950408889634f;
     a.low = 0x000F000Fu;
     a.high = 0x00F000F0u;
-    a.few = kFew;
     const Forms f = forms(p);
+    a.few = f.most_few;
     if (f.few) {
         cudaError_t e;
         if (p.type == MMQ_TYPE_F16) e = p.head_dim == 64 ? launch<__half, 64>(a, nsm, s) : launch<__half, 128>(a, nsm, s);

@@ -1,8 +1,8 @@
 // Attention over a 4-bit paged cache on the tensor cores: sequences with many
 // rows (a chunk of a prompt, or a speculative step of a wide group).
 //
-// A unit is 128 or 256 rows of one sequence's kv head.  Per 128 keys it takes
-// two products of 128 rows x 128 keys x D for each 128 rows, S = Q K^T and
+// A unit is 128 or 256 rows of one sequence's kv head.  Per tile of 64 keys it
+// takes two products of 128 rows x 64 keys x D for each 128 rows, S = Q K^T and
 // O += P V with P = 2^(S f - m) as fp16, the rest f32; the keys and values, (code
 // - 8) * scale, are exact in fp16, so that P's rounding is the only one beside the
 // result's.  Q is fp16: a bfloat16 row with its largest element in [2^13,
@@ -20,8 +20,22 @@
 // Runs of equal length of all units' key tiles are the CTAs' work, as in the
 // few-row kernel; the parts of units that lie in several runs are joined by a
 // second kernel.  kTwo: 256 rows to a unit, both groups share each key tile,
-// expanded once, and their issuers take turns (as in attention_tc.cu, where the
-// reason is measured).  Else 128 rows, and each group has a run of its own.
+// expanded once.  Else 128 rows, and each group has a run of its own.
+//
+// S has two buffers: a group's softmax works on one tile while the next one's
+// product is made.  What is expanded goes to a slot each for keys and for
+// values, so that the two are not tied to one another.
+//
+// Bound: neither rate.  A chunk of 3 x 2047 tokens over up to 12k (32 heads, 8
+// of keys, D = 128) takes 637 us, 950 TFLOP/s, half the products' measured rate.
+// A tile's chain, scores to softmax to product, has 2300 cycles, of which its
+// products take 1700; with the exponentials or the expansion left out it was
+// hardly faster: what the roles wait for one another bounds it.  Few rows (33
+// sequences, 35 rows, 5001 tokens: 70 us) pay for the expansion of every key
+// with products that are a quarter full.  Tiles of 128 keys with one buffer of
+// scores: 706 us for the chunk against 704, and 87 against 70 for the few rows;
+// keys and values expanded by one warpgroup: 706 against 693 then.  Two raw
+// slots: the same as three.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
