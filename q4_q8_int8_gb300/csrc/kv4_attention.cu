@@ -37,13 +37,15 @@
 // 2^14, and what they lose in fp16 is small against the largest.
 //
 // Bound: a decode step of 64 sequences of up to 32k tokens, 8 heads of keys,
-// reads 1.26 GB in 233 us, 5.4 TB/s, 80 % of a copy's rate (float16 results: 262
+// reads 1.26 GB in 225 us, 5.6 TB/s, 83 % of a copy's rate (float16 results: 251
 // us, for their second product).  There the warps' instructions bound it as much
 // as memory does: what cut instructions cut time (347 us at first; 250 with
-// scales by pairs of tiles, the offset by a product and steps of two tiles; 244
-// and 233 with fewer stores and pages looked up ahead).  Four warps to a CTA,
-// three CTAs to an SM for eight rows, two for sixteen; a ring of three or four
-// steps for each warp.
+// scales by pairs of tiles, the offset by a product and steps of two tiles; 233
+// with fewer stores and pages looked up ahead; the rest by equal runs).  Short
+// sequences pay for the chain of loads that each unit starts with: 256 of up to
+// 512 tokens take 46 us, 12 of them their bytes'.  Four warps to a CTA, three
+// CTAs to an SM for eight rows, two for sixteen; a ring of three or four steps
+// for each warp.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,6 +67,10 @@ constexpr int kWarps = 4;
 constexpr int kStep = 2 * kTokens;   // keys that a warp takes at a time
 constexpr float kLift = 7.f, kSpan = 14.f;   // a row's reference is 7 (in log2) under its largest score at first, 14 at most
 constexpr float kNone = -3.402823466e38f;   // the reference before any score: no score is under it but -Inf
+// Steps' time that a unit costs whatever its length: the chain of its first loads takes 5000 to 8000 cycles and its results'
+// stores as many, a step 2600.  Units as long as their steps alone: 256 sequences of up to 512 tokens 66 us, and 46; of 3, 7
+// and 12 in place of 5: 47, 46 and 45, but 64 sequences of 32k tokens 228, 226 and 229, and 226 by 5.
+constexpr int kIdle = 5;
 constexpr int kLeast = 2;   // steps to a run, where there are too few for all warps
 
 __device__ __forceinline__ float ex2(float x) {
@@ -196,9 +202,9 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ struct {
         int64_t total[kWarps];
-        int64_t first[kWarps + 1];      // each warp's first tile of all
-        int b[kWarps];                  // the sequence it lies in
-        int64_t offset[kWarps];         // and its place there
+        int64_t first[kWarps + 1];      // where each warp's run starts, and the next CTA's first
+        int b[kWarps + 1];              // the sequence it lies in
+        int64_t offset[kWarps + 1];     // and its place there
         // the parts of each warp, its first and its last: the unit's name or -1, whether it starts and ends there
         int64_t name[2 * kWarps];
         int whole[2 * kWarps];          // bit 0: starts, bit 1: ends
@@ -220,29 +226,32 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     griddep_launch_dependents();
     griddep_wait();
 
-    // ---- who does what: a scan over the sequences' tiles
+    // ---- who does what: a scan over the sequences
     const int per = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
     const int b0 = min(p.batch, int(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
-    auto steps_of = [&](const Sequence& s) {   // of one head
-        return int64_t(s.n) * a.group > a.few ? 0 : head_steps<R, kStep>(s, a.group);
+    auto length_of = [&](const Sequence& s) {   // of one head
+        return int64_t(s.n) * a.group > a.few ? 0 : head_length<R, kStep, kIdle>(s, a.group);
     };
     int64_t mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
+    for (int b = b0; b < b1; ++b) mine += length_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
     const int64_t x1 = cta_scan<kWarps>(mine, sh.total, total), x0 = x1 - mine;
     const Runs runs(total, max(int64_t(1), min(int64_t(gridDim.x) * kWarps, total / kLeast)));
     for (int w = 0; w <= kWarps; ++w) {
         const int64_t at = runs.start(int64_t(blockIdx.x) * kWarps + w);
-        if (threadIdx.x == 0) sh.first[w] = at;
-        if (w < kWarps && x0 <= at && at < x1) {   // of one thread
+        if (threadIdx.x == 0 && at >= total) sh.first[w] = total;
+        if (x0 <= at && at < x1) {   // of one thread
             int64_t x = x0;
             for (int b = b0; b < b1; ++b) {
-                const int64_t n = steps_of(sequence(a, b, false)) * p.kv_heads;
-                if (at < x + n) {
+                const Sequence s = sequence(a, b, false);
+                const int64_t each = length_of(s);
+                if (at < x + each * p.kv_heads) {
+                    const int moved = cut<R, kStep, kIdle>(s, a.group, each, at - x).moved;
+                    sh.first[w] = at - moved;
                     sh.b[w] = b;
-                    sh.offset[w] = at - x;
+                    sh.offset[w] = at - moved - x;
                     break;
                 }
-                x += n;
+                x += each * p.kv_heads;
             }
         }
     }
@@ -258,7 +267,8 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     };
     int stage = 0, fill = 0, flying = 0;   // the ring's next step to take, to fill, and those under way
     uint32_t phase = 0;
-    bool withheld = a.inject && blockIdx.x == 0 && warp == 0;   // test hook: the first copies never come
+    const bool inject = a.inject && at == 0 && end > 0;   // test hook: the first copies never come
+    bool withheld = inject;
     bool ok = true, bad_page = false;
     // The masks are kernel arguments so that they stay in registers: an instruction takes one constant, the other bits.
     const uint32_t low = a.low, high = a.high;   // 0x000F000F, 0x00F000F0
@@ -267,24 +277,17 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
 
     while (at < end && ok) {
         const Sequence s = sequence(a, b, false);
-        const int64_t each = steps_of(s);
+        const int64_t each = length_of(s);
         if (offset >= each * p.kv_heads) {   // also a sequence without rows
             ++b;
             offset = 0;
             continue;
         }
-        Unit u;
-        u.b = b;
-        u.h = int(offset / each);
-        int64_t in_head = offset - u.h * each;
-        u.tile = 0;
-        int tiles;
-        while (in_head >= (tiles = unit_steps<R, kStep>(s, a.group, u.tile))) {
-            in_head -= tiles;
-            ++u.tile;
-        }
-        const int t0 = int(in_head), t1 = int(min(int64_t(tiles), t0 + (end - at)));
-        const int64_t name = at - t0;        // the unit's first tile of all
+        const Cut from = cut<R, kStep, kIdle>(s, a.group, each, offset);   // not moved: it has been, or is a unit's start
+        const Unit u{b, from.h, from.u};
+        const int length = unit_length<R, kStep, kIdle>(s, a.group, u.tile), upto = int(min(int64_t(length), from.in + (end - at)));
+        const int t0 = max(0, from.in - kIdle), t1 = upto - kIdle;
+        const int64_t name = at - from.in;   // the unit's place
         const int row0 = u.tile * R;   // first row of the unit
 
         const int most = min(unit_keys<R>(s, a.group, u.tile), t1 * kStep);   // that the unit's last row sees of these
@@ -609,9 +612,9 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], d);
 
-        at += t1 - t0;
-        offset += t1 - t0;
-        const bool starts = t0 == 0, ends = t1 == tiles;
+        at += upto - from.in;
+        offset += upto - from.in;
+        const bool starts = t0 == 0, ends = upto == length;
         if (starts && ends) {
             float inv[NT][2];
 #pragma unroll
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
     }
     if (bad_page) atomicCAS(a.status, 0, MMQ_ERR_ARG);
     // After a wait that ran out: the copies still in flight.
-    for (bool never = a.inject && blockIdx.x == 0 && warp == 0; flying > 0; --flying, never = false) {
+    for (bool never = inject; flying > 0; --flying, never = false) {
         if (!never) wait_drain(bars + 8u * uint32_t(stage), phase, a.status);
         stage = stage + 1 == kStages ? 0 : stage + 1;
         phase ^= stage == 0 ? 1u : 0u;
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
             } else {
                 join.keep(a, int64_t(blockIdx.x) * 2 + (starts ? 1 : 0));
                 if (starts) {
-                    const int64_t end = name + unit_steps<R, kStep>(sequence(a, u.b, false), a.group, u.tile);
+                    const int64_t end = name + unit_length<R, kStep, kIdle>(sequence(a, u.b, false), a.group, u.tile);
                     mark = Mark{int(runs.of(end - 1) / kWarps), u.b, u.h, u.tile};
                 }
             }
@@ -811,10 +814,17 @@ int sm_count() {
     return n;
 }
 
-// Eight rows to a unit where a sequence has no more on average, else sixteen.  33 sequences of 5001 tokens, four heads
-// of keys, seven rows each: 35 us, and 47 by units of sixteen; 14 rows: 50 us by twice as many units of eight, and 45.
-// 64 sequences of 32k tokens, four rows: 235 and 327; sixteen rows: 466 and 336.
-bool narrow(const mmq_kv4_attention_t& p) { return p.tokens * (p.heads / p.kv_heads) <= int64_t(8) * p.batch; }
+// A ragged batch of more than eight tokens a sequence on average, which is taken to hold chunks, and single tokens beside.
+bool mixed(const mmq_kv4_attention_t& p) { return p.q_starts && p.tokens > int64_t(8) * p.batch; }
+
+// Eight rows to a unit where a sequence has no more on average, else sixteen.  33 sequences of 5001 tokens, four heads of
+// keys: seven rows 30 us, and 34 by units of sixteen; 14 rows 40 by twice as many units of eight, and 35.  64 sequences of
+// 32k tokens: four rows 226 and 311, sixteen 432 and 313.  Beside chunks the others are taken to have one token: 60 of 4096
+// tokens, four rows, and two chunks of 500: 158 and 169.
+bool narrow(const mmq_kv4_attention_t& p) {
+    const int64_t group = p.heads / p.kv_heads;
+    return p.tokens * group <= int64_t(8) * p.batch || (mixed(p) && group <= 8);
+}
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -855,15 +865,17 @@ struct Forms {
 Forms forms(const mmq_kv4_attention_t& p) {
     const int64_t group = p.heads / p.kv_heads, rows = p.tokens * group;   // of all sequences
     const int64_t most = p.q_starts ? rows : rows / p.batch;               // of one, at most
-    // 33 sequences of 5001 tokens, four heads of keys, alike: 14 rows 43 us by units of sixteen and 62 by the other kernel;
-    // 21 rows 56 and 63, 35 rows 143 and 70.  A ragged batch costs the time of two kernels where it has rows for both: one
-    // to five tokens (7 to 35 rows) 86 us cut at 16 rows, 100 at 24, 80 at 40.  So where the average tells that most are
-    // few, the cut is high.
+    // 33 sequences of 5001 tokens, four heads of keys, alike: 21 rows 51 us by two units of sixteen and 62 by the other
+    // kernel, 35 rows 64 and 61.  A ragged batch costs the time of two kernels where it has rows for both: 48 sequences of
+    // 8192 tokens, one to eight new ones, four rows each, 159 us cut at 16 rows, 146 at 24, 126 at 40.  So where the average
+    // tells that most are few, the cut is high.
     const bool mostly_few = rows <= int64_t(24) * p.batch;
     const int most_few = p.q_starts ? mostly_few ? 40 : 16 : 24;
-    // 256 rows: chunks of 2047 tokens 684 us, and 1082 by units of 128; 64 tokens of 8 sequences, 256 rows each, 70 and 95.
-    // Up to 128 rows: 128 rows 99 us, and 110 by a unit of 256 that is half empty; 35 rows 70 and 99.
-    return Forms{p.q_starts || most <= most_few, most > most_few, rows > int64_t(128) * p.batch, most_few};
+    // 256 rows: chunks of 2047 tokens 662 us, and 1127 by units of 128; 64 tokens of 8 sequences, 256 rows each, 65 and 93.
+    // Up to 128 rows: 128 rows 97 us, and 103 by a unit of 256 that is half empty; 35 rows 61 and 71.  Two chunks of 500
+    // tokens beside 60 single ones: 128 and 169.
+    const bool two = rows > int64_t(128) * p.batch || mixed(p);
+    return Forms{p.q_starts || most <= most_few, most > most_few, two, most_few};
 }
 size_t all_part_bytes(const mmq_kv4_attention_t& p, int nsm) {
     const Forms f = forms(p);
@@ -886,7 +898,7 @@ cudaError_t launch_kv4_join(const Kv4Args& a, int R, int runs, cudaStream_t s) {
     cfg.stream = s;
     // Many parts to a unit (its share of the runs), so that a warp alone would take them one after the other: one sequence
     // of 32k tokens 27 us, and 36 by a warp per row.  Else a warp per row is the faster: 33 sequences of one to five
-    // tokens 82 us shared and 78 not, 64 of 32k tokens 235 and 233.
+    // tokens 74 us shared and 69 not, 64 of 32k tokens 228 and 226.
     const bool share = R <= 16 && int64_t(a.p.batch) * a.p.kv_heads * 4 <= runs;
     cfg.gridDim = dim3(unsigned(runs), unsigned(share ? R : R / kJoinRows));
     cfg.blockDim = dim3(kJoinRows * 32);

@@ -3,8 +3,11 @@
 //
 // Rows are the (new token, head of the group) pairs of one kv head, row r of a
 // sequence being token r / group.  R rows make a unit, which needs every step
-// of kStep keys that its last row sees.  All units' steps, sequence by
-// sequence, head by head, unit by unit, are cut into runs of equal length.
+// of kStep keys that its last row sees.  All units, sequence by sequence, head
+// by head, are laid out one after the other, each kIdle long for what it costs
+// whatever its length (its rows' loads and stores) and one for each step, and
+// cut into runs of equal length.  A cut at a unit's first step or before it is
+// moved to the unit's start.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -89,19 +92,40 @@ template <int R, int kStep>
 __device__ __forceinline__ int unit_steps(const Sequence& s, int group, int u) {
     return max(1, (unit_keys<R>(s, group, u) + kStep - 1) / kStep);
 }
-template <int R, int kStep>
-__device__ __forceinline__ int64_t head_steps(const Sequence& s, int group) {
+// A unit's length in the layout, and that of one head's units.
+template <int R, int kStep, int kIdle>
+__device__ __forceinline__ int unit_length(const Sequence& s, int group, int u) {
+    return kIdle + unit_steps<R, kStep>(s, group, u);
+}
+template <int R, int kStep, int kIdle>
+__device__ __forceinline__ int64_t head_length(const Sequence& s, int group) {
     int64_t n = 0;
     const int m = units<R>(s, group);
-    for (int u = 0; u < m; ++u) n += unit_steps<R, kStep>(s, group, u);
+    for (int u = 0; u < m; ++u) n += unit_length<R, kStep, kIdle>(s, group, u);
     return n;
 }
-// Runs that share `total` steps: the first `longer` of them have one more than the others.
+// A cut `at` past the start of a sequence whose heads are `each` long: its head and unit, how far it lies in that one,
+// and by how much it was moved.
+struct Cut {
+    int h, u, in, moved;
+};
+template <int R, int kStep, int kIdle>
+__device__ __forceinline__ Cut cut(const Sequence& s, int group, int64_t each, int64_t at) {
+    Cut c;
+    c.h = int(at / each);
+    int64_t in_head = at - c.h * each;
+    c.u = 0;
+    for (int length; in_head >= (length = unit_length<R, kStep, kIdle>(s, group, c.u)); ++c.u) in_head -= length;
+    c.moved = in_head <= kIdle ? int(in_head) : 0;
+    c.in = int(in_head) - c.moved;
+    return c;
+}
+// Runs that share a layout of length `total`: the first `longer` of them have one more than the others.
 struct Runs {
     int64_t total, each, longer;
     __device__ __forceinline__ Runs(int64_t total, int64_t runs) : total(total), each(total / runs), longer(total - each * runs) {}
     __device__ __forceinline__ int64_t start(int64_t run) const { return min(total, run * each + min(run, longer)); }
-    // The run that step `at` lies in.
+    // The run that place `at` lies in.
     __device__ __forceinline__ int64_t of(int64_t at) const {
         const int64_t first = longer * (each + 1);
         return at < first ? at / (each + 1) : longer + (at - first) / each;

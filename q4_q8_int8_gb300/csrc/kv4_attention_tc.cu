@@ -27,13 +27,13 @@
 // values, so that the two are not tied to one another.
 //
 // Bound: neither rate.  A chunk of 3 x 2047 tokens over up to 12k (32 heads, 8
-// of keys, D = 128) takes 637 us, 950 TFLOP/s, half the products' measured rate.
+// of keys, D = 128) takes 610 us, 990 TFLOP/s, half the products' measured rate.
 // A tile's chain, scores to softmax to product, has 2300 cycles, of which its
 // products take 1700; with the exponentials or the expansion left out it was
 // hardly faster: what the roles wait for one another bounds it.  Few rows (33
-// sequences, 35 rows, 5001 tokens: 70 us) pay for the expansion of every key
+// sequences, 35 rows, 5001 tokens: 61 us) pay for the expansion of every key
 // with products that are a quarter full.  Tiles of 128 keys with one buffer of
-// scores: 706 us for the chunk against 704, and 87 against 70 for the few rows;
+// scores: 706 us for the chunk against 704, and 87 against 70 for the few rows, then;
 // keys and values expanded by one warpgroup: 706 against 693 then.  Two raw
 // slots: the same as three.
 #include <cuda_bf16.h>
@@ -67,23 +67,26 @@ __device__ __forceinline__ float reference(float m) { return fabsf(m) < kWide ? 
 
 __device__ __align__(16) const uint8_t zero_tiles[kKeys / kTokens * tile_bytes(128)] = {};   // of a page that does not exist
 
-// Where a run starts: tile t of unit u of head h of sequence b, and its length.
+// Tiles' time that a unit costs whatever its length.  256 rows: chunks of 512 tokens 371 us with none, 356, 342, 335 and 341
+// with 2, 4, 8 and 12.  128: 33 sequences of 35 rows 70 with none, 64, 61, 62.5 and 65.
+__host__ __device__ constexpr int idle(int R) { return R > kRows ? 8 : 4; }
+
+// Where a run starts in the layout and where the next does, and in it: place t of unit u of head h of sequence b.
 struct Start {
-    int64_t steps, first;   // first: the run's first step of all
+    int64_t first, end;
     int b, h, u, t;
 };
 
-// A run's units one after the other, each with the key tiles [t, t1) that the run has of it.
+// A run's units one after the other, each with the places [t, t1) that the run has of it.
 template <int R>
 struct Walk {
     const Kv4Args& a;
-    int64_t left, name;   // steps after this piece; the unit's first step of all
+    int64_t left, name;   // length after this piece; the unit's place
     Sequence s;
-    int b, h, u, t, t1, steps;
-    bool starts;          // the unit's first tile is this piece's
+    int b, h, u, t, t1, length;
 
     __device__ __forceinline__ Walk(const Kv4Args& args, const Start& from) : a(args) {
-        left = from.steps;
+        left = from.end - from.first;
         b = from.b;
         h = from.h;
         u = from.u;
@@ -95,20 +98,22 @@ struct Walk {
         }
     }
     __device__ __forceinline__ bool valid() const { return t < t1; }
-    __device__ __forceinline__ bool ends() const { return t1 == steps; }
+    __device__ __forceinline__ int first_tile() const { return max(0, t - idle(R)); }
+    __device__ __forceinline__ int end_tile() const { return t1 - idle(R); }
+    __device__ __forceinline__ bool starts() const { return t == 0; }
+    __device__ __forceinline__ bool ends() const { return t1 == length; }
     __device__ __forceinline__ int most() const { return unit_keys<R>(s, a.group, u); }     // keys that its last row sees
     __device__ __forceinline__ int least() const { return seen(s, u * R / a.group); }       // and its first
     __device__ __forceinline__ void begin(int from) {
-        steps = unit_steps<R, kKeys>(s, a.group, u);
-        starts = from == 0;
+        length = unit_length<R, kKeys, idle(R)>(s, a.group, u);
         t = from;
-        t1 = int(min(int64_t(steps), from + left));
+        t1 = int(min(int64_t(length), from + left));
         left -= t1 - t;
     }
     __device__ __forceinline__ void next() {   // the next piece
         t = t1;
         if (left == 0) return;
-        name += steps;
+        name += length;
         if (++u == units<R>(s, a.group)) {
             u = 0;
             if (++h == a.p.kv_heads) {
@@ -118,9 +123,6 @@ struct Walk {
             }
         }
         begin(0);
-    }
-    __device__ __forceinline__ void step() {   // the next tile
-        if (++t == t1) next();
     }
 };
 
@@ -263,39 +265,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     // ---- who does what
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(p.batch, int(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
-    auto steps_of = [&](const Sequence& s) {   // of one head
-        return int64_t(s.n) * a.group <= a.few ? 0 : head_steps<kR, kKeys>(s, a.group);
+    auto length_of = [&](const Sequence& s) {   // of one head
+        return int64_t(s.n) * a.group <= a.few ? 0 : head_length<kR, kKeys, idle(kR)>(s, a.group);
     };
     int64_t mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += steps_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
+    for (int b = b0; b < b1; ++b) mine += length_of(sequence(a, b, blockIdx.x == 0)) * p.kv_heads;
     const int64_t x1 = cta_scan<kThreads / 32>(mine, sums, total), x0 = x1 - mine;
     const Runs runs(total, max(int64_t(1), min(int64_t(gridDim.x) * kStreams, total)));
     if (threadIdx.x < kStreams) a.marks[blockIdx.x + threadIdx.x * gridDim.x] = Mark{-1, 0, 0, 0};
 
-#pragma unroll
-    for (int st = 0; st < kStreams; ++st) {
-        const int64_t run = blockIdx.x + int64_t(st) * gridDim.x;
-        const int64_t lo = runs.start(run), hi = runs.start(run + 1);
-        if (threadIdx.x == 0) {
-            from[st].steps = hi - lo;
-            from[st].first = lo;
-        }
-        if (lo < hi && x0 <= lo && lo < x1) {   // of one thread
+#pragma unroll 1
+    for (int i = 0; i < 2 * kStreams; ++i) {   // where each stream's run starts and where the next one does
+        const int st = i >> 1;
+        const int64_t at = runs.start(blockIdx.x + int64_t(st) * gridDim.x + (i & 1));
+        int64_t& place = i & 1 ? from[st].end : from[st].first;
+        if (threadIdx.x == 0 && at >= total) place = total;
+        if (x0 <= at && at < x1) {   // of one thread
             int64_t x = x0;
             for (int b = b0; b < b1; ++b) {
                 const Sequence s = sequence(a, b, false);
-                const int64_t each = steps_of(s);
-                if (lo < x + each * p.kv_heads) {
-                    int64_t in_head = (lo - x) % each;
-                    int u = 0, steps;
-                    while (in_head >= (steps = unit_steps<kR, kKeys>(s, a.group, u))) {
-                        in_head -= steps;
-                        ++u;
+                const int64_t each = length_of(s);
+                if (at < x + each * p.kv_heads) {
+                    const Cut c = cut<kR, kKeys, idle(kR)>(s, a.group, each, at - x);
+                    place = at - c.moved;
+                    if ((i & 1) == 0) {
+                        from[st].b = b;
+                        from[st].h = c.h;
+                        from[st].u = c.u;
+                        from[st].t = c.in;
                     }
-                    from[st].b = b;
-                    from[st].h = int((lo - x) / each);
-                    from[st].u = u;
-                    from[st].t = int(in_head);
                     break;
                 }
                 x += each * p.kv_heads;
@@ -450,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         if (warp == kWarpFetch) {
             // ------------------------------------------------------ raw tiles
             uint32_t issued = 0, parity = 0;   // slots with a copy, the parity of its arrival
-            bool withhold = a.inject && blockIdx.x == 0;
+            bool withhold = false;   // test hook: the first copy never comes
+            for (int st = 0; st < kStreams; ++st) withhold |= a.inject && from[st].first == 0 && from[st].end > 0;
             const int tile_shift = a.page_shift - 4;
             constexpr int kOf = kKeys / kTokens;   // tiles of 16
             // A copy takes as many of a key tile's tiles of 16 as lie on one page, up to all; lane i issues the i-th.
@@ -569,15 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             for (uint32_t i = 0;; ++i) {
                 if (!wait_bounded(done_with(lane, i), ((i / kPieces) & 1u) ^ 1u, abort_flag, status)) break;
                 Piece& to = piece_at(lane, i);
-                to.t0 = q.t;
-                to.t1 = q.t1;
+                to.t0 = to.t1 = 0;
                 if (q.valid()) {
+                    to.t0 = q.first_tile();
+                    to.t1 = q.end_tile();
                     to.start = q.s.start;
-                    to.last = int(runs.of(q.name + q.steps - 1));
+                    to.last = int(runs.of(q.name + q.length - 1));
                     to.b = q.b;
                     to.h = q.h;
                     to.u = q.u;
-                    to.starts = q.starts;
+                    to.starts = q.starts();
                     to.ends = q.ends();
                     to.n = q.s.n;
                     to.len = q.s.len;
