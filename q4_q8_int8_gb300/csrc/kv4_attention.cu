@@ -326,25 +326,35 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
             ++flying;
             ++next;
         };
-        for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
-
-        // Queries: lane's row is r8 (of each eight), its dimensions 2 c, 2 c + 1 and those + 8 of every 16.
-        uint32_t qf[NT][D / 16][2];
-        uint32_t qs[NT][2];            // -8 sum q' of each block, times 2^112, as an operand
-        float f[NT][2];
-        int see[NT][2];
+        // Queries: lane's row is r8 (of each eight), its dimensions 2 c, 2 c + 1 and those + 8 of every 16.  On their way
+        // beside the pages' numbers.
+        uint32_t raw[NT][D / 16][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = row0 + 8 * nt + r8, j = row / a.group;
             const bool has = j < s.n;
             const T* src = static_cast<const T*>(p.q) + (s.start + (has ? j : 0)) * p.q_stride +
                            (int64_t(u.h) * a.group + (has ? row - j * a.group : 0)) * D + 2 * c4;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) raw[nt][i][k] = has ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8 * k) : 0u;
+        }
+        for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
+
+        uint32_t qf[NT][D / 16][2];
+        uint32_t qs[NT][2];            // -8 sum q' of each block, times 2^112, as an operand
+        float f[NT][2];
+        int see[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int j = (row0 + 8 * nt + r8) / a.group;
+            const bool has = j < s.n;
             float x[D / 16][4];
             float top = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                const uint32_t lo = has ? *reinterpret_cast<const uint32_t*>(src + 16 * i) : 0u;
-                const uint32_t hi = has ? *reinterpret_cast<const uint32_t*>(src + 16 * i + 8) : 0u;
+                const uint32_t lo = raw[nt][i][0], hi = raw[nt][i][1];
                 if (std::is_same<T, __half>::value) {
                     const float2 u0 = __half22float2(u2h(lo)), u1 = __half22float2(u2h(hi));
                     x[i][0] = u0.x; x[i][1] = u0.y; x[i][2] = u1.x; x[i][3] = u1.y;
@@ -925,6 +935,7 @@ cudaError_t launch_kv4_attention(const mmq_kv4_attention_t& p, void* workspace, 
     a.page_shift = 0;
     while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
     a.group = p.heads / p.kv_heads;
+    a.each = p.batch ? int(p.tokens / p.batch) : 0;
     a.scale_log2 = p.scale * 1.4426950408889634f;
     a.low = 0x000F000Fu;
     a.high = 0x00F000F0u;

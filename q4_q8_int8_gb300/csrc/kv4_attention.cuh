@@ -26,6 +26,7 @@ struct Kv4Args {
     int* status;
     int inject;
     int page_shift, group;
+    int each;             // without q_starts: new tokens of every sequence
     float scale_log2;
     uint32_t low, high;   // masks of codes: 0x000F000F, 0x00F000F0
     int few;              // sequences of up to so many rows are the few-row kernel's, others the tensor-core kernel's
@@ -66,7 +67,7 @@ __device__ __forceinline__ Sequence sequence(const Kv4Args& a, int b, bool tell)
         s.start = lo;
         s.n = bad ? 0 : int(hi - lo);
     } else {
-        s.n = int(p.tokens / p.batch);
+        s.n = a.each;
         s.start = int64_t(b) * s.n;
     }
     const int64_t room = p.table_width << a.page_shift, len = p.lens[b];
@@ -78,14 +79,15 @@ __device__ __forceinline__ Sequence sequence(const Kv4Args& a, int b, bool tell)
 // Keys that new token j of a sequence sees.
 __device__ __forceinline__ int seen(const Sequence& s, int j) { return max(0, s.len - s.n + 1 + j); }
 
+// (A sequence's rows are fewer than 2^31, as the arguments' check has it.)
 template <int R>
 __device__ __forceinline__ int units(const Sequence& s, int group) {
-    return int((int64_t(s.n) * group + R - 1) / R);
+    return int((uint32_t(s.n) * uint32_t(group) + (R - 1)) / R);
 }
 // Keys that the unit's last row sees, the most of all.
 template <int R>
 __device__ __forceinline__ int unit_keys(const Sequence& s, int group, int u) {
-    return seen(s, int(min(int64_t(s.n) - 1, (int64_t(u) * R + R - 1) / group)));
+    return seen(s, min(s.n - 1, int((uint32_t(u) * R + (R - 1)) / uint32_t(group))));
 }
 // Steps of kStep keys of one unit, at least one: a unit without keys still has zeros to write.
 template <int R, int kStep>
