@@ -437,9 +437,9 @@ int mmq_status(void* stream);
 const char* mmq_strerror(int code);
 
 /* Programmatic dependent launch (process-wide, default off): when enabled,
- * the q8_1 prepass, the GEMM kernels (few-token and tcgen05), the head norms
- * and the first kernel of an attention or mixture-of-experts call are launched
- * so that each may start while the previous kernel on its stream finishes.
+ * the q8_1 prepass, the GEMM kernels (few-token and tcgen05), the head norms,
+ * the writes, reads and copies of caches and pages and the first kernel of an
+ * attention, compaction or mixture-of-experts call are launched so that each may start while the previous kernel on its stream finishes.
  * (The later kernels of such a call always are; they belong to the call.)
  * A kernel so launched issues only its weight loads (or, for the tcgen05
  * kernel, only its set-up) before it waits for the previous grid to
@@ -681,8 +681,13 @@ size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
  * and zeros for a token that sees no key.  n may differ from sequence to
  * sequence and be zero.  Rows of q that belong to no sequence are not read and
  * those of out are left as they were.  What the cache holds past a token's last
- * key is never used, whatever it is.  Results are bitwise the same run to run
- * on one device and build.  A length over table_width * page_size is cut to
+ * key is never used, whatever it is.  Scores, maxima and sums are float32.
+ * Weights exp(s - m) are rounded to float16 for their product with the values
+ * (errors of 2^-12 of a result at most, beside its own rounding); in the form
+ * for few rows (a sequence's tokens times heads / kv_heads up to 16, or up to 40
+ * by the batch's average) they have 22 bits where type or out_type shows it.
+ * Results are bitwise the same run to run on one device and build, but depend
+ * in their last bits on the other sequences of the batch (how its work is cut).  A length over table_width * page_size is cut to
  * it, a page number outside [0, n_pages) stands for a page of zeros, and a
  * sequence whose q_starts do not lie in order within [0, tokens] is left out;
  * each sets the device status word to MMQ_ERR_ARG.
@@ -758,8 +763,8 @@ int mmq_pages_compact(const mmq_pages_compact_t* p, void* workspace, size_t work
 int mmq_debug_force_gemv_split(int ks);
 
 /* Test hook: when nonzero, the next launch on this host thread of a
- * tensor-core GEMM, an attention call with a prefix or a mixture of experts
- * withholds one producer arrival so that its consumers' bounded
+ * tensor-core GEMM, an attention call with a prefix or over a 4-bit cache or a
+ * mixture of experts withholds one producer arrival so that its consumers' bounded
  * waits run out; the kernel then records MMQ_ERR_DEVICE_TIMEOUT and returns
  * without hanging.  Used only to test the failure path. */
 void mmq_debug_inject_timeout(int enable);

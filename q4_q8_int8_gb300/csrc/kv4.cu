@@ -7,7 +7,16 @@
 // each rounding to nearest even and the quotient's exactly that of x / d.  A
 // block with a NaN or an infinity has d = NaN.
 //
-// A CTA takes 16 tokens of a head, a thread eight values of one token.
+// A warp takes 16 tokens of a head (of two, for D = 64), keys or values: a lane
+// what its words of the tile hold, so that it puts whole words together, and
+// 32 bytes of a token at a time are one lane's.  Tokens whose tile is not all
+// theirs, in order, go byte by byte.
+//
+// Bound: memory.  32k tokens of 8 heads, D = 128, pages in any order: written
+// from float16 in 31 us, read to float16 in 30 us, 5.5 and 5.8 TB/s, 81 and 85 %
+// of a copy's rate.  (A thread with eight values of one token, bytes put
+// together in shared memory: 45 us for 8192 tokens written and read, now 23,
+// and 61 us for the 32k read.)  Few tokens: 3 us, the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -232,8 +241,7 @@ __device__ __forceinline__ uint2 quantize(const Values<T>& x, __half& scale) {
     return none ? make_uint2(0x88888888u, 0x88888888u) : make_uint2(w[0], w[1]);
 }
 
-// Bound by what it reads and writes where there are many tokens (see the
-// launch's figures), by its latency where there are few.
+// Inputs in 16-byte loads: by 32 bytes, as read() stores, 8192 tokens took 12.2 us in place of 10.8.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const WriteArgs a) {
     const mmq_kv4_write_t& p = a.p;
@@ -311,7 +319,8 @@ __device__ __forceinline__ __half2 expand(uint32_t pair, __half2 scale) {
     const uint32_t w = (pair & 0x000F000Fu) | 0x64006400u;
     return __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1032.f)), scale);
 }
-// 32 bytes, a whole sector, in one store where the address allows it.
+// 32 bytes, a whole sector, in one store where the address allows it: 32k tokens 30 us, and 37 by two of 16 bytes; 8192 as
+// float32 14.5 and 30.5.
 __device__ __forceinline__ void store8(void* at, const uint32_t* w, bool aligned) {
     if (aligned) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
