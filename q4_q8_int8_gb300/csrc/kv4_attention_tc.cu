@@ -186,6 +186,12 @@ __device__ __forceinline__ uint32_t expand_high(uint32_t v, uint32_t scales) {
     asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(d) : "r"(v));
     return h2u(__hmul2(__hsub2(u2h(d), __float2half2_rn(72.f)), u2h(scales)));
 }
+// One thread of the warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 template <int N>
 __device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t* w) {
     if (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     if ((issued >> s) & 1u) wait_drain(raw_full(s), (parity >> s) & 1u, status);
         } else if (warp <= kWarpMma + 1) {
             // ---------------------------------------------------- MMA issuers
-            if (lane == 0) {
+            if (elect_one()) {
                 const int g = warp - kWarpMma, st = kTwo ? 0 : g;
                 constexpr uint32_t kIdQK = idesc_f16_f32(kRows, kKeys), kIdPV = idesc_f16_f32(kRows, D);
                 constexpr uint64_t kTileDesc = uint64_t(L::kTile >> 4);
