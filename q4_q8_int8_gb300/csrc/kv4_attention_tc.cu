@@ -513,18 +513,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             if (elect_one()) {
                 const int g = warp - kWarpMma, st = kTwo ? 0 : g;
                 constexpr uint32_t kIdQK = idesc_f16_f32(kRows, kKeys), kIdPV = idesc_f16_f32(kRows, D);
-                constexpr uint64_t kTileDesc = uint64_t(L::kTile >> 4);
-                const uint64_t dq = smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kQ));
-                const uint64_t slots = smem_desc_sw128(sbase + uint32_t(L::kOffSlots));
+                // Descriptors by their lower words, which hold the address; the upper is the same for all.
+                constexpr uint32_t kTileDesc = uint32_t(L::kTile >> 4);
+                const uint32_t dq = uint32_t(smem_desc_sw128(sbase + uint32_t(L::kOffQ + g * L::kQ)));
+                const uint32_t slots = uint32_t(smem_desc_sw128(sbase + uint32_t(L::kOffSlots)));
+                auto desc = [](uint32_t low) { return (smem_desc_sw128(0) >> 32 << 32) | low; };
                 const uint32_t ts = tmem + kColS + 128u * uint32_t(g), to = tmem + kColO + 128u * uint32_t(g);
                 auto arrived = [&](int kind, uint32_t no) {
                     return wait_bounded(full(slot_of(st, kind, no)), phase_of(no), abort_flag, status);
                 };
-                // A tile's descriptor, opaque so that the loop does not keep one for every product: this thread has few
-                // registers, and of those that went to local memory (128 rows, D = 128) the upper words, which hold the
-                // swizzle and strides, did not reach the products.
-                auto described = [](uint64_t d) {
-                    asm volatile("" : "+l"(d));
+                // A tile's, opaque so that the loop does not keep one for every product: this thread has few registers.
+                auto described = [](uint32_t d) {
+                    asm volatile("" : "+r"(d));
                     return d;
                 };
                 uint32_t no = 0;   // tiles so far, the buffer of S in turn
@@ -533,11 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     if (!arrived(0, i)) return false;
                     tc_fence_after();
                     const int slot = slot_of(st, 0, i);
-                    const uint64_t dk = described(slots + uint64_t(slot) * kTileDesc), dq_now = described(dq);
+                    const uint32_t dk = described(slots + uint32_t(slot) * kTileDesc), dq_now = described(dq);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        mma_f16(ts + 64u * (i & 1u), dq_now + uint64_t(kk >> 2) * uint64_t(kRows * 128 >> 4) + uint64_t((kk & 3) * 2),
-                                dk + uint64_t(kk >> 2) * uint64_t(kKeys * 128 >> 4) + uint64_t((kk & 3) * 2), kIdQK, uint32_t(kk > 0));
+                        mma_f16(ts + 64u * (i & 1u), desc(dq_now + uint32_t((kk >> 2) * (kRows * 128 >> 4) + (kk & 3) * 2)),
+                                desc(dk + uint32_t((kk >> 2) * (kKeys * 128 >> 4) + (kk & 3) * 2)), kIdQK, uint32_t(kk > 0));
                     mma_commit(s_full(g, i));
                     mma_commit(empty(slot));
                     return true;
@@ -556,10 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                         if (!ok) break;
                         tc_fence_after();
                         const int slot = slot_of(st, 1, no);
-                        const uint64_t dv = described(slots + uint64_t(slot) * kTileDesc);
+                        const uint32_t dv = described(slots + uint32_t(slot) * kTileDesc);
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_f16_ta(to, ts + 64u * (no & 1u) + 8u * uint32_t(kk), dv + uint64_t(kk * 2), kIdPV, uint32_t(s > 0 || kk > 0));
+                            mma_f16_ta(to, ts + 64u * (no & 1u) + 8u * uint32_t(kk), desc(dv + uint32_t(kk * 2)), kIdPV, uint32_t(s > 0 || kk > 0));
                         mma_commit(o_done(g));
                         mma_commit(empty(slot));
                         if (s + 2 < tiles) ok = scores(no + 2);
