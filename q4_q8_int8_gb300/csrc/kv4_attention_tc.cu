@@ -151,9 +151,9 @@ struct Layout {
     static constexpr int kOffStart = kOffSums + (kThreads / 32) * 8;
     static constexpr int kOffPieces = kOffStart + 2 * int(sizeof(Start));
     static constexpr int kOffBar = kOffPieces + 2 * kPieces * int(sizeof(Piece));
-    // barriers: raw_full, raw_empty; full, empty per slot; q_full, o_done per group, s_full, p_full per group and
+    // barriers: raw_full, raw_empty; full, empty per slot; q_full per group, o_done, s_full, p_full per group and
     // buffer; drain; told, done per piece
-    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 13 + 4 * kPieces) * 8;
+    static constexpr int kOffMisc = kOffBar + (2 * kRawSlots + 2 * kSlots + 15 + 4 * kPieces) * 8;
     static constexpr int kBytes = kOffMisc + 32 + 1024;
     static constexpr int kR = kTwo ? 2 * kRows : kRows;      // rows of a unit
 };
@@ -212,11 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     auto empty = [&](int s) { return bar0 + 8u * uint32_t(2 * kRawSlots + kSlots + s); };
     const uint32_t bar1 = bar0 + 8u * uint32_t(2 * kRawSlots + 2 * kSlots);
     auto q_full = [&](int g) { return bar1 + 8u * uint32_t(g); };
-    auto o_done = [&](int g) { return bar1 + 8u * uint32_t(2 + g); };
-    auto s_full = [&](int g, uint32_t no) { return bar1 + 8u * (4u + 2u * uint32_t(g) + (no & 1u)); };
-    auto p_full = [&](int g, uint32_t no) { return bar1 + 8u * (8u + 2u * uint32_t(g) + (no & 1u)); };
-    const uint32_t drain = bar1 + 8u * 12u;
-    auto told = [&](int st, uint32_t i) { return bar1 + 8u * (13u + uint32_t(st * kPieces) + i % kPieces); };
+    auto o_done = [&](int g, uint32_t no) { return bar1 + 8u * (2u + 2u * uint32_t(g) + (no & 1u)); };
+    auto s_full = [&](int g, uint32_t no) { return bar1 + 8u * (6u + 2u * uint32_t(g) + (no & 1u)); };
+    auto p_full = [&](int g, uint32_t no) { return bar1 + 8u * (10u + 2u * uint32_t(g) + (no & 1u)); };
+    const uint32_t drain = bar1 + 8u * 14u;
+    auto told = [&](int st, uint32_t i) { return bar1 + 8u * (15u + uint32_t(st * kPieces) + i % kPieces); };
     auto done_with = [&](int st, uint32_t i) { return told(st, i) + 8u * 2u * kPieces; };
     Piece* const pieces = reinterpret_cast<Piece*>(smem + L::kOffPieces);
     auto piece_at = [&](int st, uint32_t i) -> Piece& { return pieces[st * kPieces + int(i % kPieces)]; };
@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(q_full(g), 4);
-            mbar_init(o_done(g), 1);
             for (uint32_t i = 0; i < 2; ++i) {
+                mbar_init(o_done(g, i), 1);
                 mbar_init(s_full(g, i), 1);
                 mbar_init(p_full(g, i), 4);
             }
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
                             mma_f16_ta(to, ts + 64u * (no & 1u) + 8u * uint32_t(kk), desc(dv + uint32_t(kk * 2)), kIdPV, uint32_t(s > 0 || kk > 0));
-                        mma_commit(o_done(g));
+                        mma_commit(o_done(g, no));
                         mma_commit(empty(slot));
                         if (s + 2 < tiles) ok = scores(no + 2);
                     }
@@ -702,10 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             float m = kNone, l = 0.f;
             bool wide = false;
             int n = 0;
-            // The product of the tile before.  Every tile waits for it before it hands P on, long after it has been, so
-            // that o_done is never more than a phase ahead or behind.
+            // The product of the tile before; the one before that has come with the last scores, so that o_done, one for
+            // every other tile, is never two phases off.
             auto await_product = [&]() {
-                ok = __all_sync(0xffffffffu, wait_bounded(o_done(g), (no & 1u) ^ 1u, abort_flag, status));
+                ok = __all_sync(0xffffffffu, wait_bounded(o_done(g, no - 1), ((no - 1) >> 1) & 1u, abort_flag, status));
                 tc_fence_after();
             };
             auto scale_o = [&](float f) {   // O at rest
@@ -773,8 +773,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     }
                     tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);
                 }
-                if (n > 0) await_product();
-                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -824,8 +822,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                     for (int k = 0; k < 16; ++k) pk[k] = pack16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
                     tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);   // over what has been read
                 }
-                if (n > 0) await_product();
-                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
