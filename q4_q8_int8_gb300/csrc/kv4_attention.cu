@@ -37,13 +37,13 @@
 // 2^14, and what they lose in fp16 is small against the largest.
 //
 // Bound: a decode step of 64 sequences of up to 32k tokens, 8 heads of keys,
-// reads 1.26 GB in 225 us, 5.6 TB/s, 83 % of a copy's rate (float16 results: 251
+// reads 1.26 GB in 221 us, 5.7 TB/s, 84 % of a copy's rate (float16 results: 250
 // us, for their second product).  There the warps' instructions bound it as much
 // as memory does: what cut instructions cut time (347 us at first; 250 with
 // scales by pairs of tiles, the offset by a product and steps of two tiles; 233
-// with fewer stores and pages looked up ahead; the rest by equal runs).  Short
+// with fewer stores and pages looked up ahead; the rest by runs of equal time).  Short
 // sequences pay for the chain of loads that each unit starts with: 256 of up to
-// 512 tokens take 46 us, 12 of them their bytes'.  Four warps to a CTA, three
+// 512 tokens take 42 us, 12 of them their bytes'.  Four warps to a CTA, three
 // CTAs to an SM for eight rows, two for sixteen; a ring of three or four steps
 // for each warp.
 #include <cuda_bf16.h>

@@ -27,15 +27,16 @@
 // values, so that the two are not tied to one another.
 //
 // Bound: neither rate.  A chunk of 3 x 2047 tokens over up to 12k (32 heads, 8
-// of keys, D = 128) takes 610 us, 990 TFLOP/s, half the products' measured rate.
-// A tile's chain, scores to softmax to product, has 2300 cycles, of which its
-// products take 1700; with the exponentials or the expansion left out it was
-// hardly faster: what the roles wait for one another bounds it.  Few rows (33
-// sequences, 35 rows, 5001 tokens: 61 us) pay for the expansion of every key
-// with products that are a quarter full.  Tiles of 128 keys with one buffer of
-// scores: 706 us for the chunk against 704, and 87 against 70 for the few rows, then;
-// keys and values expanded by one warpgroup: 706 against 693 then.  Two raw
-// slots: the same as three.
+// of keys, D = 128) takes 525 us, 1150 TFLOP/s, 60 % of the products' measured
+// rate.  A tile's chain, scores to softmax to product, is longer than the
+// products of both groups; with the exponentials or the expansion left out it
+// was hardly faster: what the roles wait for one another bounds it.  Few rows (33
+// sequences, 35 rows, 5001 tokens: 56 us) pay for the expansion of every key
+// with products that are a quarter full.  Products issued by lane 0 in place of
+// an elected thread: 649 us and 582 (of a chunk that takes 554 now).  Tiles of 128
+// keys with one buffer of scores: 706 us and 704, and 87 and 70 for the few rows,
+// before that; keys and values expanded by one warpgroup: 706 and 693 then.  Two
+// raw slots: the same as three.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -68,7 +69,8 @@ __device__ __forceinline__ float reference(float m) { return fabsf(m) < kWide ? 
 __device__ __align__(16) const uint8_t zero_tiles[kKeys / kTokens * tile_bytes(128)] = {};   // of a page that does not exist
 
 // Tiles' time that a unit costs whatever its length.  256 rows: chunks of 512 tokens 371 us with none, 356, 342, 335 and 341
-// with 2, 4, 8 and 12.  128: 33 sequences of 35 rows 70 with none, 64, 61, 62.5 and 65.
+// with 2, 4, 8 and 12.  128: 33 sequences of 35 rows 70 with none, 64, 61, 62.5 and 65.  (Both before products were issued
+// as they are now.)
 __host__ __device__ constexpr int idle(int R) { return R > kRows ? 8 : 4; }
 
 // Where a run starts in the layout and where the next does, and in it: place t of unit u of head h of sequence b.
