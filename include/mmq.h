@@ -525,8 +525,8 @@ typedef struct {
     float scale;
 } mmq_shared_prefix_attention_t;
 
-/* Device workspace of one call (its sizes only; 0 for sizes the call
- * refuses).  256-byte aligned, caller-owned, not used by anything else until
+/* Device workspace of one call (by its sizes, and whether q_starts is NULL; 0
+ * for sizes the call refuses).  256-byte aligned, caller-owned, not used by anything else until
  * the stream passes the call. */
 size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t* p);
 
@@ -683,9 +683,9 @@ size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
  * those of out are left as they were.  What the cache holds past a token's last
  * key is never used, whatever it is.  Scores, maxima and sums are float32.
  * Weights exp(s - m) are rounded to float16 for their product with the values
- * (errors of 2^-12 of a result at most, beside its own rounding); in the form
- * for few rows (a sequence's tokens times heads / kv_heads up to 16, or up to 40
- * by the batch's average) they have 22 bits where type or out_type shows it.
+ * (2^-11 of a weight at most); in the form for few rows (16, 24 or 40 of a
+ * sequence's tokens times heads / kv_heads, by the batch) they have 22 bits
+ * where type or out_type shows it.
  * Results are bitwise the same run to run on one device and build, but depend
  * in their last bits on the other sequences of the batch (how its work is cut).  A length over table_width * page_size is cut to
  * it, a page number outside [0, n_pages) stands for a page of zeros, and a

@@ -176,3 +176,34 @@ def test_whole_tiles_in_other_orders():
     assert torch.equal(a.double(), torch.where(here, (kq - 8) * ksc, 0.0))
     assert torch.equal(b.double(), torch.where(here, (vq - 8) * vsc, 0.0))
     assert mmq.status() == 0
+
+
+@pytest.mark.parametrize("out_dtype", [None, torch.float32])
+@pytest.mark.parametrize("news,kind", [([1, 1, 1], "f16"), ([3, 0, 9], "bf16"), ([60, 1, 31], "f16"), ([300, 5, 1], "bf16"),
+                                       ([257, 64, 65], "f16")])
+def test_a_padded_batch_of_strided_queries(news, kind, out_dtype):
+    """Rows before the first sequence and behind the last: not read (they hold NaN), and left as they were."""
+    mmq = require_gpu()
+    d = make(mmq, news, [n + 70 * i for i, n in enumerate(news)], 8, 2, 64, 32, kind, 9)
+    T, heads, D = d["q"].shape
+    wide = torch.full((T + 9, heads, 2 * D), float("nan"), dtype=d["q"].dtype, device="cuda").view(T + 9, heads * 2, D)
+    q = wide[:, :heads]
+    q[2:2 + T] = d["q"]
+    out = torch.full((T + 9, heads, D), 7.0, dtype=out_dtype or q.dtype, device="cuda")
+    mmq.kv4_attention(q, d["cache"], d["page_table"], d["lens"], q_starts=d["q_starts"] + 2, out=out)
+    assert mmq.status() == 0
+    assert (out[:2] == 7).all() and (out[2 + T:] == 7).all()
+    check(out[2:2 + T], d)
+
+
+def test_one_long_sequence_of_each_form_past_many_short_ones():
+    """Units of one step and of hundreds side by side: cuts between runs anywhere in the layout."""
+    mmq = require_gpu()
+    for seed, (long, new) in enumerate([(9000, 1), (9000, 12), (5000, 70), (5000, 300)]):
+        news = [1] * 40 + [new] + [1, 0, 2] * 11
+        lens = [1 + i % 5 for i in range(40)] + [long] + [3 + i % 7 for i in range(33)]
+        d = make(mmq, news, lens, 8, 2, 128, 16, "bf16" if seed % 2 else "f16", 50 + seed)
+        got = call(mmq, d)
+        assert mmq.status() == 0
+        check(got, d)
+        assert torch.equal(call(mmq, d), got)
