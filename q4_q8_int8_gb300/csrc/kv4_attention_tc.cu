@@ -36,7 +36,9 @@
 // an elected thread: 649 us and 582 (of a chunk that takes 554 now).  Tiles of 128
 // keys with one buffer of scores: 706 us and 704, and 87 and 70 for the few rows,
 // before that; keys and values expanded by one warpgroup: 706 and 693 then.  Two
-// raw slots: the same as three.
+// raw slots: the same as three.  The maximum of a tile's first half beside the
+// load of its second, 577 us and 556; its weights beside the maximum, 553 and 559,
+// but 70.7 and 69.8 for 64 rows of 16 sequences.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -68,9 +70,9 @@ __device__ __forceinline__ float reference(float m) { return fabsf(m) < kWide ? 
 
 __device__ __align__(16) const uint8_t zero_tiles[kKeys / kTokens * tile_bytes(128)] = {};   // of a page that does not exist
 
-// Tiles' time that a unit costs whatever its length.  256 rows: chunks of 512 tokens 371 us with none, 356, 342, 335 and 341
-// with 2, 4, 8 and 12.  128: 33 sequences of 35 rows 70 with none, 64, 61, 62.5 and 65.  (Both before products were issued
-// as they are now.)
+// Tiles' time that a unit costs whatever its length.  256 rows, chunks of 512 tokens: 291 us with 5, 288 with 8, 290 and 292
+// with 10 and 12 (371 with none and 335 with 8, before products were issued as they are now).  128 rows, 33 sequences of 35
+// rows: 54 to 56 with 3 to 6 (70 with none and 61 with 4, before).
 __host__ __device__ constexpr int idle(int R) { return R > kRows ? 8 : 4; }
 
 // Where a run starts in the layout and where the next does, and in it: place t of unit u of head h of sequence b.
