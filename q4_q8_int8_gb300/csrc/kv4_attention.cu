@@ -22,10 +22,12 @@
 //   Keys: a code masked out of its word is an fp16 subnormal, n 2^-24 (or 2^-20
 //   from the upper nibble, for which q' is 2^-4 times smaller), and the block's
 //   scale multiplies the f32 sum.  The 8 is taken off in one more product,
-//   scales times -8 sum q' of their blocks: a scale's bits, shifted by three,
-//   are a bfloat16 (times 2^-112), and each f32 sum is three of them.  q' has
-//   its row's largest element in [2^13, 2^14): nothing of a bfloat16's or
-//   float16's eleven bits is lost down to 2^-28 of it.
+//   scales times -8 sum q' of their blocks: a scale, of at most eight
+//   significant bits, is a bfloat16, and each f32 sum is three of them.  (By
+//   value: float16's bits shifted by three are not, where it is subnormal.)  q'
+//   has its row's largest element in [2^13, 2^14): nothing of a bfloat16's or
+//   float16's eleven bits is lost down to 2^-23 of it, and of what is smaller no
+//   more than 2^-34 of it.
 //   Values: (n - 8) d, exact in fp16, because here the scale's index is summed
 //   over.  kFine (float16 queries, float32 results): weights are the sum of two
 //   fp16 values (22 bits, 2^-25 of the reference at worst), a product each; one
@@ -107,6 +109,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+
+// Two float16 of at most eight significant bits as bfloat16, exactly.
+__device__ __forceinline__ uint32_t bf16_of(uint32_t v) {
+    const float2 f = __half22float2(u2h(v));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
 
 // ------------------------------------------------------------------ output
 __device__ __forceinline__ void store_value(void* out, int type, int64_t at, float x) {
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
         for (int i = 0; i < kStages - 1 && next < last; ++i) fetch();
 
         uint32_t qf[NT][D / 16][2];
-        uint32_t qs[NT][2];            // -8 sum q' of each block, times 2^112, as an operand
+        uint32_t qs[NT][2];            // -8 sum q' of each block, as an operand
         float f[NT][2];
         int see[NT][2];
 #pragma unroll
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
             for (int g = 0; g < kGroups; ++g) {
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
                 sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-                sum[g] *= -8.f * 0x1p-24f * 0x1p112f;
+                sum[g] *= -8.f * 0x1p-24f;
             }
             // As three bfloat16 each, in the order in which take() has the scales: of 16 places, lane c has 2 c, 2 c + 1
             // (first word) and those + 8 (second), the scales of blocks 2 c, 2 c + 1 modulo their number.
@@ -453,12 +462,11 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, NT>::kCtas) kv4_rows_kern
                 } else {
                     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ks[0]), "=r"(ks[1]) : "r"(from) : "memory");
                 }
-                // What the codes' 8 takes off: the scales, as bfloat16 of 2^-112 their value (float16's bits moved by
-                // three), times the blocks' sums.
+                // What the codes' 8 takes off: the scales, as bfloat16, times the blocks' sums.
                 {
                     const uint32_t w0 = D == 128 && (c4 & 1) ? ks[kGroups / 2 - 1] : ks[0];
                     const uint32_t w1 = D == 128 && (c4 & 1) ? ks[kGroups - 1] : ks[kGroups / 2];
-                    const uint32_t d0 = and_or(w0, 0x80008000u, (w0 >> 3) & 0x0FFF0FFFu), d1 = and_or(w1, 0x80008000u, (w1 >> 3) & 0x0FFF0FFFu);
+                    const uint32_t d0 = bf16_of(w0), d1 = bf16_of(w1);
                     const uint32_t A[4] = {d0, d1, d0, d1};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma16816_bf16_0(y[j][nt], A, qs[nt][0], qs[nt][1]);
