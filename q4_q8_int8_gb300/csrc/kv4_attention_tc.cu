@@ -755,10 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * scale;
                 const bool rises = top > m + kGrow;
                 if (__any_sync(0xffffffffu, rises)) {
-                    const float was = m;
-                    wide = __any_sync(0xffffffffu, rises && !(fabsf(top) < kWide));
+                    const float was = m, now = fmaxf(m, top);   // of every row, also one that rises by less than kGrow
+                    wide = __any_sync(0xffffffffu, now != m && !(fabsf(now) < kWide));
                     if (wide) break;
-                    m = fmaxf(m, top);
+                    m = now;
                     if (n > 0) scale_o(ex2(was - m));
                     if (!ok) break;
                 }
