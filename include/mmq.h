@@ -687,10 +687,11 @@ size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
  * sequence's tokens times heads / kv_heads, by the batch) they have 22 bits
  * where type or out_type shows it.
  * Results are bitwise the same run to run on one device and build, but depend
- * in their last bits on the other sequences of the batch (how its work is cut).  A length over table_width * page_size is cut to
- * it, a page number outside [0, n_pages) stands for a page of zeros, and a
- * sequence whose q_starts do not lie in order within [0, tokens] is left out;
- * each sets the device status word to MMQ_ERR_ARG.
+ * in their last bits on the other sequences of the batch (how its work is cut).
+ * A length over table_width * page_size, or over 2^31 - 1024, is cut to it, a
+ * page number outside [0, n_pages) stands for a page of zeros, and a sequence
+ * whose q_starts do not lie in order within [0, tokens] is left out; each sets
+ * the device status word to MMQ_ERR_ARG.
  * scale > 0; heads a multiple of kv_heads; q_stride a multiple of 8; pointers
  * 16-byte aligned (page_table, lens, q_starts: 4-byte); batch == 0 or tokens ==
  * 0 does nothing.  MMQ_ERR_ARG (a small workspace included) / MMQ_ERR_ALIGN /

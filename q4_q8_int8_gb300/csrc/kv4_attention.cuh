@@ -52,6 +52,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // --------------------------------------------------------------- sequences
+// The most keys of a sequence: places of keys are 32-bit numbers, the end of a last step and the pages that are looked
+// up ahead of it, up to 720 keys past that end, among them.  (As numbers without a sign, so that 2^31 - 1 could be held,
+// those comparisons cost the few-row kernel 2 %: 64 sequences of 32k tokens 227 us, and 222.)
+constexpr int64_t kMostKeys = (int64_t(1) << 31) - 1024;
 struct Sequence {
     int n, len;       // new tokens, tokens
     int64_t start;    // first row of q
@@ -70,7 +74,7 @@ __device__ __forceinline__ Sequence sequence(const Kv4Args& a, int b, bool tell)
         s.n = a.each;
         s.start = int64_t(b) * s.n;
     }
-    const int64_t room = p.table_width << a.page_shift, len = p.lens[b];
+    const int64_t room = min(p.table_width << a.page_shift, kMostKeys), len = p.lens[b];
     bad = bad || len > room;
     s.len = int(max(int64_t(0), min(len, room)));
     if (tell && bad) atomicCAS(a.status, 0, MMQ_ERR_ARG);
