@@ -576,8 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
             // ---------------------------------------------- the runs' pieces
             Walk<kR> q(a, from[lane]);
             for (uint32_t i = 0;; ++i) {
-                if (!wait_bounded(done_with(lane, i), ((i / kPieces) & 1u) ^ 1u, abort_flag, status)) break;
                 Piece& to = piece_at(lane, i);
+                // Until a whole piece is done, which may have millions of tiles: 1 us each, 20 are granted.
+                const uint64_t limit = kWaitLimitNs + (i < kPieces ? 0 : uint64_t(to.t1 - to.t0) * 20000);
+                if (!wait_bounded(done_with(lane, i), ((i / kPieces) & 1u) ^ 1u, abort_flag, status, limit)) break;
                 to.t0 = to.t1 = 0;
                 if (q.valid()) {
                     to.t0 = q.first_tile();

@@ -112,17 +112,17 @@ struct AbortFlag {
 };
 
 // Wait for phase `parity` of `bar`.  Returns false (without waiting further)
-// if another thread of the CTA already aborted, or after kWaitLimitNs, in
+// if another thread of the CTA already aborted, or after limit_ns, in
 // which case it raises the CTA's abort flag and the device status word, there
 // over whatever another kernel found wrong in its arguments.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, AbortFlag abort_flag,
-                                             int* status) {
+                                             int* status, uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (abort_flag.raised()) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
+        if (globaltimer() - t0 > limit_ns) {
             abort_flag.set(1u);
             atomicExch(status, MMQ_ERR_DEVICE_TIMEOUT);
             return false;
