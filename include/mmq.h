@@ -682,10 +682,11 @@ size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
  * sequence and be zero.  Rows of q that belong to no sequence are not read and
  * those of out are left as they were.  What the cache holds past a token's last
  * key is never used, whatever it is.  Scores, maxima and sums are float32.
- * Weights exp(s - m) are rounded to float16 for their product with the values
- * (2^-11 of a weight at most); in the form for few rows (16, 24 or 40 of a
- * sequence's tokens times heads / kv_heads, by the batch) they have 22 bits
- * where type or out_type shows it.
+ * For their product with the values, weights exp(s - m) have 22 bits where
+ * out_type is float32, and are rounded to float16 (by 2^-11 of a weight at most)
+ * where it is not; but for a float16 result they have 22 bits too where a
+ * sequence has few rows (tokens times heads / kv_heads: up to 16, 24 or 40, by
+ * the batch).
  * Results are bitwise the same run to run on one device and build, but depend
  * in their last bits on the other sequences of the batch (how its work is cut).
  * A length over table_width * page_size, or over 2^31 - 1024, is cut to it, a

@@ -5,7 +5,10 @@
 // takes two products of 128 rows x 64 keys x D for each 128 rows, S = Q K^T and
 // O += P V with P = 2^(S f - m) as fp16, the rest f32; the keys and values, (code
 // - 8) * scale, are exact in fp16, so that P's rounding is the only one beside the
-// result's.  Q is fp16: a bfloat16 row with its largest element in [2^13,
+// result's.  A 16-bit result takes one fp16 value per weight, which a float16 one
+// shows (its error 2.9e-4 of the norm, 2.1e-4 its own rounding); a float32 result
+// takes two (kFine: 22 bits, what is left of P over the other half of S, with a
+// product of its own; 513 us and 653 for the chunks below).  Q is fp16: a bfloat16 row with its largest element in [2^13,
 // 2^14), of which fp16 loses nothing down to 2^-28 of it, and 2^-e in f.
 //
 // One CTA per SM:
@@ -177,6 +180,11 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// What pack16 left of them.
+__device__ __forceinline__ uint32_t rest16(float a, float b, uint32_t packed) {
+    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+    return pack16(a - back.x, b - back.y);
+}
 __device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 // Two codes in the lower nibbles, or the upper ones, of v's bytes 0 and 2, less 8, times the scales.
@@ -202,7 +210,8 @@ __device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t* w) {
     else w[0] = ld_shared_u32(addr);
 }
 
-template <typename T, int D, bool kTwo>
+// kFine: weights as two fp16 values, for a float32 result.
+template <typename T, int D, bool kTwo, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     using L = Layout<D, kTwo>;
     constexpr int kSlots = L::kSlots, kRawSlots = L::kRawSlots, kStreams = L::kStreams, kBufs = L::kBufs, kR = L::kR;
@@ -564,6 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
                             mma_f16_ta(to, ts + 64u * (no & 1u) + 8u * uint32_t(kk), desc(dv + uint32_t(kk * 2)), kIdPV, uint32_t(s > 0 || kk > 0));
+                        if constexpr (kFine) {
+#pragma unroll
+                            for (int kk = 0; kk < kKeys / 16; ++kk)
+                                mma_f16_ta(to, ts + 64u * (no & 1u) + 32u + 8u * uint32_t(kk), desc(dv + uint32_t(kk * 2)), kIdPV, 1u);
+                        }
                         mma_commit(o_done(g, no));
                         mma_commit(empty(slot));
                         if (s + 2 < tiles) ok = scores(no + 2);
@@ -769,15 +783,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[16];
+                    uint32_t pk[16], rest[kFine ? 16 : 1];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const uint64_t e = ffma2(pack2u(s[c][2 * k], s[c][2 * k + 1]), scale2, base2);
                         const float u = ex2(lo_f(e)), v = ex2(hi_f(e));
                         sum[k & 1] = fadd2(sum[k & 1], pack2(u, v));
                         pk[k] = pack16(u, v);
+                        if constexpr (kFine) rest[k] = rest16(u, v, pk[k]);
                     }
                     tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);
+                    if constexpr (kFine) tmem_st_32x32b_x16(ts + 32u + 16u * uint32_t(c), rest);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -813,11 +829,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
                 const float base = reference(m);
                 if (n > 0) scale_o(ex2(reference(was) - base));
                 if (!ok) break;
+                uint32_t second[kFine ? 32 : 1];   // the rests of the first half's weights go over the second half
+                if constexpr (kFine) {
+                    tmem_ld_32x32b_x32(ts + 32u, second);
+                    tmem_wait_ld(second);
+                }
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     uint32_t x[32], pk[16];
-                    tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
-                    tmem_wait_ld(x);
+                    if (!kFine || c == 0) {
+                        tmem_ld_32x32b_x32(ts + 32u * uint32_t(c), x);
+                        tmem_wait_ld(x);
+                    }
+                    if constexpr (kFine) {
+                        if (c == 1) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = second[k];
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         const float y = __fmul_rn(__uint_as_float(x[k]), scale);
@@ -827,6 +856,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) pk[k] = pack16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
                     tmem_st_32x32b_x16(ts + 16u * uint32_t(c), pk);   // over what has been read
+                    if constexpr (kFine) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) pk[k] = rest16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), pk[k]);
+                        tmem_st_32x32b_x16(ts + 32u + 16u * uint32_t(c), pk);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -938,25 +972,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4Args a) {
     }
 }
 
-template <typename T, int D, bool kTwo>
+template <typename T, int D, bool kTwo, bool kFine>
 cudaError_t launch(const Kv4Args& a, int nsm, cudaLaunchConfig_t cfg) {
     using L = Layout<D, kTwo>;
+    auto* const kernel = kv4_tc_kernel<T, D, kTwo, kFine>;
     static const bool registers_ok = [] {   // else the split's increase would wait forever
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, kv4_tc_kernel<T, D, kTwo>) == cudaSuccess && f.numRegs == int(kRegsLaunch);
+        return cudaFuncGetAttributes(&f, kv4_tc_kernel<T, D, kTwo, kFine>) == cudaSuccess && f.numRegs == int(kRegsLaunch);
     }();
     if (!registers_ok) return cudaErrorLaunchOutOfResources;
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(kv4_tc_kernel<T, D, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes))) return e;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes))) return e;
     cfg.gridDim = dim3(unsigned(nsm));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = L::kBytes;
-    if ((e = cudaLaunchKernelEx(&cfg, kv4_tc_kernel<T, D, kTwo>, a))) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a))) return e;
     return mmq::launch_kv4_join(a, L::kR, nsm * L::kStreams, cfg.stream);
 }
 template <typename T, int D>
 cudaError_t launch(const Kv4Args& a, bool two, int nsm, const cudaLaunchConfig_t& cfg) {
-    return two ? launch<T, D, true>(a, nsm, cfg) : launch<T, D, false>(a, nsm, cfg);
+    if (a.p.out_type == MMQ_TYPE_F32)
+        return two ? launch<T, D, true, true>(a, nsm, cfg) : launch<T, D, false, true>(a, nsm, cfg);
+    return two ? launch<T, D, true, false>(a, nsm, cfg) : launch<T, D, false, false>(a, nsm, cfg);
 }
 
 }  // namespace
