@@ -439,7 +439,8 @@ const char* mmq_strerror(int code);
 /* Programmatic dependent launch (process-wide, default off): when enabled,
  * the q8_1 prepass, the GEMM kernels (few-token and tcgen05), the head norms,
  * the writes, reads and copies of caches and pages and the first kernel of an
- * attention, compaction or mixture-of-experts call are launched so that each may start while the previous kernel on its stream finishes.
+ * attention, compaction or mixture-of-experts call are launched so that each
+ * may start while the previous kernel on its stream finishes.
  * (The later kernels of such a call always are; they belong to the call.)
  * A kernel so launched issues only its weight loads (or, for the tcgen05
  * kernel, only its set-up) before it waits for the previous grid to
@@ -525,8 +526,8 @@ typedef struct {
     float scale;
 } mmq_shared_prefix_attention_t;
 
-/* Device workspace of one call (by its sizes, and whether q_starts is NULL; 0
- * for sizes the call refuses).  256-byte aligned, caller-owned, not used by anything else until
+/* Device workspace of one call (its sizes only; 0 for sizes the call
+ * refuses).  256-byte aligned, caller-owned, not used by anything else until
  * the stream passes the call. */
 size_t mmq_shared_prefix_attention_workspace(const mmq_shared_prefix_attention_t* p);
 
@@ -668,9 +669,10 @@ typedef struct {
     float scale;
 } mmq_kv4_attention_t;
 
-/* Device workspace of one call (its sizes only; 0 for sizes the call
- * refuses).  256-byte aligned, caller-owned, not used by anything else until
- * the stream passes the call. */
+/* Device workspace of one call (by its sizes, and whether q_starts is NULL: of
+ * the same sizes it needs more where it is not, and fewer tokens may need more
+ * than many; 0 for sizes the call refuses).  256-byte aligned, caller-owned,
+ * not used by anything else until the stream passes the call. */
 size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
 
 /* Causal attention of a batch over its pages of a 4-bit cache.  With n the new
