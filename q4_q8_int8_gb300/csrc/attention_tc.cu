@@ -59,6 +59,7 @@
 #include <type_traits>
 
 #include "attention.h"
+#include "half_ops.cuh"
 #include "mmq_internal.h"
 #include "sm103_ptx.cuh"
 #include "tc_common.cuh"
@@ -107,25 +108,6 @@ static_assert(Layout<128>::kBytes <= 232448, "shared memory budget");
 struct Maps {
     CUtensorMap k, v;
 };
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc_16(int N, bool b_rows_are_k) {

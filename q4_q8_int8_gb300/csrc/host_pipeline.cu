@@ -40,8 +40,6 @@ cudaError_t pipe_for(int dev, HostPipe** out) {
     return cudaSuccess;
 }
 
-size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
-
 // The fixed device workspace of mmq_q4K_gemm_host_noalloc.  Every device on
 // which the library's code is loaded holds it until the process exits.  In
 // host code the name is only a host-side stand-in for the array; its device

@@ -53,6 +53,7 @@
 
 #include <type_traits>
 
+#include "half_ops.cuh"
 #include "kv4_attention.cuh"
 #include "mmq_internal.h"
 #include "sm103_ptx.cuh"
@@ -63,6 +64,7 @@ namespace {
 using namespace mmq::ptx;
 using namespace mmq::kv4;
 using mmq::tc::ld_shared_v4;
+using mmq::up256;
 
 __device__ __align__(16) const uint8_t zero_tile[tile_bytes(128)] = {};   // of a page that does not exist
 constexpr int kWarps = 4;
@@ -75,17 +77,7 @@ constexpr float kNone = -3.402823466e38f;   // the reference before any score: n
 constexpr int kIdle = 5;
 constexpr int kLeast = 2;   // steps to a run, where there are too few for all warps
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// The same without an accumulator, and with bfloat16 operands.
+// mma16816 without an accumulator, and with bfloat16 operands.
 __device__ __forceinline__ void mma16816_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -107,8 +99,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
-__device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-__device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
 // Two float16 of at most eight significant bits as bfloat16, exactly.
 __device__ __forceinline__ uint32_t bf16_of(uint32_t v) {
@@ -822,16 +812,6 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv4_join_kernel(const Kv4Args 
     store(row, acc, l);
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
-
 // A ragged batch of more than eight tokens a sequence on average, which is taken to hold chunks, and single tokens beside.
 bool mixed(const mmq_kv4_attention_t& p) { return p.q_starts && p.tokens > int64_t(8) * p.batch; }
 
@@ -843,8 +823,6 @@ bool narrow(const mmq_kv4_attention_t& p) {
     const int64_t group = p.heads / p.kv_heads;
     return p.tokens * group <= int64_t(8) * p.batch || (mixed(p) && group <= 8);
 }
-
-size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 template <int D, int NT>
 size_t part_bytes(int nsm) {

@@ -47,6 +47,7 @@
 
 #include <type_traits>
 
+#include "half_ops.cuh"
 #include "kv4_attention.cuh"
 #include "mmq_internal.h"
 #include "sm103_ptx.cuh"
@@ -166,27 +167,12 @@ struct Layout {
 };
 static_assert(Layout<128, true>::kBytes <= 232448 && Layout<128, false>::kBytes <= 232448, "shared memory budget");
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack16(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
+__device__ __forceinline__ uint32_t pack16(float a, float b) { return h2u(__floats2half2_rn(a, b)); }
 // What pack16 left of them.
 __device__ __forceinline__ uint32_t rest16(float a, float b, uint32_t packed) {
-    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+    const float2 back = __half22float2(u2h(packed));
     return pack16(a - back.x, b - back.y);
 }
-__device__ __forceinline__ uint32_t h2u(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-__device__ __forceinline__ __half2 u2h(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 // Two codes in the lower nibbles, or the upper ones, of v's bytes 0 and 2, less 8, times the scales.
 __device__ __forceinline__ uint32_t expand_low(uint32_t v, uint32_t scales) {
     uint32_t d;

@@ -12,6 +12,18 @@ namespace mmq {
 // turned it on.
 bool programmatic_launch_enabled();
 
+// Multiprocessors of the current device; 0 on a CUDA error.
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
 // Launch configuration with the programmatic-dependent-launch attribute
 // when it is enabled; attr must have room for it (numAttrs 0 or 1 on return,
 // more may be appended by the caller).

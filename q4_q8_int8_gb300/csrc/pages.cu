@@ -18,6 +18,7 @@
 namespace {
 
 using namespace mmq::ptx;
+using mmq::up256;
 
 constexpr int kThreads = 256;
 constexpr int kFlight = 8;                             // 16-byte loads in flight per thread
@@ -195,8 +196,6 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(const __grid_const
     }
 }
 
-size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-
 struct Layout {
     size_t bits, before, src, dst, plan, bytes;
 };
@@ -210,16 +209,6 @@ Layout layout(int64_t n_pages) {
     l.plan = l.dst + up256(moves * 4);
     l.bytes = l.plan + up256(sizeof(Plan));
     return l;
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
 }
 
 }  // namespace

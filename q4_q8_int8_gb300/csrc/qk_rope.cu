@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "half_ops.cuh"
 #include "mmq_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -34,15 +35,6 @@ using namespace mmq::ptx;
 
 constexpr int kThreads = 64;
 constexpr int kHeads = 3;   // heads in flight per lane group
-
-__device__ __forceinline__ uint32_t pack16(float a, float b, __half*) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16*) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 struct RopeArgs {
     mmq_qk_norm_rope_t p;
