@@ -65,3 +65,63 @@ def test_calls_of_all_forms_over_one_workspace(kind, out_dtype):
         assert mmq.status() == 0
         for i, (a, b) in enumerate(zip(got, want)):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("on", [False, True])
+def test_a_step_captured_and_replayed(on):
+    """A whole step in one graph, its launches programmatic or not: new inputs at each replay, results as of plain calls."""
+    mmq = require_gpu()
+    kv, heads, D, page, width = 2, 8, 64, 16, 40
+    g = torch.Generator(device="cuda").manual_seed(19)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.randperm(2 * width, device="cuda", generator=g).view(2, width).to(torch.int32)
+    cache = mmq.empty_kv4_cache(2 * width + 2, kv, D, page)
+    k, v = torch.empty((2, 310, kv, D), dtype=torch.float16, device="cuda")
+    q = torch.empty((310, heads, D), dtype=torch.float16, device="cuda")
+    slots, lens = torch.empty(310, **i32), torch.empty(2, **i32)
+    starts, last = torch.tensor([0, 3, 310], **i32), torch.tensor([0, 1, 2], **i32)
+    moved, free = torch.empty((2, width), **i32), torch.tensor([2 * width], **i32)
+    outs = [torch.empty_like(q), torch.empty_like(q[:2]), torch.empty((310, kv, D), dtype=torch.float16, device="cuda"),
+            torch.empty((310, kv, D), dtype=torch.float16, device="cuda")]
+
+    def step():
+        mmq.kv4_write(k, v, slots, cache)
+        mmq.kv4_attention(q, cache, table, lens, q_starts=starts, out=outs[0])
+        mmq.kv4_attention(q[:2], cache, table, lens, out=outs[1])
+        mmq.kv4_read(cache, slots, out=(outs[2], outs[3]))
+        mmq.pages_compact([cache], table, lens, page, table_out=moved)
+        mmq.pages_copy([cache], moved[1, :1], free)
+        mmq.kv4_attention(q[:3], cache, moved, lens, q_starts=last, out=q[3:6])
+
+    def fill(seed):
+        g.manual_seed(seed)
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+        cache.random_(0, 16, generator=g)      # scales that are small numbers
+        n = [3 + 97 * seed % 400, 307 + 31 * seed % 300]
+        lens.copy_(torch.tensor(n))
+        at = torch.cat([torch.arange(n[0] - 3, n[0]), torch.arange(n[1] - 307, n[1])]).cuda()
+        slots.copy_(table.flatten()[at // page + torch.tensor([0] * 3 + [width] * 307).cuda()] * page + at % page)
+
+    def results():
+        torch.cuda.synchronize()
+        assert mmq.status() == 0
+        return [x.clone() for x in outs + [moved, cache, q]]
+
+    fill(0)
+    step()
+    torch.cuda.synchronize()
+    mmq.mmq_set_programmatic_launch(on)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    finally:
+        mmq.mmq_set_programmatic_launch(False)
+    for seed in range(1, 6):
+        fill(seed)
+        step()
+        want = results()
+        fill(seed)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
