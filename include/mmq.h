@@ -680,9 +680,9 @@ size_t mmq_kv4_attention_workspace(const mmq_kv4_attention_t* p);
  * keys of the sequence (key i on page page_table[b][i / page_size], place i %
  * page_size); head h uses kv head h / (heads / kv_heads); s = scale * q.k,
  *     out = sum_i exp(s_i - max s) v_i / sum_i exp(s_i - max s)
- * and zeros for a token that sees no key.  n may differ from sequence to
- * sequence and be zero.  Rows of q that belong to no sequence are not read and
- * those of out are left as they were.  What the cache holds past a token's last
+ * and zeros for a token that sees no key, or none whose score is above
+ * -infinity.  n may differ from sequence to sequence and be zero.  Rows of q
+ * that belong to no sequence are not read and those of out are left as they were.  What the cache holds past a token's last
  * key is never used, whatever it is.  Scores, maxima and sums are float32.
  * For their product with the values, weights exp(s - m) have 22 bits where
  * out_type is float32, and are rounded to float16 (by 2^-11 of a weight at most)

@@ -1046,7 +1046,7 @@ def kv4_attention(q, cache, page_table, lens, q_starts=None, scale=None, out=Non
     the new tokens of all sequences, whose keys and values are in the cache
     already; cache uint8 [pages][kv_heads][page_size / 16][18 D] as in kv4_write;
     page_table int32 [batch][width]; lens int32 [batch]: each sequence's tokens,
-    its new ones among them; q_starts int32 [batch + 1]: sequence b's rows of q
+    its new ones among them, at most 2^31 - 1024; q_starts int32 [batch + 1]: sequence b's rows of q
     are q_starts[b] .. q_starts[b + 1] - 1 (rows of none are left alone in
     `out`), or None for T / batch of them each.  scale: 1/sqrt(D) by default.
     Returns [T][heads][D] in q's type, or into `out` (which may also be

@@ -32,14 +32,14 @@
 //   over.  kFine (float16 queries, float32 results): weights are the sum of two
 //   fp16 values (22 bits, 2^-25 of the reference at worst), a product each; one
 //   alone would double the error of a float16 result.  For a bfloat16 result,
-//   rounded eight times as coarsely, one is taken, and the sum of weights is
-//   that of the rounded ones.
+//   rounded eight times as coarsely, one is taken.  The sum of weights is that of
+//   the float32 ones either way.
 // The reference m of a row starts kLift (in log2) under its first largest score
 // and is raised when a score is more than kSpan above it: weights stay below
 // 2^14, and what they lose in fp16 is small against the largest.
 //
 // Bound: a decode step of 64 sequences of up to 32k tokens, 8 heads of keys,
-// reads 1.26 GB in 221 us, 5.7 TB/s, 84 % of a copy's rate (float16 results: 250
+// reads 1.26 GB in 221 us, 5.7 TB/s, 84 % of a copy's rate (float16 results: 251
 // us, for their second product).  There the warps' instructions bound it as much
 // as memory does: what cut instructions cut time (347 us at first; 250 with
 // scales by pairs of tiles, the offset by a product and steps of two tiles; 233
@@ -816,9 +816,9 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv4_join_kernel(const Kv4Args 
 bool mixed(const mmq_kv4_attention_t& p) { return p.q_starts && p.tokens > int64_t(8) * p.batch; }
 
 // Eight rows to a unit where a sequence has no more on average, else sixteen.  33 sequences of 5001 tokens, four heads of
-// keys: seven rows 30 us, and 34 by units of sixteen; 14 rows 40 by twice as many units of eight, and 35.  64 sequences of
-// 32k tokens: four rows 226 and 311, sixteen 432 and 313.  Beside chunks the others are taken to have one token: 60 of 4096
-// tokens, four rows, and two chunks of 500: 158 and 169.
+// keys: seven rows 27 us, and 31 by units of sixteen; 14 rows 37 by twice as many units of eight, and 33.  64 sequences of
+// 32k tokens: four rows 221 and 308, sixteen 424 and 310.  Beside chunks the others are taken to have one token: 60 of 4096
+// tokens, four rows, and two chunks of 500: 105 and 116.
 bool narrow(const mmq_kv4_attention_t& p) {
     const int64_t group = p.heads / p.kv_heads;
     return p.tokens * group <= int64_t(8) * p.batch || (mixed(p) && group <= 8);
@@ -861,15 +861,18 @@ struct Forms {
 Forms forms(const mmq_kv4_attention_t& p) {
     const int64_t group = p.heads / p.kv_heads, rows = p.tokens * group;   // of all sequences
     const int64_t most = p.q_starts ? rows : rows / p.batch;               // of one, at most
-    // 33 sequences of 5001 tokens, four heads of keys, alike: 21 rows 51 us by two units of sixteen and 62 by the other
-    // kernel, 35 rows 64 and 61.  A ragged batch costs the time of two kernels where it has rows for both: 48 sequences of
-    // 8192 tokens, one to eight new ones, four rows each, 159 us cut at 16 rows, 146 at 24, 126 at 40.  So where the average
-    // tells that most are few, the cut is high.
+    // 33 sequences of 5001 tokens, four heads of keys, alike: 21 rows 47 us by two units of sixteen and 54 by the other
+    // kernel, 28 rows 48 and 56, 35 rows 60 and 54.  A ragged batch costs the time of two kernels where it has rows for
+    // both: 48 sequences of 8192 tokens, one to eight new ones, four rows each, 143 us cut at 16 rows, 136 at 24, 123 at 40
+    // (and 170 by the other kernel alone); 33 of 5001, one to five, seven rows each, 68, 68, 60 (and 62).  So where the
+    // average tells that most are few, the cut is high.  Around that border (one to eleven or twelve new ones, four rows
+    // each, 24 or 26 on average) little depends on it: of 8192 tokens 145 us cut at 16 and 141 at 40, of 2000 tokens 74
+    // and 77.
     const bool mostly_few = rows <= int64_t(24) * p.batch;
     const int most_few = p.q_starts ? mostly_few ? 40 : 16 : 24;
-    // 256 rows: chunks of 2047 tokens 662 us, and 1127 by units of 128; 64 tokens of 8 sequences, 256 rows each, 65 and 93.
-    // Up to 128 rows: 128 rows 97 us, and 103 by a unit of 256 that is half empty; 35 rows 61 and 71.  Two chunks of 500
-    // tokens beside 60 single ones: 128 and 169.
+    // 256 rows: chunks of 2047 tokens 556 us, and 924 by units of 128; 64 tokens of 8 sequences, 256 rows each, 57 and 85.
+    // Up to 128 rows: 128 rows 89 us, and 90 by a unit of 256 that is half empty; 35 rows 54 and 65.  Two chunks of 500
+    // tokens beside 60 single ones: 105 and 131.
     const bool two = rows > int64_t(128) * p.batch || mixed(p);
     return Forms{p.q_starts || most <= most_few, most > most_few, two, most_few};
 }
@@ -893,8 +896,8 @@ cudaError_t launch_kv4_join(const Kv4Args& a, int R, int runs, cudaStream_t s) {
     cfg.numAttrs = 1;
     cfg.stream = s;
     // Many parts to a unit (its share of the runs), so that a warp alone would take them one after the other: one sequence
-    // of 32k tokens 27 us, and 36 by a warp per row.  Else a warp per row is the faster: 33 sequences of one to five
-    // tokens 74 us shared and 69 not, 64 of 32k tokens 228 and 226.
+    // of 32k tokens 25 us, and 34 by a warp per row.  Else a warp per row is the faster: 33 sequences of one to five
+    // tokens 64 us shared and 60 not, 64 of 32k tokens 224 and 222.
     const bool share = R <= 16 && int64_t(a.p.batch) * a.p.kv_heads * 4 <= runs;
     cfg.gridDim = dim3(unsigned(runs), unsigned(share ? R : R / kJoinRows));
     cfg.blockDim = dim3(kJoinRows * 32);

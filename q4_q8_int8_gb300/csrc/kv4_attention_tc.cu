@@ -8,7 +8,7 @@
 // result's.  A 16-bit result takes one fp16 value per weight, which a float16 one
 // shows (its error 2.9e-4 of the norm, 2.1e-4 its own rounding); a float32 result
 // takes two (kFine: 22 bits, what is left of P over the other half of S, with a
-// product of its own; 513 us and 653 for the chunks below).  Q is fp16: a bfloat16 row with its largest element in [2^13,
+// product of its own; 653 us in place of 513 for the chunks below).  Q is fp16: a bfloat16 row with its largest element in [2^13,
 // 2^14), of which fp16 loses nothing down to 2^-28 of it, and 2^-e in f.
 //
 // One CTA per SM:
@@ -29,14 +29,15 @@
 // product is made.  What is expanded goes to a slot each for keys and for
 // values, so that the two are not tied to one another.
 //
-// Bound: neither rate.  A chunk of 3 x 2047 tokens over up to 12k (32 heads, 8
-// of keys, D = 128) takes 525 us, 1150 TFLOP/s, 60 % of the products' measured
+// Bound: neither rate.  Chunks of up to 3 x 2047 tokens over up to 12k (32 heads, 8
+// of keys, D = 128) take 519 us, 1160 TFLOP/s, 61 % of the products' measured
 // rate.  A tile's chain, scores to softmax to product, is longer than the
 // products of both groups; with the exponentials or the expansion left out it
 // was hardly faster: what the roles wait for one another bounds it.  Few rows (33
-// sequences, 35 rows, 5001 tokens: 56 us) pay for the expansion of every key
-// with products that are a quarter full.  Products issued by lane 0 in place of
-// an elected thread: 649 us and 582 (of a chunk that takes 554 now).  Tiles of 128
+// sequences, 35 rows, 5001 tokens: 54 us) pay for the expansion of every key
+// with products that are a quarter full.  What steps gave, on three chunks of 2047
+// tokens each, which take 554 us with all of them: products issued by lane 0 in
+// place of an elected thread, 649 us and 582.  Tiles of 128
 // keys with one buffer of scores: 706 us and 704, and 87 and 70 for the few rows,
 // before that; keys and values expanded by one warpgroup: 706 and 693 then.  Two
 // raw slots: the same as three.  The maximum of a tile's first half beside the
